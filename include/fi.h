@@ -66,6 +66,7 @@ typedef enum fi_status {
 #define FI_DEVERR_PAGE_OOB 0x1     /* a page index >= num_pages was skipped */
 #define FI_DEVERR_WAIT_TIMEOUT 0x2 /* a pipeline wait gave up after its iteration limit */
 #define FI_DEVERR_TMEM 0x4         /* tensor-memory allocation returned an unusable address */
+#define FI_DEVERR_KEPT 0x8         /* fi_compact skipped a kept entry that is out of range or not ascending */
 
 typedef struct fi_workspace fi_workspace;
 
@@ -303,6 +304,122 @@ int fi_run_merge(fi_workspace* ws, const void* q, const void* k_pages, const voi
  */
 int fi_merge_states(const void* o_a, const float* lse_a, const void* o_b, const float* lse_b, void* o, float* lse,
                     int rows, int heads, int head_dim, void* stream);
+
+/* ---- Cache operators -------------------------------------------------------------------------------
+ *
+ * The life of a paged KV-cache around fi_run: new tokens are written into the pages (fi_append), the
+ * attention weight of every cached key is accumulated (fi_key_weights), the keys worth keeping are
+ * chosen (fi_select_keys) and moved to the front of each request's pages (fi_compact).  All four run
+ * on the workspace's current plan: its requests, page lists, page size, layout, KV type, window and
+ * soft-cap.  With a composable plan they see the per-request part.
+ *
+ * Common behaviour: asynchronous on `stream`, launched as programmatic dependents that read nothing
+ * before the previous kernel on the stream has completed; capturable in a CUDA graph.  A captured
+ * launch reads the requests and page lists of the plan that is current when it runs; page size, layout,
+ * KV type, window, soft-cap, the pointers and the numbers passed by value are those of the capture, a
+ * later plan must keep fi_plan_info header[1] (the path), and the conditions on pages below hold
+ * for it too, unchecked.  The workspace's device must be the current one (else INVALID_ARG).  Page
+ * ids >= num_pages: INVALID_ARG (in a replay: skipped, FI_DEVERR_PAGE_OOB).  Calls that share a
+ * workspace must not overlap on the GPU.  Results are bit-identical from run to run.
+ * `weights` is float32 [num_pages, num_kv_heads, page_size] for either page layout.
+ */
+
+/*
+ * fi_workspace_set_rope -- rotary position of the following fi_append calls.
+ *
+ *   inv_freq     HOST double [rotary_dim / 2]: radians per position of each pair (finite; copied)
+ *   rotary_dim   leading dims of a head that rotate: 0 (default, none) to 128, a multiple of 16
+ *   interleaved  0: pair j is (j, j + rotary_dim / 2); 1: pair j is (2j, 2j + 1)
+ * Errors: INVALID_ARG, UNSUPPORTED (even rotary_dim that is not a multiple of 16).
+ */
+int fi_workspace_set_rope(fi_workspace* ws, const double* inv_freq, int32_t rotary_dim, int32_t interleaved);
+
+/*
+ * fi_cache_plan_compute -- what the cache operators derive from a batch, on the host, with no device work.
+ *
+ *   inputs   as for fi_plan
+ *   geo      HOST int32 [batch + 1][8]: per request {first query token, l_q, first page entry, l_kv, 32-key
+ *            blocks before it, 256-key tiles before it, 0, 0}; the last entry holds the totals
+ *   twice    HOST int32 [2]: [0] a page is listed twice (fi_key_weights and fi_compact refuse), [1] a page
+ *            takes new tokens from two places of the list (fi_append refuses)
+ * Errors: INVALID_ARG, UNSUPPORTED, CAPACITY.
+ */
+int fi_cache_plan_compute(const int32_t* qo_indptr, const int32_t* kv_indptr, const int32_t* kv_indices,
+                          const int32_t* last_page_len, int batch, int page_size, int32_t* geo, int32_t* twice);
+
+/*
+ * fi_append -- norm and rotate the plan's query tokens; write q, and K/V into the pages.
+ *
+ * Query token t of request i (l_q tokens, l_kv keys) is the key l_kv - l_q + t of its own cache.  For
+ * every head of q and k: x * w / sqrt(mean(x^2) + eps) with a weight, then the rotation at the token's
+ * position.  q goes to q_out, k and v to the key's page slot: bf16, or e4m3 codes of k / k_scale and
+ * v / v_scale saturated at +-448.  Computed in fp32, rounded once.  A token before its request's first
+ * key (l_q > l_kv) has no slot: only its q is written.  No other slot is touched.
+ *
+ *   q, k, v      DEVICE bf16, heads x 128 contiguous per token; *_stride = elements from one token to the
+ *                next (a multiple of 8, at least heads * 128), so all three may lie in one fused tensor
+ *   q_weight, k_weight   DEVICE bf16 [128], or NULL for no norm of that tensor; eps >= 0
+ *   positions    DEVICE int32 [total_q], or NULL for l_kv - l_q + t; needed with a composable plan
+ *                (INVALID_ARG) and after a compaction, when positions run ahead of the cache length
+ *   q_out        DEVICE bf16 [total_q, num_qo_heads, 128]; may be q itself when q is dense
+ *   k_pages, v_pages   as for fi_run (written)
+ * Errors: NO_PLAN, INVALID_ARG (null or not 16-byte aligned pointers, strides), UNSUPPORTED (a page
+ * that takes new tokens from two requests), CUDA.
+ */
+int fi_append(fi_workspace* ws, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+              int64_t v_stride, const void* q_weight, const void* k_weight, float eps, const int32_t* positions,
+              void* q_out, void* k_pages, void* v_pages, int num_pages, void* stream);
+
+/*
+ * fi_key_weights -- add the attention weight that the plan's query rows gave to each cached key.
+ *
+ *   weights[page(j), h, slot(j)] = decay * weights[...] + sum over query tokens t that see key j and
+ *   the query heads of KV head h of exp(logit(t, head, j) - lse[t, head])
+ *
+ * for every key of every request; the logit is fi_run's (scale, soft-cap, mask, window, k_scale).  Rows
+ * with lse = -inf (no key) add nothing.  Keys that no row sees are decayed too.
+ *
+ *   q, k_pages, lse   as given to / written by fi_run
+ *   decay        in [0, 1]; 1 keeps plain sums; 0 ignores the old contents (NaN included)
+ *   new_keys     1: the last min(l_q, l_kv) keys of each request are new, their old contents are not
+ *                read; 0: every key has a running sum
+ * Slots outside the plan's keys are untouched.  A page listed twice by the plan (a prefix shared between
+ * requests, or with the shared part of a composable plan) is UNSUPPORTED: its sum would have two writers.
+ * Errors: NO_PLAN, INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+int fi_key_weights(fi_workspace* ws, const void* q, const void* k_pages, int num_pages, const float* lse, float decay,
+                   int32_t new_keys, float* weights, void* stream);
+
+/*
+ * fi_select_keys -- the keys to keep under a budget, for each request and KV head.
+ *
+ * A request of at most `budget` keys keeps all of them.  A longer one keeps its first `sink` keys, its
+ * last `recent` keys and, of the others, the budget - sink - recent with the largest weights; equal
+ * weights go to the lowest position, NaN counts as the largest.
+ *
+ *   kept   DEVICE int32 [batch, num_kv_heads, budget] (written): positions in ascending order, then -1
+ * sink, recent >= 0, budget >= 1, sink + recent <= budget (else INVALID_ARG).
+ * Errors: NO_PLAN, INVALID_ARG, CUDA.
+ */
+int fi_select_keys(fi_workspace* ws, const float* weights, int num_pages, int32_t sink, int32_t recent, int32_t budget,
+                   int32_t* kept, void* stream);
+
+/*
+ * fi_compact -- move the kept keys to the front of each request's pages, in place.
+ *
+ * For each request of more than `budget` keys and each KV head, slot j < budget receives the K and V rows
+ * (and the running weight) of key kept[j].  Slots from `budget` on keep what they hold; requests of
+ * at most `budget` keys are left alone.  Afterwards request i holds min(l_kv, budget) keys: plan it with that
+ * many, and free the pages behind them.
+ *
+ *   kept     DEVICE int32 [batch, num_kv_heads, budget], ascending, as fi_select_keys writes it; an entry
+ *            that is not above the one before it or not in [j, l_kv) is skipped (FI_DEVERR_KEPT)
+ *   weights  as for fi_key_weights, or NULL
+ * A page listed twice by the plan is UNSUPPORTED (other requests still read it).
+ * Errors: NO_PLAN, INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+int fi_compact(fi_workspace* ws, const int32_t* kept, int32_t budget, void* k_pages, void* v_pages, float* weights,
+               int num_pages, void* stream);
 
 /*
  * fi_get_error -- read and clear the workspace's device-side error word

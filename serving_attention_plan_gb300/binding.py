@@ -8,7 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_float, c_int, c_int32, c_int64, c_void_p
+from ctypes import POINTER, c_double, c_float, c_int, c_int32, c_int64, c_void_p
 
 import numpy as np
 
@@ -19,6 +19,7 @@ STATUS = {0: "ok", 1: "invalid argument", 2: "capacity", 3: "unsupported", 4: "c
 DEVERR_PAGE_OOB = 0x1
 DEVERR_WAIT_TIMEOUT = 0x2
 DEVERR_TMEM = 0x4
+DEVERR_KEPT = 0x8
 
 _LIB = None
 
@@ -56,6 +57,13 @@ def lib() -> ctypes.CDLL:
                                c_void_p]
     L.fi_merge_states.argtypes = [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int,
                                   c_void_p]
+    L.fi_workspace_set_rope.argtypes = [c_void_p, POINTER(c_double), c_int32, c_int32]
+    L.fi_cache_plan_compute.argtypes = [P32, P32, P32, P32, c_int, c_int, P32, P32]
+    L.fi_append.argtypes = [c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p,
+                            c_float, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_void_p]
+    L.fi_key_weights.argtypes = [c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_float, c_int32, c_void_p, c_void_p]
+    L.fi_select_keys.argtypes = [c_void_p, c_void_p, c_int, c_int32, c_int32, c_int32, c_void_p, c_void_p]
+    L.fi_compact.argtypes = [c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int, c_void_p]
     L.fi_get_error.argtypes = [c_void_p, P32]
     L.fi_plan_info.argtypes = [c_void_p, P32]
     L.fi_plan_compute.argtypes = [P32, P32, P32, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int64, c_int64,
@@ -74,7 +82,8 @@ def lib() -> ctypes.CDLL:
                  "fi_workspace_set_variant", "fi_workspace_set_kv_dtype", "fi_plan", "fi_run",
                  "fi_run_merge", "fi_merge_states", "fi_get_error", "fi_plan_info", "fi_plan_compute", "fi_device_sm_count",
                  "fi_decode_noalloc", "fi_decode_noalloc_get_error", "fi_plan_composable_compute",
-                 "fi_plan_composable"):
+                 "fi_plan_composable", "fi_workspace_set_rope", "fi_append", "fi_key_weights", "fi_select_keys",
+                 "fi_compact", "fi_cache_plan_compute"):
         getattr(L, name).restype = c_int
     _LIB = L
     return L
@@ -105,6 +114,22 @@ def _stream_ptr(stream) -> c_void_p:
 
 def _dptr(t) -> c_void_p:
     return c_void_p(0 if t is None else t.data_ptr())
+
+
+def _need(ok, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _dense(t, name: str, dtypes, shape=None):
+    """Checks a device tensor argument: type, contiguity and shape."""
+    _need(t.is_cuda, f"{name}: a CUDA tensor is needed")
+    _need(str(t.dtype)[6:] in dtypes, f"{name}: {t.dtype}, expected {' or '.join(dtypes)}")
+    _need(t.is_contiguous(), f"{name}: a contiguous tensor is needed")
+    _need(shape is None or tuple(t.shape) == shape, f"{name}: shape {tuple(t.shape)}, expected {shape}")
+
+
+_BF16, _F32, _I32, _E4M3 = ("bfloat16",), ("float32",), ("int32",), ("float8_e4m3fn", "uint8")
 
 
 def plan_compute(qo_indptr, kv_indptr, last_page_len, num_qo_heads, num_kv_heads, page_size, causal, num_sms,
@@ -143,6 +168,17 @@ def plan_composable_compute(shared, unique, num_qo_heads, num_kv_heads, page_siz
     return out[: n.value]
 
 
+def cache_plan_compute(qo_indptr, kv_indptr, kv_indices, last_page_len, page_size):
+    """What the cache operators derive from a batch (no GPU): (geometry [batch + 1, 8], pages twice, tails twice)."""
+    qo, kv, idx, last = _i32(qo_indptr), _i32(kv_indptr), _i32(kv_indices), _i32(last_page_len)
+    if idx.size == 0:
+        idx = np.zeros(1, np.int32)
+    geo, twice = np.zeros((qo.shape[0], 8), np.int32), np.zeros(2, np.int32)
+    _check(lib().fi_cache_plan_compute(_p32(qo), _p32(kv), _p32(idx), _p32(last), qo.shape[0] - 1, page_size, _p32(geo),
+                                       _p32(twice)), "fi_cache_plan_compute")
+    return geo, bool(twice[0]), bool(twice[1])
+
+
 def device_sm_count() -> int:
     v = c_int(0)
     _check(lib().fi_device_sm_count(ctypes.byref(v)), "fi_device_sm_count")
@@ -157,6 +193,8 @@ class Workspace:
         _check(lib().fi_workspace_create(max_batch, max_total_q, max_kv_pages, num_qo_heads, num_kv_heads, head_dim,
                                          num_sms, ctypes.byref(self._h)), "fi_workspace_create")
         self.num_qo_heads, self.num_kv_heads, self.head_dim = num_qo_heads, num_kv_heads, head_dim
+        self._layout, self._kv_dtype = "HND", "bf16"
+        self._plan = None  # (total_q, batch, page_size, layout, kv_dtype) of the current plan
 
     def close(self):
         if self._h:
@@ -177,11 +215,20 @@ class Workspace:
         layout = {"HND": 0, "NHD": 1}[kv_layout]
         _check(lib().fi_workspace_set_variant(self._h, int(window_left), float(logits_soft_cap), layout),
                "fi_workspace_set_variant")
+        self._layout = kv_layout
 
     def set_kv_dtype(self, kv_dtype="bf16", k_scale=1.0, v_scale=1.0):
         """KV page element type ("bf16" or "e4m3", with per-tensor scales) for the following plan()."""
         _check(lib().fi_workspace_set_kv_dtype(self._h, {"bf16": 0, "e4m3": 1}[kv_dtype], float(k_scale),
                                                float(v_scale)), "fi_workspace_set_kv_dtype")
+        self._kv_dtype = kv_dtype
+
+    def set_rope(self, inv_freq, interleaved=False):
+        """Rotary position of the following append() calls: radians per position of each pair (empty: none)."""
+        f = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64))
+        _need(f.ndim == 1, "inv_freq: one value for each rotated pair")
+        _check(lib().fi_workspace_set_rope(self._h, f.ctypes.data_as(POINTER(c_double)), 2 * f.shape[0],
+                                           int(interleaved)), "fi_workspace_set_rope")
 
     def plan(self, qo_indptr, kv_indptr, kv_indices, last_page_len, page_size, causal, stream=None):
         qo, kv, idx, last = _i32(qo_indptr), _i32(kv_indptr), _i32(kv_indices), _i32(last_page_len)
@@ -189,6 +236,7 @@ class Workspace:
             idx = np.zeros(1, np.int32)
         _check(lib().fi_plan(self._h, _p32(qo), _p32(kv), _p32(idx), _p32(last), qo.shape[0] - 1, self.num_qo_heads,
                              self.num_kv_heads, self.head_dim, page_size, int(causal), _stream_ptr(stream)), "fi_plan")
+        self._plan = (int(qo[-1]), qo.shape[0] - 1, page_size, self._layout, self._kv_dtype)
 
     def plan_composable(self, shared, unique, page_size, causal, stream=None):
         """Composable plan: shared and unique are (qo_indptr, kv_indptr, kv_indices, last_page_len)."""
@@ -200,6 +248,7 @@ class Workspace:
                                         _p32(uk), _p32(ui), _p32(ul), uq.shape[0] - 1, self.num_qo_heads,
                                         self.num_kv_heads, self.head_dim, page_size, int(causal), _stream_ptr(stream)),
                "fi_plan_composable")
+        self._plan = (int(uq[-1]), uq.shape[0] - 1, page_size, self._layout, self._kv_dtype)
 
     def run(self, q, k_pages, v_pages, o, lse, stream=None):
         _check(lib().fi_run(self._h, _dptr(q), _dptr(k_pages), _dptr(v_pages), int(k_pages.shape[0]), _dptr(o),
@@ -210,6 +259,77 @@ class Workspace:
         _check(lib().fi_run_merge(self._h, _dptr(q), _dptr(k_pages), _dptr(v_pages), int(k_pages.shape[0]),
                                   _dptr(o_prev), _dptr(lse_prev), _dptr(o), _dptr(lse), _stream_ptr(stream)),
                "fi_run_merge")
+
+    def _pages_shape(self, name: str, pages):
+        """Checks K/V pages against the current plan."""
+        if self._plan is None:
+            raise FiError(6, "cache operator")
+        _, _, ps, layout, dtype = self._plan
+        tail = (self.num_kv_heads, ps, self.head_dim) if layout == "HND" else (ps, self.num_kv_heads, self.head_dim)
+        _dense(pages, name, _BF16 if dtype == "bf16" else _E4M3)
+        _need(pages.dim() == 4 and tuple(pages.shape[1:]) == tail, f"{name}: shape {tuple(pages.shape)}, expected (pages, {', '.join(map(str, tail))})")
+
+    def _weights_shape(self, weights, num_pages=None):
+        if self._plan is None:
+            raise FiError(6, "cache operator")
+        n = weights.shape[0] if num_pages is None else num_pages
+        _dense(weights, "weights", _F32, (n, self.num_kv_heads, self._plan[2]))
+
+    def _rows(self, name: str, t, heads: int) -> int:
+        """Checks a [total_q, heads, 128] tensor with dense heads; returns its token stride in elements."""
+        n, d = self._plan[0], self.head_dim
+        _need(t.is_cuda and str(t.dtype) == "torch.bfloat16", f"{name}: a bfloat16 CUDA tensor is needed")
+        _need(tuple(t.shape) == (n, heads, d), f"{name}: shape {tuple(t.shape)}, expected {(n, heads, d)}")
+        st = t.stride()
+        _need(st[2] == 1 and (st[1] == d or heads == 1), f"{name}: the heads of a token must be contiguous")
+        return st[0] if n > 1 else max(st[0], heads * d)
+
+    def append(self, q, k, v, k_pages, v_pages, q_out, q_weight=None, k_weight=None, eps=1e-6, positions=None,
+               stream=None):
+        """Norm (with weights) and rotate q and k of the plan's tokens; write q_out and the K/V page slots."""
+        self._pages_shape("k_pages", k_pages)
+        self._pages_shape("v_pages", v_pages)
+        _need(v_pages.shape[0] == k_pages.shape[0], "k_pages and v_pages: the same number of pages is needed")
+        sq = self._rows("q", q, self.num_qo_heads)
+        sk, sv = self._rows("k", k, self.num_kv_heads), self._rows("v", v, self.num_kv_heads)
+        _dense(q_out, "q_out", _BF16, (self._plan[0], self.num_qo_heads, self.head_dim))
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is not None:
+                _dense(w, name, _BF16, (self.head_dim,))
+        if positions is not None:
+            _dense(positions, "positions", _I32, (self._plan[0],))
+        _check(lib().fi_append(self._h, _dptr(q), sq, _dptr(k), sk, _dptr(v), sv, _dptr(q_weight), _dptr(k_weight),
+                               float(eps), _dptr(positions), _dptr(q_out), _dptr(k_pages), _dptr(v_pages),
+                               int(k_pages.shape[0]), _stream_ptr(stream)), "fi_append")
+
+    def key_weights(self, q, k_pages, lse, weights, decay=1.0, new_keys=True, stream=None):
+        """Add the attention weight of each cached key (from q, K and run()'s lse) to the decayed sums in weights."""
+        self._pages_shape("k_pages", k_pages)
+        self._weights_shape(weights, k_pages.shape[0])
+        n = self._plan[0]
+        _dense(q, "q", _BF16, (n, self.num_qo_heads, self.head_dim))
+        _dense(lse, "lse", _F32, (n, self.num_qo_heads))
+        _check(lib().fi_key_weights(self._h, _dptr(q), _dptr(k_pages), int(k_pages.shape[0]), _dptr(lse), float(decay),
+                                    int(new_keys), _dptr(weights), _stream_ptr(stream)), "fi_key_weights")
+
+    def select_keys(self, weights, budget, kept, recent=0, sink=0, stream=None):
+        """kept[request, KV head] = the positions to keep: the first sink, the last recent, the heaviest of the rest."""
+        self._weights_shape(weights)
+        _dense(kept, "kept", _I32, (self._plan[1], self.num_kv_heads, int(budget)))
+        _check(lib().fi_select_keys(self._h, _dptr(weights), int(weights.shape[0]), int(sink), int(recent),
+                                    int(budget), _dptr(kept), _stream_ptr(stream)), "fi_select_keys")
+
+    def compact(self, kept, k_pages, v_pages, weights=None, stream=None):
+        """Move the kept K/V rows (and weights) of every request over the budget (kept's last size) to its first slots."""
+        self._pages_shape("k_pages", k_pages)
+        self._pages_shape("v_pages", v_pages)
+        _need(v_pages.shape[0] == k_pages.shape[0], "k_pages and v_pages: the same number of pages is needed")
+        if weights is not None:
+            self._weights_shape(weights, k_pages.shape[0])
+        _need(kept.dim() == 3, "kept: [batch, num_kv_heads, budget] is needed")
+        _dense(kept, "kept", _I32, (self._plan[1], self.num_kv_heads, kept.shape[2]))
+        _check(lib().fi_compact(self._h, _dptr(kept), int(kept.shape[2]), _dptr(k_pages), _dptr(v_pages),
+                                _dptr(weights), int(k_pages.shape[0]), _stream_ptr(stream)), "fi_compact")
 
     def info(self) -> np.ndarray:
         h = np.zeros(16, np.int32)

@@ -1,0 +1,102 @@
+// Cache operators that run on a workspace's plan: append of new tokens, accumulated attention
+// weights, selection of the keys to keep, compaction.  Parameter blocks and launchers (each returns
+// an fi_status).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace fi {
+
+// Geometry of one request of the plan (host and device); entry [batch] holds the totals in q0, kv0,
+// blk0 and tile0.
+struct Geo {
+  int32_t q0, lq;    // first query token, query tokens
+  int32_t kv0, lkv;  // first entry in the page list, keys
+  int32_t blk0;      // 32-key blocks of the requests before this one
+  int32_t tile0;     // 256-key tiles of the requests before this one
+  int32_t pad0, pad1;
+};
+constexpr int kBlkKeys = 32;
+constexpr int kTileKeys = 256;
+
+struct GeoTotals {
+  bool ok = false;     // the counts below fit the entries' 32-bit fields
+  int64_t blocks = 0;  // 32-key blocks
+  int64_t tiles = 0;   // 256-key tiles
+  int32_t max_lkv = 0;
+  int32_t max_lq = 0;
+};
+// The entries [0, batch] of a validated batch (cache_plan.cpp, host only, like the two checks).
+GeoTotals fill_geo(const int32_t* qo_indptr, const int32_t* kv_indptr, const int32_t* last_page_len, int batch,
+                   int page_size, Geo* out);
+// FI_OK if no page id (0 .. max_page) occurs twice in the two lists, else FI_ERR_UNSUPPORTED; FI_ERR_CAPACITY without host memory.
+int check_pages_once(const int32_t* a, int64_t na, const int32_t* b, int64_t nb, int32_t max_page);
+// FI_OK if no page takes new tokens (the last l_q keys of a request) from two places of the list.
+int check_tails_once(const Geo* geo, const int32_t* kv_indices, int batch, int page_size);
+// Radians per position -> the fraction of a turn per position, in 2^-64 turns.
+uint64_t turns_fraction(double inv_freq);
+
+struct PageView {  // the plan and the page pool, as every cache operator sees them
+  const Geo* geo;
+  const int32_t* header;
+  const int32_t* kv_indices;
+  int32_t* err;
+  int num_pages, page_size;
+  int page_shift;  // log2(page_size), or -1
+  int hkv;
+  // element strides of K/V pages
+  long long page_stride, head_stride, tok_stride;
+};
+
+constexpr int kMaxFreqs = 64;
+struct AppendParams {
+  PageView pv;
+  const void *q, *k, *v;
+  long long q_stride, k_stride, v_stride;  // elements between tokens
+  const void *q_weight, *k_weight;         // bf16 [128] or null
+  const int32_t* positions;                // or null
+  void* q_out;
+  void *k_pages, *v_pages;
+  float eps, k_inv_scale, v_inv_scale;
+  int hqo;
+  int rotary;       // rotated dims: a multiple of 16, 0 for none
+  int interleaved;  // pairs (2j, 2j + 1) instead of (j, j + rotary / 2)
+  uint64_t freq[kMaxFreqs];  // revolutions per position, as a 64-bit fraction of a turn
+};
+int launch_append(const AppendParams& p, int total_q, bool fp8, int num_sms, cudaStream_t stream);
+
+struct WeightsParams {
+  PageView pv;
+  const void* q;       // bf16 [total_q, hqo, 128]
+  const void* k_pages;
+  const float* lse;    // [total_q, hqo]
+  float* weights;      // [num_pages, hkv, page_size]
+  float decay;
+  int new_keys;        // 1: a request's last l_q keys start from zero
+  int hqo, group;
+  float scale_log2;    // logit scale in the log2 domain (includes k_scale)
+  float cap_log2, inv_cap_log2;  // soft-cap, 0 for none
+  int window_left;     // >= 0: sliding window
+};
+int launch_weights_rows(const WeightsParams& p, bool fp8, int64_t n_blk, int num_sms, cudaStream_t stream);
+
+struct SelectParams {
+  PageView pv;
+  const float* weights;
+  int32_t* kept;  // [batch, hkv, budget]
+  int sink, recent, budget;
+};
+int launch_select(const SelectParams& p, int batch, int max_lkv, int num_sms, cudaStream_t stream);
+
+struct CompactParams {
+  PageView pv;
+  const int32_t* kept;  // [batch, hkv, budget]
+  void *k_pages, *v_pages;
+  float* weights;  // or null
+  int budget;
+};
+int launch_compact(const CompactParams& p, int batch, bool fp8, int num_sms, cudaStream_t stream);
+
+}  // namespace fi

@@ -1,0 +1,77 @@
+// Host side of the cache operators: request geometry, page conditions, rotary frequencies.
+#include <algorithm>
+#include <cmath>
+#include <exception>
+#include <vector>
+
+#include "../../include/fi.h"
+#include "cache_ops.h"
+
+namespace fi {
+
+GeoTotals fill_geo(const int32_t* qo_indptr, const int32_t* kv_indptr, const int32_t* last_page_len, int batch,
+                   int page_size, Geo* out) {
+  GeoTotals t;
+  for (int i = 0; i <= batch; ++i) {
+    Geo g{};
+    g.q0 = qo_indptr[i];
+    g.kv0 = kv_indptr[i];
+    g.blk0 = int32_t(t.blocks);
+    g.tile0 = int32_t(t.tiles);
+    if (i < batch) {
+      const int32_t pages = kv_indptr[i + 1] - kv_indptr[i];
+      // at most 2^30, as the planner accepts
+      const int64_t keys = pages > 0 ? int64_t(pages - 1) * page_size + last_page_len[i] : 0;
+      g.lq = qo_indptr[i + 1] - qo_indptr[i];
+      g.lkv = int32_t(keys);
+      t.blocks += (keys + kBlkKeys - 1) / kBlkKeys;
+      t.tiles += (keys + kTileKeys - 1) / kTileKeys;
+      t.max_lkv = std::max(t.max_lkv, g.lkv);
+      t.max_lq = std::max(t.max_lq, g.lq);
+    }
+    out[i] = g;
+  }
+  t.ok = t.blocks <= INT32_MAX;
+  return t;
+}
+
+int check_pages_once(const int32_t* a, int64_t na, const int32_t* b, int64_t nb, int32_t max_page) {
+  try {
+    std::vector<bool> seen(size_t(max_page) + 1, false);
+    auto once = [&](const int32_t* idx, int64_t n) {
+      for (int64_t k = 0; k < n; ++k) {
+        if (seen[size_t(idx[k])]) return false;
+        seen[size_t(idx[k])] = true;
+      }
+      return true;
+    };
+    return once(a, na) && once(b, nb) ? FI_OK : FI_ERR_UNSUPPORTED;
+  } catch (const std::exception&) {
+    return FI_ERR_CAPACITY;
+  }
+}
+
+int check_tails_once(const Geo* geo, const int32_t* kv_indices, int batch, int page_size) {
+  try {
+    std::vector<int32_t> pages;
+    for (int i = 0; i < batch; ++i) {
+      const Geo& g = geo[i];
+      if (g.lq == 0 || g.lkv == 0) continue;
+      const int first = std::max(0, g.lkv - g.lq) / page_size, last = (g.lkv - 1) / page_size;
+      pages.insert(pages.end(), kv_indices + g.kv0 + first, kv_indices + g.kv0 + last + 1);
+    }
+    std::sort(pages.begin(), pages.end());
+    return std::adjacent_find(pages.begin(), pages.end()) == pages.end() ? FI_OK : FI_ERR_UNSUPPORTED;
+  } catch (const std::exception&) {
+    return FI_ERR_CAPACITY;
+  }
+}
+
+uint64_t turns_fraction(double inv_freq) {
+  double turns = inv_freq / 6.283185307179586476925286766559;
+  turns -= std::floor(turns);
+  const double scaled = std::ldexp(turns, 64);
+  return scaled >= 18446744073709551616.0 ? 0 : static_cast<uint64_t>(scaled);
+}
+
+}  // namespace fi

@@ -15,6 +15,7 @@
 #include <string>
 
 #include "../../include/fi.h"
+#include "cache_ops.h"
 #include "decode_launch.cuh"
 #include "merge_kernel.cuh"
 #include "plan.h"
@@ -52,7 +53,7 @@ struct fi_workspace {
 
   // segment byte offsets; [0, plan_bytes) is mirrored in pinned host memory.  The a_* segments and
   // the ext list hold the shared part of a composable plan.
-  size_t off_header = 0, off_cta = 0, off_items = 0, off_units = 0, off_slot_unit = 0, off_kv = 0, plan_bytes = 0;
+  size_t off_header = 0, off_cta = 0, off_geo = 0, off_items = 0, off_units = 0, off_slot_unit = 0, off_kv = 0, plan_bytes = 0;
   size_t off_a_header = 0, off_a_cta = 0, off_a_items = 0, off_a_kv = 0, off_ext = 0;
   int64_t max_ext = 0;
   size_t off_counters = 0, off_err = 0, off_part_lse = 0, off_part_o = 0, dev_bytes = 0;
@@ -68,6 +69,15 @@ struct fi_workspace {
   int32_t max_page = -1;
   int64_t plan_nnz = 0;
   int32_t plan_total_q = 0;
+
+  // the cache operators' view of the plan: geo entries (also in hbuf) and what the host checks of them
+  fi::GeoTotals geo;
+  int64_t plan_nnz_shared = 0;  // entries of a composable plan's shared page list
+  signed char pages_once = 0;   // every page listed once: 1 yes, -1 no, 0 not yet checked
+  signed char tails_once = 0;   // every page that takes new tokens takes them from one request
+  // rotary position, as set for fi_append
+  int rotary = 0, interleaved = 0;
+  uint64_t freq[fi::kMaxFreqs] = {0};
 };
 
 namespace {
@@ -96,6 +106,71 @@ int launch_decode(int grid, const fi::DecodeParams& p, cudaStream_t stream, bool
   return var ? fi::launch_decode_as<R, 0, kV>(grid, p, stream, pdl)
              : fi::launch_decode_as<R, 0, 0>(grid, p, stream, pdl);
 }
+
+// The requests of the (per-request) plan as the cache operators read them, into the pinned mirror.
+void set_geo(fi_workspace* ws, const int32_t* qo_indptr, const int32_t* kv_indptr, const int32_t* last_page_len,
+             int batch, int page_size) {
+  ws->geo = fi::fill_geo(qo_indptr, kv_indptr, last_page_len, batch, page_size,
+                         reinterpret_cast<fi::Geo*>(ws->hbuf + ws->off_geo));
+  ws->pages_once = ws->tails_once = 0;
+}
+
+// The conditions on pages are checked once per plan, when an operator first asks.
+int check_pages_once(fi_workspace* ws) {
+  if (ws->pages_once == 0) {
+    const int st = fi::check_pages_once(reinterpret_cast<const int32_t*>(ws->hbuf + ws->off_kv),
+                                        ws->plan_nnz - ws->plan_nnz_shared,
+                                        reinterpret_cast<const int32_t*>(ws->hbuf + ws->off_a_kv),
+                                        ws->plan_nnz_shared, ws->max_page);
+    if (st == FI_ERR_CAPACITY) return st;
+    ws->pages_once = st == FI_OK ? 1 : -1;
+  }
+  return ws->pages_once > 0 ? FI_OK : FI_ERR_UNSUPPORTED;
+}
+
+int check_tails_once(fi_workspace* ws) {
+  if (ws->tails_once == 0) {
+    const int st = fi::check_tails_once(reinterpret_cast<const fi::Geo*>(ws->hbuf + ws->off_geo),
+                                        reinterpret_cast<const int32_t*>(ws->hbuf + ws->off_kv),
+                                        ws->header[fi::H_BATCH], ws->header[fi::H_PAGE_SIZE]);
+    if (st == FI_ERR_CAPACITY) return st;
+    ws->tails_once = st == FI_OK ? 1 : -1;
+  }
+  return ws->tails_once > 0 ? FI_OK : FI_ERR_UNSUPPORTED;
+}
+
+// What every cache operator needs of a workspace: a plan, on the current device, whose pages lie in
+// the given pool.
+int check_cache_call(const fi_workspace* ws, int num_pages) {
+  if (ws == nullptr) return FI_ERR_INVALID_ARG;
+  if (!ws->has_plan) return FI_ERR_NO_PLAN;
+  if (!ws->geo.ok) return FI_ERR_UNSUPPORTED;
+  if (num_pages < 0 || ws->max_page >= num_pages) return FI_ERR_INVALID_ARG;
+  int dev = -1;
+  FI_CUDA(cudaGetDevice(&dev));
+  return dev == ws->device ? FI_OK : FI_ERR_INVALID_ARG;
+}
+
+fi::PageView page_view(const fi_workspace* ws, int num_pages) {
+  fi::PageView v{};
+  char* d = ws->dbuf;
+  const int ps = ws->header[fi::H_PAGE_SIZE];
+  const bool nhd = ws->plan_variant.kv_layout == FI_KV_LAYOUT_NHD;
+  v.geo = reinterpret_cast<const fi::Geo*>(d + ws->off_geo);
+  v.header = reinterpret_cast<const int32_t*>(d + ws->off_header);
+  v.kv_indices = reinterpret_cast<const int32_t*>(d + ws->off_kv);
+  v.err = reinterpret_cast<int32_t*>(d + ws->off_err);
+  v.num_pages = num_pages;
+  v.page_size = ps;
+  v.page_shift = (ps & (ps - 1)) == 0 ? __builtin_ctz(unsigned(ps)) : -1;
+  v.hkv = ws->hkv;
+  v.page_stride = (long long)ws->hkv * ps * fi::kHeadDim;
+  v.head_stride = nhd ? fi::kHeadDim : (long long)ps * fi::kHeadDim;
+  v.tok_stride = nhd ? (long long)ws->hkv * fi::kHeadDim : fi::kHeadDim;
+  return v;
+}
+
+bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
 bool var_on(const fi::Variant& v) { return v.window_left >= 0 || v.soft_cap > 0.f; }
 
@@ -164,6 +239,7 @@ int fi_workspace_create(int max_batch, int max_total_q, int max_kv_pages, int nu
   };
   ws->off_header = seg(sizeof(int32_t) * fi::kHeaderLen);
   ws->off_cta = seg(sizeof(int32_t) * (ws->max_ctas + 1));
+  ws->off_geo = seg(sizeof(fi::Geo) * (size_t(max_batch) + 1));
   ws->off_items = seg(sizeof(int32_t) * fi::kItemFields * ws->max_items);
   ws->off_units = seg(sizeof(int32_t) * fi::kUnitFields * ws->max_units);
   ws->off_slot_unit = seg(sizeof(int32_t) * ws->max_slots);
@@ -277,6 +353,7 @@ int fi_plan(fi_workspace* ws, const int32_t* qo_indptr, const int32_t* kv_indptr
   char* h = ws->hbuf;
   std::memcpy(h + ws->off_header, plan.header, sizeof(plan.header));
   std::memcpy(h + ws->off_cta, plan.cta_indptr.data(), plan.cta_indptr.size() * sizeof(int32_t));
+  set_geo(ws, qo_indptr, kv_indptr, last_page_len, batch, page_size);
   if (n_items) std::memcpy(h + ws->off_items, plan.items.data(), plan.items.size() * sizeof(int32_t));
   if (n_units) std::memcpy(h + ws->off_units, plan.units.data(), plan.units.size() * sizeof(int32_t));
   if (n_slots) std::memcpy(h + ws->off_slot_unit, plan.slot_unit.data(), plan.slot_unit.size() * sizeof(int32_t));
@@ -287,6 +364,7 @@ int fi_plan(fi_workspace* ws, const int32_t* qo_indptr, const int32_t* kv_indptr
   } segs[] = {
       {ws->off_header, sizeof(plan.header)},
       {ws->off_cta, plan.cta_indptr.size() * sizeof(int32_t)},
+      {ws->off_geo, (size_t(batch) + 1) * sizeof(fi::Geo)},
       {ws->off_items, plan.items.size() * sizeof(int32_t)},
       {ws->off_units, plan.units.size() * sizeof(int32_t)},
       {ws->off_slot_unit, plan.slot_unit.size() * sizeof(int32_t)},
@@ -314,6 +392,7 @@ int fi_plan(fi_workspace* ws, const int32_t* qo_indptr, const int32_t* kv_indptr
   std::memcpy(ws->header, plan.header, sizeof(plan.header));
   ws->max_page = max_page;
   ws->plan_nnz = nnz;
+  ws->plan_nnz_shared = 0;
   ws->plan_total_q = qo_indptr[batch];
   ws->has_plan = true;
   ws->composable = false;
@@ -381,6 +460,7 @@ int fi_plan_composable(fi_workspace* ws, const int32_t* shared_qo_indptr, const 
   } segs[] = {
       {ws->off_header, pb.header, sizeof(pb.header)},
       {ws->off_cta, pb.cta_indptr.data(), pb.cta_indptr.size() * sizeof(int32_t)},
+      {ws->off_geo, nullptr, (size_t(batch) + 1) * sizeof(fi::Geo)},  // already in the mirror
       {ws->off_items, pb.items.data(), pb.items.size() * sizeof(int32_t)},
       {ws->off_units, pb.units.data(), pb.units.size() * sizeof(int32_t)},
       {ws->off_slot_unit, pb.slot_unit.data(), pb.slot_unit.size() * sizeof(int32_t)},
@@ -391,9 +471,10 @@ int fi_plan_composable(fi_workspace* ws, const int32_t* shared_qo_indptr, const 
       {ws->off_a_kv, shared_kv_indices, size_t(nnz_a) * sizeof(int32_t)},
       {ws->off_ext, cp.ext.data(), cp.ext.size() * sizeof(int32_t)},
   };
+  set_geo(ws, qo_indptr, kv_indptr, last_page_len, batch, page_size);
   for (const Seg& sg : segs) {
     if (sg.bytes == 0) continue;
-    std::memcpy(h + sg.off, sg.src, sg.bytes);
+    if (sg.src != nullptr) std::memcpy(h + sg.off, sg.src, sg.bytes);
     FI_CUDA(cudaMemcpyAsync(ws->dbuf + sg.off, h + sg.off, sg.bytes, cudaMemcpyHostToDevice, s));
   }
   FI_CUDA(cudaEventRecord(ws->copy_done, s));
@@ -403,6 +484,7 @@ int fi_plan_composable(fi_workspace* ws, const int32_t* shared_qo_indptr, const 
   std::memcpy(ws->a_header, pa.header, sizeof(pa.header));
   ws->max_page = max_page;
   ws->plan_nnz = nnz_a + nnz_b;
+  ws->plan_nnz_shared = nnz_a;
   ws->plan_total_q = qo_indptr[batch];
   ws->has_plan = true;
   ws->composable = true;
@@ -630,6 +712,168 @@ int fi_merge_states(const void* o_a, const float* lse_a, const void* o_b, const 
       static_cast<__nv_bfloat16*>(o), lse, n);
   FI_CUDA(cudaGetLastError());
   return FI_OK;
+}
+
+int fi_workspace_set_rope(fi_workspace* ws, const double* inv_freq, int32_t rotary_dim, int32_t interleaved) {
+  if (ws == nullptr || rotary_dim < 0 || rotary_dim > ws->head_dim || rotary_dim % 2 != 0 ||
+      (interleaved != 0 && interleaved != 1) || (rotary_dim > 0 && inv_freq == nullptr))
+    return FI_ERR_INVALID_ARG;
+  if (rotary_dim % 16 != 0) return FI_ERR_UNSUPPORTED;
+  uint64_t freq[fi::kMaxFreqs] = {0};
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    if (!std::isfinite(inv_freq[i])) return FI_ERR_INVALID_ARG;
+    freq[i] = fi::turns_fraction(inv_freq[i]);
+  }
+  std::memcpy(ws->freq, freq, sizeof(freq));
+  ws->rotary = rotary_dim;
+  ws->interleaved = interleaved;
+  return FI_OK;
+}
+
+int fi_cache_plan_compute(const int32_t* qo_indptr, const int32_t* kv_indptr, const int32_t* kv_indices,
+                          const int32_t* last_page_len, int batch, int page_size, int32_t* geo, int32_t* twice) {
+  if (geo == nullptr || twice == nullptr) return FI_ERR_INVALID_ARG;
+  fi::PlanInput in{qo_indptr, kv_indptr, last_page_len, batch, 1, 1, fi::kHeadDim, page_size, 0, 1};
+  int st = fi::validate_input(in);
+  if (st != FI_OK) return st;
+  const int64_t nnz = kv_indptr[batch];
+  if (nnz > 0 && kv_indices == nullptr) return FI_ERR_INVALID_ARG;
+  int32_t max_page = -1;
+  for (int64_t k = 0; k < nnz; ++k) {
+    if (kv_indices[k] < 0) return FI_ERR_INVALID_ARG;
+    max_page = std::max(max_page, kv_indices[k]);
+  }
+  for (int i = 0; i < batch; ++i)
+    if (int64_t(kv_indptr[i + 1] - kv_indptr[i]) * page_size > (int64_t(1) << 30) + page_size) return FI_ERR_UNSUPPORTED;
+  fi::Geo* out = reinterpret_cast<fi::Geo*>(geo);
+  if (!fi::fill_geo(qo_indptr, kv_indptr, last_page_len, batch, page_size, out).ok) return FI_ERR_UNSUPPORTED;
+  twice[0] = twice[1] = 0;
+  st = fi::check_pages_once(kv_indices, nnz, nullptr, 0, max_page);
+  if (st == FI_ERR_CAPACITY) return st;
+  twice[0] = st != FI_OK;
+  st = fi::check_tails_once(out, kv_indices, batch, page_size);
+  if (st == FI_ERR_CAPACITY) return st;
+  twice[1] = st != FI_OK;
+  return FI_OK;
+}
+
+int fi_append(fi_workspace* ws, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+              int64_t v_stride, const void* q_weight, const void* k_weight, float eps, const int32_t* positions,
+              void* q_out, void* k_pages, void* v_pages, int num_pages, void* stream) {
+  int st = check_cache_call(ws, num_pages);
+  if (st != FI_OK) return st;
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return FI_ERR_INVALID_ARG;
+  const int total_q = ws->plan_total_q;
+  if (total_q == 0) return FI_OK;
+  const int64_t dq = int64_t(ws->hqo) * fi::kHeadDim, dkv = int64_t(ws->hkv) * fi::kHeadDim;
+  if (q == nullptr || k == nullptr || v == nullptr || q_out == nullptr) return FI_ERR_INVALID_ARG;
+  if (ws->plan_nnz > 0 && (k_pages == nullptr || v_pages == nullptr)) return FI_ERR_INVALID_ARG;
+  if (q_stride < dq || k_stride < dkv || v_stride < dkv || q_stride % 8 || k_stride % 8 || v_stride % 8)
+    return FI_ERR_INVALID_ARG;
+  for (const void* a : {q, k, v, q_weight, k_weight, static_cast<const void*>(q_out),
+                        static_cast<const void*>(k_pages), static_cast<const void*>(v_pages)})
+    if (misaligned(a, 16)) return FI_ERR_INVALID_ARG;
+  if (misaligned(positions, 4)) return FI_ERR_INVALID_ARG;
+  if (ws->composable && positions == nullptr) return FI_ERR_INVALID_ARG;  // the shared keys come before the own ones
+  st = check_tails_once(ws);
+  if (st != FI_OK) return st;
+  fi::AppendParams p{};
+  p.pv = page_view(ws, num_pages);
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.positions = positions;
+  p.q_out = q_out;
+  p.k_pages = k_pages;
+  p.v_pages = v_pages;
+  p.eps = eps;
+  p.k_inv_scale = 1.f / ws->plan_variant.k_scale;
+  p.v_inv_scale = 1.f / ws->plan_variant.v_scale;
+  p.hqo = ws->hqo;
+  p.rotary = ws->rotary;
+  p.interleaved = ws->interleaved;
+  std::memcpy(p.freq, ws->freq, sizeof(p.freq));
+  return fi::launch_append(p, total_q, ws->plan_variant.kv_dtype == FI_KV_DTYPE_E4M3, ws->num_sms,
+                           static_cast<cudaStream_t>(stream));
+}
+
+int fi_key_weights(fi_workspace* ws, const void* q, const void* k_pages, int num_pages, const float* lse, float decay,
+                   int32_t new_keys, float* weights, void* stream) {
+  int st = check_cache_call(ws, num_pages);
+  if (st != FI_OK) return st;
+  if (!(decay >= 0.f && decay <= 1.f) || (new_keys != 0 && new_keys != 1)) return FI_ERR_INVALID_ARG;
+  if (ws->plan_nnz - ws->plan_nnz_shared == 0) return FI_OK;  // no key to weigh
+  if (k_pages == nullptr || weights == nullptr || (ws->plan_total_q > 0 && (q == nullptr || lse == nullptr)))
+    return FI_ERR_INVALID_ARG;
+  if (misaligned(q, 16) || misaligned(k_pages, 16) || misaligned(lse, 4) || misaligned(weights, 4))
+    return FI_ERR_INVALID_ARG;
+  st = check_pages_once(ws);
+  if (st != FI_OK) return st;
+  const fi::Variant& var = ws->plan_variant;
+  fi::WeightsParams p{};
+  p.pv = page_view(ws, num_pages);
+  p.q = q;
+  p.k_pages = k_pages;
+  p.lse = lse;
+  p.weights = weights;
+  p.decay = decay;
+  p.new_keys = new_keys;
+  p.hqo = ws->hqo;
+  p.group = ws->hqo / ws->hkv;
+  p.scale_log2 = fi::kLog2e / std::sqrt(float(ws->head_dim));
+  const bool fp8 = var.kv_dtype == FI_KV_DTYPE_E4M3;
+  if (fp8) p.scale_log2 *= var.k_scale;
+  p.cap_log2 = var.soft_cap > 0.f ? var.soft_cap * fi::kLog2e : 0.f;
+  p.inv_cap_log2 = var.soft_cap > 0.f ? 1.f / p.cap_log2 : 0.f;
+  p.window_left = var.window_left;
+  return fi::launch_weights_rows(p, fp8, ws->geo.blocks, ws->num_sms, static_cast<cudaStream_t>(stream));
+}
+
+int fi_select_keys(fi_workspace* ws, const float* weights, int num_pages, int32_t sink, int32_t recent, int32_t budget,
+                   int32_t* kept, void* stream) {
+  const int st = check_cache_call(ws, num_pages);
+  if (st != FI_OK) return st;
+  if (sink < 0 || recent < 0 || budget < 1 || int64_t(sink) + recent > budget) return FI_ERR_INVALID_ARG;
+  const int batch = ws->header[fi::H_BATCH];
+  if (batch == 0) return FI_OK;
+  if (kept == nullptr || (ws->plan_nnz - ws->plan_nnz_shared > 0 && weights == nullptr)) return FI_ERR_INVALID_ARG;
+  if (misaligned(weights, 4) || misaligned(kept, 4)) return FI_ERR_INVALID_ARG;
+  fi::SelectParams p{};
+  p.pv = page_view(ws, num_pages);
+  p.weights = weights;
+  p.kept = kept;
+  p.sink = sink;
+  p.recent = recent;
+  p.budget = budget;
+  return fi::launch_select(p, batch, ws->geo.max_lkv, ws->num_sms, static_cast<cudaStream_t>(stream));
+}
+
+int fi_compact(fi_workspace* ws, const int32_t* kept, int32_t budget, void* k_pages, void* v_pages, float* weights,
+               int num_pages, void* stream) {
+  int st = check_cache_call(ws, num_pages);
+  if (st != FI_OK) return st;
+  if (budget < 1) return FI_ERR_INVALID_ARG;
+  const int batch = ws->header[fi::H_BATCH];
+  if (batch == 0 || ws->plan_nnz - ws->plan_nnz_shared == 0) return FI_OK;
+  if (kept == nullptr || k_pages == nullptr || v_pages == nullptr || misaligned(kept, 4) || misaligned(k_pages, 16) ||
+      misaligned(v_pages, 16) || misaligned(weights, 4))
+    return FI_ERR_INVALID_ARG;
+  st = check_pages_once(ws);
+  if (st != FI_OK) return st;
+  fi::CompactParams p{};
+  p.pv = page_view(ws, num_pages);
+  p.kept = kept;
+  p.k_pages = k_pages;
+  p.v_pages = v_pages;
+  p.weights = weights;
+  p.budget = budget;
+  return fi::launch_compact(p, batch, ws->plan_variant.kv_dtype == FI_KV_DTYPE_E4M3, ws->num_sms,
+                            static_cast<cudaStream_t>(stream));
 }
 
 int fi_get_error(fi_workspace* ws, int32_t* err_bits) {

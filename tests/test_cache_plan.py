@@ -1,0 +1,65 @@
+"""Host side of the cache operators (no GPU): request geometry, page conditions, refusals of the binding."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from oracle import cache as C
+from serving_attention_plan_gb300 import binding as B
+from serving_attention_plan_gb300 import build as BLD
+from serving_attention_plan_gb300 import workloads as W
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    BLD.build()
+    B.lib()
+
+
+@pytest.mark.parametrize("seed,batch,ps,ql,kl", [(0, 1, 16, (1, 1), (1, 1)), (1, 7, 16, (0, 40), (0, 700)),
+                                                 (2, 130, 1, (1, 1), (0, 90)), (3, 3, 5, (2, 9), (0, 31))])
+def test_geometry(seed, batch, ps, ql, kl):
+    b = W.random_small_batch(seed, batch, 4, 2, ps, False, ql, kl)
+    geo, pages_twice, tails_twice = B.cache_plan_compute(b.qo_indptr, b.kv_indptr, b.kv_indices, b.last_page_len, ps)
+    l_q, l_kv = C.lengths(b)
+    assert np.array_equal(geo[:, 0], b.qo_indptr) and np.array_equal(geo[:, 2], b.kv_indptr)
+    assert np.array_equal(geo[:-1, 1], l_q) and np.array_equal(geo[:-1, 3], l_kv)
+    assert np.array_equal(geo[:, 4], np.concatenate([[0], np.cumsum(-(-l_kv // 32))]))
+    assert np.array_equal(geo[:, 5], np.concatenate([[0], np.cumsum(-(-l_kv // 256))]))
+    assert not pages_twice and not tails_twice
+
+
+@pytest.mark.parametrize("lists,q,last,pages,tails", [
+    ([[0, 1], [0, 2]], [1, 1], [3, 4], True, False),      # a shared full prefix page, own tails
+    ([[0, 1], [2, 1]], [1, 1], [3, 4], True, True),       # a shared tail
+    ([[0, 1], [2, 1]], [1, 0], [3, 4], True, False),      # a shared tail that only one request writes
+    ([[0, 0]], [1], [2], True, False),                    # the same page twice, one token
+    ([[0, 0]], [5], [2], True, True),                     # the same page twice, both written
+    ([[], [3]], [2, 1], [0, 1], False, False),            # a request without pages
+])
+def test_page_conditions(lists, q, last, pages, tails):
+    kv = np.concatenate([[0], np.cumsum([len(x) for x in lists])])
+    got = B.cache_plan_compute(np.concatenate([[0], np.cumsum(q)]), kv, [p for x in lists for p in x], last, 4)
+    assert got[1:] == (pages, tails)
+
+
+def test_bad_batches_are_refused():
+    for args in (([0, 1], [0, 1], [-1], [1]), ([0, 1], [0, 1], [0], [5]), ([0, 1], [0, 1], [0], [0]),
+                 ([1, 1], [0, 1], [0], [1]), ([0, 1], [1, 0], [0], [1])):
+        with pytest.raises(B.FiError) as e:
+            B.cache_plan_compute(*args, 4)
+        assert e.value.status == 1
+    with pytest.raises(B.FiError) as e:  # a key position above 2^30
+        B.cache_plan_compute([0, 1], [0, 3], [0, 1, 2], [1], 1 << 30)
+    assert e.value.status == 3
+
+
+def test_null_workspace_and_pointers():
+    L = B.lib()
+    z = ctypes.c_void_p(0)
+    assert L.fi_workspace_set_rope(z, None, 0, 0) == 1
+    assert L.fi_append(z, z, 0, z, 0, z, 0, z, z, 0.0, z, z, z, z, 0, z) == 1
+    assert L.fi_key_weights(z, z, z, 0, z, 1.0, 0, z, z) == 1
+    assert L.fi_select_keys(z, z, 0, 0, 0, 1, z, z) == 1
+    assert L.fi_compact(z, z, 1, z, z, z, 0, z) == 1
+    assert L.fi_cache_plan_compute(None, None, None, None, 0, 1, None, None) == 1

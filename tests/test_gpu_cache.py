@@ -1,0 +1,650 @@
+"""GPU parity of the cache operators (append, key weights, selection, compaction) against the float64 oracle."""
+import dataclasses
+
+import numpy as np
+import pytest
+
+from oracle import attention as A
+from oracle import cache as C
+from serving_attention_plan_gb300 import workloads as W
+
+from .gpu_helpers import torch_mod
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from serving_attention_plan_gb300 import build
+    build.build()
+    assert torch_mod().cuda.is_available()
+
+
+def bf16(bits):
+    torch = torch_mod()
+    return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).cuda().view(torch.bfloat16)
+
+
+def dev(a):
+    return torch_mod().from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def f64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def bits(t):
+    return t.view(torch_mod().int16).cpu().numpy().view(np.uint16)
+
+
+def batch_of(lq, lkv, hq, hk, ps, causal=False, seed=0, extra=3, scale=1.0):
+    rng = np.random.default_rng(seed)
+    n = sum(-(-x // ps) for x in lkv)
+    return W.make_paged_batch(rng, "cache", lq, lkv, hq, hk, ps, causal, pool_pages=n + extra, scale=scale)
+
+
+def as_layout(a, layout):
+    return a if layout == "HND" else np.ascontiguousarray(a.transpose(0, 2, 1, 3))
+
+
+def workspace(b, window=-1, cap=0.0, layout="HND", dtype="bf16", scales=(1.0, 1.0), num_sms=0):
+    from serving_attention_plan_gb300 import binding as B
+    ws = B.Workspace(max(b.batch_size, 1), max(b.total_q, 1), max(int(b.kv_indptr[-1]), 1), b.num_qo_heads,
+                     b.num_kv_heads, 128, num_sms)
+    ws.set_variant(window, cap, layout)
+    ws.set_kv_dtype(dtype, *scales)
+    ws.plan(b.qo_indptr, b.kv_indptr, b.kv_indices, b.last_page_len, b.page_size, b.causal)
+    return ws
+
+
+# ---- append ----------------------------------------------------------------------------------------
+
+APPEND = [
+    # lq, lkv, hq, hk, page, dtype, layout, rotary, interleaved, norm, fused, first position
+    ([1], [1], 1, 1, 1, "bf16", "HND", 128, False, True, False, 0),
+    ([1, 1, 1, 1], [37, 128, 255, 512], 8, 2, 16, "bf16", "HND", 128, False, True, True, 0),
+    ([1, 0, 2, 1], [5, 9, 2, 300], 4, 4, 5, "bf16", "HND", 64, True, True, True, 1_000_003),
+    ([33, 0, 129, 5], [33, 4, 500, 3], 12, 4, 8, "bf16", "NHD", 96, False, False, True, 100_000),
+    ([70, 1], [70, 65], 40, 8, 64, "e4m3", "NHD", 32, True, True, False, 7),
+    ([17, 40], [20, 41], 16, 1, 32, "e4m3", "HND", 16, False, False, True, 131_071),
+    ([9] * 150, [9] * 150, 8, 8, 16, "bf16", "HND", 128, True, False, True, 5),   # four tokens a step, odd batches
+    ([300, 961], [300, 1000], 16, 8, 16, "bf16", "HND", 0, False, True, True, 0),
+    ([1300, 11], [1300, 11], 2, 2, 128, "e4m3", "NHD", 112, False, True, True, 2_000_000_000),
+]
+
+
+@pytest.mark.parametrize("case", APPEND, ids=range(len(APPEND)))
+def test_append(case):
+    torch = torch_mod()
+    lq, lkv, hq, hk, ps, dtype, layout, rotary, inter, norm, fused, first = case
+    b = batch_of(lq, lkv, hq, hk, ps, False, seed=len(lq) + ps)
+    rng = np.random.default_rng(11)
+    n = b.total_q
+    x = rng.standard_normal((n, hq + 2 * hk, 128)).astype(np.float32) * 2
+    raw = bf16(W.f32_to_bf16_bits(x))
+    x = f64(raw)
+    q, k, v = raw[:, :hq], raw[:, hq:hq + hk], raw[:, hq + hk:]
+    if not fused:
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+    wq, wk = (bf16(W.f32_to_bf16_bits(1 + 0.3 * rng.standard_normal(128).astype(np.float32))) for _ in range(2))
+    inv_freq = 10000.0 ** (-np.arange(0, rotary, 2) / max(rotary, 1))
+    tok, page, slot, key = C.append_places(b)
+    positions = key + first
+    scales = (0.03125, 0.0625) if dtype == "e4m3" else (1.0, 1.0)
+    ws = workspace(b, layout=layout, dtype=dtype, scales=scales)
+    ws.set_rope(inv_freq, inter)
+    if dtype == "bf16":
+        k0, v0 = as_layout(b.k_pages, layout), as_layout(b.v_pages, layout)
+        kp, vp = bf16(k0), bf16(v0)
+    else:
+        k0, v0 = (as_layout(rng.integers(0, 127, size=b.k_pages.shape).astype(np.uint8), layout) for _ in range(2))
+        kp, vp = dev(k0), dev(v0)
+    out = torch.full((n, hq, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    ws.append(q, k, v, kp, vp, out, wq if norm else None, wk if norm else None, 1e-5,
+              dev(positions.astype(np.int32)) if first else None)
+    torch.cuda.synchronize()
+    assert ws.get_error() == 0
+    rq = C.norm_rotate(x[:, :hq], f64(wq) if norm else None, 1e-5, inv_freq, positions.astype(np.float64), inter)
+    rk = C.norm_rotate(x[:, hq:hq + hk], f64(wk) if norm else None, 1e-5, inv_freq, positions.astype(np.float64), inter)
+    rv = x[:, hq + hk:]
+    # fp32 steps before the rounding: a dozen of half a unit each of values up to the row's largest, and the
+    # angle (2^-25 turns after the fp32 rounding of the fraction): 2^-19 of the row's largest covers both
+    slack = lambda r: np.abs(r).max(-1, keepdims=True) * 2.0 ** -19
+    assert (np.abs(f64(out) - rq) <= np.abs(rq) * 2.0 ** -8 + slack(rq)).all()
+    for got, before, ref, scale in ((kp, k0, rk, scales[0]), (vp, v0, rv, scales[1])):
+        host = bits(got) if dtype == "bf16" else got.cpu().numpy()
+        rows = host[page, :, slot] if layout == "HND" else host[page, slot]
+        ref = ref[tok]
+        if dtype == "bf16":
+            assert (np.abs(A.bf16_to_f64(rows) - ref) <= np.abs(ref) * 2.0 ** -8 + slack(ref)).all()
+        else:
+            lim = np.clip(ref / scale, -448, 448)
+            # half a step: 2^-4 of a normal value, 2^-10 below the smallest normal
+            assert (np.abs(A.e4m3_to_f64(rows) - lim) <= np.maximum(np.abs(lim) * 2.0 ** -4, 2.0 ** -10) + slack(ref) / scale).all()
+        # every other slot is as it was
+        rest = np.ones(host.shape[:1] + (ps,), bool)
+        rest[page, slot] = False
+        a, z = (host.transpose(0, 2, 1, 3), before.transpose(0, 2, 1, 3)) if layout == "HND" else (host, before)
+        assert np.array_equal(a[rest], z[rest])
+
+
+def test_append_in_place_q_and_saturation():
+    """q_out is q; e4m3 saturates at +-448 and infinities with it; NaN becomes the NaN code; -0 and denormal inputs pass."""
+    torch = torch_mod()
+    b = batch_of([1, 1], [4, 7], 2, 1, 4)
+    ws = workspace(b, dtype="e4m3", scales=(1.0, 1.0))
+    q = torch.randn(2, 2, 128, device="cuda").to(torch.bfloat16)
+    want = q.clone()
+    k = torch.zeros(2, 1, 128, device="cuda", dtype=torch.bfloat16)
+    k[0, 0, :6] = torch.tensor([1e30, -1e30, float("inf"), -float("inf"), float("nan"), -0.0])
+    kp, vp = (torch.zeros(b.num_pages, 1, 4, 128, dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2))
+    ws.append(q, k, k, kp, vp, q)
+    torch.cuda.synchronize()
+    assert torch.equal(q, want)
+    _, page, slot, _ = C.append_places(b)
+    row = kp[page[0], 0, slot[0]].float().cpu()
+    assert row[:4].tolist() == [448, -448, 448, -448] and torch.isnan(row[4]) and row[5] == 0 and torch.signbit(row[5])
+    assert torch.equal(kp.view(torch.uint8), vp.view(torch.uint8))
+
+
+# ---- key weights -----------------------------------------------------------------------------------
+
+WEIGHTS = [
+    # lq, lkv, hq, hk, page, causal, dtype, layout, window, cap, decay, new keys, SM budget
+    ([1], [1], 1, 1, 1, False, "bf16", "HND", -1, 0.0, 1.0, True, 0),
+    ([1] * 4, [37, 128, 255, 512], 8, 2, 16, False, "bf16", "HND", -1, 0.0, 0.9, False, 0),
+    ([1, 0, 1, 2], [33, 64, 0, 700], 16, 4, 5, True, "bf16", "HND", -1, 0.0, 0.5, True, 1),
+    ([1, 1], [900, 31], 64, 8, 1, False, "e4m3", "HND", -1, 30.0, 0.0, True, 3),
+    ([2, 1], [300, 257], 20, 5, 4, True, "bf16", "HND", 40, 0.0, 0.75, True, 0),
+    ([1, 1, 1], [32, 63, 65], 6, 2, 8, False, "e4m3", "NHD", -1, 0.0, 1.0, True, 0),
+    ([17, 40, 0], [17, 300, 5], 8, 2, 16, True, "bf16", "HND", -1, 0.0, 0.9, True, 0),
+    ([130, 1], [130, 700], 32, 8, 16, True, "bf16", "NHD", -1, 0.0, 1.0, False, 5),
+    ([257, 9], [513, 9], 10, 2, 32, True, "e4m3", "HND", -1, 20.0, 0.3, True, 0),
+    ([200, 64], [600, 64], 12, 4, 8, True, "bf16", "HND", 128, 5.0, 1.0, True, 2),
+    ([40, 20], [10, 300], 8, 8, 64, True, "bf16", "HND", -1, 0.0, 0.9, True, 0),   # rows that see no key
+    ([66, 3], [200, 129], 16, 16, 128, False, "e4m3", "NHD", -1, 0.0, 0.9, False, 0),
+    ([5, 9], [290, 70], 130, 1, 16, True, "bf16", "HND", -1, 0.0, 1.0, True, 0),   # 130 heads a group
+    ([520], [1100], 4, 1, 16, True, "bf16", "HND", -1, 0.0, 1.0, True, 0),
+]
+
+
+def lse_of(b, q, kp, k_scale, window, cap, layout):
+    """float32 log-sum-exp per row, from the definition."""
+    l_q, l_kv = C.lengths(b)
+    g = b.num_qo_heads // b.num_kv_heads
+    lse = np.full((b.total_q, b.num_qo_heads), -np.inf)
+    for i in range(b.batch_size):
+        n, t = int(l_kv[i]), int(l_q[i])
+        if n == 0 or t == 0:
+            continue
+        rows = slice(int(b.qo_indptr[i]), int(b.qo_indptr[i]) + t)
+        pos, j = n - t + np.arange(t)[:, None], np.arange(n)[None, :]
+        seen = (j <= pos) & ((j >= pos - window) | (window < 0)) if b.causal else np.ones((t, n), bool)
+        for h in range(b.num_qo_heads):
+            x = q[rows, h] @ (A.gather_kv(kp, b.kv_indptr, b.kv_indices, n, b.page_size, i, h // g, layout) * k_scale).T
+            x /= np.sqrt(128)
+            x = cap * np.tanh(x / cap) if cap else x
+            with np.errstate(divide="ignore"):
+                lse[rows, h] = np.log(np.where(seen, np.exp(x), 0).sum(1))
+    return lse.astype(np.float32)
+
+
+def weights_case(case, seed=5):
+    lq, lkv, hq, hk, ps, causal, dtype, layout, window, cap, decay, new, sms = case
+    b = batch_of(lq, lkv, hq, hk, ps, causal, seed=seed, scale=1.3)
+    rng = np.random.default_rng(3)
+    k_scale = 0.03125 if dtype == "e4m3" else 1.0
+    k = b.k_pages if dtype == "bf16" else W.to_e4m3(A.bf16_to_f64(b.k_pages) / k_scale)
+    k = as_layout(k, layout)
+    q = A.bf16_to_f64(b.q)
+    lse = lse_of(b, q, k, k_scale, window, cap, layout)
+    old = rng.random((b.num_pages, hk, ps)).astype(np.float32) * 3
+    return b, q, k, k_scale, lse, old
+
+
+def weights_tol(reach, lse):
+    """Relative error of one term: the logit's fp32 sum (128 products, each sum up to a unit in the last place of the
+    largest partial sum), the exponent's own roundings and the exponential (2^-21)."""
+    big = float(np.abs(np.where(np.isfinite(lse), lse, 0)).max(initial=0.0))
+    return reach * 128 * 2.0 ** -23 + (reach + big) * 2.0 ** -21 + 2.0 ** -20
+
+
+@pytest.mark.parametrize("case", WEIGHTS, ids=range(len(WEIGHTS)))
+def test_key_weights(case):
+    torch = torch_mod()
+    lq, lkv, hq, hk, ps, causal, dtype, layout, window, cap, decay, new, sms = case
+    b, q, k, k_scale, lse, old = weights_case(case)
+    # what must not be read: new keys' former sums (with new_keys), slots no key has, with NaN in both
+    _, l_kv = C.lengths(b)
+    l_q, _ = C.lengths(b)
+    used = np.zeros((b.num_pages, ps), bool)
+    start = old.copy()
+    for i in range(b.batch_size):
+        p, s = C.places(b, i, np.arange(int(l_kv[i])))
+        used[p, s] = True
+        if new:
+            p, s = C.places(b, i, np.arange(max(0, int(l_kv[i] - l_q[i])), int(l_kv[i])))
+            start[p, :, s] = np.nan
+    start.transpose(0, 2, 1)[~used] = np.nan
+    if decay == 0.0:
+        start[:] = np.nan
+    k = k.copy()
+    nan = 0x7FFF if dtype == "bf16" else 0x7F
+    (k.transpose(0, 2, 1, 3) if layout == "HND" else k)[~used] = nan
+    ws = workspace(b, window, cap, layout, dtype, (k_scale, 1.0), sms)
+    w = dev(start)
+    kd = bf16(k) if dtype == "bf16" else dev(k)
+    ws.key_weights(bf16(b.q), kd, dev(lse), w, decay, new)
+    torch.cuda.synchronize()
+    assert ws.get_error() == 0
+    ref, reach = C.key_weights(b, q, k, lse, old, decay, new, k_scale, window, cap, layout)
+    got = w.cpu().numpy()
+    assert np.isnan(got.transpose(0, 2, 1)[~used]).all()
+    g, r = got.transpose(0, 2, 1)[used].astype(np.float64), ref.transpose(0, 2, 1)[used]
+    tol = weights_tol(reach, lse)
+    # sums of n terms in fp32: n / 2 half units more at the very worst order
+    n = max(lq) * (hq // hk)
+    assert (np.abs(g - r) <= r * (tol + n * 2.0 ** -24) + 1e-30).all(), (np.abs(g - r) / np.maximum(r, 1e-30)).max()
+
+
+def test_key_weights_masked_rows_and_infinities():
+    """A row with lse = -inf adds nothing even with NaN in its q; NaN in another request's q or in keys a row does not
+    see stays there; a key of infinities poisons only its own sum."""
+    torch = torch_mod()
+    b = batch_of([20, 20], [40, 90], 8, 2, 16, True, scale=1.0)
+    q = A.bf16_to_f64(b.q)
+    lse = lse_of(b, q, b.k_pages, 1.0, -1, 0.0, "HND")
+    old = np.zeros((b.num_pages, 2, 16), np.float32)
+    ref, reach = C.key_weights(b, q, b.k_pages, np.where(np.arange(40)[:, None] == 3, -np.inf, lse), old, 1.0, True)
+    bad_q = b.q.copy()
+    bad_q[20:] = 0x7FC0  # the second request: NaN
+    bad_q[3] = 0x7FC0
+    lse_dev = lse.copy()
+    lse_dev[3] = -np.inf
+    k = b.k_pages.copy()
+    p, s = C.places(b, 0, [39])  # the first request's last key: seen by its last token alone
+    k[p, :, s] = 0x7F80          # +inf
+    ws = workspace(b)
+    w = dev(old)
+    ws.key_weights(bf16(bad_q), bf16(k), dev(lse_dev), w, 1.0, True)
+    torch.cuda.synchronize()
+    got = w.cpu().numpy()
+    p, s = C.places(b, 0, np.arange(39))
+    tol = weights_tol(reach, lse) + 80 * 2.0 ** -24
+    assert (np.abs(got[p, :, s] - ref[p, :, s]) <= ref[p, :, s] * tol + 1e-30).all()
+    p, s = C.places(b, 1, np.arange(90))
+    assert np.isnan(got[p, :, s]).all()
+
+
+# ---- selection -------------------------------------------------------------------------------------
+
+SELECT = [
+    # lkv, hk, page, budget, recent, sink, kind, SM budget
+    ([1], 1, 1, 1, 0, 0, "random", 0),
+    ([5, 0, 8, 9], 3, 4, 8, 2, 1, "random", 0),
+    ([100, 33, 700], 2, 16, 32, 32, 0, "random", 0),      # nothing but recent keys
+    ([100, 33, 700], 2, 16, 33, 0, 33, "equal", 1),       # nothing but sinks
+    ([1000, 513], 8, 5, 257, 31, 4, "ties", 0),
+    ([4000], 2, 16, 3999, 0, 0, "equal", 0),              # one key goes
+    ([20000], 1, 16, 1, 0, 0, "random", 0),               # a cluster shares the row
+    ([40001, 12], 3, 1, 20000, 100, 4, "ties", 0),
+    ([300000], 1, 64, 1000, 10, 4, "random", 0),          # slices longer than shared memory at 8 CTAs: 37.5 K each
+    ([450000], 1, 128, 400, 0, 0, "ties", 0),             # 56 K keys a slice: read again from memory
+    ([64] * 40, 8, 16, 20, 5, 2, "signs", 2),
+    ([777] * 3, 2, 8, 100, 7, 3, "special", 0),
+]
+
+
+def some_weights(rng, shape, kind):
+    if kind == "equal":
+        return np.full(shape, 0.25, np.float32)
+    if kind == "ties":
+        return rng.integers(0, 4, size=shape).astype(np.float32)
+    if kind == "signs":
+        return rng.standard_normal(shape).astype(np.float32).round(1)
+    w = np.exp(3 * rng.standard_normal(shape)).astype(np.float32)
+    if kind == "special":
+        w = np.where(rng.random(shape) < 0.3, rng.choice(np.array([0.0, -0.0, np.inf, -np.inf, np.nan, 1e-45, -1e-45, 3e38], np.float32), shape), w)
+    return w.astype(np.float32)
+
+
+@pytest.mark.parametrize("case", SELECT, ids=range(len(SELECT)))
+def test_select_keys(case):
+    torch = torch_mod()
+    lkv, hk, ps, budget, recent, sink, kind, sms = case
+    rng = np.random.default_rng(9)
+    b = W.make_paged_batch(rng, "select", [1] * len(lkv), lkv, hk, hk, ps, False, with_data=False)
+    w = some_weights(rng, (max(b.num_pages, 1), hk, ps), kind)
+    _, l_kv = C.lengths(b)
+    used = np.zeros((w.shape[0], ps), bool)
+    for i in range(b.batch_size):
+        p, s = C.places(b, i, np.arange(int(l_kv[i])))
+        used[p, s] = True
+    w.transpose(0, 2, 1)[~used] = np.nan  # slots behind the last key are not read
+    ws = workspace(b, num_sms=sms)
+    kept = torch.full((b.batch_size, hk, budget), -7, dtype=torch.int32, device="cuda")
+    ws.select_keys(dev(w), budget, kept, recent=recent, sink=sink)
+    torch.cuda.synchronize()
+    assert ws.get_error() == 0
+    assert np.array_equal(kept.cpu().numpy(), C.select(b, w, budget, recent, sink))
+
+
+# ---- compaction ------------------------------------------------------------------------------------
+
+COMPACT = [
+    # lkv, hk, page, budget, dtype, layout, weights, pick
+    ([1], 1, 1, 1, "bf16", "HND", True, "random"),
+    ([9, 3, 0, 40], 2, 4, 8, "bf16", "HND", True, "random"),
+    ([700, 650, 333], 3, 5, 300, "bf16", "HND", False, "random"),
+    ([1000, 129], 8, 16, 128, "e4m3", "NHD", True, "random"),
+    ([2000], 1, 1, 1999, "bf16", "HND", True, "drop first"),   # every row moves down by one slot
+    ([3000, 2999], 2, 16, 2500, "e4m3", "HND", True, "drop first"),
+    ([9000], 2, 64, 8000, "bf16", "NHD", True, "random"),
+    ([600], 4, 16, 500, "bf16", "HND", True, "front"),         # nothing moves
+    ([600], 4, 16, 7, "e4m3", "HND", True, "back"),
+]
+
+
+@pytest.mark.parametrize("case", COMPACT, ids=range(len(COMPACT)))
+def test_compact(case):
+    torch = torch_mod()
+    lkv, hk, ps, budget, dtype, layout, with_w, pick = case
+    rng = np.random.default_rng(4)
+    b = W.make_paged_batch(rng, "compact", [1] * len(lkv), lkv, hk, hk, ps, False, with_data=False, pool_pages=None)
+    shape = (max(b.num_pages, 1), hk, ps, 128)
+    kind = np.uint16 if dtype == "bf16" else np.uint8
+    k, v = (as_layout(rng.integers(0, np.iinfo(kind).max, size=shape, endpoint=True).astype(kind), layout) for _ in range(2))
+    w = rng.random(shape[:3]).astype(np.float32)
+    kept = np.full((len(lkv), hk, budget), -1, np.int32)
+    for i, n in enumerate(lkv):
+        for h in range(hk):
+            m = min(n, budget)
+            kept[i, h, :m] = {"random": lambda: np.sort(rng.choice(n, m, replace=False)), "front": lambda: np.arange(m),
+                              "back": lambda: np.arange(n - m, n), "drop first": lambda: np.arange(n - m, n)}[pick]()
+    ws = workspace(b, layout=layout, dtype=dtype)
+    kd, vd = (bf16(k), bf16(v)) if dtype == "bf16" else (dev(k), dev(v))
+    wd = dev(w)
+    ws.compact(dev(kept), kd, vd, wd if with_w else None)
+    torch.cuda.synchronize()
+    assert ws.get_error() == 0
+    rk, rv, rw = C.compact(b, kept, [k, v, w], [layout, layout, "HND"])
+    host = (lambda t: bits(t)) if dtype == "bf16" else (lambda t: t.cpu().numpy())
+    assert np.array_equal(host(kd), rk) and np.array_equal(host(vd), rv)
+    assert np.array_equal(wd.cpu().numpy(), rw if with_w else w)
+
+
+def test_compact_skips_bad_entries():
+    """Entries out of range or out of order are skipped and reported; the others move."""
+    from serving_attention_plan_gb300 import binding as B
+    torch = torch_mod()
+    b = batch_of([1], [20], 1, 1, 4)
+    ws = workspace(b)
+    kept = np.array([[[0, 5, 5, 20, 2**30, 19]]], np.int32)  # ok, ok, not above, out of range (2), ok only if ascending
+    k, v = bf16(b.k_pages), bf16(b.v_pages)
+    ws.compact(dev(kept), k, v)
+    torch.cuda.synchronize()
+    assert ws.get_error() == B.DEVERR_KEPT
+    want = b.k_pages.copy()
+    fp, fs = C.places(b, 0, [5])
+    tp, ts = C.places(b, 0, [1])
+    want[tp, :, ts] = b.k_pages[fp, :, fs]
+    assert np.array_equal(bits(k), want)
+    kept = np.array([[[-1, 1, 3, 4, 6, 7]]], np.int32)
+    ws.compact(dev(kept), k, v)
+    torch.cuda.synchronize()
+    assert ws.get_error() == B.DEVERR_KEPT
+
+
+# ---- together --------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype,layout,causal_chunk", [("bf16", "HND", False), ("e4m3", "NHD", False), ("bf16", "HND", True)])
+def test_life_of_a_cache(dtype, layout, causal_chunk):
+    """Prompt, decode steps, eviction, more decode steps: the attention over the evicted cache is the oracle's over the
+    rows that the oracle's own selection keeps."""
+    from serving_attention_plan_gb300 import binding as B
+    torch = torch_mod()
+    rng = np.random.default_rng(21)
+    hq, hk, ps, budget, recent, sink = 8, 2, 16, 48, 8, 2
+    prompts = [100, 37, 260]
+    n_req, steps, pool = 3, 4, 64
+    free = list(rng.permutation(pool))
+    lists = [[] for _ in range(n_req)]
+    length, position = [0] * n_req, [0] * n_req
+    scales = (0.0625, 0.0625) if dtype == "e4m3" else (1.0, 1.0)
+    inv_freq = 10000.0 ** (-np.arange(0, 128, 2) / 128)
+    ws = B.Workspace(n_req, 1024, pool, hq, hk)
+    ws.set_variant(kv_layout=layout)
+    ws.set_kv_dtype(dtype, *scales)
+    ws.set_rope(inv_freq)
+    t = torch.bfloat16 if dtype == "bf16" else torch.float8_e4m3fn
+    shape = (pool, hk, ps, 128) if layout == "HND" else (pool, ps, hk, 128)
+    kp, vp = torch.zeros(shape, device="cuda", dtype=t), torch.zeros(shape, device="cuda", dtype=t)
+    w = torch.full((pool, hk, ps), float("nan"), device="cuda")
+    raw = (lambda x: bits(x)) if dtype == "bf16" else (lambda x: x.view(torch.uint8).cpu().numpy())
+
+    def step(new):
+        nonlocal lists
+        for i in range(n_req):
+            length[i] += new[i]
+            while len(lists[i]) * ps < length[i]:
+                lists[i].append(free.pop())
+        qo = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        kv = np.concatenate([[0], np.cumsum([len(x) for x in lists])]).astype(np.int32)
+        last = np.array([length[i] - (len(lists[i]) - 1) * ps for i in range(n_req)], np.int32)
+        b = W.PagedBatch("life", hq, hk, 128, ps, True, qo, kv, np.concatenate(lists).astype(np.int32), last, None, None, None)
+        ws.plan(qo, kv, b.kv_indices, last, ps, True)
+        n = int(qo[-1])
+        x = bf16(W.f32_to_bf16_bits(rng.standard_normal((n, hq + 2 * hk, 128), dtype=np.float32)))
+        pos = np.concatenate([np.arange(position[i], position[i] + new[i]) for i in range(n_req)])
+        for i in range(n_req):
+            position[i] += new[i]
+        q = torch.empty(n, hq, 128, device="cuda", dtype=torch.bfloat16)
+        o, lse = torch.empty_like(q), torch.empty(n, hq, device="cuda")
+        ws.append(x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:], kp, vp, q, positions=dev(pos.astype(np.int32)))
+        ws.run(q, kp, vp, o, lse)
+        ws.key_weights(q, kp, lse, w, decay=0.9)
+        torch.cuda.synchronize()
+        assert ws.get_error() == 0
+        b = dataclasses.replace(b, q=bits(q), k_pages=raw(kp), v_pages=raw(vp))
+        ro, rl = A.batch_attention(b, layout=layout, k_scale=scales[0], v_scale=scales[1])
+        assert np.abs(f64(o) - ro).max() <= 2e-2 and np.abs(f64(lse) - rl).max() <= 1e-3 * max(1, np.abs(rl).max())
+        return b, f64(q), lse.cpu().numpy()
+
+    want = np.zeros((pool, hk, ps))
+    for k_step in range(steps):
+        new = prompts if k_step == 0 else ([20, 1, 33] if causal_chunk else [1] * n_req)
+        b, q, lse = step(new)
+        want, reach = C.key_weights(b, q, b.k_pages, lse, want, 0.9, True, scales[0], layout=layout)
+        got = w.cpu().numpy()
+        tol = weights_tol(reach, lse) + 1024 * 2.0 ** -24
+        for i in range(n_req):
+            p, s = C.places(b, i, np.arange(length[i]))
+            assert (np.abs(got[p, :, s] - want[p, :, s]) <= (k_step + 1) * tol * want[p, :, s] + 1e-30).all()
+            want[p, :, s] = got[p, :, s]
+            # every row spreads a weight of one over its keys
+        if k_step % 2 == 1:
+            kept = torch.empty(n_req, hk, budget, device="cuda", dtype=torch.int32)
+            ws.select_keys(w, budget, kept, recent=recent, sink=sink)
+            ws.compact(kept, kp, vp, w)
+            torch.cuda.synchronize()
+            assert ws.get_error() == 0
+            rkept = C.select(b, got, budget, recent, sink)
+            assert np.array_equal(kept.cpu().numpy(), rkept)
+            rk, rv, rw = C.compact(b, rkept, [b.k_pages, b.v_pages, got], [layout, layout, "HND"])
+            assert np.array_equal(raw(kp), rk) and np.array_equal(raw(vp), rv)
+            assert np.array_equal(w.cpu().numpy(), rw, equal_nan=True)
+            want = rw.astype(np.float64)
+            for i in range(n_req):
+                length[i] = min(length[i], budget)
+                keep = -(-length[i] // ps)
+                free.extend(lists[i][keep:])
+                lists[i] = lists[i][:keep]
+
+
+def test_captured_chain_follows_a_new_plan():
+    """append, run, key_weights, select and compact captured once: a replay after another plan of the same path does what
+    separate calls do, on a side stream, twice over."""
+    torch = torch_mod()
+    hq, hk, ps, budget = 8, 2, 16, 100
+
+    def one(lkv, seed):
+        b = batch_of([1] * len(lkv), lkv, hq, hk, ps, True, seed=seed, extra=60 - sum(-(-x // ps) for x in lkv))
+        return b
+    first, second = one([130, 90, 20], 1), one([220, 31, 300, 101], 2)
+    from serving_attention_plan_gb300 import binding as B
+    ws = B.Workspace(4, 4, 60, hq, hk)
+    ws.set_rope(10000.0 ** (-np.arange(0, 128, 2) / 128))
+    side = torch.cuda.Stream()
+    x = torch.randn(4, hq + 2 * hk, 128, device="cuda").to(torch.bfloat16)
+    kp0, vp0 = bf16(first.k_pages), bf16(first.v_pages)
+    w0 = torch.rand(60, hk, ps, device="cuda")
+
+    def buffers():
+        return dict(kp=kp0.clone(), vp=vp0.clone(), w=w0.clone(), q=torch.zeros(4, hq, 128, device="cuda", dtype=torch.bfloat16),
+                    o=torch.zeros(4, hq, 128, device="cuda", dtype=torch.bfloat16), lse=torch.zeros(4, hq, device="cuda"),
+                    kept=torch.full((4, hk, budget), -9, device="cuda", dtype=torch.int32))
+
+    def plan(b):
+        ws.plan(b.qo_indptr, b.kv_indptr, b.kv_indices, b.last_page_len, ps, True, stream=side)
+
+    def calls(d, n):
+        v = lambda t: t[:n]
+        ws.append(x[:n, :hq], x[:n, hq:hq + hk], x[:n, hq + hk:], d["kp"], d["vp"], v(d["q"]), stream=side)
+        ws.run(v(d["q"]), d["kp"], d["vp"], v(d["o"]), v(d["lse"]), stream=side)
+        ws.key_weights(v(d["q"]), d["kp"], v(d["lse"]), d["w"], 0.9, True, stream=side)
+        ws.select_keys(d["w"], budget, v(d["kept"]), recent=10, sink=2, stream=side)
+        ws.compact(v(d["kept"]), d["kp"], d["vp"], d["w"], stream=side)
+
+    cap = buffers()
+    torch.cuda.synchronize()
+    plan(first)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        calls(cap, 3)
+    for b in (first, second, first):
+        for k, val in buffers().items():
+            cap[k].copy_(val)
+        ref = buffers()
+        torch.cuda.synchronize()
+        plan(b)
+        with torch.cuda.stream(side):
+            graph.replay()
+        side.synchronize()
+        calls(ref, b.batch_size)
+        side.synchronize()
+        assert ws.get_error() == 0
+        for k in ref:
+            assert torch.equal(ref[k], cap[k]), k
+
+
+def test_composable_plan():
+    """With a composable plan the operators work on the per-request part; positions must be given."""
+    from serving_attention_plan_gb300 import binding as B
+    torch = torch_mod()
+    sp = W.shared_prefix_decode(n_req=5, prefix_len=64, lo=20, hi=50)
+    s = sp.suffix
+    ws = B.Workspace(5, 5, 200, 32, 8)
+    idx = lambda b: (b.qo_indptr, b.kv_indptr, b.kv_indices, b.last_page_len)
+    ws.plan_composable(idx(sp.prefix), idx(s), 16, False)
+    q, kp, vp = bf16(s.q), bf16(s.k_pages), bf16(s.v_pages)
+    o, lse = torch.empty_like(q), torch.empty(5, 32, device="cuda")
+    ws.run(q, kp, vp, o, lse)
+    w = torch.zeros(s.num_pages, 8, 16, device="cuda")
+    ws.key_weights(q, kp, lse, w)
+    torch.cuda.synchronize()
+    lse_h = lse.cpu().numpy()
+    ref, reach = C.key_weights(s, A.bf16_to_f64(s.q), s.k_pages, lse_h, np.zeros(w.shape), 1.0, True)
+    assert (np.abs(w.cpu().numpy() - ref) <= ref * weights_tol(reach, lse_h) + 1e-30).all()
+    x = torch.randn(5, 8, 128, device="cuda").to(torch.bfloat16)
+    with pytest.raises(B.FiError) as e:
+        ws.append(q, x, x, kp, vp, o)
+    assert e.value.status == 1
+    ws.append(q, x, x, kp, vp, o, positions=torch.arange(5, device="cuda", dtype=torch.int32))
+    torch.cuda.synchronize()
+    _, page, slot, _ = C.append_places(s)
+    want = s.k_pages.copy()
+    want[page, :, slot] = bits(x)
+    assert np.array_equal(bits(kp), want) and ws.get_error() == 0
+
+
+# ---- refusals --------------------------------------------------------------------------------------
+
+
+def test_refusals():
+    from serving_attention_plan_gb300 import binding as B
+    torch = torch_mod()
+    b = batch_of([1, 1], [20, 30], 4, 2, 4)
+    q, kp, vp = bf16(b.q), bf16(b.k_pages), bf16(b.v_pages)
+    n = b.num_pages
+    k = torch.zeros(2, 2, 128, device="cuda", dtype=torch.bfloat16)
+    o, lse = torch.empty_like(q), torch.zeros(2, 4, device="cuda")
+    w = torch.zeros(n, 2, 4, device="cuda")
+    kept = torch.zeros(2, 2, 8, device="cuda", dtype=torch.int32)
+    fresh = B.Workspace(2, 2, 64, 4, 2)
+    for call in (lambda: fresh.append(q, k, k, kp, vp, o), lambda: fresh.key_weights(q, kp, lse, w),
+                 lambda: fresh.select_keys(w, 8, kept), lambda: fresh.compact(kept, kp, vp)):
+        with pytest.raises(B.FiError) as e:
+            call()
+        assert e.value.status == 6
+    ws = workspace(b)
+    used = int(b.kv_indices.max())
+    bad = [
+        (1, lambda: ws.append(q, k, k, kp[:used], vp[:used], o)),            # a planned page outside the pool
+        (1, lambda: ws.key_weights(q, kp[:used], lse, w[:used])),
+        (1, lambda: ws.select_keys(w[:used], 8, kept)),
+        (1, lambda: ws.compact(kept, kp[:used], vp[:used])),
+        (1, lambda: ws.append(q, k, k, kp, vp, o, eps=-1.0)),
+        (1, lambda: ws.append(q, k, k, kp, vp, o, eps=float("nan"))),
+        (1, lambda: ws.key_weights(q, kp, lse, w, decay=1.5)),
+        (1, lambda: ws.key_weights(q, kp, lse, w, decay=float("nan"))),
+        (1, lambda: ws.select_keys(w, 8, kept, recent=5, sink=4)),
+        (1, lambda: ws.select_keys(w, 8, kept, recent=-1)),
+        (1, lambda: ws.set_rope([float("inf")] * 8)),
+        (1, lambda: ws.set_rope(np.ones(65))),
+        (3, lambda: ws.set_rope(np.ones(9))),
+    ]
+    for status, call in bad:
+        with pytest.raises(B.FiError) as e:
+            call()
+        assert e.value.status == status
+    wrong = [
+        lambda: ws.append(q.float(), k, k, kp, vp, o), lambda: ws.append(q[:1], k, k, kp, vp, o),
+        lambda: ws.append(q, k.transpose(0, 1), k, kp, vp, o), lambda: ws.append(q, k, k, kp, vp, o[..., :64]),
+        lambda: ws.append(q, k, k, kp.view(torch.uint8), vp, o), lambda: ws.append(q, k, k, kp, vp[:-1], o),
+        lambda: ws.append(q, k, k, kp, vp, o, positions=torch.zeros(2, device="cuda")),
+        lambda: ws.append(q, k, k, kp, vp, o, q_weight=torch.ones(128, device="cuda")),
+        lambda: ws.append(q.cpu(), k, k, kp, vp, o),
+        lambda: ws.key_weights(q, kp, lse.double(), w), lambda: ws.key_weights(q, kp, lse, w[:, :1]),
+        lambda: ws.key_weights(q, kp, lse, w.half()), lambda: ws.select_keys(w, 9, kept),
+        lambda: ws.select_keys(w, 8, kept.long()), lambda: ws.compact(kept[:1], kp, vp),
+        lambda: ws.compact(kept[0], kp, vp), lambda: ws.compact(kept, kp, vp, w[:-1]),
+        lambda: ws.set_rope(np.ones((2, 8))),
+    ]
+    for call in wrong:
+        with pytest.raises(ValueError):
+            call()
+    # shared pages: one tail for two requests, one prefix for two requests
+    ws.plan([0, 1, 2], [0, 2, 4], [0, 1, 2, 1], [2, 3], 4, False)
+    for call in (lambda: ws.append(q, k, k, kp, vp, o), lambda: ws.key_weights(q, kp, lse, w), lambda: ws.compact(kept, kp, vp)):
+        with pytest.raises(B.FiError) as e:
+            call()
+        assert e.value.status == 3
+    ws.plan([0, 1, 2], [0, 2, 4], [0, 1, 0, 3], [2, 3], 4, False)
+    ws.append(q, k, k, kp, vp, o)
+    with pytest.raises(B.FiError):
+        ws.key_weights(q, kp, lse, w)
+    # nothing to do: no requests, no tokens, no keys
+    ws.plan([0], [0], [], [], 4, False)
+    ws.append(q[:0], k[:0], k[:0], kp, vp, o[:0])
+    ws.key_weights(q[:0], kp, lse[:0], w)
+    ws.select_keys(w, 8, kept[:0])
+    ws.compact(kept[:0], kp, vp, w)
+    ws.plan([0, 1], [0, 0], [], [0], 4, False)
+    ws.append(q[:1], k[:1], k[:1], kp, vp, o[:1])
+    ws.key_weights(q[:1], kp, lse[:1], w)
+    ws.select_keys(w, 8, kept[:1])
+    ws.compact(kept[:1], kp, vp, w)
+    torch.cuda.synchronize()
+    assert (kept[0] == -1).all() and torch.equal(o[0], q[0]) and (w == 0).all() and ws.get_error() == 0
