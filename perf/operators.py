@@ -166,6 +166,8 @@ def prepare(case, seed):
             ws.set_rope(s["inv_freq"].cpu().numpy(), case["interleaved"])
         ws.plan(s["qo"], s["kv"], order.cpu().numpy(), s["last"], page, case.get("causal", False))
         s["ws"] = ws
+        if case["op"] == "compact":
+            s["kept"] = s["kept"].contiguous()  # the calls take dense tensors
     return s
 
 
