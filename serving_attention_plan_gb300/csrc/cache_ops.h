@@ -16,10 +16,29 @@ struct Geo {
   int32_t kv0, lkv;  // first entry in the page list, keys
   int32_t blk0;      // 32-key blocks of the requests before this one
   int32_t tile0;     // 256-key tiles of the requests before this one
-  int32_t pad0, pad1;
+  int32_t work0;     // tensor-core weights: Q tiles (over all KV heads) of the requests before this one
+  int32_t pad;
 };
 constexpr int kBlkKeys = 32;
 constexpr int kTileKeys = 256;
+constexpr int kWeightTileRows = 128;  // query rows of a Q tile of the tensor-core weights
+
+// Of key tile kt: the first query token that sees one of its keys, how many tokens from there on do,
+// and the Q tiles of `tile_tokens` tokens they take (at least 1: the decay has to reach every key).
+__host__ __device__ inline void weight_item(int lq, int lkv, int kt, bool causal, int window, int tile_tokens, int* t0,
+                                            int* tokens, int* cost) {
+  int first = 0, last = lq;
+  if (causal) {
+    const int key0 = kt * kTileKeys, key1 = key0 + kTileKeys < lkv ? key0 + kTileKeys : lkv, off = lkv - lq;
+    if (key0 - off > 0) first = key0 - off;
+    if (window >= 0 && key1 - off + (long long)window < last) last = key1 - off + window;
+  }
+  const int n = last > first ? last - first : 0;
+  *t0 = first;
+  *tokens = n;
+  const int c = (n + tile_tokens - 1) / tile_tokens;
+  *cost = c > 1 ? c : 1;
+}
 
 struct GeoTotals {
   bool ok = false;     // the counts below fit the entries' 32-bit fields
@@ -27,10 +46,13 @@ struct GeoTotals {
   int64_t tiles = 0;   // 256-key tiles
   int32_t max_lkv = 0;
   int32_t max_lq = 0;
+  bool work_ok = false;  // the Q tiles were counted and fit 32 bits
 };
 // The entries [0, batch] of a validated batch (cache_plan.cpp, host only, like the two checks).
 GeoTotals fill_geo(const int32_t* qo_indptr, const int32_t* kv_indptr, const int32_t* last_page_len, int batch,
                    int page_size, Geo* out);
+// The work0 fields of filled entries: Q tiles of the tensor-core weights.
+void fill_work(Geo* geo, int batch, int hkv, int tile_tokens, bool causal, int window, GeoTotals* totals);
 // FI_OK if no page id (0 .. max_page) occurs twice in the two lists, else FI_ERR_UNSUPPORTED; FI_ERR_CAPACITY without host memory.
 int check_pages_once(const int32_t* a, int64_t na, const int32_t* b, int64_t nb, int32_t max_page);
 // FI_OK if no page takes new tokens (the last l_q keys of a request) from two places of the list.
@@ -79,8 +101,14 @@ struct WeightsParams {
   float scale_log2;    // logit scale in the log2 domain (includes k_scale)
   float cap_log2, inv_cap_log2;  // soft-cap, 0 for none
   int window_left;     // >= 0: sliding window
+  // tensor-core form
+  int tile_tokens;      // tokens of a Q tile: 128 / group
+  float* part;          // [CTAs][2][256] partial sums of items cut between CTAs
+  uint32_t* part_count; // [CTAs], zero between launches
 };
 int launch_weights_rows(const WeightsParams& p, bool fp8, int64_t n_blk, int num_sms, cudaStream_t stream);
+
+int launch_weights_tc(const WeightsParams& p, int total_q, bool fp8, int num_sms, cudaStream_t stream);
 
 struct SelectParams {
   PageView pv;

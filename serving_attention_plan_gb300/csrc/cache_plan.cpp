@@ -35,6 +35,23 @@ GeoTotals fill_geo(const int32_t* qo_indptr, const int32_t* kv_indptr, const int
   return t;
 }
 
+void fill_work(Geo* geo, int batch, int hkv, int tile_tokens, bool causal, int window, GeoTotals* totals) {
+  int64_t work = 0;
+  for (int i = 0; i <= batch; ++i) {
+    geo[i].work0 = int32_t(work);
+    if (i == batch) break;
+    int64_t head = 0;
+    for (int kt = 0; int64_t(kt) * kTileKeys < geo[i].lkv; ++kt) {
+      int t0, tokens, cost;
+      weight_item(geo[i].lq, geo[i].lkv, kt, causal, window, tile_tokens, &t0, &tokens, &cost);
+      head += cost;
+    }
+    work += head * hkv;
+    if (work > INT32_MAX) return;
+  }
+  totals->work_ok = true;
+}
+
 int check_pages_once(const int32_t* a, int64_t na, const int32_t* b, int64_t nb, int32_t max_page) {
   try {
     std::vector<bool> seen(size_t(max_page) + 1, false);

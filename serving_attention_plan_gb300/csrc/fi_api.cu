@@ -56,7 +56,7 @@ struct fi_workspace {
   size_t off_header = 0, off_cta = 0, off_geo = 0, off_items = 0, off_units = 0, off_slot_unit = 0, off_kv = 0, plan_bytes = 0;
   size_t off_a_header = 0, off_a_cta = 0, off_a_items = 0, off_a_kv = 0, off_ext = 0;
   int64_t max_ext = 0;
-  size_t off_counters = 0, off_err = 0, off_part_lse = 0, off_part_o = 0, dev_bytes = 0;
+  size_t off_counters = 0, off_wcount = 0, off_wpart = 0, off_err = 0, off_part_lse = 0, off_part_o = 0, dev_bytes = 0;
   char* dbuf = nullptr;
   char* hbuf = nullptr;
   cudaEvent_t copy_done = nullptr;
@@ -109,9 +109,13 @@ int launch_decode(int grid, const fi::DecodeParams& p, cudaStream_t stream, bool
 
 // The requests of the (per-request) plan as the cache operators read them, into the pinned mirror.
 void set_geo(fi_workspace* ws, const int32_t* qo_indptr, const int32_t* kv_indptr, const int32_t* last_page_len,
-             int batch, int page_size) {
+             int batch, int page_size, int path, int causal) {
   ws->geo = fi::fill_geo(qo_indptr, kv_indptr, last_page_len, batch, page_size,
                          reinterpret_cast<fi::Geo*>(ws->hbuf + ws->off_geo));
+  const int group = ws->hqo / ws->hkv;
+  if (path == fi::kPathTensor && group <= fi::kWeightTileRows)
+    fi::fill_work(reinterpret_cast<fi::Geo*>(ws->hbuf + ws->off_geo), batch, ws->hkv, fi::kWeightTileRows / group,
+                  causal != 0, ws->variant.window_left, &ws->geo);
   ws->pages_once = ws->tails_once = 0;
 }
 
@@ -251,9 +255,11 @@ int fi_workspace_create(int max_batch, int max_total_q, int max_kv_pages, int nu
   ws->off_ext = seg(sizeof(int32_t) * 2 * ws->max_ext);
   ws->plan_bytes = off;
   ws->off_counters = seg(sizeof(uint32_t) * ws->max_units);
+  ws->off_wcount = seg(sizeof(uint32_t) * num_sms);
   ws->off_err = seg(sizeof(int32_t) * 4);
   ws->off_part_lse = seg(sizeof(float) * ws->max_slots * fi::kTcRows);
   ws->off_part_o = seg(sizeof(float) * ws->max_slots * fi::kTcRows * fi::kHeadDim);
+  ws->off_wpart = seg(sizeof(float) * 2 * size_t(num_sms) * fi::kTileKeys);
   ws->dev_bytes = off;
 
   cudaError_t e = cudaMalloc(&ws->dbuf, ws->dev_bytes);
@@ -353,7 +359,7 @@ int fi_plan(fi_workspace* ws, const int32_t* qo_indptr, const int32_t* kv_indptr
   char* h = ws->hbuf;
   std::memcpy(h + ws->off_header, plan.header, sizeof(plan.header));
   std::memcpy(h + ws->off_cta, plan.cta_indptr.data(), plan.cta_indptr.size() * sizeof(int32_t));
-  set_geo(ws, qo_indptr, kv_indptr, last_page_len, batch, page_size);
+  set_geo(ws, qo_indptr, kv_indptr, last_page_len, batch, page_size, plan.header[fi::H_PATH], causal);
   if (n_items) std::memcpy(h + ws->off_items, plan.items.data(), plan.items.size() * sizeof(int32_t));
   if (n_units) std::memcpy(h + ws->off_units, plan.units.data(), plan.units.size() * sizeof(int32_t));
   if (n_slots) std::memcpy(h + ws->off_slot_unit, plan.slot_unit.data(), plan.slot_unit.size() * sizeof(int32_t));
@@ -471,7 +477,7 @@ int fi_plan_composable(fi_workspace* ws, const int32_t* shared_qo_indptr, const 
       {ws->off_a_kv, shared_kv_indices, size_t(nnz_a) * sizeof(int32_t)},
       {ws->off_ext, cp.ext.data(), cp.ext.size() * sizeof(int32_t)},
   };
-  set_geo(ws, qo_indptr, kv_indptr, last_page_len, batch, page_size);
+  set_geo(ws, qo_indptr, kv_indptr, last_page_len, batch, page_size, fi::kPathComposable, causal);
   for (const Seg& sg : segs) {
     if (sg.bytes == 0) continue;
     if (sg.src != nullptr) std::memcpy(h + sg.off, sg.src, sg.bytes);
@@ -831,6 +837,13 @@ int fi_key_weights(fi_workspace* ws, const void* q, const void* k_pages, int num
   p.cap_log2 = var.soft_cap > 0.f ? var.soft_cap * fi::kLog2e : 0.f;
   p.inv_cap_log2 = var.soft_cap > 0.f ? 1.f / p.cap_log2 : 0.f;
   p.window_left = var.window_left;
+  // more than 8 rows a request: tensor cores (a group of more than 128 heads does not fit their tile)
+  if (ws->header[fi::H_PATH] == fi::kPathTensor && ws->geo.work_ok) {
+    p.tile_tokens = fi::kWeightTileRows / p.group;
+    p.part = reinterpret_cast<float*>(ws->dbuf + ws->off_wpart);
+    p.part_count = reinterpret_cast<uint32_t*>(ws->dbuf + ws->off_wcount);
+    return fi::launch_weights_tc(p, ws->plan_total_q, fp8, ws->num_sms, static_cast<cudaStream_t>(stream));
+  }
   return fi::launch_weights_rows(p, fp8, ws->geo.blocks, ws->num_sms, static_cast<cudaStream_t>(stream));
 }
 
