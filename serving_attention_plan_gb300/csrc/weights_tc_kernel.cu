@@ -10,9 +10,17 @@
 // traffic of Q) against all query rows that see one of them, in tiles of 128 rows (128 / g tokens x
 // g heads, one TMA box a 64-dim half).
 //
-// What bounds it: per Q tile and item the tensor cores take 2 x 128x128x128 products (1024 clocks at
+// The item's keys stay in tensor memory as the A operand (128 columns), so the products read only Q
+// from shared memory; from shared memory both operands of a 128-column product take its whole
+// bandwidth.  The -lse of a column is the same for all keys: it is added by one more 16-wide k-step
+// with ones on the key side and -lse / scale, split into three bf16 parts (24 bits), on the query
+// side.  (Read from shared memory by the threads, 128 values a thread and tile, it took as long as
+// the exponentials: a broadcast still moves 16 bytes a lane.)  The exponential's argument is then one
+// multiplication.  With a soft-cap the -lse cannot go inside the tanh and is read that way.
+//
+// What bounds it: per Q tile and item the tensor cores take 2 x 128x128x144 products (1152 clocks at
 // the nominal rate) and the exponentials 32768 results (1024 clocks at 32 a clock and SM): the two
-// run at the same time, with two score buffers per half.
+// run at the same time, over three score buffers of 128 columns.
 //
 // Work split: the Q tiles of all items lie on one line, request by request, KV head by KV head, key
 // tile by key tile (the causal mask gives later key tiles fewer Q tiles); CTA c takes the c-th
@@ -21,16 +29,18 @@
 // line order: the result does not depend on who is last.  Each CTA has at most two cut items, so the
 // slots are bounded by the grid, not by the batch.
 //
-// One CTA per SM, 14 warps:
+// One CTA per SM, 18 warps:
 //   warps 0-7    exponentials and sums: warps 0-3 the first 128 keys, 4-7 the others
-//   warp 8       TMA producer of Q tiles (three stages) and their lse rows
-//   warp 9       tensor memory, MMA issue
-//   warps 10-13  K tile loader (two stages): 16-byte loads into the 128-byte swizzle, any page size and
-//                layout; e4m3 codes are widened to bf16 (exact) on the way, so Q stays bf16
+//   warps 8-15   key loader: a thread holds one key's 128 dims in registers until the previous item's
+//                last product is done, then stores them to tensor memory; any page size and layout;
+//                e4m3 codes are widened to bf16 (exact) on the way, so Q stays bf16
+//   warp 16      TMA producer of Q tiles (four stages) and writer of their -lse rows
+//   warp 17      tensor memory, MMA issue
 #include <cuda.h>
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <cstddef>
 #include <mutex>
 
 #include "cache_common.cuh"
@@ -41,22 +51,30 @@ namespace fi {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kTcThreads = 448;
+constexpr int kTcThreads = 640;  // five warpgroups; the last one's second half is idle
+// Registers after launch (640 threads x 96): 256 x 88 + 256 x 112 + 128 x 80 = 640 x 96.
+constexpr uint32_t kSumRegs = 88;
+constexpr uint32_t kLoadRegs = 112;
+constexpr uint32_t kControlRegs = 80;
 constexpr int kKeys = kTileKeys;                // keys of an item
 constexpr int kCols = kWeightTileRows;          // query rows of a Q tile
-constexpr int kKHalfBytes = kKeys * 128;        // one 64-dim half of the K tile
-constexpr int kQHalfBytes = kCols * 128;
-constexpr int kQStages = 3;
-constexpr int kKStages = 2;
-constexpr uint32_t kTmemCols = 512;             // S[half][buffer]: 128 columns each
+constexpr int kQHalfBytes = kCols * 128;        // 64 dims of a Q tile, or its -lse rows
+constexpr int kQStages = 4;
+constexpr int kSBufs = 3;
+constexpr int kRing = 8;                        // tiles whose column notes are kept
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColK = 0;                   // 64 columns per half of the item's keys
+constexpr uint32_t kColS = 128;                 // kSBufs score buffers of 128 columns
+constexpr float kDead = -1e30f;                 // -lse / scale of a column that counts for nothing
 
 struct TcSmem {
-  uint8_t k[kKStages][2 * kKHalfBytes];
   uint8_t q[kQStages][2 * kQHalfBytes];
-  float nl[kQStages][kCols];  // -lse in the log2 domain, -inf for columns that count for nothing
-  int special[kQStages];      // 1: some column of the tile counts for nothing (its score may be anything)
-  uint64_t k_full[kKStages], k_empty[kKStages], q_full[kQStages], q_empty[kQStages], l_full[kQStages], l_empty[kQStages];
-  uint64_t s_full[2][2], s_empty[2][2];
+  uint8_t l[kQStages][kQHalfBytes];  // per column 128 bytes: {hi, mid, lo, 0...} of -lse / scale, rest zero
+  uint8_t ones[kQHalfBytes];         // the key side of the -lse step: {1, 1, 1, 0...}
+  float nl[kRing][kCols];            // soft-cap: -lse in the log2 domain
+  uint32_t dead[kRing][4];           // columns that count for nothing, whatever their score is
+  uint64_t k_full, k_empty, q_full[kQStages], q_empty[kQStages], l_full[kRing];
+  uint64_t s_full[kSBufs], s_empty[kSBufs];
   uint32_t tmem_base;
   int abort;
   int last;
@@ -147,87 +165,86 @@ __device__ __forceinline__ uint2 widen4(uint32_t codes) {
   return make_uint2(f2_to_bf16x2(a.x, a.y), f2_to_bf16x2(b.x, b.y));
 }
 
+// One key row a thread: 128 dims as 64 bf16 pairs, in tensor-memory columns 0..63 of the half.
 template <bool kFp8>
-__device__ void load_keys(const WeightsParams& p, TcSmem& sm, Walk w, bool causal) {
+__device__ void load_keys(const WeightsParams& p, TcSmem& sm, Walk w, bool causal, uint32_t tmem) {
   const PageView& pv = p.pv;
-  const int tid = threadIdx.x - 320;             // 0..127
-  constexpr int kLanes = kFp8 ? 8 : 16;          // threads of a row, 16 bytes each
-  constexpr int kRowsPass = 128 / kLanes;
-  constexpr int kBatch = 8;
-  const int ch = tid % kLanes, row0 = tid / kLanes;
-  const uint8_t* pages = static_cast<const uint8_t*>(p.k_pages);
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 8;
+  const int row = warp * 32 + lane;
+  const uint32_t t_k = tmem + (uint32_t((warp & 3) * 32) << 16) + kColK + uint32_t((warp >> 2) * 64);
   for (int n = 0; w.more(); w.next(p, causal), ++n) {
-    const int ks = n % kKStages;
-    bool ok = true;
-    if (n >= kKStages) ok = mbar_wait(&sm.k_empty[ks], (n / kKStages - 1) & 1, pv.err, &sm.abort);
-    if (!__all_sync(kAll, ok)) return;
-    for (int i0 = 0; i0 < kKeys; i0 += kBatch * kRowsPass) {
-      uint4 v[kBatch];
-      long long off[kBatch];
+    const int key = w.kt * kKeys + row;
+    uint32_t v[2][32];
+    int page, slot;
+    const bool on = key < w.g.lkv && locate(pv, w.g.kv0, key, page, slot);
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.k_pages) +
+                                                      (on ? kv_offset(pv, page, slot, w.head) * (kFp8 ? 1 : 2) : 0));
+    if constexpr (kFp8) {
+      uint4 x[8];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int key = w.kt * kKeys + i0 + i * kRowsPass + row0;
-        int page, slot;
-        off[i] = -1;
-        if (key < w.g.lkv && locate(pv, w.g.kv0, key, page, slot)) off[i] = kv_offset(pv, page, slot, w.head);
-      }
+      for (int i = 0; i < 8; ++i) x[i] = on ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        v[i] = off[i] >= 0 ? __ldg(reinterpret_cast<const uint4*>(pages + off[i] * (kFp8 ? 1 : 2) + 16 * ch))
-                           : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int row = i0 + i * kRowsPass + row0;
-        auto put = [&](int c16, uint4 x) {  // 16-byte piece c16 (0..15) of a bf16 row
-          uint8_t* at = sm.k[ks] + (c16 >> 3) * kKHalfBytes + row * 128 + (((c16 & 7) ^ (row & 7)) << 4);
-          *reinterpret_cast<uint4*>(at) = x;
-        };
-        if constexpr (kFp8) {
-          const uint2 a = widen4(v[i].x), b = widen4(v[i].y), c = widen4(v[i].z), d = widen4(v[i].w);
-          put(2 * ch, make_uint4(a.x, a.y, b.x, b.y));
-          put(2 * ch + 1, make_uint4(c.x, c.y, d.x, d.y));
-        } else {
-          put(ch, v[i]);
+        for (int e = 0; e < 4; ++e) {
+          const uint2 y = widen4(u[e]);
+          v[i >> 2][(8 * i + 2 * e) & 31] = y.x;
+          v[i >> 2][(8 * i + 2 * e + 1) & 31] = y.y;
         }
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint4 x = on ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+        v[i >> 3][(4 * i) & 31] = x.x;
+        v[i >> 3][(4 * i + 1) & 31] = x.y;
+        v[i >> 3][(4 * i + 2) & 31] = x.z;
+        v[i >> 3][(4 * i + 3) & 31] = x.w;
+      }
     }
-    fence_proxy_async_smem();
-    mbar_arrive(&sm.k_full[ks]);
+    __syncwarp();
+    if (n > 0 && !__all_sync(kAll, mbar_wait(&sm.k_empty, (n - 1) & 1, pv.err, &sm.abort))) return;
+    tc::fence_after_sync();
+    tc::tmem_st32(t_k, v[0]);
+    tc::tmem_st32(t_k + 32, v[1]);
+    tc::tmem_wait_st();
+    tc::fence_before_sync();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.k_full);
   }
 }
 
+template <bool kCap>
 __device__ void load_queries(const WeightsParams& p, TcSmem& sm, Walk w, bool causal, const CUtensorMap* tm_q) {
   const int lane = threadIdx.x & 31;
   const int cols = p.tile_tokens * p.group;
+  const float unit = kCap ? -kLog2e : -kLog2e / p.scale_log2;  // soft-cap: log2 domain; else in units of the raw score
+  // this lane's columns are lane + 32 i: their place in the tile does not change
+  int tok[4], hh[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    tok[i] = (lane + 32 * i) / p.group;
+    hh[i] = (lane + 32 * i) - tok[i] * p.group;
+  }
   int n = 0;
   bool ok = true;
   for (; ok && w.more(); w.next(p, causal)) {
-    // this lane's columns are lane + 32 i: their place in the tile does not change
-    int tok[4], hh[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      tok[i] = (lane + 32 * i) / p.group;
-      hh[i] = (lane + 32 * i) - tok[i] * p.group;
-    }
     auto fetch = [&](int qt, float (&nl)[4]) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int t = qt * p.tile_tokens + tok[i];
         nl[i] = -INFINITY;
-        if (lane + 32 * i < cols && t < w.tokens) {
-          const float l = __ldg(p.lse + (long long)(w.g.q0 + w.t0 + t) * p.hqo + w.head * p.group + hh[i]);
-          if (l != -INFINITY) nl[i] = -kLog2e * l;
-        }
+        if (lane + 32 * i < cols && t < w.tokens)
+          nl[i] = __ldg(p.lse + (long long)(w.g.q0 + w.t0 + t) * p.hqo + w.head * p.group + hh[i]);
       }
     };
     float cur[4], nxt[4];
     fetch(w.q0, cur);
     for (int qt = w.q0; ok && qt < w.q1; ++qt, ++n) {
-      const int qs = n % kQStages;
+      const int qs = n % kQStages, ring = n % kRing;
       if (n >= kQStages) {
-        ok = mbar_wait(&sm.q_empty[qs], (n / kQStages - 1) & 1, p.pv.err, &sm.abort) &&
-             mbar_wait(&sm.l_empty[qs], (n / kQStages - 1) & 1, p.pv.err, &sm.abort);
-        ok = __all_sync(kAll, ok);
+        ok = __all_sync(kAll, mbar_wait(&sm.q_empty[qs], (n / kQStages - 1) & 1, p.pv.err, &sm.abort));
         if (!ok) break;
       }
       if (lane == 0) {
@@ -237,103 +254,113 @@ __device__ void load_queries(const WeightsParams& p, TcSmem& sm, Walk w, bool ca
         tc::tma_load_3d(sm.q[qs] + kQHalfBytes, tm_q, 64, w.head * p.group, tok0, &sm.q_full[qs]);
       }
       if (qt + 1 < w.q1) fetch(qt + 1, nxt);
-      bool dead = false;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        sm.nl[qs][lane + 32 * i] = cur[i];
-        dead |= lane + 32 * i < cols && cur[i] == -INFINITY;
+        const int c = lane + 32 * i;
+        const bool dead = cur[i] == -INFINITY;
+        const float v = dead ? kDead : cur[i] * unit;
+        if constexpr (kCap) {
+          sm.nl[ring][c] = v;
+        } else {
+          const float hi = __bfloat162float(__float2bfloat16_rn(v));
+          const float mid = __bfloat162float(__float2bfloat16_rn(v - hi));
+          // 16-byte piece 0 of the 128-byte swizzled row
+          *reinterpret_cast<uint2*>(sm.l[qs] + c * 128 + ((c & 7) << 4)) =
+              make_uint2(f2_to_bf16x2(hi, mid), f2_to_bf16x2(v - hi - mid, 0.f));
+        }
+        const uint32_t bits = __ballot_sync(kAll, dead);
+        if (lane == 0) sm.dead[ring][i] = bits;
         cur[i] = nxt[i];
       }
-      const bool any = __any_sync(kAll, dead);
-      if (lane == 0) sm.special[qs] = any;
+      if constexpr (!kCap) fence_proxy_async_smem();  // the MMA reads the -lse rows
+      mbar_arrive(&sm.q_full[qs]);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.l_full[qs]);
+      if (lane == 0) mbar_arrive(&sm.l_full[ring]);
     }
   }
   // never leave with tensor copies still landing in this CTA's shared memory
   for (int k = max(0, n - kQStages); k < n; ++k) mbar_wait_bounded(&sm.q_full[k % kQStages], (k / kQStages) & 1);
 }
 
+template <bool kCap>
 __device__ void issue(const WeightsParams& p, TcSmem& sm, Walk w, bool causal, uint32_t tmem) {
   constexpr uint32_t idesc = tc::idesc_bf16_f32(128, kCols, 0, 0);  // A = keys, B = query rows, both K-major
   const bool lead = (threadIdx.x & 31) == 0;
-  const uint32_t k_addr = smem_u32(sm.k[0]), q_addr = smem_u32(sm.q[0]);
-  int n = 0;
+  const uint32_t q_addr = smem_u32(sm.q[0]), l_addr = smem_u32(sm.l[0]), ones_addr = smem_u32(sm.ones);
+  int n = 0, u = 0;
   for (int seg = 0; w.more(); w.next(p, causal), ++seg) {
-    const int ks = seg % kKStages;
-    if (!__all_sync(kAll, mbar_wait(&sm.k_full[ks], (seg / kKStages) & 1, p.pv.err, &sm.abort))) return;
+    if (!__all_sync(kAll, mbar_wait(&sm.k_full, seg & 1, p.pv.err, &sm.abort))) return;
     for (int qt = w.q0; qt < w.q1; ++qt, ++n) {
-      const int qs = n % kQStages, b = n & 1;
+      const int qs = n % kQStages;
       if (!__all_sync(kAll, mbar_wait(&sm.q_full[qs], (n / kQStages) & 1, p.pv.err, &sm.abort))) return;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (n >= 2 && !__all_sync(kAll, mbar_wait(&sm.s_empty[h][b], ((n >> 1) - 1) & 1, p.pv.err, &sm.abort))) return;
+      for (int h = 0; h < 2; ++h, ++u) {
+        const int b = u % kSBufs;
+        if (u >= kSBufs && !__all_sync(kAll, mbar_wait(&sm.s_empty[b], (u / kSBufs - 1) & 1, p.pv.err, &sm.abort)))
+          return;
         tc::fence_after_sync();
         if (lead) {
+          const uint32_t d = tmem + kColS + uint32_t(b * kCols);
 #pragma unroll
-          for (int kh = 0; kh < 2; ++kh) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t a = tc::smem_desc(k_addr + ks * 2 * kKHalfBytes + kh * kKHalfBytes + h * (128 * 128) + kk * 32,
-                                               16, 1024, tc::kLayoutSw128);
-              const uint64_t bd = tc::smem_desc(q_addr + qs * 2 * kQHalfBytes + kh * kQHalfBytes + kk * 32, 16, 1024,
-                                                tc::kLayoutSw128);
-              tc::mma_ss(tmem + uint32_t((2 * h + b) * kCols), a, bd, idesc, (kh | kk) != 0 ? 1u : 0u);
-            }
+          for (int k = 0; k < 8; ++k) {  // 16 dims: 8 columns of the keys, 32 bytes of the Q rows
+            const uint64_t bd = tc::smem_desc(q_addr + qs * 2 * kQHalfBytes + (k >> 2) * kQHalfBytes + (k & 3) * 32, 16,
+                                              1024, tc::kLayoutSw128);
+            tc::mma_ts(d, tmem + kColK + uint32_t(h * 64 + k * 8), bd, idesc, k != 0 ? 1u : 0u);
           }
-          tc::commit(&sm.s_full[h][b]);
+          if constexpr (!kCap)
+            tc::mma_ss(d, tc::smem_desc(ones_addr, 16, 1024, tc::kLayoutSw128),
+                       tc::smem_desc(l_addr + qs * kQHalfBytes, 16, 1024, tc::kLayoutSw128), idesc, 1u);
+          tc::commit(&sm.s_full[b]);
         }
         __syncwarp();
       }
       if (lead) tc::commit(&sm.q_empty[qs]);
     }
-    if (lead) tc::commit(&sm.k_empty[ks]);
+    if (lead) tc::commit(&sm.k_empty);
     __syncwarp();
   }
 }
 
+constexpr int kChunk = 16;  // score columns a thread holds at a time (two chunks in flight)
+__device__ __forceinline__ void load_scores(uint32_t taddr, uint32_t (&r)[kChunk]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+               "%15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(taddr));
+}
 // Waits for the tensor-memory loads in flight.  The registers pass through, so that nothing that uses
 // them can be scheduled before the wait.
-__device__ __forceinline__ void wait_scores(uint32_t (&r)[32]) {
+__device__ __forceinline__ void wait_scores(uint32_t (&r)[kChunk]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
-                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                 "+r"(r[30]), "+r"(r[31])::"memory");
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 
-// 32 scores of the thread's key -> added to acc.  Columns outside [lo, hi) and those with nl = -inf
-// count for nothing when kMasked; without it none is outside and all scores are finite or their own
-// row's business.
+// A chunk of scores of the thread's key -> added to acc.  With kMasked, columns outside [lo, hi) and dead
+// ones count for nothing whatever their score is; without it none is outside, and a dead column's score
+// is so low that its power is 0.
 template <bool kMasked, bool kCap>
-__device__ __forceinline__ void add32(const uint32_t (&s)[32], const float* nl, int lo, int hi, const WeightsParams& p,
-                                      float2 (&acc)[4]) {
-  const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+__device__ __forceinline__ void add_chunk(const uint32_t (&s)[kChunk], const float* nl, int lo, int hi, uint32_t dead,
+                                          const WeightsParams& p, float2 (&acc)[4]) {
+  float2 x[kChunk / 2];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float4 n4 = *reinterpret_cast<const float4*>(nl + 4 * j);
-    const float nn[4] = {n4.x, n4.y, n4.z, n4.w};
-#pragma unroll
-    for (int e = 0; e < 4; e += 2) {
-      const int c = 4 * j + e;
-      float2 x = make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-      const float2 n2 = make_float2(nn[e], nn[e + 1]);
-      if constexpr (kCap) {
-        x = make_float2(p.cap_log2 * tanh_exp2(x.x * p.scale_log2 * p.inv_cap_log2),
-                        p.cap_log2 * tanh_exp2(x.y * p.scale_log2 * p.inv_cap_log2));
-        x = __fadd2_rn(x, n2);
-      } else {
-        x = __ffma2_rn(x, sc2, n2);
-      }
-      float2 w = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-      if constexpr (kMasked) {
-        w.x = c >= lo && c < hi && nn[e] != -INFINITY ? w.x : 0.f;
-        w.y = c + 1 >= lo && c + 1 < hi && nn[e + 1] != -INFINITY ? w.y : 0.f;
-      }
-      acc[(c >> 1) & 3] = __fadd2_rn(acc[(c >> 1) & 3], w);
+  for (int i = 0; i < kChunk / 2; ++i) {
+    const float2 v = make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+    if constexpr (kCap) {
+      const float in = p.scale_log2 * p.inv_cap_log2;
+      const float2 n2 = *reinterpret_cast<const float2*>(nl + 2 * i);
+      x[i] = __fadd2_rn(make_float2(p.cap_log2 * tanh_exp2(v.x * in), p.cap_log2 * tanh_exp2(v.y * in)), n2);
+    } else {
+      x[i] = __fmul2_rn(v, make_float2(p.scale_log2, p.scale_log2));
+    }
+    if constexpr (kMasked) {
+      if (2 * i < lo || 2 * i >= hi || ((dead >> (2 * i)) & 1u)) x[i].x = -INFINITY;
+      if (2 * i + 1 < lo || 2 * i + 1 >= hi || ((dead >> (2 * i + 1)) & 1u)) x[i].y = -INFINITY;
     }
   }
+#pragma unroll
+  for (int i = 0; i < kChunk / 2; ++i) acc[i & 3] = __fadd2_rn(acc[i & 3], make_float2(fast_exp2(x[i].x), fast_exp2(x[i].y)));
 }
 
 template <bool kWin, bool kCap>
@@ -356,12 +383,12 @@ __device__ void sum_weights(const WeightsParams& p, TcSmem& sm, Walk w, bool cau
     }
     float sum = 0.f;
     for (int qt = w.q0; qt < w.q1; ++qt, ++n) {
-      const int qs = n % kQStages, b = n & 1;
-      alive = alive && __all_sync(kAll, mbar_wait(&sm.l_full[qs], (n / kQStages) & 1, pv.err, &sm.abort) &&
-                                            mbar_wait(&sm.s_full[h][b], (n >> 1) & 1, pv.err, &sm.abort));
+      const int ring = n % kRing, u = 2 * n + h, b = u % kSBufs;
+      alive = alive && __all_sync(kAll, mbar_wait(&sm.l_full[ring], (n / kRing) & 1, pv.err, &sm.abort) &&
+                                            mbar_wait(&sm.s_full[b], (u / kSBufs) & 1, pv.err, &sm.abort));
       if (alive) {
         tc::fence_after_sync();
-        const uint32_t t_s = lane_base + uint32_t((2 * h + b) * kCols);
+        const uint32_t t_s = lane_base + kColS + uint32_t(b * kCols);
         const int tok = w.t0 + qt * p.tile_tokens;  // first token of the tile
         // column c belongs to token tok + c / g; key sees tokens from key - diag to key - diag + window
         int lo = 0, hi = kCols;
@@ -370,31 +397,33 @@ __device__ void sum_weights(const WeightsParams& p, TcSmem& sm, Walk w, bool cau
           if (kWin) hi = int(max(0ll, min((long long)p.tile_tokens, (long long)key - diag - tok + p.window_left + 1))) * p.group;
           if (kWin && hi == p.tile_tokens * p.group) hi = kCols;
         }
-        const bool masked = __any_sync(kAll, lo > 0 || hi < kCols) || sm.special[qs];
+        const uint4 dead = *reinterpret_cast<const uint4*>(sm.dead[ring]);
+        const bool masked = __any_sync(kAll, lo > 0 || hi < kCols) || (dead.x | dead.y | dead.z | dead.w) != 0u;
         float2 acc[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i] = make_float2(0.f, 0.f);
-        uint32_t s[2][32];
-        tc::tmem_ld32(t_s, s[0]);
+        uint32_t s[2][kChunk];
+        load_scores(t_s, s[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kCols / kChunk; ++c) {
           wait_scores(s[c & 1]);
-          if (c < 3) tc::tmem_ld32(t_s + 32 * (c + 1), s[(c + 1) & 1]);
-          if (c == 3) {
+          if (c + 1 < kCols / kChunk) {
+            load_scores(t_s + kChunk * (c + 1), s[(c + 1) & 1]);
+          } else {
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.s_empty[h][b]);
+            if (lane == 0) mbar_arrive(&sm.s_empty[b]);
           }
+          const float* nl = sm.nl[ring] + kChunk * c;
+          const uint32_t word = c < 2 ? dead.x : c < 4 ? dead.y : c < 6 ? dead.z : dead.w;
           if (masked)
-            add32<true, kCap>(s[c & 1], sm.nl[qs] + 32 * c, lo - 32 * c, hi - 32 * c, p, acc);
+            add_chunk<true, kCap>(s[c & 1], nl, lo - kChunk * c, hi - kChunk * c, word >> (kChunk * (c & 1)), p, acc);
           else
-            add32<false, kCap>(s[c & 1], sm.nl[qs] + 32 * c, 0, 32, p, acc);
+            add_chunk<false, kCap>(s[c & 1], nl, 0, 0, 0u, p, acc);
         }
         const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
         sum += a.x + a.y;
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.l_empty[qs]);
     }
     if (!alive) out = nullptr;  // the error is recorded; the barriers and counts below still go their way
     if (w.q0 == 0 && w.q1 == w.cost) {
@@ -426,30 +455,31 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   TcSmem& sm = *reinterpret_cast<TcSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kKStages; ++i) {
-      mbar_init(&sm.k_full[i], 128);
-      mbar_init(&sm.k_empty[i], 1);
-    }
+    mbar_init(&sm.k_full, 8);
+    mbar_init(&sm.k_empty, 1);
     for (int i = 0; i < kQStages; ++i) {
-      mbar_init(&sm.q_full[i], 1);
+      mbar_init(&sm.q_full[i], 33);  // the copy's issuer and the 32 writers of the -lse rows
       mbar_init(&sm.q_empty[i], 1);
-      mbar_init(&sm.l_full[i], 1);
-      mbar_init(&sm.l_empty[i], 8);
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&sm.s_full[i >> 1][i & 1], 1);
-      mbar_init(&sm.s_empty[i >> 1][i & 1], 4);
+    for (int i = 0; i < kRing; ++i) mbar_init(&sm.l_full[i], 1);
+    for (int i = 0; i < kSBufs; ++i) {
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.s_empty[i], 4);
     }
     sm.abort = 0;
     fence_mbar_init();
   }
-  if (p.tile_tokens * p.group < kCols) {  // rows of the Q stages that no copy fills: zero scores
-    for (int i = threadIdx.x; i < int(sizeof(sm.q) / 16); i += kTcThreads)
-      reinterpret_cast<uint4*>(sm.q[0])[i] = make_uint4(0, 0, 0, 0);
-    fence_proxy_async_smem();
+  // rows of the Q stages that no copy fills, the -lse rows' zeros, the ones
+  const int first = p.tile_tokens * p.group < kCols ? 0 : int(offsetof(TcSmem, l) / 16);
+  for (int i = first + threadIdx.x; i < int(offsetof(TcSmem, ones) / 16); i += kTcThreads)
+    reinterpret_cast<uint4*>(&sm)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = threadIdx.x; i < kQHalfBytes / 16; i += kTcThreads) {
+    const int r = i >> 3, piece = (i & 7) ^ (r & 7);
+    reinterpret_cast<uint4*>(sm.ones)[i] = piece == 0 ? make_uint4(0x3f803f80u, 0x00003f80u, 0, 0) : make_uint4(0, 0, 0, 0);
   }
-  if (warp == 8 && lane == 0) tc::tma_prefetch_desc(&tm_q);
-  if (warp == 9) {
+  fence_proxy_async_smem();
+  if (warp == 16 && lane == 0) tc::tma_prefetch_desc(&tm_q);
+  if (warp == 17) {
     tc::tmem_alloc(&sm.tmem_base, kTmemCols);
     tc::tmem_relinquish();
   }
@@ -467,18 +497,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   } else if (int(blockIdx.x) < ctas) {
     Walk w;
     w.init(p, causal, batch, int((long long)line * blockIdx.x / ctas), int((long long)line * (blockIdx.x + 1) / ctas));
-    if (warp < 8)
+    if (warp < 8) {
+      tc::regs_decrease<kSumRegs>();
       sum_weights<kWin, kCap>(p, sm, w, causal, tmem, line, ctas);
-    else if (warp == 8)
-      load_queries(p, sm, w, causal, &tm_q);
-    else if (warp == 9)
-      issue(p, sm, w, causal, tmem);
-    else
-      load_keys<kFp8>(p, sm, w, causal);
+    } else if (warp < 16) {
+      tc::regs_increase<kLoadRegs>();
+      load_keys<kFp8>(p, sm, w, causal, tmem);
+    } else {
+      tc::regs_decrease<kControlRegs>();
+      if (warp == 16)
+        load_queries<kCap>(p, sm, w, causal, &tm_q);
+      else if (warp == 17)
+        issue<kCap>(p, sm, w, causal, tmem);
+    }
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kTmemCols);
   }
