@@ -3,24 +3,20 @@
 //
 //   w_j = sum over query rows r (tokens x heads of the group) that see key j of exp2(scale2 q_r.k_j - lse2_r)
 //
-// The scores are computed as S^T = K Q^T: keys are the 128 lanes of the tcgen05 accumulator, query
-// rows its columns.  A thread then owns one key and sums over columns in its own registers: no
-// maximum, no cross-lane step, no second product, and one write per key at the end.  A work item is
-// 256 keys of one KV head (two 128-lane MMA tiles that share every Q tile, which halves the L2
-// traffic of Q) against all query rows that see one of them, in tiles of 128 rows (128 / g tokens x
-// g heads, one TMA box a 64-dim half).
+// A work item is 256 keys of one KV head against all query rows that see one of them, in Q tiles of 128
+// rows (128 / g tokens x g heads, one TMA box a 64-dim half).  The item's keys stay in shared memory as
+// the 256-column B operand; every Q tile is one 128 x 256 product.  Query rows are the accumulator's
+// lanes: a thread's scores all belong to one row, whose -lse and mask bounds sit in registers, so a
+// score costs one multiply-add, one exponential and one addition, into 64 running column sums a thread.
+// There is no maximum, no second product, and lanes are added up once per item.
+//   The other way round (keys on the lanes, one running sum a thread) needs the -lse of each column in
+// every thread: read from shared memory it took as long as the exponentials, and as a further k-step of
+// the product an eighth more tensor time.  Products of 128 columns measured 75 clocks a 16-dim step with the
+// keys in tensor memory and 108 from shared memory (96 columns: 59 and 92), those of 256 columns 172:
+// a 128 x 256 tile takes 1376 clocks this way, 1200 + the -lse step the other way.
 //
-// The item's keys stay in tensor memory as the A operand (128 columns), so the products read only Q
-// from shared memory; from shared memory both operands of a 128-column product take its whole
-// bandwidth.  The -lse of a column is the same for all keys: it is added by one more 16-wide k-step
-// with ones on the key side and -lse / scale, split into three bf16 parts (24 bits), on the query
-// side.  (Read from shared memory by the threads, 128 values a thread and tile, it took as long as
-// the exponentials: a broadcast still moves 16 bytes a lane.)  The exponential's argument is then one
-// multiplication.  With a soft-cap the -lse cannot go inside the tanh and is read that way.
-//
-// What bounds it: per Q tile and item the tensor cores take 2 x 128x128x144 products (1152 clocks at
-// the nominal rate) and the exponentials 32768 results (1024 clocks at 32 a clock and SM): the two
-// run at the same time, over three score buffers of 128 columns.
+// What bounds it: the products (1376 clocks a tile, above) beside 32768 exponentials (1024 clocks at 32 a
+// clock and SM); both run at the same time, over two score buffers.
 //
 // Work split: the Q tiles of all items lie on one line, request by request, KV head by KV head, key
 // tile by key tile (the causal mask gives later key tiles fewer Q tiles); CTA c takes the c-th
@@ -29,13 +25,12 @@
 // line order: the result does not depend on who is last.  Each CTA has at most two cut items, so the
 // slots are bounded by the grid, not by the batch.
 //
-// One CTA per SM, 18 warps:
-//   warps 0-7    exponentials and sums: warps 0-3 the first 128 keys, 4-7 the others
-//   warps 8-15   key loader: a thread holds one key's 128 dims in registers until the previous item's
-//                last product is done, then stores them to tensor memory; any page size and layout;
-//                e4m3 codes are widened to bf16 (exact) on the way, so Q stays bf16
-//   warp 16      TMA producer of Q tiles (four stages) and writer of their -lse rows
-//   warp 17      tensor memory, MMA issue
+// One CTA per SM, 20 warps:
+//   warps 0-15   exponentials and sums: 4 warps (128 rows) for each 64 of the 256 keys
+//   warps 16-17  key loader (two stages), any page size and layout: 16-byte asynchronous copies into the
+//                128-byte swizzle; e4m3 codes are widened to bf16 (exact) on the way, so Q stays bf16
+//   warp 18      TMA producer of Q tiles (three stages)
+//   warp 19      tensor memory, MMA issue
 #include <cuda.h>
 #include <cuda_fp8.h>
 
@@ -51,34 +46,21 @@ namespace fi {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kTcThreads = 640;  // five warpgroups; the last one's second half is idle
-// Registers after launch (640 threads x 96): 256 x 88 + 256 x 112 + 128 x 80 = 640 x 96.
-constexpr uint32_t kSumRegs = 88;
-constexpr uint32_t kLoadRegs = 112;
-constexpr uint32_t kControlRegs = 80;
+constexpr int kTcThreads = 640;
+constexpr int kSumThreads = 512;
+// Registers after launch (640 threads x 96): 512 x 104 + 128 x 64 = 640 x 96.
+constexpr uint32_t kSumRegs = 104;
+constexpr uint32_t kControlRegs = 64;
 constexpr int kKeys = kTileKeys;                // keys of an item
-constexpr int kCols = kWeightTileRows;          // query rows of a Q tile
-constexpr int kQHalfBytes = kCols * 128;        // 64 dims of a Q tile, or its -lse rows
-constexpr int kQStages = 4;
-constexpr int kSBufs = 3;
-constexpr int kRing = 8;                        // tiles whose column notes are kept
+constexpr int kRows = kWeightTileRows;          // query rows of a Q tile
+constexpr int kCols = 64;                       // keys of a summing warp
+constexpr int kLoadThreads = 64;
+constexpr int kKHalfBytes = kKeys * 128;        // 64 dims of the item's keys
+constexpr int kQHalfBytes = kRows * 128;        // 64 dims of a Q tile
+constexpr int kQStages = 3;
+constexpr int kKStages = 2;
+constexpr int kSBufs = 2;                       // score buffers of 256 columns
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColK = 0;                   // 64 columns per half of the item's keys
-constexpr uint32_t kColS = 128;                 // kSBufs score buffers of 128 columns
-constexpr float kDead = -1e30f;                 // -lse / scale of a column that counts for nothing
-
-struct TcSmem {
-  uint8_t q[kQStages][2 * kQHalfBytes];
-  uint8_t l[kQStages][kQHalfBytes];  // per column 128 bytes: {hi, mid, lo, 0...} of -lse / scale, rest zero
-  uint8_t ones[kQHalfBytes];         // the key side of the -lse step: {1, 1, 1, 0...}
-  float nl[kRing][kCols];            // soft-cap: -lse in the log2 domain
-  uint32_t dead[kRing][4];           // columns that count for nothing, whatever their score is
-  uint64_t k_full, k_empty, q_full[kQStages], q_empty[kQStages], l_full[kRing];
-  uint64_t s_full[kSBufs], s_empty[kSBufs];
-  uint32_t tmem_base;
-  int abort;
-  int last;
-};
 
 // The CTA's walk over its piece of the line, one segment (run of Q tiles of one item) at a time.
 // Every member is uniform over the warp; whole warps call init and next.
@@ -137,6 +119,25 @@ struct Walk {
     q0 = rem - before;
     segment(p, causal);
   }
+  // Thread 0 of the summing warps: the segment at hand, written down.
+  template <typename S>
+  __device__ void publish(const WeightsParams& p, S& s, int line, int ctas) const {
+    const int tok = t0 + q0 * p.tile_tokens, start = pos - q0;
+    s.tiles = more() ? q1 - q0 : 0;
+    if (!more()) return;
+    s.pos = g.lkv - g.lq + tok - kt * kKeys;
+    s.tokens = tokens - q0 * p.tile_tokens;
+    s.whole = q0 == 0 && q1 == cost;
+    s.piece = int(blockIdx.x) * 2 + (q0 == 0 ? 1 : 0);
+    s.c1 = int(((long long)(start + 1) * ctas - 1) / line);
+    s.c2 = int(((long long)(start + cost) * ctas - 1) / line);
+    s.key0 = kt * kKeys;
+    s.head = head;
+    s.kv0 = g.kv0;
+    s.lkv = g.lkv;
+    s.first_new = p.new_keys ? g.lkv - g.lq : g.lkv;
+    s.lse = (long long)(g.q0 + tok) * p.hqo + head * p.group;
+  }
   __device__ __forceinline__ bool more() const { return pos < end; }
   __device__ void next(const WeightsParams& p, bool causal) {
     pos += q1 - q0;
@@ -157,6 +158,29 @@ struct Walk {
   }
 };
 
+// What the summing warps keep of a segment, in shared memory: their registers hold the column sums.
+struct Segment {
+  int tiles;       // 0: no more
+  int pos;         // key position of the first tile's first token, relative to the item's first key
+  int tokens;      // query tokens from that one on
+  int whole;       // 1: all of the item's Q tiles
+  int piece, c1, c2;  // cut items: this CTA's slot, the first and last CTA that have a piece
+  int key0, head, kv0, lkv, first_new;
+  long long lse;   // offset of the first token's first head
+};
+
+struct TcSmem {
+  uint8_t k[kKStages][2 * kKHalfBytes];
+  uint8_t q[kQStages][2 * kQHalfBytes];
+  Walk walk;         // of the summing warps, one ahead of them
+  Segment seg[3];    // what they know of a segment: the one at work, the next, and the last one's write-out
+  float red[kKeys];  // the item's sums, added up over the four groups of 32 rows
+  uint64_t k_full[kKStages], k_empty[kKStages], q_full[kQStages], q_empty[kQStages], s_full[kSBufs], s_empty[kSBufs];
+  uint32_t tmem_base;
+  int abort;
+  int last;
+};
+
 // Four e4m3 codes -> four bf16 (exact: e4m3 values have 4 significant bits and small exponents).
 __device__ __forceinline__ uint2 widen4(uint32_t codes) {
   const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes & 0xffffu), __NV_E4M3);
@@ -165,285 +189,277 @@ __device__ __forceinline__ uint2 widen4(uint32_t codes) {
   return make_uint2(f2_to_bf16x2(a.x, a.y), f2_to_bf16x2(b.x, b.y));
 }
 
-// One key row a thread: 128 dims as 64 bf16 pairs, in tensor-memory columns 0..63 of the half.
 template <bool kFp8>
-__device__ void load_keys(const WeightsParams& p, TcSmem& sm, Walk w, bool causal, uint32_t tmem) {
+__device__ void load_keys(const WeightsParams& p, TcSmem& sm, Walk w, bool causal) {
   const PageView& pv = p.pv;
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 8;
-  const int row = warp * 32 + lane;
-  const uint32_t t_k = tmem + (uint32_t((warp & 3) * 32) << 16) + kColK + uint32_t((warp >> 2) * 64);
+  const int tid = threadIdx.x - kSumThreads;     // 0..63
+  constexpr int kLanes = kFp8 ? 8 : 16;          // threads of a row, 16 bytes each
+  constexpr int kRowsPass = kLoadThreads / kLanes;
+  constexpr int kBatch = kFp8 ? 4 : 8;
+  const int ch = tid % kLanes, row0 = tid / kLanes;
+  const uint8_t* pages = static_cast<const uint8_t*>(p.k_pages);
   for (int n = 0; w.more(); w.next(p, causal), ++n) {
-    const int key = w.kt * kKeys + row;
-    uint32_t v[2][32];
-    int page, slot;
-    const bool on = key < w.g.lkv && locate(pv, w.g.kv0, key, page, slot);
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.k_pages) +
-                                                      (on ? kv_offset(pv, page, slot, w.head) * (kFp8 ? 1 : 2) : 0));
-    if constexpr (kFp8) {
-      uint4 x[8];
+    const int ks = n % kKStages;
+    bool ok = true;
+    if (n >= kKStages) ok = mbar_wait(&sm.k_empty[ks], (n / kKStages - 1) & 1, pv.err, &sm.abort);
+    if (!__all_sync(kAll, ok)) return;
+    auto place = [&](int row, int c16) {  // 16-byte piece c16 (0..15) of a bf16 row
+      return sm.k[ks] + (c16 >> 3) * kKHalfBytes + row * 128 + (((c16 & 7) ^ (row & 7)) << 4);
+    };
+    for (int i0 = row0; i0 < kKeys; i0 += kBatch * kRowsPass) {
+      const uint8_t* src[kBatch];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = on ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < kBatch; ++i) {
+        const int key = w.kt * kKeys + i0 + i * kRowsPass;
+        int page, slot;
+        src[i] = nullptr;
+        if (key < w.g.lkv && locate(pv, w.g.kv0, key, page, slot))
+          src[i] = pages + kv_offset(pv, page, slot, w.head) * (kFp8 ? 1 : 2) + 16 * ch;
+      }
+      if constexpr (kFp8) {
+        uint4 v[kBatch];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        for (int i = 0; i < kBatch; ++i)
+          v[i] = src[i] ? __ldg(reinterpret_cast<const uint4*>(src[i])) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint2 y = widen4(u[e]);
-          v[i >> 2][(8 * i + 2 * e) & 31] = y.x;
-          v[i >> 2][(8 * i + 2 * e + 1) & 31] = y.y;
+        for (int i = 0; i < kBatch; ++i) {
+          const int row = i0 + i * kRowsPass;
+          const uint2 a = widen4(v[i].x), b = widen4(v[i].y), c = widen4(v[i].z), d = widen4(v[i].w);
+          *reinterpret_cast<uint4*>(place(row, 2 * ch)) = make_uint4(a.x, a.y, b.x, b.y);
+          *reinterpret_cast<uint4*>(place(row, 2 * ch + 1)) = make_uint4(c.x, c.y, d.x, d.y);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int row = i0 + i * kRowsPass;
+          if (src[i])
+            cp_async_16(place(row, ch), src[i]);
+          else
+            *reinterpret_cast<uint4*>(place(row, ch)) = make_uint4(0, 0, 0, 0);
         }
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint4 x = on ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-        v[i >> 3][(4 * i) & 31] = x.x;
-        v[i >> 3][(4 * i + 1) & 31] = x.y;
-        v[i >> 3][(4 * i + 2) & 31] = x.z;
-        v[i >> 3][(4 * i + 3) & 31] = x.w;
-      }
     }
-    __syncwarp();
-    if (n > 0 && !__all_sync(kAll, mbar_wait(&sm.k_empty, (n - 1) & 1, pv.err, &sm.abort))) return;
-    tc::fence_after_sync();
-    tc::tmem_st32(t_k, v[0]);
-    tc::tmem_st32(t_k + 32, v[1]);
-    tc::tmem_wait_st();
-    tc::fence_before_sync();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.k_full);
+    cp_async_wait_all();
+    fence_proxy_async_smem();
+    mbar_arrive(&sm.k_full[ks]);
   }
 }
 
-template <bool kCap>
 __device__ void load_queries(const WeightsParams& p, TcSmem& sm, Walk w, bool causal, const CUtensorMap* tm_q) {
-  const int lane = threadIdx.x & 31;
-  const int cols = p.tile_tokens * p.group;
-  const float unit = kCap ? -kLog2e : -kLog2e / p.scale_log2;  // soft-cap: log2 domain; else in units of the raw score
-  // this lane's columns are lane + 32 i: their place in the tile does not change
-  int tok[4], hh[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    tok[i] = (lane + 32 * i) / p.group;
-    hh[i] = (lane + 32 * i) - tok[i] * p.group;
-  }
+  const uint32_t bytes = uint32_t(2 * 128 * p.tile_tokens * p.group);
   int n = 0;
   bool ok = true;
   for (; ok && w.more(); w.next(p, causal)) {
-    auto fetch = [&](int qt, float (&nl)[4]) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = qt * p.tile_tokens + tok[i];
-        nl[i] = -INFINITY;
-        if (lane + 32 * i < cols && t < w.tokens)
-          nl[i] = __ldg(p.lse + (long long)(w.g.q0 + w.t0 + t) * p.hqo + w.head * p.group + hh[i]);
-      }
-    };
-    float cur[4], nxt[4];
-    fetch(w.q0, cur);
-    for (int qt = w.q0; ok && qt < w.q1; ++qt, ++n) {
-      const int qs = n % kQStages, ring = n % kRing;
-      if (n >= kQStages) {
-        ok = __all_sync(kAll, mbar_wait(&sm.q_empty[qs], (n / kQStages - 1) & 1, p.pv.err, &sm.abort));
-        if (!ok) break;
-      }
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&sm.q_full[qs], uint32_t(2 * 128 * cols));
-        const int tok0 = w.g.q0 + w.t0 + qt * p.tile_tokens;
-        tc::tma_load_3d(sm.q[qs], tm_q, 0, w.head * p.group, tok0, &sm.q_full[qs]);
-        tc::tma_load_3d(sm.q[qs] + kQHalfBytes, tm_q, 64, w.head * p.group, tok0, &sm.q_full[qs]);
-      }
-      if (qt + 1 < w.q1) fetch(qt + 1, nxt);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = lane + 32 * i;
-        const bool dead = cur[i] == -INFINITY;
-        const float v = dead ? kDead : cur[i] * unit;
-        if constexpr (kCap) {
-          sm.nl[ring][c] = v;
-        } else {
-          const float hi = __bfloat162float(__float2bfloat16_rn(v));
-          const float mid = __bfloat162float(__float2bfloat16_rn(v - hi));
-          // 16-byte piece 0 of the 128-byte swizzled row
-          *reinterpret_cast<uint2*>(sm.l[qs] + c * 128 + ((c & 7) << 4)) =
-              make_uint2(f2_to_bf16x2(hi, mid), f2_to_bf16x2(v - hi - mid, 0.f));
-        }
-        const uint32_t bits = __ballot_sync(kAll, dead);
-        if (lane == 0) sm.dead[ring][i] = bits;
-        cur[i] = nxt[i];
-      }
-      if constexpr (!kCap) fence_proxy_async_smem();  // the MMA reads the -lse rows
-      mbar_arrive(&sm.q_full[qs]);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.l_full[ring]);
+    for (int qt = w.q0; qt < w.q1; ++qt, ++n) {
+      const int qs = n % kQStages;
+      if (n >= kQStages) ok = mbar_wait(&sm.q_empty[qs], (n / kQStages - 1) & 1, p.pv.err, &sm.abort);
+      if (!ok) break;
+      mbar_arrive_expect_tx(&sm.q_full[qs], bytes);
+      const int tok0 = w.g.q0 + w.t0 + qt * p.tile_tokens;
+      tc::tma_load_3d(sm.q[qs], tm_q, 0, w.head * p.group, tok0, &sm.q_full[qs]);
+      tc::tma_load_3d(sm.q[qs] + kQHalfBytes, tm_q, 64, w.head * p.group, tok0, &sm.q_full[qs]);
     }
   }
   // never leave with tensor copies still landing in this CTA's shared memory
   for (int k = max(0, n - kQStages); k < n; ++k) mbar_wait_bounded(&sm.q_full[k % kQStages], (k / kQStages) & 1);
 }
 
-template <bool kCap>
+// One lane of the warp, the same each time; the branch on it keeps the warp's control flow uniform, so
+// descriptors stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t on;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+  return on != 0;
+}
+
+// Issues the products, one thread of a warp that walks together (issued from a branch on the lane number a
+// product took 131 clocks of its thread, whatever its size).  The descriptors of a stage are the first
+// stage's plus an address step in 16-byte units.
 __device__ void issue(const WeightsParams& p, TcSmem& sm, Walk w, bool causal, uint32_t tmem) {
-  constexpr uint32_t idesc = tc::idesc_bf16_f32(128, kCols, 0, 0);  // A = keys, B = query rows, both K-major
-  const bool lead = (threadIdx.x & 31) == 0;
-  const uint32_t q_addr = smem_u32(sm.q[0]), l_addr = smem_u32(sm.l[0]), ones_addr = smem_u32(sm.ones);
-  int n = 0, u = 0;
+  constexpr uint32_t idesc = tc::idesc_bf16_f32(kRows, kKeys, 0, 0);  // A = query rows, B = keys, both K-major
+  const uint64_t q_desc = tc::smem_desc(smem_u32(sm.q[0]), 16, 1024, tc::kLayoutSw128);
+  const uint64_t k_desc = tc::smem_desc(smem_u32(sm.k[0]), 16, 1024, tc::kLayoutSw128);
+  int n = 0;
   for (int seg = 0; w.more(); w.next(p, causal), ++seg) {
-    if (!__all_sync(kAll, mbar_wait(&sm.k_full, seg & 1, p.pv.err, &sm.abort))) return;
+    const int ks = seg % kKStages;
+    if (!__all_sync(kAll, mbar_wait(&sm.k_full[ks], (seg / kKStages) & 1, p.pv.err, &sm.abort))) return;
+    const uint64_t kd = k_desc + uint64_t(ks * (2 * kKHalfBytes / 16));
     for (int qt = w.q0; qt < w.q1; ++qt, ++n) {
-      const int qs = n % kQStages;
+      const int qs = n % kQStages, b = n % kSBufs;
       if (!__all_sync(kAll, mbar_wait(&sm.q_full[qs], (n / kQStages) & 1, p.pv.err, &sm.abort))) return;
+      if (n >= kSBufs && !__all_sync(kAll, mbar_wait(&sm.s_empty[b], (n / kSBufs - 1) & 1, p.pv.err, &sm.abort))) return;
+      tc::fence_after_sync();
+      const uint64_t qd = q_desc + uint64_t(qs * (2 * kQHalfBytes / 16));
+      if (elect_one()) {
+        const uint32_t d = tmem + uint32_t(b * kKeys);
 #pragma unroll
-      for (int h = 0; h < 2; ++h, ++u) {
-        const int b = u % kSBufs;
-        if (u >= kSBufs && !__all_sync(kAll, mbar_wait(&sm.s_empty[b], (u / kSBufs - 1) & 1, p.pv.err, &sm.abort)))
-          return;
-        tc::fence_after_sync();
-        if (lead) {
-          const uint32_t d = tmem + kColS + uint32_t(b * kCols);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {  // 16 dims: 8 columns of the keys, 32 bytes of the Q rows
-            const uint64_t bd = tc::smem_desc(q_addr + qs * 2 * kQHalfBytes + (k >> 2) * kQHalfBytes + (k & 3) * 32, 16,
-                                              1024, tc::kLayoutSw128);
-            tc::mma_ts(d, tmem + kColK + uint32_t(h * 64 + k * 8), bd, idesc, k != 0 ? 1u : 0u);
-          }
-          if constexpr (!kCap)
-            tc::mma_ss(d, tc::smem_desc(ones_addr, 16, 1024, tc::kLayoutSw128),
-                       tc::smem_desc(l_addr + qs * kQHalfBytes, 16, 1024, tc::kLayoutSw128), idesc, 1u);
-          tc::commit(&sm.s_full[b]);
-        }
-        __syncwarp();
+        for (int k = 0; k < 8; ++k)  // 16 dims: 32 bytes of the swizzled rows
+          tc::mma_ss(d, qd + uint64_t(((k >> 2) * kQHalfBytes + (k & 3) * 32) / 16),
+                     kd + uint64_t(((k >> 2) * kKHalfBytes + (k & 3) * 32) / 16), idesc, k != 0 ? 1u : 0u);
+        tc::commit(&sm.s_full[b]);
+        tc::commit(&sm.q_empty[qs]);
       }
-      if (lead) tc::commit(&sm.q_empty[qs]);
+      __syncwarp();
     }
-    if (lead) tc::commit(&sm.k_empty);
+    if (elect_one()) tc::commit(&sm.k_empty[ks]);
     __syncwarp();
   }
 }
 
-constexpr int kChunk = 16;  // score columns a thread holds at a time (two chunks in flight)
+constexpr int kChunk = 8;  // scores a thread loads at a time; the next chunk is in flight meanwhile
 __device__ __forceinline__ void load_scores(uint32_t taddr, uint32_t (&r)[kChunk]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-               "%15}, [%16];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
 // Waits for the tensor-memory loads in flight.  The registers pass through, so that nothing that uses
 // them can be scheduled before the wait.
 __device__ __forceinline__ void wait_scores(uint32_t (&r)[kChunk]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])::"memory");
 }
 
-// A chunk of scores of the thread's key -> added to acc.  With kMasked, columns outside [lo, hi) and dead
-// ones count for nothing whatever their score is; without it none is outside, and a dead column's score
-// is so low that its power is 0.
+// A chunk of the row's scores -> added to the column sums.  With kMasked, columns outside [lo, hi) get
+// nothing whatever their score is.
 template <bool kMasked, bool kCap>
-__device__ __forceinline__ void add_chunk(const uint32_t (&s)[kChunk], const float* nl, int lo, int hi, uint32_t dead,
-                                          const WeightsParams& p, float2 (&acc)[4]) {
-  float2 x[kChunk / 2];
+__device__ __forceinline__ void add_chunk(const uint32_t (&s)[kChunk], float nl, int lo, int hi, const WeightsParams& p,
+                                          float2* acc) {
 #pragma unroll
   for (int i = 0; i < kChunk / 2; ++i) {
-    const float2 v = make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
+    float2 x = make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
     if constexpr (kCap) {
       const float in = p.scale_log2 * p.inv_cap_log2;
-      const float2 n2 = *reinterpret_cast<const float2*>(nl + 2 * i);
-      x[i] = __fadd2_rn(make_float2(p.cap_log2 * tanh_exp2(v.x * in), p.cap_log2 * tanh_exp2(v.y * in)), n2);
+      x = __ffma2_rn(make_float2(tanh_exp2(x.x * in), tanh_exp2(x.y * in)), make_float2(p.cap_log2, p.cap_log2),
+                     make_float2(nl, nl));
     } else {
-      x[i] = __fmul2_rn(v, make_float2(p.scale_log2, p.scale_log2));
+      x = __ffma2_rn(x, make_float2(p.scale_log2, p.scale_log2), make_float2(nl, nl));
     }
     if constexpr (kMasked) {
-      if (2 * i < lo || 2 * i >= hi || ((dead >> (2 * i)) & 1u)) x[i].x = -INFINITY;
-      if (2 * i + 1 < lo || 2 * i + 1 >= hi || ((dead >> (2 * i + 1)) & 1u)) x[i].y = -INFINITY;
+      if (2 * i < lo || 2 * i >= hi) x.x = -INFINITY;
+      if (2 * i + 1 < lo || 2 * i + 1 >= hi) x.y = -INFINITY;
     }
+    acc[i] = __fadd2_rn(acc[i], make_float2(fast_exp2(x.x), fast_exp2(x.y)));
   }
+}
+
+// The row's 64 scores of a tile.
+template <bool kMasked, bool kCap>
+__device__ __forceinline__ void add_tile(uint32_t t_s, float nl, int lo, int hi, const WeightsParams& p, uint64_t* s_empty,
+                                         float2 (&acc)[kCols / 2]) {
+  uint32_t s[2][kChunk];
+  load_scores(t_s, s[0]);
 #pragma unroll
-  for (int i = 0; i < kChunk / 2; ++i) acc[i & 3] = __fadd2_rn(acc[i & 3], make_float2(fast_exp2(x[i].x), fast_exp2(x[i].y)));
+  for (int c = 0; c < kCols / kChunk; ++c) {
+    wait_scores(s[c & 1]);
+    if (c + 1 < kCols / kChunk) {
+      load_scores(t_s + kChunk * (c + 1), s[(c + 1) & 1]);
+    } else {
+      tc::fence_before_sync();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(s_empty);
+    }
+    add_chunk<kMasked, kCap>(s[c & 1], nl, lo - kChunk * c, hi - kChunk * c, p, acc + c * (kChunk / 2));
+  }
 }
 
 template <bool kWin, bool kCap>
-__device__ void sum_weights(const WeightsParams& p, TcSmem& sm, Walk w, bool causal, uint32_t tmem, int line, int ctas) {
+__device__ void sum_weights(const WeightsParams& p, TcSmem& sm, bool causal, uint32_t tmem, int line, int ctas) {
   const PageView& pv = p.pv;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = warp >> 2;
-  const int row = threadIdx.x;  // key of the item: 128 h + TMEM lane
-  const uint32_t lane_base = tmem + (uint32_t((warp & 3) * 32) << 16);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = threadIdx.x & (kRows - 1);   // query row of the tile: TMEM lane
+  const int col0 = (warp >> 2) * kCols;        // first key of this warp
+  const uint32_t t_lane = tmem + (uint32_t((warp & 3) * 32) << 16) + uint32_t(col0);
   int n = 0;
   bool alive = true;
-  for (; w.more(); w.next(p, causal)) {
-    const int key = w.kt * kKeys + row;
-    const int diag = w.g.lkv - w.g.lq;  // position of the request's first query token
-    float* out = nullptr;
-    float old = 0.f;
-    {
-      int page, slot;
-      if (key < w.g.lkv && locate(pv, w.g.kv0, key, page, slot)) out = p.weights + weight_offset(pv, page, slot, w.head);
-      if (out != nullptr && p.decay != 0.f && !(p.new_keys && key >= diag)) old = p.decay * __ldcg(out);
+  for (int i = 0; sm.seg[i].tiles > 0; i = i == 2 ? 0 : i + 1) {
+    const Segment& g = sm.seg[i];
+    if (threadIdx.x == 0) {  // the next segment; its readers come to it after the barriers below
+      sm.walk.next(p, causal);
+      sm.walk.publish(p, sm.seg[i == 2 ? 0 : i + 1], line, ctas);
     }
-    float sum = 0.f;
-    for (int qt = w.q0; qt < w.q1; ++qt, ++n) {
-      const int ring = n % kRing, u = 2 * n + h, b = u % kSBufs;
-      alive = alive && __all_sync(kAll, mbar_wait(&sm.l_full[ring], (n / kRing) & 1, pv.err, &sm.abort) &&
-                                            mbar_wait(&sm.s_full[b], (u / kSBufs) & 1, pv.err, &sm.abort));
+    __syncwarp();
+    float2 acc[kCols / 2];
+#pragma unroll
+    for (int k = 0; k < kCols / 2; ++k) acc[k] = make_float2(0.f, 0.f);
+    const int my_tok = row / p.group;
+    int pos = g.pos + my_tok - col0;                                     // the row sees columns up to this one
+    int left = my_tok < p.tile_tokens ? g.tokens - my_tok : 0;           // rows from here on, in tokens
+    const float* lse_at = p.lse + g.lse + (long long)my_tok * p.hqo + (row - my_tok * p.group);
+    // lse of the thread's row in the next tile, -inf where there is none.  Nothing looks at it before the
+    // next tile: a use here would wait for the load (600 clocks a tile).
+    float lse = -INFINITY;
+    if (left > 0) lse = __ldg(lse_at);
+    const int n_end = n + g.tiles;
+    for (; n < n_end; ++n) {
+      const int b = n % kSBufs;
+      const float nl = -kLog2e * lse;
+      int lo = 0, hi = kCols;  // the columns the row sees
+      if (causal) {
+        hi = min(kCols, pos + 1);
+        if (kWin) lo = max(0, pos - p.window_left);
+      }
+      if (lse == -INFINITY) hi = 0;  // no such row, or one that saw no key
+      const bool masked = __any_sync(kAll, lo > 0 || hi < kCols);
+      pos += p.tile_tokens;
+      left -= p.tile_tokens;
+      lse_at += (long long)p.tile_tokens * p.hqo;
+      lse = -INFINITY;
+      if (n + 1 < n_end && left > 0) lse = __ldg(lse_at);
+      alive = alive && __all_sync(kAll, mbar_wait(&sm.s_full[b], (n / kSBufs) & 1, pv.err, &sm.abort));
       if (alive) {
         tc::fence_after_sync();
-        const uint32_t t_s = lane_base + kColS + uint32_t(b * kCols);
-        const int tok = w.t0 + qt * p.tile_tokens;  // first token of the tile
-        // column c belongs to token tok + c / g; key sees tokens from key - diag to key - diag + window
-        int lo = 0, hi = kCols;
-        if (causal) {
-          lo = min(kCols, max(0, (key - diag - tok)) * p.group);
-          if (kWin) hi = int(max(0ll, min((long long)p.tile_tokens, (long long)key - diag - tok + p.window_left + 1))) * p.group;
-          if (kWin && hi == p.tile_tokens * p.group) hi = kCols;
-        }
-        const uint4 dead = *reinterpret_cast<const uint4*>(sm.dead[ring]);
-        const bool masked = __any_sync(kAll, lo > 0 || hi < kCols) || (dead.x | dead.y | dead.z | dead.w) != 0u;
-        float2 acc[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = make_float2(0.f, 0.f);
-        uint32_t s[2][kChunk];
-        load_scores(t_s, s[0]);
-#pragma unroll
-        for (int c = 0; c < kCols / kChunk; ++c) {
-          wait_scores(s[c & 1]);
-          if (c + 1 < kCols / kChunk) {
-            load_scores(t_s + kChunk * (c + 1), s[(c + 1) & 1]);
-          } else {
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.s_empty[b]);
-          }
-          const float* nl = sm.nl[ring] + kChunk * c;
-          const uint32_t word = c < 2 ? dead.x : c < 4 ? dead.y : c < 6 ? dead.z : dead.w;
-          if (masked)
-            add_chunk<true, kCap>(s[c & 1], nl, lo - kChunk * c, hi - kChunk * c, word >> (kChunk * (c & 1)), p, acc);
-          else
-            add_chunk<false, kCap>(s[c & 1], nl, 0, 0, 0u, p, acc);
-        }
-        const float2 a = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
-        sum += a.x + a.y;
+        const uint32_t t_s = t_lane + uint32_t(b * kKeys);
+        if (masked)
+          add_tile<true, kCap>(t_s, nl, lo, hi, p, &sm.s_empty[b], acc);
+        else
+          add_tile<false, kCap>(t_s, nl, 0, kCols, p, &sm.s_empty[b], acc);
       }
     }
-    if (!alive) out = nullptr;  // the error is recorded; the barriers and counts below still go their way
-    if (w.q0 == 0 && w.q1 == w.cost) {
-      if (out != nullptr) *out = old + sum;
-      continue;
+    // 64 column sums in each of 32 lanes -> two in each: at every step a lane keeps one half of its columns
+    // and gives the other to its partner
+    float* v = reinterpret_cast<float*>(acc);
+#pragma unroll
+    for (int m = 0; m < 5; ++m) {
+      const int half = kCols >> (m + 1);
+      const bool up = (lane >> (4 - m)) & 1;
+#pragma unroll
+      for (int k = 0; k < half; ++k) {
+        const float give = up ? v[k] : v[k + half], keep = up ? v[k + half] : v[k];
+        v[k] = keep + __shfl_xor_sync(kAll, give, 16 >> m);
+      }
     }
-    // a cut item: leave this piece, the last of its CTAs adds all of them in line order
-    const int start = w.pos - w.q0;
-    const int c1 = int(((long long)(start + 1) * ctas - 1) / line), c2 = int(((long long)(start + w.cost) * ctas - 1) / line);
-    p.part[(size_t(blockIdx.x) * 2 + (w.q0 == 0 ? 1 : 0)) * kKeys + row] = sum;
-    __threadfence();
-    named_bar_sync(1, 256);
-    if (threadIdx.x == 0) sm.last = atomicAdd(p.part_count + c1, 1u) == unsigned(c2 - c1);
-    named_bar_sync(1, 256);
-    if (sm.last) {
+    // lane l now holds columns 2 l and 2 l + 1; the four groups of rows add theirs in turn
+    named_bar_sync(1, kSumThreads);  // the last item's sums are not read any more
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+      if ((warp & 3) == k) {
+        float2* at = reinterpret_cast<float2*>(sm.red + col0) + lane;
+        *at = k == 0 ? make_float2(v[0], v[1]) : __fadd2_rn(*at, make_float2(v[0], v[1]));
+      }
+      named_bar_sync(1, kSumThreads);
+    }
+    if (threadIdx.x >= kKeys) continue;
+    float sum = sm.red[threadIdx.x];
+    if (!g.whole) {
+      // a cut item: leave this piece, the last of its CTAs adds all of them in line order
+      p.part[size_t(g.piece) * kKeys + threadIdx.x] = sum;
       __threadfence();
-      float total = 0.f;
-      for (int c = c1; c <= c2; ++c) total += __ldcg(p.part + (size_t(c) * 2 + (c == c1 ? 1 : 0)) * kKeys + row);
-      if (out != nullptr) *out = old + total;
-      if (threadIdx.x == 0) p.part_count[c1] = 0;
+      named_bar_sync(2, kKeys);
+      if (threadIdx.x == 0) sm.last = atomicAdd(p.part_count + g.c1, 1u) == unsigned(g.c2 - g.c1);
+      named_bar_sync(2, kKeys);
+      if (!sm.last) continue;
+      __threadfence();
+      sum = 0.f;
+      for (int c = g.c1; c <= g.c2; ++c)
+        sum += __ldcg(p.part + (size_t(c) * 2 + (c == g.c1 ? 1 : 0)) * kKeys + threadIdx.x);
+      if (threadIdx.x == 0) p.part_count[g.c1] = 0;
+    }
+    const int key = g.key0 + int(threadIdx.x);
+    int page, slot;
+    // after a wait that gave up (the error is recorded) nothing is written
+    if (alive && key < g.lkv && locate(pv, g.kv0, key, page, slot)) {
+      float* out = p.weights + weight_offset(pv, page, slot, g.head);
+      *out = (key >= g.first_new || p.decay == 0.f ? 0.f : p.decay * *out) + sum;
     }
   }
 }
@@ -455,31 +471,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   TcSmem& sm = *reinterpret_cast<TcSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    mbar_init(&sm.k_full, 8);
-    mbar_init(&sm.k_empty, 1);
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(&sm.k_full[i], kLoadThreads);
+      mbar_init(&sm.k_empty[i], 1);
+    }
     for (int i = 0; i < kQStages; ++i) {
-      mbar_init(&sm.q_full[i], 33);  // the copy's issuer and the 32 writers of the -lse rows
+      mbar_init(&sm.q_full[i], 1);
       mbar_init(&sm.q_empty[i], 1);
     }
-    for (int i = 0; i < kRing; ++i) mbar_init(&sm.l_full[i], 1);
     for (int i = 0; i < kSBufs; ++i) {
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.s_empty[i], 4);
+      mbar_init(&sm.s_empty[i], kSumThreads / 32);
     }
     sm.abort = 0;
     fence_mbar_init();
   }
-  // rows of the Q stages that no copy fills, the -lse rows' zeros, the ones
-  const int first = p.tile_tokens * p.group < kCols ? 0 : int(offsetof(TcSmem, l) / 16);
-  for (int i = first + threadIdx.x; i < int(offsetof(TcSmem, ones) / 16); i += kTcThreads)
-    reinterpret_cast<uint4*>(&sm)[i] = make_uint4(0, 0, 0, 0);
-  for (int i = threadIdx.x; i < kQHalfBytes / 16; i += kTcThreads) {
-    const int r = i >> 3, piece = (i & 7) ^ (r & 7);
-    reinterpret_cast<uint4*>(sm.ones)[i] = piece == 0 ? make_uint4(0x3f803f80u, 0x00003f80u, 0, 0) : make_uint4(0, 0, 0, 0);
+  if (p.tile_tokens * p.group < kRows) {  // rows of the Q stages that no copy fills
+    for (int i = threadIdx.x; i < int(sizeof(sm.q) / 16); i += kTcThreads)
+      reinterpret_cast<uint4*>(sm.q[0])[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
   }
-  fence_proxy_async_smem();
-  if (warp == 16 && lane == 0) tc::tma_prefetch_desc(&tm_q);
-  if (warp == 17) {
+  if (warp == 18 && lane == 0) tc::tma_prefetch_desc(&tm_q);
+  if (warp == 19) {
     tc::tmem_alloc(&sm.tmem_base, kTmemCols);
     tc::tmem_relinquish();
   }
@@ -497,23 +510,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   } else if (int(blockIdx.x) < ctas) {
     Walk w;
     w.init(p, causal, batch, int((long long)line * blockIdx.x / ctas), int((long long)line * (blockIdx.x + 1) / ctas));
-    if (warp < 8) {
-      tc::regs_decrease<kSumRegs>();
-      sum_weights<kWin, kCap>(p, sm, w, causal, tmem, line, ctas);
-    } else if (warp < 16) {
-      tc::regs_increase<kLoadRegs>();
-      load_keys<kFp8>(p, sm, w, causal, tmem);
+    if (warp < 16) {
+      if (threadIdx.x == 0) {
+        sm.walk = w;
+        w.publish(p, sm.seg[0], line, ctas);
+      }
+      named_bar_sync(1, kSumThreads);
+      tc::regs_increase<kSumRegs>();
+      sum_weights<kWin, kCap>(p, sm, causal, tmem, line, ctas);
     } else {
       tc::regs_decrease<kControlRegs>();
-      if (warp == 16)
-        load_queries<kCap>(p, sm, w, causal, &tm_q);
-      else if (warp == 17)
-        issue<kCap>(p, sm, w, causal, tmem);
+      if (warp < 18)
+        load_keys<kFp8>(p, sm, w, causal);
+      else if (warp == 18 && lane == 0)
+        load_queries(p, sm, w, causal, &tm_q);
+      else if (warp == 19)
+        issue(p, sm, w, causal, tmem);
     }
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 17) {
+  if (warp == 19) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kTmemCols);
   }
@@ -526,6 +543,7 @@ int launch_weights_tc(const WeightsParams& p, int total_q, bool fp8, int num_sms
   if (!make_query_map(&tq, p.q, p.hqo, total_q, p.group, p.tile_tokens)) return FI_ERR_INVALID_ARG;
   constexpr size_t smem = sizeof(TcSmem) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory exceeds the per-CTA limit");
+  static_assert(kSBufs * kKeys <= int(kTmemCols) && kKeys == 4 * kCols, "score buffers, columns of the summing warps");
   using Kernel = void (*)(const WeightsParams, const CUtensorMap);
   static const Kernel kernels[8] = {
       weights_tc_kernel<false, false, false>, weights_tc_kernel<false, false, true>, weights_tc_kernel<false, true, false>,
