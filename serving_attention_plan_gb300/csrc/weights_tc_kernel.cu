@@ -121,21 +121,12 @@ struct Walk {
   }
   // Thread 0 of the summing warps: the segment at hand, written down.
   template <typename S>
-  __device__ void publish(const WeightsParams& p, S& s, int line, int ctas) const {
-    const int tok = t0 + q0 * p.tile_tokens, start = pos - q0;
+  __device__ void publish(const WeightsParams& p, S& s) const {
     s.tiles = more() ? q1 - q0 : 0;
     if (!more()) return;
+    const int tok = t0 + q0 * p.tile_tokens;
     s.pos = g.lkv - g.lq + tok - kt * kKeys;
     s.tokens = tokens - q0 * p.tile_tokens;
-    s.whole = q0 == 0 && q1 == cost;
-    s.piece = int(blockIdx.x) * 2 + (q0 == 0 ? 1 : 0);
-    s.c1 = int(((long long)(start + 1) * ctas - 1) / line);
-    s.c2 = int(((long long)(start + cost) * ctas - 1) / line);
-    s.key0 = kt * kKeys;
-    s.head = head;
-    s.kv0 = g.kv0;
-    s.lkv = g.lkv;
-    s.first_new = p.new_keys ? g.lkv - g.lq : g.lkv;
     s.lse = (long long)(g.q0 + tok) * p.hqo + head * p.group;
   }
   __device__ __forceinline__ bool more() const { return pos < end; }
@@ -163,9 +154,6 @@ struct Segment {
   int tiles;       // 0: no more
   int pos;         // key position of the first tile's first token, relative to the item's first key
   int tokens;      // query tokens from that one on
-  int whole;       // 1: all of the item's Q tiles
-  int piece, c1, c2;  // cut items: this CTA's slot, the first and last CTA that have a piece
-  int key0, head, kv0, lkv, first_new;
   long long lse;   // offset of the first token's first head
 };
 
@@ -173,9 +161,10 @@ struct TcSmem {
   uint8_t k[kKStages][2 * kKHalfBytes];
   uint8_t q[kQStages][2 * kQHalfBytes];
   Walk walk;         // of the summing warps, one ahead of them
-  Segment seg[3];    // what they know of a segment: the one at work, the next, and the last one's write-out
-  float red[kKeys];  // the item's sums, added up over the four groups of 32 rows
+  Segment seg[2];    // what they know of a segment: the one at work and the next
+  float red[2][kKeys];  // a segment's sums, added up over the four groups of 32 rows
   uint64_t k_full[kKStages], k_empty[kKStages], q_full[kQStages], q_empty[kQStages], s_full[kSBufs], s_empty[kSBufs];
+  uint64_t red_full[2], red_empty[2];
   uint32_t tmem_base;
   int abort;
   int last;
@@ -189,60 +178,129 @@ __device__ __forceinline__ uint2 widen4(uint32_t codes) {
   return make_uint2(f2_to_bf16x2(a.x, a.y), f2_to_bf16x2(b.x, b.y));
 }
 
-template <bool kFp8>
-__device__ void load_keys(const WeightsParams& p, TcSmem& sm, Walk w, bool causal) {
+// Writes a finished segment's sums out (the key loader's threads, four keys each).  Of a cut item each
+// piece goes to its slot, and the last of its CTAs to come adds all of them in line order.  After a wait
+// that gave up (the error is recorded) nothing is written, but the barriers and counts go their way.
+__device__ void write_sums(const WeightsParams& p, TcSmem& sm, const Walk& w, int n, int line, int ctas, bool& alive) {
   const PageView& pv = p.pv;
-  const int tid = threadIdx.x - kSumThreads;     // 0..63
-  constexpr int kLanes = kFp8 ? 8 : 16;          // threads of a row, 16 bytes each
-  constexpr int kRowsPass = kLoadThreads / kLanes;
-  constexpr int kBatch = kFp8 ? 4 : 8;
-  const int ch = tid % kLanes, row0 = tid / kLanes;
+  const int tid = threadIdx.x - kSumThreads;
+  constexpr int kMine = kKeys / kLoadThreads;
+  float sum[kMine], old[kMine];
+  float* out[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int key = w.kt * kKeys + tid + i * kLoadThreads;
+    int page, slot;
+    out[i] = nullptr;
+    old[i] = 0.f;
+    if (key < w.g.lkv && locate(pv, w.g.kv0, key, page, slot)) {
+      out[i] = p.weights + weight_offset(pv, page, slot, w.head);
+      if (!(p.new_keys && key >= w.g.lkv - w.g.lq) && p.decay != 0.f) old[i] = p.decay * __ldcg(out[i]);
+    }
+  }
+  alive = alive && __all_sync(kAll, mbar_wait(&sm.red_full[n & 1], (n >> 1) & 1, pv.err, &sm.abort));
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) sum[i] = sm.red[n & 1][tid + i * kLoadThreads];
+  mbar_arrive(&sm.red_empty[n & 1]);
+  if (w.q0 != 0 || w.q1 != w.cost) {
+    const int start = w.pos - w.q0;
+    const int c1 = int(((long long)(start + 1) * ctas - 1) / line), c2 = int(((long long)(start + w.cost) * ctas - 1) / line);
+    float* piece = p.part + (size_t(blockIdx.x) * 2 + (w.q0 == 0 ? 1 : 0)) * kKeys + tid;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) piece[i * kLoadThreads] = sum[i];
+    __threadfence();
+    named_bar_sync(2, kLoadThreads);
+    if (tid == 0) sm.last = atomicAdd(p.part_count + c1, 1u) == unsigned(c2 - c1);
+    named_bar_sync(2, kLoadThreads);
+    if (!sm.last) return;
+    __threadfence();
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) sum[i] = 0.f;
+    for (int c = c1; c <= c2; ++c) {
+      const float* at = p.part + (size_t(c) * 2 + (c == c1 ? 1 : 0)) * kKeys + tid;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) sum[i] += __ldcg(at + i * kLoadThreads);
+    }
+    if (tid == 0) p.part_count[c1] = 0;
+  }
+  if (!alive) return;
+#pragma unroll
+  for (int i = 0; i < kMine; ++i)
+    if (out[i] != nullptr) *out[i] = old[i] + sum[i];
+}
+
+template <bool kFp8>
+__device__ void load_keys(const WeightsParams& p, TcSmem& sm, Walk w, bool causal, int line, int ctas) {
+  const PageView& pv = p.pv;
+  const int lane = threadIdx.x & 31;
+  constexpr int kLanes = kFp8 ? 8 : 16;           // lanes of a row, 16 bytes each
+  constexpr int kRowsPass = 32 / kLanes;          // rows of a warp's pass
+  constexpr int kMine = kKeys / kLoadThreads;     // rows a lane looks up
+  const int first = (threadIdx.x - kSumThreads) / 32 * (kKeys / 2);  // this warp's half of the rows
+  const int ch = lane % kLanes, sub = lane / kLanes;
   const uint8_t* pages = static_cast<const uint8_t*>(p.k_pages);
+  Walk done = w;  // the segment whose sums are written out next
+  int written = 0;
+  bool alive = true;
   for (int n = 0; w.more(); w.next(p, causal), ++n) {
     const int ks = n % kKStages;
-    bool ok = true;
-    if (n >= kKStages) ok = mbar_wait(&sm.k_empty[ks], (n / kKStages - 1) & 1, pv.err, &sm.abort);
-    if (!__all_sync(kAll, ok)) return;
+    if (n >= kKStages)
+      alive = alive && __all_sync(kAll, mbar_wait(&sm.k_empty[ks], (n / kKStages - 1) & 1, pv.err, &sm.abort));
     auto place = [&](int row, int c16) {  // 16-byte piece c16 (0..15) of a bf16 row
       return sm.k[ks] + (c16 >> 3) * kKHalfBytes + row * 128 + (((c16 & 7) ^ (row & 7)) << 4);
     };
-    for (int i0 = row0; i0 < kKeys; i0 += kBatch * kRowsPass) {
-      const uint8_t* src[kBatch];
+    if (alive) {
+      // each lane looks up four rows (one memory latency for all 256), the passes below fetch them by shuffle
+      int at[kMine];  // row of the page pool (128 elements each), -1: no key
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int key = w.kt * kKeys + i0 + i * kRowsPass;
+      for (int i = 0; i < kMine; ++i) {
+        const int key = w.kt * kKeys + first + lane + 32 * i;
         int page, slot;
-        src[i] = nullptr;
+        at[i] = -1;
         if (key < w.g.lkv && locate(pv, w.g.kv0, key, page, slot))
-          src[i] = pages + kv_offset(pv, page, slot, w.head) * (kFp8 ? 1 : 2) + 16 * ch;
+          at[i] = int(kv_offset(pv, page, slot, w.head) / kHeadDim);
       }
-      if constexpr (kFp8) {
-        uint4 v[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-          v[i] = src[i] ? __ldg(reinterpret_cast<const uint4*>(src[i])) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < kMine; ++i) {
+        constexpr int kBatch = kFp8 ? 8 : 16;  // passes of 32 rows: 8 with e4m3 codes, 16 without
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int row = i0 + i * kRowsPass;
-          const uint2 a = widen4(v[i].x), b = widen4(v[i].y), c = widen4(v[i].z), d = widen4(v[i].w);
-          *reinterpret_cast<uint4*>(place(row, 2 * ch)) = make_uint4(a.x, a.y, b.x, b.y);
-          *reinterpret_cast<uint4*>(place(row, 2 * ch + 1)) = make_uint4(c.x, c.y, d.x, d.y);
-        }
-      } else {
+        for (int k0 = 0; k0 < kBatch; k0 += 4) {
+          uint4 v[4];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int row = i0 + i * kRowsPass;
-          if (src[i])
-            cp_async_16(place(row, ch), src[i]);
-          else
-            *reinterpret_cast<uint4*>(place(row, ch)) = make_uint4(0, 0, 0, 0);
+          for (int k = 0; k < 4; ++k) {
+            const int r = (k0 + k) * kRowsPass + sub, row = first + 32 * i + r;
+            const int src = __shfl_sync(kAll, at[i], r);
+            const uint8_t* from = pages + (long long)src * (kHeadDim * (kFp8 ? 1 : 2)) + 16 * ch;
+            if constexpr (kFp8) {
+              v[k] = src >= 0 ? __ldg(reinterpret_cast<const uint4*>(from)) : make_uint4(0, 0, 0, 0);
+            } else {
+              if (src >= 0)
+                cp_async_16(place(row, ch), from);
+              else
+                *reinterpret_cast<uint4*>(place(row, ch)) = make_uint4(0, 0, 0, 0);
+            }
+          }
+          if constexpr (kFp8) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int row = first + 32 * i + (k0 + k) * kRowsPass + sub;
+              const uint2 a = widen4(v[k].x), b = widen4(v[k].y), c = widen4(v[k].z), d = widen4(v[k].w);
+              *reinterpret_cast<uint4*>(place(row, 2 * ch)) = make_uint4(a.x, a.y, b.x, b.y);
+              *reinterpret_cast<uint4*>(place(row, 2 * ch + 1)) = make_uint4(c.x, c.y, d.x, d.y);
+            }
+          }
         }
       }
     }
     cp_async_wait_all();
     fence_proxy_async_smem();
-    mbar_arrive(&sm.k_full[ks]);
+    if (alive) mbar_arrive(&sm.k_full[ks]);
+    if (n >= kKStages) {  // k_empty says that segment n - 2's products are done: its sums are near
+      write_sums(p, sm, done, written++, line, ctas, alive);
+      done.next(p, causal);
+    }
   }
+  for (; done.more(); done.next(p, causal)) write_sums(p, sm, done, written++, line, ctas, alive);
 }
 
 __device__ void load_queries(const WeightsParams& p, TcSmem& sm, Walk w, bool causal, const CUtensorMap* tm_q) {
@@ -363,7 +421,7 @@ __device__ __forceinline__ void add_tile(uint32_t t_s, float nl, int lo, int hi,
 }
 
 template <bool kWin, bool kCap>
-__device__ void sum_weights(const WeightsParams& p, TcSmem& sm, bool causal, uint32_t tmem, int line, int ctas) {
+__device__ void sum_weights(const WeightsParams& p, TcSmem& sm, bool causal, uint32_t tmem) {
   const PageView& pv = p.pv;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = threadIdx.x & (kRows - 1);   // query row of the tile: TMEM lane
@@ -371,11 +429,12 @@ __device__ void sum_weights(const WeightsParams& p, TcSmem& sm, bool causal, uin
   const uint32_t t_lane = tmem + (uint32_t((warp & 3) * 32) << 16) + uint32_t(col0);
   int n = 0;
   bool alive = true;
-  for (int i = 0; sm.seg[i].tiles > 0; i = i == 2 ? 0 : i + 1) {
-    const Segment& g = sm.seg[i];
+  for (int i = 0; sm.seg[i & 1].tiles > 0; ++i) {
+    const Segment g = sm.seg[i & 1];
+    named_bar_sync(1, kSumThreads);  // all have read it, and what the one after it overwrites
     if (threadIdx.x == 0) {  // the next segment; its readers come to it after the barriers below
       sm.walk.next(p, causal);
-      sm.walk.publish(p, sm.seg[i == 2 ? 0 : i + 1], line, ctas);
+      sm.walk.publish(p, sm.seg[(i + 1) & 1]);
     }
     __syncwarp();
     float2 acc[kCols / 2];
@@ -429,46 +488,26 @@ __device__ void sum_weights(const WeightsParams& p, TcSmem& sm, bool causal, uin
       }
     }
     // lane l now holds columns 2 l and 2 l + 1; the four groups of rows add theirs in turn
-    named_bar_sync(1, kSumThreads);  // the last item's sums are not read any more
+    if (i >= 2) alive = alive && __all_sync(kAll, mbar_wait(&sm.red_empty[i & 1], ((i >> 1) - 1) & 1, pv.err, &sm.abort));
 #pragma unroll 1
     for (int k = 0; k < 4; ++k) {
       if ((warp & 3) == k) {
-        float2* at = reinterpret_cast<float2*>(sm.red + col0) + lane;
+        float2* at = reinterpret_cast<float2*>(sm.red[i & 1] + col0) + lane;
         *at = k == 0 ? make_float2(v[0], v[1]) : __fadd2_rn(*at, make_float2(v[0], v[1]));
       }
       named_bar_sync(1, kSumThreads);
     }
-    if (threadIdx.x >= kKeys) continue;
-    float sum = sm.red[threadIdx.x];
-    if (!g.whole) {
-      // a cut item: leave this piece, the last of its CTAs adds all of them in line order
-      p.part[size_t(g.piece) * kKeys + threadIdx.x] = sum;
-      __threadfence();
-      named_bar_sync(2, kKeys);
-      if (threadIdx.x == 0) sm.last = atomicAdd(p.part_count + g.c1, 1u) == unsigned(g.c2 - g.c1);
-      named_bar_sync(2, kKeys);
-      if (!sm.last) continue;
-      __threadfence();
-      sum = 0.f;
-      for (int c = g.c1; c <= g.c2; ++c)
-        sum += __ldcg(p.part + (size_t(c) * 2 + (c == g.c1 ? 1 : 0)) * kKeys + threadIdx.x);
-      if (threadIdx.x == 0) p.part_count[g.c1] = 0;
-    }
-    const int key = g.key0 + int(threadIdx.x);
-    int page, slot;
-    // after a wait that gave up (the error is recorded) nothing is written
-    if (alive && key < g.lkv && locate(pv, g.kv0, key, page, slot)) {
-      float* out = p.weights + weight_offset(pv, page, slot, g.head);
-      *out = (key >= g.first_new || p.decay == 0.f ? 0.f : p.decay * *out) + sum;
-    }
+    if (alive && threadIdx.x == 0) mbar_arrive(&sm.red_full[i & 1]);
   }
 }
 
 template <bool kFp8, bool kWin, bool kCap>
 __global__ void __launch_bounds__(kTcThreads, 1)
     weights_tc_kernel(const __grid_constant__ WeightsParams p, const __grid_constant__ CUtensorMap tm_q) {
-  extern __shared__ unsigned char smem_raw[];
-  TcSmem& sm = *reinterpret_cast<TcSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // the kernel has no static shared memory, so this starts at the CTA's first (1024-byte aligned) address;
+  // the check below holds it to that, the swizzled tiles need it
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  TcSmem& sm = *reinterpret_cast<TcSmem*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKStages; ++i) {
@@ -482,6 +521,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (int i = 0; i < kSBufs; ++i) {
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.s_empty[i], kSumThreads / 32);
+      mbar_init(&sm.red_full[i], 1);
+      mbar_init(&sm.red_empty[i], kLoadThreads);
     }
     sm.abort = 0;
     fence_mbar_init();
@@ -505,7 +546,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const bool causal = __ldg(p.pv.header + H_CAUSAL) != 0;
   const int line = __ldg(&p.pv.geo[batch].work0);
   const int ctas = min(int(gridDim.x), line);
-  if ((tmem & 0xFFFFu) + kTmemCols > 512u) {
+  if ((tmem & 0xFFFFu) + kTmemCols > 512u || (smem_u32(smem_raw) & 1023u) != 0) {
     if (threadIdx.x == 0) atomicOr(p.pv.err, FI_DEVERR_TMEM);
   } else if (int(blockIdx.x) < ctas) {
     Walk w;
@@ -513,15 +554,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (warp < 16) {
       if (threadIdx.x == 0) {
         sm.walk = w;
-        w.publish(p, sm.seg[0], line, ctas);
+        w.publish(p, sm.seg[0]);
       }
       named_bar_sync(1, kSumThreads);
       tc::regs_increase<kSumRegs>();
-      sum_weights<kWin, kCap>(p, sm, causal, tmem, line, ctas);
+      sum_weights<kWin, kCap>(p, sm, causal, tmem);
     } else {
       tc::regs_decrease<kControlRegs>();
       if (warp < 18)
-        load_keys<kFp8>(p, sm, w, causal);
+        load_keys<kFp8>(p, sm, w, causal, line, ctas);
       else if (warp == 18 && lane == 0)
         load_queries(p, sm, w, causal, &tm_q);
       else if (warp == 19)
@@ -541,7 +582,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 int launch_weights_tc(const WeightsParams& p, int total_q, bool fp8, int num_sms, cudaStream_t stream) {
   CUtensorMap tq;
   if (!make_query_map(&tq, p.q, p.hqo, total_q, p.group, p.tile_tokens)) return FI_ERR_INVALID_ARG;
-  constexpr size_t smem = sizeof(TcSmem) + 1024;
+  constexpr size_t smem = sizeof(TcSmem);
   static_assert(smem <= 227 * 1024, "shared memory exceeds the per-CTA limit");
   static_assert(kSBufs * kKeys <= int(kTmemCols) && kKeys == 4 * kCols, "score buffers, columns of the summing warps");
   using Kernel = void (*)(const WeightsParams, const CUtensorMap);
