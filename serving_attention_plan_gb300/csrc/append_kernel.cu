@@ -28,8 +28,8 @@ namespace {
 
 constexpr int kAppendThreads = 256;
 constexpr int kRowLanes = 8;
-constexpr int kRowsPass = kAppendThreads / kRowLanes;  // normed rows of a pass
-constexpr int kInFlight = 2;                           // passes whose loads are in flight
+constexpr int kRowsPass = kAppendThreads / kRowLanes;  // rows of a pass; the next pass is in flight meanwhile
+constexpr int kAppendCtasPerSm = 3;
 
 __device__ __forceinline__ void unpack8(uint4 w, float2 (&x)[4]) {
   x[0] = bf16x2_to_f2(w.x);
@@ -63,7 +63,7 @@ __device__ __forceinline__ void put8(void* pages, long long off, const float2 (&
 // A step is kTok tokens: four for long batches (the sync and the search for the request are paid once for four
 // tokens), one for decode steps, where tokens are few and each CTA should take one.
 template <int kTok, bool kFp8>
-__global__ void __launch_bounds__(kAppendThreads, 3) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, kAppendCtasPerSm) append_kernel(const __grid_constant__ AppendParams p) {
   // cos and sin of a token's frequencies: piece k of a split half holds frequencies 8 k .. 8 k + 7, its first
   // four at [k], the others at [8 + k], so the lanes' 16-byte reads fall into different banks; interleaved
   // pairs are in order, piece k holds [k]
@@ -130,114 +130,110 @@ __global__ void __launch_bounds__(kAppendThreads, 3) append_kernel(const __grid_
   };
   if (warp < kTok) prepare(s0, 0);
 
-  const int normed = p.hqo + pv.hkv;  // q and k heads
+  const int heads = p.hqo + 2 * pv.hkv;  // rows of a token: q, k, v
+  uint4 next[2];
+  int next_t = 0, next_h = -1;  // row of the step that `next` holds, -1: none
+  auto load = [&](int step, int row) {
+    next_h = -1;
+    const int base = step * kTok;
+    if (step >= s1 || row >= min(kTok, total - base) * heads) return;
+    next_t = kTok == 1 ? 0 : int(__umulhi(unsigned(row), p.heads_inv));
+    next_h = row - next_t * heads;
+    const long long tok = base + next_t;
+    const __nv_bfloat16* at;
+    if (next_h < p.hqo)
+      at = static_cast<const __nv_bfloat16*>(p.q) + tok * p.q_stride + next_h * kHeadDim;
+    else if (next_h < p.hqo + pv.hkv)
+      at = static_cast<const __nv_bfloat16*>(p.k) + tok * p.k_stride + (next_h - p.hqo) * kHeadDim;
+    else
+      at = static_cast<const __nv_bfloat16*>(p.v) + tok * p.v_stride + (next_h - p.hqo - pv.hkv) * kHeadDim;
+    next[0] = __ldcs(reinterpret_cast<const uint4*>(at) + pa);
+    next[1] = __ldcs(reinterpret_cast<const uint4*>(at) + pb);
+  };
+  load(s0, sub);
   int par = 0;
   for (int step = s0; step < s1; ++step, par ^= 1) {
-    const int base = step * kTok, tokens = min(kTok, total - base);
-    const int rows = tokens * normed;
-    uint4 raw[kInFlight][2];
-    int tt[kInFlight], hh[kInFlight];
-    auto load = [&](int row0) {
-#pragma unroll
-      for (int i = 0; i < kInFlight; ++i) {
-        const int row = row0 + i * kRowsPass;
-        raw[i][0] = raw[i][1] = make_uint4(0, 0, 0, 0);
-        tt[i] = kTok == 1 ? 0 : int(__umulhi(unsigned(row), p.normed_inv));
-        hh[i] = row - tt[i] * normed;
-        if (row < rows) {
-          const long long tok = base + tt[i];
-          const uint4* at = reinterpret_cast<const uint4*>(
-              hh[i] < p.hqo ? static_cast<const __nv_bfloat16*>(p.q) + tok * p.q_stride + hh[i] * kHeadDim
-                            : static_cast<const __nv_bfloat16*>(p.k) + tok * p.k_stride + (hh[i] - p.hqo) * kHeadDim);
-          raw[i][0] = __ldcs(at + pa);
-          raw[i][1] = __ldcs(at + pb);
-        }
-      }
-    };
-    load(sub);
+    const int base = step * kTok, rows = min(kTok, total - base) * heads;
     __syncthreads();
     if (warp < kTok) prepare(step + 1, par ^ 1);
-    for (int row0 = sub; row0 - sub < rows; row0 += kInFlight * kRowsPass) {  // whole warps: the sums shuffle
-      if (row0 != sub) load(row0);
-#pragma unroll
-      for (int i = 0; i < kInFlight; ++i) {
-        if (row0 - sub + i * kRowsPass >= rows) break;
-        const bool on = row0 + i * kRowsPass < rows, is_q = hh[i] < p.hqo;
-        const int t = on ? tt[i] : 0;
-        float2 a[4], b[4];
-        unpack8(raw[i][0], a);
-        unpack8(raw[i][1], b);
-        if (is_q ? p.q_weight != nullptr : p.k_weight != nullptr) {
-          float2 w[4], s2 = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s2 = __ffma2_rn(b[e], b[e], __ffma2_rn(a[e], a[e], s2));
-          float ss = s2.x + s2.y;
-          // the lanes of a row agree on the branch
-          const unsigned mates = 0xffu << (lane & 24);
-#pragma unroll
-          for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(mates, ss, o);
-          const float inv = rsqrtf(fmaf(ss, 1.f / kHeadDim, p.eps));
-          const float2 i2 = make_float2(inv, inv);
-          unpack8(is_q ? wq[0] : wk[0], w);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) a[e] = __fmul2_rn(__fmul2_rn(a[e], i2), w[e]);
-          unpack8(is_q ? wq[1] : wk[1], w);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) b[e] = __fmul2_rn(__fmul2_rn(b[e], i2), w[e]);
+    for (int row = sub; row - sub < rows; row += kRowsPass) {
+      const uint4 raw[2] = {next[0], next[1]};
+      const int t = next_t, h = next_h;
+      if (row - sub + kRowsPass < rows)
+        load(step, row + kRowsPass);
+      else
+        load(step + 1, sub);
+      if (h < 0) continue;
+      float2 a[4], b[4];
+      unpack8(raw[0], a);
+      unpack8(raw[1], b);
+      if (h >= p.hqo + pv.hkv) {  // v: as it is
+        if (place[par][t] < 0) continue;
+        const long long off = place[par][t] + (h - p.hqo - pv.hkv) * pv.head_stride;
+        if constexpr (kFp8) {
+          put8<true>(p.v_pages, off + 8 * pa, a, p.v_inv_scale);
+          put8<true>(p.v_pages, off + 8 * pb, b, p.v_inv_scale);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.v_pages) + off);
+          dst[pa] = raw[0];
+          dst[pb] = raw[1];
         }
-        if (p.interleaved) {
-          auto turn = [&](float2 (&x)[4], int piece) {
-            if (piece >= 2 * hp) return;
-            const float4 c = cosines[par][t][piece], s = sines[par][t][piece];
-            const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+        continue;
+      }
+      const bool is_q = h < p.hqo;
+      if (is_q ? p.q_weight != nullptr : p.k_weight != nullptr) {
+        float2 w[4], s2 = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              x[e] = make_float2(x[e].x * cc[e] - x[e].y * sn[e], x[e].x * sn[e] + x[e].y * cc[e]);
-          };
-          turn(a, pa);
-          turn(b, pb);
-        } else if (l < hp) {
+        for (int e = 0; e < 4; ++e) s2 = __ffma2_rn(b[e], b[e], __ffma2_rn(a[e], a[e], s2));
+        float ss = s2.x + s2.y;
+        // the lanes of a row agree on all branches
+        const unsigned mates = 0xffu << (lane & 24);
 #pragma unroll
-          for (int e2 = 0; e2 < 2; ++e2) {
-            const float4 c = cosines[par][t][8 * e2 + l], s = sines[par][t][8 * e2 + l];
-            const float2 cc[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)};
-            const float2 sn[2] = {make_float2(s.x, s.y), make_float2(s.z, s.w)};
+        for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(mates, ss, o);
+        const float inv = rsqrtf(fmaf(ss, 1.f / kHeadDim, p.eps));
+        const float2 i2 = make_float2(inv, inv);
+        unpack8(is_q ? wq[0] : wk[0], w);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float2 x = a[2 * e2 + e], y = b[2 * e2 + e];
-              const float2 ms = make_float2(-sn[e].x, -sn[e].y);
-              a[2 * e2 + e] = __ffma2_rn(y, ms, __fmul2_rn(x, cc[e]));
-              b[2 * e2 + e] = __ffma2_rn(x, sn[e], __fmul2_rn(y, cc[e]));
-            }
+        for (int e = 0; e < 4; ++e) a[e] = __fmul2_rn(__fmul2_rn(a[e], i2), w[e]);
+        unpack8(is_q ? wq[1] : wk[1], w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[e] = __fmul2_rn(__fmul2_rn(b[e], i2), w[e]);
+      }
+      if (p.interleaved) {
+        auto turn = [&](float2 (&x)[4], int piece) {
+          if (piece >= 2 * hp) return;
+          const float4 c = cosines[par][t][piece], s = sines[par][t][piece];
+          const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[e] = make_float2(x[e].x * cc[e] - x[e].y * sn[e], x[e].x * sn[e] + x[e].y * cc[e]);
+        };
+        turn(a, pa);
+        turn(b, pb);
+      } else if (l < hp) {
+#pragma unroll
+        for (int e2 = 0; e2 < 2; ++e2) {
+          const float4 c = cosines[par][t][8 * e2 + l], s = sines[par][t][8 * e2 + l];
+          const float2 cc[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)};
+          const float2 sn[2] = {make_float2(s.x, s.y), make_float2(s.z, s.w)};
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 x = a[2 * e2 + e], y = b[2 * e2 + e];
+            const float2 ms = make_float2(-sn[e].x, -sn[e].y);
+            a[2 * e2 + e] = __ffma2_rn(y, ms, __fmul2_rn(x, cc[e]));
+            b[2 * e2 + e] = __ffma2_rn(x, sn[e], __fmul2_rn(y, cc[e]));
           }
         }
-        if (!on) continue;
-        if (is_q) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.q_out) +
-                                                ((long long)(base + t) * p.hqo + hh[i]) * kHeadDim);
-          dst[pa] = pack8(a);
-          dst[pb] = pack8(b);
-        } else if (place[par][t] >= 0) {
-          const long long off = place[par][t] + (hh[i] - p.hqo) * pv.head_stride;
-          put8<kFp8>(p.k_pages, off + 8 * pa, a, p.k_inv_scale);
-          put8<kFp8>(p.k_pages, off + 8 * pb, b, p.k_inv_scale);
-        }
       }
-    }
-    // v: 16 lanes a row, one piece each
-    const int vrows = tokens * pv.hkv, vl = threadIdx.x & 15;
-    for (int row = threadIdx.x >> 4; row < vrows; row += kAppendThreads / 16) {
-      const int t = row / pv.hkv, h = row - t * pv.hkv;
-      const uint4 x = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.v) +
-                                                            (long long)(base + t) * p.v_stride + h * kHeadDim) + vl);
-      if (place[par][t] < 0) continue;
-      const long long off = place[par][t] + h * pv.head_stride + 8 * vl;
-      if constexpr (kFp8) {
-        float2 f[4];
-        unpack8(x, f);
-        put8<true>(p.v_pages, off, f, p.v_inv_scale);
-      } else {
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.v_pages) + off) = x;  // bits as they are
+      if (is_q) {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.q_out) +
+                                              ((long long)(base + t) * p.hqo + h) * kHeadDim);
+        dst[pa] = pack8(a);
+        dst[pb] = pack8(b);
+      } else if (place[par][t] >= 0) {
+        const long long off = place[par][t] + (h - p.hqo) * pv.head_stride;
+        put8<kFp8>(p.k_pages, off + 8 * pa, a, p.k_inv_scale);
+        put8<kFp8>(p.k_pages, off + 8 * pb, b, p.k_inv_scale);
       }
     }
   }
@@ -247,8 +243,9 @@ __global__ void __launch_bounds__(kAppendThreads, 3) append_kernel(const __grid_
 
 int launch_append(AppendParams p, int total_q, bool fp8, int num_sms, cudaStream_t stream) {
   const bool many = total_q >= 8 * num_sms;
-  const unsigned grid = unsigned(many ? std::min((total_q + 3) / 4, 3 * num_sms) : total_q);
-  p.normed_inv = unsigned(((1ull << 32) + unsigned(p.hqo + p.pv.hkv) - 1) / unsigned(p.hqo + p.pv.hkv));  // rows / heads, by a high product
+  const unsigned grid = unsigned(many ? std::min((total_q + 3) / 4, kAppendCtasPerSm * num_sms) : total_q);
+  const unsigned heads = unsigned(p.hqo + 2 * p.pv.hkv);
+  p.heads_inv = unsigned(((1ull << 32) + heads - 1) / heads);  // division by a high product: exact below 2^32 / heads
   cudaError_t e;
   if (many)
     e = fp8 ? launch_dependent(append_kernel<4, true>, grid, kAppendThreads, 0, 1, stream, p)

@@ -202,86 +202,180 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
 }
 
 // ---- compaction ----------------------------------------------------------------------------------
-// Row j of the first n slots receives row kept[j] >= j.  Steps go up in j, and within a step every
-// row is read before any is written: a write of step s lands at or below its last j, every later
-// step reads at or above that, so nothing is overwritten before it has been read, and the copy is
-// safe in place.  The bound is memory traffic: each moved row is read once and written once.  Rows
-// live in registers between the two halves of a step.  A cluster shares one (request, head, K or V) when there are few of them; its
-// barrier then orders the step's reads before its writes.
+// Row j of the first n slots receives row kept[j] >= j.  Steps go up in j, and the rows of a step are
+// written only when all rows up to that step have been read: a write of step s lands at or below its
+// last j, every later step reads at or above that, so nothing is overwritten before it has been read, and
+// the copy is safe in place, however far reads run ahead.  The bound is memory traffic: each moved row is
+// read once and written once, so reads run three steps (96 KB a CTA) ahead through shared memory, and the
+// positions and page ids of the steps behind those are fetched one and two steps earlier still.  (Read and
+// written step by step from registers, each step waited for four dependent loads: 310 us for 64 x 8
+// rows of 2048 keys, 52 % of the copy bandwidth.)  A cluster shares a task (request, head, K or V) when there are few
+// of them; its barrier then orders a step's reads before its writes.
 constexpr int kCmpThreads = 256;
-constexpr int kCmpVecs = 8;  // 16-byte pieces a thread carries
+constexpr int kCmpVecs = 8;    // 16-byte pieces of a thread and step
+constexpr int kCmpAhead = 3;   // steps in flight
+constexpr int kIdxRing = kCmpAhead + 2;
+
+struct CompactSmem {
+  uint4 data[kCmpAhead][kCmpVecs][kCmpThreads];
+  int2 idx[kIdxRing][kCmpThreads];  // (source, destination) row of the page pool; source -1: the row stays
+};
+
+// Checks entry j of a kept list of n entries; -1 for one that stays, is out of range or is behind the end.
+__device__ __forceinline__ int kept_source(const CompactParams& p, int j, int k, int prev, int lkv) {
+  if (k < j || k >= lkv || k <= prev) {
+    atomicOr(p.pv.err, FI_DEVERR_KEPT);
+    return -1;
+  }
+  return k == j ? -1 : k;
+}
+
+// The running weights of one (request, head): rows of four bytes, through registers.
+__device__ void compact_weights(const CompactParams& p, const Geo& g, const int32_t* kept, int head, unsigned nr,
+                                unsigned rank) {
+  const PageView& pv = p.pv;
+  const int n = p.budget, step = kCmpThreads * kCmpVecs;
+  for (int s0 = 0; s0 < n; s0 += int(nr) * step) {
+    const int j0 = s0 + int(rank) * step + threadIdx.x;
+    int src[kCmpVecs];
+    float v[kCmpVecs];
+#pragma unroll
+    for (int i = 0; i < kCmpVecs; ++i) {
+      const int j = j0 + i * kCmpThreads;
+      src[i] = j < n ? kept_source(p, j, __ldg(kept + j), j > 0 ? __ldg(kept + j - 1) : -1, g.lkv) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kCmpVecs; ++i) {
+      int page, slot;
+      if (src[i] >= 0 && locate(pv, g.kv0, src[i], page, slot))
+        v[i] = __ldcg(p.weights + weight_offset(pv, page, slot, head));
+      else
+        src[i] = -1;
+    }
+    if (nr > 1)
+      cluster_sync_all();
+    else
+      __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kCmpVecs; ++i) {
+      int page, slot;
+      if (src[i] >= 0 && locate(pv, g.kv0, j0 + i * kCmpThreads, page, slot))
+        p.weights[weight_offset(pv, page, slot, head)] = v[i];
+    }
+  }
+}
 
 template <bool kFp8>
-__global__ void __launch_bounds__(kCmpThreads) compact_kernel(const __grid_constant__ CompactParams p) {
+__global__ void __launch_bounds__(kCmpThreads, 2) compact_kernel(const __grid_constant__ CompactParams p) {
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  CompactSmem& sm = *reinterpret_cast<CompactSmem*>(smem_raw);
   wait_prior_grid();
   const PageView& pv = p.pv;
-  constexpr int kLanes = kFp8 ? 8 : 16;                         // threads of one row
-  constexpr int kRowsPass = kCmpThreads / kLanes;               // rows one piece of all threads covers
+  constexpr int kLanes = kFp8 ? 8 : 16;            // threads of one row
+  constexpr int kRowBytes = kFp8 ? kHeadDim : 2 * kHeadDim;
+  constexpr int kRowsPass = kCmpThreads / kLanes;  // rows one piece of all threads covers
   constexpr int kRowsStep = kRowsPass * kCmpVecs;
+  static_assert(kRowsStep <= kCmpThreads, "one thread looks a row up");
   const int batch = __ldg(pv.header + H_BATCH);
   const unsigned nr = cluster_size(), rank = cluster_rank();
   const int sub = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
-  const int tasks = batch * pv.hkv * 2;
+  const int kinds = p.weights ? 3 : 2;
+  const int tasks = batch * pv.hkv * kinds;
   for (int task = blockIdx.x / nr; task < tasks; task += gridDim.x / nr) {
-    const int which = task & 1, row = task >> 1;
+    const int which = task % kinds, row = task / kinds;
     const int r = row / pv.hkv, head = row - r * pv.hkv;
     const Geo g = load_geo(pv.geo, r);
     if (g.lkv <= p.budget) continue;  // nothing moves
     const int n = p.budget;
     const int32_t* kept = p.kept + (long long)row * p.budget;
+    if (which == 2) {
+      compact_weights(p, g, kept, head, nr, rank);
+      continue;
+    }
     uint8_t* pages = static_cast<uint8_t*>(which ? p.v_pages : p.k_pages);
-    float* weights = which ? nullptr : p.weights;
     const int stride = int(nr) * kRowsStep;
+    const int steps = (n + stride - 1) / stride;
+    const int mine = int(rank) * kRowsStep + int(threadIdx.x);  // the row of step 0 that this thread looks up
 
-    uint4 v[kCmpVecs];
-    float wv[kCmpVecs];
-    int src[kCmpVecs];  // -1: row stays or is out of range
-    auto read = [&](int j0) {
-#pragma unroll
-      for (int i = 0; i < kCmpVecs; ++i) {
-        const int j = j0 + i * kRowsPass + sub;
-        src[i] = -1;
-        if (j < n) {
-          const int k = __ldg(kept + j);
-          const int prev = j > 0 ? __ldg(kept + j - 1) : -1;
-          if (k < j || k >= g.lkv || k <= prev)
-            atomicOr(pv.err, FI_DEVERR_KEPT);
-          else if (k != j)
-            src[i] = k;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kCmpVecs; ++i) {
-        int page, slot;
-        if (src[i] < 0) continue;
-        if (!locate(pv, g.kv0, src[i], page, slot)) {
-          src[i] = -1;
-          continue;
-        }
-        const uint8_t* at = pages + kv_offset(pv, page, slot, head) * (kFp8 ? 1 : 2) + 16 * l;
-        v[i] = __ldcg(reinterpret_cast<const uint4*>(at));
-        if (weights && l == 0) wv[i] = __ldcg(weights + weight_offset(pv, page, slot, head));
+    // look-up of a step's rows, in three parts, so that no part waits for its own loads
+    int k1 = 0, k1_prev = 0, src2 = -1, src_page = -1, dst_page = -1;  // later step's entry; its page ids
+    auto fetch_entry = [&](int step) {
+      const int j = step * stride + mine;
+      if (threadIdx.x < kRowsStep && step < steps && j < n) {
+        k1 = __ldg(kept + j);
+        k1_prev = j > 0 ? __ldg(kept + j - 1) : -1;
       }
     };
-    auto write = [&](int j0) {
-#pragma unroll
-      for (int i = 0; i < kCmpVecs; ++i) {
-        int page, slot;
-        if (src[i] < 0 || !locate(pv, g.kv0, j0 + i * kRowsPass + sub, page, slot)) continue;
-        uint8_t* at = pages + kv_offset(pv, page, slot, head) * (kFp8 ? 1 : 2) + 16 * l;
-        *reinterpret_cast<uint4*>(at) = v[i];
-        if (weights && l == 0) weights[weight_offset(pv, page, slot, head)] = wv[i];
+    auto page_entry = [&](int j) { return pv.kv_indices + g.kv0 + (pv.page_shift >= 0 ? j >> pv.page_shift : j / pv.page_size); };
+    auto fetch_pages = [&](int step) {
+      const int j = step * stride + mine;
+      src2 = -1;
+      if (threadIdx.x < kRowsStep && step < steps && j < n) {
+        src2 = kept_source(p, j, k1, k1_prev, g.lkv);
+        if (src2 >= 0) {
+          src_page = __ldg(page_entry(src2));
+          dst_page = __ldg(page_entry(j));
+        }
       }
     };
-    for (int s0 = 0; s0 < n; s0 += stride) {
-      const int j0 = s0 + int(rank) * kRowsStep;
-      read(j0);
+    auto put_rows = [&](int step) {
+      if (threadIdx.x >= kRowsStep) return;
+      int2 at = make_int2(-1, 0);
+      if (src2 >= 0) {
+        if (unsigned(src_page) < unsigned(pv.num_pages) && unsigned(dst_page) < unsigned(pv.num_pages)) {
+          const int j = step * stride + mine;
+          const int ss = pv.page_shift >= 0 ? src2 & (pv.page_size - 1) : src2 % pv.page_size;
+          const int ds = pv.page_shift >= 0 ? j & (pv.page_size - 1) : j % pv.page_size;
+          at = make_int2(int(kv_offset(pv, src_page, ss, head) / kHeadDim), int(kv_offset(pv, dst_page, ds, head) / kHeadDim));
+        } else {
+          atomicOr(pv.err, FI_DEVERR_PAGE_OOB);
+        }
+      }
+      sm.idx[step % kIdxRing][threadIdx.x] = at;
+    };
+    auto read = [&](int step) {
+      if (step < steps) {
+#pragma unroll
+        for (int i = 0; i < kCmpVecs; ++i) {
+          const int src = sm.idx[step % kIdxRing][i * kRowsPass + sub].x;
+          if (src >= 0) cp_async_16(&sm.data[step % kCmpAhead][i][threadIdx.x], pages + (long long)src * kRowBytes + 16 * l);
+        }
+      }
+      cp_async_commit();
+    };
+    auto write = [&](int step) {
+#pragma unroll
+      for (int i = 0; i < kCmpVecs; ++i) {
+        const int2 at = sm.idx[step % kIdxRing][i * kRowsPass + sub];
+        if (at.x >= 0)
+          *reinterpret_cast<uint4*>(pages + (long long)at.y * kRowBytes + 16 * l) = sm.data[step % kCmpAhead][i][threadIdx.x];
+      }
+    };
+    __syncthreads();  // the last task's look-ups are not read any more
+    for (int i = 0; i <= kCmpAhead; ++i) {
+      fetch_entry(i);
+      fetch_pages(i);
+      put_rows(i);
+    }
+    fetch_entry(kCmpAhead + 1);
+    fetch_pages(kCmpAhead + 1);
+    fetch_entry(kCmpAhead + 2);
+    __syncthreads();
+    for (int i = 0; i < kCmpAhead; ++i) read(i);
+    for (int step = 0; step < steps; ++step) {
+      cp_async_wait<kCmpAhead - 1>();  // this thread's reads of the step have landed
       if (nr > 1)
         cluster_sync_all();
       else
         __syncthreads();
-      write(j0);
+      // everybody's have.  The look-ups of step + ahead + 1 go into the place of step - 1's.
+      put_rows(step + kCmpAhead + 1);
+      fetch_pages(step + kCmpAhead + 2);
+      fetch_entry(step + kCmpAhead + 3);
+      write(step);
+      read(step + kCmpAhead);
     }
+    cp_async_wait<0>();
   }
 }
 
@@ -306,12 +400,21 @@ int launch_select(const SelectParams& p, int batch, int max_lkv, int num_sms, cu
 }
 
 int launch_compact(const CompactParams& p, int batch, bool fp8, int num_sms, cudaStream_t stream) {
-  const int64_t tasks = int64_t(batch) * p.pv.hkv * 2;
+  const int64_t tasks = int64_t(batch) * p.pv.hkv * (p.weights ? 3 : 2);
   unsigned cluster = 1;
-  while (cluster < 8 && tasks * cluster * 2 <= num_sms) cluster *= 2;
-  const unsigned grid = unsigned(std::min<int64_t>(tasks, 16 * num_sms)) * cluster;
-  const cudaError_t e = fp8 ? launch_dependent(compact_kernel<true>, grid, kCmpThreads, 0, cluster, stream, p)
-                            : launch_dependent(compact_kernel<false>, grid, kCmpThreads, 0, cluster, stream, p);
+  while (cluster < 8 && tasks * cluster * 2 <= 2 * num_sms) cluster *= 2;
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  std::call_once(once, [] {
+    attr = cudaFuncSetAttribute(compact_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(CompactSmem)));
+    if (attr == cudaSuccess)
+      attr = cudaFuncSetAttribute(compact_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(CompactSmem)));
+  });
+  if (attr != cudaSuccess) return record_cuda_error(attr, "cudaFuncSetAttribute(compact_kernel)");
+  const unsigned grid = unsigned(std::min<int64_t>(tasks, 64 * num_sms)) * cluster;
+  const size_t smem = sizeof(CompactSmem);
+  const cudaError_t e = fp8 ? launch_dependent(compact_kernel<true>, grid, kCmpThreads, smem, cluster, stream, p)
+                            : launch_dependent(compact_kernel<false>, grid, kCmpThreads, smem, cluster, stream, p);
   return e == cudaSuccess ? 0 : record_cuda_error(e, "compact_kernel launch");
 }
 
