@@ -20,9 +20,13 @@ __device__ __forceinline__ unsigned cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync_all() {
+__device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync_all() {
+  cluster_arrive();
+  cluster_wait();
 }
 // Reads a 32-bit word at the same shared-memory place of another CTA of the cluster.
 __device__ __forceinline__ uint32_t peer_word(const void* local, unsigned rank) {
@@ -352,29 +356,59 @@ __global__ void __launch_bounds__(kCmpThreads, 2) compact_kernel(const __grid_co
       }
     };
     __syncthreads();  // the last task's look-ups are not read any more
-    for (int i = 0; i <= kCmpAhead; ++i) {
-      fetch_entry(i);
-      fetch_pages(i);
-      put_rows(i);
+    {
+      // the first steps' look-ups, side by side
+      int k[kCmpAhead + 2], prev[kCmpAhead + 2];
+#pragma unroll
+      for (int i = 0; i < kCmpAhead + 2; ++i) {
+        fetch_entry(i);
+        k[i] = k1;
+        prev[i] = k1_prev;
+      }
+      int s2[kCmpAhead + 2], sp[kCmpAhead + 2], dp[kCmpAhead + 2];
+#pragma unroll
+      for (int i = 0; i < kCmpAhead + 2; ++i) {
+        k1 = k[i];
+        k1_prev = prev[i];
+        fetch_pages(i);
+        s2[i] = src2;
+        sp[i] = src_page;
+        dp[i] = dst_page;
+      }
+      fetch_entry(kCmpAhead + 2);
+#pragma unroll
+      for (int i = 0; i < kCmpAhead + 2; ++i) {
+        src2 = s2[i];
+        src_page = sp[i];
+        dst_page = dp[i];
+        if (i <= kCmpAhead) put_rows(i);  // the last one stays in the registers, as the loop below expects it
+      }
     }
-    fetch_entry(kCmpAhead + 1);
-    fetch_pages(kCmpAhead + 1);
-    fetch_entry(kCmpAhead + 2);
     __syncthreads();
     for (int i = 0; i < kCmpAhead; ++i) read(i);
+    if (nr > 1) {
+      cp_async_wait<kCmpAhead - 1>();
+      cluster_arrive();
+    }
     for (int step = 0; step < steps; ++step) {
-      cp_async_wait<kCmpAhead - 1>();  // this thread's reads of the step have landed
-      if (nr > 1)
-        cluster_sync_all();
-      else
+      if (nr > 1) {
+        // everybody has read this step; say so of the next one, whose barrier then runs beside the writes
+        cluster_wait();
         __syncthreads();
-      // everybody's have.  The look-ups of step + ahead + 1 go into the place of step - 1's.
+        cp_async_wait<kCmpAhead - 2>();
+        cluster_arrive();
+      } else {
+        cp_async_wait<kCmpAhead - 1>();
+        __syncthreads();
+      }
+      // the look-ups of step + ahead + 1 go into the place of step - 1's
       put_rows(step + kCmpAhead + 1);
       fetch_pages(step + kCmpAhead + 2);
       fetch_entry(step + kCmpAhead + 3);
       write(step);
       read(step + kCmpAhead);
     }
+    if (nr > 1) cluster_wait();
     cp_async_wait<0>();
   }
 }
