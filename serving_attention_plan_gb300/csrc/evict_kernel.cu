@@ -225,6 +225,12 @@ struct CompactSmem {
   int2 idx[kIdxRing][kCmpThreads];  // (source, destination) row of the page pool; source -1: the row stays
 };
 
+// 16 bytes global -> shared, or nothing (the source is not read, the destination gets zeros).
+__device__ __forceinline__ void cp_async_16_or_none(void* dst_smem, const void* src_gmem, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst_smem)), "l"(src_gmem), "r"(on ? 16 : 0)
+               : "memory");
+}
+
 // Checks entry j of a kept list of n entries; -1 for one that stays, is out of range or is behind the end.
 __device__ __forceinline__ int kept_source(const CompactParams& p, int j, int k, int prev, int lkv) {
   if (k < j || k >= lkv || k <= prev) {
@@ -296,63 +302,70 @@ __global__ void __launch_bounds__(kCmpThreads, 2) compact_kernel(const __grid_co
       compact_weights(p, g, kept, head, nr, rank);
       continue;
     }
-    uint8_t* pages = static_cast<uint8_t*>(which ? p.v_pages : p.k_pages);
+    uint8_t* pages = static_cast<uint8_t*>(which ? p.v_pages : p.k_pages) + 16 * l;
     const int stride = int(nr) * kRowsStep;
     const int steps = (n + stride - 1) / stride;
+    const bool looks = threadIdx.x < kRowsStep;
     const int mine = int(rank) * kRowsStep + int(threadIdx.x);  // the row of step 0 that this thread looks up
+    const int32_t* list = pv.kv_indices + g.kv0;
+    // rows of the pool (128 elements each, so they fit 32 bits): per page, slot and head
+    const int page_rows = int(pv.page_stride / kHeadDim), slot_rows = int(pv.tok_stride / kHeadDim),
+              head_row = head * int(pv.head_stride / kHeadDim);
+    auto page_of = [&](int j) { return pv.page_shift >= 0 ? j >> pv.page_shift : j / pv.page_size; };
 
     // look-up of a step's rows, in three parts, so that no part waits for its own loads
     int k1 = 0, k1_prev = 0, src2 = -1, src_page = -1, dst_page = -1;  // later step's entry; its page ids
     auto fetch_entry = [&](int step) {
       const int j = step * stride + mine;
-      if (threadIdx.x < kRowsStep && step < steps && j < n) {
+      k1 = j;  // stays
+      k1_prev = -1;
+      if (looks && j < n) {
         k1 = __ldg(kept + j);
-        k1_prev = j > 0 ? __ldg(kept + j - 1) : -1;
+        if (j > 0) k1_prev = __ldg(kept + j - 1);
       }
     };
-    auto page_entry = [&](int j) { return pv.kv_indices + g.kv0 + (pv.page_shift >= 0 ? j >> pv.page_shift : j / pv.page_size); };
     auto fetch_pages = [&](int step) {
       const int j = step * stride + mine;
-      src2 = -1;
-      if (threadIdx.x < kRowsStep && step < steps && j < n) {
-        src2 = kept_source(p, j, k1, k1_prev, g.lkv);
-        if (src2 >= 0) {
-          src_page = __ldg(page_entry(src2));
-          dst_page = __ldg(page_entry(j));
-        }
+      src2 = j < n ? kept_source(p, j, k1, k1_prev, g.lkv) : -1;
+      if (looks && src2 >= 0) {
+        src_page = __ldg(list + page_of(src2));
+        dst_page = __ldg(list + page_of(j));
       }
     };
-    auto put_rows = [&](int step) {
-      if (threadIdx.x >= kRowsStep) return;
-      int2 at = make_int2(-1, 0);
+    auto put_rows = [&](int step, int at) {
+      if (!looks) return;
+      int2 rows = make_int2(-1, 0);
       if (src2 >= 0) {
         if (unsigned(src_page) < unsigned(pv.num_pages) && unsigned(dst_page) < unsigned(pv.num_pages)) {
           const int j = step * stride + mine;
-          const int ss = pv.page_shift >= 0 ? src2 & (pv.page_size - 1) : src2 % pv.page_size;
-          const int ds = pv.page_shift >= 0 ? j & (pv.page_size - 1) : j % pv.page_size;
-          at = make_int2(int(kv_offset(pv, src_page, ss, head) / kHeadDim), int(kv_offset(pv, dst_page, ds, head) / kHeadDim));
+          rows.x = src_page * page_rows + (src2 - page_of(src2) * pv.page_size) * slot_rows + head_row;
+          rows.y = dst_page * page_rows + (j - page_of(j) * pv.page_size) * slot_rows + head_row;
         } else {
           atomicOr(pv.err, FI_DEVERR_PAGE_OOB);
         }
       }
-      sm.idx[step % kIdxRing][threadIdx.x] = at;
+      sm.idx[at][threadIdx.x] = rows;
     };
-    auto read = [&](int step) {
+    // rows that stay are copied too, as nothing (no bytes read, none written): no branch in between
+    auto read = [&](int step, int at, int to) {
       if (step < steps) {
+        int src[kCmpVecs];
 #pragma unroll
-        for (int i = 0; i < kCmpVecs; ++i) {
-          const int src = sm.idx[step % kIdxRing][i * kRowsPass + sub].x;
-          if (src >= 0) cp_async_16(&sm.data[step % kCmpAhead][i][threadIdx.x], pages + (long long)src * kRowBytes + 16 * l);
-        }
+        for (int i = 0; i < kCmpVecs; ++i) src[i] = sm.idx[at][i * kRowsPass + sub].x;
+#pragma unroll
+        for (int i = 0; i < kCmpVecs; ++i)
+          cp_async_16_or_none(&sm.data[to][i][threadIdx.x], pages + (long long)max(src[i], 0) * kRowBytes, src[i] >= 0);
       }
       cp_async_commit();
     };
-    auto write = [&](int step) {
+    auto write = [&](int at, int from) {
+      int2 rows[kCmpVecs];
+#pragma unroll
+      for (int i = 0; i < kCmpVecs; ++i) rows[i] = sm.idx[at][i * kRowsPass + sub];
 #pragma unroll
       for (int i = 0; i < kCmpVecs; ++i) {
-        const int2 at = sm.idx[step % kIdxRing][i * kRowsPass + sub];
-        if (at.x >= 0)
-          *reinterpret_cast<uint4*>(pages + (long long)at.y * kRowBytes + 16 * l) = sm.data[step % kCmpAhead][i][threadIdx.x];
+        const uint4 v = sm.data[from][i][threadIdx.x];
+        if (rows[i].x >= 0) *reinterpret_cast<uint4*>(pages + (long long)rows[i].y * kRowBytes) = v;
       }
     };
     __syncthreads();  // the last task's look-ups are not read any more
@@ -381,15 +394,17 @@ __global__ void __launch_bounds__(kCmpThreads, 2) compact_kernel(const __grid_co
         src2 = s2[i];
         src_page = sp[i];
         dst_page = dp[i];
-        if (i <= kCmpAhead) put_rows(i);  // the last one stays in the registers, as the loop below expects it
+        if (i <= kCmpAhead) put_rows(i, i);  // the last one stays in the registers, as the loop below expects it
       }
     }
     __syncthreads();
-    for (int i = 0; i < kCmpAhead; ++i) read(i);
+    for (int i = 0; i < kCmpAhead; ++i) read(i, i, i);
     if (nr > 1) {
       cp_async_wait<kCmpAhead - 1>();
       cluster_arrive();
     }
+    // places in the rings of the step at work, and of the look-ups of steps ahead of it
+    int at = 0, at_read = kCmpAhead, at_put = kCmpAhead + 1, data = 0;
     for (int step = 0; step < steps; ++step) {
       if (nr > 1) {
         // everybody has read this step; say so of the next one, whose barrier then runs beside the writes
@@ -402,11 +417,15 @@ __global__ void __launch_bounds__(kCmpThreads, 2) compact_kernel(const __grid_co
         __syncthreads();
       }
       // the look-ups of step + ahead + 1 go into the place of step - 1's
-      put_rows(step + kCmpAhead + 1);
+      put_rows(step + kCmpAhead + 1, at_put);
       fetch_pages(step + kCmpAhead + 2);
       fetch_entry(step + kCmpAhead + 3);
-      write(step);
-      read(step + kCmpAhead);
+      write(at, data);
+      read(step + kCmpAhead, at_read, data);
+      at = at + 1 == kIdxRing ? 0 : at + 1;
+      at_read = at_read + 1 == kIdxRing ? 0 : at_read + 1;
+      at_put = at_put + 1 == kIdxRing ? 0 : at_put + 1;
+      data = data + 1 == kCmpAhead ? 0 : data + 1;
     }
     if (nr > 1) cluster_wait();
     cp_async_wait<0>();
