@@ -24,6 +24,11 @@ __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// An arrival that publishes no writes: enough to say that this thread's reads have come back.  (The release
+// form waits for the thread's stores as well.)
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_sync_all() {
   cluster_arrive();
   cluster_wait();
@@ -401,7 +406,7 @@ __global__ void __launch_bounds__(kCmpThreads, 2) compact_kernel(const __grid_co
     for (int i = 0; i < kCmpAhead; ++i) read(i, i, i);
     if (nr > 1) {
       cp_async_wait<kCmpAhead - 1>();
-      cluster_arrive();
+      cluster_arrive_relaxed();
     }
     // places in the rings of the step at work, and of the look-ups of steps ahead of it
     int at = 0, at_read = kCmpAhead, at_put = kCmpAhead + 1, data = 0;
@@ -411,7 +416,7 @@ __global__ void __launch_bounds__(kCmpThreads, 2) compact_kernel(const __grid_co
         cluster_wait();
         __syncthreads();
         cp_async_wait<kCmpAhead - 2>();
-        cluster_arrive();
+        cluster_arrive_relaxed();
       } else {
         cp_async_wait<kCmpAhead - 1>();
         __syncthreads();
