@@ -116,8 +116,9 @@ struct SelectParams {
   const float* weights;
   int32_t* kept;  // [batch, hkv, budget]
   int sink, recent, budget;
+  int by_four;  // weights can be fetched four slots at a time; set by the launcher
 };
-int launch_select(const SelectParams& p, int batch, int max_lkv, int num_sms, cudaStream_t stream);
+int launch_select(SelectParams p, int batch, int max_lkv, int num_sms, cudaStream_t stream);
 
 struct CompactParams {
   PageView pv;

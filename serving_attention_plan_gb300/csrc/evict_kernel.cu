@@ -1,6 +1,7 @@
 // Selection of the keys to keep, and their compaction, per (request, KV head).
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "cache_common.cuh"
 #include "prefill_launch.h"
@@ -49,13 +50,18 @@ __device__ __forceinline__ uint32_t peer_word(const void* local, unsigned rank) 
 // change the result.  The kept positions come out ascending by ranking (greater, equal) counts over
 // the range in order.  Weights are read from memory once (the slice of the range that a CTA owns
 // stays in shared memory); a cluster of CTAs shares a row when there are few rows.
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
+//   Where pages hold whole groups of four slots, a thread fetches four weights at a time (one page id, one 16-byte
+// load); one at a time the instructions around the loads took most of the time.  In a cluster each CTA adds
+// up one part of the bins over its peers, and only the part that holds the threshold is read by all:
+// every CTA reading every bin of every peer took 4 us a pass with 8 CTAs.
 constexpr int kBins = 2048;
+constexpr int kFetch = 8;  // weights a thread has in flight
 
 struct SelectSmem {
   uint32_t hist[3][kBins];
-  uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
+  uint32_t part[kBins / 2];  // cluster: the row's counts of this CTA's part of the bins
+  uint32_t part_sum[3];
+  uint32_t warp_gt[32], warp_eq[32];
   uint32_t total_gt, total_eq;  // of this CTA's slice
   uint32_t digit, above;        // result of a pass
 };
@@ -67,9 +73,37 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ SelectParams p, int cap) {
-  extern __shared__ uint32_t keys[];  // [cap]: the CTA's slice of the row
+// The sum of v[0 .. warp - 1], v in shared memory; a whole warp calls it.
+__device__ __forceinline__ uint32_t sum_before(const uint32_t* v, int warp) {
+  const int lane = threadIdx.x & 31;
+  return __reduce_add_sync(kAll, lane < warp ? v[lane] : 0u);
+}
+
+// The sum of `mine` over the threads before this one; the whole CTA calls it.
+__device__ __forceinline__ uint32_t scan_before(uint32_t mine, uint32_t* warp_sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(kAll, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) warp_sums[warp] = incl;
+  __syncthreads();
+  return incl - mine + sum_before(warp_sums, warp);
+}
+
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 6) select_kernel(const __grid_constant__ SelectParams p, int cap) {
+  extern __shared__ __align__(16) uint32_t keys[];  // [cap]: the CTA's slice of the row
   __shared__ SelectSmem sm;
+  constexpr int kWarps = kThreads / 32, kMine = kBins / kThreads;
+  auto clear = [&]() {
+    for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&sm.hist[0][0])[i] = 0;
+    if (threadIdx.x < 3) sm.part_sum[threadIdx.x] = 0;
+  };
+  clear();
+  __syncthreads();
   wait_prior_grid();
   const PageView& pv = p.pv;
   const int batch = __ldg(pv.header + H_BATCH);
@@ -81,33 +115,58 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     const Geo g = load_geo(pv.geo, r);
     int32_t* kept = p.kept + (long long)row * p.budget;
     if (g.lkv <= p.budget) {
-      for (int i = rank * kSelThreads + tid; i < p.budget; i += nr * kSelThreads) kept[i] = i < g.lkv ? i : -1;
+      for (int i = rank * kThreads + tid; i < p.budget; i += nr * kThreads) kept[i] = i < g.lkv ? i : -1;
       continue;  // the same for every CTA of the cluster
     }
     const int f0 = p.sink, f1 = g.lkv - p.recent;
     const int need = p.budget - p.sink - p.recent;
-    for (int i = rank * kSelThreads + tid; i < p.sink + p.recent; i += nr * kSelThreads) {
+    for (int i = rank * kThreads + tid; i < p.sink + p.recent; i += nr * kThreads) {
       if (i < p.sink)
         kept[i] = i;
       else
         kept[p.budget - p.recent + i - p.sink] = g.lkv - p.recent + i - p.sink;
     }
     if (need == 0) continue;
-    // this CTA's slice, a multiple of a warp's step so that warps own whole steps
-    const int per = (((f1 - f0 + int(nr) - 1) / int(nr)) + 31) & ~31;
-    const int s0 = min(f1, f0 + int(rank) * per), s1 = min(f1, s0 + per);
-    const int n = s1 - s0;
+    // this CTA's slice of whole steps of 32 positions; key 0, which no weight maps to, marks positions outside
+    // the free range
+    const int a0 = f0 & ~31;
+    const int per = (((f1 - a0 + int(nr) - 1) / int(nr)) + 31) & ~31;
+    const int s0 = min(f1, a0 + int(rank) * per), n = min(f1, s0 + per) - s0;
     const bool in_smem = n <= cap;
-    auto fetch = [&](int i) -> uint32_t {  // key i of the slice, from memory
+    auto fetch_one = [&](int i) -> uint32_t {
       int page, slot;
-      if (!locate(pv, g.kv0, s0 + i, page, slot)) return 0u;
+      if (s0 + i < f0 || i >= n || !locate(pv, g.kv0, s0 + i, page, slot)) return 0u;
       return order_key(__ldg(p.weights + weight_offset(pv, page, slot, head)));
     };
-    for (int i = tid; i < 3 * kBins; i += kSelThreads) (&sm.hist[0][0])[i] = 0;
-    if (in_smem)
-      for (int i = tid; i < n; i += kSelThreads) keys[i] = fetch(i);
-    auto key = [&](int i) { return in_smem ? keys[i] : fetch(i); };
-    __syncthreads();
+    // kFetch keys: kFetch / kVec groups of kVec positions, `apart` groups between them; all page ids first
+    auto fetch = [&](int group, int apart, uint32_t (&x)[kFetch], auto vec) {
+      constexpr int kVec = decltype(vec)::value;
+      int at[kFetch / kVec];  // a pool holds fewer than 2^31 rows: its K alone takes 128 bytes each
+#pragma unroll
+      for (int k = 0; k < kFetch / kVec; ++k) {
+        const int i = (group + k * apart) * kVec;
+        int page, slot;
+        at[k] = -1;
+        if (i < n && s0 + i + kVec > f0 && locate(pv, g.kv0, s0 + i, page, slot))
+          at[k] = int(weight_offset(pv, page, slot, head));
+      }
+#pragma unroll
+      for (int k = 0; k < kFetch / kVec; ++k) {
+        float w[kVec];
+        if (at[k] >= 0) {
+          if constexpr (kVec == 4)
+            *reinterpret_cast<float4*>(w) = __ldg(reinterpret_cast<const float4*>(p.weights + at[k]));
+          else
+            w[0] = __ldg(p.weights + at[k]);
+        }
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+          const int i = (group + k * apart) * kVec + e;
+          x[k * kVec + e] = at[k] >= 0 && i < n && s0 + i >= f0 ? order_key(w[e]) : 0u;
+        }
+      }
+    };
+    auto key = [&](int i) { return in_smem ? keys[i] : fetch_one(i); };
 
     uint32_t prefix = 0;  // the digits found so far, in place
     uint32_t left = uint32_t(need);
@@ -115,83 +174,126 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const uint32_t mask = pass == 2 ? 1023u : 2047u;
       const uint32_t known = pass == 0 ? 0u : pass == 1 ? 0xffe00000u : 0xfffffc00u;
-      for (int i = tid; i < n; i += kSelThreads) {
-        const uint32_t x = key(i);
-        if ((x & known) == prefix) atomicAdd(&sm.hist[pass][(x >> shift) & mask], 1u);
-      }
-      __syncthreads();
-      if (nr > 1) cluster_sync_all();
-      // thread t sums the row's counts of 4 bins, highest bins first
-      uint32_t c[kBins / kSelThreads], mine = 0;
+      auto count = [&](uint32_t x) {
+        if (x != 0 && (x & known) == prefix) atomicAdd(&sm.hist[pass][(x >> shift) & mask], 1u);
+      };
+      if (pass > 0 && in_smem) {
+        for (int i = tid; i < n; i += kThreads) count(keys[i]);
+      } else {
+        auto all = [&](auto vec) {
+          constexpr int kVec = decltype(vec)::value;
+          const int groups = (n + kVec - 1) / kVec;
+          for (int q = tid; q < groups; q += kFetch / kVec * kThreads) {
+            uint32_t x[kFetch];
+            fetch(q, kThreads, x, vec);
 #pragma unroll
-      for (int k = 0; k < kBins / kSelThreads; ++k) {
-        const int bin = kBins - 1 - (tid * (kBins / kSelThreads) + k);
-        uint32_t v = 0;
-        if (nr == 1)
-          v = sm.hist[pass][bin];
+            for (int k = 0; k < kFetch / kVec; ++k) {
+              const int i = (q + k * kThreads) * kVec;
+              if (i >= n) break;
+              if (in_smem) {  // the slice's storage is a multiple of four
+                if constexpr (kVec == 4)
+                  *reinterpret_cast<uint4*>(keys + i) = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                else
+                  keys[i] = x[k];
+              }
+#pragma unroll
+              for (int e = 0; e < kVec; ++e) count(x[k * kVec + e]);
+            }
+          }
+        };
+        if (p.by_four)
+          all(std::integral_constant<int, 4>());
         else
-          for (unsigned q = 0; q < nr; ++q) v += peer_word(&sm.hist[pass][bin], q);
-        c[k] = v;
-        mine += v;
+          all(std::integral_constant<int, 1>());
       }
-      uint32_t incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t v = __shfl_up_sync(kAll, incl, o);
-        if (lane >= o) incl += v;
-      }
-      if (lane == 31) sm.warp_gt[warp] = incl;
       __syncthreads();
-      uint32_t before = incl - mine;
-      for (int w = 0; w < warp; ++w) before += sm.warp_gt[w];
+      // the bin that holds the `left`-th largest: threads take bins in falling order
+      if (nr == 1) {
+        uint32_t c[kMine], mine = 0;
 #pragma unroll
-      for (int k = 0; k < kBins / kSelThreads; ++k) {
-        if (before < left && left <= before + c[k]) {
-          sm.digit = uint32_t(kBins - 1 - (tid * (kBins / kSelThreads) + k));
+        for (int k = 0; k < kMine; ++k) {
+          c[k] = sm.hist[pass][kBins - 1 - (tid * kMine + k)];
+          mine += c[k];
+        }
+        uint32_t before = scan_before(mine, sm.warp_gt);
+#pragma unroll
+        for (int k = 0; k < kMine; ++k) {
+          if (before < left && left <= before + c[k]) {
+            sm.digit = uint32_t(kBins - 1 - (tid * kMine + k));
+            sm.above = before;
+          }
+          before += c[k];
+        }
+      } else {
+        cluster_sync_all();
+        const int part = kBins / int(nr);  // at most kThreads
+        uint32_t v = 0;
+        if (tid < part) {
+#pragma unroll 8
+          for (unsigned q = 0; q < nr; ++q) v += peer_word(&sm.hist[pass][int(rank) * part + tid], q);
+          sm.part[tid] = v;
+        }
+        v = __reduce_add_sync(kAll, v);
+        if (lane == 0 && v) atomicAdd(&sm.part_sum[pass], v);
+        __syncthreads();
+        cluster_sync_all();
+        // lane l holds part nr - 1 - l
+        const uint32_t sum = lane < int(nr) ? peer_word(&sm.part_sum[pass], nr - 1 - lane) : 0u;
+        uint32_t upto = sum;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+          const uint32_t u = __shfl_up_sync(kAll, upto, o);
+          if (lane >= o) upto += u;
+        }
+        const int hit = __ffs(__ballot_sync(kAll, lane < int(nr) && left <= upto)) - 1;
+        const uint32_t skipped = __shfl_sync(kAll, upto - sum, hit);
+        const int owner = int(nr) - 1 - hit;
+        const uint32_t c = tid < part ? peer_word(&sm.part[part - 1 - tid], unsigned(owner)) : 0u;
+        const uint32_t before = skipped + scan_before(c, sm.warp_gt);
+        if (before < left && left <= before + c) {
+          sm.digit = uint32_t(owner * part + part - 1 - tid);
           sm.above = before;
         }
-        before += c[k];
       }
       __syncthreads();
       prefix |= sm.digit << shift;
       left -= sm.above;
-      __syncthreads();
     }
     // `prefix` is the K-th largest weight; every greater key stays, and the first `left` equal ones.
     // Warps own consecutive steps of 32 keys.
     const int steps = (n + 31) >> 5;
-    const int w0 = steps * warp / kSelWarps, w1 = steps * (warp + 1) / kSelWarps;
+    const int w0 = steps * warp / kWarps, w1 = steps * (warp + 1) / kWarps;
     uint32_t gt = 0, eq = 0;
     for (int st = w0; st < w1; ++st) {
       const int i = st * 32 + lane;
       const uint32_t x = i < n ? key(i) : 0u;
-      gt += __popc(__ballot_sync(kAll, i < n && x > prefix));
-      eq += __popc(__ballot_sync(kAll, i < n && x == prefix));
+      gt += i < n && x > prefix;
+      eq += i < n && x == prefix;
     }
+    gt = __reduce_add_sync(kAll, gt);
+    eq = __reduce_add_sync(kAll, eq);
+    __syncthreads();  // the last pass's sums are not read any more
     if (lane == 0) {
       sm.warp_gt[warp] = gt;
       sm.warp_eq[warp] = eq;
     }
     __syncthreads();
-    if (tid == 0) {
-      uint32_t a = 0, b = 0;
-      for (int w = 0; w < kSelWarps; ++w) {
-        a += sm.warp_gt[w];
-        b += sm.warp_eq[w];
+    if (warp == 0) {
+      const uint32_t a = sum_before(sm.warp_gt, kWarps), b = sum_before(sm.warp_eq, kWarps);
+      if (lane == 0) {
+        sm.total_gt = a;
+        sm.total_eq = b;
       }
-      sm.total_gt = a;
-      sm.total_eq = b;
     }
-    __syncthreads();
-    if (nr > 1) cluster_sync_all();
-    gt = eq = 0;
-    for (unsigned q = 0; q < rank; ++q) {
-      gt += peer_word(&sm.total_gt, q);
-      eq += peer_word(&sm.total_eq, q);
-    }
-    for (int w = 0; w < warp; ++w) {
-      gt += sm.warp_gt[w];
-      eq += sm.warp_eq[w];
+    gt = sum_before(sm.warp_gt, warp);
+    eq = sum_before(sm.warp_eq, warp);
+    if (nr > 1) {
+      __syncthreads();
+      cluster_sync_all();
+      for (unsigned q = 0; q < rank; ++q) {
+        gt += peer_word(&sm.total_gt, q);
+        eq += peer_word(&sm.total_eq, q);
+      }
     }
     const uint32_t below = (1u << lane) - 1u;
     for (int st = w0; st < w1; ++st) {
@@ -204,9 +306,13 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
       gt += __popc(bg);
       eq += __popc(be);
     }
-    // peers may still read this CTA's totals and counts; the next row overwrites them
-    __syncthreads();
-    if (nr > 1) cluster_sync_all();
+    // a further row starts over; peers may still read this CTA's counts
+    if (row + int(gridDim.x / nr) < rows || nr > 1) {
+      __syncthreads();
+      if (nr > 1) cluster_sync_all();
+      clear();
+      __syncthreads();
+    }
   }
 }
 
@@ -439,8 +545,9 @@ __global__ void __launch_bounds__(kCmpThreads, 2) compact_kernel(const __grid_co
 
 }  // namespace
 
-int launch_select(const SelectParams& p, int batch, int max_lkv, int num_sms, cudaStream_t stream) {
+int launch_select(SelectParams p, int batch, int max_lkv, int num_sms, cudaStream_t stream) {
   const int rows = batch * p.pv.hkv;
+  p.by_four = p.pv.page_size % 4 == 0 && reinterpret_cast<uintptr_t>(p.weights) % 16 == 0;
   unsigned cluster = 1;
   while (cluster < 8 && rows * int(cluster) * 2 <= num_sms && max_lkv / int(cluster) > 4096) cluster *= 2;
   const int64_t want = (int64_t(max_lkv) / cluster + 64 + 31) / 32 * 32;
@@ -449,11 +556,16 @@ int launch_select(const SelectParams& p, int batch, int max_lkv, int num_sms, cu
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 48 * 1024 * 4);
+    attr = cudaFuncSetAttribute(select_kernel<256>, cudaFuncAttributeMaxDynamicSharedMemorySize, 48 * 1024 * 4);
+    if (attr == cudaSuccess)
+      attr = cudaFuncSetAttribute(select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, 48 * 1024 * 4);
   });
   if (attr != cudaSuccess) return record_cuda_error(attr, "cudaFuncSetAttribute(select_kernel)");
   const unsigned grid = unsigned(std::min<int64_t>(rows, 4 * num_sms)) * cluster;
-  const cudaError_t e = launch_dependent(select_kernel, grid, kSelThreads, smem, cluster, stream, p, cap);
+  // short rows take 256 threads, six to an SM; long ones, and clusters, 1024
+  const bool wide = cluster > 1 || max_lkv > 4096;
+  const cudaError_t e = wide ? launch_dependent(select_kernel<1024>, grid, 1024, smem, cluster, stream, p, cap)
+                             : launch_dependent(select_kernel<256>, grid, 256, smem, cluster, stream, p, cap);
   return e == cudaSuccess ? 0 : record_cuda_error(e, "select_kernel launch");
 }
 
