@@ -51,16 +51,17 @@ __device__ __forceinline__ uint32_t peer_word(const void* local, unsigned rank) 
 // the range in order.  Weights are read from memory once (the slice of the range that a CTA owns
 // stays in shared memory); a cluster of CTAs shares a row when there are few rows.
 //   Where pages hold whole groups of four slots, a thread fetches four weights at a time (one page id, one 16-byte
-// load); one at a time the instructions around the loads took most of the time.  In a cluster each CTA adds
-// up one part of the bins over its peers, and only the part that holds the threshold is read by all:
-// every CTA reading every bin of every peer took 4 us a pass with 8 CTAs.
+// load); one at a time the instructions around the loads took most of the time.  In a cluster every CTA
+// reads its peers' counts in two steps, 64 coarse bins and then the 32 bins of the one that holds the threshold:
+// reading all bins of all peers took 4 us a pass with 8 CTAs.
 constexpr int kBins = 2048;
+constexpr int kCoarse = kBins / 32;
 constexpr int kFetch = 8;  // weights a thread has in flight
 
 struct SelectSmem {
   uint32_t hist[3][kBins];
-  uint32_t part[kBins / 2];  // cluster: the row's counts of this CTA's part of the bins
-  uint32_t part_sum[3];
+  uint32_t coarse[3][kCoarse];  // cluster: the histogram in runs of 32 bins
+  uint32_t row[kCoarse + 32];   // cluster: the row's coarse counts, and the 32 of the hit
   uint32_t warp_gt[32], warp_eq[32];
   uint32_t total_gt, total_eq;  // of this CTA's slice
   uint32_t digit, above;        // result of a pass
@@ -100,7 +101,6 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 6) select_ker
   constexpr int kWarps = kThreads / 32, kMine = kBins / kThreads;
   auto clear = [&]() {
     for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&sm.hist[0][0])[i] = 0;
-    if (threadIdx.x < 3) sm.part_sum[threadIdx.x] = 0;
   };
   clear();
   __syncthreads();
@@ -225,34 +225,55 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 6) select_ker
           before += c[k];
         }
       } else {
-        cluster_sync_all();
-        const int part = kBins / int(nr);  // at most kThreads
-        uint32_t v = 0;
-        if (tid < part) {
-#pragma unroll 8
-          for (unsigned q = 0; q < nr; ++q) v += peer_word(&sm.hist[pass][int(rank) * part + tid], q);
-          sm.part[tid] = v;
+        // warp w adds up runs w, w + 32 of 32 bins (a cluster's CTAs have 32 warps)
+#pragma unroll
+        for (int k = 0; k < kCoarse / 32; ++k) {
+          const uint32_t v = __reduce_add_sync(kAll, sm.hist[pass][(warp + 32 * k) * 32 + lane]);
+          if (lane == 0) sm.coarse[pass][warp + 32 * k] = v;
         }
-        v = __reduce_add_sync(kAll, v);
-        if (lane == 0 && v) atomicAdd(&sm.part_sum[pass], v);
+        if (tid < kCoarse + 32) sm.row[tid] = 0;
         __syncthreads();
         cluster_sync_all();
-        // lane l holds part nr - 1 - l
-        const uint32_t sum = lane < int(nr) ? peer_word(&sm.part_sum[pass], nr - 1 - lane) : 0u;
-        uint32_t upto = sum;
+        const int bin = tid & (kCoarse - 1);
+        if (tid < kCoarse * int(nr)) {
+          const uint32_t v = peer_word(&sm.coarse[pass][bin], unsigned(tid / kCoarse));
+          if (v) atomicAdd(&sm.row[bin], v);
+        }
+        __syncthreads();
+        // every warp finds the hit by itself: lane l takes runs 63 - 2 l and 62 - 2 l
+        const uint32_t c0 = sm.row[kCoarse - 1 - 2 * lane], c1 = sm.row[kCoarse - 2 - 2 * lane];
+        uint32_t upto = c0 + c1;
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) {
+        for (int o = 1; o < 32; o <<= 1) {
           const uint32_t u = __shfl_up_sync(kAll, upto, o);
           if (lane >= o) upto += u;
         }
-        const int hit = __ffs(__ballot_sync(kAll, lane < int(nr) && left <= upto)) - 1;
-        const uint32_t skipped = __shfl_sync(kAll, upto - sum, hit);
-        const int owner = int(nr) - 1 - hit;
-        const uint32_t c = tid < part ? peer_word(&sm.part[part - 1 - tid], unsigned(owner)) : 0u;
-        const uint32_t before = skipped + scan_before(c, sm.warp_gt);
-        if (before < left && left <= before + c) {
-          sm.digit = uint32_t(owner * part + part - 1 - tid);
-          sm.above = before;
+        const int hit = __ffs(__ballot_sync(kAll, left <= upto)) - 1;
+        uint32_t skipped = __shfl_sync(kAll, upto - c0 - c1, hit);
+        const uint32_t h0 = __shfl_sync(kAll, c0, hit);
+        int run = kCoarse - 1 - 2 * hit;
+        if (left > skipped + h0) {
+          skipped += h0;
+          --run;
+        }
+        if (tid < 32 * int(nr)) {
+          const uint32_t v = peer_word(&sm.hist[pass][run * 32 + lane], unsigned(warp));
+          if (v) atomicAdd(&sm.row[kCoarse + lane], v);
+        }
+        __syncthreads();
+        if (warp == 0) {  // bins from the run's last down
+          const uint32_t c = sm.row[kCoarse + 31 - lane];
+          uint32_t incl = c;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(kAll, incl, o);
+            if (lane >= o) incl += u;
+          }
+          const uint32_t before = skipped + incl - c;
+          if (before < left && left <= before + c) {
+            sm.digit = uint32_t(run * 32 + 31 - lane);
+            sm.above = before;
+          }
         }
       }
       __syncthreads();
@@ -264,11 +285,19 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 6) select_ker
     const int steps = (n + 31) >> 5;
     const int w0 = steps * warp / kWarps, w1 = steps * (warp + 1) / kWarps;
     uint32_t gt = 0, eq = 0;
-    for (int st = w0; st < w1; ++st) {
-      const int i = st * 32 + lane;
-      const uint32_t x = i < n ? key(i) : 0u;
-      gt += i < n && x > prefix;
-      eq += i < n && x == prefix;
+    auto keys4 = [&](int st, uint32_t (&x)[4]) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = st + k < w1 && (st + k) * 32 + lane < n ? key((st + k) * 32 + lane) : 0u;
+    };
+    // (key 0, a position outside the range, is neither above nor equal to the threshold)
+    for (int st = w0; st < w1; st += 4) {
+      uint32_t x[4];
+      keys4(st, x);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        gt += x[k] > prefix;
+        eq += x[k] == prefix;
+      }
     }
     gt = __reduce_add_sync(kAll, gt);
     eq = __reduce_add_sync(kAll, eq);
@@ -294,22 +323,25 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 6) select_ker
         gt += peer_word(&sm.total_gt, q);
         eq += peer_word(&sm.total_eq, q);
       }
+      cluster_arrive();  // this CTA reads no peer from here on; the wait below lets it go on or leave
     }
     const uint32_t below = (1u << lane) - 1u;
-    for (int st = w0; st < w1; ++st) {
-      const int i = st * 32 + lane;
-      const uint32_t x = i < n ? key(i) : 0u;
-      const unsigned bg = __ballot_sync(kAll, i < n && x > prefix), be = __ballot_sync(kAll, i < n && x == prefix);
-      const uint32_t eq_before = eq + __popc(be & below);
-      const bool keep = ((bg >> lane) & 1u) || (((be >> lane) & 1u) && eq_before < left);
-      if (keep) kept[p.sink + gt + __popc(bg & below) + min(left, eq_before)] = s0 + i;
-      gt += __popc(bg);
-      eq += __popc(be);
+    for (int st = w0; st < w1; st += 4) {
+      uint32_t x[4];
+      keys4(st, x);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const unsigned bg = __ballot_sync(kAll, x[k] > prefix), be = __ballot_sync(kAll, x[k] == prefix);
+        const uint32_t eq_before = eq + __popc(be & below);
+        const bool keep = ((bg >> lane) & 1u) || (((be >> lane) & 1u) && eq_before < left);
+        if (keep) kept[p.sink + gt + __popc(bg & below) + min(left, eq_before)] = s0 + (st + k) * 32 + lane;
+        gt += __popc(bg);
+        eq += __popc(be);
+      }
     }
-    // a further row starts over; peers may still read this CTA's counts
-    if (row + int(gridDim.x / nr) < rows || nr > 1) {
+    if (nr > 1) cluster_wait();
+    if (row + int(gridDim.x / nr) < rows) {  // a further row starts over
       __syncthreads();
-      if (nr > 1) cluster_sync_all();
       clear();
       __syncthreads();
     }
