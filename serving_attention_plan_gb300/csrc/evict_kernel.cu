@@ -80,25 +80,11 @@ __device__ __forceinline__ uint32_t sum_before(const uint32_t* v, int warp) {
   return __reduce_add_sync(kAll, lane < warp ? v[lane] : 0u);
 }
 
-// The sum of `mine` over the threads before this one; the whole CTA calls it.
-__device__ __forceinline__ uint32_t scan_before(uint32_t mine, uint32_t* warp_sums) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t v = __shfl_up_sync(kAll, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) warp_sums[warp] = incl;
-  __syncthreads();
-  return incl - mine + sum_before(warp_sums, warp);
-}
-
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 6) select_kernel(const __grid_constant__ SelectParams p, int cap) {
   extern __shared__ __align__(16) uint32_t keys[];  // [cap]: the CTA's slice of the row
   __shared__ SelectSmem sm;
-  constexpr int kWarps = kThreads / 32, kMine = kBins / kThreads;
+  constexpr int kWarps = kThreads / 32;
   auto clear = [&]() {
     for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&sm.hist[0][0])[i] = 0;
   };
@@ -178,7 +164,13 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 6) select_ker
         if (x != 0 && (x & known) == prefix) atomicAdd(&sm.hist[pass][(x >> shift) & mask], 1u);
       };
       if (pass > 0 && in_smem) {
-        for (int i = tid; i < n; i += kThreads) count(keys[i]);
+        for (int i = 4 * tid; i < n; i += 4 * kThreads) {
+          const uint4 x = *reinterpret_cast<const uint4*>(keys + i);
+          count(x.x);
+          if (i + 1 < n) count(x.y);
+          if (i + 2 < n) count(x.z);
+          if (i + 3 < n) count(x.w);
+        }
       } else {
         auto all = [&](auto vec) {
           constexpr int kVec = decltype(vec)::value;
@@ -207,41 +199,28 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 6) select_ker
           all(std::integral_constant<int, 1>());
       }
       __syncthreads();
-      // the bin that holds the `left`-th largest: threads take bins in falling order
-      if (nr == 1) {
-        uint32_t c[kMine], mine = 0;
+      // the bin that holds the `left`-th largest: first its run of 32 bins, then itself
 #pragma unroll
-        for (int k = 0; k < kMine; ++k) {
-          c[k] = sm.hist[pass][kBins - 1 - (tid * kMine + k)];
-          mine += c[k];
-        }
-        uint32_t before = scan_before(mine, sm.warp_gt);
-#pragma unroll
-        for (int k = 0; k < kMine; ++k) {
-          if (before < left && left <= before + c[k]) {
-            sm.digit = uint32_t(kBins - 1 - (tid * kMine + k));
-            sm.above = before;
-          }
-          before += c[k];
-        }
-      } else {
-        // warp w adds up runs w, w + 32 of 32 bins (a cluster's CTAs have 32 warps)
-#pragma unroll
-        for (int k = 0; k < kCoarse / 32; ++k) {
-          const uint32_t v = __reduce_add_sync(kAll, sm.hist[pass][(warp + 32 * k) * 32 + lane]);
-          if (lane == 0) sm.coarse[pass][warp + 32 * k] = v;
-        }
-        if (tid < kCoarse + 32) sm.row[tid] = 0;
-        __syncthreads();
+      for (int k = 0; k < kCoarse / kWarps; ++k) {
+        const uint32_t v = __reduce_add_sync(kAll, sm.hist[pass][(warp + kWarps * k) * 32 + lane]);
+        if (lane == 0) sm.coarse[pass][warp + kWarps * k] = v;
+      }
+      if (nr > 1 && tid < kCoarse + 32) sm.row[tid] = 0;
+      __syncthreads();
+      const uint32_t* coarse = sm.coarse[pass];
+      if (nr > 1) {
         cluster_sync_all();
-        const int bin = tid & (kCoarse - 1);
         if (tid < kCoarse * int(nr)) {
+          const int bin = tid & (kCoarse - 1);
           const uint32_t v = peer_word(&sm.coarse[pass][bin], unsigned(tid / kCoarse));
           if (v) atomicAdd(&sm.row[bin], v);
         }
         __syncthreads();
-        // every warp finds the hit by itself: lane l takes runs 63 - 2 l and 62 - 2 l
-        const uint32_t c0 = sm.row[kCoarse - 1 - 2 * lane], c1 = sm.row[kCoarse - 2 - 2 * lane];
+        coarse = sm.row;
+      }
+      {
+        // every warp finds the run by itself: lane l takes runs 63 - 2 l and 62 - 2 l
+        const uint32_t c0 = coarse[kCoarse - 1 - 2 * lane], c1 = coarse[kCoarse - 2 - 2 * lane];
         uint32_t upto = c0 + c1;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -256,13 +235,17 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 6) select_ker
           skipped += h0;
           --run;
         }
-        if (tid < 32 * int(nr)) {
-          const uint32_t v = peer_word(&sm.hist[pass][run * 32 + lane], unsigned(warp));
-          if (v) atomicAdd(&sm.row[kCoarse + lane], v);
+        const uint32_t* fine = &sm.hist[pass][run * 32];
+        if (nr > 1) {
+          if (tid < 32 * int(nr)) {
+            const uint32_t v = peer_word(fine + lane, unsigned(warp));
+            if (v) atomicAdd(&sm.row[kCoarse + lane], v);
+          }
+          __syncthreads();
+          fine = sm.row + kCoarse;
         }
-        __syncthreads();
         if (warp == 0) {  // bins from the run's last down
-          const uint32_t c = sm.row[kCoarse + 31 - lane];
+          const uint32_t c = fine[31 - lane];
           uint32_t incl = c;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
