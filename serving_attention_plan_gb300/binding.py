@@ -121,15 +121,20 @@ def _need(ok, what: str):
         raise ValueError(what)
 
 
-def _dense(t, name: str, dtypes, shape=None):
-    """Checks a device tensor argument: type, contiguity and shape."""
+def _dense_error(t, name: str, dtypes, shape):
+    """Says what is wrong with a tensor argument that should be dense, on the GPU, of a type and shape."""
+    _need(t.dtype in dtypes, f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}")
     _need(t.is_cuda, f"{name}: a CUDA tensor is needed")
-    _need(str(t.dtype)[6:] in dtypes, f"{name}: {t.dtype}, expected {' or '.join(dtypes)}")
-    _need(t.is_contiguous(), f"{name}: a contiguous tensor is needed")
-    _need(shape is None or tuple(t.shape) == shape, f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    _need(tuple(t.shape) == tuple(shape), f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name}: a contiguous tensor is needed")
 
 
-_BF16, _F32, _I32, _E4M3 = ("bfloat16",), ("float32",), ("int32",), ("float8_e4m3fn", "uint8")
+def _raw_stream(stream, device) -> int:
+    """The stream's handle; the device's current stream for None."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def plan_compute(qo_indptr, kv_indptr, last_page_len, num_qo_heads, num_kv_heads, page_size, causal, num_sms,
@@ -194,7 +199,7 @@ class Workspace:
                                          num_sms, ctypes.byref(self._h)), "fi_workspace_create")
         self.num_qo_heads, self.num_kv_heads, self.head_dim = num_qo_heads, num_kv_heads, head_dim
         self._layout, self._kv_dtype = "HND", "bf16"
-        self._plan = None  # (total_q, batch, page_size, layout, kv_dtype) of the current plan
+        self._plan = None  # what the cache operators check arguments against: _set_plan()
 
     def close(self):
         if self._h:
@@ -236,7 +241,7 @@ class Workspace:
             idx = np.zeros(1, np.int32)
         _check(lib().fi_plan(self._h, _p32(qo), _p32(kv), _p32(idx), _p32(last), qo.shape[0] - 1, self.num_qo_heads,
                              self.num_kv_heads, self.head_dim, page_size, int(causal), _stream_ptr(stream)), "fi_plan")
-        self._plan = (int(qo[-1]), qo.shape[0] - 1, page_size, self._layout, self._kv_dtype)
+        self._set_plan(int(qo[-1]), qo.shape[0] - 1, page_size)
 
     def plan_composable(self, shared, unique, page_size, causal, stream=None):
         """Composable plan: shared and unique are (qo_indptr, kv_indptr, kv_indices, last_page_len)."""
@@ -248,7 +253,7 @@ class Workspace:
                                         _p32(uk), _p32(ui), _p32(ul), uq.shape[0] - 1, self.num_qo_heads,
                                         self.num_kv_heads, self.head_dim, page_size, int(causal), _stream_ptr(stream)),
                "fi_plan_composable")
-        self._plan = (int(uq[-1]), uq.shape[0] - 1, page_size, self._layout, self._kv_dtype)
+        self._set_plan(int(uq[-1]), uq.shape[0] - 1, page_size)
 
     def run(self, q, k_pages, v_pages, o, lse, stream=None):
         _check(lib().fi_run(self._h, _dptr(q), _dptr(k_pages), _dptr(v_pages), int(k_pages.shape[0]), _dptr(o),
@@ -260,76 +265,94 @@ class Workspace:
                                   _dptr(o_prev), _dptr(lse_prev), _dptr(o), _dptr(lse), _stream_ptr(stream)),
                "fi_run_merge")
 
-    def _pages_shape(self, name: str, pages):
-        """Checks K/V pages against the current plan."""
+    def _set_plan(self, total_q: int, batch: int, page_size: int):
+        import torch
+        h, d = self.num_kv_heads, self.head_dim
+        self._bf16, self._f32, self._i32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
+        self._kv_types = self._bf16 if self._kv_dtype == "bf16" else (torch.float8_e4m3fn, torch.uint8)
+        self._page_tail = (h, page_size, d) if self._layout == "HND" else (page_size, h, d)
+        self._q_shape, self._kv_shape = (total_q, self.num_qo_heads, d), (total_q, h, d)
+        self._lse_shape, self._kept_rows, self._page_size = (total_q, self.num_qo_heads), (batch, h), page_size
+        self._pool, self._pool_shape, self._weights_shape = -1, None, None
+        self._plan = (total_q, batch)
+
+    def _set_pool(self, num_pages: int):
+        """Shapes that go with a pool of so many pages."""
         if self._plan is None:
             raise FiError(6, "cache operator")
-        _, _, ps, layout, dtype = self._plan
-        tail = (self.num_kv_heads, ps, self.head_dim) if layout == "HND" else (ps, self.num_kv_heads, self.head_dim)
-        _dense(pages, name, _BF16 if dtype == "bf16" else _E4M3)
-        _need(pages.dim() == 4 and tuple(pages.shape[1:]) == tail, f"{name}: shape {tuple(pages.shape)}, expected (pages, {', '.join(map(str, tail))})")
+        if num_pages != self._pool:
+            self._pool = num_pages
+            self._pool_shape = (num_pages, *self._page_tail)
+            self._weights_shape = (num_pages, self.num_kv_heads, self._page_size)
 
-    def _weights_shape(self, weights, num_pages=None):
-        if self._plan is None:
-            raise FiError(6, "cache operator")
-        n = weights.shape[0] if num_pages is None else num_pages
-        _dense(weights, "weights", _F32, (n, self.num_kv_heads, self._plan[2]))
+    # every argument is checked in one expression; the slow path says what is wrong with it
+    def _dense(self, t, name, dtypes, shape) -> int:
+        if t.dtype in dtypes and t.is_cuda and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+        _dense_error(t, name, dtypes, shape)
 
-    def _rows(self, name: str, t, heads: int) -> int:
-        """Checks a [total_q, heads, 128] tensor with dense heads; returns its token stride in elements."""
-        n, d = self._plan[0], self.head_dim
-        _need(t.is_cuda and str(t.dtype) == "torch.bfloat16", f"{name}: a bfloat16 CUDA tensor is needed")
-        _need(tuple(t.shape) == (n, heads, d), f"{name}: shape {tuple(t.shape)}, expected {(n, heads, d)}")
-        st = t.stride()
-        _need(st[2] == 1 and (st[1] == d or heads == 1), f"{name}: the heads of a token must be contiguous")
-        return st[0] if n > 1 else max(st[0], heads * d)
+    def _rows(self, t, name, shape):
+        """A tensor of shape [total_q, heads, 128] with dense heads: (pointer, token stride in elements)."""
+        if t.dtype in self._bf16 and t.is_cuda and t.shape == shape:
+            st = t.stride()
+            if st[2] == 1 and (st[1] == shape[2] or shape[1] == 1):
+                return t.data_ptr(), (st[0] if shape[0] > 1 else max(st[0], shape[1] * shape[2]))
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+        _dense_error(t, name, self._bf16, shape)
 
     def append(self, q, k, v, k_pages, v_pages, q_out, q_weight=None, k_weight=None, eps=1e-6, positions=None,
                stream=None):
         """Norm (with weights) and rotate q and k of the plan's tokens; write q_out and the K/V page slots."""
-        self._pages_shape("k_pages", k_pages)
-        self._pages_shape("v_pages", v_pages)
-        _need(v_pages.shape[0] == k_pages.shape[0], "k_pages and v_pages: the same number of pages is needed")
-        sq = self._rows("q", q, self.num_qo_heads)
-        sk, sv = self._rows("k", k, self.num_kv_heads), self._rows("v", v, self.num_kv_heads)
-        _dense(q_out, "q_out", _BF16, (self._plan[0], self.num_qo_heads, self.head_dim))
-        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-            if w is not None:
-                _dense(w, name, _BF16, (self.head_dim,))
-        if positions is not None:
-            _dense(positions, "positions", _I32, (self._plan[0],))
-        _check(lib().fi_append(self._h, _dptr(q), sq, _dptr(k), sk, _dptr(v), sv, _dptr(q_weight), _dptr(k_weight),
-                               float(eps), _dptr(positions), _dptr(q_out), _dptr(k_pages), _dptr(v_pages),
-                               int(k_pages.shape[0]), _stream_ptr(stream)), "fi_append")
+        pool = k_pages.shape[0]
+        self._set_pool(pool)
+        dense = self._dense
+        kp, vp = dense(k_pages, "k_pages", self._kv_types, self._pool_shape), dense(v_pages, "v_pages", self._kv_types, self._pool_shape)
+        (pq, sq), (pk, sk), (pv, sv) = self._rows(q, "q", self._q_shape), self._rows(k, "k", self._kv_shape), self._rows(v, "v", self._kv_shape)
+        out = dense(q_out, "q_out", self._bf16, self._q_shape)
+        wq = None if q_weight is None else dense(q_weight, "q_weight", self._bf16, (self.head_dim,))
+        wk = None if k_weight is None else dense(k_weight, "k_weight", self._bf16, (self.head_dim,))
+        pos = None if positions is None else dense(positions, "positions", self._i32, (self._plan[0],))
+        st = lib().fi_append(self._h, pq, sq, pk, sk, pv, sv, wq, wk, float(eps), pos, out, kp, vp, pool,
+                             _raw_stream(stream, q.get_device()))
+        if st:
+            _check(st, "fi_append")
 
     def key_weights(self, q, k_pages, lse, weights, decay=1.0, new_keys=True, stream=None):
         """Add the attention weight of each cached key (from q, K and run()'s lse) to the decayed sums in weights."""
-        self._pages_shape("k_pages", k_pages)
-        self._weights_shape(weights, k_pages.shape[0])
-        n = self._plan[0]
-        _dense(q, "q", _BF16, (n, self.num_qo_heads, self.head_dim))
-        _dense(lse, "lse", _F32, (n, self.num_qo_heads))
-        _check(lib().fi_key_weights(self._h, _dptr(q), _dptr(k_pages), int(k_pages.shape[0]), _dptr(lse), float(decay),
-                                    int(new_keys), _dptr(weights), _stream_ptr(stream)), "fi_key_weights")
+        pool = k_pages.shape[0]
+        self._set_pool(pool)
+        dense = self._dense
+        st = lib().fi_key_weights(self._h, dense(q, "q", self._bf16, self._q_shape),
+                                  dense(k_pages, "k_pages", self._kv_types, self._pool_shape), pool,
+                                  dense(lse, "lse", self._f32, self._lse_shape), float(decay), int(new_keys),
+                                  dense(weights, "weights", self._f32, self._weights_shape),
+                                  _raw_stream(stream, weights.get_device()))
+        if st:
+            _check(st, "fi_key_weights")
 
     def select_keys(self, weights, budget, kept, recent=0, sink=0, stream=None):
         """kept[request, KV head] = the positions to keep: the first sink, the last recent, the heaviest of the rest."""
-        self._weights_shape(weights)
-        _dense(kept, "kept", _I32, (self._plan[1], self.num_kv_heads, int(budget)))
-        _check(lib().fi_select_keys(self._h, _dptr(weights), int(weights.shape[0]), int(sink), int(recent),
-                                    int(budget), _dptr(kept), _stream_ptr(stream)), "fi_select_keys")
+        pool, budget = weights.shape[0], int(budget)
+        self._set_pool(pool)
+        st = lib().fi_select_keys(self._h, self._dense(weights, "weights", self._f32, self._weights_shape), pool,
+                                  int(sink), int(recent), budget, self._dense(kept, "kept", self._i32, (*self._kept_rows, budget)),
+                                  _raw_stream(stream, weights.get_device()))
+        if st:
+            _check(st, "fi_select_keys")
 
     def compact(self, kept, k_pages, v_pages, weights=None, stream=None):
         """Move the kept K/V rows (and weights) of every request over the budget (kept's last size) to its first slots."""
-        self._pages_shape("k_pages", k_pages)
-        self._pages_shape("v_pages", v_pages)
-        _need(v_pages.shape[0] == k_pages.shape[0], "k_pages and v_pages: the same number of pages is needed")
-        if weights is not None:
-            self._weights_shape(weights, k_pages.shape[0])
-        _need(kept.dim() == 3, "kept: [batch, num_kv_heads, budget] is needed")
-        _dense(kept, "kept", _I32, (self._plan[1], self.num_kv_heads, kept.shape[2]))
-        _check(lib().fi_compact(self._h, _dptr(kept), int(kept.shape[2]), _dptr(k_pages), _dptr(v_pages),
-                                _dptr(weights), int(k_pages.shape[0]), _stream_ptr(stream)), "fi_compact")
+        pool = k_pages.shape[0]
+        self._set_pool(pool)
+        dense = self._dense
+        budget = kept.shape[-1]
+        st = lib().fi_compact(self._h, dense(kept, "kept", self._i32, (*self._kept_rows, budget)), budget,
+                              dense(k_pages, "k_pages", self._kv_types, self._pool_shape),
+                              dense(v_pages, "v_pages", self._kv_types, self._pool_shape),
+                              None if weights is None else dense(weights, "weights", self._f32, self._weights_shape), pool,
+                              _raw_stream(stream, k_pages.get_device()))
+        if st:
+            _check(st, "fi_compact")
 
     def info(self) -> np.ndarray:
         h = np.zeros(16, np.int32)
