@@ -66,6 +66,12 @@ __device__ __forceinline__ bool locate(const PageView& pv, int kv0, int j, int& 
   return false;
 }
 
+// 16 bytes global -> shared, or nothing (the source is not read, the destination gets zeros).
+__device__ __forceinline__ void cp_async_16_or_none(void* dst_smem, const void* src_gmem, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst_smem)), "l"(src_gmem), "r"(on ? 16 : 0)
+               : "memory");
+}
+
 __device__ __forceinline__ long long kv_offset(const PageView& pv, int page, int slot, int head) {
   return page * pv.page_stride + head * pv.head_stride + slot * pv.tok_stride;
 }

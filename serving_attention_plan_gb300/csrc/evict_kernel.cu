@@ -351,12 +351,6 @@ struct CompactSmem {
   int2 idx[kIdxRing][kCmpThreads];  // (source, destination) row of the page pool; source -1: the row stays
 };
 
-// 16 bytes global -> shared, or nothing (the source is not read, the destination gets zeros).
-__device__ __forceinline__ void cp_async_16_or_none(void* dst_smem, const void* src_gmem, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst_smem)), "l"(src_gmem), "r"(on ? 16 : 0)
-               : "memory");
-}
-
 // Checks entry j of a kept list of n entries; -1 for one that stays, is out of range or is behind the end.
 __device__ __forceinline__ int kept_source(const CompactParams& p, int j, int k, int prev, int lkv) {
   if (k < j || k >= lkv || k <= prev) {
