@@ -17,7 +17,7 @@ struct Geo {
   int32_t blk0;      // 32-key blocks of the requests before this one
   int32_t tile0;     // 256-key tiles of the requests before this one
   int32_t work0;     // tensor-core weights: Q tiles (over all KV heads) of the requests before this one
-  int32_t pad;
+  int32_t window;    // entry [batch]: the sliding window that work0 was counted with (-1: none)
 };
 constexpr int kBlkKeys = 32;
 constexpr int kTileKeys = 256;
@@ -101,7 +101,7 @@ struct WeightsParams {
   int hqo, group;
   float scale_log2;    // logit scale in the log2 domain (includes k_scale)
   float cap_log2, inv_cap_log2;  // soft-cap, 0 for none
-  int window_left;     // >= 0: sliding window
+  int window_left;     // >= 0: sliding window (the tensor-core form reads it from the plan)
   // tensor-core form
   int tile_tokens;      // tokens of a Q tile: 128 / group
   float* part;          // [CTAs][2][256] partial sums of items cut between CTAs

@@ -39,7 +39,10 @@ void fill_work(Geo* geo, int batch, int hkv, int tile_tokens, bool causal, int w
   int64_t work = 0;
   for (int i = 0; i <= batch; ++i) {
     geo[i].work0 = int32_t(work);
-    if (i == batch) break;
+    if (i == batch) {
+      geo[i].window = window;
+      break;
+    }
     int64_t head = 0;
     for (int kt = 0; int64_t(kt) * kTileKeys < geo[i].lkv; ++kt) {
       int t0, tokens, cost;
@@ -54,15 +57,19 @@ void fill_work(Geo* geo, int batch, int hkv, int tile_tokens, bool causal, int w
 
 int check_pages_once(const int32_t* a, int64_t na, const int32_t* b, int64_t nb, int32_t max_page) {
   try {
-    std::vector<bool> seen(size_t(max_page) + 1, false);
-    auto once = [&](const int32_t* idx, int64_t n) {
+    std::vector<uint64_t> seen((size_t(max_page) >> 6) + 1, 0);
+    uint64_t twice = 0;  // no branch in the loop
+    auto scan = [&](const int32_t* idx, int64_t n) {
       for (int64_t k = 0; k < n; ++k) {
-        if (seen[size_t(idx[k])]) return false;
-        seen[size_t(idx[k])] = true;
+        uint64_t& w = seen[size_t(idx[k]) >> 6];
+        const uint64_t bit = uint64_t(1) << (idx[k] & 63);
+        twice |= w & bit;
+        w |= bit;
       }
-      return true;
     };
-    return once(a, na) && once(b, nb) ? FI_OK : FI_ERR_UNSUPPORTED;
+    scan(a, na);
+    scan(b, nb);
+    return twice == 0 ? FI_OK : FI_ERR_UNSUPPORTED;
   } catch (const std::exception&) {
     return FI_ERR_CAPACITY;
   }

@@ -115,7 +115,7 @@ void set_geo(fi_workspace* ws, const int32_t* qo_indptr, const int32_t* kv_indpt
   const int group = ws->hqo / ws->hkv;
   if (path == fi::kPathTensor && group <= fi::kWeightTileRows)
     fi::fill_work(reinterpret_cast<fi::Geo*>(ws->hbuf + ws->off_geo), batch, ws->hkv, fi::kWeightTileRows / group,
-                  causal != 0, ws->variant.window_left, &ws->geo);
+                  causal != 0, std::min(ws->variant.window_left, 1 << 30), &ws->geo);  // no request has more keys
   ws->pages_once = ws->tails_once = 0;
 }
 

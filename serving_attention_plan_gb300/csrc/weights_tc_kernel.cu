@@ -65,6 +65,7 @@ constexpr uint32_t kTmemCols = 512;
 // The CTA's walk over its piece of the line, one segment (run of Q tiles of one item) at a time.
 // Every member is uniform over the warp; whole warps call init and next.
 struct Walk {
+  int win;               // the plan's sliding window: the line was cut with it
   int pos, end;          // remaining piece of the line
   int r, head, kt;       // request, KV head, key tile
   Geo g;
@@ -73,9 +74,9 @@ struct Walk {
   int tokens;            // query tokens that see the item
   int q0, q1;            // Q tiles of this segment
 
-  __device__ __forceinline__ static void item(const WeightsParams& p, bool causal, const Geo& g, int kt, int& t0,
-                                              int& tokens, int& cost) {
-    weight_item(g.lq, g.lkv, kt, causal, p.window_left, p.tile_tokens, &t0, &tokens, &cost);
+  __device__ __forceinline__ void item(const WeightsParams& p, bool causal, const Geo& g, int kt, int& t0, int& tokens,
+                                       int& cost) const {
+    weight_item(g.lq, g.lkv, kt, causal, win, p.tile_tokens, &t0, &tokens, &cost);
   }
   __device__ __forceinline__ void load(const WeightsParams& p) {
     g = load_geo(p.pv.geo, r);
@@ -87,6 +88,7 @@ struct Walk {
   }
   __device__ void init(const WeightsParams& p, bool causal, int batch, int begin, int finish) {
     const int lane = threadIdx.x & 31;
+    win = __ldg(&p.pv.geo[batch].window);
     pos = begin;
     end = finish;
     if (pos >= end) return;
@@ -98,7 +100,7 @@ struct Walk {
     rem -= head * per_head;
     // the key tile that holds position `rem` of the head's line: a scan over 32 tiles at a time
     int before = 0;
-    for (kt = 0;; kt += 32) {
+    for (kt = 0; kt * kKeys < g.lkv; kt += 32) {
       int a, b, c = 0;
       if ((kt + lane) * kKeys < g.lkv) item(p, causal, g, kt + lane, a, b, c);
       int incl = c;
@@ -473,6 +475,7 @@ __device__ void sum_weights(const WeightsParams& p, TcSmem& sm, bool causal, uin
   const int row = threadIdx.x & (kRows - 1);   // query row of the tile: TMEM lane
   const int col0 = (warp >> 2) * kCols;        // first key of this warp
   const uint32_t t_lane = tmem + (uint32_t((warp & 3) * 32) << 16) + uint32_t(col0);
+  const int win = sm.walk.win;
   int n = 0;
   bool alive = true;
   for (int i = 0; sm.seg[i & 1].tiles > 0; ++i) {
@@ -501,7 +504,7 @@ __device__ void sum_weights(const WeightsParams& p, TcSmem& sm, bool causal, uin
       int lo = 0, hi = kCols;  // the columns the row sees
       if (causal) {
         hi = min(kCols, pos + 1);
-        if (kWin) lo = max(0, pos - p.window_left);
+        if (kWin && win >= 0) lo = max(0, pos - win);
       }
       if (lse == -INFINITY) hi = 0;  // no such row, or one that saw no key
       const bool masked = __any_sync(kAll, lo > 0 || hi < kCols);

@@ -648,3 +648,72 @@ def test_refusals():
     ws.compact(kept[:1], kp, vp, w)
     torch.cuda.synchronize()
     assert (kept[0] == -1).all() and torch.equal(o[0], q[0]) and (w == 0).all() and ws.get_error() == 0
+
+
+def test_captured_prompt_weights_follow_a_new_plan():
+    """The tensor-core weights captured once: a replay after a plan of other lengths (the same total of query tokens)."""
+    torch = torch_mod()
+    from serving_attention_plan_gb300 import binding as B
+    first = batch_of([100, 300, 40], [120, 900, 40], 8, 2, 16, True, seed=1, extra=20)
+    second = batch_of([440], [1210], 8, 2, 16, True, seed=2, extra=first.num_pages - 76)
+    assert second.num_pages == first.num_pages and second.total_q == first.total_q
+    ws = B.Workspace(4, 500, 200, 8, 2)
+    side = torch.cuda.Stream()
+    q, k = bf16(first.q), bf16(first.k_pages)
+    lse = torch.full((440, 8), 5.0, device="cuda")
+    w, want = torch.zeros(first.num_pages, 2, 16, device="cuda"), torch.zeros(first.num_pages, 2, 16, device="cuda")
+    plan = lambda b: ws.plan(b.qo_indptr, b.kv_indptr, b.kv_indices, b.last_page_len, 16, True, stream=side)
+    torch.cuda.synchronize()
+    plan(first)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        ws.key_weights(q, k, lse, w, 1.0, True, stream=side)
+    for b in (second, first, second):
+        plan(b)
+        w.zero_()
+        want.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph.replay()
+        ws.key_weights(q, k, lse, want, 1.0, True, stream=side)
+        side.synchronize()
+        assert ws.get_error() == 0 and torch.equal(w, want) and w.abs().sum() > 0
+        ref, reach = C.key_weights(b, f64(q), first.k_pages, lse.cpu().numpy(), np.zeros(w.shape), 1.0, True)
+        tol = weights_tol(reach, lse.cpu().numpy()) + 1800 * 2.0 ** -24
+        assert (np.abs(w.cpu().numpy() - ref) <= ref * tol + 1e-30).all()
+
+
+@pytest.mark.parametrize("n_req,lq,causal,window", [(1500, 1, False, -1), (1100, 9, True, 2**31 - 1), (1100, 9, True, 3)])
+def test_many_requests(n_req, lq, causal, window):
+    """More requests than two rounds of the 32-way search, some of them empty; append and weights."""
+    torch = torch_mod()
+    rng = np.random.default_rng(6)
+    ql = np.where(rng.random(n_req) < 0.2, 0, lq)
+    kl = np.where(rng.random(n_req) < 0.1, 0, rng.integers(1, 40, n_req))
+    kl = np.where(ql > 0, np.maximum(kl, 1), kl)
+    b = batch_of(list(ql), list(kl), 2, 1, 8, causal, seed=3)
+    q = A.bf16_to_f64(b.q)
+    lse = lse_of(b, q, b.k_pages, 1.0, window, 0.0, "HND")
+    old = rng.random((b.num_pages, 1, 8)).astype(np.float32)
+    ws = workspace(b, window=window)
+    w = dev(old)
+    ws.key_weights(bf16(b.q), bf16(b.k_pages), dev(lse), w, 0.5, True)
+    torch.cuda.synchronize()
+    ref, reach = C.key_weights(b, q, b.k_pages, lse, old, 0.5, True, window=window)
+    used = np.zeros((b.num_pages, 8), bool)
+    for i in range(n_req):
+        p, s = C.places(b, i, np.arange(int(kl[i])))
+        used[p, s] = True
+    got = w.cpu().numpy()
+    tol = weights_tol(reach, lse) + 18 * 2.0 ** -24
+    assert (np.abs(got - ref)[:, 0][used] <= (ref * tol + 1e-30)[:, 0][used]).all()
+    assert np.array_equal(got[:, 0][~used], old[:, 0][~used])
+    k = torch.randn(b.total_q, 1, 128, device="cuda").to(torch.bfloat16)
+    kp, vp, out = bf16(b.k_pages), bf16(b.v_pages), torch.zeros(b.total_q, 2, 128, device="cuda", dtype=torch.bfloat16)
+    ws.append(bf16(b.q), k, k, kp, vp, out)
+    torch.cuda.synchronize()
+    tok, page, slot, _ = C.append_places(b)
+    want = b.k_pages.copy()
+    want[page, :, slot] = bits(k)[tok]
+    assert np.array_equal(bits(kp), want) and np.array_equal(bits(out), b.q) and ws.get_error() == 0
