@@ -47,8 +47,9 @@ __device__ __forceinline__ uint32_t peer_word(const void* local, unsigned rank) 
 // largest stay, ties to the lowest position.  A radix select finds the K-th largest exactly: the
 // weights are mapped to 32-bit integers in the same order, and three passes of 11, 11 and 10 bits
 // narrow the threshold down by counting.  Counts are integers, so shared-memory atomics do not
-// change the result.  The kept positions come out ascending by ranking (greater, equal) counts over
-// the range in order.  Weights are read from memory once (the slice of the range that a CTA owns
+// change the result.  A pass ends the search when all keys of its bin stay, which without many equal weights
+// the second does.  The kept positions come out ascending by ranking (greater, equal) counts over the range in
+// order, four positions a thread.  Weights are read from memory once (the slice of the range that a CTA owns
 // stays in shared memory); a cluster of CTAs shares a row when there are few rows.
 //   Where pages hold whole groups of four slots, a thread fetches four weights at a time (one page id, one 16-byte
 // load); one at a time the instructions around the loads took most of the time.  In a cluster every CTA
@@ -62,9 +63,9 @@ struct SelectSmem {
   uint32_t hist[3][kBins];
   uint32_t coarse[3][kCoarse];  // cluster: the histogram in runs of 32 bins
   uint32_t row[kCoarse + 32];   // cluster: the row's coarse counts, and the 32 of the hit
-  uint32_t warp_gt[32], warp_eq[32];
+  uint32_t scan[2][32];         // the warps' counts of a chunk
   uint32_t total_gt, total_eq;  // of this CTA's slice
-  uint32_t digit, above;        // result of a pass
+  uint32_t digit[3], above, within;  // result of a pass: the bin, the keys above it and in it
 };
 
 // Order-preserving map; -0 counts as 0 and every NaN as the largest.
@@ -74,12 +75,6 @@ __device__ __forceinline__ uint32_t order_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// The sum of v[0 .. warp - 1], v in shared memory; a whole warp calls it.
-__device__ __forceinline__ uint32_t sum_before(const uint32_t* v, int warp) {
-  const int lane = threadIdx.x & 31;
-  return __reduce_add_sync(kAll, lane < warp ? v[lane] : 0u);
-}
-
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 6) select_kernel(const __grid_constant__ SelectParams p, int cap) {
   extern __shared__ __align__(16) uint32_t keys[];  // [cap]: the CTA's slice of the row
@@ -87,6 +82,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 6) select_ker
   constexpr int kWarps = kThreads / 32;
   auto clear = [&]() {
     for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&sm.hist[0][0])[i] = 0;
+    if (threadIdx.x == 0) sm.total_gt = sm.total_eq = 0;
   };
   clear();
   __syncthreads();
@@ -152,11 +148,11 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 6) select_ker
         }
       }
     };
-    auto key = [&](int i) { return in_smem ? keys[i] : fetch_one(i); };
-
     uint32_t prefix = 0;  // the digits found so far, in place
     uint32_t left = uint32_t(need);
-    for (int pass = 0; pass < 3; ++pass) {
+    int passes = 0;
+    bool all_in = false;  // every key of the last bin stays: there is no need to look into it
+    for (int pass = 0; pass < 3 && !all_in; ++pass, ++passes) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const uint32_t mask = pass == 2 ? 1023u : 2047u;
       const uint32_t known = pass == 0 ? 0u : pass == 1 ? 0xffe00000u : 0xfffffc00u;
@@ -254,52 +250,32 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 6) select_ker
           }
           const uint32_t before = skipped + incl - c;
           if (before < left && left <= before + c) {
-            sm.digit = uint32_t(run * 32 + 31 - lane);
+            sm.digit[pass] = uint32_t(run * 32 + 31 - lane);
             sm.above = before;
+            sm.within = c;
           }
         }
       }
       __syncthreads();
-      prefix |= sm.digit << shift;
+      prefix |= sm.digit[pass] << shift;
       left -= sm.above;
+      all_in = left == sm.within;
     }
-    // `prefix` is the K-th largest weight; every greater key stays, and the first `left` equal ones.
-    // Warps own consecutive steps of 32 keys.
-    const int steps = (n + 31) >> 5;
-    const int w0 = steps * warp / kWarps, w1 = steps * (warp + 1) / kWarps;
-    uint32_t gt = 0, eq = 0;
-    auto keys4 = [&](int st, uint32_t (&x)[4]) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = st + k < w1 && (st + k) * 32 + lane < n ? key((st + k) * 32 + lane) : 0u;
-    };
-    // (key 0, a position outside the range, is neither above nor equal to the threshold)
-    for (int st = w0; st < w1; st += 4) {
-      uint32_t x[4];
-      keys4(st, x);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        gt += x[k] > prefix;
-        eq += x[k] == prefix;
-      }
-    }
-    gt = __reduce_add_sync(kAll, gt);
-    eq = __reduce_add_sync(kAll, eq);
-    __syncthreads();  // the last pass's sums are not read any more
-    if (lane == 0) {
-      sm.warp_gt[warp] = gt;
-      sm.warp_eq[warp] = eq;
-    }
-    __syncthreads();
-    if (warp == 0) {
-      const uint32_t a = sum_before(sm.warp_gt, kWarps), b = sum_before(sm.warp_eq, kWarps);
-      if (lane == 0) {
-        sm.total_gt = a;
-        sm.total_eq = b;
-      }
-    }
-    gt = sum_before(sm.warp_gt, warp);
-    eq = sum_before(sm.warp_eq, warp);
+    // `prefix` is the K-th largest weight: every greater key stays, and the first `left` equal ones; or, with
+    // all_in, the least of its bin: every key from there on stays
+    const uint32_t above = all_in ? prefix - 1 : prefix;  // (prefix > 0: no weight maps to the first bins)
+    if (all_in) left = 0;
+    uint32_t gt = 0, eq = 0;  // kept, and equal, before the chunk at work
     if (nr > 1) {
+      // what the slices of the lower ranks hold follows from their own counts
+      uint32_t mine = 0;
+      for (int pass = 0; pass < passes; ++pass) {
+        const uint32_t from = sm.digit[pass] + (all_in && pass == passes - 1 ? 0 : 1);
+        for (uint32_t i = from + tid; i < kBins; i += kThreads) mine += sm.hist[pass][i];
+      }
+      mine = __reduce_add_sync(kAll, mine);
+      if (lane == 0 && mine) atomicAdd(&sm.total_gt, mine);
+      if (tid == 0 && !all_in) sm.total_eq = sm.hist[2][sm.digit[2]];
       __syncthreads();
       cluster_sync_all();
       for (unsigned q = 0; q < rank; ++q) {
@@ -308,19 +284,47 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 6) select_ker
       }
       cluster_arrive();  // this CTA reads no peer from here on; the wait below lets it go on or leave
     }
-    const uint32_t below = (1u << lane) - 1u;
-    for (int st = w0; st < w1; st += 4) {
-      uint32_t x[4];
-      keys4(st, x);
+    // chunks of four positions a thread, in order: (greater, equal) counts packed in one word, added up over the
+    // warp by shuffles and over the warps through shared memory
+    for (int c0 = 0, par = 0; c0 < n; c0 += 4 * kThreads, par ^= 1) {
+      const int i = c0 + 4 * tid;
+      uint32_t x[4] = {0, 0, 0, 0};
+      if (in_smem) {
+        if (i < n) {
+          const uint4 v = *reinterpret_cast<const uint4*>(keys + i);
+          x[0] = v.x;
+          x[1] = i + 1 < n ? v.y : 0u;
+          x[2] = i + 2 < n ? v.z : 0u;
+          x[3] = i + 3 < n ? v.w : 0u;
+        }
+      } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const unsigned bg = __ballot_sync(kAll, x[k] > prefix), be = __ballot_sync(kAll, x[k] == prefix);
-        const uint32_t eq_before = eq + __popc(be & below);
-        const bool keep = ((bg >> lane) & 1u) || (((be >> lane) & 1u) && eq_before < left);
-        if (keep) kept[p.sink + gt + __popc(bg & below) + min(left, eq_before)] = s0 + (st + k) * 32 + lane;
-        gt += __popc(bg);
-        eq += __popc(be);
+        for (int e = 0; e < 4; ++e) x[e] = fetch_one(i + e);
       }
+      uint32_t mine = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mine += (x[e] > above ? 1u : 0u) + (x[e] == above && !all_in ? 0x10000u : 0u);
+      uint32_t incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(kAll, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (lane == 31) sm.scan[par][warp] = incl;
+      __syncthreads();
+      const uint32_t w = lane < kWarps ? sm.scan[par][lane] : 0u;
+      const uint32_t before = incl - mine + __reduce_add_sync(kAll, lane < warp ? w : 0u);
+      const uint32_t all = __reduce_add_sync(kAll, w);
+      uint32_t my_gt = gt + (before & 0xffffu), my_eq = eq + (before >> 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool is_gt = x[e] > above, is_eq = x[e] == above && !all_in;
+        if (is_gt || (is_eq && my_eq < left)) kept[p.sink + my_gt + min(left, my_eq)] = s0 + i + e;
+        my_gt += is_gt;
+        my_eq += is_eq;
+      }
+      gt += all & 0xffffu;
+      eq += all >> 16;
     }
     if (nr > 1) cluster_wait();
     if (row + int(gridDim.x / nr) < rows) {  // a further row starts over
