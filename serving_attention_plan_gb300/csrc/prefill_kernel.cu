@@ -982,12 +982,6 @@ bool make_decode_map_bf16(CUtensorMap* m, const void* base, int hkv, int page_si
                   uint32_t(box_rows), 1u);
 }
 
-bool make_query_map(CUtensorMap* m, const void* q, int hqo, int total_q, int heads, int tokens) {
-  if (encode_fn() == nullptr) return false;
-  const uint64_t row = uint64_t(kHeadDim) * 2;
-  return make_map(m, q, uint64_t(hqo), uint64_t(total_q), row, row * hqo, uint32_t(heads), uint32_t(tokens));
-}
-
 int launch_prefill(const PrefillArgs& a, cudaStream_t stream) {
   if (encode_fn() == nullptr) return record_cuda_error(cudaErrorNotSupported, "cuTensorMapEncodeTiled entry point");
   if (a.page_size % 8 != 0 || kTile % a.page_size != 0 || a.group > kItemRows || a.group * a.tile_tokens > kItemRows)

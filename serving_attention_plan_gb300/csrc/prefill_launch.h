@@ -57,11 +57,6 @@ int record_cuda_error(cudaError_t e, const char* what);
 bool make_decode_map_e4m3(CUtensorMap* m, const void* base, int hkv, int page_size, int num_pages, bool nhd,
                           int box_rows);
 
-// Tensor map of the queries [total_q][hqo][128] for tiles of `tokens` tokens x `heads` heads: a box is
-// 64 dims of tokens * heads rows, token by token, 128-byte swizzled.  Rows behind total_q read as zeros.
-// Returns false if the driver's encoder is missing or refuses the map.
-bool make_query_map(CUtensorMap* m, const void* q, int hqo, int total_q, int heads, int tokens);
-
 // Tensor map of bf16 HND K or V pages [pages][H_kv][page_size][128] for the decode kernel's TMA
 // copier: (dim, token in page, page * H_kv + head), one box 64 dims x box_rows tokens (the copier's
 // min(page_size, stage tokens)), 128-byte swizzled.  Returns false if the driver's encoder is

@@ -32,6 +32,7 @@
 //   warp 18      TMA producer of Q tiles (three stages)
 //   warp 19      tensor memory, MMA issue
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -624,6 +625,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, kTmemCols);
   }
+}
+
+// Tensor map of the queries [total_q][hqo][128] for tiles of `tokens` tokens x `heads` heads: a box is
+// 64 dims of tokens * heads rows, token by token, 128-byte swizzled.  Rows behind total_q read as zeros.
+// Returns false if the driver's encoder is missing or refuses the map.
+bool make_query_map(CUtensorMap* m, const void* q, int hqo, int total_q, int heads, int tokens) {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) == cudaSuccess &&
+        found == cudaDriverEntryPointSuccess)
+      encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  if (encode == nullptr) return false;
+  const cuuint64_t row = cuuint64_t(kHeadDim) * 2;
+  const cuuint64_t dims[3] = {cuuint64_t(kHeadDim), cuuint64_t(hqo), cuuint64_t(total_q)}, strides[2] = {row, row * hqo};
+  const cuuint32_t box[3] = {64u, cuuint32_t(heads), cuuint32_t(tokens)}, step[3] = {1u, 1u, 1u};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
