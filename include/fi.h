@@ -320,7 +320,8 @@ int fi_merge_states(const void* o_a, const float* lse_a, const void* o_b, const 
  * type and scales, window, soft-cap) and fi_plan_info header[1] (the path; on the tensor-core path also the
  * total query count for fi_key_weights, as for fi_run), and the conditions on pages below hold for it too,
  * unchecked.  The workspace's device must be the current one (else INVALID_ARG).  Page
- * ids >= num_pages: INVALID_ARG (in a replay: skipped, FI_DEVERR_PAGE_OOB).  Calls that share a
+ * ids >= num_pages: INVALID_ARG (in a replay: skipped, FI_DEVERR_PAGE_OOB).  Pools of more than
+ * 2^31 - 1 rows (pages * page size * KV heads): UNSUPPORTED.  Calls that share a
  * workspace must not overlap on the GPU.  Results are bit-identical from run to run.
  * `weights` is float32 [num_pages, num_kv_heads, page_size] for either page layout.
  */
@@ -365,7 +366,7 @@ int fi_cache_plan_compute(const int32_t* qo_indptr, const int32_t* kv_indptr, co
  *   q_out        DEVICE bf16 [total_q, num_qo_heads, 128]; may be q itself when q is dense
  *   k_pages, v_pages   as for fi_run (written)
  * Errors: NO_PLAN, INVALID_ARG (null or not 16-byte aligned pointers, strides), UNSUPPORTED (a page
- * that takes new tokens from two requests), CUDA.
+ * that takes new tokens from two requests, or that a composable plan's shared part reads), CUDA.
  */
 int fi_append(fi_workspace* ws, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
               int64_t v_stride, const void* q_weight, const void* k_weight, float eps, const int32_t* positions,

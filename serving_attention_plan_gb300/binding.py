@@ -199,7 +199,8 @@ class Workspace:
                                          num_sms, ctypes.byref(self._h)), "fi_workspace_create")
         self.num_qo_heads, self.num_kv_heads, self.head_dim = num_qo_heads, num_kv_heads, head_dim
         self._layout, self._kv_dtype = "HND", "bf16"
-        self._plan = None  # what the cache operators check arguments against: _set_plan()
+        self._plan = None  # (total_q, batch, page_size, layout, kv_dtype) of the current plan
+        self._shapes_of = None  # the plan whose argument shapes the cache operators hold: _set_plan()
 
     def close(self):
         if self._h:
@@ -241,7 +242,7 @@ class Workspace:
             idx = np.zeros(1, np.int32)
         _check(lib().fi_plan(self._h, _p32(qo), _p32(kv), _p32(idx), _p32(last), qo.shape[0] - 1, self.num_qo_heads,
                              self.num_kv_heads, self.head_dim, page_size, int(causal), _stream_ptr(stream)), "fi_plan")
-        self._set_plan(int(qo[-1]), qo.shape[0] - 1, page_size)
+        self._plan = (int(qo[-1]), qo.shape[0] - 1, page_size, self._layout, self._kv_dtype)
 
     def plan_composable(self, shared, unique, page_size, causal, stream=None):
         """Composable plan: shared and unique are (qo_indptr, kv_indptr, kv_indices, last_page_len)."""
@@ -253,7 +254,7 @@ class Workspace:
                                         _p32(uk), _p32(ui), _p32(ul), uq.shape[0] - 1, self.num_qo_heads,
                                         self.num_kv_heads, self.head_dim, page_size, int(causal), _stream_ptr(stream)),
                "fi_plan_composable")
-        self._set_plan(int(uq[-1]), uq.shape[0] - 1, page_size)
+        self._plan = (int(uq[-1]), uq.shape[0] - 1, page_size, self._layout, self._kv_dtype)
 
     def run(self, q, k_pages, v_pages, o, lse, stream=None):
         _check(lib().fi_run(self._h, _dptr(q), _dptr(k_pages), _dptr(v_pages), int(k_pages.shape[0]), _dptr(o),
@@ -265,21 +266,24 @@ class Workspace:
                                   _dptr(o_prev), _dptr(lse_prev), _dptr(o), _dptr(lse), _stream_ptr(stream)),
                "fi_run_merge")
 
-    def _set_plan(self, total_q: int, batch: int, page_size: int):
+    def _set_plan(self):
+        """The shapes and types that go with the current plan."""
         import torch
+        if self._plan is None:
+            raise FiError(6, "cache operator")
+        total_q, batch, page_size, layout, kv_dtype = self._plan
         h, d = self.num_kv_heads, self.head_dim
         self._bf16, self._f32, self._i32 = (torch.bfloat16,), (torch.float32,), (torch.int32,)
-        self._kv_types = self._bf16 if self._kv_dtype == "bf16" else (torch.float8_e4m3fn, torch.uint8)
-        self._page_tail = (h, page_size, d) if self._layout == "HND" else (page_size, h, d)
+        self._kv_types = self._bf16 if kv_dtype == "bf16" else (torch.float8_e4m3fn, torch.uint8)
+        self._page_tail = (h, page_size, d) if layout == "HND" else (page_size, h, d)
         self._q_shape, self._kv_shape = (total_q, self.num_qo_heads, d), (total_q, h, d)
         self._lse_shape, self._kept_rows, self._page_size = (total_q, self.num_qo_heads), (batch, h), page_size
-        self._pool, self._pool_shape, self._weights_shape = -1, None, None
-        self._plan = (total_q, batch)
+        self._pool, self._shapes_of = -1, self._plan
 
     def _set_pool(self, num_pages: int):
         """Shapes that go with a pool of so many pages."""
-        if self._plan is None:
-            raise FiError(6, "cache operator")
+        if self._plan is None or self._plan is not self._shapes_of:
+            self._set_plan()
         if num_pages != self._pool:
             self._pool = num_pages
             self._pool_shape = (num_pages, *self._page_tail)

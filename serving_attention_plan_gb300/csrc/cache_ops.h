@@ -55,8 +55,10 @@ GeoTotals fill_geo(const int32_t* qo_indptr, const int32_t* kv_indptr, const int
 void fill_work(Geo* geo, int batch, int hkv, int tile_tokens, bool causal, int window, GeoTotals* totals);
 // FI_OK if no page id (0 .. max_page) occurs twice in the two lists, else FI_ERR_UNSUPPORTED; FI_ERR_CAPACITY without host memory.
 int check_pages_once(const int32_t* a, int64_t na, const int32_t* b, int64_t nb, int32_t max_page);
-// FI_OK if no page takes new tokens (the last l_q keys of a request) from two places of the list.
-int check_tails_once(const Geo* geo, const int32_t* kv_indices, int batch, int page_size);
+// FI_OK if no page takes new tokens (the last l_q keys of a request) from two places of the list, or while the
+// shared list (of a composable plan; n_shared may be 0) holds it too.
+int check_tails_once(const Geo* geo, const int32_t* kv_indices, int batch, int page_size, const int32_t* shared,
+                     int64_t n_shared);
 // Radians per position -> the fraction of a turn per position, in 2^-64 turns.
 uint64_t turns_fraction(double inv_freq);
 

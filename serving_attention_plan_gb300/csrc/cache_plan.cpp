@@ -75,7 +75,8 @@ int check_pages_once(const int32_t* a, int64_t na, const int32_t* b, int64_t nb,
   }
 }
 
-int check_tails_once(const Geo* geo, const int32_t* kv_indices, int batch, int page_size) {
+int check_tails_once(const Geo* geo, const int32_t* kv_indices, int batch, int page_size, const int32_t* shared,
+                     int64_t n_shared) {
   try {
     std::vector<int32_t> pages;
     for (int i = 0; i < batch; ++i) {
@@ -85,7 +86,9 @@ int check_tails_once(const Geo* geo, const int32_t* kv_indices, int batch, int p
       pages.insert(pages.end(), kv_indices + g.kv0 + first, kv_indices + g.kv0 + last + 1);
     }
     std::sort(pages.begin(), pages.end());
-    return std::adjacent_find(pages.begin(), pages.end()) == pages.end() ? FI_OK : FI_ERR_UNSUPPORTED;
+    bool once = std::adjacent_find(pages.begin(), pages.end()) == pages.end();
+    for (int64_t k = 0; k < n_shared && once; ++k) once = !std::binary_search(pages.begin(), pages.end(), shared[k]);
+    return once ? FI_OK : FI_ERR_UNSUPPORTED;
   } catch (const std::exception&) {
     return FI_ERR_CAPACITY;
   }

@@ -136,7 +136,9 @@ int check_tails_once(fi_workspace* ws) {
   if (ws->tails_once == 0) {
     const int st = fi::check_tails_once(reinterpret_cast<const fi::Geo*>(ws->hbuf + ws->off_geo),
                                         reinterpret_cast<const int32_t*>(ws->hbuf + ws->off_kv),
-                                        ws->header[fi::H_BATCH], ws->header[fi::H_PAGE_SIZE]);
+                                        ws->header[fi::H_BATCH], ws->header[fi::H_PAGE_SIZE],
+                                        reinterpret_cast<const int32_t*>(ws->hbuf + ws->off_a_kv),
+                                        ws->plan_nnz_shared);
     if (st == FI_ERR_CAPACITY) return st;
     ws->tails_once = st == FI_OK ? 1 : -1;
   }
@@ -150,6 +152,8 @@ int check_cache_call(const fi_workspace* ws, int num_pages) {
   if (!ws->has_plan) return FI_ERR_NO_PLAN;
   if (!ws->geo.ok) return FI_ERR_UNSUPPORTED;
   if (num_pages < 0 || ws->max_page >= num_pages) return FI_ERR_INVALID_ARG;
+  // the kernels number a pool's rows (one key of one head) in 32 bits
+  if (int64_t(num_pages) * ws->header[fi::H_PAGE_SIZE] > INT32_MAX / ws->hkv) return FI_ERR_UNSUPPORTED;
   int dev = -1;
   FI_CUDA(cudaGetDevice(&dev));
   return dev == ws->device ? FI_OK : FI_ERR_INVALID_ARG;
@@ -757,7 +761,7 @@ int fi_cache_plan_compute(const int32_t* qo_indptr, const int32_t* kv_indptr, co
   st = fi::check_pages_once(kv_indices, nnz, nullptr, 0, max_page);
   if (st == FI_ERR_CAPACITY) return st;
   twice[0] = st != FI_OK;
-  st = fi::check_tails_once(out, kv_indices, batch, page_size);
+  st = fi::check_tails_once(out, kv_indices, batch, page_size, nullptr, 0);
   if (st == FI_ERR_CAPACITY) return st;
   twice[1] = st != FI_OK;
   return FI_OK;

@@ -563,6 +563,15 @@ def test_composable_plan():
     assert e.value.status == 1
     ws.append(q, x, x, kp, vp, o, positions=torch.arange(5, device="cuda", dtype=torch.int32))
     torch.cuda.synchronize()
+    ws2 = B.Workspace(5, 5, 200, 32, 8)
+    shares = s.kv_indices.copy()
+    shares[int(s.kv_indptr[1]) - 1] = sp.prefix.kv_indices[0]  # a tail page that is the prefix's too
+    ws2.plan_composable(idx(sp.prefix), (s.qo_indptr, s.kv_indptr, shares, s.last_page_len), 16, False)
+    for call in (lambda: ws2.append(q, x, x, kp, vp, o, positions=torch.arange(5, device="cuda", dtype=torch.int32)),
+                 lambda: ws2.key_weights(q, kp, lse, w)):
+        with pytest.raises(B.FiError) as e:
+            call()
+        assert e.value.status == 3
     _, page, slot, _ = C.append_places(s)
     want = s.k_pages.copy()
     want[page, :, slot] = bits(x)
@@ -717,3 +726,50 @@ def test_many_requests(n_req, lq, causal, window):
     want = b.k_pages.copy()
     want[page, :, slot] = bits(k)[tok]
     assert np.array_equal(bits(kp), want) and np.array_equal(bits(out), b.q) and ws.get_error() == 0
+
+
+@pytest.mark.parametrize("lq,causal", [(1, False), (30, True)])
+def test_pool_beyond_32_bit_offsets(lq, causal):
+    """Pages at the end of a pool of more than 2^31 elements (and 2^32 bytes): append, weights, selection, compaction."""
+    torch = torch_mod()
+    pool, hk, ps, hq = (1 << 31) // (8 * 16 * 128) + 50, 8, 16, 16
+    b = batch_of([lq, lq], [300, 77], hq, hk, ps, causal, seed=2, extra=0)
+    n = b.num_pages
+    high = dataclasses.replace(b, kv_indices=(b.kv_indices + pool - n).astype(np.int32))
+    kp, vp = (torch.empty(pool, hk, ps, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    w = torch.empty(pool, hk, ps, device="cuda")
+    for t in (kp, vp, w):
+        t[-2 * n:] = 0
+    kp[-n:], vp[-n:] = bf16(b.k_pages), bf16(b.v_pages)
+    rng = np.random.default_rng(1)
+    old = rng.random((n, hk, ps)).astype(np.float32)
+    w[-n:] = dev(old)
+    q = A.bf16_to_f64(b.q)
+    lse = lse_of(b, q, b.k_pages, 1.0, -1, 0.0, "HND")
+    ws = workspace(high)
+    ws.key_weights(bf16(b.q), kp, dev(lse), w, 0.5, True)
+    kept = torch.empty(2, hk, 64, dtype=torch.int32, device="cuda")
+    ws.select_keys(w, 64, kept, recent=8, sink=4)
+    torch.cuda.synchronize()
+    ref, reach = C.key_weights(b, q, b.k_pages, lse, old, 0.5, True)
+    got = w[-n:].cpu().numpy()
+    used = np.zeros((n, ps), bool)
+    for i, length in enumerate((300, 77)):
+        p, s = C.places(b, i, np.arange(length))
+        used[p, s] = True
+    err, lim = np.abs(got - ref), ref * (weights_tol(reach, lse) + 60 * 2.0 ** -24) + 1e-30
+    assert (err <= lim).transpose(0, 2, 1)[used].all()
+    rkept = C.select(b, got, 64, 8, 4)
+    assert np.array_equal(kept.cpu().numpy(), rkept)
+    ws.compact(kept, kp, vp, w)
+    torch.cuda.synchronize()
+    rk, rv, rw = C.compact(b, rkept, [b.k_pages, b.v_pages, got], ["HND"] * 3)
+    assert np.array_equal(bits(kp[-n:]), rk) and np.array_equal(bits(vp[-n:]), rv) and np.array_equal(w[-n:].cpu().numpy(), rw)
+    x = torch.randn(2 * lq, hk, 128, device="cuda").to(torch.bfloat16)
+    out = torch.empty(2 * lq, hq, 128, dtype=torch.bfloat16, device="cuda")
+    ws.append(bf16(b.q), x, x, kp, vp, out)
+    torch.cuda.synchronize()
+    tok, page, slot, _ = C.append_places(b)
+    rk[page, :, slot], rv[page, :, slot] = bits(x)[tok], bits(x)[tok]
+    assert np.array_equal(bits(kp[-n:]), rk) and np.array_equal(bits(vp[-n:]), rv)
+    assert not kp[-2 * n:-n].any() and not w[-2 * n:-n].any() and ws.get_error() == 0
