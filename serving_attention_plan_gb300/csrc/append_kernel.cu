@@ -71,9 +71,9 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtasPerSm) append_kerne
   __shared__ long long place[2][kTok];  // element offset of KV head 0 in the pages, -1: no slot
   wait_prior_grid();
   const PageView& pv = p.pv;
-  const int batch = __ldg(pv.header + H_BATCH);
+  const GeoHead plan = load_head(pv.geo);
+  const int batch = plan.batch, total = plan.total_q;
   if (batch == 0) return;
-  const int total = __ldg(&pv.geo[batch].q0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = threadIdx.x / kRowLanes, l = threadIdx.x % kRowLanes;
   const int half = p.rotary >> 1;  // frequencies

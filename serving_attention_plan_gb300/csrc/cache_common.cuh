@@ -55,6 +55,12 @@ __device__ __forceinline__ Geo load_geo(const Geo* geo, int r) {
   return Geo{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 
+__device__ __forceinline__ GeoHead load_head(const Geo* geo) {
+  const int4 a = __ldg(reinterpret_cast<const int4*>(geo) - 2);
+  const int4 b = __ldg(reinterpret_cast<const int4*>(geo) - 1);
+  return GeoHead{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+}
+
 // Page id and slot of key j of the request whose page list starts at kv0; false (with the error bit
 // set) for a page outside the pool.
 __device__ __forceinline__ bool locate(const PageView& pv, int kv0, int j, int& page, int& slot) {

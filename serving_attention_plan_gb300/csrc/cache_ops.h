@@ -17,8 +17,17 @@ struct Geo {
   int32_t blk0;      // 32-key blocks of the requests before this one
   int32_t tile0;     // 256-key tiles of the requests before this one
   int32_t work0;     // tensor-core weights: Q tiles (over all KV heads) of the requests before this one
-  int32_t window;    // entry [batch]: the sliding window that work0 was counted with (-1: none)
+  int32_t pad;
 };
+// The plan as a whole, in the place before the first entry: one load gives a kernel all of it.
+struct GeoHead {
+  int32_t batch, total_q;
+  int32_t blocks;          // 32-key blocks
+  int32_t work;            // Q tiles of the tensor-core weights, 0 if they were not counted
+  int32_t causal, window;  // the window that work was counted with (-1: none)
+  int32_t pad0, pad1;
+};
+static_assert(sizeof(Geo) == 32 && sizeof(GeoHead) == sizeof(Geo), "one sector each");
 constexpr int kBlkKeys = 32;
 constexpr int kTileKeys = 256;
 constexpr int kWeightTileRows = 128;  // query rows of a Q tile of the tensor-core weights
@@ -63,8 +72,7 @@ int check_tails_once(const Geo* geo, const int32_t* kv_indices, int batch, int p
 uint64_t turns_fraction(double inv_freq);
 
 struct PageView {  // the plan and the page pool, as every cache operator sees them
-  const Geo* geo;
-  const int32_t* header;
+  const Geo* geo;  // a GeoHead lies before the first entry
   const int32_t* kv_indices;
   int32_t* err;
   int num_pages, page_size;

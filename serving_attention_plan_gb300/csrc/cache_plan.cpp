@@ -39,10 +39,7 @@ void fill_work(Geo* geo, int batch, int hkv, int tile_tokens, bool causal, int w
   int64_t work = 0;
   for (int i = 0; i <= batch; ++i) {
     geo[i].work0 = int32_t(work);
-    if (i == batch) {
-      geo[i].window = window;
-      break;
-    }
+    if (i == batch) break;
     int64_t head = 0;
     for (int kt = 0; int64_t(kt) * kTileKeys < geo[i].lkv; ++kt) {
       int t0, tokens, cost;

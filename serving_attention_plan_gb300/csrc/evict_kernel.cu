@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 6) select_ker
   __syncthreads();
   wait_prior_grid();
   const PageView& pv = p.pv;
-  const int batch = __ldg(pv.header + H_BATCH);
+  const int batch = load_head(pv.geo).batch;
   const unsigned nr = cluster_size(), rank = cluster_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rows = batch * pv.hkv;
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kCmpThreads, 2) compact_kernel(const __grid_co
   constexpr int kRowsPass = kCmpThreads / kLanes;  // rows one piece of all threads covers
   constexpr int kRowsStep = kRowsPass * kCmpVecs;
   static_assert(kRowsStep <= kCmpThreads, "one thread looks a row up");
-  const int batch = __ldg(pv.header + H_BATCH);
+  const int batch = load_head(pv.geo).batch;
   const unsigned nr = cluster_size(), rank = cluster_rank();
   const int sub = threadIdx.x / kLanes, l = threadIdx.x % kLanes;
   const int kinds = p.weights ? 3 : 2;

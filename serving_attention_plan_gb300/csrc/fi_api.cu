@@ -70,7 +70,7 @@ struct fi_workspace {
   int64_t plan_nnz = 0;
   int32_t plan_total_q = 0;
 
-  // the cache operators' view of the plan: geo entries (also in hbuf) and what the host checks of them
+  // the cache operators' view of the plan: the GeoHead and Geo entries (also in hbuf) and what the host checks of them
   fi::GeoTotals geo;
   int64_t plan_nnz_shared = 0;  // entries of a composable plan's shared page list
   signed char pages_once = 0;   // every page listed once: 1 yes, -1 no, 0 not yet checked
@@ -110,12 +110,15 @@ int launch_decode(int grid, const fi::DecodeParams& p, cudaStream_t stream, bool
 // The requests of the (per-request) plan as the cache operators read them, into the pinned mirror.
 void set_geo(fi_workspace* ws, const int32_t* qo_indptr, const int32_t* kv_indptr, const int32_t* last_page_len,
              int batch, int page_size, int path, int causal) {
-  ws->geo = fi::fill_geo(qo_indptr, kv_indptr, last_page_len, batch, page_size,
-                         reinterpret_cast<fi::Geo*>(ws->hbuf + ws->off_geo));
+  fi::Geo* geo = reinterpret_cast<fi::Geo*>(ws->hbuf + ws->off_geo) + 1;
+  ws->geo = fi::fill_geo(qo_indptr, kv_indptr, last_page_len, batch, page_size, geo);
   const int group = ws->hqo / ws->hkv;
+  const int window = std::min(ws->variant.window_left, 1 << 30);  // no request has more keys
   if (path == fi::kPathTensor && group <= fi::kWeightTileRows)
-    fi::fill_work(reinterpret_cast<fi::Geo*>(ws->hbuf + ws->off_geo), batch, ws->hkv, fi::kWeightTileRows / group,
-                  causal != 0, std::min(ws->variant.window_left, 1 << 30), &ws->geo);  // no request has more keys
+    fi::fill_work(geo, batch, ws->hkv, fi::kWeightTileRows / group, causal != 0, window, &ws->geo);
+  const fi::GeoHead head = {batch, qo_indptr[batch], int32_t(ws->geo.blocks), ws->geo.work_ok ? geo[batch].work0 : 0,
+                            causal, window, 0, 0};
+  std::memcpy(geo - 1, &head, sizeof(head));
   ws->pages_once = ws->tails_once = 0;
 }
 
@@ -134,7 +137,7 @@ int check_pages_once(fi_workspace* ws) {
 
 int check_tails_once(fi_workspace* ws) {
   if (ws->tails_once == 0) {
-    const int st = fi::check_tails_once(reinterpret_cast<const fi::Geo*>(ws->hbuf + ws->off_geo),
+    const int st = fi::check_tails_once(reinterpret_cast<const fi::Geo*>(ws->hbuf + ws->off_geo) + 1,
                                         reinterpret_cast<const int32_t*>(ws->hbuf + ws->off_kv),
                                         ws->header[fi::H_BATCH], ws->header[fi::H_PAGE_SIZE],
                                         reinterpret_cast<const int32_t*>(ws->hbuf + ws->off_a_kv),
@@ -164,8 +167,7 @@ fi::PageView page_view(const fi_workspace* ws, int num_pages) {
   char* d = ws->dbuf;
   const int ps = ws->header[fi::H_PAGE_SIZE];
   const bool nhd = ws->plan_variant.kv_layout == FI_KV_LAYOUT_NHD;
-  v.geo = reinterpret_cast<const fi::Geo*>(d + ws->off_geo);
-  v.header = reinterpret_cast<const int32_t*>(d + ws->off_header);
+  v.geo = reinterpret_cast<const fi::Geo*>(d + ws->off_geo) + 1;
   v.kv_indices = reinterpret_cast<const int32_t*>(d + ws->off_kv);
   v.err = reinterpret_cast<int32_t*>(d + ws->off_err);
   v.num_pages = num_pages;
@@ -247,7 +249,7 @@ int fi_workspace_create(int max_batch, int max_total_q, int max_kv_pages, int nu
   };
   ws->off_header = seg(sizeof(int32_t) * fi::kHeaderLen);
   ws->off_cta = seg(sizeof(int32_t) * (ws->max_ctas + 1));
-  ws->off_geo = seg(sizeof(fi::Geo) * (size_t(max_batch) + 1));
+  ws->off_geo = seg(sizeof(fi::Geo) * (size_t(max_batch) + 2));
   ws->off_items = seg(sizeof(int32_t) * fi::kItemFields * ws->max_items);
   ws->off_units = seg(sizeof(int32_t) * fi::kUnitFields * ws->max_units);
   ws->off_slot_unit = seg(sizeof(int32_t) * ws->max_slots);
@@ -374,7 +376,7 @@ int fi_plan(fi_workspace* ws, const int32_t* qo_indptr, const int32_t* kv_indptr
   } segs[] = {
       {ws->off_header, sizeof(plan.header)},
       {ws->off_cta, plan.cta_indptr.size() * sizeof(int32_t)},
-      {ws->off_geo, (size_t(batch) + 1) * sizeof(fi::Geo)},
+      {ws->off_geo, (size_t(batch) + 2) * sizeof(fi::Geo)},
       {ws->off_items, plan.items.size() * sizeof(int32_t)},
       {ws->off_units, plan.units.size() * sizeof(int32_t)},
       {ws->off_slot_unit, plan.slot_unit.size() * sizeof(int32_t)},
@@ -470,7 +472,7 @@ int fi_plan_composable(fi_workspace* ws, const int32_t* shared_qo_indptr, const 
   } segs[] = {
       {ws->off_header, pb.header, sizeof(pb.header)},
       {ws->off_cta, pb.cta_indptr.data(), pb.cta_indptr.size() * sizeof(int32_t)},
-      {ws->off_geo, nullptr, (size_t(batch) + 1) * sizeof(fi::Geo)},  // already in the mirror
+      {ws->off_geo, nullptr, (size_t(batch) + 2) * sizeof(fi::Geo)},  // already in the mirror
       {ws->off_items, pb.items.data(), pb.items.size() * sizeof(int32_t)},
       {ws->off_units, pb.units.data(), pb.units.size() * sizeof(int32_t)},
       {ws->off_slot_unit, pb.slot_unit.data(), pb.slot_unit.size() * sizeof(int32_t)},

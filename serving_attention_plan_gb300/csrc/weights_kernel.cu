@@ -96,12 +96,13 @@ __global__ void __launch_bounds__(32 * kRowsWarps<kFp8>, 1) weights_rows_kernel(
   constexpr int kS = kAhead<kFp8>, kP = kPieces<kFp8>, kW = kRowsWarps<kFp8>;
   wait_prior_grid();
   const PageView& pv = p.pv;
-  const int batch = __ldg(pv.header + H_BATCH);
+  const GeoHead plan = load_head(pv.geo);
+  const int batch = plan.batch;
   if (batch == 0) return;
-  const bool causal = __ldg(pv.header + H_CAUSAL) != 0;
+  const bool causal = plan.causal != 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, t = lane & 3;
   // this CTA's run of (block, KV head) units, heads fastest; its warps take them in turn
-  const long long units = (long long)__ldg(&pv.geo[batch].blk0) * pv.hkv;
+  const long long units = (long long)plan.blocks * pv.hkv;
   const long long begin = units * blockIdx.x / gridDim.x, end = units * (blockIdx.x + 1) / gridDim.x;
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
   const uint8_t* pages = static_cast<const uint8_t*>(p.k_pages);

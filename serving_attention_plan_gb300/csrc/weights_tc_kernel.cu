@@ -87,13 +87,14 @@ struct Walk {
     item(p, causal, g, kt, t0, tokens, cost);
     q1 = min(cost, q0 + end - pos);
   }
-  __device__ void init(const WeightsParams& p, bool causal, int batch, int begin, int finish) {
+  __device__ void init(const WeightsParams& p, const GeoHead& plan, int begin, int finish) {
+    const bool causal = plan.causal != 0;
     const int lane = threadIdx.x & 31;
-    win = __ldg(&p.pv.geo[batch].window);
+    win = plan.window;
     pos = begin;
     end = finish;
     if (pos >= end) return;
-    r = find_request(p.pv.geo, batch, &Geo::work0, pos);
+    r = find_request(p.pv.geo, plan.batch, &Geo::work0, pos);
     load(p);
     const int per_head = (work1 - g.work0) / p.pv.hkv;
     int rem = pos - g.work0;
@@ -592,15 +593,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc::fence_after_sync();
   wait_prior_grid();
   const uint32_t tmem = sm.tmem_base;
-  const int batch = __ldg(p.pv.header + H_BATCH);
-  const bool causal = __ldg(p.pv.header + H_CAUSAL) != 0;
-  const int line = __ldg(&p.pv.geo[batch].work0);
+  const GeoHead plan = load_head(p.pv.geo);
+  const bool causal = plan.causal != 0;
+  const int line = plan.work;
   const int ctas = min(int(gridDim.x), line);
   if ((tmem & 0xFFFFu) + kTmemCols > 512u || (smem_u32(smem_raw) & 1023u) != 0) {
     if (threadIdx.x == 0) atomicOr(p.pv.err, FI_DEVERR_TMEM);
   } else if (int(blockIdx.x) < ctas) {
     Walk w;
-    w.init(p, causal, batch, int((long long)line * blockIdx.x / ctas), int((long long)line * (blockIdx.x + 1) / ctas));
+    w.init(p, plan, int((long long)line * blockIdx.x / ctas), int((long long)line * (blockIdx.x + 1) / ctas));
     if (warp < 16) {
       if (threadIdx.x == 0) {
         sm.walk = w;
