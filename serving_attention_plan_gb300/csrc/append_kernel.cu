@@ -9,8 +9,8 @@
 // two halves of a rotated pair lie in one lane: piece l and piece l + rotary / 16.  The norm is three
 // shuffles, the rotation none, and all arithmetic is packed two by two.  (With 16 lanes of one piece, the
 // partner's values fetched by shuffles, the issue slots bound it: 250 us for 26 K tokens of 32/8
-// heads, now 125: 5.1 TB/s, 0.76 of the copy rate.  Norm and rotation are 6 % of that; more passes in flight, more or fewer
-// warps, a warp for each token and other token orders changed nothing.)  The angles of a token are computed once, by the warp that also finds its page slot,
+// heads.  With one pass in flight in registers each pass waited for its own load: 125 us; now 110, 5.8 TB/s,
+// 0.86 of the copy rate, and 4 % less without norm and rotation.)  The angles of a token are computed once, by the warp that also finds its page slot,
 // one step ahead of the rows, and shared by all its heads through shared memory.
 //
 // Angles: a position times a frequency is taken in turns as a 64-bit fraction, p * F mod 2^64 with
@@ -20,6 +20,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "cache_common.cuh"
 #include "prefill_launch.h"
@@ -29,8 +30,10 @@ namespace {
 
 constexpr int kAppendThreads = 256;
 constexpr int kRowLanes = 8;
-constexpr int kRowsPass = kAppendThreads / kRowLanes;  // rows of a pass; the next pass is in flight meanwhile
-constexpr int kAppendCtasPerSm = 3;
+constexpr int kAppendCtasPerSm = 2;
+// Passes in flight of a group: 96 KB a CTA for warps, a decode token's two or three for a whole CTA.
+template <int kGroup>
+constexpr int kPassesAhead = kGroup == 32 ? 12 : 3;
 
 __device__ __forceinline__ void unpack8(uint4 w, float2 (&x)[4]) {
   x[0] = bf16x2_to_f2(w.x);
@@ -61,50 +64,81 @@ __device__ __forceinline__ void put8(void* pages, long long off, const float2 (&
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(pages) + off) = pack8(x);
 }
 
-// A step is kTok tokens: four for long batches (the sync and the search for the request are paid once for four
-// tokens), one for decode steps, where tokens are few and each CTA should take one.
-template <int kTok, bool kFp8>
+// Threads work in groups that take one token at a time: a warp for long batches, the whole CTA for decode steps,
+// where tokens are few and a token's rows should go side by side.  A pass of a group is kGroup / 8 rows;
+// kPassesAhead passes are in flight, across tokens, each lane's own 32 bytes of them by asynchronous copies
+// into a ring of its own (in registers the ring spilled, and a spill waits for its load).
+template <int kGroup, bool kFp8>
 __global__ void __launch_bounds__(kAppendThreads, kAppendCtasPerSm) append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int kGroups = kAppendThreads / kGroup, kRowsPass = kGroup / kRowLanes, kDepth = kPassesAhead<kGroup>;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  uint4(*ring)[2][kAppendThreads] = reinterpret_cast<uint4(*)[2][kAppendThreads]>(smem_raw);  // [kDepth]
   // cos and sin of a token's frequencies: piece k of a split half holds frequencies 8 k .. 8 k + 7, its first
   // four at [k], the others at [8 + k], so the lanes' 16-byte reads fall into different banks; interleaved
   // pairs are in order, piece k holds [k]
-  __shared__ float4 cosines[2][kTok][16], sines[2][kTok][16];
-  __shared__ long long place[2][kTok];  // element offset of KV head 0 in the pages, -1: no slot
+  __shared__ float4 cosines[kGroups][2][16], sines[kGroups][2][16];
+  __shared__ long long place[kGroups][2];  // element offset of KV head 0 in the pages, -1: no slot
+  __shared__ uint4 norm_weight[2][16];     // of q and k
   wait_prior_grid();
   const PageView& pv = p.pv;
   const GeoHead plan = load_head(pv.geo);
   const int batch = plan.batch, total = plan.total_q;
   if (batch == 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = threadIdx.x / kRowLanes, l = threadIdx.x % kRowLanes;
+  const int lane = threadIdx.x & 31, l = threadIdx.x % kRowLanes;
+  const int group = threadIdx.x / kGroup, sub = threadIdx.x % kGroup / kRowLanes;
+  const bool leads = threadIdx.x % kGroup < 32;  // the group's first warp looks slots and angles up
+  auto sync = [&]() {
+    if constexpr (kGroup == 32)
+      __syncwarp();
+    else
+      __syncthreads();
+  };
   const int half = p.rotary >> 1;  // frequencies
   const int hp = p.rotary >> 4;    // 16-byte pieces of a rotated half
-  // the lane's two pieces, and whether they rotate (together, or each by itself when interleaved)
-  const int pa = p.interleaved ? l : (l < hp ? l : 2 * hp + 2 * (l - hp));
-  const int pb = p.interleaved ? l + 8 : (l < hp ? l + hp : pa + 1);
-  uint4 wq[2] = {}, wk[2] = {};
-  if (p.q_weight) {
-    wq[0] = __ldg(reinterpret_cast<const uint4*>(p.q_weight) + pa);
-    wq[1] = __ldg(reinterpret_cast<const uint4*>(p.q_weight) + pb);
+  // the lane's two pieces: l and its partner of the other half, or two of the pieces that do not rotate;
+  // interleaved pairs lie inside a piece.  Neighbouring lanes take neighbouring pieces, so that a copy's
+  // 16 bytes a lane make whole sectors.
+  const int pa = p.interleaved || l < hp ? l : hp + l;
+  const int pb = p.interleaved ? l + 8 : (l < hp ? l + hp : l + 8);
+  if (threadIdx.x < 32) {
+    const void* w = threadIdx.x < 16 ? p.q_weight : p.k_weight;
+    if (w) norm_weight[threadIdx.x >> 4][threadIdx.x & 15] = __ldg(static_cast<const uint4*>(w) + (threadIdx.x & 15));
   }
-  if (p.k_weight) {
-    wk[0] = __ldg(reinterpret_cast<const uint4*>(p.k_weight) + pa);
-    wk[1] = __ldg(reinterpret_cast<const uint4*>(p.k_weight) + pb);
-  }
-  // this CTA's run of steps
-  const int steps = (total + kTok - 1) / kTok;
-  const int s0 = int((long long)steps * blockIdx.x / gridDim.x), s1 = int((long long)steps * (blockIdx.x + 1) / gridDim.x);
+  // this group's run of tokens
+  const long long me = (long long)blockIdx.x * kGroups + group, groups = (long long)gridDim.x * kGroups;
+  const int s0 = int(total * me / groups), s1 = int(total * (me + 1) / groups);
+
+  const int heads = p.hqo + 2 * pv.hkv;  // rows of a token: q, k, v
+  int f_tok = s0, f_row = sub;  // what is fetched next
+  auto fetch = [&](int slot) {
+    const bool on = f_tok < s1 && f_row < heads;
+    const long long tok = on ? f_tok : 0;
+    const int row = on ? f_row : 0;
+    const __nv_bfloat16* at = static_cast<const __nv_bfloat16*>(p.q) + tok * p.q_stride + row * kHeadDim;
+    if (row >= p.hqo) at = static_cast<const __nv_bfloat16*>(p.k) + tok * p.k_stride + (row - p.hqo) * kHeadDim;
+    if (row >= p.hqo + pv.hkv)
+      at = static_cast<const __nv_bfloat16*>(p.v) + tok * p.v_stride + (row - p.hqo - pv.hkv) * kHeadDim;
+    cp_async_16_or_none(&ring[slot][0][threadIdx.x], at + 8 * pa, on);
+    cp_async_16_or_none(&ring[slot][1][threadIdx.x], at + 8 * pb, on);
+    cp_async_commit();
+    f_row += kRowsPass;
+    if (f_row - sub >= heads) {
+      f_row = sub;
+      ++f_tok;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kDepth; ++i) fetch(i);
 
   uint64_t f0 = 0, f1 = 0;  // the lane's two frequencies
-  if (warp < kTok) {
+  if (leads) {
     if (lane < half) f0 = p.freq[lane];
     if (lane + 32 < half) f1 = p.freq[lane + 32];
   }
-  Geo g{};  // the request of the warp's last token
-  // slot and angles of the step's token `warp`, by that warp
-  auto prepare = [&](int step, int par) {
-    const int tok = step * kTok + warp;
-    if (step >= s1 || tok >= total) return;
+  Geo g{};  // the request of the last token
+  // slot and angles of a token, by the group's first warp
+  auto prepare = [&](int tok, int par) {
+    if (tok >= s1) return;
     if (tok < g.q0 || tok >= g.q0 + g.lq) g = load_geo(pv.geo, find_request(pv.geo, batch, &Geo::q0, tok));
     const int j = g.lkv - g.lq + tok - g.q0;
     const int pos = p.positions ? __ldg(p.positions + tok) : j;
@@ -112,10 +146,10 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtasPerSm) append_kerne
       long long off = -1;
       int page, slot;
       if (j >= 0 && locate(pv, g.kv0, j, page, slot)) off = kv_offset(pv, page, slot, 0);
-      place[par][warp] = off;
+      place[group][par] = off;
     }
-    float* c = reinterpret_cast<float*>(cosines[par][warp]);
-    float* s = reinterpret_cast<float*>(sines[par][warp]);
+    float* c = reinterpret_cast<float*>(cosines[group][par]);
+    float* s = reinterpret_cast<float*>(sines[group][par]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int f = lane + 32 * i;
@@ -129,48 +163,27 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtasPerSm) append_kerne
       }
     }
   };
-  if (warp < kTok) prepare(s0, 0);
+  if (leads) prepare(s0, 0);
+  __syncthreads();  // the norm weights
 
-  const int heads = p.hqo + 2 * pv.hkv;  // rows of a token: q, k, v
-  uint4 next[2];
-  int next_t = 0, next_h = -1;  // row of the step that `next` holds, -1: none
-  auto load = [&](int step, int row) {
-    next_h = -1;
-    const int base = step * kTok;
-    if (step >= s1 || row >= min(kTok, total - base) * heads) return;
-    next_t = kTok == 1 ? 0 : int(__umulhi(unsigned(row), p.heads_inv));
-    next_h = row - next_t * heads;
-    const long long tok = base + next_t;
-    const __nv_bfloat16* at;
-    if (next_h < p.hqo)
-      at = static_cast<const __nv_bfloat16*>(p.q) + tok * p.q_stride + next_h * kHeadDim;
-    else if (next_h < p.hqo + pv.hkv)
-      at = static_cast<const __nv_bfloat16*>(p.k) + tok * p.k_stride + (next_h - p.hqo) * kHeadDim;
-    else
-      at = static_cast<const __nv_bfloat16*>(p.v) + tok * p.v_stride + (next_h - p.hqo - pv.hkv) * kHeadDim;
-    next[0] = __ldcs(reinterpret_cast<const uint4*>(at) + pa);
-    next[1] = __ldcs(reinterpret_cast<const uint4*>(at) + pb);
-  };
-  load(s0, sub);
-  int par = 0;
-  for (int step = s0; step < s1; ++step, par ^= 1) {
-    const int base = step * kTok, rows = min(kTok, total - base) * heads;
-    __syncthreads();
-    if (warp < kTok) prepare(step + 1, par ^ 1);
-    for (int row = sub; row - sub < rows; row += kRowsPass) {
-      const uint4 raw[2] = {next[0], next[1]};
-      const int t = next_t, h = next_h;
-      if (row - sub + kRowsPass < rows)
-        load(step, row + kRowsPass);
-      else
-        load(step + 1, sub);
-      if (h < 0) continue;
+  int par = 0, slot = 0;
+  for (int tok = s0; tok < s1; ++tok, par ^= 1) {
+    sync();
+    if (leads) prepare(tok + 1, par ^ 1);
+    const float4 *cosine = cosines[group][par], *sine = sines[group][par];
+    const long long off0 = place[group][par];
+    for (int h = sub; h - sub < heads; h += kRowsPass) {
+      cp_async_wait<kDepth - 1>();
+      const uint4 raw[2] = {ring[slot][0][threadIdx.x], ring[slot][1][threadIdx.x]};
+      fetch(slot);
+      slot = slot + 1 == kDepth ? 0 : slot + 1;
+      if (h >= heads) continue;
       float2 a[4], b[4];
       unpack8(raw[0], a);
       unpack8(raw[1], b);
       if (h >= p.hqo + pv.hkv) {  // v: as it is
-        if (place[par][t] < 0) continue;
-        const long long off = place[par][t] + (h - p.hqo - pv.hkv) * pv.head_stride;
+        if (off0 < 0) continue;
+        const long long off = off0 + (h - p.hqo - pv.hkv) * pv.head_stride;
         if constexpr (kFp8) {
           put8<true>(p.v_pages, off + 8 * pa, a, p.v_inv_scale);
           put8<true>(p.v_pages, off + 8 * pb, b, p.v_inv_scale);
@@ -193,17 +206,17 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtasPerSm) append_kerne
         for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(mates, ss, o);
         const float inv = rsqrtf(fmaf(ss, 1.f / kHeadDim, p.eps));
         const float2 i2 = make_float2(inv, inv);
-        unpack8(is_q ? wq[0] : wk[0], w);
+        unpack8(norm_weight[is_q ? 0 : 1][pa], w);
 #pragma unroll
         for (int e = 0; e < 4; ++e) a[e] = __fmul2_rn(__fmul2_rn(a[e], i2), w[e]);
-        unpack8(is_q ? wq[1] : wk[1], w);
+        unpack8(norm_weight[is_q ? 0 : 1][pb], w);
 #pragma unroll
         for (int e = 0; e < 4; ++e) b[e] = __fmul2_rn(__fmul2_rn(b[e], i2), w[e]);
       }
       if (p.interleaved) {
         auto turn = [&](float2 (&x)[4], int piece) {
           if (piece >= 2 * hp) return;
-          const float4 c = cosines[par][t][piece], s = sines[par][t][piece];
+          const float4 c = cosine[piece], s = sine[piece];
           const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -214,7 +227,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtasPerSm) append_kerne
       } else if (l < hp) {
 #pragma unroll
         for (int e2 = 0; e2 < 2; ++e2) {
-          const float4 c = cosines[par][t][8 * e2 + l], s = sines[par][t][8 * e2 + l];
+          const float4 c = cosine[8 * e2 + l], s = sine[8 * e2 + l];
           const float2 cc[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)};
           const float2 sn[2] = {make_float2(s.x, s.y), make_float2(s.z, s.w)};
 #pragma unroll
@@ -228,32 +241,39 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtasPerSm) append_kerne
       }
       if (is_q) {
         uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.q_out) +
-                                              ((long long)(base + t) * p.hqo + h) * kHeadDim);
+                                              ((long long)tok * p.hqo + h) * kHeadDim);
         dst[pa] = pack8(a);
         dst[pb] = pack8(b);
-      } else if (place[par][t] >= 0) {
-        const long long off = place[par][t] + (h - p.hqo) * pv.head_stride;
+      } else if (off0 >= 0) {
+        const long long off = off0 + (h - p.hqo) * pv.head_stride;
         put8<kFp8>(p.k_pages, off + 8 * pa, a, p.k_inv_scale);
         put8<kFp8>(p.k_pages, off + 8 * pb, b, p.k_inv_scale);
       }
     }
   }
+  cp_async_wait<0>();
 }
 
 }  // namespace
 
-int launch_append(AppendParams p, int total_q, bool fp8, int num_sms, cudaStream_t stream) {
-  const bool many = total_q >= 8 * num_sms;
-  const unsigned grid = unsigned(many ? std::min((total_q + 3) / 4, kAppendCtasPerSm * num_sms) : total_q);
-  const unsigned heads = unsigned(p.hqo + 2 * p.pv.hkv);
-  p.heads_inv = unsigned(((1ull << 32) + heads - 1) / heads);  // division by a high product: exact below 2^32 / heads
-  cudaError_t e;
-  if (many)
-    e = fp8 ? launch_dependent(append_kernel<4, true>, grid, kAppendThreads, 0, 1, stream, p)
-            : launch_dependent(append_kernel<4, false>, grid, kAppendThreads, 0, 1, stream, p);
-  else
-    e = fp8 ? launch_dependent(append_kernel<1, true>, grid, kAppendThreads, 0, 1, stream, p)
-            : launch_dependent(append_kernel<1, false>, grid, kAppendThreads, 0, 1, stream, p);
+int launch_append(const AppendParams& p, int total_q, bool fp8, int num_sms, cudaStream_t stream) {
+  using Kernel = void (*)(const AppendParams);
+  static const Kernel kernels[4] = {append_kernel<kAppendThreads, false>, append_kernel<kAppendThreads, true>,
+                                    append_kernel<32, false>, append_kernel<32, true>};
+  constexpr size_t ring = sizeof(uint4) * 2 * kAppendThreads;  // of one pass
+  const size_t smem[2] = {ring * kPassesAhead<kAppendThreads>, ring * kPassesAhead<32>};
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  std::call_once(once, [&] {
+    for (int i = 0; i < 4 && attr == cudaSuccess; ++i)
+      attr = cudaFuncSetAttribute(kernels[i], cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem[i / 2]));
+  });
+  if (attr != cudaSuccess) return record_cuda_error(attr, "cudaFuncSetAttribute(append_kernel)");
+  // a warp for each token once they fill the grid's warps
+  const int ctas = kAppendCtasPerSm * num_sms;
+  const bool many = total_q >= ctas * (kAppendThreads / 32);
+  const cudaError_t e = launch_dependent(kernels[(many ? 2 : 0) + (fp8 ? 1 : 0)], unsigned(std::min(total_q, ctas)),
+                                         kAppendThreads, smem[many ? 1 : 0], 1, stream, p);
   return e == cudaSuccess ? 0 : record_cuda_error(e, "append_kernel launch");
 }
 

@@ -95,10 +95,9 @@ struct AppendParams {
   int hqo;
   int rotary;       // rotated dims: a multiple of 16, 0 for none
   int interleaved;  // pairs (2j, 2j + 1) instead of (j, j + rotary / 2)
-  unsigned heads_inv;  // 2^32 / (q, k and v heads), rounded up; set by the launcher
   uint64_t freq[kMaxFreqs];  // revolutions per position, as a 64-bit fraction of a turn
 };
-int launch_append(AppendParams p, int total_q, bool fp8, int num_sms, cudaStream_t stream);
+int launch_append(const AppendParams& p, int total_q, bool fp8, int num_sms, cudaStream_t stream);
 
 struct WeightsParams {
   PageView pv;
