@@ -773,3 +773,73 @@ def test_pool_beyond_32_bit_offsets(lq, causal):
     rk[page, :, slot], rv[page, :, slot] = bits(x)[tok], bits(x)[tok]
     assert np.array_equal(bits(kp[-n:]), rk) and np.array_equal(bits(vp[-n:]), rv)
     assert not kp[-2 * n:-n].any() and not w[-2 * n:-n].any() and ws.get_error() == 0
+
+
+def test_c_entry_refusals():
+    """Misaligned pointers, narrow or odd strides, null pointers and a workspace of another shape, at the C entry."""
+    from serving_attention_plan_gb300 import binding as B
+    torch = torch_mod()
+    L = B.lib()
+    b = batch_of([2, 1], [20, 30], 4, 2, 4)
+    ws = workspace(b)
+    n = b.num_pages
+    q, kp = bf16(b.q), bf16(b.k_pages)
+    x = torch.zeros(3, 2, 128, device="cuda", dtype=torch.bfloat16)
+    w, lse = torch.zeros(n, 2, 4, device="cuda"), torch.zeros(3, 4, device="cuda")
+    kept = torch.zeros(2, 2, 8, device="cuda", dtype=torch.int32)
+    h, s = ws._h, torch.cuda.current_stream().cuda_stream
+    P = {k: t.data_ptr() for k, t in dict(q=q, x=x, kp=kp, w=w, lse=lse, kept=kept).items()}
+
+    def append(q=P["q"], sq=512, k=P["x"], sk=256, v=P["x"], sv=256, wq=None, wk=None, eps=0.0, pos=None, out=P["q"],
+               kp=P["kp"], vp=P["kp"], pages=n):
+        return L.fi_append(h, q, sq, k, sk, v, sv, wq, wk, eps, pos, out, kp, vp, pages, s)
+
+    for bad in (dict(q=P["q"] + 2), dict(k=P["x"] + 8), dict(v=None), dict(q=None), dict(out=None), dict(out=P["q"] + 4), dict(kp=None),
+                dict(vp=P["kp"] + 2), dict(sq=511), dict(sq=516), dict(sk=128), dict(sv=260), dict(wq=P["x"] + 2), dict(pos=P["lse"] + 1),
+                dict(eps=float("inf")), dict(pages=-1), dict(pages=int(b.kv_indices.max()))):
+        assert append(**bad) == 1, bad
+    weights = lambda q=P["q"], k=P["kp"], pages=n, lse=P["lse"], decay=1.0, new=1, w=P["w"]: L.fi_key_weights(h, q, k, pages, lse, decay, new, w, s)
+    for bad in (dict(q=None), dict(q=P["q"] + 2), dict(k=None), dict(k=P["kp"] + 8), dict(lse=None), dict(lse=P["lse"] + 2), dict(w=None),
+                dict(w=P["w"] + 1), dict(decay=-0.1), dict(new=2), dict(pages=0)):
+        assert weights(**bad) == 1, bad
+    select = lambda w=P["w"], pages=n, sink=1, recent=2, budget=8, kept=P["kept"]: L.fi_select_keys(h, w, pages, sink, recent, budget, kept, s)
+    for bad in (dict(w=None), dict(w=P["w"] + 2), dict(kept=None), dict(kept=P["kept"] + 2), dict(budget=0), dict(sink=-1), dict(recent=8),
+                dict(sink=2**31 - 1, recent=2**31 - 1), dict(pages=1)):
+        assert select(**bad) == 1, bad
+    compact = lambda kept=P["kept"], budget=8, k=P["kp"], v=P["kp"], w=None, pages=n: L.fi_compact(h, kept, budget, k, v, w, pages, s)
+    for bad in (dict(kept=None), dict(kept=P["kept"] + 1), dict(budget=0), dict(k=None), dict(v=None), dict(k=P["kp"] + 4), dict(w=P["w"] + 3), dict(pages=2)):
+        assert compact(**bad) == 1, bad
+    # more rows than the kernels number in 32 bits
+    assert append(pages=2**31 - 1) == 3 and select(pages=2**30) == 3
+    torch.cuda.synchronize()
+    assert np.array_equal(bits(kp), b.k_pages) and np.array_equal(bits(q), b.q) and ws.get_error() == 0
+
+
+def test_two_workspaces_at_once():
+    """Prompts on one stream and a decode batch on another, each with its own workspace, launched without waiting."""
+    torch = torch_mod()
+    jobs = []
+    for seed, (lq, lkv) in enumerate([([700, 300], [900, 300]), ([1] * 40, list(range(50, 850, 20)))]):
+        b = batch_of(lq, lkv, 16, 4, 16, True, seed=seed)
+        q = A.bf16_to_f64(b.q)
+        lse = lse_of(b, q, b.k_pages, 1.0, -1, 0.0, "HND")
+        jobs.append((workspace(b), bf16(b.q), bf16(b.k_pages), dev(lse), b, q, lse, torch.cuda.Stream()))
+    alone = []
+    for ws, q, k, lse, b, *_ in jobs:
+        w = torch.zeros(b.num_pages, 4, 16, device="cuda")
+        for _ in range(8):
+            ws.key_weights(q, k, lse, w, 1.0, False)
+        alone.append(w)
+    torch.cuda.synchronize()
+    both = [torch.zeros_like(w) for w in alone]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for (ws, q, k, lse, b, _, _, stream), w in zip(jobs, both):
+            ws.key_weights(q, k, lse, w, 1.0, False, stream=stream)
+    torch.cuda.synchronize()
+    for (ws, *_), w, ref in zip(jobs, both, alone):
+        assert torch.equal(w, ref) and ws.get_error() == 0
+    for (_, _, _, _, b, q, lse, _), w in zip(jobs, both):
+        one, reach = C.key_weights(b, q, b.k_pages, lse, np.zeros(w.shape), 1.0, False)
+        tol = weights_tol(reach, lse) + (2800 + 8) * 2.0 ** -24
+        assert (np.abs(w.cpu().numpy() - 8 * one) <= 8 * one * tol + 1e-30).all()
