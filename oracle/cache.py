@@ -104,11 +104,12 @@ def select(batch, weights, budget, recent, sink):
                 continue
             page, slot = places(batch, i, np.arange(n))
             w = weights[page, h, slot].astype(np.float64)
-            free = list(range(sink, n - recent))
+            free = np.arange(sink, n - recent)
             # the largest first (NaN before everything), then the lowest position
-            free.sort(key=lambda j: (0 if np.isnan(w[j]) else 1, -w[j] if not np.isnan(w[j]) else 0.0, j))
-            chosen = set(range(sink)) | set(range(n - recent, n)) | set(free[:budget - sink - recent])
-            kept[i, h] = sorted(chosen)
+            nan = np.isnan(w[free])
+            order = np.lexsort((free, np.where(nan, 0.0, -w[free]), ~nan))
+            best = free[order[:budget - sink - recent]]
+            kept[i, h] = np.sort(np.concatenate([np.arange(sink), best, np.arange(n - recent, n)]))
     return kept
 
 

@@ -562,8 +562,12 @@ __global__ void __launch_bounds__(kCmpThreads, 2) compact_kernel(const __grid_co
 int launch_select(SelectParams p, int batch, int max_lkv, int num_sms, cudaStream_t stream) {
   const int rows = batch * p.pv.hkv;
   p.by_four = p.pv.page_size % 4 == 0 && reinterpret_cast<uintptr_t>(p.weights) % 16 == 0;
+  // a cluster shares a row while there are SMs for it (131 K keys of 8 heads: 8 CTAs 17 us), or as long as a slice does
+  // not fit into shared memory and would be read again in each pass (16 x 8 rows of 100 K keys: 81 us, 121 without)
   unsigned cluster = 1;
-  while (cluster < 8 && rows * int(cluster) * 2 <= num_sms && max_lkv / int(cluster) > 4096) cluster *= 2;
+  while (cluster < 8 && ((int64_t(rows) * cluster * 2 <= num_sms && max_lkv / int(cluster) > 4096) ||
+                         max_lkv / int(cluster) > 48 * 1024 - 64))
+    cluster *= 2;
   const int64_t want = (int64_t(max_lkv) / cluster + 64 + 31) / 32 * 32;
   const int cap = int(std::min<int64_t>(want, 48 * 1024));
   const size_t smem = size_t(cap) * 4;

@@ -290,6 +290,7 @@ SELECT = [
     ([40001, 12], 3, 1, 20000, 100, 4, "ties", 0),
     ([300000], 1, 64, 1000, 10, 4, "random", 0),          # slices longer than shared memory at 8 CTAs: 37.5 K each
     ([450000], 1, 128, 400, 0, 0, "ties", 0),             # 56 K keys a slice: read again from memory
+    ([60000, 100, 59999] * 4, 8, 64, 9000, 64, 4, "random", 0),  # many rows, each too long for one CTA's shared memory
     ([64] * 40, 8, 16, 20, 5, 2, "signs", 2),
     ([777] * 3, 2, 8, 100, 7, 3, "special", 0),
 ]
