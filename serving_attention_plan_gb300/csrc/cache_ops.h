@@ -14,7 +14,7 @@ namespace fi {
 struct Geo {
   int32_t q0, lq;    // first query token, query tokens
   int32_t kv0, lkv;  // first entry in the page list, keys
-  int32_t blk0;      // 32-key blocks of the requests before this one
+  int32_t blk0;      // 32-key blocks of the requests before this one that take the row form of the weights
   int32_t tile0;     // 256-key tiles of the requests before this one
   int32_t work0;     // tensor-core weights: Q tiles (over all KV heads) of the requests before this one
   int32_t pad;
@@ -22,7 +22,7 @@ struct Geo {
 // The plan as a whole, in the place before the first entry: one load gives a kernel all of it.
 struct GeoHead {
   int32_t batch, total_q;
-  int32_t blocks;          // 32-key blocks
+  int32_t blocks;          // 32-key blocks of the row form
   int32_t work;            // Q tiles of the tensor-core weights, 0 if they were not counted
   int32_t causal, window;  // the window that work was counted with (-1: none)
   int32_t pad0, pad1;
@@ -51,7 +51,8 @@ __host__ __device__ inline void weight_item(int lq, int lkv, int kt, bool causal
 
 struct GeoTotals {
   bool ok = false;     // the counts below fit the entries' 32-bit fields
-  int64_t blocks = 0;  // 32-key blocks
+  int64_t blocks = 0;  // 32-key blocks (of the row form, once split)
+  int64_t work = 0;    // Q tiles of the tensor-core form
   int64_t tiles = 0;   // 256-key tiles
   int32_t max_lkv = 0;
   int32_t max_lq = 0;
@@ -60,8 +61,15 @@ struct GeoTotals {
 // The entries [0, batch] of a validated batch (cache_plan.cpp, host only, like the two checks).
 GeoTotals fill_geo(const int32_t* qo_indptr, const int32_t* kv_indptr, const int32_t* last_page_len, int batch,
                    int page_size, Geo* out);
-// The work0 fields of filled entries: Q tiles of the tensor-core weights.
-void fill_work(Geo* geo, int batch, int hkv, int tile_tokens, bool causal, int window, GeoTotals* totals);
+// Splits the requests of filled entries between the two forms of the weights: those of more than row_limit query
+// rows get Q tiles (work0) and no blocks (blk0), the others blocks and no tiles.
+void split_weights(Geo* geo, int batch, int hkv, int group, int row_limit, bool causal, int window, GeoTotals* totals);
+// Query rows (tokens x heads of a group) up to which a request takes the row form in a batch that needs the
+// tensor cores.  Measured, row form against tensor cores, 128 requests of U[64, 4096] keys, 32/8 heads: bf16 16 rows
+// 147 / 359 us, 32 rows 254 / 396, 64 rows 382 / 338, 128 rows 783 / 361; e4m3 32 rows 240 / 695, 64 rows
+// 419 / 661, 128 rows 959 / 776; 4 requests of U[64, 16384], bf16 32 rows 36 / 47, 64 rows 33 / 25.
+constexpr int kRowFormMostBf16 = 32;
+constexpr int kRowFormMostE4m3 = 64;
 // FI_OK if no page id (0 .. max_page) occurs twice in the two lists, else FI_ERR_UNSUPPORTED; FI_ERR_CAPACITY without host memory.
 int check_pages_once(const int32_t* a, int64_t na, const int32_t* b, int64_t nb, int32_t max_page);
 // FI_OK if no page takes new tokens (the last l_q keys of a request) from two places of the list, or while the

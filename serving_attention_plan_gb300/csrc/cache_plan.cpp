@@ -35,20 +35,35 @@ GeoTotals fill_geo(const int32_t* qo_indptr, const int32_t* kv_indptr, const int
   return t;
 }
 
-void fill_work(Geo* geo, int batch, int hkv, int tile_tokens, bool causal, int window, GeoTotals* totals) {
-  int64_t work = 0;
+void split_weights(Geo* geo, int batch, int hkv, int group, int row_limit, bool causal, int window, GeoTotals* totals) {
+  int64_t work = 0, blocks = 0;
   for (int i = 0; i <= batch; ++i) {
     geo[i].work0 = int32_t(work);
+    geo[i].blk0 = int32_t(blocks);
     if (i == batch) break;
+    if (int64_t(geo[i].lq) * group <= row_limit) {
+      blocks += (int64_t(geo[i].lkv) + kBlkKeys - 1) / kBlkKeys;
+      continue;
+    }
     int64_t head = 0;
     for (int kt = 0; int64_t(kt) * kTileKeys < geo[i].lkv; ++kt) {
       int t0, tokens, cost;
-      weight_item(geo[i].lq, geo[i].lkv, kt, causal, window, tile_tokens, &t0, &tokens, &cost);
+      weight_item(geo[i].lq, geo[i].lkv, kt, causal, window, kWeightTileRows / group, &t0, &tokens, &cost);
       head += cost;
     }
     work += head * hkv;
-    if (work > INT32_MAX) return;
+    if (work > INT32_MAX) {  // not with the tensor cores: all requests as they were
+      blocks = 0;
+      for (int k = 0; k <= batch; ++k) {
+        geo[k].work0 = 0;
+        geo[k].blk0 = int32_t(blocks);
+        if (k < batch) blocks += (int64_t(geo[k].lkv) + kBlkKeys - 1) / kBlkKeys;
+      }
+      return;
+    }
   }
+  totals->blocks = blocks;
+  totals->work = work;
   totals->work_ok = true;
 }
 

@@ -115,8 +115,10 @@ void set_geo(fi_workspace* ws, const int32_t* qo_indptr, const int32_t* kv_indpt
   const int group = ws->hqo / ws->hkv;
   const int window = std::min(ws->variant.window_left, 1 << 30);  // no request has more keys
   if (path == fi::kPathTensor && group <= fi::kWeightTileRows)
-    fi::fill_work(geo, batch, ws->hkv, fi::kWeightTileRows / group, causal != 0, window, &ws->geo);
-  const fi::GeoHead head = {batch, qo_indptr[batch], int32_t(ws->geo.blocks), ws->geo.work_ok ? geo[batch].work0 : 0,
+    fi::split_weights(geo, batch, ws->hkv, group,
+                      ws->variant.kv_dtype == FI_KV_DTYPE_E4M3 ? fi::kRowFormMostE4m3 : fi::kRowFormMostBf16,
+                      causal != 0, window, &ws->geo);
+  const fi::GeoHead head = {batch, qo_indptr[batch], int32_t(ws->geo.blocks), int32_t(ws->geo.work),
                             causal, window, 0, 0};
   std::memcpy(geo - 1, &head, sizeof(head));
   ws->pages_once = ws->tails_once = 0;
@@ -843,14 +845,24 @@ int fi_key_weights(fi_workspace* ws, const void* q, const void* k_pages, int num
   p.cap_log2 = var.soft_cap > 0.f ? var.soft_cap * fi::kLog2e : 0.f;
   p.inv_cap_log2 = var.soft_cap > 0.f ? 1.f / p.cap_log2 : 0.f;
   p.window_left = std::min(var.window_left, 1 << 30);  // no request has more keys
-  // more than 8 rows a request: tensor cores (a group of more than 128 heads does not fit their tile)
-  if (ws->header[fi::H_PATH] == fi::kPathTensor && ws->geo.work_ok) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // a batch that needs the tensor cores is split by request (a group of more than 128 heads does not fit their
+  // tile); a captured launch has to serve later plans of the path, so it gets both kernels
+  if (ws->header[fi::H_PATH] == fi::kPathTensor && p.group <= fi::kWeightTileRows) {
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    FI_CUDA(cudaStreamIsCapturing(s, &capture));
+    const bool both = capture != cudaStreamCaptureStatusNone;
     p.tile_tokens = fi::kWeightTileRows / p.group;
     p.part = reinterpret_cast<float*>(ws->dbuf + ws->off_wpart);
     p.part_count = reinterpret_cast<uint32_t*>(ws->dbuf + ws->off_wcount);
-    return fi::launch_weights_tc(p, ws->plan_total_q, fp8, ws->num_sms, static_cast<cudaStream_t>(stream));
+    if (ws->geo.work > 0 || both) {
+      st = fi::launch_weights_tc(p, ws->plan_total_q, fp8, ws->num_sms, s);
+      if (st != FI_OK) return st;
+    }
+    if (ws->geo.blocks == 0 && !both) return FI_OK;
+    return fi::launch_weights_rows(p, fp8, both ? INT32_MAX : ws->geo.blocks, ws->num_sms, s);
   }
-  return fi::launch_weights_rows(p, fp8, ws->geo.blocks, ws->num_sms, static_cast<cudaStream_t>(stream));
+  return fi::launch_weights_rows(p, fp8, ws->geo.blocks, ws->num_sms, s);
 }
 
 int fi_select_keys(fi_workspace* ws, const float* weights, int num_pages, int32_t sink, int32_t recent, int32_t budget,

@@ -165,6 +165,9 @@ WEIGHTS = [
     ([66, 3], [200, 129], 16, 16, 128, False, "e4m3", "NHD", -1, 0.0, 0.9, False, 0),
     ([5, 9], [290, 70], 130, 1, 16, True, "bf16", "HND", -1, 0.0, 1.0, True, 0),   # 130 heads a group
     ([520], [1100], 4, 1, 16, True, "bf16", "HND", -1, 0.0, 1.0, True, 0),
+    # row counts around the limit between the two kernels, in one batch with long ones and empty ones
+    ([8, 9, 1, 0, 300, 7, 2], [700, 70, 513, 40, 400, 7, 1000], 16, 4, 16, True, "bf16", "HND", -1, 0.0, 0.9, True, 0),
+    ([16, 17, 1, 0, 90, 33], [700, 70, 513, 40, 400, 290], 16, 4, 16, True, "e4m3", "NHD", 60, 10.0, 0.9, True, 3),
 ]
 
 
@@ -666,7 +669,8 @@ def test_captured_prompt_weights_follow_a_new_plan():
     from serving_attention_plan_gb300 import binding as B
     first = batch_of([100, 300, 40], [120, 900, 40], 8, 2, 16, True, seed=1, extra=20)
     second = batch_of([440], [1210], 8, 2, 16, True, seed=2, extra=first.num_pages - 76)
-    assert second.num_pages == first.num_pages and second.total_q == first.total_q
+    third = batch_of([400, 39, 1], [500, 600, 100], 8, 2, 16, True, seed=4, extra=first.num_pages - 77)  # both kernels
+    assert second.num_pages == first.num_pages == third.num_pages and second.total_q == first.total_q == third.total_q
     ws = B.Workspace(4, 500, 200, 8, 2)
     side = torch.cuda.Stream()
     q, k = bf16(first.q), bf16(first.k_pages)
@@ -679,7 +683,7 @@ def test_captured_prompt_weights_follow_a_new_plan():
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph, stream=side):
         ws.key_weights(q, k, lse, w, 1.0, True, stream=side)
-    for b in (second, first, second):
+    for b in (second, third, first, third, second):
         plan(b)
         w.zero_()
         want.zero_()
