@@ -397,7 +397,8 @@ int fi_key_weights(fi_workspace* ws, const void* q, const void* k_pages, int num
  *
  * A request of at most `budget` keys keeps all of them.  A longer one keeps its first `sink` keys, its
  * last `recent` keys and, of the others, the budget - sink - recent with the largest weights; equal
- * weights go to the lowest position, NaN counts as the largest.
+ * weights go to the lowest position, NaN counts as the largest.  Keys whose page a replay skips are left out of the
+ * choice; where too few are left, the recent keys follow them and -1 fills the rest.
  *
  *   kept   DEVICE int32 [batch, num_kv_heads, budget] (written): positions in ascending order, then -1
  * sink, recent >= 0, budget >= 1, sink + recent <= budget (else INVALID_ARG).

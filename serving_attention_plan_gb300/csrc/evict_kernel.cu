@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 6) select_ker
   constexpr int kWarps = kThreads / 32;
   auto clear = [&]() {
     for (int i = threadIdx.x; i < 3 * kBins; i += kThreads) (&sm.hist[0][0])[i] = 0;
-    if (threadIdx.x == 0) sm.total_gt = sm.total_eq = 0;
+    if (threadIdx.x == 0) sm.total_gt = sm.total_eq = sm.digit[0] = sm.digit[1] = sm.digit[2] = sm.above = sm.within = 0;
   };
   clear();
   __syncthreads();
@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 6) select_ker
     uint32_t left = uint32_t(need);
     int passes = 0;
     bool all_in = false;  // every key of the last bin stays: there is no need to look into it
+    int missing = 0;      // free places that no key takes: pages outside the pool hold the others (error bit set)
     for (int pass = 0; pass < 3 && !all_in; ++pass, ++passes) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const uint32_t mask = pass == 2 ? 1023u : 2047u;
@@ -223,6 +224,17 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 6) select_ker
         for (int o = 1; o < 32; o <<= 1) {
           const uint32_t u = __shfl_up_sync(kAll, upto, o);
           if (lane >= o) upto += u;
+        }
+        // Fewer keys than places (the whole cluster sees the same sum): all that were counted stay.  Only the
+        // first pass can find so, later ones look into a bin that holds enough.  The bins' own counts place the slices, as
+        // after a pass whose bin 0 stays as a whole.
+        const uint32_t counted = __shfl_sync(kAll, upto, 31);
+        if (counted < left) {
+          missing = int(left - counted);
+          prefix = 1;
+          all_in = true;
+          passes = 1;
+          break;  // sm.digit[0] is 0 still
         }
         const int hit = __ffs(__ballot_sync(kAll, left <= upto)) - 1;
         uint32_t skipped = __shfl_sync(kAll, upto - c0 - c1, hit);
@@ -320,12 +332,18 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 6) select_ker
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const bool is_gt = x[e] > above, is_eq = x[e] == above && !all_in;
-        if (is_gt || (is_eq && my_eq < left)) kept[p.sink + my_gt + min(left, my_eq)] = s0 + i + e;
+        const uint32_t at = my_gt + min(left, my_eq);
+        // (the bound holds unless the weights change meanwhile)
+        if ((is_gt || (is_eq && my_eq < left)) && at < uint32_t(need)) kept[p.sink + at] = s0 + i + e;
         my_gt += is_gt;
         my_eq += is_eq;
       }
       gt += all & 0xffffu;
       eq += all >> 16;
+    }
+    if (missing > 0) {  // the recent keys move up behind the free ones; their first places were written before the barriers
+      for (int i = rank * kThreads + tid; i < missing + p.recent; i += nr * kThreads)
+        kept[p.sink + need - missing + i] = i < p.recent ? g.lkv - p.recent + i : -1;
     }
     if (nr > 1) cluster_wait();
     if (row + int(gridDim.x / nr) < rows) {  // a further row starts over

@@ -333,6 +333,61 @@ def test_select_keys(case):
     assert np.array_equal(kept.cpu().numpy(), C.select(b, w, budget, recent, sink))
 
 
+# lkv, hk, page, budget, recent, sink, kind, SM budget, share of the free keys' pages that lie outside the pool
+OUTSIDE = [
+    ([100, 33, 700, 64], 2, 4, 32, 8, 2, "random", 1, 0.95),   # rows one after another in a CTA
+    ([1000, 513], 2, 5, 257, 31, 4, "ties", 0, 0.9),           # one weight a load
+    ([1000, 900], 2, 16, 500, 0, 0, "random", 0, 1.0),         # nothing left
+    ([20000, 18000], 1, 16, 5000, 100, 4, "random", 0, 0.9),   # a cluster shares the row
+    ([450000], 1, 128, 4000, 50, 0, "special", 0, 0.995),      # slices that are read again from memory
+    ([3000, 2000], 4, 16, 300, 20, 4, "random", 0, 0.3),       # enough keys are left
+]
+
+
+@pytest.mark.parametrize("case", OUTSIDE, ids=range(len(OUTSIDE)))
+def test_replayed_selection_with_pages_outside_the_pool(case):
+    """A replay whose plan lists pages that the captured pool does not have: their keys are left out, the error bit is set,
+    every entry of kept is written and nothing beside it is."""
+    from serving_attention_plan_gb300 import binding as B
+    torch = torch_mod()
+    lkv, hk, ps, budget, recent, sink, kind, sms, share = case
+    rng = np.random.default_rng(12)
+    b = W.make_paged_batch(rng, "select", [1] * len(lkv), lkv, hk, hk, ps, False, with_data=False)
+    w = some_weights(rng, (b.num_pages, hk, ps), kind)
+    ws = workspace(b, num_sms=sms)
+    guard, n_kept = 256, b.batch_size * hk * budget
+    flat = torch.full((n_kept + 2 * guard,), -7, dtype=torch.int32, device="cuda")
+    kept = flat[guard:guard + n_kept].view(b.batch_size, hk, budget)
+    wd, side = dev(w), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        ws.select_keys(wd, budget, kept, recent=recent, sink=sink, stream=side)
+    lost = rng.random(b.kv_indices.shape[0]) < share
+    idx = np.where(lost, b.kv_indices + b.num_pages, b.kv_indices).astype(np.int32)
+    ws.plan(b.qo_indptr, b.kv_indptr, idx, b.last_page_len, ps, False, stream=side)
+    for _ in range(2):
+        with torch.cuda.stream(side):
+            graph.replay()
+        side.synchronize()
+        assert ws.get_error() == B.DEVERR_PAGE_OOB
+    want = np.full((b.batch_size, hk, budget), -1, np.int32)
+    for i, n in enumerate(lkv):
+        j = np.arange(n)
+        gone = lost[int(b.kv_indptr[i]) + j // ps]
+        page, slot = C.places(b, i, j)
+        for h in range(hk):
+            free = np.arange(sink, n - recent)
+            free = free[~gone[free]]
+            x = w[page[free], h, slot[free]].astype(np.float64)
+            order = np.lexsort((free, np.where(np.isnan(x), 0.0, -x), ~np.isnan(x)))[:budget - sink - recent]
+            row = np.concatenate([j[:sink], np.sort(free[order]), j[n - recent:]]) if n > budget else j
+            want[i, h, :len(row)] = row
+    got = flat.cpu().numpy()
+    assert np.array_equal(got[guard:guard + n_kept].reshape(want.shape), want)
+    assert (got[:guard] == -7).all() and (got[guard + n_kept:] == -7).all()
+
+
 # ---- compaction ------------------------------------------------------------------------------------
 
 COMPACT = [
