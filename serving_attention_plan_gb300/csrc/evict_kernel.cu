@@ -98,7 +98,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 1024 ? 1 : 6) select_ker
     const Geo g = load_geo(pv.geo, r);
     int32_t* kept = p.kept + (long long)row * p.budget;
     if (g.lkv <= p.budget) {
-      for (int i = rank * kThreads + tid; i < p.budget; i += nr * kThreads) kept[i] = i < g.lkv ? i : -1;
+      // (a budget may be as large as 2^31 - 1, where a signed counter would overflow)
+      for (unsigned i = rank * kThreads + tid; i < unsigned(p.budget); i += nr * kThreads)
+        kept[i] = i < unsigned(g.lkv) ? int(i) : -1;
       continue;  // the same for every CTA of the cluster
     }
     const int f0 = p.sink, f1 = g.lkv - p.recent;

@@ -388,6 +388,22 @@ def test_replayed_selection_with_pages_outside_the_pool(case):
     assert (got[:guard] == -7).all() and (got[guard + n_kept:] == -7).all()
 
 
+
+def test_select_keys_largest_budget():
+    """A budget of 2^31 - 1, far beyond the request: the keys, then -1 to the last entry, nothing beside them."""
+    torch = torch_mod()
+    budget, guard = 2**31 - 1, 1024
+    b = batch_of([1], [5], 1, 1, 4)
+    ws = workspace(b)
+    flat = torch.full((budget + 2 * guard,), -7, dtype=torch.int32, device="cuda")
+    kept = flat[guard:guard + budget].view(1, 1, budget)
+    ws.select_keys(torch.zeros(b.num_pages, 1, 4, device="cuda"), budget, kept, recent=3, sink=1)
+    torch.cuda.synchronize()
+    assert ws.get_error() == 0 and kept[0, 0, :5].tolist() == [0, 1, 2, 3, 4]
+    assert int(kept.min()) == -1 and int(kept[0, 0, 5:].max()) == -1
+    assert (flat[:guard] == -7).all() and (flat[guard + budget:] == -7).all()
+
+
 # ---- compaction ------------------------------------------------------------------------------------
 
 COMPACT = [
