@@ -68,6 +68,7 @@ void split_weights(Geo* geo, int batch, int hkv, int group, int row_limit, bool 
 }
 
 int check_pages_once(const int32_t* a, int64_t na, const int32_t* b, int64_t nb, int32_t max_page) {
+  if (na + nb == 0) return FI_OK;  // max_page is -1
   try {
     std::vector<uint64_t> seen((size_t(max_page) >> 6) + 1, 0);
     uint64_t twice = 0;  // no branch in the loop

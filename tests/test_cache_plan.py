@@ -43,6 +43,14 @@ def test_page_conditions(lists, q, last, pages, tails):
     assert got[1:] == (pages, tails)
 
 
+@pytest.mark.parametrize("q,last", [([], []), ([0], [0]), ([1], [0]), ([3, 0, 2], [0, 0, 0])])
+def test_batches_without_pages(q, last):
+    """No request, or requests that have no page: a geometry of no keys, and no page listed twice."""
+    geo, pages_twice, tails_twice = B.cache_plan_compute(np.concatenate([[0], np.cumsum(q)]), [0] * (len(q) + 1), [], last, 16)
+    assert np.array_equal(geo[:, 0], np.concatenate([[0], np.cumsum(q)])) and np.array_equal(geo[:-1, 1], q)
+    assert not geo[:, 2:].any() and not pages_twice and not tails_twice
+
+
 def test_bad_batches_are_refused():
     for args in (([0, 1], [0, 1], [-1], [1]), ([0, 1], [0, 1], [0], [5]), ([0, 1], [0, 1], [0], [0]),
                  ([1, 1], [0, 1], [0], [1]), ([0, 1], [1, 0], [0], [1])):
