@@ -316,10 +316,11 @@ int fi_merge_states(const void* o_a, const float* lse_a, const void* o_b, const 
  * Common behaviour: asynchronous on `stream`, launched as programmatic dependents that read nothing
  * before the previous kernel on the stream has completed; capturable in a CUDA graph.  A captured
  * launch reads the requests and page lists of the plan that is current when it runs.  The pointers and the
- * numbers passed by value are those of the capture.  A later plan must keep the page size, the variant (layout, KV
- * type and scales, window, soft-cap) and fi_plan_info header[1] (the path; on the tensor-core path also the
- * total query count for fi_key_weights, as for fi_run), and the conditions on pages below hold for it too,
- * unchecked.  The workspace's device must be the current one (else INVALID_ARG).  Page
+ * numbers passed by value are those of the capture: during one a call is recorded even if the plan at hand has no
+ * requests, tokens or keys, and null pointers that such a plan would otherwise excuse are INVALID_ARG.  A later plan
+ * must keep the page size, the variant (layout, KV type and scales, window, soft-cap) and fi_plan_info header[1] (the
+ * path; on the tensor-core path also the total query count for fi_key_weights, as for fi_run), and the conditions on
+ * pages below hold for it too, unchecked.  The workspace's device must be the current one (else INVALID_ARG).  Page
  * ids >= num_pages: INVALID_ARG (in a replay: skipped, FI_DEVERR_PAGE_OOB).  Pools of more than
  * 2^31 - 1 rows (pages * page size * KV heads): UNSUPPORTED.  Calls that share a
  * workspace must not overlap on the GPU.  Results are bit-identical from run to run.

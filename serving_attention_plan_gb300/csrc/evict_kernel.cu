@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(kCmpThreads, 2) compact_kernel(const __grid_co
 }  // namespace
 
 int launch_select(SelectParams p, int batch, int max_lkv, int num_sms, cudaStream_t stream) {
-  const int rows = batch * p.pv.hkv;
+  const int rows = std::max(1, batch * p.pv.hkv);
   p.by_four = p.pv.page_size % 4 == 0 && reinterpret_cast<uintptr_t>(p.weights) % 16 == 0;
   // a cluster shares a row while there are SMs for it (131 K keys of 8 heads: 8 CTAs 17 us), or as long as a slice does
   // not fit into shared memory and would be read again in each pass (16 x 8 rows of 100 K keys: 81 us, 121 without)
@@ -608,7 +608,7 @@ int launch_select(SelectParams p, int batch, int max_lkv, int num_sms, cudaStrea
 }
 
 int launch_compact(const CompactParams& p, int batch, bool fp8, int num_sms, cudaStream_t stream) {
-  const int64_t tasks = int64_t(batch) * p.pv.hkv * (p.weights ? 3 : 2);
+  const int64_t tasks = int64_t(std::max(1, batch)) * p.pv.hkv * (p.weights ? 3 : 2);
   unsigned cluster = 1;
   while (cluster < 8 && tasks * cluster * 2 <= 2 * num_sms) cluster *= 2;
   static std::once_flag once;

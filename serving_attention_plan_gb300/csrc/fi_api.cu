@@ -164,6 +164,15 @@ int check_cache_call(const fi_workspace* ws, int num_pages) {
   return dev == ws->device ? FI_OK : FI_ERR_INVALID_ARG;
 }
 
+// Whether a capture is under way on the stream.  A captured launch serves later plans: it is made even where the plan
+// at hand leaves it nothing to do, and needs every pointer that a plan with tokens and keys needs.
+int is_capturing(cudaStream_t s, bool* on) {
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+  FI_CUDA(cudaStreamIsCapturing(s, &st));
+  *on = st != cudaStreamCaptureStatusNone;
+  return FI_OK;
+}
+
 fi::PageView page_view(const fi_workspace* ws, int num_pages) {
   fi::PageView v{};
   char* d = ws->dbuf;
@@ -778,10 +787,14 @@ int fi_append(fi_workspace* ws, const void* q, int64_t q_stride, const void* k, 
   if (st != FI_OK) return st;
   if (!(eps >= 0.f) || !std::isfinite(eps)) return FI_ERR_INVALID_ARG;
   const int total_q = ws->plan_total_q;
-  if (total_q == 0) return FI_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  bool captured = false;
+  st = is_capturing(s, &captured);
+  if (st != FI_OK) return st;
+  if (total_q == 0 && !captured) return FI_OK;
   const int64_t dq = int64_t(ws->hqo) * fi::kHeadDim, dkv = int64_t(ws->hkv) * fi::kHeadDim;
   if (q == nullptr || k == nullptr || v == nullptr || q_out == nullptr) return FI_ERR_INVALID_ARG;
-  if (ws->plan_nnz > 0 && (k_pages == nullptr || v_pages == nullptr)) return FI_ERR_INVALID_ARG;
+  if ((ws->plan_nnz > 0 || captured) && (k_pages == nullptr || v_pages == nullptr)) return FI_ERR_INVALID_ARG;
   if (q_stride < dq || k_stride < dkv || v_stride < dkv || q_stride % 8 || k_stride % 8 || v_stride % 8)
     return FI_ERR_INVALID_ARG;
   for (const void* a : {q, k, v, q_weight, k_weight, static_cast<const void*>(q_out),
@@ -812,8 +825,7 @@ int fi_append(fi_workspace* ws, const void* q, int64_t q_stride, const void* k, 
   p.rotary = ws->rotary;
   p.interleaved = ws->interleaved;
   std::memcpy(p.freq, ws->freq, sizeof(p.freq));
-  return fi::launch_append(p, total_q, ws->plan_variant.kv_dtype == FI_KV_DTYPE_E4M3, ws->num_sms,
-                           static_cast<cudaStream_t>(stream));
+  return fi::launch_append(p, total_q, ws->plan_variant.kv_dtype == FI_KV_DTYPE_E4M3, ws->num_sms, s);
 }
 
 int fi_key_weights(fi_workspace* ws, const void* q, const void* k_pages, int num_pages, const float* lse, float decay,
@@ -821,8 +833,12 @@ int fi_key_weights(fi_workspace* ws, const void* q, const void* k_pages, int num
   int st = check_cache_call(ws, num_pages);
   if (st != FI_OK) return st;
   if (!(decay >= 0.f && decay <= 1.f) || (new_keys != 0 && new_keys != 1)) return FI_ERR_INVALID_ARG;
-  if (ws->plan_nnz - ws->plan_nnz_shared == 0) return FI_OK;  // no key to weigh
-  if (k_pages == nullptr || weights == nullptr || (ws->plan_total_q > 0 && (q == nullptr || lse == nullptr)))
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  bool captured = false;
+  st = is_capturing(s, &captured);
+  if (st != FI_OK) return st;
+  if (ws->plan_nnz - ws->plan_nnz_shared == 0 && !captured) return FI_OK;  // no key to weigh
+  if (k_pages == nullptr || weights == nullptr || ((ws->plan_total_q > 0 || captured) && (q == nullptr || lse == nullptr)))
     return FI_ERR_INVALID_ARG;
   if (misaligned(q, 16) || misaligned(k_pages, 16) || misaligned(lse, 4) || misaligned(weights, 4))
     return FI_ERR_INVALID_ARG;
@@ -845,34 +861,35 @@ int fi_key_weights(fi_workspace* ws, const void* q, const void* k_pages, int num
   p.cap_log2 = var.soft_cap > 0.f ? var.soft_cap * fi::kLog2e : 0.f;
   p.inv_cap_log2 = var.soft_cap > 0.f ? 1.f / p.cap_log2 : 0.f;
   p.window_left = std::min(var.window_left, 1 << 30);  // no request has more keys
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   // a batch that needs the tensor cores is split by request (a group of more than 128 heads does not fit their
   // tile); a captured launch has to serve later plans of the path, so it gets both kernels
   if (ws->header[fi::H_PATH] == fi::kPathTensor && p.group <= fi::kWeightTileRows) {
-    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-    FI_CUDA(cudaStreamIsCapturing(s, &capture));
-    const bool both = capture != cudaStreamCaptureStatusNone;
     p.tile_tokens = fi::kWeightTileRows / p.group;
     p.part = reinterpret_cast<float*>(ws->dbuf + ws->off_wpart);
     p.part_count = reinterpret_cast<uint32_t*>(ws->dbuf + ws->off_wcount);
-    if (ws->geo.work > 0 || both) {
+    if (ws->geo.work > 0 || captured) {
       st = fi::launch_weights_tc(p, ws->plan_total_q, fp8, ws->num_sms, s);
       if (st != FI_OK) return st;
     }
-    if (ws->geo.blocks == 0 && !both) return FI_OK;
-    return fi::launch_weights_rows(p, fp8, both ? INT32_MAX : ws->geo.blocks, ws->num_sms, s);
+    if (ws->geo.blocks == 0 && !captured) return FI_OK;
+    return fi::launch_weights_rows(p, fp8, captured ? INT32_MAX : ws->geo.blocks, ws->num_sms, s);
   }
   return fi::launch_weights_rows(p, fp8, ws->geo.blocks, ws->num_sms, s);
 }
 
 int fi_select_keys(fi_workspace* ws, const float* weights, int num_pages, int32_t sink, int32_t recent, int32_t budget,
                    int32_t* kept, void* stream) {
-  const int st = check_cache_call(ws, num_pages);
+  int st = check_cache_call(ws, num_pages);
   if (st != FI_OK) return st;
   if (sink < 0 || recent < 0 || budget < 1 || int64_t(sink) + recent > budget) return FI_ERR_INVALID_ARG;
   const int batch = ws->header[fi::H_BATCH];
-  if (batch == 0) return FI_OK;
-  if (kept == nullptr || (ws->plan_nnz - ws->plan_nnz_shared > 0 && weights == nullptr)) return FI_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  bool captured = false;
+  st = is_capturing(s, &captured);
+  if (st != FI_OK) return st;
+  if (batch == 0 && !captured) return FI_OK;
+  if (kept == nullptr || ((ws->plan_nnz - ws->plan_nnz_shared > 0 || captured) && weights == nullptr))
+    return FI_ERR_INVALID_ARG;
   if (misaligned(weights, 4) || misaligned(kept, 4)) return FI_ERR_INVALID_ARG;
   fi::SelectParams p{};
   p.pv = page_view(ws, num_pages);
@@ -881,7 +898,7 @@ int fi_select_keys(fi_workspace* ws, const float* weights, int num_pages, int32_
   p.sink = sink;
   p.recent = recent;
   p.budget = budget;
-  return fi::launch_select(p, batch, ws->geo.max_lkv, ws->num_sms, static_cast<cudaStream_t>(stream));
+  return fi::launch_select(p, batch, ws->geo.max_lkv, ws->num_sms, s);
 }
 
 int fi_compact(fi_workspace* ws, const int32_t* kept, int32_t budget, void* k_pages, void* v_pages, float* weights,
@@ -890,7 +907,11 @@ int fi_compact(fi_workspace* ws, const int32_t* kept, int32_t budget, void* k_pa
   if (st != FI_OK) return st;
   if (budget < 1) return FI_ERR_INVALID_ARG;
   const int batch = ws->header[fi::H_BATCH];
-  if (batch == 0 || ws->plan_nnz - ws->plan_nnz_shared == 0) return FI_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  bool captured = false;
+  st = is_capturing(s, &captured);
+  if (st != FI_OK) return st;
+  if ((batch == 0 || ws->plan_nnz - ws->plan_nnz_shared == 0) && !captured) return FI_OK;
   if (kept == nullptr || k_pages == nullptr || v_pages == nullptr || misaligned(kept, 4) || misaligned(k_pages, 16) ||
       misaligned(v_pages, 16) || misaligned(weights, 4))
     return FI_ERR_INVALID_ARG;
@@ -903,8 +924,7 @@ int fi_compact(fi_workspace* ws, const int32_t* kept, int32_t budget, void* k_pa
   p.v_pages = v_pages;
   p.weights = weights;
   p.budget = budget;
-  return fi::launch_compact(p, batch, ws->plan_variant.kv_dtype == FI_KV_DTYPE_E4M3, ws->num_sms,
-                            static_cast<cudaStream_t>(stream));
+  return fi::launch_compact(p, batch, ws->plan_variant.kv_dtype == FI_KV_DTYPE_E4M3, ws->num_sms, s);
 }
 
 int fi_get_error(fi_workspace* ws, int32_t* err_bits) {

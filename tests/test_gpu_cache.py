@@ -614,6 +614,84 @@ def test_captured_chain_follows_a_new_plan():
             assert torch.equal(ref[k], cap[k]), k
 
 
+
+EMPTY_PLANS = {  # what the capture's plan holds: (qo_indptr, kv_indptr, kv_indices, last_page_len), and the later plan's (l_q, l_kv)
+    "no requests": (([0], [0], [], []), [1, 1, 1], [130, 90, 20]),
+    "no tokens": (([0, 0], [0, 2], [0, 1], [3]), [1, 1, 1], [130, 90, 20]),
+    "no keys": (([0, 1, 2, 3], [0, 0, 0, 0], [], [0, 0, 0]), [1, 1, 1], [130, 90, 20]),
+    "prompts without keys": (([0, 20, 60], [0, 0, 0], [], [0, 0]), [20, 40], [120, 300]),
+}
+
+
+@pytest.mark.parametrize("which", EMPTY_PLANS)
+def test_capture_on_an_empty_plan(which):
+    """The operators captured while the plan has no requests, tokens or keys: a replay after a plan that has all of them
+    does what direct calls do.  Null pointers are refused then, whatever the plan at hand would excuse."""
+    torch = torch_mod()
+    from serving_attention_plan_gb300 import binding as B
+    L = B.lib()
+    empty, lq, lkv = EMPTY_PLANS[which]
+    hq, hk, ps, budget = 8, 2, 16, 60
+    b = batch_of(lq, lkv, hq, hk, ps, True, seed=3)
+    n, rows, pages = b.batch_size, b.total_q, b.num_pages
+    ws = B.Workspace(4, 64, 64, hq, hk)
+    side = torch.cuda.Stream()
+    x = torch.randn(rows, hq + 2 * hk, 128, device="cuda").to(torch.bfloat16)
+    lse = dev(lse_of(b, A.bf16_to_f64(b.q), b.k_pages, 1.0, -1, 0.0, "HND"))
+    q = bf16(b.q)
+    w0 = torch.rand(pages, hk, ps, device="cuda")
+
+    def buffers():
+        return dict(kp=bf16(b.k_pages), vp=bf16(b.v_pages), w=w0.clone(), out=torch.zeros(rows, hq, 128, device="cuda", dtype=torch.bfloat16),
+                    kept=torch.full((n, hk, budget), -9, device="cuda", dtype=torch.int32))
+
+    cap, ref = buffers(), buffers()
+    P = {k: t.data_ptr() for k, t in cap.items()}
+    h, s = ws._h, side.cuda_stream
+    d, width = x.data_ptr(), (hq + 2 * hk) * 128
+
+    def append(q=d, k=d + 256 * hq, v=d + 256 * (hq + hk), out=P["out"], kp=P["kp"], vp=P["vp"]):
+        return L.fi_append(h, q, width, k, width, v, width, None, None, 0.0, None, out, kp, vp, pages, s)
+
+    def weights(q=q.data_ptr(), kp=P["kp"], lse=lse.data_ptr(), w=P["w"]):
+        return L.fi_key_weights(h, q, kp, pages, lse, 0.5, 1, w, s)
+
+    def select(w=P["w"], kept=P["kept"]):
+        return L.fi_select_keys(h, w, pages, 2, 10, budget, kept, s)
+
+    def compact(kept=P["kept"], kp=P["kp"], vp=P["vp"], w=P["w"]):
+        return L.fi_compact(h, kept, budget, kp, vp, w, pages, s)
+
+    torch.cuda.synchronize()
+    ws.plan(*empty, ps, True, stream=side)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        refused = [append(q=None), append(k=None), append(v=None), append(out=None), append(kp=None), append(vp=None), weights(q=None),
+                   weights(kp=None), weights(lse=None), weights(w=None), select(w=None), select(kept=None), compact(kept=None),
+                   compact(kp=None), compact(vp=None)]
+        taken = [weights(), select(), compact(), append()]
+    assert refused == [1] * 15 and taken == [0] * 4
+    for plan in (empty, (b.qo_indptr, b.kv_indptr, b.kv_indices, b.last_page_len)) * 2:
+        for k, t in buffers().items():
+            cap[k].copy_(t)
+        ws.plan(*plan, ps, True, stream=side)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph.replay()
+        side.synchronize()
+        assert ws.get_error() == 0
+    ws.plan(b.qo_indptr, b.kv_indptr, b.kv_indices, b.last_page_len, ps, True)
+    ws.key_weights(q, ref["kp"], lse, ref["w"], 0.5, True)
+    ws.select_keys(ref["w"], budget, ref["kept"], recent=10, sink=2)
+    ws.compact(ref["kept"], ref["kp"], ref["vp"], ref["w"])
+    ws.append(x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:], ref["kp"], ref["vp"], ref["out"])
+    torch.cuda.synchronize()
+    for k in ref:
+        assert torch.equal(ref[k], cap[k]), k
+    assert not torch.equal(cap["w"], w0) and (cap["kept"] > budget).any() and cap["out"].any()
+
+
 def test_composable_plan():
     """With a composable plan the operators work on the per-request part; positions must be given."""
     from serving_attention_plan_gb300 import binding as B
