@@ -313,17 +313,22 @@ int fi_merge_states(const void* o_a, const float* lse_a, const void* o_b, const 
  * on the workspace's current plan: its requests, page lists, page size, layout, KV type, window and
  * soft-cap.  With a composable plan they see the per-request part.
  *
- * Common behaviour: asynchronous on `stream`, launched as programmatic dependents that read nothing
- * before the previous kernel on the stream has completed; capturable in a CUDA graph.  A captured
- * launch reads the requests and page lists of the plan that is current when it runs.  The pointers and the
- * numbers passed by value are those of the capture: during one a call is recorded even if the plan at hand has no
- * requests, tokens or keys, and null pointers that such a plan would otherwise excuse are INVALID_ARG.  A later plan
- * must keep the page size, the variant (layout, KV type and scales, window, soft-cap) and fi_plan_info header[1] (the
- * path; on the tensor-core path also the total query count for fi_key_weights, as for fi_run), and the conditions on
- * pages below hold for it too, unchecked.  The workspace's device must be the current one (else INVALID_ARG).  Page
- * ids >= num_pages: INVALID_ARG (in a replay: skipped, FI_DEVERR_PAGE_OOB).  Pools of more than
- * 2^31 - 1 rows (pages * page size * KV heads): UNSUPPORTED.  Calls that share a
- * workspace must not overlap on the GPU.  Results are bit-identical from run to run.
+ * Common behaviour: asynchronous on `stream`, launched as programmatic dependents that read nothing before
+ * the previous kernel on the stream has completed.  Calls that share a workspace must not overlap on the GPU.
+ * Results are bit-identical from run to run.  The workspace's device must be the current one (else
+ * INVALID_ARG).  Page ids >= num_pages: INVALID_ARG (in a replay: skipped, FI_DEVERR_PAGE_OOB).  Pools of
+ * more than 2^31 - 1 rows (pages * page size * KV heads): UNSUPPORTED.
+ *
+ * Capturable in a CUDA graph: a captured launch reads the requests and page lists of the plan that is current
+ * when it runs.  The pointers and the numbers passed by value are those of the capture.  A later plan must
+ * keep the page size, the variant (layout, KV type and scales, window, soft-cap) and fi_plan_info header[1]
+ * (the path; on the tensor-core path also the total query count for fi_key_weights, as for fi_run), and the
+ * conditions on pages below hold for it too, unchecked.  During a capture a call is recorded even if the plan
+ * at hand has no requests, tokens or keys, and null pointers that such a plan would otherwise excuse are
+ * INVALID_ARG.  The grid is made for the workspace's capacity; the shared memory and clusters of
+ * fi_select_keys and fi_compact, and whether fi_append gives a token a CTA or a warp, are those of the
+ * capture's plan, so capture them on a batch of the usual size.
+ *
  * `weights` is float32 [num_pages, num_kv_heads, page_size] for either page layout.
  */
 

@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendCtasPerSm) append_kerne
 
 }  // namespace
 
-int launch_append(const AppendParams& p, int total_q, bool fp8, int num_sms, cudaStream_t stream) {
+int launch_append(const AppendParams& p, int total_q, int most_q, bool fp8, int num_sms, cudaStream_t stream) {
   using Kernel = void (*)(const AppendParams);
   static const Kernel kernels[4] = {append_kernel<kAppendThreads, false>, append_kernel<kAppendThreads, true>,
                                     append_kernel<32, false>, append_kernel<32, true>};
@@ -272,7 +272,7 @@ int launch_append(const AppendParams& p, int total_q, bool fp8, int num_sms, cud
   // a warp for each token once they fill the grid's warps
   const int ctas = kAppendCtasPerSm * num_sms;
   const bool many = total_q >= ctas * (kAppendThreads / 32);
-  const cudaError_t e = launch_dependent(kernels[(many ? 2 : 0) + (fp8 ? 1 : 0)], unsigned(std::max(1, std::min(total_q, ctas))),
+  const cudaError_t e = launch_dependent(kernels[(many ? 2 : 0) + (fp8 ? 1 : 0)], unsigned(std::min(most_q, ctas)),
                                          kAppendThreads, smem[many ? 1 : 0], 1, stream, p);
   return e == cudaSuccess ? 0 : record_cuda_error(e, "append_kernel launch");
 }

@@ -105,7 +105,9 @@ struct AppendParams {
   int interleaved;  // pairs (2j, 2j + 1) instead of (j, j + rotary / 2)
   uint64_t freq[kMaxFreqs];  // revolutions per position, as a 64-bit fraction of a turn
 };
-int launch_append(const AppendParams& p, int total_q, bool fp8, int num_sms, cudaStream_t stream);
+// In the launchers below, `most_*` is what the grid is made for: the plan's own number, or, of a captured launch, the
+// workspace's capacity, since a later plan may fill it.
+int launch_append(const AppendParams& p, int total_q, int most_q, bool fp8, int num_sms, cudaStream_t stream);
 
 struct WeightsParams {
   PageView pv;
@@ -124,7 +126,7 @@ struct WeightsParams {
   float* part;          // [CTAs][2][256] partial sums of items cut between CTAs
   uint32_t* part_count; // [CTAs], zero between launches
 };
-int launch_weights_rows(const WeightsParams& p, bool fp8, int64_t n_blk, int num_sms, cudaStream_t stream);
+int launch_weights_rows(const WeightsParams& p, bool fp8, int64_t most_blk, int num_sms, cudaStream_t stream);
 
 int launch_weights_tc(const WeightsParams& p, int total_q, bool fp8, int num_sms, cudaStream_t stream);
 
@@ -135,7 +137,7 @@ struct SelectParams {
   int sink, recent, budget;
   int by_four;  // weights can be fetched four slots at a time; set by the launcher
 };
-int launch_select(SelectParams p, int batch, int max_lkv, int num_sms, cudaStream_t stream);
+int launch_select(SelectParams p, int batch, int most_batch, int max_lkv, int num_sms, cudaStream_t stream);
 
 struct CompactParams {
   PageView pv;
@@ -144,6 +146,6 @@ struct CompactParams {
   float* weights;  // or null
   int budget;
 };
-int launch_compact(const CompactParams& p, int batch, bool fp8, int num_sms, cudaStream_t stream);
+int launch_compact(const CompactParams& p, int batch, int most_batch, bool fp8, int num_sms, cudaStream_t stream);
 
 }  // namespace fi

@@ -579,8 +579,9 @@ __global__ void __launch_bounds__(kCmpThreads, 2) compact_kernel(const __grid_co
 
 }  // namespace
 
-int launch_select(SelectParams p, int batch, int max_lkv, int num_sms, cudaStream_t stream) {
-  const int rows = std::max(1, batch * p.pv.hkv);
+int launch_select(SelectParams p, int batch, int most_batch, int max_lkv, int num_sms, cudaStream_t stream) {
+  if (batch == 0) batch = most_batch;  // captured on an empty plan
+  const int rows = batch * p.pv.hkv;
   p.by_four = p.pv.page_size % 4 == 0 && reinterpret_cast<uintptr_t>(p.weights) % 16 == 0;
   // a cluster shares a row while there are SMs for it (131 K keys of 8 heads: 8 CTAs 17 us), or as long as a slice does
   // not fit into shared memory and would be read again in each pass (16 x 8 rows of 100 K keys: 81 us, 121 without)
@@ -599,16 +600,19 @@ int launch_select(SelectParams p, int batch, int max_lkv, int num_sms, cudaStrea
       attr = cudaFuncSetAttribute(select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, 48 * 1024 * 4);
   });
   if (attr != cudaSuccess) return record_cuda_error(attr, "cudaFuncSetAttribute(select_kernel)");
-  const unsigned grid = unsigned(std::min<int64_t>(rows, 4 * num_sms)) * cluster;
   // short rows take 256 threads, six to an SM; long ones, and clusters, 1024
   const bool wide = cluster > 1 || max_lkv > 4096;
+  // rows of later plans of a captured launch: CTAs that fit the GPU at once, and that do nothing otherwise
+  const int64_t later = std::min<int64_t>(int64_t(most_batch) * p.pv.hkv, std::max(1, wide ? num_sms / int(cluster) : 4 * num_sms));
+  const unsigned grid = unsigned(std::max(std::min<int64_t>(rows, 4 * num_sms), later)) * cluster;
   const cudaError_t e = wide ? launch_dependent(select_kernel<1024>, grid, 1024, smem, cluster, stream, p, cap)
                              : launch_dependent(select_kernel<256>, grid, 256, smem, cluster, stream, p, cap);
   return e == cudaSuccess ? 0 : record_cuda_error(e, "select_kernel launch");
 }
 
-int launch_compact(const CompactParams& p, int batch, bool fp8, int num_sms, cudaStream_t stream) {
-  const int64_t tasks = int64_t(std::max(1, batch)) * p.pv.hkv * (p.weights ? 3 : 2);
+int launch_compact(const CompactParams& p, int batch, int most_batch, bool fp8, int num_sms, cudaStream_t stream) {
+  if (batch == 0) batch = most_batch;  // captured on an empty plan
+  const int64_t of_one = int64_t(p.pv.hkv) * (p.weights ? 3 : 2), tasks = batch * of_one;
   unsigned cluster = 1;
   while (cluster < 8 && tasks * cluster * 2 <= 2 * num_sms) cluster *= 2;
   static std::once_flag once;
@@ -619,7 +623,9 @@ int launch_compact(const CompactParams& p, int batch, bool fp8, int num_sms, cud
       attr = cudaFuncSetAttribute(compact_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(CompactSmem)));
   });
   if (attr != cudaSuccess) return record_cuda_error(attr, "cudaFuncSetAttribute(compact_kernel)");
-  const unsigned grid = unsigned(std::min<int64_t>(tasks, 64 * num_sms)) * cluster;
+  // as above; of clusters fewer than two CTAs an SM find room at once (38 clusters of 8: 145 us where 24 take 124)
+  const int64_t later = std::min<int64_t>(most_batch * of_one, cluster > 1 ? std::max(1, num_sms / int(cluster)) : 2 * num_sms);
+  const unsigned grid = unsigned(std::max(std::min<int64_t>(tasks, 64 * num_sms), later)) * cluster;
   const size_t smem = sizeof(CompactSmem);
   const cudaError_t e = fp8 ? launch_dependent(compact_kernel<true>, grid, kCmpThreads, smem, cluster, stream, p)
                             : launch_dependent(compact_kernel<false>, grid, kCmpThreads, smem, cluster, stream, p);

@@ -825,7 +825,7 @@ int fi_append(fi_workspace* ws, const void* q, int64_t q_stride, const void* k, 
   p.rotary = ws->rotary;
   p.interleaved = ws->interleaved;
   std::memcpy(p.freq, ws->freq, sizeof(p.freq));
-  return fi::launch_append(p, total_q, ws->plan_variant.kv_dtype == FI_KV_DTYPE_E4M3, ws->num_sms, s);
+  return fi::launch_append(p, total_q, captured ? ws->max_total_q : total_q, ws->plan_variant.kv_dtype == FI_KV_DTYPE_E4M3, ws->num_sms, s);
 }
 
 int fi_key_weights(fi_workspace* ws, const void* q, const void* k_pages, int num_pages, const float* lse, float decay,
@@ -874,7 +874,7 @@ int fi_key_weights(fi_workspace* ws, const void* q, const void* k_pages, int num
     if (ws->geo.blocks == 0 && !captured) return FI_OK;
     return fi::launch_weights_rows(p, fp8, captured ? INT32_MAX : ws->geo.blocks, ws->num_sms, s);
   }
-  return fi::launch_weights_rows(p, fp8, ws->geo.blocks, ws->num_sms, s);
+  return fi::launch_weights_rows(p, fp8, captured ? INT32_MAX : ws->geo.blocks, ws->num_sms, s);
 }
 
 int fi_select_keys(fi_workspace* ws, const float* weights, int num_pages, int32_t sink, int32_t recent, int32_t budget,
@@ -898,7 +898,7 @@ int fi_select_keys(fi_workspace* ws, const float* weights, int num_pages, int32_
   p.sink = sink;
   p.recent = recent;
   p.budget = budget;
-  return fi::launch_select(p, batch, ws->geo.max_lkv, ws->num_sms, s);
+  return fi::launch_select(p, batch, captured ? ws->max_batch : batch, ws->geo.max_lkv, ws->num_sms, s);
 }
 
 int fi_compact(fi_workspace* ws, const int32_t* kept, int32_t budget, void* k_pages, void* v_pages, float* weights,
@@ -924,7 +924,7 @@ int fi_compact(fi_workspace* ws, const int32_t* kept, int32_t budget, void* k_pa
   p.v_pages = v_pages;
   p.weights = weights;
   p.budget = budget;
-  return fi::launch_compact(p, batch, ws->plan_variant.kv_dtype == FI_KV_DTYPE_E4M3, ws->num_sms, s);
+  return fi::launch_compact(p, batch, captured ? ws->max_batch : batch, ws->plan_variant.kv_dtype == FI_KV_DTYPE_E4M3, ws->num_sms, s);
 }
 
 int fi_get_error(fi_workspace* ws, int32_t* err_bits) {

@@ -278,8 +278,8 @@ __global__ void __launch_bounds__(32 * kRowsWarps<kFp8>, 1) weights_rows_kernel(
 
 }  // namespace
 
-int launch_weights_rows(const WeightsParams& p, bool fp8, int64_t n_blk, int num_sms, cudaStream_t stream) {
-  const int64_t units = n_blk * p.pv.hkv;
+int launch_weights_rows(const WeightsParams& p, bool fp8, int64_t most_blk, int num_sms, cudaStream_t stream) {
+  const int64_t units = most_blk * p.pv.hkv;
   const int warps = fp8 ? kRowsWarps<true> : kRowsWarps<false>;
   const unsigned grid = unsigned(std::max<int64_t>(1, std::min<int64_t>((units + warps - 1) / warps, num_sms)));
   const bool var = p.window_left >= 0 || p.cap_log2 > 0.f;

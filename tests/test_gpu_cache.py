@@ -692,6 +692,55 @@ def test_capture_on_an_empty_plan(which):
     assert not torch.equal(cap["w"], w0) and (cap["kept"] > budget).any() and cap["out"].any()
 
 
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_captured_small_replayed_large(dtype):
+    """The operators captured on one request of one key, replayed on forty of up to 3000: the same as direct calls."""
+    torch = torch_mod()
+    from serving_attention_plan_gb300 import binding as B
+    hq, hk, ps, budget, n = 8, 2, 16, 700, 40
+    rng = np.random.default_rng(2)
+    lkv = [int(x) for x in rng.integers(1, 3000, n)]
+    pages = sum(-(-x // ps) for x in lkv)
+    b, one = (batch_of([1] * len(x), x, hq, hk, ps, True, seed=4, extra=0) for x in (lkv, [1]))
+    ws = B.Workspace(64, 64, pages, hq, hk)
+    ws.set_kv_dtype(dtype, 0.0625, 0.0625)
+    scale = 0.0625 if dtype == "e4m3" else 1.0
+    k = b.k_pages if dtype == "bf16" else W.to_e4m3(A.bf16_to_f64(b.k_pages) / scale)
+    lse = dev(lse_of(b, A.bf16_to_f64(b.q), k, scale, -1, 0.0, "HND"))
+    x = torch.randn(n, hq + 2 * hk, 128, device="cuda").to(torch.bfloat16)
+    w0, q = torch.rand(pages, hk, ps, device="cuda"), bf16(b.q)
+
+    def buffers():
+        pool = bf16(k) if dtype == "bf16" else dev(k)
+        return dict(kp=pool, vp=pool.clone(), w=w0.clone(), out=torch.zeros(n, hq, 128, device="cuda", dtype=torch.bfloat16),
+                    kept=torch.full((n, hk, budget), -9, device="cuda", dtype=torch.int32))
+
+    def calls(d, m):
+        ws.key_weights(q[:m], d["kp"], lse[:m], d["w"], 0.5, True, stream=side)
+        ws.select_keys(d["w"], budget, d["kept"][:m], recent=10, sink=2, stream=side)
+        ws.compact(d["kept"][:m], d["kp"], d["vp"], d["w"], stream=side)
+        ws.append(x[:m, :hq], x[:m, hq:hq + hk], x[:m, hq + hk:], d["kp"], d["vp"], d["out"][:m], stream=side)
+
+    side = torch.cuda.Stream()
+    plan = lambda b: ws.plan(b.qo_indptr, b.kv_indptr, b.kv_indices, b.last_page_len, ps, True, stream=side)
+    cap, ref = buffers(), buffers()
+    torch.cuda.synchronize()
+    plan(one)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        calls(cap, 1)
+    plan(b)
+    with torch.cuda.stream(side):
+        graph.replay()
+    calls(ref, n)
+    side.synchronize()
+    assert ws.get_error() == 0
+    for name in ref:
+        assert torch.equal(ref[name].view(torch.uint8), cap[name].view(torch.uint8)), name
+
+
 def test_composable_plan():
     """With a composable plan the operators work on the per-request part; positions must be given."""
     from serving_attention_plan_gb300 import binding as B
