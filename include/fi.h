@@ -123,7 +123,9 @@ int fi_workspace_set_cost_model(fi_workspace* ws, int64_t alpha, int64_t beta, i
  *                    at key position p = l_kv - l_q + t, sees keys p - window_left
  *                    .. p.  The plan reads only the keys windows reach.
  *   logits_soft_cap  0 for none; else the scaled logit x = scale * q.k becomes
- *                    cap * tanh(x / cap) before the softmax.
+ *                    cap * tanh(x / cap) before the softmax.  fi_run takes the tanh
+ *                    with an absolute error of about 1e-7, so a logit is right to
+ *                    1e-7 * cap; fi_key_weights above a cap of 64 to 3e-6 of the logit.
  *   kv_layout        FI_KV_LAYOUT_HND or FI_KV_LAYOUT_NHD.
  *
  * The variant is fixed into the plan at fi_plan; fi_run uses the plan's.  A

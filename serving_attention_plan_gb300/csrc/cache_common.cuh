@@ -72,6 +72,16 @@ __device__ __forceinline__ bool locate(const PageView& pv, int kv0, int j, int& 
   return false;
 }
 
+// tanh(y) / y as the first terms of its series in u = y^2: 1e-8 relative up to kNearReach (|y| = 1/4).
+constexpr float kNearReach = 0.0625f;
+__device__ __forceinline__ float2 tanh_near_factor(float2 u) {
+  constexpr float c[5] = {1.f, -1.f / 3.f, 2.f / 15.f, -17.f / 315.f, 62.f / 2835.f};
+  float2 t = make_float2(c[4], c[4]);
+#pragma unroll
+  for (int i = 3; i >= 0; --i) t = __ffma2_rn(t, u, make_float2(c[i], c[i]));
+  return t;
+}
+
 // 16 bytes global -> shared, or nothing (the source is not read, the destination gets zeros).
 __device__ __forceinline__ void cp_async_16_or_none(void* dst_smem, const void* src_gmem, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst_smem)), "l"(src_gmem), "r"(on ? 16 : 0)

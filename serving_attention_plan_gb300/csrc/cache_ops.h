@@ -109,6 +109,11 @@ struct AppendParams {
 // workspace's capacity, since a later plan may fill it.
 int launch_append(const AppendParams& p, int total_q, int most_q, bool fp8, int num_sms, cudaStream_t stream);
 
+// The tanh of a soft-cap by exponentials has an absolute error of 1.5e-7, which the cap multiplies: up to this cap 1e-5 in
+// a logit.  Above it the tanh is taken with a relative error (tanh_near below |y| = 1/4, by exponentials from there on, where
+// 1.5e-7 is 6e-7 of the value).
+constexpr float kExpTanhMostCap = 64.f;
+
 struct WeightsParams {
   PageView pv;
   const void* q;       // bf16 [total_q, hqo, 128]
@@ -120,6 +125,7 @@ struct WeightsParams {
   int hqo, group;
   float scale_log2;    // logit scale in the log2 domain (includes k_scale)
   float cap_log2, inv_cap_log2;  // soft-cap, 0 for none
+  int wide_cap;        // the soft-cap is above kExpTanhMostCap
   int window_left;     // >= 0: sliding window (the tensor-core form reads it from the plan)
   // tensor-core form
   int tile_tokens;      // tokens of a Q tile: 128 / group

@@ -860,6 +860,7 @@ int fi_key_weights(fi_workspace* ws, const void* q, const void* k_pages, int num
   if (fp8) p.scale_log2 *= var.k_scale;
   p.cap_log2 = var.soft_cap > 0.f ? var.soft_cap * fi::kLog2e : 0.f;
   p.inv_cap_log2 = var.soft_cap > 0.f ? 1.f / p.cap_log2 : 0.f;
+  p.wide_cap = var.soft_cap > fi::kExpTanhMostCap;
   p.window_left = std::min(var.window_left, 1 << 30);  // no request has more keys
   // a batch that needs the tensor cores is split by request (a group of more than 128 heads does not fit their
   // tile); a captured launch has to serve later plans of the path, so it gets both kernels

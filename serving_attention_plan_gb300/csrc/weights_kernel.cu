@@ -253,7 +253,10 @@ __global__ void __launch_bounds__(32 * kRowsWarps<kFp8>, 1) weights_rows_kernel(
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float x = acc[i >> 1][2 * (i & 1) + c] * p.scale_log2;
-          if (kVar && p.cap_log2 > 0.f) x = p.cap_log2 * tanh_exp2(x * p.inv_cap_log2);
+          if (kVar && p.cap_log2 > 0.f) {
+            const float y = x * p.inv_cap_log2, u = y * y;
+            x = p.cap_log2 * (p.wide_cap && u <= kNearReach ? y * tanh_near_factor(make_float2(u, u)).x : tanh_exp2(y));
+          }
           // the select drops what hidden keys and missing rows computed, NaN included
           const bool seen = key < lim[c] && (!kVar || key >= low[c]);
           sum[i] += seen ? fast_exp2(x + nl[c]) : 0.f;

@@ -409,13 +409,26 @@ __device__ __forceinline__ float2 tanh2_poly(float2 y, float2 u) {
   return __fmul2_rn(t, y);
 }
 
+// Soft-cap of a kernel: none, the two ways above, or a cap so large that their absolute error would show
+// (kExpTanhMostCap), where every score takes the series or the exponentials by its own |y|.
+enum Cap { kCapNone = 0, kCapMixed, kCapWide };
+__device__ __forceinline__ float2 tanh2_wide(float2 y) {
+  const float2 u = __fmul2_rn(y, y), near = __fmul2_rn(tanh_near_factor(u), y), far = tanh2_exp(y);
+  return make_float2(u.x <= kNearReach ? near.x : far.x, u.y <= kNearReach ? near.y : far.y);
+}
+
 // A chunk of the row's scores -> added to the column sums.  With kMasked, columns outside [lo, hi) get
 // nothing whatever their score is.
-template <bool kMasked, bool kCap>
+template <bool kMasked, int kCap>
 __device__ __forceinline__ void add_chunk(const uint32_t (&s)[kChunk], float nl, int lo, int hi, const WeightsParams& p,
                                           float2* acc) {
   float2 th[kChunk / 2];
-  if constexpr (kCap) {
+  if constexpr (kCap == kCapWide) {
+    const float in = p.scale_log2 * p.inv_cap_log2;
+#pragma unroll
+    for (int i = 0; i < kChunk / 2; ++i)
+      th[i] = tanh2_wide(__fmul2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), make_float2(in, in)));
+  } else if constexpr (kCap == kCapMixed) {
     const float in = p.scale_log2 * p.inv_cap_log2;
     float2 y[kChunk / 2], u[kPolyPairs];
 #pragma unroll
@@ -441,7 +454,7 @@ __device__ __forceinline__ void add_chunk(const uint32_t (&s)[kChunk], float nl,
 #pragma unroll
   for (int i = 0; i < kChunk / 2; ++i) {
     float2 x = make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1]));
-    if constexpr (kCap) {
+    if constexpr (kCap != kCapNone) {
       x = __ffma2_rn(th[i], make_float2(p.cap_log2, p.cap_log2), make_float2(nl, nl));
     } else {
       x = __ffma2_rn(x, make_float2(p.scale_log2, p.scale_log2), make_float2(nl, nl));
@@ -455,7 +468,7 @@ __device__ __forceinline__ void add_chunk(const uint32_t (&s)[kChunk], float nl,
 }
 
 // The row's 64 scores of a tile.
-template <bool kMasked, bool kCap>
+template <bool kMasked, int kCap>
 __device__ __forceinline__ void add_tile(uint32_t t_s, float nl, int lo, int hi, const WeightsParams& p, uint64_t* s_empty,
                                          float2 (&acc)[kCols / 2]) {
   uint32_t s[2][kChunk];
@@ -474,7 +487,7 @@ __device__ __forceinline__ void add_tile(uint32_t t_s, float nl, int lo, int hi,
   }
 }
 
-template <bool kWin, bool kCap>
+template <bool kWin, int kCap>
 __device__ void sum_weights(const WeightsParams& p, TcSmem& sm, bool causal, uint32_t tmem) {
   const PageView& pv = p.pv;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -556,7 +569,7 @@ __device__ void sum_weights(const WeightsParams& p, TcSmem& sm, bool causal, uin
   }
 }
 
-template <bool kFp8, bool kWin, bool kCap>
+template <bool kFp8, bool kWin, int kCap>
 __global__ void __launch_bounds__(kTcThreads, 1)
     weights_tc_kernel(const __grid_constant__ WeightsParams p, const __grid_constant__ CUtensorMap tm_q) {
   // the kernel has no static shared memory, so this starts at the CTA's first (1024-byte aligned) address;
@@ -663,18 +676,20 @@ int launch_weights_tc(const WeightsParams& p, int total_q, bool fp8, int num_sms
   static_assert(smem <= 227 * 1024, "shared memory exceeds the per-CTA limit");
   static_assert(kSBufs * kKeys <= int(kTmemCols) && kKeys == 4 * kCols, "score buffers, columns of the summing warps");
   using Kernel = void (*)(const WeightsParams, const CUtensorMap);
-  static const Kernel kernels[8] = {
-      weights_tc_kernel<false, false, false>, weights_tc_kernel<false, false, true>, weights_tc_kernel<false, true, false>,
-      weights_tc_kernel<false, true, true>,   weights_tc_kernel<true, false, false>, weights_tc_kernel<true, false, true>,
-      weights_tc_kernel<true, true, false>,   weights_tc_kernel<true, true, true>};
+  static const Kernel kernels[12] = {
+      weights_tc_kernel<false, false, kCapNone>, weights_tc_kernel<false, false, kCapMixed>, weights_tc_kernel<false, false, kCapWide>,
+      weights_tc_kernel<false, true, kCapNone>,  weights_tc_kernel<false, true, kCapMixed>,  weights_tc_kernel<false, true, kCapWide>,
+      weights_tc_kernel<true, false, kCapNone>,  weights_tc_kernel<true, false, kCapMixed>,  weights_tc_kernel<true, false, kCapWide>,
+      weights_tc_kernel<true, true, kCapNone>,   weights_tc_kernel<true, true, kCapMixed>,   weights_tc_kernel<true, true, kCapWide>};
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [] {
-    for (int i = 0; i < 8 && attr == cudaSuccess; ++i)
+    for (int i = 0; i < 12 && attr == cudaSuccess; ++i)
       attr = cudaFuncSetAttribute(kernels[i], cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   });
   if (attr != cudaSuccess) return record_cuda_error(attr, "cudaFuncSetAttribute(weights_tc_kernel)");
-  const Kernel k = kernels[(fp8 ? 4 : 0) + (p.window_left >= 0 ? 2 : 0) + (p.cap_log2 > 0.f ? 1 : 0)];
+  const int cap = p.cap_log2 > 0.f ? (p.wide_cap ? kCapWide : kCapMixed) : kCapNone;
+  const Kernel k = kernels[(fp8 ? 6 : 0) + (p.window_left >= 0 ? 3 : 0) + cap];
   const cudaError_t e = launch_dependent(k, unsigned(num_sms), kTcThreads, smem, 1, stream, p, tq);
   return e == cudaSuccess ? 0 : record_cuda_error(e, "weights_tc_kernel launch");
 }

@@ -279,6 +279,62 @@ def test_key_weights_masked_rows_and_infinities():
     assert np.isnan(got[p, :, s]).all()
 
 
+
+def exact_case(lq, lkv, hq, hk, dtype, gain, seed=7):
+    """q and K of few significant bits: multiples of gain / 8 and 1 / 8 up to 15 / 8, so that products and their sums
+    (below 2^15 units) are exact in every type and order, and a weight's error is that of its exponential, its tanh and its sum."""
+    b = batch_of(lq, lkv, hq, hk, 16, True, seed=seed)
+    rng = np.random.default_rng(seed)
+    q = rng.integers(-15, 16, size=b.q.shape) * (gain / 8)
+    k = rng.integers(-15, 16, size=b.k_pages.shape) / 8
+    qb = W.f32_to_bf16_bits(q.astype(np.float32))
+    kb = W.f32_to_bf16_bits(k.astype(np.float32)) if dtype == "bf16" else W.to_e4m3(k)
+    back = A.bf16_to_f64(kb) if dtype == "bf16" else A.e4m3_to_f64(kb)
+    assert np.array_equal(A.bf16_to_f64(qb), q) and np.array_equal(back, k)
+    return dataclasses.replace(b, q=qb), q, kb
+
+
+@pytest.mark.parametrize("cap,gain", [(0.0, 1), (0.0, 8), (2.0, 1), (5.0, 1), (30.0, 1), (30.0, 4), (64.0, 8), (65.0, 8), (100.0, 8), (1e4, 1), (1e4, 8),
+                                      (1e6, 1), (1e30, 8)])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lq,lkv", [([1, 1, 2], [300, 77, 512]), ([70, 130], [300, 600])], ids=["rows", "tiles"])
+def test_key_weights_of_exact_products(lq, lkv, dtype, cap, gain):
+    """Soft-caps from saturation to none at all, on both sides of where the tanh changes its form, at a bound that a
+    coarser exponential or tanh would miss."""
+    torch = torch_mod()
+    hq, hk = 8, 2
+    b, q, k = exact_case(lq, lkv, hq, hk, dtype, gain)
+    lse = lse_of(b, q, k, 1.0, -1, cap, "HND")
+    ws = workspace(b, cap=cap, dtype=dtype)
+    w = torch.zeros(b.num_pages, hk, 16, device="cuda")
+    ws.key_weights(bf16(b.q), bf16(k) if dtype == "bf16" else dev(k), dev(lse), w, 0.0, True)
+    torch.cuda.synchronize()
+    assert ws.get_error() == 0
+    ref, _ = C.key_weights(b, q, k, lse, np.zeros(w.shape), 0.0, True, cap=cap)
+    # largest |logit| before and after the cap and largest |lse|, in powers of two
+    keys = [A.gather_kv(k, b.kv_indptr, b.kv_indices, n, 16, i, h, "HND") for i, n in enumerate(lkv) for h in range(hk)]
+    raw = max(float(np.abs(q[int(b.qo_indptr[i // hk]):int(b.qo_indptr[i // hk + 1]), 4 * (i % hk):4 * (i % hk) + 4] @ x.T).max())
+              for i, x in enumerate(keys)) / np.sqrt(128)
+    x2 = (cap * np.tanh(raw / cap) if cap else raw) / np.log(2)
+    l2 = float(np.abs(lse[np.isfinite(lse)]).max()) / np.log(2)
+    unit = 2.0 ** -24
+    # error of the exponent: -lse in powers of two (constant, product), the last sum, and the logit:
+    steps = 2 * l2 + (x2 + l2)
+    if not cap:
+        steps += 4 * x2  # log2 e, the root, their quotient, the product
+    elif cap <= 64:
+        # tanh by exponentials: at most 2^-21 (2^-22 of its exponential, 2^-23 of the reciprocal, twice); its argument's eight
+        # roundings times y (1 - tanh(y)^2) < 0.45; the cap's own two and the product
+        steps += cap / np.log(2) * (8 + 8 * 0.45) + 3 * x2
+    else:
+        # relative: sixteen roundings through the series; by exponentials 2^-21 of at least 0.244
+        steps += x2 * (16 if raw <= cap / 4 else 48)
+    n = max(lq) * (hq // hk) + 16  # additions of one sum
+    tol = np.log(2) * steps * unit + 2.0 ** -22 + n * unit
+    got = w.cpu().numpy().astype(np.float64)
+    assert (np.abs(got - ref) <= ref * tol + 1e-30).all(), (float((np.abs(got - ref) / np.maximum(ref, 1e-30)).max()), tol)
+
+
 # ---- selection -------------------------------------------------------------------------------------
 
 SELECT = [
