@@ -121,10 +121,11 @@ def _need(ok, what: str):
         raise ValueError(what)
 
 
-def _dense_error(t, name: str, dtypes, shape):
-    """Says what is wrong with a tensor argument that should be dense, on the GPU, of a type and shape."""
+def _dense_error(t, name: str, dtypes, shape, device):
+    """Says what is wrong with a tensor argument that should be dense, on the workspace's GPU, of a type and shape."""
     _need(t.dtype in dtypes, f"{name}: {t.dtype}, expected {' or '.join(map(str, dtypes))}")
     _need(t.is_cuda, f"{name}: a CUDA tensor is needed")
+    _need(t.get_device() == device, f"{name}: on GPU {t.get_device()}, the workspace is on GPU {device}")
     _need(tuple(t.shape) == tuple(shape), f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     raise ValueError(f"{name}: a contiguous tensor is needed")
 
@@ -197,6 +198,8 @@ class Workspace:
         self._h = c_void_p(0)
         _check(lib().fi_workspace_create(max_batch, max_total_q, max_kv_pages, num_qo_heads, num_kv_heads, head_dim,
                                          num_sms, ctypes.byref(self._h)), "fi_workspace_create")
+        import torch
+        self._device = torch.cuda.current_device()  # where the workspace was just made
         self.num_qo_heads, self.num_kv_heads, self.head_dim = num_qo_heads, num_kv_heads, head_dim
         self._layout, self._kv_dtype = "HND", "bf16"
         self._plan = None  # (total_q, batch, page_size, layout, kv_dtype) of the current plan
@@ -291,18 +294,18 @@ class Workspace:
 
     # every argument is checked in one expression; the slow path says what is wrong with it
     def _dense(self, t, name, dtypes, shape) -> int:
-        if t.dtype in dtypes and t.is_cuda and t.shape == shape and t.is_contiguous():
+        if t.dtype in dtypes and t.get_device() == self._device and t.shape == shape and t.is_contiguous():
             return t.data_ptr()
-        _dense_error(t, name, dtypes, shape)
+        _dense_error(t, name, dtypes, shape, self._device)
 
     def _rows(self, t, name, shape):
         """A tensor of shape [total_q, heads, 128] with dense heads: (pointer, token stride in elements)."""
-        if t.dtype in self._bf16 and t.is_cuda and t.shape == shape:
+        if t.dtype in self._bf16 and t.get_device() == self._device and t.shape == shape:
             st = t.stride()
             if st[2] == 1 and (st[1] == shape[2] or shape[1] == 1):
                 return t.data_ptr(), (st[0] if shape[0] > 1 else max(st[0], shape[1] * shape[2]))
             raise ValueError(f"{name}: the heads of a token must be contiguous")
-        _dense_error(t, name, self._bf16, shape)
+        _dense_error(t, name, self._bf16, shape, self._device)
 
     def append(self, q, k, v, k_pages, v_pages, q_out, q_weight=None, k_weight=None, eps=1e-6, positions=None,
                stream=None):

@@ -71,3 +71,51 @@ def test_null_workspace_and_pointers():
     assert L.fi_select_keys(z, z, 0, 0, 0, 1, z, z) == 1
     assert L.fi_compact(z, z, 1, z, z, z, 0, z) == 1
     assert L.fi_cache_plan_compute(None, None, None, None, 0, 1, None, None) == 1
+
+
+class OnGpu:
+    """Stands for a dense CUDA tensor of a GPU (there is none here): what the binding asks of a tensor, and no memory."""
+
+    def __init__(self, shape, dtype, gpu):
+        self.shape, self.dtype, self.gpu, self.is_cuda = shape, dtype, gpu, True
+
+    def get_device(self):
+        return self.gpu
+
+    def stride(self):
+        return tuple(int(np.prod(self.shape[i + 1:])) for i in range(len(self.shape)))
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 0
+
+
+@pytest.mark.parametrize("which", range(13))
+def test_tensors_of_another_gpu_are_refused(which):
+    """Each tensor of each cache operator on GPU 1, the others and the workspace on GPU 0."""
+    torch = pytest.importorskip("torch")
+    ws = B.Workspace.__new__(B.Workspace)
+    ws._h, ws._device = ctypes.c_void_p(0), 0
+    ws.num_qo_heads, ws.num_kv_heads, ws.head_dim = 4, 2, 128
+    ws._plan, ws._shapes_of = (3, 3, 16, "HND", "bf16"), None
+    made = 0
+
+    def t(shape, dtype=torch.bfloat16):
+        nonlocal made
+        made += 1
+        return OnGpu(shape, dtype, int(made - 1 == which))
+
+    q, k, v, out = t((3, 4, 128)), t((3, 2, 128)), t((3, 2, 128)), t((3, 4, 128))
+    kp, vp = t((9, 2, 16, 128)), t((9, 2, 16, 128))
+    wq, wk, pos = t((128,)), t((128,)), t((3,), torch.int32)
+    lse, w, kept, none = t((3, 4), torch.float32), t((9, 2, 16), torch.float32), t((3, 2, 8), torch.int32), t((1,))
+    assert made == 13
+    uses = {ws.append: (q, k, v, kp, vp, out, wq, wk, 1e-6, pos), ws.key_weights: (q, kp, lse, w), ws.select_keys: (w, 8, kept),
+            ws.compact: (kept, kp, vp, w)}
+    for call, args in uses.items():
+        away = any(getattr(a, "gpu", 0) for a in args)
+        with pytest.raises(ValueError if away else B.FiError) as e:
+            call(*args, stream=0)
+        assert "on GPU 1, the workspace is on GPU 0" in str(e.value) if away else e.value.status == 1  # no workspace behind it
