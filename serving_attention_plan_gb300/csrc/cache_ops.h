@@ -132,6 +132,7 @@ struct WeightsParams {
   float* part;          // [CTAs][2][256] partial sums of items cut between CTAs
   uint32_t* part_count; // [CTAs], zero between launches
 };
+constexpr int kRowsMostWarps = 16;  // most warps of a CTA of the row form
 int launch_weights_rows(const WeightsParams& p, bool fp8, int64_t most_blk, int num_sms, cudaStream_t stream);
 
 int launch_weights_tc(const WeightsParams& p, int total_q, bool fp8, int num_sms, cudaStream_t stream);

@@ -164,11 +164,12 @@ int check_cache_call(const fi_workspace* ws, int num_pages) {
   return dev == ws->device ? FI_OK : FI_ERR_INVALID_ARG;
 }
 
-// Whether a capture is under way on the stream.  A captured launch serves later plans: it is made even where the plan
-// at hand leaves it nothing to do, and needs every pointer that a plan with tokens and keys needs.
-int is_capturing(cudaStream_t s, bool* on) {
+// Whether a capture is under way on the stream, where the launch could depend on it.  A captured launch serves later
+// plans: it is made even where the plan at hand leaves it nothing to do, for the workspace's capacity, and needs every
+// pointer that a plan with tokens and keys needs.  (Asking takes 0.1 us of the 4 to 6 that a call takes the host.)
+int is_capturing(cudaStream_t s, bool could_matter, bool* on) {
   cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-  FI_CUDA(cudaStreamIsCapturing(s, &st));
+  if (could_matter) FI_CUDA(cudaStreamIsCapturing(s, &st));
   *on = st != cudaStreamCaptureStatusNone;
   return FI_OK;
 }
@@ -789,7 +790,7 @@ int fi_append(fi_workspace* ws, const void* q, int64_t q_stride, const void* k, 
   const int total_q = ws->plan_total_q;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   bool captured = false;
-  st = is_capturing(s, &captured);
+  st = is_capturing(s, total_q < ws->max_total_q || k_pages == nullptr || v_pages == nullptr, &captured);
   if (st != FI_OK) return st;
   if (total_q == 0 && !captured) return FI_OK;
   const int64_t dq = int64_t(ws->hqo) * fi::kHeadDim, dkv = int64_t(ws->hkv) * fi::kHeadDim;
@@ -835,7 +836,9 @@ int fi_key_weights(fi_workspace* ws, const void* q, const void* k_pages, int num
   if (!(decay >= 0.f && decay <= 1.f) || (new_keys != 0 && new_keys != 1)) return FI_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   bool captured = false;
-  st = is_capturing(s, &captured);
+  const bool tensor = ws->header[fi::H_PATH] == fi::kPathTensor && ws->hqo / ws->hkv <= fi::kWeightTileRows;
+  const bool full = ws->geo.blocks * ws->hkv >= int64_t(fi::kRowsMostWarps) * ws->num_sms;  // the row form's grid
+  st = is_capturing(s, tensor || !full || q == nullptr || lse == nullptr, &captured);
   if (st != FI_OK) return st;
   if (ws->plan_nnz - ws->plan_nnz_shared == 0 && !captured) return FI_OK;  // no key to weigh
   if (k_pages == nullptr || weights == nullptr || ((ws->plan_total_q > 0 || captured) && (q == nullptr || lse == nullptr)))
@@ -864,7 +867,7 @@ int fi_key_weights(fi_workspace* ws, const void* q, const void* k_pages, int num
   p.window_left = std::min(var.window_left, 1 << 30);  // no request has more keys
   // a batch that needs the tensor cores is split by request (a group of more than 128 heads does not fit their
   // tile); a captured launch has to serve later plans of the path, so it gets both kernels
-  if (ws->header[fi::H_PATH] == fi::kPathTensor && p.group <= fi::kWeightTileRows) {
+  if (tensor) {
     p.tile_tokens = fi::kWeightTileRows / p.group;
     p.part = reinterpret_cast<float*>(ws->dbuf + ws->off_wpart);
     p.part_count = reinterpret_cast<uint32_t*>(ws->dbuf + ws->off_wcount);
@@ -886,7 +889,7 @@ int fi_select_keys(fi_workspace* ws, const float* weights, int num_pages, int32_
   const int batch = ws->header[fi::H_BATCH];
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   bool captured = false;
-  st = is_capturing(s, &captured);
+  st = is_capturing(s, batch < ws->max_batch || weights == nullptr, &captured);
   if (st != FI_OK) return st;
   if (batch == 0 && !captured) return FI_OK;
   if (kept == nullptr || ((ws->plan_nnz - ws->plan_nnz_shared > 0 || captured) && weights == nullptr))
@@ -910,7 +913,7 @@ int fi_compact(fi_workspace* ws, const int32_t* kept, int32_t budget, void* k_pa
   const int batch = ws->header[fi::H_BATCH];
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   bool captured = false;
-  st = is_capturing(s, &captured);
+  st = is_capturing(s, batch < ws->max_batch || ws->plan_nnz - ws->plan_nnz_shared == 0, &captured);
   if (st != FI_OK) return st;
   if ((batch == 0 || ws->plan_nnz - ws->plan_nnz_shared == 0) && !captured) return FI_OK;
   if (kept == nullptr || k_pages == nullptr || v_pages == nullptr || misaligned(kept, 4) || misaligned(k_pages, 16) ||

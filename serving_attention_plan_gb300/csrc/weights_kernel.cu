@@ -31,7 +31,7 @@ namespace {
 // each: 8 x 3 x 8 KB of bf16, 16 x 3 x 4 KB of e4m3, whose conversions need more warps (2 x 115 K
 // keys: 54 us, with 8 x 6 units 69).
 template <bool kFp8>
-constexpr int kRowsWarps = kFp8 ? 16 : 8;
+constexpr int kRowsWarps = kFp8 ? kRowsMostWarps : 8;
 template <bool kFp8>
 constexpr int kAhead = 3;
 constexpr unsigned kAll = 0xffffffffu;
