@@ -154,7 +154,8 @@ int fi_workspace_set_variant(fi_workspace* ws, int32_t window_left, float logits
  * codes to f16 in shared memory (exactly), convert q to f16 there and run f16
  * MMAs; they take the page sizes of bf16 pages.  Composable plans (fi_plan_composable) take
  * e4m3 HND pages of a power-of-two size.  fi_plan returns UNSUPPORTED
- * otherwise.  NaN codes in the pages give undefined rows.  Errors: INVALID_ARG.
+ * otherwise.  NaN codes in the pages give undefined rows.  q is exact in f16 from 2^-14
+ * to 65504; smaller values lose bits, larger ones become infinite.  Errors: INVALID_ARG.
  */
 int fi_workspace_set_kv_dtype(fi_workspace* ws, int32_t kv_dtype, float k_scale, float v_scale);
 
@@ -387,7 +388,9 @@ int fi_append(fi_workspace* ws, const void* q, int64_t q_stride, const void* k, 
  *   the query heads of KV head h of exp(logit(t, head, j) - lse[t, head])
  *
  * for every key of every request; the logit is fi_run's (scale, soft-cap, mask, window, k_scale).  Rows
- * with lse = -inf (no key) add nothing.  Keys that no row sees are decayed too.
+ * with lse = -inf (no key) add nothing.  Keys that no row sees are decayed too.  With e4m3 pages q is rounded to
+ * f16, as in fi_run, for requests of at most 64 query rows (tokens x heads of a group) and for groups of more than
+ * 128 heads; other requests keep it in bf16.  The two differ where |q| lies outside f16's range, 2^-14 to 65504.
  *
  *   q, k_pages, lse   as given to / written by fi_run
  *   decay        in [0, 1]; 1 keeps plain sums; 0 ignores the old contents (NaN included)

@@ -14,9 +14,9 @@
 // one step ahead of the rows, and shared by all its heads through shared memory.
 //
 // Angles: a position times a frequency is taken in turns as a 64-bit fraction, p * F mod 2^64 with
-// F = round(2^64 frac(f / 2 pi)): whole turns drop out exactly in the integer product, so the angle
-// is right to 2^-33 turns + the rounding of F (p * 2^-65) at any position, where a 32-bit product
-// loses the angle itself beyond some ten thousand positions.
+// F = 2^64 frac(f / 2 pi): whole turns drop out exactly in the integer product.  What is left is the rounding of
+// the product's upper half to 24 bits (2^-26 turns) and that of F, a quotient of doubles (p * 2^-55 turns for
+// f <= 1: as much again at p = 2^29), where a 32-bit product loses the angle itself beyond some ten thousand positions.
 #include <cuda_fp8.h>
 
 #include <algorithm>

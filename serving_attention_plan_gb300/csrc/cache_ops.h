@@ -15,7 +15,7 @@ struct Geo {
   int32_t q0, lq;    // first query token, query tokens
   int32_t kv0, lkv;  // first entry in the page list, keys
   int32_t blk0;      // 32-key blocks of the requests before this one that take the row form of the weights
-  int32_t tile0;     // 256-key tiles of the requests before this one
+  int32_t tile0;     // 256-key tiles of the requests before this one (told by fi_cache_plan_compute, read by no kernel)
   int32_t work0;     // tensor-core weights: Q tiles (over all KV heads) of the requests before this one
   int32_t pad;
 };
@@ -53,10 +53,7 @@ struct GeoTotals {
   bool ok = false;     // the counts below fit the entries' 32-bit fields
   int64_t blocks = 0;  // 32-key blocks (of the row form, once split)
   int64_t work = 0;    // Q tiles of the tensor-core form
-  int64_t tiles = 0;   // 256-key tiles
   int32_t max_lkv = 0;
-  int32_t max_lq = 0;
-  bool work_ok = false;  // the Q tiles were counted and fit 32 bits
 };
 // The entries [0, batch] of a validated batch (cache_plan.cpp, host only, like the two checks).
 GeoTotals fill_geo(const int32_t* qo_indptr, const int32_t* kv_indptr, const int32_t* last_page_len, int batch,

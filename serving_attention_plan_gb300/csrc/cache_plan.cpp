@@ -12,12 +12,13 @@ namespace fi {
 GeoTotals fill_geo(const int32_t* qo_indptr, const int32_t* kv_indptr, const int32_t* last_page_len, int batch,
                    int page_size, Geo* out) {
   GeoTotals t;
+  int64_t tiles = 0;
   for (int i = 0; i <= batch; ++i) {
     Geo g{};
     g.q0 = qo_indptr[i];
     g.kv0 = kv_indptr[i];
     g.blk0 = int32_t(t.blocks);
-    g.tile0 = int32_t(t.tiles);
+    g.tile0 = int32_t(tiles);
     if (i < batch) {
       const int32_t pages = kv_indptr[i + 1] - kv_indptr[i];
       // at most 2^30, as the planner accepts
@@ -25,9 +26,8 @@ GeoTotals fill_geo(const int32_t* qo_indptr, const int32_t* kv_indptr, const int
       g.lq = qo_indptr[i + 1] - qo_indptr[i];
       g.lkv = int32_t(keys);
       t.blocks += (keys + kBlkKeys - 1) / kBlkKeys;
-      t.tiles += (keys + kTileKeys - 1) / kTileKeys;
+      tiles += (keys + kTileKeys - 1) / kTileKeys;
       t.max_lkv = std::max(t.max_lkv, g.lkv);
-      t.max_lq = std::max(t.max_lq, g.lq);
     }
     out[i] = g;
   }
@@ -64,7 +64,6 @@ void split_weights(Geo* geo, int batch, int hkv, int group, int row_limit, bool 
   }
   totals->blocks = blocks;
   totals->work = work;
-  totals->work_ok = true;
 }
 
 int check_pages_once(const int32_t* a, int64_t na, const int32_t* b, int64_t nb, int32_t max_page) {

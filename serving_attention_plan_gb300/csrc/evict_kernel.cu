@@ -25,8 +25,9 @@ __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// An arrival that publishes no writes: enough to say that this thread's reads have come back.  (The release
-// form waits for the thread's stores as well.)
+// An arrival that publishes no writes.  It says that this thread's reads have come back, and rests on a wait that comes
+// before it (cp.async.wait_group, or a use of the value): the barrier itself orders nothing then.  (The release form
+// waits for the thread's stores as well.)
 __device__ __forceinline__ void cluster_arrive_relaxed() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
@@ -600,7 +601,7 @@ int launch_select(SelectParams p, int batch, int most_batch, int max_lkv, int nu
       attr = cudaFuncSetAttribute(select_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, 48 * 1024 * 4);
   });
   if (attr != cudaSuccess) return record_cuda_error(attr, "cudaFuncSetAttribute(select_kernel)");
-  // short rows take 256 threads, six to an SM; long ones, and clusters, 1024
+  // short rows take 256 threads, six to an SM up to 2900 keys and five to 4096; long ones, and clusters, 1024
   const bool wide = cluster > 1 || max_lkv > 4096;
   // rows of later plans of a captured launch: CTAs that fit the GPU at once, and that do nothing otherwise
   const int64_t later = std::min<int64_t>(int64_t(most_batch) * p.pv.hkv, std::max(1, wide ? num_sms / int(cluster) : 4 * num_sms));

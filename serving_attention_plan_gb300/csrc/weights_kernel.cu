@@ -10,7 +10,7 @@
 // the lane (asynchronous copies, no registers, no barrier), several units ahead; page ids are fetched one
 // unit earlier still.  (With the fragments loaded straight into registers a warp had one unit in flight
 // behind its look-ups: 115 us for 128 requests of U[1, 4096] keys and 88 us for 2 x 115 K keys of e4m3 at page size
-// 1, now 93 (0.92 of the copy rate) and 54.)
+// 1, now 95 (0.90 of the copy rate) and 56.)
 // The keys sit on the 16-row side and 8 query rows on the other; K stays in registers while the warp walks
 // over the query rows in groups of 8, so the form is right for any number of rows.  Query fragments
 // of at most 8 rows are kept from unit to unit while the request and head stay the same, which the unit order makes
@@ -29,7 +29,7 @@ namespace {
 
 // Warps of a CTA (one CTA per SM), multiples of eight so that a warp mostly keeps its head, and units in flight of
 // each: 8 x 3 x 8 KB of bf16, 16 x 3 x 4 KB of e4m3, whose conversions need more warps (2 x 115 K
-// keys: 54 us, with 8 x 6 units 69).
+// keys: 56 us, with 8 x 6 units 69).
 template <bool kFp8>
 constexpr int kRowsWarps = kFp8 ? kRowsMostWarps : 8;
 template <bool kFp8>

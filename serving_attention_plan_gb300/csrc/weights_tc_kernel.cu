@@ -16,9 +16,12 @@
 // a 128 x 256 tile takes 1376 clocks this way, 1200 + the -lse step the other way.
 //
 // What bounds it: the products (1376 clocks a tile, above) beside 32768 exponentials (1024 clocks at 32 a
-// clock and SM); both run at the same time, over two score buffers.  Measured: 1490-1640 clocks a tile, 1.35
-// PFLOP/s (0.70 of the bf16 burst rate) on four prompts of 2000 to 4096 tokens.  A share of the exponentials by a
-// polynomial on the multiply-add pipe made it slower (an eighth 145 us, a quarter 152, none 138).
+// clock and SM); both run at the same time, over two score buffers.  Measured: 1490-1640 clocks a tile, on four
+// prompts of 1024 to 4096 tokens 123 us: 1.12 PFLOP/s of visible pairs (0.59 of the bf16 burst rate; tiles cut by the
+// diagonal are computed whole).  A share of the exponentials by a polynomial on the multiply-add pipe made it slower
+// (an eighth 145 us, a quarter 152, where none took 138).
+//   e4m3: the key loader's widening does not fit its 64 registers (174 to 214 bytes spilled, in all e4m3 variants), and its
+// loads come in eight rounds of four a lane and item; 128 requests of 128 rows take 776 us, 361 with bf16 pages.
 //
 // Work split: the Q tiles of all items lie on one line, request by request, KV head by KV head, key
 // tile by key tile (the causal mask gives later key tiles fewer Q tiles); CTA c takes the c-th
