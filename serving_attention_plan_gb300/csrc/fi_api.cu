@@ -10,6 +10,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <limits>
 #include <mutex>
 #include <new>
 #include <string>
@@ -820,8 +821,10 @@ int fi_append(fi_workspace* ws, const void* q, int64_t q_stride, const void* k, 
   p.k_pages = k_pages;
   p.v_pages = v_pages;
   p.eps = eps;
-  p.k_inv_scale = 1.f / ws->plan_variant.k_scale;
-  p.v_inv_scale = 1.f / ws->plan_variant.v_scale;
+  // a scale below 2^-128 has no finite reciprocal; with the largest one zeros stay zeros (infinity makes them NaN), and
+  // of the others only elements below 2e-36 would be stored otherwise
+  p.k_inv_scale = std::min(1.f / ws->plan_variant.k_scale, std::numeric_limits<float>::max());
+  p.v_inv_scale = std::min(1.f / ws->plan_variant.v_scale, std::numeric_limits<float>::max());
   p.hqo = ws->hqo;
   p.rotary = ws->rotary;
   p.interleaved = ws->interleaved;

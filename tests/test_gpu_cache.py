@@ -836,6 +836,24 @@ def test_composable_plan():
     assert np.array_equal(bits(kp), want) and ws.get_error() == 0
 
 
+
+def test_append_smallest_scales():
+    """Scales whose reciprocal is beyond 32 bits: everything saturates, zeros stay zero."""
+    torch = torch_mod()
+    b = batch_of([1, 1], [4, 7], 2, 1, 4)
+    ws = workspace(b, dtype="e4m3", scales=(1e-40, 1e-44))
+    q = torch.randn(2, 2, 128, device="cuda").to(torch.bfloat16)
+    k = torch.zeros(2, 1, 128, device="cuda", dtype=torch.bfloat16)
+    k[:, :, 1], k[:, :, 2] = 0.5, -3.0
+    kp, vp = (torch.full((b.num_pages, 1, 4, 128), 1.0, device="cuda").to(torch.float8_e4m3fn) for _ in range(2))
+    ws.append(q, k, k, kp, vp, torch.empty_like(q))
+    torch.cuda.synchronize()
+    _, page, slot, _ = C.append_places(b)
+    for pool in (kp, vp):
+        rows = pool.float().cpu()[page, 0, slot]
+        assert (rows[:, 1] == 448).all() and (rows[:, 2] == -448).all() and (rows[:, 0] == 0).all() and (rows[:, 3:] == 0).all()
+
+
 # ---- refusals --------------------------------------------------------------------------------------
 
 
