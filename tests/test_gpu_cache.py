@@ -837,6 +837,108 @@ def test_composable_plan():
 
 
 
+@pytest.mark.parametrize("lq,lkv,dtype,layout", [([1, 1, 2, 1], [300, 77, 513, 40], "bf16", "HND"), ([1, 1], [200, 900], "e4m3", "NHD"),
+                                                 ([130, 1, 40], [300, 500, 40], "bf16", "NHD"), ([200, 9], [700, 130], "e4m3", "HND")])
+def test_replays_skip_pages_outside_the_pool(lq, lkv, dtype, layout):
+    """Append, weights and compaction replayed after a plan with pages that the captured pool does not have: the error bit is
+    set, keys of those pages are left alone, all others get what they should."""
+    from serving_attention_plan_gb300 import binding as B
+    torch = torch_mod()
+    hq, hk, ps, budget, scale = 8, 2, 16, 33, 0.03125 if dtype == "e4m3" else 1.0
+    b = batch_of(lq, lkv, hq, hk, ps, True, seed=6, extra=0)
+    n, pages = b.batch_size, b.num_pages
+    rng = np.random.default_rng(8)
+    k = b.k_pages if dtype == "bf16" else W.to_e4m3(A.bf16_to_f64(b.k_pages) / scale)
+    k = as_layout(k, layout)
+    pool = lambda: bf16(k) if dtype == "bf16" else dev(k)
+    host = (lambda t: bits(t)) if dtype == "bf16" else (lambda t: t.cpu().numpy())
+    lost = rng.random(b.kv_indices.shape[0]) < 0.4
+    lost[0], lost[-1] = True, False
+    idx = np.where(lost, b.kv_indices + pages, b.kv_indices).astype(np.int32)
+    ws = workspace(b, layout=layout, dtype=dtype, scales=(scale, scale))
+    side = torch.cuda.Stream()
+    plan = lambda idx: ws.plan(b.qo_indptr, b.kv_indptr, idx, b.last_page_len, ps, True, stream=side)
+    x = torch.randn(b.total_q, hk, 128, device="cuda").to(torch.bfloat16)
+    q, out = bf16(b.q), torch.zeros(b.total_q, hq, 128, device="cuda", dtype=torch.bfloat16)
+    qd = A.bf16_to_f64(b.q)
+    lse = lse_of(b, qd, k, scale, -1, 0.0, layout)
+    old = rng.random((pages, hk, ps)).astype(np.float32)
+    kept = np.full((n, hk, budget), -1, np.int32)
+    for i, length in enumerate(lkv):
+        for h in range(hk):
+            m = min(length, budget)
+            kept[i, h, :m] = np.sort(rng.choice(length, m, replace=False))
+    kp, vp, w, ck, cv, cw = pool(), pool(), dev(old), pool(), pool(), dev(old)
+    lse_d, kept_d = dev(lse), dev(kept)
+    torch.cuda.synchronize()
+    graphs = []
+    for call in (lambda: ws.append(q, x, x, kp, vp, out, stream=side), lambda: ws.key_weights(q, ck, lse_d, w, 0.5, True, stream=side),
+                 lambda: ws.compact(kept_d, ck, cv, cw, stream=side)):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=side):
+            call()
+    plan(idx)
+    for g in graphs:
+        before = [host(kp), host(vp)] if g is graphs[0] else None
+        with torch.cuda.stream(side):
+            g.replay()
+        side.synchronize()
+        err = ws.get_error()
+        if g is graphs[0]:
+            tok, page, slot, key = C.append_places(b)
+            entry = np.concatenate([int(b.kv_indptr[i]) + key[int(b.qo_indptr[i]):int(b.qo_indptr[i + 1])] // ps for i in range(n)])
+            here = ~lost[entry[tok]]
+            assert err == (0 if here.all() else B.DEVERR_PAGE_OOB) and torch.equal(out, q)
+            rows = x if dtype == "bf16" else (x.float() / scale).clamp(-448, 448).to(torch.float8_e4m3fn)
+            rows = bits(rows) if dtype == "bf16" else rows.view(torch.uint8).cpu().numpy()
+            for got, want in zip((host(kp), host(vp)), before):
+                if layout == "HND":
+                    want[page[here], :, slot[here]] = rows[tok[here]]
+                else:
+                    want[page[here], slot[here]] = rows[tok[here]]
+                assert np.array_equal(got, want)
+        elif g is graphs[1]:
+            assert err == B.DEVERR_PAGE_OOB
+            # (the weights read a pool whose pages hold the plan's keys; compaction comes after)
+            ref, reach = C.key_weights(b, qd, k, lse, old, 0.5, True, scale, layout=layout)
+            got = w.cpu().numpy()
+            gone = np.zeros(pages, bool)
+            gone[b.kv_indices[lost]] = True
+            used = np.zeros((pages, ps), bool)
+            for i, length in enumerate(lkv):
+                used[C.places(b, i, np.arange(length))] = True
+            used[gone] = False
+            tol = weights_tol(reach, lse) + 1000 * 2.0 ** -24
+            err_w, lim = np.abs(got - ref).transpose(0, 2, 1), (ref * tol + 1e-30).transpose(0, 2, 1)
+            assert (err_w[used] <= lim[used]).all()
+            assert np.array_equal(got.transpose(0, 2, 1)[~used], old.transpose(0, 2, 1)[~used])
+        else:
+            assert err == B.DEVERR_PAGE_OOB
+            rk, rw = k.copy(), old.copy()
+            for i, length in enumerate(lkv):
+                if length <= budget:
+                    continue
+                for h in range(hk):
+                    j = np.arange(budget)
+                    src = kept[i, h]
+                    at = int(b.kv_indptr[i])
+                    ok = ~lost[at + j // ps] & ~lost[at + src // ps]
+                    tp, ts = C.places(b, i, j[ok])
+                    fp, fs = C.places(b, i, src[ok])
+                    if layout == "HND":
+                        rk[tp, h, ts] = k[fp, h, fs]
+                    else:
+                        rk[tp, ts, h] = k[fp, fs, h]
+                    rw[tp, h, ts] = old[fp, h, fs]
+            assert np.array_equal(host(ck), rk) and np.array_equal(host(cv), rk) and np.array_equal(cw.cpu().numpy(), rw)
+
+
+@pytest.mark.parametrize("lq,lkv,dtype", [([1, 2, 1], [37, 64, 1], "bf16"), ([90, 1, 300], [90, 70, 700], "bf16"), ([90, 200], [400, 200], "e4m3")])
+def test_key_weights_window_of_zero(lq, lkv, dtype):
+    """A window of zero: every token sees the key of its own position alone."""
+    test_key_weights((lq, lkv, 8, 2, 16, True, dtype, "HND", 0, 0.0, 0.5, False, 0))
+
+
 def test_append_smallest_scales():
     """Scales whose reciprocal is beyond 32 bits: everything saturates, zeros stay zero."""
     torch = torch_mod()
