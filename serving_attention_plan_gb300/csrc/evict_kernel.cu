@@ -50,7 +50,7 @@ __device__ __forceinline__ uint32_t peer_word(const void* local, unsigned rank) 
 // narrow the threshold down by counting.  Counts are integers, so shared-memory atomics do not
 // change the result.  A pass ends the search when all keys of its bin stay, which without many equal weights
 // the second does.  The kept positions come out ascending by ranking (greater, equal) counts over the range in
-// order, four positions a thread.  Measured: 64 x 8 rows of 2 to 4 K keys 14.5 us, 8 rows of 131 K 17 us; the look-ups and
+// order, four positions a thread.  Measured: 64 x 8 rows of 2 to 4 K keys 15.2 us, 8 rows of 131 K 17.8 us; the look-ups and
 // weights of a row take a third of that, the rest is a chain of counting steps.  Weights are read from memory once (the slice of the range that a CTA owns
 // stays in shared memory); a cluster of CTAs shares a row when there are few rows.
 //   Where pages hold whole groups of four slots, a thread fetches four weights at a time (one page id, one 16-byte
@@ -584,7 +584,7 @@ int launch_select(SelectParams p, int batch, int most_batch, int max_lkv, int nu
   if (batch == 0) batch = most_batch;  // captured on an empty plan
   const int rows = batch * p.pv.hkv;
   p.by_four = p.pv.page_size % 4 == 0 && reinterpret_cast<uintptr_t>(p.weights) % 16 == 0;
-  // a cluster shares a row while there are SMs for it (131 K keys of 8 heads: 8 CTAs 17 us), or as long as a slice does
+  // a cluster shares a row while there are SMs for it (131 K keys of 8 heads: 8 CTAs 17.8 us), or as long as a slice does
   // not fit into shared memory and would be read again in each pass (16 x 8 rows of 100 K keys: 81 us, 121 without)
   unsigned cluster = 1;
   while (cluster < 8 && ((int64_t(rows) * cluster * 2 <= num_sms && max_lkv / int(cluster) > 4096) ||
