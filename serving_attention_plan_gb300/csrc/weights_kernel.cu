@@ -90,7 +90,10 @@ __device__ __forceinline__ void load_q(const __nv_bfloat16* row, int t, uint32_t
   }
 }
 
-template <bool kFp8, bool kVar>
+// Variant of a kernel: none, a window or soft-cap, or a soft-cap above kExpTanhMostCap (with or without a window).
+enum Var { kVarNone = 0, kVarOn, kVarWideCap };
+
+template <bool kFp8, int kVar>
 __global__ void __launch_bounds__(32 * kRowsWarps<kFp8>, 1) weights_rows_kernel(const __grid_constant__ WeightsParams p) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   RowsSmem<kFp8>& sm = *reinterpret_cast<RowsSmem<kFp8>*>(smem_raw);
@@ -253,9 +256,11 @@ __global__ void __launch_bounds__(32 * kRowsWarps<kFp8>, 1) weights_rows_kernel(
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           float x = acc[i >> 1][2 * (i & 1) + c] * p.scale_log2;
-          if (kVar && p.cap_log2 > 0.f) {
+          if constexpr (kVar == kVarWideCap) {
             const float y = x * p.inv_cap_log2, u = y * y;
-            x = p.cap_log2 * (p.wide_cap && u <= kNearReach ? y * tanh_near_factor(make_float2(u, u)).x : tanh_exp2(y));
+            x = p.cap_log2 * (u <= kNearReach ? y * tanh_near_factor(make_float2(u, u)).x : tanh_exp2(y));
+          } else if (kVar != kVarNone && p.cap_log2 > 0.f) {
+            x = p.cap_log2 * tanh_exp2(x * p.inv_cap_log2);
           }
           // the select drops what hidden keys and missing rows computed, NaN included
           const bool seen = key < lim[c] && (!kVar || key >= low[c]);
@@ -285,21 +290,21 @@ int launch_weights_rows(const WeightsParams& p, bool fp8, int64_t most_blk, int 
   const int64_t units = most_blk * p.pv.hkv;
   const int warps = fp8 ? kRowsWarps<true> : kRowsWarps<false>;
   const unsigned grid = unsigned(std::max<int64_t>(1, std::min<int64_t>((units + warps - 1) / warps, num_sms)));
-  const bool var = p.window_left >= 0 || p.cap_log2 > 0.f;
+  const int var = p.wide_cap ? kVarWideCap : p.window_left >= 0 || p.cap_log2 > 0.f ? kVarOn : kVarNone;
   using Kernel = void (*)(const WeightsParams);
-  static const Kernel kernels[4] = {weights_rows_kernel<false, false>, weights_rows_kernel<false, true>,
-                                    weights_rows_kernel<true, false>, weights_rows_kernel<true, true>};
+  static const Kernel kernels[6] = {weights_rows_kernel<false, kVarNone>, weights_rows_kernel<false, kVarOn>, weights_rows_kernel<false, kVarWideCap>,
+                                    weights_rows_kernel<true, kVarNone>, weights_rows_kernel<true, kVarOn>, weights_rows_kernel<true, kVarWideCap>};
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   const size_t smem[2] = {sizeof(RowsSmem<false>), sizeof(RowsSmem<true>)};
   static_assert(sizeof(RowsSmem<false>) <= 227 * 1024 && sizeof(RowsSmem<true>) <= 227 * 1024, "shared memory per CTA");
   std::call_once(once, [&] {
-    for (int i = 0; i < 4 && attr == cudaSuccess; ++i)
-      attr = cudaFuncSetAttribute(kernels[i], cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem[i >> 1]));
+    for (int i = 0; i < 6 && attr == cudaSuccess; ++i)
+      attr = cudaFuncSetAttribute(kernels[i], cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem[i / 3]));
   });
   if (attr != cudaSuccess) return record_cuda_error(attr, "cudaFuncSetAttribute(weights_rows_kernel)");
   const cudaError_t e =
-      launch_dependent(kernels[(fp8 ? 2 : 0) + (var ? 1 : 0)], grid, unsigned(32 * warps), smem[fp8 ? 1 : 0], 1, stream, p);
+      launch_dependent(kernels[(fp8 ? 3 : 0) + var], grid, unsigned(32 * warps), smem[fp8 ? 1 : 0], 1, stream, p);
   return e == cudaSuccess ? 0 : record_cuda_error(e, "weights_rows_kernel launch");
 }
 

@@ -20,7 +20,7 @@
 // prompts of 1024 to 4096 tokens 123 us: 1.12 PFLOP/s of visible pairs (0.59 of the bf16 burst rate; tiles cut by the
 // diagonal are computed whole).  A share of the exponentials by a polynomial on the multiply-add pipe made it slower
 // (an eighth 145 us, a quarter 152, where none took 138).
-//   e4m3: the key loader's widening does not fit its 64 registers (174 to 214 bytes spilled, in all e4m3 variants), and its
+//   e4m3: the key loader's widening does not fit its 64 registers (174 to 234 bytes spilled, in all e4m3 variants), and its
 // loads come in eight rounds of four a lane and item; 128 requests of 128 rows take 776 us, 361 with bf16 pages.
 //
 // Work split: the Q tiles of all items lie on one line, request by request, KV head by KV head, key
@@ -428,9 +428,21 @@ __device__ __forceinline__ void add_chunk(const uint32_t (&s)[kChunk], float nl,
   float2 th[kChunk / 2];
   if constexpr (kCap == kCapWide) {
     const float in = p.scale_log2 * p.inv_cap_log2;
+    float2 y[kChunk / 2];
+    float far = 0.f;
 #pragma unroll
-    for (int i = 0; i < kChunk / 2; ++i)
-      th[i] = tanh2_wide(__fmul2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), make_float2(in, in)));
+    for (int i = 0; i < kChunk / 2; ++i) {
+      y[i] = __fmul2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), make_float2(in, in));
+      far = fmaxf(far, fmaxf(fabsf(y[i].x), fabsf(y[i].y)));
+    }
+    // (a NaN passes fmaxf by and goes through the series as a NaN)
+    if (!__any_sync(kAll, far * far > kNearReach)) {
+#pragma unroll
+      for (int i = 0; i < kChunk / 2; ++i) th[i] = __fmul2_rn(tanh_near_factor(__fmul2_rn(y[i], y[i])), y[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kChunk / 2; ++i) th[i] = tanh2_wide(y[i]);
+    }
   } else if constexpr (kCap == kCapMixed) {
     const float in = p.scale_log2 * p.inv_cap_log2;
     float2 y[kChunk / 2], u[kPolyPairs];
