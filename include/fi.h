@@ -66,7 +66,7 @@ typedef enum fi_status {
 #define FI_DEVERR_PAGE_OOB 0x1     /* a page index >= num_pages was skipped */
 #define FI_DEVERR_WAIT_TIMEOUT 0x2 /* a pipeline wait gave up after its iteration limit */
 #define FI_DEVERR_TMEM 0x4         /* tensor-memory allocation returned an unusable address */
-#define FI_DEVERR_KEPT 0x8         /* fi_compact skipped a kept entry that is out of range or not ascending */
+#define FI_DEVERR_KEPT 0x8         /* an entry of a list was skipped: fi_compact, fi_tree_commit, fi_run_pages */
 
 typedef struct fi_workspace fi_workspace;
 
@@ -434,6 +434,112 @@ int fi_select_keys(fi_workspace* ws, const float* weights, int num_pages, int32_
  */
 int fi_compact(fi_workspace* ws, const int32_t* kept, int32_t budget, void* k_pages, void* v_pages, float* weights,
                int num_pages, void* stream);
+
+/* ---- Attention over parts of a cache ---------------------------------------------------------------
+ *
+ * Speculative decoding over long contexts: drafts attend to the pages that a cheap score selects
+ * (fi_page_bounds, fi_score_pages, fi_select_pages, fi_run_pages), the tree of drafted tokens is verified against the
+ * whole cache (fi_tree_run), and the accepted path's keys move to their places (fi_tree_commit).  All run on the workspace's
+ * current plan, with the common behaviour of the cache operators above.  Query token t of request i (l_q tokens, l_kv keys)
+ * is the key l_kv - l_q + t of its own cache, whose K and V fi_append has written.
+ */
+
+/*
+ * fi_tree_run -- attention of drafted tokens that form a tree (or any other set) behind each request's context.
+ *
+ * Query token t sees key j of its request when j < l_kv - l_q (the context), or when bit u = j - (l_kv - l_q) of its mask is
+ * set; the plan's causal flag is not looked at.  A token that shall see itself needs its own bit.  Scale, soft-cap and e4m3
+ * scales as for fi_run; the soft-cap's tanh is as exact as fi_key_weights's.  A row that sees nothing gets o = 0, lse = -inf.  A
+ * plain K of any value in a key that a row does not see (NaN, infinite) does not reach the row; a V that is not finite
+ * reaches every row of the request.
+ *
+ *   mask         DEVICE int32 [total_q, mask_words]: bit u % 32 of word u / 32; bits from l_q on are ignored
+ *   mask_words   at least ceil(l_q / 32) of the longest request (INVALID_ARG; in a replay: missing words count as zeros)
+ *   q, k_pages, v_pages, num_pages, o, lse   as for fi_run; o 16-byte aligned
+ * UNSUPPORTED: composable plans, a sliding window, page sizes other than 8, 16, 32, 64 and 128, more than 128 query heads a KV
+ * head.  A plan without query tokens: nothing is done or captured.  A replay needs the total query count of the capture.
+ * Errors: NO_PLAN, INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+int fi_tree_run(fi_workspace* ws, const void* q, const void* k_pages, const void* v_pages, int num_pages, const void* mask,
+                int32_t mask_words, void* o, float* lse, void* stream);
+
+/*
+ * fi_tree_commit -- the K and V rows of the accepted drafted tokens to the first drafted slots, in place.
+ *
+ * The slot of key l_kv - l_q + j receives the rows of key l_kv - l_q + path[i][j].  Other slots keep what they hold.  With n accepted
+ * tokens the request then has l_kv - l_q + n keys: plan it with that many.
+ *
+ *   path       DEVICE int32 [batch, path_len]: places of the tokens within their request, ascending, then -1; what follows a -1
+ *              is not read.  An entry that is not above the one before it or not in [j, l_q) is skipped (FI_DEVERR_KEPT).
+ *   path_len   >= 1; entries from l_q on are not read
+ * UNSUPPORTED: a page that takes new tokens from two requests, or that a composable plan's shared part reads.
+ * Errors: NO_PLAN, INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+int fi_tree_commit(fi_workspace* ws, const int32_t* path, int32_t path_len, void* k_pages, void* v_pages, int num_pages,
+                   void* stream);
+
+/*
+ * fi_page_bounds -- the smallest and the largest value of each dim over the keys of a page, for each KV head.
+ *
+ *   bounds     DEVICE bf16 [num_pages, num_kv_heads, 2, 128] (written for the pages visited, others keep what they hold):
+ *              [0] smallest, [1] largest; exact, NaN wins.  With e4m3 pages of the codes' values, without k_scale.
+ *   new_keys   0: every page of the plan; 1: the pages that hold the last min(l_q, l_kv) keys of a request, in
+ *              full (after fi_append or fi_tree_commit)
+ * Slots past a request's last key are not looked at.  A page that several requests list must be filled alike in all of them.
+ * Errors: NO_PLAN, INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+int fi_page_bounds(fi_workspace* ws, const void* k_pages, int num_pages, int32_t new_keys, void* bounds, void* stream);
+
+/*
+ * fi_score_pages -- an upper bound of the logits that a page's keys can have, for each query token and KV head.
+ *
+ *   scores[t][h][e] = scale * max over the query heads of KV head h of sum_d (min(q_d, 0) lo_d + max(q_d, 0) hi_d)
+ *
+ * for entry e of the page list of t's request, with scale = 1 / sqrt(128) (times k_scale); -inf for a page all of whose keys t
+ * does not see (causal plans), or that a replay skips.  No soft-cap (it keeps the order).  fp32 sums.
+ *
+ *   bounds      as fi_page_bounds writes it
+ *   scores      DEVICE float32 [total_q, num_kv_heads, row_pages]; entries from the request's page count on keep what they hold
+ *   row_pages   at least the pages of the longest request (INVALID_ARG; a replay's plan must keep to it, unchecked)
+ * UNSUPPORTED: composable plans, a sliding window.  Errors: NO_PLAN, INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+int fi_score_pages(fi_workspace* ws, const void* q, const void* bounds, int num_pages, float* scores, int32_t row_pages,
+                   void* stream);
+
+/*
+ * fi_select_pages -- the pages to attend to under a budget, for each query token and KV head.
+ *
+ * Of the n pages that hold a key that the token sees (causal plans: up to its own key): all if n <= budget, else the first `sink`,
+ * the last `recent` and, of the others, those with the largest scores; equal scores go to the lowest place in the list, NaN
+ * counts as the largest.
+ *
+ *   scores     as for fi_score_pages
+ *   selected   DEVICE int32 [total_q, num_kv_heads, budget] (written): page ids in the order of the request's list, then -1
+ * sink, recent >= 0, budget >= 1, sink + recent <= budget (else INVALID_ARG).
+ * UNSUPPORTED: composable plans, a sliding window.  Errors: NO_PLAN, INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+int fi_select_pages(fi_workspace* ws, const float* scores, int32_t row_pages, int32_t sink, int32_t recent, int32_t budget,
+                    int32_t* selected, void* stream);
+
+/*
+ * fi_run_pages -- attention of each query token and KV head over its own list of pages.
+ *
+ * The kernels are fi_run's, on a work plan that a first launch makes from the lists: equal pieces of the line of all lists for
+ * each CTA of the SM budget.  o and lse as fi_run; a token whose list is empty gets o = 0, lse = -inf.
+ *
+ *   selected   DEVICE int32 [total_q, num_kv_heads, budget]: page ids of the token's request, then -1.  The page that holds the
+ *              last key that the token sees counts up to that key and has to come last, if it is there and not full (a list with
+ *              it elsewhere, too, counts as empty, FI_DEVERR_KEPT); other pages count in full, so none behind
+ *              it may be listed.  A page listed twice counts twice.  Ids >= num_pages set FI_DEVERR_PAGE_OOB; what the rows of such a
+ *              list are then is not defined.
+ * UNSUPPORTED: composable plans, a sliding window; total_q * num_kv_heads * budget above 2^31 - 1 (in a replay: rows are not
+ * written, FI_DEVERR_KEPT); up to 8 query heads a KV head, what fi_plan refuses for decode tiles, above that page sizes other than 8,
+ * 16, 32, 64 and 128; more than 256 heads.  A replay on fi_run's tensor-core tiles (more than 8 heads) needs the total query count
+ * of the capture.
+ * Errors: NO_PLAN, INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+int fi_run_pages(fi_workspace* ws, const void* q, const void* k_pages, const void* v_pages, int num_pages,
+                 const int32_t* selected, int32_t budget, void* o, float* lse, void* stream);
 
 /*
  * fi_get_error -- read and clear the workspace's device-side error word

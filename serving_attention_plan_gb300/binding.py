@@ -64,6 +64,12 @@ def lib() -> ctypes.CDLL:
     L.fi_key_weights.argtypes = [c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_float, c_int32, c_void_p, c_void_p]
     L.fi_select_keys.argtypes = [c_void_p, c_void_p, c_int, c_int32, c_int32, c_int32, c_void_p, c_void_p]
     L.fi_compact.argtypes = [c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_void_p, c_int, c_void_p]
+    L.fi_tree_run.argtypes = [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_int32, c_void_p, c_void_p, c_void_p]
+    L.fi_tree_commit.argtypes = [c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int, c_void_p]
+    L.fi_page_bounds.argtypes = [c_void_p, c_void_p, c_int, c_int32, c_void_p, c_void_p]
+    L.fi_score_pages.argtypes = [c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_int32, c_void_p]
+    L.fi_select_pages.argtypes = [c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32, c_void_p, c_void_p]
+    L.fi_run_pages.argtypes = [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_int32, c_void_p, c_void_p, c_void_p]
     L.fi_get_error.argtypes = [c_void_p, P32]
     L.fi_plan_info.argtypes = [c_void_p, P32]
     L.fi_plan_compute.argtypes = [P32, P32, P32, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int64, c_int64,
@@ -83,7 +89,8 @@ def lib() -> ctypes.CDLL:
                  "fi_run_merge", "fi_merge_states", "fi_get_error", "fi_plan_info", "fi_plan_compute", "fi_device_sm_count",
                  "fi_decode_noalloc", "fi_decode_noalloc_get_error", "fi_plan_composable_compute",
                  "fi_plan_composable", "fi_workspace_set_rope", "fi_append", "fi_key_weights", "fi_select_keys",
-                 "fi_compact", "fi_cache_plan_compute"):
+                 "fi_compact", "fi_cache_plan_compute", "fi_tree_run", "fi_tree_commit", "fi_page_bounds", "fi_score_pages",
+                 "fi_select_pages", "fi_run_pages"):
         getattr(L, name).restype = c_int
     _LIB = L
     return L
@@ -185,6 +192,24 @@ def cache_plan_compute(qo_indptr, kv_indptr, kv_indices, last_page_len, page_siz
     return geo, bool(twice[0]), bool(twice[1])
 
 
+def tree_mask(qo_indptr, parents) -> np.ndarray:
+    """tree_run's mask of drafted trees: parents[t] is the place, within its request, of query token t's parent (before t's own), or -1
+    for a child of the context.  int32 [total_q, words]: bit u of row t says that t sees its request's token u (ancestors and itself)."""
+    qo, parents = _i32(qo_indptr), _i32(parents)
+    _need(parents.shape == (int(qo[-1]),), f"parents: shape {parents.shape}, expected {(int(qo[-1]),)}")
+    lens = np.diff(qo)
+    words = max(1, -(-int(lens.max(initial=0)) // 32))
+    mask = np.zeros((parents.shape[0], words), np.uint32)
+    for q0, n in zip(qo[:-1], lens):
+        for t in range(n):
+            up = int(parents[q0 + t])
+            _need(-1 <= up < t, f"parents[{q0 + t}] = {up}: a token's parent comes before it")
+            if up >= 0:
+                mask[q0 + t] = mask[q0 + up]
+            mask[q0 + t, t >> 5] |= np.uint32(1 << (t & 31))
+    return mask.view(np.int32)
+
+
 def device_sm_count() -> int:
     v = c_int(0)
     _check(lib().fi_device_sm_count(ctypes.byref(v)), "fi_device_sm_count")
@@ -283,10 +308,13 @@ class Workspace:
         self._lse_shape, self._kept_rows, self._page_size = (total_q, self.num_qo_heads), (batch, h), page_size
         self._pool, self._shapes_of = -1, self._plan
 
-    def _set_pool(self, num_pages: int):
-        """Shapes that go with a pool of so many pages."""
+    def _need_plan(self):
         if self._plan is None or self._plan is not self._shapes_of:
             self._set_plan()
+
+    def _set_pool(self, num_pages: int):
+        """Shapes that go with a pool of so many pages."""
+        self._need_plan()
         if num_pages != self._pool:
             self._pool = num_pages
             self._pool_shape = (num_pages, *self._page_tail)
@@ -360,6 +388,79 @@ class Workspace:
                               _raw_stream(stream, k_pages.get_device()))
         if st:
             _check(st, "fi_compact")
+
+    def tree_run(self, q, k_pages, v_pages, mask, o, lse, stream=None):
+        """Attention of drafted tokens: each query token sees the context and the drafted tokens of its row of mask (see tree_mask)."""
+        pool = k_pages.shape[0]
+        self._set_pool(pool)
+        dense, n = self._dense, self._plan[0]
+        words = mask.shape[-1] if mask.dim() == 2 else -1
+        st = lib().fi_tree_run(self._h, dense(q, "q", self._bf16, self._q_shape),
+                               dense(k_pages, "k_pages", self._kv_types, self._pool_shape),
+                               dense(v_pages, "v_pages", self._kv_types, self._pool_shape), pool,
+                               dense(mask, "mask", self._i32, (n, words)), words,
+                               dense(o, "o", self._bf16, self._q_shape), dense(lse, "lse", self._f32, self._lse_shape),
+                               _raw_stream(stream, q.get_device()))
+        if st:
+            _check(st, "fi_tree_run")
+
+    def tree_commit(self, path, k_pages, v_pages, stream=None):
+        """Move the K/V rows of each request's accepted drafted tokens (path: ascending, then -1) to the first drafted slots."""
+        pool = k_pages.shape[0]
+        self._set_pool(pool)
+        dense, length = self._dense, path.shape[-1]
+        st = lib().fi_tree_commit(self._h, dense(path, "path", self._i32, (self._plan[1], length)), length,
+                                  dense(k_pages, "k_pages", self._kv_types, self._pool_shape),
+                                  dense(v_pages, "v_pages", self._kv_types, self._pool_shape), pool,
+                                  _raw_stream(stream, k_pages.get_device()))
+        if st:
+            _check(st, "fi_tree_commit")
+
+    def page_bounds(self, k_pages, bounds, new_keys=False, stream=None):
+        """bounds[page, KV head] = smallest and largest key of the plan's pages (new_keys: of those that hold the new tokens), per dim."""
+        pool = k_pages.shape[0]
+        self._set_pool(pool)
+        st = lib().fi_page_bounds(self._h, self._dense(k_pages, "k_pages", self._kv_types, self._pool_shape), pool, int(new_keys),
+                                  self._dense(bounds, "bounds", self._bf16, (pool, self.num_kv_heads, 2, self.head_dim)),
+                                  _raw_stream(stream, k_pages.get_device()))
+        if st:
+            _check(st, "fi_page_bounds")
+
+    def score_pages(self, q, bounds, scores, stream=None):
+        """scores[token, KV head, place in the page list] = upper bound of the logits of the page's keys for the token's heads."""
+        pool, row = bounds.shape[0], scores.shape[-1]
+        self._set_pool(pool)
+        st = lib().fi_score_pages(self._h, self._dense(q, "q", self._bf16, self._q_shape),
+                                  self._dense(bounds, "bounds", self._bf16, (pool, self.num_kv_heads, 2, self.head_dim)), pool,
+                                  self._dense(scores, "scores", self._f32, (self._plan[0], self.num_kv_heads, row)), row,
+                                  _raw_stream(stream, q.get_device()))
+        if st:
+            _check(st, "fi_score_pages")
+
+    def select_pages(self, scores, selected, recent=0, sink=0, stream=None):
+        """selected[token, KV head] = the page ids to attend to: the first sink, the last recent, the best of the rest, then -1."""
+        self._need_plan()
+        row, budget = scores.shape[-1], selected.shape[-1]
+        st = lib().fi_select_pages(self._h, self._dense(scores, "scores", self._f32, (self._plan[0], self.num_kv_heads, row)), row,
+                                   int(sink), int(recent), budget,
+                                   self._dense(selected, "selected", self._i32, (self._plan[0], self.num_kv_heads, budget)),
+                                   _raw_stream(stream, scores.get_device()))
+        if st:
+            _check(st, "fi_select_pages")
+
+    def run_pages(self, q, k_pages, v_pages, selected, o, lse, stream=None):
+        """Attention of each query token and KV head over its own list of pages (as select_pages writes it)."""
+        pool = k_pages.shape[0]
+        self._set_pool(pool)
+        dense, budget = self._dense, selected.shape[-1]
+        st = lib().fi_run_pages(self._h, dense(q, "q", self._bf16, self._q_shape),
+                                dense(k_pages, "k_pages", self._kv_types, self._pool_shape),
+                                dense(v_pages, "v_pages", self._kv_types, self._pool_shape), pool,
+                                dense(selected, "selected", self._i32, (self._plan[0], self.num_kv_heads, budget)), budget,
+                                dense(o, "o", self._bf16, self._q_shape), dense(lse, "lse", self._f32, self._lse_shape),
+                                _raw_stream(stream, q.get_device()))
+        if st:
+            _check(st, "fi_run_pages")
 
     def info(self) -> np.ndarray:
         h = np.zeros(16, np.int32)

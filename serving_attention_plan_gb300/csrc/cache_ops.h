@@ -17,7 +17,7 @@ struct Geo {
   int32_t blk0;      // 32-key blocks of the requests before this one that take the row form of the weights
   int32_t tile0;     // 256-key tiles of the requests before this one (told by fi_cache_plan_compute, read by no kernel)
   int32_t work0;     // tensor-core weights: Q tiles (over all KV heads) of the requests before this one
-  int32_t pad;
+  int32_t tree0;     // tree attention: 128-key tiles (over KV heads and row tiles) of the requests before this one
 };
 // The plan as a whole, in the place before the first entry: one load gives a kernel all of it.
 struct GeoHead {
@@ -25,7 +25,8 @@ struct GeoHead {
   int32_t blocks;          // 32-key blocks of the row form
   int32_t work;            // Q tiles of the tensor-core weights, 0 if they were not counted
   int32_t causal, window;  // the window that work was counted with (-1: none)
-  int32_t pad0, pad1;
+  int32_t tree;            // tiles of the tree attention, 0 if they were not counted
+  int32_t pad;
 };
 static_assert(sizeof(Geo) == 32 && sizeof(GeoHead) == sizeof(Geo), "one sector each");
 constexpr int kBlkKeys = 32;

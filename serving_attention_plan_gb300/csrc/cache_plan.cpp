@@ -6,6 +6,7 @@
 
 #include "../../include/fi.h"
 #include "cache_ops.h"
+#include "tree_ops.h"
 
 namespace fi {
 
@@ -64,6 +65,20 @@ void split_weights(Geo* geo, int batch, int hkv, int group, int row_limit, bool 
   }
   totals->blocks = blocks;
   totals->work = work;
+}
+
+bool fill_tree(Geo* geo, int batch, int hkv, int group, int32_t* total) {
+  const int tokens = kTreeRows / group;
+  int64_t tiles = 0;
+  for (int i = 0; i <= batch; ++i) {
+    geo[i].tree0 = int32_t(tiles);
+    if (i == batch) break;
+    const int64_t keys = std::max<int64_t>(1, (int64_t(geo[i].lkv) + kTreeKeys - 1) / kTreeKeys);
+    tiles += int64_t(hkv) * ((int64_t(geo[i].lq) + tokens - 1) / tokens) * keys;
+    if (tiles > INT32_MAX / 2) return false;  // a CTA's end of the line stays in 32 bits
+  }
+  *total = int32_t(tiles);
+  return true;
 }
 
 int check_pages_once(const int32_t* a, int64_t na, const int32_t* b, int64_t nb, int32_t max_page) {

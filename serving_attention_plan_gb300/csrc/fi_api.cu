@@ -21,6 +21,7 @@
 #include "merge_kernel.cuh"
 #include "plan.h"
 #include "prefill_launch.h"
+#include "tree_ops.h"
 
 namespace {
 
@@ -56,6 +57,8 @@ struct fi_workspace {
   // the ext list hold the shared part of a composable plan.
   size_t off_header = 0, off_cta = 0, off_geo = 0, off_items = 0, off_units = 0, off_slot_unit = 0, off_kv = 0, plan_bytes = 0;
   size_t off_a_header = 0, off_a_cta = 0, off_a_items = 0, off_a_kv = 0, off_ext = 0;
+  // the work of fi_run_pages, made on the GPU
+  size_t off_l_header = 0, off_l_cta = 0, off_l_items = 0, off_l_units = 0, off_l_slot_unit = 0;
   int64_t max_ext = 0;
   size_t off_counters = 0, off_wcount = 0, off_wpart = 0, off_err = 0, off_part_lse = 0, off_part_o = 0, dev_bytes = 0;
   char* dbuf = nullptr;
@@ -73,6 +76,8 @@ struct fi_workspace {
 
   // the cache operators' view of the plan: the GeoHead and Geo entries (also in hbuf) and what the host checks of them
   fi::GeoTotals geo;
+  bool tree_ok = false;         // the plan's tiles of the tree attention were counted
+  int32_t max_pages = 0, max_lq = 0;  // most pages and query tokens of a request
   int64_t plan_nnz_shared = 0;  // entries of a composable plan's shared page list
   signed char pages_once = 0;   // every page listed once: 1 yes, -1 no, 0 not yet checked
   signed char tails_once = 0;   // every page that takes new tokens takes them from one request
@@ -119,9 +124,16 @@ void set_geo(fi_workspace* ws, const int32_t* qo_indptr, const int32_t* kv_indpt
     fi::split_weights(geo, batch, ws->hkv, group,
                       ws->variant.kv_dtype == FI_KV_DTYPE_E4M3 ? fi::kRowFormMostE4m3 : fi::kRowFormMostBf16,
                       causal != 0, window, &ws->geo);
+  int32_t tree = 0;
+  ws->tree_ok = group <= fi::kTreeRows && fi::fill_tree(geo, batch, ws->hkv, group, &tree);
   const fi::GeoHead head = {batch, qo_indptr[batch], int32_t(ws->geo.blocks), int32_t(ws->geo.work),
-                            causal, window, 0, 0};
+                            causal, window, tree, 0};
   std::memcpy(geo - 1, &head, sizeof(head));
+  ws->max_pages = ws->max_lq = 0;
+  for (int i = 0; i < batch; ++i) {
+    ws->max_pages = std::max(ws->max_pages, kv_indptr[i + 1] - kv_indptr[i]);
+    ws->max_lq = std::max(ws->max_lq, geo[i].lq);
+  }
   ws->pages_once = ws->tails_once = 0;
 }
 
@@ -151,8 +163,17 @@ int check_tails_once(fi_workspace* ws) {
   return ws->tails_once > 0 ? FI_OK : FI_ERR_UNSUPPORTED;
 }
 
-// What every cache operator needs of a workspace: a plan, on the current device, whose pages lie in
-// the given pool.
+// What every cache operator needs of a workspace: a plan, on the current device.
+int check_plan_call(const fi_workspace* ws) {
+  if (ws == nullptr) return FI_ERR_INVALID_ARG;
+  if (!ws->has_plan) return FI_ERR_NO_PLAN;
+  if (!ws->geo.ok) return FI_ERR_UNSUPPORTED;
+  int dev = -1;
+  FI_CUDA(cudaGetDevice(&dev));
+  return dev == ws->device ? FI_OK : FI_ERR_INVALID_ARG;
+}
+
+// The same, with the plan's pages in the given pool.
 int check_cache_call(const fi_workspace* ws, int num_pages) {
   if (ws == nullptr) return FI_ERR_INVALID_ARG;
   if (!ws->has_plan) return FI_ERR_NO_PLAN;
@@ -160,9 +181,7 @@ int check_cache_call(const fi_workspace* ws, int num_pages) {
   if (num_pages < 0 || ws->max_page >= num_pages) return FI_ERR_INVALID_ARG;
   // the kernels number a pool's rows (one key of one head) in 32 bits
   if (int64_t(num_pages) * ws->header[fi::H_PAGE_SIZE] > INT32_MAX / ws->hkv) return FI_ERR_UNSUPPORTED;
-  int dev = -1;
-  FI_CUDA(cudaGetDevice(&dev));
-  return dev == ws->device ? FI_OK : FI_ERR_INVALID_ARG;
+  return check_plan_call(ws);
 }
 
 // Whether a capture is under way on the stream, where the launch could depend on it.  A captured launch serves later
@@ -196,6 +215,112 @@ fi::PageView page_view(const fi_workspace* ws, int num_pages) {
 bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
 bool var_on(const fi::Variant& v) { return v.window_left >= 0 || v.soft_cap > 0.f; }
+
+// Keys of a CTA's piece of the lists' line, as long as there are enough: a piece more costs a merge.
+constexpr int64_t kListLeastKeys = 128;
+
+// A work plan in device memory: the host planner's, or the one that fi_run_pages makes on the GPU.
+struct Work {
+  const int32_t *header, *cta_indptr, *items, *units, *slot_unit, *kv_indices;
+  int path, rows_tile, tile_tokens, num_ctas;
+};
+
+// The attention launch of one path over a work plan, with the current plan's page size and variant.
+int run_work(fi_workspace* ws, const Work& w, const void* q, const void* k_pages, const void* v_pages, int num_pages,
+             const void* o_prev, const float* lse_prev, void* o, float* lse, cudaStream_t s) {
+  const int ps = ws->header[fi::H_PAGE_SIZE];
+  const float scale_log2 = fi::kLog2e / std::sqrt(float(ws->head_dim));
+  char* d = ws->dbuf;
+  if (w.path == fi::kPathDecode) {
+    fi::DecodeParams p{};
+    p.cta_indptr = w.cta_indptr;
+    p.items = w.items;
+    p.units = w.units;
+    p.slot_unit = w.slot_unit;
+    p.kv_indices = w.kv_indices;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k = static_cast<const __nv_bfloat16*>(k_pages);
+    p.v = static_cast<const __nv_bfloat16*>(v_pages);
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    p.o_prev = static_cast<const __nv_bfloat16*>(o_prev);
+    p.lse_prev = lse_prev;
+    p.part_o = reinterpret_cast<float*>(d + ws->off_part_o);
+    p.part_lse = reinterpret_cast<float*>(d + ws->off_part_lse);
+    p.counters = reinterpret_cast<uint32_t*>(d + ws->off_counters);
+    p.err = reinterpret_cast<int32_t*>(d + ws->off_err);
+    const fi::Variant& var = ws->plan_variant;
+    const bool nhd = var.kv_layout == FI_KV_LAYOUT_NHD;
+    p.page_stride = (long long)ws->hkv * ps * fi::kHeadDim;
+    p.head_stride = nhd ? fi::kHeadDim : (long long)ps * fi::kHeadDim;
+    p.window_left = var.window_left;
+    p.cap_log2 = var.soft_cap > 0.f ? var.soft_cap * fi::kLog2e : 0.f;
+    p.inv_cap_log2 = var.soft_cap > 0.f ? 1.f / p.cap_log2 : 0.f;
+    p.v_scale = 1.f;
+    p.num_pages = num_pages;
+    p.page_size = ps;
+    p.page_shift = (ps & (ps - 1)) == 0 ? __builtin_ctz(unsigned(ps)) : -1;
+    p.hqo = ws->hqo;
+    p.group = ws->hqo / ws->hkv;
+    p.slot_rows = fi::kTcRows;
+    p.scale_log2 = scale_log2;
+    // launched as a programmatic dependent: the CTAs set up their shared memory while the previous
+    // kernel on the stream drains, then wait for it before the first global read
+    p.wait_prior = 1;
+    if (var.kv_dtype == FI_KV_DTYPE_E4M3) {  // every field above is set before this launch
+      p.scale_log2 *= var.k_scale;           // logits of the stored codes, scaled back to K
+      p.v_scale = var.v_scale;
+      return fi::launch_decode_fp8(w.rows_tile, nhd, w.num_ctas, p, s, true);
+    }
+    const bool variant = var_on(var);
+    if (nhd)
+      return fi::launch_decode_nhd(w.rows_tile, __builtin_ctz(unsigned(ws->hkv)), w.num_ctas, p, s,
+                                   true);
+    switch (w.rows_tile) {
+      case 1: return launch_decode<1>(w.num_ctas, p, s, variant, true);
+      case 2: return launch_decode<2>(w.num_ctas, p, s, variant, true);
+      case 4: return launch_decode<4>(w.num_ctas, p, s, variant, true);
+      case 8: return launch_decode<8>(w.num_ctas, p, s, variant, true);
+      default: return FI_ERR_UNSUPPORTED;
+    }
+  }
+
+  fi::PrefillArgs a{};
+  a.cta_indptr = w.cta_indptr;
+  a.items = w.items;
+  a.units = w.units;
+  a.slot_unit = w.slot_unit;
+  a.kv_indices = w.kv_indices;
+  a.q = q;
+  a.k = k_pages;
+  a.v = v_pages;
+  a.o = o;
+  a.lse = lse;
+  a.o_prev = o_prev;
+  a.lse_prev = lse_prev;
+  a.part_o = reinterpret_cast<float*>(d + ws->off_part_o);
+  a.part_lse = reinterpret_cast<float*>(d + ws->off_part_lse);
+  a.header = w.header;
+  a.err = reinterpret_cast<int32_t*>(d + ws->off_err);
+  a.num_pages = num_pages;
+  a.page_size = ps;
+  a.hqo = ws->hqo;
+  a.hkv = ws->hkv;
+  a.group = ws->hqo / ws->hkv;
+  a.tile_tokens = w.tile_tokens;
+  a.total_q = ws->plan_total_q;
+  a.num_ctas = w.num_ctas;
+  a.scale_log2 = scale_log2;
+  a.window_left = ws->plan_variant.window_left;
+  a.cap_log2 = ws->plan_variant.soft_cap > 0.f ? ws->plan_variant.soft_cap * fi::kLog2e : 0.f;
+  a.nhd = ws->plan_variant.kv_layout == FI_KV_LAYOUT_NHD ? 1 : 0;
+  if (ws->plan_variant.kv_dtype == FI_KV_DTYPE_E4M3) {
+    a.fp8 = 1;
+    a.scale_log2 *= ws->plan_variant.k_scale;  // logits of the stored codes, scaled back to K
+    a.v_scale = ws->plan_variant.v_scale;
+  }
+  return fi::launch_prefill(a, s);
+}
 
 }  // namespace
 
@@ -279,6 +404,11 @@ int fi_workspace_create(int max_batch, int max_total_q, int max_kv_pages, int nu
   ws->off_part_lse = seg(sizeof(float) * ws->max_slots * fi::kTcRows);
   ws->off_part_o = seg(sizeof(float) * ws->max_slots * fi::kTcRows * fi::kHeadDim);
   ws->off_wpart = seg(sizeof(float) * 2 * size_t(num_sms) * fi::kTileKeys);
+  ws->off_l_header = seg(sizeof(int32_t) * fi::kHeaderLen);
+  ws->off_l_cta = seg(sizeof(int32_t) * (ws->max_ctas + 1));
+  ws->off_l_items = seg(sizeof(int32_t) * fi::kItemFields * ws->max_items);
+  ws->off_l_units = seg(sizeof(int32_t) * fi::kUnitFields * ws->max_ctas);
+  ws->off_l_slot_unit = seg(sizeof(int32_t) * ws->max_slots);
   ws->dev_bytes = off;
 
   cudaError_t e = cudaMalloc(&ws->dbuf, ws->dev_bytes);
@@ -633,95 +763,11 @@ int fi_run_merge(fi_workspace* ws, const void* q, const void* k_pages, const voi
     }
   }
 
-  if (h[fi::H_PATH] == fi::kPathDecode) {
-    fi::DecodeParams p{};
-    p.cta_indptr = reinterpret_cast<const int32_t*>(d + ws->off_cta);
-    p.items = reinterpret_cast<const int32_t*>(d + ws->off_items);
-    p.units = reinterpret_cast<const int32_t*>(d + ws->off_units);
-    p.slot_unit = reinterpret_cast<const int32_t*>(d + ws->off_slot_unit);
-    p.kv_indices = reinterpret_cast<const int32_t*>(d + ws->off_kv);
-    p.q = static_cast<const __nv_bfloat16*>(q);
-    p.k = static_cast<const __nv_bfloat16*>(k_pages);
-    p.v = static_cast<const __nv_bfloat16*>(v_pages);
-    p.o = static_cast<__nv_bfloat16*>(o);
-    p.lse = lse;
-    p.o_prev = static_cast<const __nv_bfloat16*>(o_prev);
-    p.lse_prev = lse_prev;
-    p.part_o = reinterpret_cast<float*>(d + ws->off_part_o);
-    p.part_lse = reinterpret_cast<float*>(d + ws->off_part_lse);
-    p.counters = reinterpret_cast<uint32_t*>(d + ws->off_counters);
-    p.err = reinterpret_cast<int32_t*>(d + ws->off_err);
-    const fi::Variant& var = ws->plan_variant;
-    const bool nhd = var.kv_layout == FI_KV_LAYOUT_NHD;
-    p.page_stride = (long long)ws->hkv * ps * fi::kHeadDim;
-    p.head_stride = nhd ? fi::kHeadDim : (long long)ps * fi::kHeadDim;
-    p.window_left = var.window_left;
-    p.cap_log2 = var.soft_cap > 0.f ? var.soft_cap * fi::kLog2e : 0.f;
-    p.inv_cap_log2 = var.soft_cap > 0.f ? 1.f / p.cap_log2 : 0.f;
-    p.v_scale = 1.f;
-    p.num_pages = num_pages;
-    p.page_size = ps;
-    p.page_shift = (ps & (ps - 1)) == 0 ? __builtin_ctz(unsigned(ps)) : -1;
-    p.hqo = ws->hqo;
-    p.group = h[fi::H_GROUP];
-    p.slot_rows = fi::kTcRows;
-    p.scale_log2 = scale_log2;
-    // launched as a programmatic dependent: the CTAs set up their shared memory while the previous
-    // kernel on the stream drains, then wait for it before the first global read
-    p.wait_prior = 1;
-    if (var.kv_dtype == FI_KV_DTYPE_E4M3) {  // every field above is set before this launch
-      p.scale_log2 *= var.k_scale;           // logits of the stored codes, scaled back to K
-      p.v_scale = var.v_scale;
-      return fi::launch_decode_fp8(h[fi::H_ROWS_TILE], nhd, h[fi::H_NUM_CTAS], p, s, true);
-    }
-    const bool variant = var_on(var);
-    if (nhd)
-      return fi::launch_decode_nhd(h[fi::H_ROWS_TILE], __builtin_ctz(unsigned(ws->hkv)), h[fi::H_NUM_CTAS], p, s,
-                                   true);
-    switch (h[fi::H_ROWS_TILE]) {
-      case 1: return launch_decode<1>(h[fi::H_NUM_CTAS], p, s, variant, true);
-      case 2: return launch_decode<2>(h[fi::H_NUM_CTAS], p, s, variant, true);
-      case 4: return launch_decode<4>(h[fi::H_NUM_CTAS], p, s, variant, true);
-      case 8: return launch_decode<8>(h[fi::H_NUM_CTAS], p, s, variant, true);
-      default: return FI_ERR_UNSUPPORTED;
-    }
-  }
-
-  fi::PrefillArgs a{};
-  a.cta_indptr = reinterpret_cast<const int32_t*>(d + ws->off_cta);
-  a.items = reinterpret_cast<const int32_t*>(d + ws->off_items);
-  a.units = reinterpret_cast<const int32_t*>(d + ws->off_units);
-  a.slot_unit = reinterpret_cast<const int32_t*>(d + ws->off_slot_unit);
-  a.kv_indices = reinterpret_cast<const int32_t*>(d + ws->off_kv);
-  a.q = q;
-  a.k = k_pages;
-  a.v = v_pages;
-  a.o = o;
-  a.lse = lse;
-  a.o_prev = o_prev;
-  a.lse_prev = lse_prev;
-  a.part_o = reinterpret_cast<float*>(d + ws->off_part_o);
-  a.part_lse = reinterpret_cast<float*>(d + ws->off_part_lse);
-  a.header = reinterpret_cast<const int32_t*>(d + ws->off_header);
-  a.err = reinterpret_cast<int32_t*>(d + ws->off_err);
-  a.num_pages = num_pages;
-  a.page_size = ps;
-  a.hqo = ws->hqo;
-  a.hkv = ws->hkv;
-  a.group = h[fi::H_GROUP];
-  a.tile_tokens = h[fi::H_TILE_TOKENS];
-  a.total_q = ws->plan_total_q;
-  a.num_ctas = h[fi::H_NUM_CTAS];
-  a.scale_log2 = scale_log2;
-  a.window_left = ws->plan_variant.window_left;
-  a.cap_log2 = ws->plan_variant.soft_cap > 0.f ? ws->plan_variant.soft_cap * fi::kLog2e : 0.f;
-  a.nhd = ws->plan_variant.kv_layout == FI_KV_LAYOUT_NHD ? 1 : 0;
-  if (ws->plan_variant.kv_dtype == FI_KV_DTYPE_E4M3) {
-    a.fp8 = 1;
-    a.scale_log2 *= ws->plan_variant.k_scale;  // logits of the stored codes, scaled back to K
-    a.v_scale = ws->plan_variant.v_scale;
-  }
-  return fi::launch_prefill(a, s);
+  const Work w = {reinterpret_cast<const int32_t*>(d + ws->off_header), reinterpret_cast<const int32_t*>(d + ws->off_cta),
+                  reinterpret_cast<const int32_t*>(d + ws->off_items),  reinterpret_cast<const int32_t*>(d + ws->off_units),
+                  reinterpret_cast<const int32_t*>(d + ws->off_slot_unit), reinterpret_cast<const int32_t*>(d + ws->off_kv),
+                  h[fi::H_PATH], h[fi::H_ROWS_TILE], h[fi::H_TILE_TOKENS], h[fi::H_NUM_CTAS]};
+  return run_work(ws, w, q, k_pages, v_pages, num_pages, o_prev, lse_prev, o, lse, s);
 }
 
 int fi_merge_states(const void* o_a, const float* lse_a, const void* o_b, const float* lse_b, void* o, float* lse,
@@ -932,6 +978,195 @@ int fi_compact(fi_workspace* ws, const int32_t* kept, int32_t budget, void* k_pa
   p.weights = weights;
   p.budget = budget;
   return fi::launch_compact(p, batch, captured ? ws->max_batch : batch, ws->plan_variant.kv_dtype == FI_KV_DTYPE_E4M3, ws->num_sms, s);
+}
+
+int fi_tree_run(fi_workspace* ws, const void* q, const void* k_pages, const void* v_pages, int num_pages, const void* mask,
+                int32_t mask_words, void* o, float* lse, void* stream) {
+  int st = check_cache_call(ws, num_pages);
+  if (st != FI_OK) return st;
+  const fi::Variant& var = ws->plan_variant;
+  const int ps = ws->header[fi::H_PAGE_SIZE];
+  if (ws->composable || var.window_left >= 0 || !ws->tree_ok) return FI_ERR_UNSUPPORTED;
+  if (ps % 8 != 0 || fi::kTreeKeys % ps != 0) return FI_ERR_UNSUPPORTED;
+  if (mask_words < 1 || mask_words < (int64_t(ws->max_lq) + 31) / 32) return FI_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // (a launch holds a tensor map of q with the plan's tokens, so one without tokens serves no later plan)
+  if (ws->plan_total_q == 0) return FI_OK;
+  if (q == nullptr || k_pages == nullptr || v_pages == nullptr || mask == nullptr || o == nullptr || lse == nullptr || num_pages < 1)
+    return FI_ERR_INVALID_ARG;
+  if (misaligned(q, 16) || misaligned(k_pages, 16) || misaligned(v_pages, 16) || misaligned(o, 16) || misaligned(mask, 4) ||
+      misaligned(lse, 4))
+    return FI_ERR_INVALID_ARG;
+  fi::TreeParams p{};
+  p.pv = page_view(ws, num_pages);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_pages = k_pages;
+  p.v_pages = v_pages;
+  p.mask = static_cast<const uint32_t*>(mask);
+  p.mask_words = mask_words;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.part_o = reinterpret_cast<float*>(ws->dbuf + ws->off_part_o);
+  p.part_lse = reinterpret_cast<float*>(ws->dbuf + ws->off_part_lse);
+  p.hqo = ws->hqo;
+  p.group = ws->hqo / ws->hkv;
+  p.tile_tokens = fi::kTreeRows / p.group;
+  p.q_tile_bytes = uint32_t(2 * 128 * p.group * p.tile_tokens);
+  const bool fp8 = var.kv_dtype == FI_KV_DTYPE_E4M3;
+  p.scale_log2 = fi::kLog2e / std::sqrt(float(ws->head_dim)) * (fp8 ? var.k_scale : 1.f);
+  p.v_scale = fp8 ? var.v_scale : 1.f;
+  p.cap_log2 = var.soft_cap > 0.f ? var.soft_cap * fi::kLog2e : 0.f;
+  p.inv_cap_log2 = var.soft_cap > 0.f ? 1.f / p.cap_log2 : 0.f;
+  p.wide_cap = var.soft_cap > fi::kExpTanhMostCap;
+  return fi::launch_tree(p, ws->plan_total_q, fp8, ws->num_sms, s);
+}
+
+int fi_tree_commit(fi_workspace* ws, const int32_t* path, int32_t path_len, void* k_pages, void* v_pages, int num_pages,
+                   void* stream) {
+  int st = check_cache_call(ws, num_pages);
+  if (st != FI_OK) return st;
+  if (path_len < 1) return FI_ERR_INVALID_ARG;
+  const int batch = ws->header[fi::H_BATCH];
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  bool captured = false;
+  st = is_capturing(s, batch < ws->max_batch || ws->plan_total_q == 0 || ws->plan_nnz - ws->plan_nnz_shared == 0, &captured);
+  if (st != FI_OK) return st;
+  if ((batch == 0 || ws->plan_total_q == 0 || ws->plan_nnz - ws->plan_nnz_shared == 0) && !captured) return FI_OK;
+  if (path == nullptr || k_pages == nullptr || v_pages == nullptr || misaligned(path, 4) || misaligned(k_pages, 16) ||
+      misaligned(v_pages, 16))
+    return FI_ERR_INVALID_ARG;
+  st = check_tails_once(ws);
+  if (st != FI_OK) return st;
+  fi::CommitParams p{};
+  p.pv = page_view(ws, num_pages);
+  p.path = path;
+  p.path_len = path_len;
+  p.k_pages = k_pages;
+  p.v_pages = v_pages;
+  return fi::launch_commit(p, captured ? ws->max_batch : batch, ws->plan_variant.kv_dtype == FI_KV_DTYPE_E4M3, ws->num_sms, s);
+}
+
+int fi_page_bounds(fi_workspace* ws, const void* k_pages, int num_pages, int32_t new_keys, void* bounds, void* stream) {
+  int st = check_cache_call(ws, num_pages);
+  if (st != FI_OK) return st;
+  if (new_keys != 0 && new_keys != 1) return FI_ERR_INVALID_ARG;
+  const int64_t nnz = ws->plan_nnz - ws->plan_nnz_shared;
+  const int64_t units = new_keys ? ws->plan_total_q : nnz, most = new_keys ? ws->max_total_q : ws->max_kv_pages;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  bool captured = false;
+  st = is_capturing(s, units < most, &captured);
+  if (st != FI_OK) return st;
+  if ((units == 0 || nnz == 0) && !captured) return FI_OK;
+  if (k_pages == nullptr || bounds == nullptr || misaligned(k_pages, 16) || misaligned(bounds, 16)) return FI_ERR_INVALID_ARG;
+  fi::BoundsParams p{};
+  p.pv = page_view(ws, num_pages);
+  p.k_pages = k_pages;
+  p.bounds = static_cast<__nv_bfloat16*>(bounds);
+  p.new_keys = new_keys;
+  return fi::launch_bounds(p, (captured ? most : units) * ws->hkv, ws->plan_variant.kv_dtype == FI_KV_DTYPE_E4M3, ws->num_sms, s);
+}
+
+int fi_score_pages(fi_workspace* ws, const void* q, const void* bounds, int num_pages, float* scores, int32_t row_pages,
+                   void* stream) {
+  int st = check_cache_call(ws, num_pages);
+  if (st != FI_OK) return st;
+  if (ws->composable || ws->plan_variant.window_left >= 0) return FI_ERR_UNSUPPORTED;
+  if (row_pages < 1 || row_pages < ws->max_pages) return FI_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  bool captured = false;
+  st = is_capturing(s, true, &captured);
+  if (st != FI_OK) return st;
+  if ((ws->plan_total_q == 0 || ws->plan_nnz == 0) && !captured) return FI_OK;
+  if (q == nullptr || bounds == nullptr || scores == nullptr || misaligned(q, 16) || misaligned(bounds, 16) || misaligned(scores, 4))
+    return FI_ERR_INVALID_ARG;
+  fi::ScoreParams p{};
+  p.pv = page_view(ws, num_pages);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.bounds = static_cast<const __nv_bfloat16*>(bounds);
+  p.scores = scores;
+  p.row_pages = row_pages;
+  p.hqo = ws->hqo;
+  p.group = ws->hqo / ws->hkv;
+  p.scale = 1.f / std::sqrt(float(ws->head_dim));
+  if (ws->plan_variant.kv_dtype == FI_KV_DTYPE_E4M3) p.scale *= ws->plan_variant.k_scale;
+  const int64_t blocks = captured ? int64_t(ws->max_kv_pages) / 16 + ws->max_batch : ws->plan_nnz / 16 + ws->header[fi::H_BATCH];
+  return fi::launch_scores(p, blocks * ws->hkv, ws->num_sms, s);
+}
+
+int fi_select_pages(fi_workspace* ws, const float* scores, int32_t row_pages, int32_t sink, int32_t recent, int32_t budget,
+                    int32_t* selected, void* stream) {
+  int st = check_plan_call(ws);
+  if (st != FI_OK) return st;
+  if (ws->composable || ws->plan_variant.window_left >= 0) return FI_ERR_UNSUPPORTED;
+  if (sink < 0 || recent < 0 || budget < 1 || int64_t(sink) + recent > budget || row_pages < 1 || row_pages < ws->max_pages)
+    return FI_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  bool captured = false;
+  st = is_capturing(s, ws->plan_total_q < ws->max_total_q || scores == nullptr, &captured);
+  if (st != FI_OK) return st;
+  if (ws->plan_total_q == 0 && !captured) return FI_OK;
+  if (selected == nullptr || ((ws->plan_nnz > 0 || captured) && scores == nullptr) || misaligned(scores, 4) || misaligned(selected, 4))
+    return FI_ERR_INVALID_ARG;
+  fi::PickParams p{};
+  p.pv = page_view(ws, 0);
+  p.scores = scores;
+  p.selected = selected;
+  p.row_pages = row_pages;
+  p.sink = sink;
+  p.recent = recent;
+  p.budget = budget;
+  const int64_t rows = int64_t(captured ? ws->max_total_q : ws->plan_total_q) * ws->hkv;
+  return fi::launch_pick(p, rows, captured ? row_pages : ws->max_pages, ws->num_sms, s);
+}
+
+int fi_run_pages(fi_workspace* ws, const void* q, const void* k_pages, const void* v_pages, int num_pages,
+                 const int32_t* selected, int32_t budget, void* o, float* lse, void* stream) {
+  int st = check_cache_call(ws, num_pages);
+  if (st != FI_OK) return st;
+  const fi::Variant& var = ws->plan_variant;
+  const int ps = ws->header[fi::H_PAGE_SIZE], group = ws->hqo / ws->hkv;
+  const bool nhd = var.kv_layout == FI_KV_LAYOUT_NHD, fp8 = var.kv_dtype == FI_KV_DTYPE_E4M3;
+  const bool pow2 = (ps & (ps - 1)) == 0, tensor = group > fi::kDecodeMaxRows;
+  if (ws->composable || var.window_left >= 0 || group > fi::kTcRows) return FI_ERR_UNSUPPORTED;
+  // the page sizes and layouts of the attention kernel that takes the rows of one token
+  if (tensor ? ps % 8 != 0 || fi::kTcKeys % ps != 0
+             : (fp8 && !pow2) || (nhd && (!pow2 || (ws->hkv & (ws->hkv - 1)) != 0 || ws->hkv > 16)))
+    return FI_ERR_UNSUPPORTED;
+  if (budget < 1) return FI_ERR_INVALID_ARG;
+  const int total_q = ws->plan_total_q;
+  if (int64_t(total_q) * ws->hkv * budget > INT32_MAX || int64_t(budget) * ps > (1 << 30)) return FI_ERR_UNSUPPORTED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  bool captured = false;
+  st = is_capturing(s, total_q < ws->max_total_q, &captured);
+  if (st != FI_OK) return st;
+  if (total_q == 0 && !captured) return FI_OK;
+  if (q == nullptr || k_pages == nullptr || v_pages == nullptr || selected == nullptr || o == nullptr || lse == nullptr || num_pages < 1)
+    return FI_ERR_INVALID_ARG;
+  if (misaligned(q, 16) || misaligned(k_pages, 16) || misaligned(v_pages, 16) || misaligned(o, 16) || misaligned(lse, 4) ||
+      misaligned(selected, 4))
+    return FI_ERR_INVALID_ARG;
+  char* d = ws->dbuf;
+  fi::ListPlanParams p{};
+  p.pv = page_view(ws, num_pages);
+  p.selected = selected;
+  p.budget = budget;
+  p.ctas = ws->num_sms;
+  // a step of the line is a stage of the attention kernel, or a page where that is more
+  const int stage = tensor ? fi::kTcKeys : fp8 ? 64 : fi::kStageTokens;
+  p.block_pages = std::max(1, stage / ps);
+  p.least = std::max(1, int(kListLeastKeys / (int64_t(p.block_pages) * ps)));
+  p.header = reinterpret_cast<int32_t*>(d + ws->off_l_header);
+  p.cta_indptr = reinterpret_cast<int32_t*>(d + ws->off_l_cta);
+  p.items = reinterpret_cast<int32_t*>(d + ws->off_l_items);
+  p.units = reinterpret_cast<int32_t*>(d + ws->off_l_units);
+  p.slot_unit = reinterpret_cast<int32_t*>(d + ws->off_l_slot_unit);
+  st = fi::launch_list_plan(p, int64_t(captured ? ws->max_total_q : total_q) * ws->hkv, ws->num_sms, s);
+  if (st != FI_OK) return st;
+  int rows_tile = 1;
+  while (rows_tile < group) rows_tile *= 2;
+  const Work w = {p.header, p.cta_indptr, p.items, p.units, p.slot_unit, selected, tensor ? fi::kPathTensor : fi::kPathDecode, rows_tile, 1,
+                  ws->num_sms};
+  return run_work(ws, w, q, k_pages, v_pages, num_pages, nullptr, nullptr, o, lse, s);
 }
 
 int fi_get_error(fi_workspace* ws, int32_t* err_bits) {

@@ -1,0 +1,603 @@
+// Attention over pages that a cheap score selects: bounds of the keys of a page, the pages' scores for each query, the
+// choice under a budget, and the work plan of the attention over the chosen pages.
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "cache_common.cuh"
+#include "prefill_launch.h"
+#include "tree_ops.h"
+
+namespace fi {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+
+// Last request r whose value of(r) (non-decreasing) is <= x, of(0) <= x; a whole warp, 32 probes a round.
+template <typename F>
+__device__ __forceinline__ int last_at_most(int n, int x, F of) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) >> 5;
+    const int at = lo + lane * step;
+    const unsigned le = __ballot_sync(kAll, at < hi && of(min(at, n - 1)) <= x);
+    lo += (__popc(le) - 1) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int pages_of(const PageView& pv, int keys) {
+  return pv.page_shift >= 0 ? (keys + pv.page_size - 1) >> pv.page_shift : (keys + pv.page_size - 1) / pv.page_size;
+}
+
+// ---- bounds ------------------------------------------------------------------------------------------
+//   bounds[page][head][0][d] = min, [1][d] = max over the page's keys of K[key][d]   (e4m3: of the codes' values)
+// NaN wins, so that a page with a NaN key ranks first and its attention shows it.  Exact: a minimum is one of its inputs, and every
+// e4m3 value is a bf16 value.  The keys are read once, 512 bytes a page and head are written: traffic is the bound.  A warp
+// takes one (page, head) at a time, 16 bytes a lane and load, up to eight loads in flight, compared two by two in
+// their 16-bit form.
+
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b, bool f16) {
+  uint32_t r;
+  if (f16)
+    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b, bool f16) {
+  uint32_t r;
+  if (f16)
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t widen2(uint32_t two_codes) {
+  uint32_t h;
+  const uint16_t v = static_cast<uint16_t>(two_codes);
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(v));
+  return h;
+}
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h) {
+  const __half2 v = *reinterpret_cast<const __half2*>(&h);
+  const float2 f = __half22float2(v);
+  return f2_to_bf16x2(f.x, f.y);
+}
+
+constexpr int kBoundsThreads = 256;
+constexpr int kBoundsAhead = 8;
+
+// Pairs of dims that a lane holds: 4 words of bf16, or 8 of f16 (16 codes).
+template <bool kFp8>
+__global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const __grid_constant__ BoundsParams p) {
+  constexpr int kLanes = kFp8 ? 8 : 16, kSide = 32 / kLanes, kWords = kFp8 ? 8 : 4;
+  wait_prior_grid();
+  const PageView& pv = p.pv;
+  const GeoHead plan = load_head(pv.geo);
+  if (plan.batch == 0) return;
+  const int lane = threadIdx.x & 31, sub = lane % kLanes, side = lane / kLanes;
+  // a task is a page entry (or, for new keys, a query token) and a head; heads of a page are neighbours in memory
+  const long long units = p.new_keys ? plan.total_q : __ldg(&pv.geo[plan.batch].kv0);
+  const long long tasks = units * pv.hkv, warps = (long long)gridDim.x * (kBoundsThreads / 32);
+  const long long me = (long long)blockIdx.x * (kBoundsThreads / 32) + (threadIdx.x >> 5);
+  const long long t0 = tasks * me / warps, t1 = tasks * (me + 1) / warps;
+  if (t0 >= t1) return;
+  int unit = int(t0 / pv.hkv), head = int(t0 - (long long)unit * pv.hkv);
+  int r = find_request(pv.geo, plan.batch, p.new_keys ? &Geo::q0 : &Geo::kv0, unit);
+  Geo g = load_geo(pv.geo, r);
+  int page = -1, keys = 0;  // of the unit; -1: nothing to do
+  bool fresh = true;
+  for (long long task = t0; task < t1; ++task) {
+    if (fresh) {
+      fresh = false;
+      int e;
+      if (p.new_keys) {
+        while (unit >= g.q0 + g.lq) g = load_geo(pv.geo, ++r);
+        const int t = unit - g.q0, j = g.lkv - g.lq + t;
+        // the first new token of its page speaks for the page
+        const bool first = j >= 0 && (t == 0 || j == 0 || j % pv.page_size == 0);
+        e = first ? j / pv.page_size : -1;
+      } else {
+        while (unit >= g.kv0 + pages_of(pv, g.lkv)) g = load_geo(pv.geo, ++r);
+        e = unit - g.kv0;
+      }
+      page = -1;
+      if (e >= 0) {
+        keys = min(pv.page_size, g.lkv - e * pv.page_size);
+        page = __ldg(pv.kv_indices + g.kv0 + e);
+        if (static_cast<unsigned>(page) >= static_cast<unsigned>(pv.num_pages)) {
+          atomicOr(pv.err, FI_DEVERR_PAGE_OOB);
+          page = -1;
+        }
+      }
+    }
+    if (page >= 0) {
+      const char* src = static_cast<const char*>(p.k_pages) + kv_offset(pv, page, 0, head) * (kFp8 ? 1 : 2) + sub * 16;
+      const long long step = pv.tok_stride * (kFp8 ? 1 : 2);
+      uint32_t lo[kWords], hi[kWords];
+      bool any = false;
+      for (int k0 = 0; k0 < keys; k0 += kBoundsAhead * kSide) {
+        uint4 x[kBoundsAhead];
+#pragma unroll
+        for (int i = 0; i < kBoundsAhead; ++i)  // a row behind the last key stands for the last
+          x[i] = k0 + i * kSide < keys ? __ldcs(reinterpret_cast<const uint4*>(src + min(k0 + i * kSide + side, keys - 1) * step)) : x[0];
+#pragma unroll
+        for (int i = 0; i < kBoundsAhead; ++i) {
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+          for (int k = 0; k < kWords; ++k) {
+            const uint32_t v = kFp8 ? widen2(k & 1 ? w[k / 2] >> 16 : w[k / 2]) : w[k & 3];
+            lo[k] = any || i > 0 ? min2(lo[k], v, kFp8) : v;
+            hi[k] = any || i > 0 ? max2(hi[k], v, kFp8) : v;
+          }
+        }
+        any = true;
+      }
+#pragma unroll
+      for (int m = kLanes; m < 32; m <<= 1) {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+          lo[k] = min2(lo[k], __shfl_xor_sync(kAll, lo[k], m), kFp8);
+          hi[k] = max2(hi[k], __shfl_xor_sync(kAll, hi[k], m), kFp8);
+        }
+      }
+      uint4* to = reinterpret_cast<uint4*>(p.bounds + ((long long)page * pv.hkv + head) * 2 * kHeadDim);
+      if constexpr (kFp8) {  // the row's four lanes of a sub take a half of its 16 minima or maxima each
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t a = side & 1 ? lo[4 + k] : lo[k], b = side & 1 ? hi[4 + k] : hi[k];
+          w[k] = f16x2_to_bf16x2(side & 2 ? b : a);
+        }
+        to[(side >> 1) * 16 + sub * 2 + (side & 1)] = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+        to[side * 16 + sub] = side ? make_uint4(hi[0], hi[1], hi[2], hi[3]) : make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+    }
+    if (++head == pv.hkv) {
+      head = 0;
+      ++unit;
+      fresh = true;
+    }
+  }
+}
+
+// ---- scores --------------------------------------------------------------------------------------------
+//   score(t, h, e) = scale * max over the query heads of h's group of  sum_d  min(q_d, 0) lo_d + max(q_d, 0) hi_d
+// no less than the logit of any key of page e; -inf for a page that token t does not see.  The sum is a product of 256 terms
+// whose one factor [lo, hi] is the page's row as it lies in memory, so it runs on warp-level products: 16 pages on the rows,
+// eight (token, head) columns.  Sums are fp32.  Reading the bounds once is the bound (64 products a byte at most): each
+// warp holds 16 rows in registers, 8 KB in flight, and runs all columns of the request over them.
+// The order of the 256 terms is free, so a lane's 16 bytes of a row are taken as they come, as the A operands of two
+// products, and the q operands are read in the same order: no shared memory, no shuffle.
+constexpr int kScoreThreads = 128;
+constexpr int kScorePages = 16;
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__global__ void __launch_bounds__(kScoreThreads, 4) scores_kernel(const __grid_constant__ ScoreParams p) {
+  wait_prior_grid();
+  const PageView& pv = p.pv;
+  const GeoHead plan = load_head(pv.geo);
+  if (plan.batch == 0) return;
+  const int lane = threadIdx.x & 31, row = lane >> 2, c = lane & 3;
+  // blocks of 16 pages: request r's begin at (its first entry) / 16 + r, which leaves each room for all of its own
+  const Geo* geo = pv.geo;
+  const long long blocks = (__ldg(&geo[plan.batch].kv0) >> 4) + plan.batch;
+  const long long tasks = blocks * pv.hkv, warps = (long long)gridDim.x * (kScoreThreads / 32);
+  const long long me = (long long)blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5);
+  const long long t0 = tasks * me / warps, t1 = tasks * (me + 1) / warps;
+  if (t0 >= t1) return;
+  const int fit = max(1, 8 / p.group);                // tokens of a set of eight columns
+  const int sets = (p.group + 7) / 8;                 // sets of a token
+  const int heads = min(p.group, 8);                  // columns of a token in a set
+  int block = int(t0 / pv.hkv), head = int(t0 - (long long)block * pv.hkv);
+  int r = last_at_most(plan.batch, block, [&](int k) { return (__ldg(&geo[k].kv0) >> 4) + k; });
+  Geo g = load_geo(geo, r);
+  int pages = 0, e0 = 0, id = -1;
+  bool fresh = true;
+  for (long long task = t0; task < t1; ++task) {
+    if (fresh) {
+      fresh = false;
+      while (r + 1 < plan.batch && block >= (__ldg(&geo[r + 1].kv0) >> 4) + r + 1) g = load_geo(geo, ++r);
+      pages = pages_of(pv, g.lkv);
+      e0 = (block - ((g.kv0 >> 4) + r)) * kScorePages;
+      id = -1;
+      if (lane < kScorePages && e0 + lane < pages) {
+        id = __ldg(pv.kv_indices + g.kv0 + e0 + lane);
+        if (static_cast<unsigned>(id) >= static_cast<unsigned>(pv.num_pages)) {
+          atomicOr(pv.err, FI_DEVERR_PAGE_OOB);
+          id = -1;
+        }
+      }
+    }
+    if (e0 < pages && g.lq > 0) {
+      const int ia = __shfl_sync(kAll, id, row), ib = __shfl_sync(kAll, id, row + 8);
+      // this lane's pieces of rows `row` and `row + 8`: 64-byte chunks 0-3 are lo, 4-7 hi
+      uint4 a[8], b[8];
+      const uint4* pa = reinterpret_cast<const uint4*>(p.bounds + ((long long)max(ia, 0) * pv.hkv + head) * 2 * kHeadDim) + c;
+      const uint4* pb = reinterpret_cast<const uint4*>(p.bounds + ((long long)max(ib, 0) * pv.hkv + head) * 2 * kHeadDim) + c;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        a[k] = ia >= 0 ? __ldcs(pa + 4 * k) : make_uint4(0, 0, 0, 0);
+        b[k] = ib >= 0 ? __ldcs(pb + 4 * k) : make_uint4(0, 0, 0, 0);
+      }
+      for (int tok = 0; tok < g.lq; tok += fit) {
+        float best[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};  // [page row][column of the lane's two]
+        for (int set = 0; set < sets; ++set) {
+          // column `row` of this set: (token, head of the group)
+          const int ct = tok + row / heads, ch = set * 8 + row % heads;
+          const bool on = row / heads < fit && ct < g.lq && ch < p.group;
+          const uint4* pq = reinterpret_cast<const uint4*>(p.q + ((long long)(g.q0 + (on ? ct : 0)) * p.hqo + head * p.group + (on ? ch : 0)) * kHeadDim) + c;
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint4 x = __ldg(pq + 4 * k);
+            const uint32_t neg[4] = {min2(x.x, 0u, false), min2(x.y, 0u, false), min2(x.z, 0u, false), min2(x.w, 0u, false)};
+            const uint32_t pos[4] = {max2(x.x, 0u, false), max2(x.y, 0u, false), max2(x.z, 0u, false), max2(x.w, 0u, false)};
+            const uint32_t l0[4] = {a[k].x, b[k].x, a[k].y, b[k].y}, l1[4] = {a[k].z, b[k].z, a[k].w, b[k].w};
+            const uint32_t h0[4] = {a[k + 4].x, b[k + 4].x, a[k + 4].y, b[k + 4].y}, h1[4] = {a[k + 4].z, b[k + 4].z, a[k + 4].w, b[k + 4].w};
+            mma_16816(acc, l0, neg[0], neg[1]);
+            mma_16816(acc, l1, neg[2], neg[3]);
+            mma_16816(acc, h0, pos[0], pos[1]);
+            mma_16816(acc, h1, pos[2], pos[3]);
+          }
+          // columns 2 c and 2 c + 1 of the set, where they are heads of the group
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const bool head_on = set * 8 + (2 * c + k) % heads < p.group;
+            best[0][k] = max_nan(best[0][k], head_on ? acc[k] : -INFINITY);
+            best[1][k] = max_nan(best[1][k], head_on ? acc[2 + k] : -INFINITY);
+          }
+        }
+        for (int f = 0; f < fit && tok + f < g.lq; ++f) {
+          // the largest over the columns of token tok + f
+          float v0 = -INFINITY, v1 = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const bool its = (2 * c + k) / heads == f;
+            v0 = max_nan(v0, its ? best[0][k] : -INFINITY);
+            v1 = max_nan(v1, its ? best[1][k] : -INFINITY);
+          }
+          v0 = max_nan(v0, __shfl_xor_sync(kAll, v0, 1));
+          v1 = max_nan(v1, __shfl_xor_sync(kAll, v1, 1));
+          v0 = max_nan(v0, __shfl_xor_sync(kAll, v0, 2));
+          v1 = max_nan(v1, __shfl_xor_sync(kAll, v1, 2));
+          const int e = e0 + row + (c & 1) * 8;
+          if (c < 2 && e < pages) {
+            const int limit = plan.causal ? g.lkv - g.lq + tok + f : g.lkv - 1;
+            const bool seen = (c ? ib : ia) >= 0 && (long long)e * pv.page_size <= limit;
+            p.scores[((long long)(g.q0 + tok + f) * pv.hkv + head) * p.row_pages + e] = seen ? (c ? v1 : v0) * p.scale : -INFINITY;
+          }
+        }
+      }
+    }
+    if (++head == pv.hkv) {
+      head = 0;
+      ++block;
+      fresh = true;
+    }
+  }
+}
+
+// ---- choice --------------------------------------------------------------------------------------------
+// Of the n pages that a (token, KV head) row sees, the first `sink`, the last `recent` and the best of the rest, budget in
+// all.  The threshold, the K-th largest score, is found bit by bit from the top: scores as integers of the same order, and
+// at each step a count of those at or above a candidate.  A count costs a compare and an add for each score that a thread
+// holds in registers, a warp sum and, with more than one warp, a barrier; it ends once exactly K are counted.  No
+// atomics: nothing depends on scheduling.  A warp holds a run of positions, so the chosen come out in order by counting.  Rows longer than the
+// CTA holds are read again for each count.
+constexpr int kPickEach = 16;  // scores of a thread
+constexpr int kPickMostWarps = 32;
+
+// Order-preserving map; -0 counts as 0 and every NaN as the largest.
+__device__ __forceinline__ uint32_t score_key(float w) {
+  if (w != w) return 0xffffffffu;
+  const uint32_t u = __float_as_uint(w + 0.f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+template <bool kOne>
+__global__ void __launch_bounds__(kOne ? 32 : 1024) pick_kernel(const __grid_constant__ PickParams p) {
+  __shared__ uint32_t counts[2][kPickMostWarps];
+  __shared__ uint2 runs[kPickMostWarps];
+  wait_prior_grid();
+  const PageView& pv = p.pv;
+  const GeoHead plan = load_head(pv.geo);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kOne ? 1 : int(blockDim.x >> 5);
+  const long long rows = (long long)plan.total_q * pv.hkv;
+  int turn = 0;
+  auto total = [&](uint32_t v) {  // over the CTA; every thread gets it
+    v = __reduce_add_sync(kAll, v);
+    if (kOne) return v;
+    if (lane == 0) counts[turn][warp] = v;
+    __syncthreads();
+    v = __reduce_add_sync(kAll, lane < warps ? counts[turn][lane] : 0u);
+    turn ^= 1;
+    return v;
+  };
+  for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
+    const int t = int(row / pv.hkv);
+    const Geo g = load_geo(pv.geo, find_request(pv.geo, plan.batch, &Geo::q0, t));
+    const int limit = plan.causal ? g.lkv - g.lq + (t - g.q0) : g.lkv - 1;  // the last key that the token sees
+    const int n = limit < 0 ? 0 : pages_of(pv, limit + 1);
+    const int32_t* ids = pv.kv_indices + g.kv0;
+    int32_t* out = p.selected + row * p.budget;
+    const int kept = min(n, p.budget);
+    for (unsigned i = unsigned(kept) + threadIdx.x; i < unsigned(p.budget); i += blockDim.x) out[i] = -1;
+    if (n <= p.budget) {
+      for (int i = threadIdx.x; i < n; i += blockDim.x) out[i] = __ldg(ids + i);
+      continue;
+    }
+    const int f0 = p.sink, f1 = n - p.recent;  // positions that the scores decide about
+    const uint32_t need = uint32_t(p.budget - p.sink - p.recent);
+    const float* scores = p.scores + row * p.row_pages;
+    const int span = warps * 32 * kPickEach;
+    // position i of this thread in the run that begins at `base`; no score maps to 0, which stands for none
+    auto fetch = [&](int base, uint32_t (&key)[kPickEach]) {
+#pragma unroll
+      for (int i = 0; i < kPickEach; ++i) {
+        const int pos = base + (warp * kPickEach + i) * 32 + lane;
+        key[i] = pos >= f0 && pos < f1 ? score_key(__ldg(scores + pos)) : 0u;
+      }
+    };
+    uint32_t key[kPickEach];
+    fetch(0, key);
+    auto at_least = [&](uint32_t x) {
+      uint32_t k = 0;
+      if (n <= span) {
+#pragma unroll
+        for (int i = 0; i < kPickEach; ++i) k += key[i] >= x;
+      } else {
+        for (int base = 0; base < n; base += span) {
+          uint32_t some[kPickEach];
+          fetch(base, some);
+#pragma unroll
+          for (int i = 0; i < kPickEach; ++i) k += some[i] >= x;
+        }
+      }
+      return total(k);
+    };
+    uint32_t limit_key = 0;  // the largest x with at least `need` scores at or above it
+    bool exact = need == 0;
+    if (exact) limit_key = 0xffffffffu;
+    for (int bit = 31; bit >= 0 && !exact; --bit) {
+      const uint32_t x = limit_key | (1u << bit);
+      const uint32_t k = at_least(x);
+      if (k >= need) limit_key = x;
+      exact = k == need;
+    }
+    // scores above the limit stay, of those at it the first few; if exactly `need` are at or above it, all of them
+    uint32_t ties = exact && need != 0 ? 0xffffffffu : 0u;
+    if (!exact) ties = need - (limit_key == 0xffffffffu ? 0u : at_least(limit_key + 1));
+    uint32_t before = 0, ties_before = 0;  // chosen positions and ties in the runs before
+    for (int base = 0; base < n; base += span) {
+      if (base > 0) fetch(base, key);
+      uint32_t sure = 0, tied = 0;  // of this warp
+      unsigned tie_mask[kPickEach];
+#pragma unroll
+      for (int i = 0; i < kPickEach; ++i) {
+        const int pos = base + (warp * kPickEach + i) * 32 + lane;
+        const bool forced = pos < f0 || (pos >= f1 && pos < n);
+        tie_mask[i] = __ballot_sync(kAll, key[i] == limit_key && key[i] != 0u);
+        sure += __popc(__ballot_sync(kAll, forced || (need != 0 && key[i] > limit_key)));
+        tied += __popc(tie_mask[i]);
+      }
+      uint32_t my_sure = before, my_ties = ties_before;
+      if (!kOne) {
+        __syncthreads();  // the last reads of `runs` and `counts`
+        if (lane == 0) runs[warp] = make_uint2(sure, tied);
+        __syncthreads();
+        const uint2 v = lane < warps ? runs[lane] : make_uint2(0u, 0u);
+        my_sure += __reduce_add_sync(kAll, lane < warp ? v.x : 0u);
+        my_ties += __reduce_add_sync(kAll, lane < warp ? v.y : 0u);
+        before += __reduce_add_sync(kAll, v.x);
+        ties_before += __reduce_add_sync(kAll, v.y);
+      } else {
+        before += sure;
+        ties_before += tied;
+      }
+      uint32_t at = my_sure + min(my_ties, ties);
+#pragma unroll
+      for (int i = 0; i < kPickEach; ++i) {
+        const int pos = base + (warp * kPickEach + i) * 32 + lane;
+        const bool forced = pos < f0 || (pos >= f1 && pos < n);
+        const unsigned below = (1u << lane) - 1;
+        const bool tie = (tie_mask[i] >> lane & 1u) && my_ties + __popc(tie_mask[i] & below) < ties;
+        const unsigned stay = __ballot_sync(kAll, forced || tie || (need != 0 && key[i] > limit_key));
+        if (stay >> lane & 1u) out[at + __popc(stay & below)] = __ldg(ids + pos);
+        at += __popc(stay);
+        my_ties += __popc(tie_mask[i]);
+      }
+    }
+    if (!kOne) __syncthreads();
+  }
+}
+
+// ---- the attention's work --------------------------------------------------------------------------------
+// A unit is a (query token, KV head) row with its own page list.  The lists form one line, counted in steps of block_pages
+// pages (a request's units by its own number of pages, or the budget if that is less), and every CTA gets an equal piece.
+// Unit u's piece in CTA c is item u + c: both grow along the line, so the items need no scan; where a CTA begins with
+// a unit, one number stays free and gets an item without rows.  A unit that spans CTAs a .. b is split unit a, with the slots
+// 2 a, 2 a + 1, ...: the next split unit begins in CTA b at the earliest, and b > a.
+// A warp reads a unit's list: the pages in it, and whether the page where the token's keys end comes last.
+constexpr int kPlanThreads = 256;
+constexpr int kPlanWarps = kPlanThreads / 32;
+
+__device__ __forceinline__ void put_item(int32_t* items, long long at, int page_base, int q_start, int q_len, int head, int lo, int hi, int slot) {
+  reinterpret_cast<int4*>(items)[2 * at] = make_int4(page_base, q_start, q_len, head);
+  reinterpret_cast<int4*>(items)[2 * at + 1] = make_int4(lo, hi, kNotCausalDiag, slot);
+}
+__device__ __forceinline__ void put_unit(int32_t* units, int at, int slot, int n, int q_start, int q_len, int head) {
+  reinterpret_cast<int4*>(units)[2 * at] = make_int4(slot, n, q_start, q_len);
+  reinterpret_cast<int4*>(units)[2 * at + 1] = make_int4(head, 0, 0, 0);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) list_plan_kernel(const __grid_constant__ ListPlanParams p) {
+  __shared__ long long sums[2][kPlanWarps];
+  wait_prior_grid();
+  const PageView& pv = p.pv;
+  const GeoHead plan = load_head(pv.geo);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long units = (long long)plan.total_q * pv.hkv;
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.header[H_NUM_UNITS] = p.ctas;
+  // (a replay may bring more tokens than the list numbers have room for)
+  const bool room = units * p.budget <= INT32_MAX;
+  if (units == 0 || !room) {
+    if (blockIdx.x == 0) {
+      for (int c = threadIdx.x; c <= p.ctas; c += kPlanThreads) p.cta_indptr[c] = 0;
+      for (int c = threadIdx.x; c < p.ctas; c += kPlanThreads) put_unit(p.units, c, 0, 0, 0, 0, 0);
+      if (threadIdx.x == 0 && !room) atomicOr(pv.err, FI_DEVERR_KEPT);
+    }
+    return;
+  }
+  const long long u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+  if (u0 >= u1) return;
+  auto steps_of = [&](const Geo& g) {
+    const int pages = min(pages_of(pv, g.lkv), p.budget);
+    return max(1, (pages + p.block_pages - 1) / p.block_pages);
+  };
+  // the line's length, and its part before the request of this CTA's first unit
+  int r = find_request(pv.geo, plan.batch, &Geo::q0, int(u0 / pv.hkv));
+  long long all = 0, before = 0;
+  for (int k = threadIdx.x; k < plan.batch; k += kPlanThreads) {
+    const Geo g = load_geo(pv.geo, k);
+    const long long n = (long long)g.lq * pv.hkv * steps_of(g);
+    all += n;
+    if (k < r) before += n;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    all += __shfl_xor_sync(kAll, all, o);
+    before += __shfl_xor_sync(kAll, before, o);
+  }
+  if (lane == 0) {
+    sums[0][warp] = all;
+    sums[1][warp] = before;
+  }
+  __syncthreads();
+  all = before = 0;
+#pragma unroll
+  for (int k = 0; k < kPlanWarps; ++k) {
+    all += sums[0][k];
+    before += sums[1][k];
+  }
+  const long long per = max((long long)p.least, (all + p.ctas - 1) / p.ctas);
+  const int used = int((all + per - 1) / per);
+
+  Geo g = load_geo(pv.geo, r);
+  int steps = steps_of(g);
+  for (long long u = u0 + warp; u < u1; u += kPlanWarps) {
+    const int t = int(u / pv.hkv), head = int(u - (long long)t * pv.hkv);
+    while (t >= g.q0 + g.lq) {
+      before += (long long)g.lq * pv.hkv * steps;
+      g = load_geo(pv.geo, ++r);
+      steps = steps_of(g);
+    }
+    const long long a = before + (u - (long long)g.q0 * pv.hkv) * steps, b = a + steps;
+    const int first = int(a / per), last = int((b - 1) / per);
+    // the list: pages up to the first -1, the page of the token's last key at its end or not at all
+    const int limit = plan.causal ? g.lkv - g.lq + (t - g.q0) : g.lkv - 1;
+    const int32_t* list = p.selected + u * p.budget;
+    const int end_page = limit >= 0 ? __ldg(pv.kv_indices + g.kv0 + limit / pv.page_size) : -1;
+    const int end_keys = limit >= 0 ? limit % pv.page_size + 1 : 0;
+    int n = 0;
+    unsigned found = 0, at_end = 0;  // places of the end page among the last 32 read, whether it is the last of the list
+    bool early = false;
+    if (limit >= 0) {
+      constexpr int kAhead = 4;
+      for (int k0 = 0; k0 < p.budget; k0 += 32 * kAhead) {
+        int id[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const int k = k0 + 32 * i + lane;
+          id[i] = k >= k0 && k < p.budget ? __ldg(list + k) : -1;
+        }
+        bool over = false;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          if (over) continue;
+          const unsigned there = __ballot_sync(kAll, id[i] >= 0);
+          const int here = there == kAll ? 32 : __ffs(~there) - 1;
+          found = __ballot_sync(kAll, lane < here && id[i] == end_page);
+          if (here > 0) {
+            early = early || at_end != 0 || (found & ~(1u << (here - 1))) != 0;
+            at_end = found >> (here - 1) & 1u;
+          }
+          n += here;
+          over = here < 32;
+        }
+        if (over || k0 > p.budget - 32 * kAhead) break;
+      }
+    }
+    // (the slots behind the token's last key are not keys: such a page is only read as the last of a list)
+    const bool wrong = early && end_keys < pv.page_size;
+    if (wrong && lane == 0) atomicOr(pv.err, FI_DEVERR_KEPT);
+    const int keys = wrong ? 0 : int(min((long long)INT32_MAX / 2, (long long)n * pv.page_size)) - (at_end ? pv.page_size - end_keys : 0);
+    for (int c = first + lane; c <= last; c += 32) {
+      const long long x0 = max(a, c * per) - a, x1 = min(b, (c + 1) * per) - a;
+      const long long step_keys = (long long)p.block_pages * pv.page_size;
+      const int lo = int(min((long long)keys, x0 * step_keys));
+      const int hi = c == last ? keys : int(min((long long)keys, x1 * step_keys));
+      put_item(p.items, u + c, int(u) * p.budget, t, 1, head, lo, hi, first == last ? -1 : 2 * first + (c - first));
+      if (first != last) p.slot_unit[2 * first + (c - first)] = first;
+      if (c * per >= a) {  // the CTA begins here
+        p.cta_indptr[c] = int(u) + c;
+        const bool inside = c * per > a;
+        if (!inside && c > 0) put_item(p.items, u + c - 1, 0, 0, 0, 0, 0, 0, -1);
+        if (c > 0) {
+          if (inside && c - 1 == first)
+            put_unit(p.units, first, 2 * first, last - first + 1, t, 1, head);
+          else
+            put_unit(p.units, c - 1, 0, 0, 0, 0, 0);
+        }
+      }
+    }
+    if (u == units - 1) {
+      for (int c = used + lane; c <= p.ctas; c += 32) {
+        p.cta_indptr[c] = int(units) + used - 1;
+        put_unit(p.units, c - 1, 0, 0, 0, 0, 0);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+int launch_bounds(const BoundsParams& p, int64_t tasks, bool fp8, int num_sms, cudaStream_t stream) {
+  constexpr int kWarps = kBoundsThreads / 32;
+  const unsigned grid = unsigned(std::max<int64_t>(1, std::min<int64_t>((tasks + kWarps - 1) / kWarps, int64_t(num_sms) * 4)));
+  const cudaError_t e = fp8 ? launch_dependent(bounds_kernel<true>, grid, kBoundsThreads, 0, 1, stream, p)
+                            : launch_dependent(bounds_kernel<false>, grid, kBoundsThreads, 0, 1, stream, p);
+  return e == cudaSuccess ? FI_OK : record_cuda_error(e, "bounds_kernel launch");
+}
+
+int launch_scores(const ScoreParams& p, int64_t tasks, int num_sms, cudaStream_t stream) {
+  constexpr int kWarps = kScoreThreads / 32;
+  const unsigned grid = unsigned(std::max<int64_t>(1, std::min<int64_t>((tasks + kWarps - 1) / kWarps, int64_t(num_sms) * 4)));
+  const cudaError_t e = launch_dependent(scores_kernel, grid, kScoreThreads, 0, 1, stream, p);
+  return e == cudaSuccess ? FI_OK : record_cuda_error(e, "scores_kernel launch");
+}
+
+int launch_pick(const PickParams& p, int64_t rows, int most_pages, int num_sms, cudaStream_t stream) {
+  const int warps = std::min(kPickMostWarps, std::max(1, (most_pages + 32 * kPickEach - 1) / (32 * kPickEach)));
+  const unsigned grid = unsigned(std::max<int64_t>(1, std::min<int64_t>(rows, int64_t(num_sms) * std::min(32, 64 / warps))));
+  const cudaError_t e = warps == 1 ? launch_dependent(pick_kernel<true>, grid, 32, 0, 1, stream, p)
+                                   : launch_dependent(pick_kernel<false>, grid, unsigned(warps) * 32, 0, 1, stream, p);
+  return e == cudaSuccess ? FI_OK : record_cuda_error(e, "pick_kernel launch");
+}
+
+int launch_list_plan(const ListPlanParams& p, int64_t units, int num_sms, cudaStream_t stream) {
+  const unsigned grid = unsigned(std::max<int64_t>(1, std::min<int64_t>((units + kPlanWarps - 1) / kPlanWarps, int64_t(num_sms) * 4)));
+  const cudaError_t e = launch_dependent(list_plan_kernel, grid, kPlanThreads, 0, 1, stream, p);
+  return e == cudaSuccess ? FI_OK : record_cuda_error(e, "list_plan_kernel launch");
+}
+
+}  // namespace fi

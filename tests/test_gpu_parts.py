@@ -1,0 +1,722 @@
+"""GPU parity of attention over parts of a cache (trees of drafted tokens, pages chosen by a score) against the float64 oracle."""
+import ctypes
+import dataclasses
+
+import numpy as np
+import pytest
+
+from oracle import attention as A
+from oracle import parts as P
+from serving_attention_plan_gb300 import binding as B
+from serving_attention_plan_gb300 import workloads as W
+
+from .gpu_helpers import torch_mod
+from .test_gpu_cache import as_layout, batch_of, bf16, bits, dev, f64, workspace
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from serving_attention_plan_gb300 import build
+    build.build()
+    assert torch_mod().cuda.is_available()
+
+
+def pool(b, side, dtype, layout, scale, spread=1.0):
+    """(device pages, their values in 64 bits) of the batch's K or V."""
+    torch = torch_mod()
+    x = as_layout(getattr(b, side), layout)
+    if dtype == "bf16":
+        return bf16(x), A.bf16_to_f64(x)
+    codes = (torch.from_numpy(A.bf16_to_f64(x).astype(np.float32)) * (spread / scale)).to(torch.float8_e4m3fn)
+    return codes.cuda(), A.e4m3_to_f64(codes.view(torch.uint8).numpy()) * scale
+
+
+def outputs(b):
+    torch = torch_mod()
+    o = torch.full((b.total_q, b.num_qo_heads, 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    return o, torch.full((b.total_q, b.num_qo_heads), float("nan"), dtype=torch.float32, device="cuda")
+
+
+def assert_state(o, lse, ref, weight_bits, cap=0.0, cap_rel=0.0):
+    """Against the definition.  A logit is off by the fp32 sum of 128 products (each of 128 additions by 2^-24 of the sum of
+    |terms|: 2^-17, twice that for products that drop bits below the sum's), by its scaling in the exponent (2^-23 of it), and by the soft-cap's tanh (1.5e-7
+    of the cap, or cap_rel of the logit); a weight by e^delta, by the exponential's 2^-22 and by its rounding to 16 bits; the output by its
+    own rounding to bf16, 2^-8.  The sums of weights and products are fp32: 2^-15 of the sum of |terms| covers some
+    hundred chained tiles."""
+    want_o, want_lse, spread, reach = ref
+    o, lse = f64(o), lse.cpu().numpy().astype(np.float64)
+    none = np.isneginf(want_lse)
+    assert not np.isnan(o).any() and not np.isnan(lse).any()
+    assert np.array_equal(np.isneginf(lse), none) and (o[none] == 0).all()
+    some = ~none
+    delta = reach * 2.0 ** -16 + cap * 2e-7 + cap_rel * cap + np.abs(np.where(none, 0, want_lse)) * 2.0 ** -20 + 2.0 ** -18
+    assert (np.abs(lse[some] - want_lse[some]) <= delta[some]).all(), np.abs(lse[some] - want_lse[some]).max()
+    tol = np.abs(want_o) * 2.0 ** -8 + spread * (weight_bits + 2 * delta[..., None] + 2.0 ** -15) + 1e-30
+    assert (np.abs(o - want_o) <= tol).all(), (np.abs(o - want_o) / tol).max()
+
+
+BF16_WEIGHTS = 2.0 ** -8
+# f16 weights: half a step of 2^-11; those below 2^-14 lose at most 2^-25 each, and a row's weights are relative to its largest
+F16_WEIGHTS = 2.0 ** -11 + 2.0 ** -14
+
+
+# ---- trees -------------------------------------------------------------------------------------------
+
+
+def random_mask(rng, b, kind):
+    """int32 [total_q, words] masks."""
+    lens = np.diff(b.qo_indptr)
+    if kind == "tree":
+        parents = np.concatenate([[rng.integers(-1, t) if t else -1 for t in range(n)] for n in lens] + [[]]).astype(np.int32)
+        return B.tree_mask(b.qo_indptr, parents)
+    words = max(1, -(-int(lens.max(initial=0)) // 32)) + (kind == "wide")
+    m = rng.integers(0, 2 ** 32, size=(b.total_q, words), dtype=np.uint64).astype(np.uint32)
+    if kind == "sparse":  # most rows see few drafted tokens, some none
+        m &= rng.integers(0, 2 ** 32, size=m.shape, dtype=np.uint64).astype(np.uint32) & rng.integers(0, 2 ** 32, size=m.shape, dtype=np.uint64).astype(np.uint32)
+        m[::3] = 0
+    return m.view(np.int32)
+
+
+TREES = [
+    # l_q, l_kv, query heads, KV heads, page, dtype, layout, cap, masks, SMs
+    ([1], [1], 1, 1, 16, "bf16", "HND", 0.0, "tree", 0),
+    ([1, 1, 1], [1, 129, 640], 8, 2, 16, "bf16", "HND", 0.0, "tree", 0),
+    ([16, 0, 11, 13], [316, 40, 11, 583], 8, 2, 16, "bf16", "HND", 0.0, "tree", 0),
+    ([5, 33, 64], [133, 33, 700], 12, 4, 8, "bf16", "NHD", 0.0, "tree", 4),
+    ([64, 100], [1500, 131], 8, 1, 32, "bf16", "HND", 0.0, "wide", 0),            # 512 and 800 rows: several row tiles
+    ([7, 9], [7, 260], 16, 2, 128, "bf16", "HND", 0.0, "sparse", 3),             # rows that see nothing
+    ([20, 3], [12, 0], 4, 2, 16, "bf16", "HND", 0.0, "sparse", 0),               # more tokens than keys, no keys
+    ([3, 2], [300, 65], 128, 1, 64, "bf16", "HND", 0.0, "tree", 0),              # one token a row tile
+    ([3, 40], [200, 999], 10, 2, 16, "bf16", "HND", 30.0, "tree", 7),            # five heads a group
+    ([17, 2], [1030, 90], 8, 2, 16, "bf16", "NHD", 200.0, "wide", 0),
+    ([1], [5000], 1, 1, 16, "bf16", "HND", 0.0, "tree", 0),                     # one row over many CTAs
+    ([2] * 70, list(range(1, 211, 3)), 4, 2, 8, "bf16", "HND", 0.0, "tree", 0),  # many short requests
+    ([1], [1], 1, 1, 16, "e4m3", "HND", 0.0, "tree", 0),
+    ([16, 0, 11, 13], [316, 40, 11, 583], 8, 2, 16, "e4m3", "HND", 0.0, "tree", 0),
+    ([5, 33, 64], [133, 33, 700], 12, 4, 8, "e4m3", "NHD", 0.0, "wide", 4),
+    ([20, 3], [12, 0], 4, 2, 128, "e4m3", "HND", 0.0, "sparse", 0),
+    ([25, 30], [1300, 777], 64, 8, 64, "e4m3", "NHD", 30.0, "tree", 0),
+    ([30], [4000], 4, 1, 32, "e4m3", "HND", 100.0, "tree", 0),
+]
+
+
+@pytest.mark.parametrize("case", TREES, ids=range(len(TREES)))
+def test_tree(case):
+    lq, lkv, hq, hk, ps, dtype, layout, cap, kind, sms = case
+    b = batch_of(lq, lkv, hq, hk, ps, False, seed=len(lq) + ps + hq, scale=1.3)
+    scales = (0.0625, 0.03125) if dtype == "e4m3" else (1.0, 1.0)
+    (k, kv), (v, vv) = pool(b, "k_pages", dtype, layout, scales[0]), pool(b, "v_pages", dtype, layout, scales[1])
+    mask = random_mask(np.random.default_rng(hq + ps), b, kind)
+    ws = workspace(b, cap=cap, layout=layout, dtype=dtype, scales=scales, num_sms=sms)
+    q, (o, lse) = bf16(b.q), outputs(b)
+    ws.tree_run(q, k, v, dev(mask), o, lse)
+    torch_mod().cuda.synchronize()
+    assert ws.get_error() == 0
+    ref = P.tree_attention(b, f64(q), kv, vv, mask, cap, layout)
+    assert_state(o, lse, ref, F16_WEIGHTS if dtype == "e4m3" else BF16_WEIGHTS, cap, 4e-6 if cap > 64 else 0.0)
+    again = outputs(b)
+    ws.tree_run(q, k, v, dev(mask), *again)
+    assert np.array_equal(bits(again[0]), bits(o)) and torch_mod().equal(again[1], lse)
+
+
+@pytest.mark.parametrize("dtype,ps", [("bf16", 16), ("bf16", 128), ("e4m3", 32)])
+def test_tree_unseen_values_and_unused_slots(dtype, ps):
+    """NaN and infinities in the page slots behind the last key, and in K rows that no token sees, reach no output."""
+    torch = torch_mod()
+    b = batch_of([4, 6], [ps + 9, 70], 8, 2, ps, False, seed=3)
+    (k, kv), (v, vv) = pool(b, "k_pages", dtype, "HND", 1.0), pool(b, "v_pages", dtype, "HND", 1.0)
+    mask = np.zeros((10, 1), np.int32)
+    mask[:4, 0] = [0b1, 0b11, 0b1, 0b1001]      # nobody sees drafted token 2 of request 0
+    mask[4:, 0] = [0b1, 0b10, 0b101, 0b1001, 0b10001, 0b100001]
+    codes_k, codes_v = (x.view(torch.uint8 if dtype == "e4m3" else torch.int16) for x in (k, v))
+    nan, inf = (0x7F, 0x7E) if dtype == "e4m3" else (0x7FC0, 0x7F80)
+    for i, n in enumerate((ps + 9, 70)):
+        page = int(b.kv_indices[b.kv_indptr[i + 1] - 1])
+        codes_k[page, :, (n - 1) % ps + 1:] = nan
+        codes_v[page, :, (n - 1) % ps + 1:] = nan
+    j = ps + 9 - 4 + 2
+    codes_k[int(b.kv_indices[j // ps]), 0, j % ps] = nan
+    codes_k[int(b.kv_indices[j // ps]), 1, j % ps] = inf
+    ws = workspace(b, dtype=dtype)
+    q, (o, lse) = bf16(b.q), outputs(b)
+    ws.tree_run(q, k, v, dev(mask), o, lse)
+    torch.cuda.synchronize()
+    assert_state(o, lse, P.tree_attention(b, f64(q), kv, vv, mask), F16_WEIGHTS if dtype == "e4m3" else BF16_WEIGHTS)
+
+
+def test_tree_of_a_chain_is_causal_attention():
+    """A chain's mask is the causal one: the same rows as fi_run's on a causal plan, within both kernels' roundings."""
+    torch = torch_mod()
+    b = batch_of([40, 7, 1], [900, 7, 300], 8, 2, 16, True, seed=9)
+    ws = workspace(b)
+    q, k, v = bf16(b.q), bf16(b.k_pages), bf16(b.v_pages)
+    mask = B.tree_mask(b.qo_indptr, np.concatenate([np.arange(n) - 1 for n in (40, 7, 1)]))
+    (o, lse), (ro, rl) = outputs(b), outputs(b)
+    ws.tree_run(q, k, v, dev(mask), o, lse)
+    ws.run(q, k, v, ro, rl)
+    torch.cuda.synchronize()
+    assert (lse - rl).abs().max() <= 2.0 ** -12 and (o.float() - ro.float()).abs().max() <= 0.04
+
+
+def capture(call):
+    torch = torch_mod()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            call()
+    torch.cuda.synchronize()
+    return g
+
+
+def plan(ws, b):
+    ws.plan(b.qo_indptr, b.kv_indptr, b.kv_indices, b.last_page_len, b.page_size, b.causal)
+
+
+def test_tree_replayed():
+    """A captured call follows later plans of as many tokens: other lengths, page lists and masks."""
+    torch = torch_mod()
+    a = batch_of([20, 12], [60, 30], 8, 2, 16, False, seed=1, extra=200)
+    b = batch_of([1, 29, 2], [900, 1500, 2], 8, 2, 16, False, seed=2, extra=a.num_pages - 153)
+    assert a.num_pages >= int(b.kv_indptr[-1])
+    ws = B.Workspace(4, 32, 300, 8, 2)
+    pages = max(a.num_pages, b.num_pages)
+    rng = np.random.default_rng(0)
+    k, v = (bf16(W.f32_to_bf16_bits(rng.standard_normal((pages, 2, 16, 128)).astype(np.float32))) for _ in range(2))
+    q, (o, lse) = bf16(a.q), outputs(a)
+    mask = torch.zeros(32, 2, dtype=torch.int32, device="cuda")
+    plan(ws, a)
+    g = capture(lambda: ws.tree_run(q, k, v, mask, o, lse))
+    for x in (b, a):
+        plan(ws, x)
+        m = random_mask(rng, x, "wide")[:, :2]
+        mask.copy_(dev(np.ascontiguousarray(m)))
+        o.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert ws.get_error() == 0
+        assert_state(o, lse, P.tree_attention(x, f64(q), A.bf16_to_f64(bits(k)), A.bf16_to_f64(bits(v)), m), BF16_WEIGHTS)
+
+
+def test_tree_refusals():
+    torch = torch_mod()
+    b = batch_of([40, 1], [100, 20], 8, 2, 16, False)
+    ws = workspace(b)
+    q, k, v, (o, lse) = bf16(b.q), bf16(b.k_pages), bf16(b.v_pages), outputs(b)
+    ones = torch.ones(41, 2, dtype=torch.int32, device="cuda")
+    for args in ((q[1:], k, v, ones, o, lse), (q, k[:, :1], v, ones, o, lse), (q, k, v, ones[:40], o, lse), (q, k, v, ones.long(), o, lse),
+                 (q, k, v, ones, o.float(), lse), (q, k, v, ones, o, lse[:, :7]), (q, k, v, ones.cpu(), o, lse), (q, k, v, ones[:, 0], o, lse),
+                 (q, k, v, ones.t().contiguous().t(), o, lse)):
+        with pytest.raises(ValueError):
+            ws.tree_run(*args)
+    with pytest.raises(B.FiError) as e:  # one word for 40 tokens
+        ws.tree_run(q, k, v, ones[:, :1].contiguous(), o, lse)
+    assert e.value.status == 1
+    for change, status in (({"window": 5, "causal": True}, 3),):
+        w = workspace(dataclasses.replace(b, causal=True), window=5)
+        with pytest.raises(B.FiError) as e:
+            w.tree_run(q, k, v, ones, o, lse)
+        assert e.value.status == status
+    small = batch_of([1, 1], [9, 20], 8, 2, 4, False)
+    w = workspace(small)
+    with pytest.raises(B.FiError) as e:  # a page size that the tiles do not take
+        w.tree_run(bf16(small.q), bf16(small.k_pages), bf16(small.v_pages), ones[:2], *outputs(small))
+    assert e.value.status == 3
+    many = batch_of([1], [9], 129, 1, 16, False)
+    w = workspace(many)
+    with pytest.raises(B.FiError) as e:
+        w.tree_run(bf16(many.q), bf16(many.k_pages), bf16(many.v_pages), ones[:1], *outputs(many))
+    assert e.value.status == 3
+    with pytest.raises(B.FiError) as e:
+        B.Workspace(2, 41, 20, 8, 2).tree_run(q, k, v, ones, o, lse)
+    assert e.value.status == 6
+    assert ws.get_error() == 0
+
+
+# ---- the accepted path ---------------------------------------------------------------------------------
+
+COMMITS = [
+    # l_q, l_kv, KV heads, page, dtype, layout, path length
+    ([1], [1], 1, 1, "bf16", "HND", 1),
+    ([16, 9, 0, 30], [116, 9, 40, 333], 2, 16, "bf16", "HND", 7),
+    ([64, 50], [80, 700], 8, 32, "bf16", "NHD", 64),          # paths over several groups of rows
+    ([5, 8], [3, 8], 2, 5, "bf16", "HND", 6),                 # a token without a slot, an odd page size
+    ([16, 9, 0, 30], [116, 9, 40, 333], 3, 8, "e4m3", "HND", 7),
+    ([60] * 40, [60 + 3 * i for i in range(40)], 4, 16, "e4m3", "NHD", 33),
+]
+
+
+@pytest.mark.parametrize("case", COMMITS, ids=range(len(COMMITS)))
+def test_commit(case):
+    torch = torch_mod()
+    lq, lkv, hk, ps, dtype, layout, length = case
+    b = batch_of(lq, lkv, hk, hk, ps, False, seed=ps + hk)
+    rng = np.random.default_rng(ps)
+    path = np.full((len(lq), length), -1, np.int32)
+    for i, n in enumerate(lq):
+        first = max(0, n - lkv[i])  # tokens before the first key have no slot
+        m = min(length, n - first, int(rng.integers(0, n + 1)) + (i % 2))
+        path[i, :m] = np.sort(rng.permutation(np.arange(first, n))[:m])
+        path[i, m + 1:] = 7  # behind the path's end
+    ws = workspace(b, layout=layout, dtype=dtype)
+    if dtype == "bf16":
+        k0, v0 = as_layout(b.k_pages, layout), as_layout(b.v_pages, layout)
+        k, v = bf16(k0), bf16(v0)
+    else:
+        k0, v0 = (as_layout(rng.integers(0, 256, size=b.k_pages.shape).astype(np.uint8), layout) for _ in range(2))
+        k, v = dev(k0), dev(v0)
+    ws.tree_commit(dev(path), k, v)
+    torch.cuda.synchronize()
+    assert ws.get_error() == 0
+    ended = np.where(np.cumsum(path < 0, 1) > 0, -1, path)
+    for got, want in zip((k, v), P.commit(b, ended, [k0, v0], layout)):
+        assert np.array_equal(bits(got) if dtype == "bf16" else got.cpu().numpy(), want)
+
+
+def test_commit_skips_bad_entries():
+    """Entries that do not ascend or lie outside the request are skipped and reported; no other slot is touched."""
+    torch = torch_mod()
+    b = batch_of([8, 8], [20, 50], 2, 2, 4, False, seed=4)
+    ws = workspace(b)
+    k0, v0 = b.k_pages, b.v_pages
+    k, v = bf16(k0), bf16(v0)
+    path = np.array([[2, 2, 5, 8, 2 ** 31 - 1], [1, 0, 7, -1, 3]], np.int32)
+    ws.tree_commit(dev(path), k, v)
+    torch.cuda.synchronize()
+    assert ws.get_error() == B.DEVERR_KEPT and ws.get_error() == 0
+    want_k, want_v = k0.copy(), v0.copy()
+    for i, j, e in ((0, 0, 2), (0, 2, 5), (1, 0, 1), (1, 2, 7)):
+        (fp,), (fs,) = P.places(b, i, [(12, 42)[i] + e])
+        (tp,), (ts,) = P.places(b, i, [(12, 42)[i] + j])
+        want_k[tp, :, ts], want_v[tp, :, ts] = k0[fp, :, fs], v0[fp, :, fs]
+    assert np.array_equal(bits(k), want_k) and np.array_equal(bits(v), want_v)
+
+
+def test_commit_refusals():
+    torch = torch_mod()
+    b = batch_of([3, 3], [9, 20], 2, 2, 16, False)
+    ws = workspace(b)
+    k, v = bf16(b.k_pages), bf16(b.v_pages)
+    path = torch.zeros(2, 3, dtype=torch.int32, device="cuda")
+    for args in ((path[:1], k, v), (path.long(), k, v), (path, k[:, :1], v), (path, k, v.float()), (path.cpu(), k, v)):
+        with pytest.raises(ValueError):
+            ws.tree_commit(*args)
+    with pytest.raises(B.FiError) as e:
+        ws.tree_commit(path[:, :0], k, v)
+    assert e.value.status == 1
+    same = b.kv_indices.copy()
+    same[-1] = same[0]  # the page of request 0's tokens takes request 1's, too
+    ws.plan(b.qo_indptr, b.kv_indptr, same, b.last_page_len, 16, False)
+    with pytest.raises(B.FiError) as e:
+        ws.tree_commit(path, k, v)
+    assert e.value.status == 3
+    assert np.array_equal(bits(k), b.k_pages) and np.array_equal(bits(v), b.v_pages)
+
+
+# ---- bounds, scores, choice ------------------------------------------------------------------------------
+
+BOUNDS = [
+    # l_q, l_kv, KV heads, page, dtype, layout
+    ([1], [1], 1, 1, "bf16", "HND"),
+    ([1, 0, 17, 300], [40, 33, 17, 900], 2, 16, "bf16", "HND"),
+    ([2, 1, 1], [7, 64, 129], 8, 64, "bf16", "NHD"),
+    ([9, 3], [5, 0], 3, 8, "bf16", "HND"),                        # more tokens than keys, no keys
+    ([1, 2], [30, 11], 1, 5, "bf16", "HND"),
+    ([130, 1], [1000, 300], 4, 128, "bf16", "HND"),
+    ([1, 0, 17, 300], [40, 33, 17, 900], 2, 16, "e4m3", "NHD"),
+    ([1, 1], [500, 3], 4, 128, "e4m3", "HND"),
+    ([1, 1, 1], [5, 4, 1], 2, 4, "e4m3", "HND"),
+    ([1] * 200, [2 * i + 1 for i in range(200)], 8, 8, "e4m3", "HND"),
+]
+
+
+@pytest.mark.parametrize("new_keys", [False, True])
+@pytest.mark.parametrize("case", BOUNDS, ids=range(len(BOUNDS)))
+def test_bounds(case, new_keys):
+    torch = torch_mod()
+    lq, lkv, hk, ps, dtype, layout = case
+    b = batch_of(lq, lkv, hk, hk, ps, False, seed=ps + hk)
+    k, kv = pool(b, "k_pages", dtype, layout, 1.0, spread=3.0)
+    # slots behind the last key hold NaN: they are not looked at
+    raw = k.view(torch.uint8 if dtype == "e4m3" else torch.int16)
+    for i, n in enumerate(lkv):
+        if n % ps:
+            page = int(b.kv_indices[b.kv_indptr[i + 1] - 1])
+            (raw[page][:, n % ps:] if layout == "HND" else raw[page][n % ps:]).fill_(0x7F if dtype == "e4m3" else 0x7FC0)
+    ws = workspace(b, layout=layout, dtype=dtype, scales=(0.5, 1.0))
+    old = torch.full((b.num_pages, hk, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    got = old.clone()
+    ws.page_bounds(k, got, new_keys=new_keys)
+    torch.cuda.synchronize()
+    assert ws.get_error() == 0
+    assert np.array_equal(f64(got), P.page_bounds(b, kv, f64(old), new_keys, layout))
+
+
+def test_bounds_of_nan_infinite_and_signed_zero_keys():
+    torch = torch_mod()
+    b = batch_of([1], [16], 1, 1, 16, False)
+    k = bf16(b.k_pages)
+    page = int(b.kv_indices[0])
+    k[page, 0, 3, 0] = float("nan")
+    k[page, 0, 4, 1], k[page, 0, 5, 1] = float("inf"), -float("inf")
+    k[page, 0, :, 2] = -0.0
+    got = torch.zeros(b.num_pages, 1, 2, 128, dtype=torch.bfloat16, device="cuda")
+    ws = workspace(b)
+    ws.page_bounds(k, got)
+    lo, hi = f64(got)[page, 0]
+    assert np.isnan(lo[0]) and np.isnan(hi[0]) and lo[1] == -np.inf and hi[1] == np.inf and lo[2] == 0 and hi[2] == 0
+    assert np.array_equal(lo[3:], f64(k)[page, 0].min(0)[3:]) and np.array_equal(hi[3:], f64(k)[page, 0].max(0)[3:])
+
+
+SCORES = [
+    # l_q, l_kv, query heads, KV heads, page, causal, row slack
+    ([1], [1], 1, 1, 16, False, 0),
+    ([1, 1, 0, 1], [500, 17, 60, 1024], 8, 2, 16, False, 3),
+    ([4, 3, 1], [600, 2, 40], 12, 4, 8, True, 0),                  # three heads a group, more tokens than keys
+    ([2, 5], [300, 299], 10, 2, 16, True, 1),                      # five
+    ([1, 2], [900, 64], 7, 1, 32, False, 0),
+    ([3, 1], [500, 129], 24, 2, 8, True, 0),                       # twelve: two sets of columns
+    ([2], [333], 33, 1, 16, False, 0),
+    ([40, 20], [700, 20], 8, 8, 16, True, 0),                      # a prompt's tokens
+    ([1, 1], [40, 0], 4, 2, 1, True, 0),
+    ([2, 1] * 40, [3 + 7 * (i % 40) for i in range(80)], 4, 2, 4, False, 0),
+]
+
+
+@pytest.mark.parametrize("case", SCORES, ids=range(len(SCORES)))
+def test_scores(case):
+    torch = torch_mod()
+    lq, lkv, hq, hk, ps, causal, slack = case
+    b = batch_of(lq, lkv, hq, hk, ps, causal, seed=ps + hq, scale=1.5)
+    rng = np.random.default_rng(hq)
+    lo = rng.standard_normal((b.num_pages, hk, 128)).astype(np.float32)
+    both = np.stack([lo, lo + np.abs(rng.standard_normal(lo.shape).astype(np.float32)) * 2], 2)
+    bounds = bf16(W.f32_to_bf16_bits(both))
+    row = max(1, int(np.diff(b.kv_indptr).max()) + slack)
+    scores = torch.full((b.total_q, hk, row), 5.0, device="cuda")
+    q = bf16(b.q)
+    ws = workspace(b, dtype="e4m3", scales=(0.25, 1.0)) if ps in (8, 16) else workspace(b)
+    ws.score_pages(q, bounds, scores)
+    torch.cuda.synchronize()
+    assert ws.get_error() == 0
+    want, reach = P.page_scores(b, f64(q), f64(bounds), np.full(scores.shape, 5.0), 0.25 if ps in (8, 16) else 1.0)
+    got = scores.cpu().numpy().astype(np.float64)
+    assert np.array_equal(np.isneginf(got), np.isneginf(want))
+    fin = np.isfinite(want)
+    # 256 exact products summed in fp32, 2^-24 of the sum of |terms| each, twice that for products that drop bits
+    assert (np.abs(got[fin] - want[fin]) <= reach * 2.0 ** -15).all()
+
+
+def test_scores_show_nan_and_infinite_bounds():
+    torch = torch_mod()
+    b = batch_of([1], [48], 4, 1, 16, False)
+    bounds = torch.zeros(b.num_pages, 1, 2, 128, dtype=torch.bfloat16, device="cuda")
+    p0, p1, p2 = (int(x) for x in b.kv_indices)
+    bounds[p0, 0, 0, 3] = float("nan")
+    bounds[p1, 0, 1, 7] = float("inf")
+    bounds[p2, 0, 1] = 1.0
+    scores = torch.zeros(1, 1, 3, device="cuda")
+    q = torch.ones(1, 4, 128, dtype=torch.bfloat16, device="cuda")
+    workspace(b).score_pages(q, bounds, scores)
+    s = scores.cpu().numpy()[0, 0]
+    assert np.isnan(s[0]) and s[1] == np.inf and abs(s[2] - 128 ** 0.5) < 1e-4
+
+
+SELECT = [
+    # l_q, l_kv, KV heads, page, causal, sink, recent, budget, kind
+    ([1], [1], 1, 16, False, 0, 0, 1, "normal"),
+    ([1, 1, 0, 1], [500, 17, 60, 4097], 2, 16, False, 1, 2, 9, "normal"),
+    ([4, 3, 2], [600, 2, 40], 4, 8, True, 1, 1, 5, "normal"),
+    ([1, 1], [3000, 2999], 2, 4, False, 0, 0, 300, "ties"),
+    ([1, 1], [3000, 2999], 2, 4, False, 2, 3, 700, "ties"),
+    ([1], [5000], 1, 1, False, 4, 100, 1000, "equal"),
+    ([1], [5000], 1, 1, False, 0, 0, 4999, "special"),
+    ([1], [700], 2, 1, False, 3, 4, 7, "special"),              # nothing but sink and recent
+    ([2, 1], [700, 9], 2, 1, True, 0, 5, 2 ** 20, "normal"),     # all pages
+    ([1], [40_000], 1, 1, False, 4, 16, 10_000, "ties"),         # longer than the threads hold
+    ([3], [20_000], 2, 1, True, 1, 0, 64, "special"),
+]
+
+
+@pytest.mark.parametrize("case", SELECT, ids=range(len(SELECT)))
+def test_select(case):
+    torch = torch_mod()
+    lq, lkv, hk, ps, causal, sink, recent, budget, kind = case
+    n = sum(-(-x // ps) for x in lkv)
+    b = W.make_paged_batch(np.random.default_rng(5), "select", lq, lkv, hk, hk, ps, causal, pool_pages=n + 3, with_data=False)
+    total_q = int(b.qo_indptr[-1])
+    rng = np.random.default_rng(budget)
+    row = int(np.diff(b.kv_indptr).max()) + 2
+    x = rng.standard_normal((total_q, hk, row)).astype(np.float32) * 8
+    if kind == "ties":
+        x = np.round(x)
+    elif kind == "equal":
+        x[:] = -3.5
+    elif kind == "special":
+        x[rng.random(x.shape) < 0.3] = -np.inf
+        x[rng.random(x.shape) < 0.01] = np.nan
+        x[rng.random(x.shape) < 0.01] = np.inf
+        x[rng.random(x.shape) < 0.05] = -0.0
+        x[rng.random(x.shape) < 0.05] = 0.0
+    ws = B.Workspace(len(lq), max(total_q, 1), n, hk, hk)
+    plan(ws, b)
+    selected = torch.full((total_q, hk, budget), 77, dtype=torch.int32, device="cuda")
+    ws.select_pages(dev(x), selected, recent=recent, sink=sink)
+    torch.cuda.synchronize()
+    assert ws.get_error() == 0
+    assert np.array_equal(selected.cpu().numpy(), P.select_pages(b, x, sink, recent, budget))
+
+
+# ---- attention over the chosen pages -----------------------------------------------------------------------
+
+PAGES = [
+    # l_q, l_kv, query heads, KV heads, page, dtype, layout, causal, cap, budget, SMs
+    ([1], [1], 1, 1, 16, "bf16", "HND", False, 0.0, 1, 0),
+    ([1, 1, 0, 1], [500, 17, 60, 1500], 8, 2, 16, "bf16", "HND", False, 0.0, 20, 0),
+    ([4, 3, 2], [600, 2, 40], 8, 2, 8, "bf16", "HND", True, 0.0, 7, 3),
+    ([1, 1], [900, 800], 16, 2, 32, "bf16", "HND", False, 0.0, 10, 0),
+    ([1, 1], [300, 77], 5, 1, 5, "bf16", "HND", True, 0.0, 30, 0),        # the loader of odd page sizes
+    ([1, 1], [64, 129], 4, 4, 64, "bf16", "NHD", False, 30.0, 2, 0),
+    ([1] * 9, [10, 0, 2000, 64, 31, 32, 33, 1000, 1], 10, 2, 1, "bf16", "HND", False, 0.0, 400, 0),
+    ([2, 3], [1000, 700], 40, 2, 16, "bf16", "HND", True, 0.0, 12, 0),     # 20 heads a group: tensor-core tiles
+    ([1], [3000], 64, 1, 8, "bf16", "NHD", False, 0.0, 200, 0),            # cut over many CTAs
+    ([1, 1, 0, 1], [500, 17, 60, 1500], 8, 2, 16, "e4m3", "HND", False, 0.0, 20, 0),
+    ([1, 4], [400, 260], 16, 2, 64, "e4m3", "NHD", True, 30.0, 3, 5),
+    ([2], [300], 2, 2, 4, "e4m3", "HND", True, 0.0, 60, 0),
+    ([2, 3], [1000, 700], 24, 2, 128, "e4m3", "HND", True, 0.0, 4, 0),
+    ([1] * 152, [40] * 152, 2, 1, 32, "bf16", "HND", False, 0.0, 2, 0),     # a CTA's piece ends where a unit does
+    ([1] * 3, [128] * 3, 8, 1, 128, "bf16", "HND", False, 0.0, 1, 2),
+]
+
+
+@pytest.mark.parametrize("case", PAGES, ids=range(len(PAGES)))
+def test_pages(case):
+    torch = torch_mod()
+    lq, lkv, hq, hk, ps, dtype, layout, causal, cap, budget, sms = case
+    b = batch_of(lq, lkv, hq, hk, ps, causal, seed=ps + hq, scale=1.3)
+    scales = (0.0625, 0.03125) if dtype == "e4m3" else (1.0, 1.0)
+    (k, kv), (v, vv) = pool(b, "k_pages", dtype, layout, scales[0]), pool(b, "v_pages", dtype, layout, scales[1])
+    rng = np.random.default_rng(budget)
+    row = max(1, int(np.diff(b.kv_indptr).max()))
+    selected = P.select_pages(b, rng.standard_normal((b.total_q, hk, row)), 0, 1 if budget > 1 else 0, budget)
+    selected[0, 0] = -1  # a list without pages
+    if b.total_q > 2:  # a list that ends before its room does
+        some = selected[2, 0][selected[2, 0] >= 0]
+        selected[2, 0] = -1
+        selected[2, 0, :len(some) // 2] = some[:len(some) // 2]
+    ws = workspace(b, cap=cap, layout=layout, dtype=dtype, scales=scales, num_sms=sms)
+    q, (o, lse) = bf16(b.q), outputs(b)
+    ws.run_pages(q, k, v, dev(selected), o, lse)
+    torch.cuda.synchronize()
+    assert ws.get_error() == 0
+    ref = P.pages_attention(b, f64(q), kv, vv, selected, cap, layout)
+    assert_state(o, lse, ref, F16_WEIGHTS if dtype == "e4m3" else BF16_WEIGHTS, cap)
+    again = outputs(b)
+    ws.run_pages(q, k, v, dev(selected), *again)
+    assert np.array_equal(bits(again[0]), bits(o)) and torch.equal(again[1], lse)
+    # fi_run of the same workspace has its own plan still
+    (ro, rl), ref = outputs(b), A.batch_attention(b) if dtype == "bf16" and layout == "HND" and cap == 0 else None
+    if ref is not None:
+        ws.run(q, k, v, ro, rl)
+        torch.cuda.synchronize()
+        assert np.abs(f64(ro) - ref[0]).max(initial=0) <= 2e-2
+
+
+def test_pages_list_with_the_end_page_elsewhere():
+    """The page that is not full counts as a list's last alone: elsewhere the list is empty and reported."""
+    torch = torch_mod()
+    b = batch_of([1, 1], [40, 48], 4, 1, 16, False, seed=6)
+    ws = workspace(b)
+    q, k, v, (o, lse) = bf16(b.q), bf16(b.k_pages), bf16(b.v_pages), outputs(b)
+    first, second = b.kv_indices[:3], b.kv_indices[3:]
+    selected = np.array([[first[[0, 2, 1]]], [second[[2, 0, 1]]]], np.int32)  # request 1's pages are full: any order
+    ws.run_pages(q, k, v, dev(selected), o, lse)
+    torch.cuda.synchronize()
+    assert ws.get_error() == B.DEVERR_KEPT
+    assert torch.isneginf(lse[0]).all() and (o[0] == 0).all()
+    selected[0] = -1
+    assert_state(o, lse, P.pages_attention(b, f64(q), f64(k), f64(v), selected), BF16_WEIGHTS)
+
+
+def test_choice_replayed():
+    """Bounds, scores, choice and attention captured in one graph on a small batch and replayed on a larger one, and on none."""
+    torch = torch_mod()
+    small = batch_of([1], [20], 8, 2, 16, True, seed=1)
+    large = batch_of([2, 1, 3], [900, 1500, 64], 8, 2, 16, True, seed=2)
+    none = batch_of([], [], 8, 2, 16, True, seed=3)
+    pages = large.num_pages + 40
+    rng = np.random.default_rng(1)
+    k, v = (bf16(W.f32_to_bf16_bits(rng.standard_normal((pages, 2, 16, 128)).astype(np.float32))) for _ in range(2))
+    q = bf16(W.f32_to_bf16_bits(rng.standard_normal((6, 8, 128)).astype(np.float32)))
+    ws = B.Workspace(4, 6, 200, 8, 2)
+    L = B.lib()
+    bounds = torch.zeros(pages, 2, 2, 128, dtype=torch.bfloat16, device="cuda")
+    scores = torch.zeros(6, 2, 100, device="cuda")
+    selected = torch.zeros(6, 2, 8, dtype=torch.int32, device="cuda")
+    o, lse = torch.zeros(6, 8, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(6, 8, device="cuda")
+
+    def step():
+        s = torch.cuda.current_stream().cuda_stream
+        h = ws.handle
+        assert L.fi_page_bounds(h, k.data_ptr(), pages, 0, bounds.data_ptr(), s) == 0
+        assert L.fi_score_pages(h, q.data_ptr(), bounds.data_ptr(), pages, scores.data_ptr(), 100, s) == 0
+        assert L.fi_select_pages(h, scores.data_ptr(), 100, 1, 1, 8, selected.data_ptr(), s) == 0
+        assert L.fi_run_pages(h, q.data_ptr(), k.data_ptr(), v.data_ptr(), pages, selected.data_ptr(), 8, o.data_ptr(), lse.data_ptr(), s) == 0
+
+    plan(ws, small)
+    g = capture(step)
+    for b in (large, none, small):
+        n = b.total_q
+        plan(ws, b)
+        o.fill_(9.0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert ws.get_error() == 0
+        assert (o[n:] == 9.0).all()  # rows behind the last token are as they were
+        if n == 0:
+            continue
+        kv, vv = A.bf16_to_f64(bits(k)), A.bf16_to_f64(bits(v))
+        want = P.page_bounds(b, kv, np.zeros(bounds.shape), False)
+        used = b.kv_indices[:int(b.kv_indptr[-1])]
+        assert np.array_equal(f64(bounds)[used], want[used])
+        sc = scores[:n].cpu().numpy()
+        sel = P.select_pages(b, sc, 1, 1, 8)
+        assert np.array_equal(selected[:n].cpu().numpy(), sel)
+        assert_state(o[:n], lse[:n], P.pages_attention(b, f64(q)[:n], kv, vv, sel), BF16_WEIGHTS)
+
+
+def test_choice_refusals():
+    torch = torch_mod()
+    b = batch_of([1, 1], [40, 20], 8, 2, 16, False)
+    ws = workspace(b)
+    q, k, v, (o, lse) = bf16(b.q), bf16(b.k_pages), bf16(b.v_pages), outputs(b)
+    bounds = torch.zeros(b.num_pages, 2, 2, 128, dtype=torch.bfloat16, device="cuda")
+    scores = torch.zeros(2, 2, 3, device="cuda")
+    sel = torch.full((2, 2, 2), -1, dtype=torch.int32, device="cuda")
+    for call in (lambda: ws.page_bounds(k, bounds[1:]), lambda: ws.page_bounds(k, bounds.float()), lambda: ws.page_bounds(k[:, :, :8], bounds),
+                 lambda: ws.score_pages(q[:1], bounds, scores), lambda: ws.score_pages(q, bounds, scores[:, :1]),
+                 lambda: ws.score_pages(q, bounds, scores.double()), lambda: ws.select_pages(scores, sel.long()),
+                 lambda: ws.select_pages(scores, sel[:1]), lambda: ws.run_pages(q, k, v, sel.long(), o, lse),
+                 lambda: ws.run_pages(q, k, v, sel, o[:, :4], lse), lambda: ws.run_pages(q, k, v, sel.cpu(), o, lse)):
+        with pytest.raises(ValueError):
+            call()
+
+    def refused(status, call):
+        with pytest.raises(B.FiError) as e:
+            call()
+        assert e.value.status == status
+
+    refused(1, lambda: ws.score_pages(q, bounds, scores[..., :2].contiguous()))  # a request has three pages
+    refused(1, lambda: ws.select_pages(scores[..., :2].contiguous(), sel))
+    refused(1, lambda: ws.select_pages(scores, sel, recent=2, sink=1))
+    refused(1, lambda: ws.select_pages(scores, sel, recent=-1))
+    refused(1, lambda: ws.select_pages(scores, sel[..., :0]))
+    refused(1, lambda: ws.run_pages(q, k, v, sel[..., :0], o, lse))
+    L, s, h = B.lib(), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream), ws.handle
+    ptr = lambda t, off=0: t.data_ptr() + off
+    assert L.fi_run_pages(h, ptr(q), ptr(k), ptr(v), b.num_pages, ptr(sel), 2, ptr(o, 8), ptr(lse), s) == 1
+    assert L.fi_run_pages(h, ptr(q), ptr(k), 0, b.num_pages, ptr(sel), 2, ptr(o), ptr(lse), s) == 1
+    assert L.fi_run_pages(h, ptr(q), ptr(k), ptr(v), b.num_pages, ptr(sel), 2 ** 30, ptr(o), ptr(lse), s) == 3
+    assert L.fi_page_bounds(h, ptr(k), b.num_pages, 2, ptr(bounds), s) == 1
+    assert L.fi_page_bounds(h, ptr(k), 1, 0, ptr(bounds), s) == 1  # pages outside the pool
+    w = workspace(dataclasses.replace(b, causal=True), window=5)
+    for call in (lambda: w.score_pages(q, bounds, scores), lambda: w.select_pages(scores, sel), lambda: w.run_pages(q, k, v, sel, o, lse)):
+        refused(3, call)
+    empty = B.Workspace(2, 2, 20, 8, 2)
+    for call in (lambda: empty.page_bounds(k, bounds), lambda: empty.score_pages(q, bounds, scores), lambda: empty.select_pages(scores, sel),
+                 lambda: empty.run_pages(q, k, v, sel, o, lse), lambda: empty.tree_commit(sel[0], k, v)):
+        refused(6, call)
+    three = batch_of([1], [40], 3, 3, 16, False)  # three KV heads, token-major
+    t = workspace(three)
+    t.set_variant(kv_layout="NHD")
+    refused(3, lambda: plan(t, three))
+    assert ws.get_error() == 0
+
+
+# ---- together ----------------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_speculative_steps(dtype):
+    """Two rounds of drafting over chosen pages, verifying the tree, and committing the path, against a cache kept on the host."""
+    torch = torch_mod()
+    rng = np.random.default_rng(8)
+    hq, hk, ps = 8, 2, 16
+    scales = (0.0625, 0.03125) if dtype == "e4m3" else (1.0, 1.0)
+    lens, pages = np.array([500, 77]), 64
+    lists = [rng.permutation(pages)[:40], None]
+    lists[1] = np.setdiff1d(np.arange(pages), lists[0])[:20]
+    ws = B.Workspace(2, 32, 64, hq, hk)
+    ws.set_kv_dtype(dtype, *scales)
+    kind = torch.bfloat16 if dtype == "bf16" else torch.float8_e4m3fn
+    k, v = ((torch.randn(pages, hk, ps, 128, device="cuda") / s).to(kind) for s in scales)
+    bounds = torch.zeros(pages, hk, 2, 128, dtype=torch.bfloat16, device="cuda")
+    weights = F16_WEIGHTS if dtype == "e4m3" else BF16_WEIGHTS
+
+    def batch(lq, lkv):
+        kv = np.concatenate([x[:-(-n // ps)] for x, n in zip(lists, lkv)]).astype(np.int32)
+        n = [-(-x // ps) for x in lkv]
+        return W.PagedBatch(name="step", num_qo_heads=hq, num_kv_heads=hk, head_dim=128, page_size=ps, causal=True,
+                            qo_indptr=np.concatenate([[0], np.cumsum(lq)]).astype(np.int32), kv_indptr=np.concatenate([[0], np.cumsum(n)]).astype(np.int32),
+                            kv_indices=kv, last_page_len=np.array([x - (m - 1) * ps for x, m in zip(lkv, n)], np.int32), q=None, k_pages=None, v_pages=None)
+
+    def values(x, s):
+        return f64(x) * s
+
+    def rows(n):
+        return torch.randn(n, hq + 2 * hk, 128, device="cuda").to(torch.bfloat16)
+
+    for turn in range(2):
+        # a draft token over eight pages of each request
+        b = batch([1, 1], lens + 1)
+        plan(ws, b)
+        x = rows(2)
+        q = torch.empty(2, hq, 128, dtype=torch.bfloat16, device="cuda")
+        ws.append(x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:], k, v, q)
+        ws.page_bounds(k, bounds, new_keys=turn > 0)
+        scores, sel = torch.zeros(2, hk, 40, device="cuda"), torch.zeros(2, hk, 8, dtype=torch.int32, device="cuda")
+        ws.score_pages(q, bounds, scores)
+        ws.select_pages(scores, sel, recent=1, sink=1)
+        o, lse = torch.empty_like(q), torch.empty(2, hq, device="cuda")
+        ws.run_pages(q, k, v, sel, o, lse)
+        host = P.select_pages(b, scores.cpu().numpy(), 1, 1, 8)
+        assert np.array_equal(sel.cpu().numpy(), host)
+        want, reach = P.page_scores(b, f64(q), P.page_bounds(b, f64(k), f64(bounds), False), np.zeros(scores.shape), scales[0])
+        assert np.abs(scores.cpu().numpy() - want).max() <= reach * 2.0 ** -15  # the bounds are those of the whole cache
+        assert_state(o, lse, P.pages_attention(b, f64(q), values(k, scales[0]), values(v, scales[1]), host), weights)
+        # a tree behind the context, verified, one path of it kept
+        lq = [9, 14]
+        b = batch(lq, lens + lq)
+        plan(ws, b)
+        x = rows(23)
+        q = torch.empty(23, hq, 128, dtype=torch.bfloat16, device="cuda")
+        ws.append(x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:], k, v, q)
+        parents = np.concatenate([[rng.integers(-1, t) if t else -1 for t in range(n)] for n in lq])
+        mask = B.tree_mask(b.qo_indptr, parents)
+        o, lse = torch.empty_like(q), torch.empty(23, hq, device="cuda")
+        ws.tree_run(q, k, v, dev(mask), o, lse)
+        torch.cuda.synchronize()
+        assert_state(o, lse, P.tree_attention(b, f64(q), values(k, scales[0]), values(v, scales[1]), mask), weights)
+        path = np.full((2, 5), -1, np.int32)
+        for i, n in enumerate(lq):
+            up, leaf = [], int(rng.integers(0, n))
+            while leaf >= 0:
+                up.append(leaf)
+                leaf = int(parents[b.qo_indptr[i] + leaf])
+            up = up[::-1][:5]
+            path[i, :len(up)] = up
+        raw = lambda t: t.view(torch.int16 if dtype == "bf16" else torch.uint8).cpu().numpy()
+        want = P.commit(b, path, [raw(k), raw(v)])
+        ws.tree_commit(dev(path), k, v)
+        torch.cuda.synchronize()
+        assert np.array_equal(raw(k), want[0]) and np.array_equal(raw(v), want[1])
+        ws.page_bounds(k, bounds, new_keys=True)  # of what the tree's slots hold now, the refused tokens' too
+        lens = lens + (path >= 0).sum(1)
+        plan(ws, batch((path >= 0).sum(1), lens))
+        ws.page_bounds(k, bounds, new_keys=True)
+        assert ws.get_error() == 0
