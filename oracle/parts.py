@@ -11,9 +11,10 @@ from .attention import gather_kv
 from .cache import lengths, places
 
 
-def state(q, k, v, seen, cap=0.0):
+def state(q, k, v, seen, cap=0.0, q_floor=0.0):
     """(o, lse, spread, reach) of rows q [m, D] over keys k, v [n, D] under seen [m, n]: softmax(x) v with x = q.k / sqrt(D),
-    soft-capped; spread = softmax(x) |v| and reach = the largest sum of |terms| of a seen logit (both for tolerances)."""
+    soft-capped; spread = softmax(x) |v| and reach = the largest sum of |terms| of a seen logit, each |q_d| with q_floor of the
+    row's largest added (both for tolerances)."""
     m, n = seen.shape
     o, lse = np.zeros((m, q.shape[1])), np.full(m, -np.inf)
     spread, reach = np.zeros_like(o), np.zeros(m)
@@ -30,7 +31,7 @@ def state(q, k, v, seen, cap=0.0):
         lse[r] = top + np.log(w.sum())
         w /= w.sum()
         o[r], spread[r] = w @ v[on], w @ np.abs(v[on])
-        reach[r] = scale * (np.abs(k[on]) @ np.abs(q[r])).max()
+        reach[r] = scale * (np.abs(k[on]) @ (np.abs(q[r]) + q_floor * np.abs(q[r]).max())).max()
     return o, lse, spread, reach
 
 
@@ -45,7 +46,7 @@ def tree_seen(mask, q0, l_q, l_kv):
     return seen
 
 
-def tree_attention(batch, q, k_pages, v_pages, mask, cap=0.0, layout="HND"):
+def tree_attention(batch, q, k_pages, v_pages, mask, cap=0.0, layout="HND", q_floor=0.0):
     """(o, lse, spread, reach) of every query row: [total_q, H_qo, D] and [total_q, H_qo]."""
     l_q, l_kv = lengths(batch)
     hkv = k_pages.shape[1] if layout == "HND" else k_pages.shape[2]
@@ -59,7 +60,7 @@ def tree_attention(batch, q, k_pages, v_pages, mask, cap=0.0, layout="HND"):
         for h in range(hkv):
             k, v = (gather_kv(x, batch.kv_indptr, batch.kv_indices, n, batch.page_size, i, h, layout) for x in (k_pages, v_pages))
             for hh in range(h * g, (h + 1) * g):
-                for a, b in zip(out, state(q[q0:q0 + t, hh], k, v, seen, cap)):
+                for a, b in zip(out, state(q[q0:q0 + t, hh], k, v, seen, cap, q_floor)):
                     a[q0:q0 + t, hh] = b
     return out
 

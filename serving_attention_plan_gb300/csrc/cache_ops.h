@@ -17,7 +17,7 @@ struct Geo {
   int32_t blk0;      // 32-key blocks of the requests before this one that take the row form of the weights
   int32_t tile0;     // 256-key tiles of the requests before this one (told by fi_cache_plan_compute, read by no kernel)
   int32_t work0;     // tensor-core weights: Q tiles (over all KV heads) of the requests before this one
-  int32_t tree0;     // tree attention: 128-key tiles (over KV heads and row tiles) of the requests before this one
+  int32_t tree0;     // tree attention: 128-key tiles (over KV heads and pairs of row tiles) of the requests before this one
 };
 // The plan as a whole, in the place before the first entry: one load gives a kernel all of it.
 struct GeoHead {

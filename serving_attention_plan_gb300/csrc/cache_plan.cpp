@@ -67,8 +67,8 @@ void split_weights(Geo* geo, int batch, int hkv, int group, int row_limit, bool 
   totals->work = work;
 }
 
-bool fill_tree(Geo* geo, int batch, int hkv, int group, int32_t* total) {
-  const int tokens = kTreeRows / group;
+bool fill_tree(Geo* geo, int batch, int hkv, int group, int ctas, int32_t* total, int32_t* starts) {
+  const int tokens = 2 * (kTreeRows / group);  // of a unit: two row tiles
   int64_t tiles = 0;
   for (int i = 0; i <= batch; ++i) {
     geo[i].tree0 = int32_t(tiles);
@@ -78,6 +78,11 @@ bool fill_tree(Geo* geo, int batch, int hkv, int group, int32_t* total) {
     if (tiles > INT32_MAX / 2) return false;  // a CTA's end of the line stays in 32 bits
   }
   *total = int32_t(tiles);
+  const int64_t per = std::max<int64_t>(kTreeLeastTiles, (tiles + ctas - 1) / ctas);
+  for (int c = 0, r = 0; c < ctas; ++c) {
+    while (r + 1 < batch && geo[r + 1].tree0 <= c * per) ++r;
+    starts[c] = r;
+  }
   return true;
 }
 

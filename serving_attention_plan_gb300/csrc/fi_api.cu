@@ -55,7 +55,7 @@ struct fi_workspace {
 
   // segment byte offsets; [0, plan_bytes) is mirrored in pinned host memory.  The a_* segments and
   // the ext list hold the shared part of a composable plan.
-  size_t off_header = 0, off_cta = 0, off_geo = 0, off_items = 0, off_units = 0, off_slot_unit = 0, off_kv = 0, plan_bytes = 0;
+  size_t off_header = 0, off_cta = 0, off_geo = 0, off_tree = 0, off_items = 0, off_units = 0, off_slot_unit = 0, off_kv = 0, plan_bytes = 0;
   size_t off_a_header = 0, off_a_cta = 0, off_a_items = 0, off_a_kv = 0, off_ext = 0;
   // the work of fi_run_pages, made on the GPU
   size_t off_l_header = 0, off_l_cta = 0, off_l_items = 0, off_l_units = 0, off_l_slot_unit = 0;
@@ -125,7 +125,8 @@ void set_geo(fi_workspace* ws, const int32_t* qo_indptr, const int32_t* kv_indpt
                       ws->variant.kv_dtype == FI_KV_DTYPE_E4M3 ? fi::kRowFormMostE4m3 : fi::kRowFormMostBf16,
                       causal != 0, window, &ws->geo);
   int32_t tree = 0;
-  ws->tree_ok = group <= fi::kTreeRows && fi::fill_tree(geo, batch, ws->hkv, group, &tree);
+  ws->tree_ok = group <= fi::kTreeRows && fi::fill_tree(geo, batch, ws->hkv, group, ws->num_sms, &tree,
+                                                                 reinterpret_cast<int32_t*>(ws->hbuf + ws->off_tree));
   const fi::GeoHead head = {batch, qo_indptr[batch], int32_t(ws->geo.blocks), int32_t(ws->geo.work),
                             causal, window, tree, 0};
   std::memcpy(geo - 1, &head, sizeof(head));
@@ -388,6 +389,7 @@ int fi_workspace_create(int max_batch, int max_total_q, int max_kv_pages, int nu
   ws->off_header = seg(sizeof(int32_t) * fi::kHeaderLen);
   ws->off_cta = seg(sizeof(int32_t) * (ws->max_ctas + 1));
   ws->off_geo = seg(sizeof(fi::Geo) * (size_t(max_batch) + 2));
+  ws->off_tree = seg(sizeof(int32_t) * num_sms);
   ws->off_items = seg(sizeof(int32_t) * fi::kItemFields * ws->max_items);
   ws->off_units = seg(sizeof(int32_t) * fi::kUnitFields * ws->max_units);
   ws->off_slot_unit = seg(sizeof(int32_t) * ws->max_slots);
@@ -520,6 +522,7 @@ int fi_plan(fi_workspace* ws, const int32_t* qo_indptr, const int32_t* kv_indptr
       {ws->off_header, sizeof(plan.header)},
       {ws->off_cta, plan.cta_indptr.size() * sizeof(int32_t)},
       {ws->off_geo, (size_t(batch) + 2) * sizeof(fi::Geo)},
+      {ws->off_tree, sizeof(int32_t) * size_t(ws->num_sms)},
       {ws->off_items, plan.items.size() * sizeof(int32_t)},
       {ws->off_units, plan.units.size() * sizeof(int32_t)},
       {ws->off_slot_unit, plan.slot_unit.size() * sizeof(int32_t)},
@@ -1002,6 +1005,7 @@ int fi_tree_run(fi_workspace* ws, const void* q, const void* k_pages, const void
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k_pages = k_pages;
   p.v_pages = v_pages;
+  p.starts = reinterpret_cast<const int32_t*>(ws->dbuf + ws->off_tree);
   p.mask = static_cast<const uint32_t*>(mask);
   p.mask_words = mask_words;
   p.o = static_cast<__nv_bfloat16*>(o);

@@ -5,24 +5,33 @@
 //   j - (l_kv - l_q) of t's mask is set.
 //
 // What bounds it: a tree has 8 to 64 tokens, so a KV head has 32 to 512 query rows; up to 128 rows a key costs
-// 2 * 128 * 128 products for 512 bytes, which the tensor cores do in a third of the time that the bytes take.  The tile is
-// therefore 128 rows of one KV head (rows are (token, head of the group) pairs) and the kernel is built to
-// stream keys; more rows are further tiles, whose keys come from L2.
+// 2 * 128 * 128 products for 512 bytes, which the tensor cores do in a third of the time that the bytes take.  The kernel
+// is therefore built to stream keys past a tile of 128 rows of one KV head (rows are (token, head of the group) pairs), or
+// past two such tiles at once: with one tile a pass, 256 rows read every key twice, and the second reading, from L2, took
+// as long as the first.
 //
-// Split: the 128-key tiles of all (request, KV head, row tile) units form one line, and every CTA takes an equal piece
-// of it, wherever that cuts a unit.  Nothing of this is planned on the host but the line's prefix per request, so a captured
-// launch follows later plans.  A unit that was cut leaves partial states, which a second launch joins in order.
+// Split: the 128-key tiles of all (request, KV head, pair of row tiles) units form one line, and every CTA takes an equal
+// piece of it, wherever that cuts a unit.  Nothing of this is planned on the host but the line's prefix per request, so a
+// captured launch follows later plans.  A unit that was cut leaves partial states, which a second launch joins in order.
 //
-// One CTA an SM.  The keys of a tile are worked on in two halves of 64, each with its own running maximum,
-// sum and accumulator, so that two softmax groups keep the tensor cores and each other busy; the halves are
-// joined when the unit's piece is written.
-//   warps 0-3, 4-7    softmax of keys 0-63 and 64-127 of every tile; a thread owns a row (TMEM lane)
-//   warps 8-11        the two halves of a finished piece joined, to the output or to a partial slot
+// One CTA an SM.  Two softmax groups, each with its own running maximum, sum and accumulator, keep the tensor cores
+// and each other busy, 64 keys a step: with one row tile group h takes keys 64 h .. 64 h + 63 of every tile, and the two
+// states are joined when the piece is written; with two it takes row tile h.
+//   warps 0-3, 4-7    softmax of group 0 and 1; a thread owns a row (TMEM lane)
+//   warps 8-11        a finished piece, to the output or to a partial slot; e4m3: Q as two e4m3 terms
 //   warps 12-15       TMA of page boxes, every stage's boxes dealt to the four (one warp's issue ends at 4 TB/s)
-//   warp 16, 17       issue of S = Q K^T (128 x 128) and of O_h += P_h V_h
-//   warps 20-23       e4m3 pages: codes widened to f16, exactly, from a ring of their own
-// TMEM: two score buffers of 128 columns (P overwrites a half's first 32), O_0 and O_1.
-// Shared memory: two Q tiles; bf16: five K / V tiles; e4m3: three widened tiles and four of codes.
+//   warps 16, 17      issue of S = Q K^T and of O_h += P_h V
+//   warp 18           the CTA's pieces, ahead of the others (found out by each warp for itself, the next piece cost 5000
+//                     clocks of waiting for its request's entry)
+//   warps 20-23       e4m3: V widened to f16
+// TMEM: two score buffers of 2 x 64 columns (P overwrites a group's first 32), O_0 and O_1.
+// Shared memory: two Q tiles; bf16: five K / V tiles; e4m3: six tiles of codes and two of widened V.
+//
+// e4m3 pages: K's codes go into the products as they are, against q as a sum of two e4m3 terms (each row scaled by a power
+// of two that brings its largest element to 128 .. 256; the sum is exact for elements above 2^-9 of that, and right to 2^-17
+// of it for the others), at the rate of as many bf16 products.  V is widened to f16, exactly, so that the weights keep 11
+// bits.  (K and V both widened: the widening and the few f16 tiles that shared memory holds set the pace, 2800
+// clocks a tile, where the bytes take 1450.)
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_fp8.h>
@@ -49,38 +58,78 @@ constexpr uint32_t kColO = 256;             // O_h at 256 + 128 h, S_b at 128 b
 constexpr float kRescaleThreshold = 8.f;    // O is rescaled when a row's maximum grows by more than 2^8
 constexpr int kLoaders = 4;
 
-// Registers of a thread per warpgroup.  Launched with 96 (bf16, 640 threads) or 80 (e4m3, 768), 480 for a thread of each
-// warpgroup together; the shares below add up to that.
+// Registers of a thread per warpgroup.  Launched with 96 (bf16, 640 threads) or 80 (e4m3, 768); the shares below add up to
+// that.
 template <bool kFp8>
 struct Shape {
   static constexpr int kThreads = kFp8 ? 768 : 640;
   static constexpr int kLaunchRegs = kFp8 ? 80 : 96;
-  static constexpr uint32_t kSoftmaxRegs = kFp8 ? 144 : 160;
-  static constexpr uint32_t kJoinRegs = 80;
+  static constexpr uint32_t kSoftmaxRegs = kFp8 ? 152 : 160;
+  static constexpr uint32_t kWriteRegs = kFp8 ? 72 : 80;
   static constexpr uint32_t kLoadRegs = kFp8 ? 32 : 40;
   static constexpr uint32_t kIssueRegs = kFp8 ? 32 : 40;
-  static constexpr uint32_t kWidenRegs = kFp8 ? 48 : 0;
-  static_assert(2 * kSoftmaxRegs + kJoinRegs + kLoadRegs + kIssueRegs + kWidenRegs == kLaunchRegs * (kThreads / 128),
+  static constexpr uint32_t kWidenRegs = kFp8 ? 40 : 0;
+  static_assert(2 * kSoftmaxRegs + kWriteRegs + kLoadRegs + kIssueRegs + kWidenRegs == kLaunchRegs * (kThreads / 128),
                 "the warpgroups' registers are those of the launch");
-  static constexpr int kTiles = kFp8 ? 3 : 5;  // K / V tiles that the products read
-  static constexpr int kRaw = kFp8 ? 4 : 0;    // tiles of codes
-  static constexpr int kRing = kFp8 ? kRaw : kTiles;  // tiles that TMA fills
+  static constexpr int kRing = kFp8 ? 6 : 5;  // tiles that TMA fills, K and V in turn
+  static constexpr int kTile = kFp8 ? kHalfBytes : kTileBytes;
+  static constexpr int kWide = kFp8 ? 2 : 0;  // V tiles widened
+  static constexpr int kReaders = 8 + 4 + kLoaders + 2 + (kFp8 ? 4 : 0);  // warps that read the pieces
 };
+
+// A run of tiles of one (request, KV head, pair of row tiles) unit.
+struct Piece {
+  int q0, nq;         // its first query token, tokens
+  int kv0, lkv, lq;   // the request's first page entry, keys, tokens
+  int head;
+  int k0, k1;         // tiles [k0, k1) of the unit's; none: the pieces end here
+  int slot;           // partial slot, or -1 for a whole unit
+  int pad[3];
+};
+static_assert(sizeof(Piece) == 48, "three 16-byte words");
+constexpr int kPieces = 4;  // found ahead
 
 template <bool kFp8>
 struct TreeSmem {
-  uint8_t q[2][kTileBytes];  // [2 dim halves][128 rows][128 B], 128B-swizzled
-  uint8_t kv[Shape<kFp8>::kTiles][kTileBytes];
-  uint8_t raw[kFp8 ? Shape<kFp8>::kRaw : 1][kFp8 ? kHalfBytes : 16];  // [128 keys][128 codes]
+  uint8_t q[2][kTileBytes];  // [2 dim halves][128 rows][128 B] of bf16, 128B-swizzled; e4m3: then [2 terms][128 rows][128 codes]
+  uint8_t kv[Shape<kFp8>::kRing][Shape<kFp8>::kTile];
+  uint8_t wide[kFp8 ? Shape<kFp8>::kWide : 1][kFp8 ? kTileBytes : 16];
   float stat_m[2][kRows], stat_l[2][kRows];
+  Piece pieces[kPieces];
+  int8_t q_exp[2][kRows];  // e4m3: q = 2^exp (term 0 + term 1), kQuiet for a row that is not finite
+  uint64_t piece_full[kPieces], piece_empty[kPieces];
   uint64_t q_full[2], q_empty[2], q_ready[2];
-  uint64_t full[Shape<kFp8>::kRing], raw_empty[kFp8 ? Shape<kFp8>::kRaw : 1];
-  uint64_t ready[Shape<kFp8>::kTiles], empty[Shape<kFp8>::kTiles];  // ready: e4m3, widened
-  uint64_t s_full[2], p_full[2][2], pv_done[2][2];  // [half][buffer]
+  uint64_t full[Shape<kFp8>::kRing], empty[Shape<kFp8>::kRing];
+  uint64_t wide_full[2], wide_empty[2];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [group][buffer]
   uint64_t stat_full, stat_empty, o_free;
   uint32_t tmem_base;
   int abort;
 };
+constexpr int kQuiet = -128;
+
+// Bounded wait for a barrier's phase: kTries tries that may each sleep for a microsecond, two seconds (60 ms if none of them
+// slept; the longest wait, for the end of a piece, is 2 us a tile).  There are some forty waits: with a look at the clock
+// in each, as in mbar_wait, the roles' code outgrew the instruction cache.
+constexpr uint32_t kTries = 1u << 21;
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, int32_t* err, volatile int* abort) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n\t"
+      "TRY:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+      "@p bra DONE;\n\t"
+      "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, %3;\n\t"
+      "@q bra TRY;\n\t"
+      "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity), "n"(kTries)
+      : "memory");
+  if (done) return true;
+  if (*abort == 0) atomicOr(err, FI_DEVERR_WAIT_TIMEOUT);
+  *abort = 1;
+  return false;
+}
 
 // ---- the line of tiles ---------------------------------------------------------------------------
 
@@ -92,69 +141,76 @@ struct Line {
   }
 };
 
-// A run of tiles of one (request, KV head, row tile) unit.
-struct Piece {
-  int q0, nq;         // its first query token, tokens
-  int kv0, lkv, lq;   // the request's first page entry, keys, tokens
-  int head;
-  int k0, k1;         // tiles [k0, k1) of the unit's
-  int slot;           // partial slot, or -1 for a whole unit
-};
-
-// The pieces of a part [pos, end) of the line, in order.
-struct Walk {
-  const Geo* geo;
-  int batch, hkv, tokens;  // tokens of a row tile
-  int pos, end, per, cta;
-  int r, tiles, row_tiles, unit, at;  // request, tiles and row tiles of its units, the unit's number, next tile
-  Geo g;
-
-  __device__ __forceinline__ void enter() {
-    g = load_geo(geo, r);
-    tiles = max(1, (g.lkv + kKeys - 1) / kKeys);
-    row_tiles = (g.lq + tokens - 1) / tokens;
-  }
-  // A whole warp; the part is not empty.
-  __device__ void init(const TreeParams& p, const GeoHead& plan, const Line& line, int cta_) {
-    geo = p.pv.geo;
-    batch = plan.batch;
-    hkv = p.pv.hkv;
-    tokens = p.tile_tokens;
-    per = line.per;
-    cta = cta_;
-    pos = cta * per;
-    end = min(line.total, pos + per);
-    r = find_request(geo, batch, &Geo::tree0, pos);
-    enter();
-    const int in = pos - g.tree0;
-    unit = in / tiles;
-    at = in - unit * tiles;
-  }
-  __device__ __forceinline__ bool next(Piece& c) {
-    if (pos >= end) return false;
-    while (unit == hkv * row_tiles) {
-      ++r;
-      unit = 0;
+// Warp 18: the pieces of the CTA's part [pos, end) of the line, which begins in request r, in order, into the ring.
+template <bool kFp8>
+__device__ void find_pieces(const TreeParams& p, TreeSmem<kFp8>& sm, const GeoHead& plan, const Line& line, int cta, int r) {
+  const int lane = threadIdx.x & 31, hkv = p.pv.hkv, tokens = 2 * p.tile_tokens;
+  int pos = cta * line.per;
+  const int end = min(line.total, pos + line.per);
+  Geo g = load_geo(p.pv.geo, r), after = load_geo(p.pv.geo, r + 1);  // (an entry lies behind the last request)
+  int tiles = max(1, (g.lkv + kKeys - 1) / kKeys), sets = (g.lq + tokens - 1) / tokens;
+  int unit = (pos - g.tree0) / tiles, at = pos - g.tree0 - unit * tiles;
+  for (int n = 0;; ++n) {
+    const int slot = n % kPieces;
+    if (n >= kPieces && !__all_sync(kAll, wait_for(&sm.piece_empty[slot], (n / kPieces - 1) & 1, p.pv.err, &sm.abort))) return;
+    Piece c = {};
+    if (pos < end) {
+      while (unit == hkv * sets) {
+        g = after;
+        after = load_geo(p.pv.geo, min(++r + 1, plan.batch));
+        tiles = max(1, (g.lkv + kKeys - 1) / kKeys);
+        sets = (g.lq + tokens - 1) / tokens;
+        unit = at = 0;
+      }
+      const int set = unit % sets;
+      c.head = unit / sets;
+      c.q0 = g.q0 + set * tokens;
+      c.nq = min(tokens, g.lq - set * tokens);
+      c.kv0 = g.kv0;
+      c.lkv = g.lkv;
+      c.lq = g.lq;
+      c.k0 = at;
+      c.k1 = at + min(tiles - at, end - pos);
+      const int a = pos - at, first = a / line.per;  // the unit's place on the line, the CTA that begins it
+      c.slot = (a + tiles - 1) / line.per != first ? 2 * first + (cta - first) : -1;
+      pos += c.k1 - c.k0;
       at = 0;
-      enter();
+      ++unit;
     }
-    const int tile = unit % row_tiles;
-    c.head = unit / row_tiles;
-    c.q0 = g.q0 + tile * tokens;
-    c.nq = min(tokens, g.lq - tile * tokens);
-    c.kv0 = g.kv0;
-    c.lkv = g.lkv;
-    c.lq = g.lq;
-    c.k0 = at;
-    c.k1 = at + min(tiles - at, end - pos);
-    const int a = pos - at, first = a / per;  // the unit's place on the line, the CTA that begins it
-    c.slot = (a + tiles - 1) / per != first ? 2 * first + (cta - first) : -1;
-    pos += c.k1 - c.k0;
-    at = 0;
-    ++unit;
-    return true;
+    if (lane == 0) {
+      sm.pieces[slot] = c;
+      mbar_arrive(&sm.piece_full[slot]);
+    }
+    __syncwarp();
+    if (c.k0 == c.k1) return;
   }
-};
+}
+
+// Piece number n, for a whole warp; false behind the last one.
+template <bool kFp8>
+__device__ __forceinline__ bool take(const TreeParams& p, TreeSmem<kFp8>& sm, int n, Piece& c) {
+  const int slot = n % kPieces;
+  const bool ok = __all_sync(kAll, wait_for(&sm.piece_full[slot], (n / kPieces) & 1, p.pv.err, &sm.abort));
+  const int4* src = reinterpret_cast<const int4*>(&sm.pieces[slot]);
+  const int4 x = src[0], y = src[1];
+  c.q0 = x.x;
+  c.nq = x.y;
+  c.kv0 = x.z;
+  c.lkv = x.w;
+  c.lq = y.x;
+  c.head = y.y;
+  c.k0 = y.z;
+  c.k1 = y.w;
+  c.slot = src[2].x;
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&sm.piece_empty[slot]);
+  return ok && c.k0 < c.k1;
+}
+
+// Steps of 64 keys a group that a piece takes.
+__device__ __forceinline__ int steps_of(const Piece& c, bool two) {
+  return two ? max(1, (min(c.k1 * kKeys, c.lkv) - c.k0 * kKeys + kHalfKeys - 1) / kHalfKeys) : c.k1 - c.k0;
+}
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t on;
@@ -165,10 +221,10 @@ __device__ __forceinline__ bool elect_one() {
 // ---- loads -----------------------------------------------------------------------------------------
 
 // Loader warp `w` of four: its share of the boxes of every tile, K and V in turn.  A box is one page and KV head, 64 dims
-// (bf16, 128B-swizzled) or 128 codes (e4m3); pages behind the request's last read as zeros.
+// (bf16) or 128 codes (e4m3), 128B-swizzled; pages behind the request's last read as zeros.
 template <bool kFp8>
-__device__ void load_tiles(const TreeParams& p, TreeSmem<kFp8>& sm, Walk walk, const CUtensorMap* tm_q,
-                           const CUtensorMap* tm_k, const CUtensorMap* tm_v, int w) {
+__device__ void load_tiles(const TreeParams& p, TreeSmem<kFp8>& sm, const CUtensorMap* tm_q, const CUtensorMap* tm_k,
+                           const CUtensorMap* tm_v, int w) {
   using S = Shape<kFp8>;
   const int lane = threadIdx.x & 31;
   const int ps = p.pv.page_size, pages = kKeys / ps;
@@ -177,9 +233,6 @@ __device__ void load_tiles(const TreeParams& p, TreeSmem<kFp8>& sm, Walk walk, c
   const int page = kFp8 ? mine : mine >> 1, half = kFp8 ? 0 : mine & 1;
   const uint32_t bytes = uint32_t((boxes - w + kLoaders - 1) / kLoaders) * uint32_t(ps) * 128u;
   const uint32_t place = uint32_t(half) * kHalfBytes + uint32_t(page * ps) * 128u;
-  uint8_t* ring = kFp8 ? sm.raw[0] : sm.kv[0];
-  constexpr int kStep = kFp8 ? kHalfBytes : kTileBytes;
-  uint64_t* empty = kFp8 ? sm.raw_empty : sm.empty;
   auto locate = [&](const Piece& c, int t) {  // the page of this lane's box, num_pages for none
     int z = p.pv.num_pages;
     const int e = t * pages + page;
@@ -193,43 +246,46 @@ __device__ void load_tiles(const TreeParams& p, TreeSmem<kFp8>& sm, Walk walk, c
     return z;
   };
   Piece c;
-  int n = 0, nu = 0;  // tiles and pieces issued
-  bool ok = true, more = walk.next(c);
-  int t = more ? c.k0 : 0;
+  int n = 0, nu = 0, nq = 0;  // tiles, pieces, Q tiles
+  bool ok = true, more = take(p, sm, nu++, c);
+  int t = c.k0;
   int z_next = more ? locate(c, t) : 0;
   while (more && ok) {
     const int z = z_next, head = c.head;
-    if (t == c.k0) {
-      if (w == 0) {
-        const int b = nu & 1;
-        if (nu >= 2) ok = __all_sync(kAll, mbar_wait(&sm.q_empty[b], ((nu >> 1) - 1) & 1, p.pv.err, &sm.abort));
-        if (ok && lane == 0) {
-          mbar_arrive_expect_tx(&sm.q_full[b], p.q_tile_bytes);
-          tc::tma_load_3d(sm.q[b], tm_q, 0, head * p.group, c.q0, &sm.q_full[b]);
-          tc::tma_load_3d(sm.q[b] + kHalfBytes, tm_q, 64, head * p.group, c.q0, &sm.q_full[b]);
-        }
-        __syncwarp();
-        if (!ok) break;
-      }
-      ++nu;
-    }
+    int q0 = c.q0, q_left = t == c.k0 ? c.nq : 0;  // the piece's Q tiles come behind its first K tile, whose place is free before theirs
     if (++t == c.k1) {
-      more = walk.next(c);
+      more = take(p, sm, nu++, c);
       t = c.k0;
     }
     if (more) z_next = locate(c, t);  // lands while this tile waits for its place
     for (int v = 0; v < 2; ++v, ++n) {
       const int slot = n % S::kRing;
-      if (n >= S::kRing) ok = __all_sync(kAll, mbar_wait(&empty[slot], (n / S::kRing - 1) & 1, p.pv.err, &sm.abort));
+      if (n >= S::kRing) ok = __all_sync(kAll, wait_for(&sm.empty[slot], (n / S::kRing - 1) & 1, p.pv.err, &sm.abort));
       if (!ok) break;
       if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], bytes);
       __syncwarp();
-      if (mine < boxes) tc::tma_load_4d(ring + slot * kStep + place, v ? tm_v : tm_k, 64 * half, head, 0, z, &sm.full[slot]);
+      if (mine < boxes) tc::tma_load_4d(sm.kv[slot] + place, v ? tm_v : tm_k, 64 * half, head, 0, z, &sm.full[slot]);
+      for (; q_left > 0; q_left -= p.tile_tokens, q0 += p.tile_tokens, ++nq) {
+        if (w != 0) continue;
+        const int b = nq & 1;
+        if (nq >= 2) ok = __all_sync(kAll, wait_for(&sm.q_empty[b], ((nq >> 1) - 1) & 1, p.pv.err, &sm.abort));
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sm.q_full[b], p.q_tile_bytes);
+          tc::tma_load_3d(sm.q[b], tm_q, 0, head * p.group, q0, &sm.q_full[b]);
+          tc::tma_load_3d(sm.q[b] + kHalfBytes, tm_q, 64, head * p.group, q0, &sm.q_full[b]);
+        }
+        __syncwarp();
+      }
+      if (!ok) {
+        ++n;
+        break;
+      }
     }
   }
   // no copy is left landing in this CTA's shared memory
   if (w == 0)
-    for (int k = max(0, nu - 2); k < nu; ++k) mbar_wait_bounded(&sm.q_full[k & 1], (k >> 1) & 1);
+    for (int k = max(0, nq - 2); k < nq; ++k) mbar_wait_bounded(&sm.q_full[k & 1], (k >> 1) & 1);
   for (int k = max(0, n - S::kRing); k < n; ++k) mbar_wait_bounded(&sm.full[k % S::kRing], (k / S::kRing) & 1);
 }
 
@@ -245,168 +301,257 @@ __device__ __forceinline__ uint32_t f2_to_f16x2(float lo, float hi) {
   return r;
 }
 
-// e4m3: widening warp `w` of four takes 32 rows of every tile: eight lanes read one row of codes and write it as f16 in the
-// products' layout (16-byte chunk c of a 64-dim half's row r at c ^ (r % 8)).  The lanes of the second half write
-// their odd chunk first, so that a row's eight lanes fill different banks.  Rows behind the last key become zeros: a page's
-// unused slots may hold NaN, which a weight of zero would not cancel.  Each piece's Q tile turns from bf16 to f16 in
-// place (exact within f16's normal range).
-__device__ void widen_tiles(const TreeParams& p, TreeSmem<true>& sm, Walk walk, int w) {
+// e4m3: widening warp `w` of four takes 32 rows of every V tile: eight lanes read one row of codes and write it as f16 in the
+// products' layout (16-byte chunk c of a 64-dim half's row r at c ^ (r % 8)).  The lanes of the second half write their odd
+// chunk first, so that a row's eight lanes fill different banks.  Rows behind the last key become zeros: a page's unused
+// slots may hold NaN, which a weight of zero would not cancel.
+__device__ void widen_tiles(const TreeParams& p, TreeSmem<true>& sm, int w) {
   using S = Shape<true>;
   const int lane = threadIdx.x & 31, chunk = lane & 7;
   const uint32_t half_off = uint32_t(chunk >> 2) * kHalfBytes;
   const bool swap = chunk >= 4;
   const int m = (2 * chunk) & 7;
+  const int r0 = 32 * w + (lane >> 3);
   Piece c;
-  int n = 0, nu = 0;
+  int tt = 0, nu = 0;
   bool ok = true;
-  while (ok && walk.next(c)) {
-    const int b = nu & 1;
-    ok = __all_sync(kAll, mbar_wait(&sm.q_full[b], (nu >> 1) & 1, p.pv.err, &sm.abort));
-    if (!ok) break;
-    const uint32_t q = smem_u32(sm.q[b]) + uint32_t(w * (kTileBytes / 4) + lane * 16);
-#pragma unroll 4
-    for (int i = 0; i < kTileBytes / 4 / 512; ++i) {
-      uint32_t x[4];
-      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(q + 512 * i) : "memory");
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = f2_to_f16x2(__uint_as_float(x[k] << 16), __uint_as_float(x[k] & 0xffff0000u));
-      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(q + 512 * i), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.q_ready[b]);
-    ++nu;
-    for (int t = c.k0; t < c.k1 && ok; ++t) {
+  for (; ok && take(p, sm, nu, c); ++nu) {
+    for (int t = c.k0; t < c.k1; ++t, ++tt) {
       const int lim = c.lkv - t * kKeys;
-      for (int v = 0; v < 2; ++v, ++n) {
-        const int from = n % S::kRaw, to = n % S::kTiles;
-        ok = __all_sync(kAll, mbar_wait(&sm.full[from], (n / S::kRaw) & 1, p.pv.err, &sm.abort) &&
-                                  (n < S::kTiles || mbar_wait(&sm.empty[to], (n / S::kTiles - 1) & 1, p.pv.err, &sm.abort)));
-        if (!ok) break;
-        const int r0 = 32 * w + (lane >> 3);
-        const uint32_t src = smem_u32(sm.raw[from]) + uint32_t(r0 * 128 + 16 * chunk);
-        const uint32_t dst = smem_u32(sm.kv[to]) + half_off + uint32_t(r0 * 128);
+      const int n = 2 * tt + 1, from = n % S::kRing, to = tt % S::kWide;
+      ok = __all_sync(kAll, wait_for(&sm.full[from], (n / S::kRing) & 1, p.pv.err, &sm.abort));
+      if (!ok) break;
+      const uint32_t src = smem_u32(sm.kv[from]) + uint32_t(r0 * 128), dst = smem_u32(sm.wide[to]) + half_off + uint32_t(r0 * 128);
 #pragma unroll
-        for (int i0 = 0; i0 < 8; i0 += 4) {
-          uint32_t x[4][4];
+      for (int i0 = 0; i0 < 8; i0 += 4) {
+        uint32_t x[4][4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(x[i][0]), "=r"(x[i][1]), "=r"(x[i][2]), "=r"(x[i][3])
-                         : "r"(src + 512 * (i0 + i))
-                         : "memory");
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = r0 + 4 * (i0 + i);
-            if (r >= lim) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0u;
-            const uint32_t a0 = e4m3x2_to_f16x2(swap ? x[i][2] : x[i][0]), a1 = e4m3x2_to_f16x2((swap ? x[i][2] : x[i][0]) >> 16);
-            const uint32_t a2 = e4m3x2_to_f16x2(swap ? x[i][3] : x[i][1]), a3 = e4m3x2_to_f16x2((swap ? x[i][3] : x[i][1]) >> 16);
-            const uint32_t b0 = e4m3x2_to_f16x2(swap ? x[i][0] : x[i][2]), b1 = e4m3x2_to_f16x2((swap ? x[i][0] : x[i][2]) >> 16);
-            const uint32_t b2 = e4m3x2_to_f16x2(swap ? x[i][1] : x[i][3]), b3 = e4m3x2_to_f16x2((swap ? x[i][1] : x[i][3]) >> 16);
-            const uint32_t row = dst + 512 * (i0 + i);
-            const int ca = (swap ? m + 1 : m) ^ (r & 7), cb = (swap ? m : m + 1) ^ (r & 7);
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(row + 16 * ca), "r"(a0), "r"(a1), "r"(a2), "r"(a3) : "memory");
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(row + 16 * cb), "r"(b0), "r"(b1), "r"(b2), "r"(b3) : "memory");
-          }
+        for (int i = 0; i < 4; ++i)
+          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(x[i][0]), "=r"(x[i][1]), "=r"(x[i][2]), "=r"(x[i][3])
+                       : "r"(src + uint32_t(512 * (i0 + i) + 16 * (chunk ^ ((r0 + 4 * (i0 + i)) & 7))))
+                       : "memory");
+        if (i0 == 0) {
+          if (tt >= S::kWide) ok = __all_sync(kAll, wait_for(&sm.wide_empty[to], (tt / S::kWide - 1) & 1, p.pv.err, &sm.abort));
+          if (!ok) break;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sm.ready[to]);
-          mbar_arrive(&sm.raw_empty[from]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = r0 + 4 * (i0 + i);
+          const bool on = r < lim;
+          const uint32_t lo[2] = {on ? x[i][0] : 0u, on ? x[i][1] : 0u}, hi[2] = {on ? x[i][2] : 0u, on ? x[i][3] : 0u};
+          const uint32_t a[2] = {swap ? hi[0] : lo[0], swap ? hi[1] : lo[1]}, b[2] = {swap ? lo[0] : hi[0], swap ? lo[1] : hi[1]};
+          const uint32_t row = dst + 512 * (i0 + i);
+          const int ca = (swap ? m + 1 : m) ^ (r & 7), cb = (swap ? m : m + 1) ^ (r & 7);
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(row + 16 * ca), "r"(e4m3x2_to_f16x2(a[0])),
+                       "r"(e4m3x2_to_f16x2(a[0] >> 16)), "r"(e4m3x2_to_f16x2(a[1])), "r"(e4m3x2_to_f16x2(a[1] >> 16))
+                       : "memory");
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(row + 16 * cb), "r"(e4m3x2_to_f16x2(b[0])),
+                       "r"(e4m3x2_to_f16x2(b[0] >> 16)), "r"(e4m3x2_to_f16x2(b[1])), "r"(e4m3x2_to_f16x2(b[1] >> 16))
+                       : "memory");
         }
+      }
+      if (!ok) break;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sm.wide_full[to]);
+        mbar_arrive(&sm.empty[from]);
       }
     }
   }
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_of(float lo, float hi) {
+  uint16_t v;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(hi), "f"(lo));
+  return v;
+}
+
+// e4m3: Q tile number n from bf16 into its two terms, in place: warp `w` of four takes 32 rows, eight lanes a row, 16 of its
+// bytes from each dim half.  A row's bytes are read by the lanes that write them, four rows a step.
+__device__ bool split_q(const TreeParams& p, TreeSmem<true>& sm, int n, int w) {
+  const int lane = threadIdx.x & 31, c = lane & 7, b = n & 1;
+  if (!__all_sync(kAll, wait_for(&sm.q_full[b], (n >> 1) & 1, p.pv.err, &sm.abort))) return false;
+  const uint32_t q = smem_u32(sm.q[b]);
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    const int r = 32 * w + 4 * i + (lane >> 3), sw = r & 7;
+    const uint32_t row = q + uint32_t(r * 128);
+    uint32_t x[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(x[4 * h]), "=r"(x[4 * h + 1]), "=r"(x[4 * h + 2]), "=r"(x[4 * h + 3])
+                   : "r"(row + uint32_t(h * kHalfBytes + 16 * (c ^ sw)))
+                   : "memory");
+    uint32_t top = 0;  // the largest |element|'s bits
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = max(top, max(x[k] & 0x7fffu, x[k] >> 16 & 0x7fffu));
+#pragma unroll
+    for (int m = 1; m < 8; m <<= 1) top = max(top, __shfl_xor_sync(kAll, top, m));
+    const int e = int(top >> 7);  // its exponent field; the factor 2^(134 - e) brings it to 128 .. 256
+    const int up = top == 0 ? 0 : min(134 - e, 126);
+    const float f = __uint_as_float(uint32_t(up + 127) << 23);
+    uint32_t t0[4], t1[4];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float2 v = __fmul2_rn(bf16x2_to_f2(x[k]), make_float2(f, f));
+      const uint32_t a = e4m3x2_of(v.x, v.y);
+      const uint32_t back = e4m3x2_to_f16x2(a);
+      const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&back));
+      const uint32_t rest = e4m3x2_of(v.x - g.x, v.y - g.y);
+      t0[k >> 1] = k & 1 ? t0[k >> 1] | a << 16 : a;
+      t1[k >> 1] = k & 1 ? t1[k >> 1] | rest << 16 : rest;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // dims 64 h + 8 c .. : half of 16-byte chunk 4 h + c / 2
+      const uint32_t at = row + uint32_t(16 * ((4 * h + (c >> 1)) ^ sw) + 8 * (c & 1));
+      asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(t0[2 * h]), "r"(t0[2 * h + 1]) : "memory");
+      asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + kHalfBytes), "r"(t1[2 * h]), "r"(t1[2 * h + 1]) : "memory");
+    }
+    if (c == 0) sm.q_exp[b][r] = int8_t(e == 255 ? kQuiet : -up);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&sm.q_ready[b]);
+  return true;
 }
 
 // ---- products ----------------------------------------------------------------------------------------
-// One warp issues S, another O; an elected lane of a uniform warp (a branch on the lane number costs each product 50
-// clocks and more).
+// One warp issues S, another O, by an elected lane of a uniform warp.  With two row tiles the scores of the two groups are
+// products of their own (64 columns), and the groups fall out of step; with one they are one product of 128 columns (two of 64
+// read Q twice: 197 against 194 us for 64 requests of 16 tokens).
 
-template <bool kFp8>
-__device__ void issue_scores(const TreeParams& p, TreeSmem<kFp8>& sm, Walk walk, uint32_t tmem) {
-  using S = Shape<kFp8>;
-  constexpr uint32_t idesc = kFp8 ? tc::idesc_f16_f32(kRows, kKeys, 0, 0) : tc::idesc_bf16_f32(kRows, kKeys, 0, 0);
-  uint64_t* k_in = kFp8 ? sm.ready : sm.full;
-  uint64_t* q_in = kFp8 ? sm.q_ready : sm.q_full;
-  const bool leads = elect_one();
-  Piece c;
-  int tt = 0, nu = 0;
-  while (walk.next(c)) {
-    if (!__all_sync(kAll, mbar_wait(&q_in[nu & 1], (nu >> 1) & 1, p.pv.err, &sm.abort))) return;
-    const uint32_t q = smem_u32(sm.q[nu & 1]);
-    for (int t = c.k0; t < c.k1; ++t, ++tt) {
-      const int n = 2 * tt, slot = n % S::kTiles, b = tt & 1;
-      bool ok = mbar_wait(&k_in[slot], (n / S::kTiles) & 1, p.pv.err, &sm.abort);
-      if (tt >= 2)  // the buffer's last P has been read
-        ok = ok && mbar_wait(&sm.pv_done[0][b], ((tt >> 1) - 1) & 1, p.pv.err, &sm.abort) &&
-             mbar_wait(&sm.pv_done[1][b], ((tt >> 1) - 1) & 1, p.pv.err, &sm.abort);
-      if (!__all_sync(kAll, ok)) return;
-      tc::fence_after_sync();
-      if (leads) {
-        const uint32_t k = smem_u32(sm.kv[slot]);
+// D (TMEM) [+]= A (shared memory) B (shared memory), e4m3 operands.
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// S (kN columns) = Q K^T from the Q tile and the key rows at the given places.
+template <bool kFp8, int kN>
+__device__ __forceinline__ void score_products(uint32_t s, uint32_t q, uint32_t k) {
+  // (an e4m3 descriptor's type fields are zero, as f16's are)
+  constexpr uint32_t idesc = kFp8 ? tc::idesc_f16_f32(kRows, kN, 0, 0) : tc::idesc_bf16_f32(kRows, kN, 0, 0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t off = uint32_t(i >> 2) * kHalfBytes + uint32_t(i & 3) * 32;
-          tc::mma_ss(tmem + uint32_t(b * kKeys), tc::smem_desc(q + off, 16, 1024, tc::kLayoutSw128),
-                     tc::smem_desc(k + off, 16, 1024, tc::kLayoutSw128), idesc, i != 0 ? 1u : 0u);
-        }
-        tc::commit(&sm.s_full[b]);
-        tc::commit(&sm.empty[slot]);
-        if (t == c.k1 - 1) tc::commit(&sm.q_empty[nu & 1]);
-      }
-      __syncwarp();
-    }
-    ++nu;
+  for (int i = 0; i < 8; ++i) {
+    // 32 bytes of dims a product: 16 bf16 of either half, or 32 codes against either term
+    const uint32_t qi = q + uint32_t(i >> 2) * kHalfBytes + uint32_t(i & 3) * 32;
+    const uint32_t ki = k + (kFp8 ? 0u : uint32_t(i >> 2) * kHalfBytes) + uint32_t(i & 3) * 32;
+    const uint64_t a = tc::smem_desc(qi, 16, 1024, tc::kLayoutSw128), b = tc::smem_desc(ki, 16, 1024, tc::kLayoutSw128);
+    if constexpr (kFp8)
+      mma_e4m3(s, a, b, idesc, i != 0 ? 1u : 0u);
+    else
+      tc::mma_ss(s, a, b, idesc, i != 0 ? 1u : 0u);
   }
 }
 
 template <bool kFp8>
-__device__ void issue_outputs(const TreeParams& p, TreeSmem<kFp8>& sm, Walk walk, uint32_t tmem) {
+__device__ void issue_scores(const TreeParams& p, TreeSmem<kFp8>& sm, uint32_t tmem) {
+  using S = Shape<kFp8>;
+  uint64_t* q_in = kFp8 ? sm.q_ready : sm.q_full;
+  Piece c;
+  int tt = 0, ss = 0, nu = 0, nq = 0;  // tiles, steps, pieces, Q tiles
+  while (take(p, sm, nu, c)) {
+    ++nu;
+    const bool two = c.nq > p.tile_tokens;
+    bool ok = wait_for(&q_in[nq & 1], (nq >> 1) & 1, p.pv.err, &sm.abort);
+    if (two) ok = ok && wait_for(&q_in[(nq + 1) & 1], ((nq + 1) >> 1) & 1, p.pv.err, &sm.abort);
+    if (!__all_sync(kAll, ok)) return;
+    const uint32_t q0 = smem_u32(sm.q[nq & 1]), q1 = smem_u32(sm.q[(nq + 1) & 1]);
+    const int steps = steps_of(c, two);
+    for (int s = 0; s < steps; ++s, ++ss) {
+      const int n = 2 * tt, slot = n % S::kRing, b = ss & 1, sub = two ? s & 1 : 0;
+      if (sub == 0 && !__all_sync(kAll, wait_for(&sm.full[slot], (n / S::kRing) & 1, p.pv.err, &sm.abort))) return;
+      const uint32_t k = smem_u32(sm.kv[slot]) + uint32_t(sub * kHalfKeys * 128);
+      const bool done = !two || sub == 1 || s == steps - 1;  // with the tile
+      // a buffer's last P has been read
+      if (ss >= 2 && !__all_sync(kAll, wait_for(&sm.pv_done[0][b], ((ss >> 1) - 1) & 1, p.pv.err, &sm.abort))) return;
+      if (ss >= 2 && !two && !__all_sync(kAll, wait_for(&sm.pv_done[1][b], ((ss >> 1) - 1) & 1, p.pv.err, &sm.abort))) return;
+      tc::fence_after_sync();
+      if (elect_one()) {
+        if (two)
+          score_products<kFp8, kHalfKeys>(tmem + uint32_t(b * kKeys), q0, k);
+        else
+          score_products<kFp8, kKeys>(tmem + uint32_t(b * kKeys), q0, k);  // both groups' keys
+        tc::commit(&sm.s_full[0][b]);
+      }
+      __syncwarp();
+      if (two) {
+        if (ss >= 2 && !__all_sync(kAll, wait_for(&sm.pv_done[1][b], ((ss >> 1) - 1) & 1, p.pv.err, &sm.abort))) return;
+        tc::fence_after_sync();
+      }
+      if (elect_one()) {
+        if (two) score_products<kFp8, kHalfKeys>(tmem + uint32_t(b * kKeys + kHalfKeys), q1, k);
+        tc::commit(&sm.s_full[1][b]);
+        if (done) tc::commit(&sm.empty[slot]);
+        if (s == steps - 1) {
+          tc::commit(&sm.q_empty[nq & 1]);
+          if (two) tc::commit(&sm.q_empty[(nq + 1) & 1]);
+        }
+      }
+      __syncwarp();
+      if (done) ++tt;
+    }
+    nq += two ? 2 : 1;
+  }
+}
+
+template <bool kFp8>
+__device__ void issue_outputs(const TreeParams& p, TreeSmem<kFp8>& sm, uint32_t tmem) {
   using S = Shape<kFp8>;
   constexpr uint32_t idesc = kFp8 ? tc::idesc_f16_f32(kRows, kHeadDim, 0, 1) : tc::idesc_bf16_f32(kRows, kHeadDim, 0, 1);
-  uint64_t* v_in = kFp8 ? sm.ready : sm.full;
-  const bool leads = elect_one();
   const int lane = threadIdx.x & 31;
   Piece c;
-  int tt = 0, nu = 0;
-  while (walk.next(c)) {
-    for (int t = c.k0; t < c.k1; ++t, ++tt) {
-      const int n = 2 * tt + 1, slot = n % S::kTiles, b = tt & 1;
-      if (!__all_sync(kAll, mbar_wait(&v_in[slot], (n / S::kTiles) & 1, p.pv.err, &sm.abort))) return;
-      const int lim = c.lkv - t * kKeys;
-      if (!kFp8 && lim < kKeys) {
-        // the box of the last page brought the slots behind the last key, which may hold NaN: a weight of zero would not
-        // cancel it (the rows behind that page came in as zeros)
-        const int stop = min(kKeys, (max(lim, 0) + p.pv.page_size - 1) / p.pv.page_size * p.pv.page_size);
-        for (int i = max(lim, 0) * 16 + lane; i < stop * 16; i += 32)
-          *reinterpret_cast<uint4*>(sm.kv[slot] + ((i >> 3) & 1) * kHalfBytes + (i >> 4) * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();
-        __syncwarp();
+  int tt = 0, ss = 0, nu = 0;
+  for (; take(p, sm, nu, c); ++nu) {
+    const bool two = c.nq > p.tile_tokens;
+    const int steps = steps_of(c, two);
+    for (int s = 0; s < steps; ++s, ++ss) {
+      const int n = 2 * tt + 1, slot = kFp8 ? tt % 2 : n % S::kRing, b = ss & 1, sub = two ? s & 1 : 0;
+      uint8_t* tile = kFp8 ? sm.wide[kFp8 ? slot : 0] : sm.kv[slot];
+      if (sub == 0) {
+        if (!__all_sync(kAll, kFp8 ? wait_for(&sm.wide_full[slot & 1], (tt >> 1) & 1, p.pv.err, &sm.abort)
+                                   : wait_for(&sm.full[slot], (n / S::kRing) & 1, p.pv.err, &sm.abort)))
+          return;
+        const int lim = c.lkv - (c.k0 + (two ? s >> 1 : s)) * kKeys;
+        if (!kFp8 && lim < kKeys) {
+          // the box of the last page brought the slots behind the last key, which may hold NaN: a weight of zero would not
+          // cancel it (the rows behind that page came in as zeros)
+          const int stop = min(kKeys, (max(lim, 0) + p.pv.page_size - 1) / p.pv.page_size * p.pv.page_size);
+          for (int i = max(lim, 0) * 16 + lane; i < stop * 16; i += 32)
+            *reinterpret_cast<uint4*>(tile + ((i >> 3) & 1) * kHalfBytes + (i >> 4) * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
       }
-      const uint32_t v = smem_u32(sm.kv[slot]);
+      const bool done = !two || sub == 1 || s == steps - 1;  // with the tile
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        bool ok = mbar_wait(&sm.p_full[h][b], (tt >> 1) & 1, p.pv.err, &sm.abort);
+        bool ok = wait_for(&sm.p_full[h][b], (ss >> 1) & 1, p.pv.err, &sm.abort);
         // the piece's first product overwrites O once the last piece's has been read out
-        if (t == c.k0 && h == 0 && nu > 0) ok = ok && mbar_wait(&sm.o_free, (nu - 1) & 1, p.pv.err, &sm.abort);
+        if (s == 0 && h == 0 && nu > 0) ok = ok && wait_for(&sm.o_free, (nu - 1) & 1, p.pv.err, &sm.abort);
         if (!__all_sync(kAll, ok)) return;
         tc::fence_after_sync();
-        if (leads) {
+        if (elect_one()) {
+          const uint32_t v = smem_u32(tile) + uint32_t((two ? sub : h) * kHalfKeys * 128);
 #pragma unroll
           for (int i = 0; i < kHalfKeys / 16; ++i)
             // V as B (keys x dims), MN-major: 16 keys are two 8-row groups, the second 64 dims the leading step
             tc::mma_ts(tmem + kColO + uint32_t(h * kHeadDim), tmem + uint32_t(b * kKeys + h * kHalfKeys + i * 8),
-                       tc::smem_desc(v + uint32_t(h * kHalfKeys * 128 + i * 2048), kHalfBytes, 1024, tc::kLayoutSw128), idesc,
-                       (t != c.k0 || i != 0) ? 1u : 0u);
+                       tc::smem_desc(v + uint32_t(i * 2048), kHalfBytes, 1024, tc::kLayoutSw128), idesc, (s != 0 || i != 0) ? 1u : 0u);
           tc::commit(&sm.pv_done[h][b]);
-          if (h == 1) tc::commit(&sm.empty[slot]);
+          if (h == 1 && done) tc::commit(kFp8 ? &sm.wide_empty[slot & 1] : &sm.empty[slot]);
         }
         __syncwarp();
       }
+      if (done) ++tt;
     }
-    ++nu;
   }
 }
 
@@ -428,15 +573,14 @@ __device__ __forceinline__ uint64_t seen_keys(const uint32_t* mask, int words, i
 }
 
 template <bool kMasked, int kCap, bool kF16>
-__device__ __forceinline__ void softmax_half(const TreeParams& p, uint32_t t_s, uint32_t t_o, uint64_t seen, float& m, float& l,
+__device__ __forceinline__ void softmax_half(const TreeParams& p, float scale, uint32_t t_s, uint32_t t_o, uint64_t seen, float& m, float& l,
                                              bool first, uint64_t* pv_done, int pv_parity, int32_t* err, int* abort, bool& alive) {
   uint32_t s[kHalfKeys];
   tc::tmem_ld32(t_s, *reinterpret_cast<uint32_t(*)[32]>(s));
   tc::tmem_ld32(t_s + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
   tc::tmem_wait_ld();
-  float scale = p.scale_log2;
   if (kCap) {
-    const float in = p.scale_log2 * p.inv_cap_log2;
+    const float in = scale * p.inv_cap_log2;
 #pragma unroll
     for (int j = 0; j < kHalfKeys; ++j) {
       const float y = __uint_as_float(s[j]) * in;
@@ -485,9 +629,9 @@ __device__ __forceinline__ void softmax_half(const TreeParams& p, uint32_t t_s, 
   tc::tmem_st32(t_s, *reinterpret_cast<uint32_t(*)[32]>(s));
   tc::tmem_wait_st();
   if (__any_sync(kAll, need)) {
-    alive = alive && __all_sync(kAll, mbar_wait(pv_done, pv_parity, err, abort));
+    alive = alive && __all_sync(kAll, wait_for(pv_done, pv_parity, err, abort));
     tc::fence_after_sync();
-#pragma unroll
+#pragma unroll 1
     for (int k = 0; k < 4; ++k) {
       uint32_t o[32];
       tc::tmem_ld32(t_o + 32 * k, o);
@@ -501,44 +645,54 @@ __device__ __forceinline__ void softmax_half(const TreeParams& p, uint32_t t_s, 
 }
 
 template <bool kFp8, int kCap>
-__device__ void softmax_keys(const TreeParams& p, TreeSmem<kFp8>& sm, Walk walk, uint32_t tmem, int h) {
+__device__ void softmax_keys(const TreeParams& p, TreeSmem<kFp8>& sm, uint32_t tmem, int h) {
   const int row = threadIdx.x & (kRows - 1), lane = threadIdx.x & 31;
   const uint32_t mine = tmem + (uint32_t(row & ~31) << 16);
   const uint32_t t_o = mine + kColO + uint32_t(h * kHeadDim);
-  const int token = row / p.group;
+  const int row_token = row / p.group;
   Piece c;
-  int tt = 0, nu = 0;
+  int ss = 0, nu = 0, nq = 0;
   bool alive = true;
-  while (walk.next(c)) {
-    const bool busy = (row & ~31) < c.nq * p.group;  // the warp has rows of the piece
-    const uint32_t* mask = p.mask + (long long)(c.q0 + min(token, c.nq - 1)) * p.mask_words;
-    const int off = c.lkv - c.lq;
-    float m = -INFINITY, l = 0.f;
-    for (int t = c.k0; t < c.k1; ++t, ++tt) {
-      const int b = tt & 1;
-      const int base = t * kKeys + h * kHalfKeys;
-      const uint64_t seen = busy ? seen_keys(mask, p.mask_words, base, off, c.lq) : 0;
-      alive = alive && __all_sync(kAll, mbar_wait(&sm.s_full[b], (tt >> 1) & 1, p.pv.err, &sm.abort));
+  for (; take(p, sm, nu, c); ++nu) {
+    const bool two = c.nq > p.tile_tokens;
+    const int first = two && h == 1 ? p.tile_tokens : 0;              // this group's tokens of the piece
+    const int tokens = min(p.tile_tokens, c.nq - first);
+    const bool busy = (row & ~31) < tokens * p.group;  // the warp has rows of the piece
+    const uint32_t* mask = p.mask + (long long)(c.q0 + first + min(row_token, tokens - 1)) * p.mask_words;
+    const int off = c.lkv - c.lq, steps = steps_of(c, two);
+    const int base0 = c.k0 * kKeys + (two ? 0 : h * kHalfKeys), base_step = two ? kHalfKeys : kKeys;
+    float m = -INFINITY, l = 0.f, scale = p.scale_log2;
+    for (int s = 0; s < steps; ++s, ++ss) {
+      const int b = ss & 1;
+      const uint64_t seen = busy ? seen_keys(mask, p.mask_words, base0 + s * base_step, off, c.lq) : 0;
+      alive = alive && __all_sync(kAll, wait_for(&sm.s_full[h][b], (ss >> 1) & 1, p.pv.err, &sm.abort));
+      if (kFp8 && s == 0) {  // the row's scale, once the products have seen the tile; then the Q tiles may go
+        const int e = sm.q_exp[(nq + (two ? h : 0)) & 1][row];
+        scale = e == kQuiet ? __uint_as_float(0x7fc00000u) : scale * __uint_as_float(uint32_t(e + 127) << 23);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_empty[nq & 1]);
+        if (lane == 0 && two) mbar_arrive(&sm.q_empty[(nq + 1) & 1]);
+        nq += two ? 2 : 1;
+      }
       if (alive && busy) {
         tc::fence_after_sync();
         const uint32_t t_s = mine + uint32_t(b * kKeys + h * kHalfKeys);
         uint64_t* before = &sm.pv_done[h][b ^ 1];  // the product that wrote O last
-        const int parity = ((tt - 1) >> 1) & 1;
+        const int parity = ((ss - 1) >> 1) & 1;
         if (__all_sync(kAll, seen == ~0ull))
-          softmax_half<false, kCap, kFp8>(p, t_s, t_o, seen, m, l, t == c.k0, before, parity, p.pv.err, &sm.abort, alive);
+          softmax_half<false, kCap, kFp8>(p, scale, t_s, t_o, seen, m, l, s == 0, before, parity, p.pv.err, &sm.abort, alive);
         else
-          softmax_half<true, kCap, kFp8>(p, t_s, t_o, seen, m, l, t == c.k0, before, parity, p.pv.err, &sm.abort, alive);
+          softmax_half<true, kCap, kFp8>(p, scale, t_s, t_o, seen, m, l, s == 0, before, parity, p.pv.err, &sm.abort, alive);
         tc::fence_before_sync();
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.p_full[h][b]);
     }
-    if (nu >= 1) alive = alive && __all_sync(kAll, mbar_wait(&sm.stat_empty, (nu - 1) & 1, p.pv.err, &sm.abort));
+    if (nu >= 1) alive = alive && __all_sync(kAll, wait_for(&sm.stat_empty, (nu - 1) & 1, p.pv.err, &sm.abort));
     sm.stat_m[h][row] = m;
     sm.stat_l[h][row] = l;
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.stat_full);
-    ++nu;
   }
 }
 
@@ -548,77 +702,115 @@ __device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
                : "r"(at));
 }
 
-// The two halves of a finished piece, joined: to the output, or as a state to the piece's slot.
+// 16 dims of a row: to the output in bf16, or to a partial slot.  32 bytes a store: a lane writes whole sectors of its row.
+__device__ __forceinline__ void put32(void* to, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+               "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+__device__ __forceinline__ void put16(const TreeParams& p, bool whole, long long row, int dim, const float (&v)[16]) {
+  uint32_t w[8];
+  if (whole) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = f2_to_bf16x2(v[2 * j], v[2 * j + 1]);
+    put32(p.o + row * kHeadDim + dim, w);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * h + j]);
+      put32(p.part_o + row * kHeadDim + dim + 8 * h, w);
+    }
+  }
+}
+
+// A finished piece, to the output or as a state to its slot: with one row tile the two groups' states of the same rows
+// joined, with two each group's own.
 template <bool kFp8>
-__device__ void join_halves(const TreeParams& p, TreeSmem<kFp8>& sm, Walk walk, uint32_t tmem) {
+__device__ void write_pieces(const TreeParams& p, TreeSmem<kFp8>& sm, uint32_t tmem) {
   const int row = threadIdx.x & (kRows - 1), lane = threadIdx.x & 31;
   const uint32_t mine = tmem + (uint32_t(row & ~31) << 16) + kColO;
-  Piece c;
-  int tt = 0, nu = 0;
-  bool alive = true;
-  while (walk.next(c)) {
-    alive = alive && __all_sync(kAll, mbar_wait(&sm.stat_full, nu & 1, p.pv.err, &sm.abort));
-    const float m0 = sm.stat_m[0][row], m1 = sm.stat_m[1][row], l0 = sm.stat_l[0][row], l1 = sm.stat_l[1][row];
+  Piece c, ahead;
+  int ss = 0, nu = 0, nq = 0;
+  bool alive = true, more = take(p, sm, 0, ahead);
+  auto split = [&]() {  // the Q tiles of the piece ahead, while the one at hand is worked on
+    if constexpr (kFp8) {
+      for (int left = ahead.nq; left > 0 && alive; left -= p.tile_tokens, ++nq) alive = split_q(p, sm, nq, (threadIdx.x >> 5) & 3);
+    }
+  };
+  if (more) split();
+  for (; more; ++nu) {
+    c = ahead;
+    more = take(p, sm, nu + 1, ahead);
+    if (more) split();
+    const bool two = c.nq > p.tile_tokens;
+    alive = alive && __all_sync(kAll, wait_for(&sm.stat_full, nu & 1, p.pv.err, &sm.abort));
+    float m[2] = {sm.stat_m[0][row], sm.stat_m[1][row]}, l[2] = {sm.stat_l[0][row], sm.stat_l[1][row]};
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.stat_empty);
-    tt += c.k1 - c.k0;
-    const int last = tt - 1;
+    ss += steps_of(c, two);
+    const int last = ss - 1;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      alive = alive && __all_sync(kAll, mbar_wait(&sm.pv_done[h][last & 1], (last >> 1) & 1, p.pv.err, &sm.abort));
+      alive = alive && __all_sync(kAll, wait_for(&sm.pv_done[h][last & 1], (last >> 1) & 1, p.pv.err, &sm.abort));
     tc::fence_after_sync();
-    const float m = fmaxf(m0, m1);
-    float w0 = 0.f, w1 = 0.f, lse2 = -INFINITY;
-    if (m != -INFINITY) {
-      w0 = fast_exp2(m0 - m);
-      w1 = fast_exp2(m1 - m);
-      const float l = w0 * l0 + w1 * l1;
-      lse2 = m + fast_log2(l);
-      const float inv = p.v_scale / l;
-      w0 *= inv;
-      w1 *= inv;
-    }
-    const int rows = c.nq * p.group;
-    const bool write = row < rows;
-    const long long orow = (long long)(c.q0 + row / p.group) * p.hqo + c.head * p.group + row % p.group;
-    const long long srow = (long long)c.slot * kRows + row;
-    if ((row & ~31) < rows) {
+    const bool whole = c.slot < 0;
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      const int first = h * p.tile_tokens, rows = min(p.tile_tokens, c.nq - first) * p.group;  // of this pass
+      if ((row & ~31) >= rows) break;
+      // the states' weights: o = w0 O_0 + w1 O_1
+      float w0, w1, lse2 = -INFINITY;
+      const float m0 = two && h == 1 ? -INFINITY : m[0], m1 = two && h == 0 ? -INFINITY : m[1];
+      const float top = fmaxf(m0, m1);
+      w0 = w1 = 0.f;
+      const float l0 = two && h == 1 ? 0.f : l[0], l1 = two && h == 0 ? 0.f : l[1];
+      if (top != -INFINITY || l0 != l0 || l1 != l1) {  // (a row of NaN has no maximum and a sum of NaN)
+        w0 = m0 == top ? 1.f : fast_exp2(m0 - top);
+        w1 = m1 == top ? 1.f : fast_exp2(m1 - top);
+        const float sum = w0 * l0 + w1 * l1;
+        lse2 = top + fast_log2(sum);
+        const float inv = p.v_scale / sum;
+        w0 *= inv;
+        w1 *= inv;
+      }
+      const bool write = row < rows;
+      const long long at = whole ? (long long)(c.q0 + first + row / p.group) * p.hqo + c.head * p.group + row % p.group
+                                 : ((long long)c.slot * 2 + h) * kRows + row;
 #pragma unroll 1
       for (int k = 0; k < kHeadDim; k += 16) {
-        uint32_t a[16], b[16];
-        tmem_ld16(mine + k, a);
-        tmem_ld16(mine + kHeadDim + k, b);
-        tc::tmem_wait_ld();
         float v[16];
+        uint32_t a[16];
+        if (two) {
+          tmem_ld16(mine + h * kHeadDim + k, a);
+          tc::tmem_wait_ld();
+          const float w = h ? w1 : w0;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {  // a half without a seen key has nothing to add, not even 0 x NaN
-          const float x = w0 != 0.f ? __uint_as_float(a[j]) * w0 : 0.f;
-          v[j] = w1 != 0.f ? fmaf(__uint_as_float(b[j]), w1, x) : x;
-        }
-        if (!write) continue;
-        if (c.slot < 0) {
-          uint4* to = reinterpret_cast<uint4*>(p.o + orow * kHeadDim + k);
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            to[j] = make_uint4(f2_to_bf16x2(v[8 * j], v[8 * j + 1]), f2_to_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                               f2_to_bf16x2(v[8 * j + 4], v[8 * j + 5]), f2_to_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+          for (int j = 0; j < 16; ++j) v[j] = w != 0.f ? __uint_as_float(a[j]) * w : 0.f;
         } else {
-          float4* to = reinterpret_cast<float4*>(p.part_o + srow * kHeadDim + k);
+          uint32_t b[16];
+          tmem_ld16(mine + k, a);
+          tmem_ld16(mine + kHeadDim + k, b);
+          tc::tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 4; ++j) to[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          for (int j = 0; j < 16; ++j) {  // a group without a seen key has nothing to add, not even 0 x NaN
+            const float x = w0 != 0.f ? __uint_as_float(a[j]) * w0 : 0.f;
+            v[j] = w1 != 0.f ? fmaf(__uint_as_float(b[j]), w1, x) : x;
+          }
         }
+        if (write) put16(p, whole, at, k, v);
       }
+      if (write) {
+        if (whole)
+          p.lse[at] = lse2 * kLn2;
+        else
+          p.part_lse[at] = lse2;
+      }
+      if (!two) break;
     }
     tc::fence_before_sync();
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.o_free);
-    if (write) {
-      if (c.slot < 0)
-        p.lse[orow] = lse2 * kLn2;
-      else
-        p.part_lse[srow] = lse2;
-    }
-    ++nu;
   }
 }
 
@@ -635,19 +827,23 @@ __global__ void __launch_bounds__(Shape<kFp8>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sm.q_full[b], 1);
-      mbar_init(&sm.q_empty[b], 1);
+      mbar_init(&sm.q_empty[b], kFp8 ? 1 + 8 : 1);  // the products; e4m3: and the softmax warps
       mbar_init(&sm.q_ready[b], 4);
-      mbar_init(&sm.s_full[b], 1);
+      mbar_init(&sm.wide_full[b], 4);
+      mbar_init(&sm.wide_empty[b], 1);
       for (int h = 0; h < 2; ++h) {
+        mbar_init(&sm.s_full[h][b], 1);
         mbar_init(&sm.p_full[h][b], 4);
         mbar_init(&sm.pv_done[h][b], 1);
       }
     }
-    for (int i = 0; i < S::kRing; ++i) mbar_init(&sm.full[i], kLoaders);
-    for (int i = 0; i < S::kRaw; ++i) mbar_init(&sm.raw_empty[i], 4);
-    for (int i = 0; i < S::kTiles; ++i) {
-      mbar_init(&sm.ready[i], 4);
-      mbar_init(&sm.empty[i], 1);
+    for (int i = 0; i < S::kRing; ++i) {
+      mbar_init(&sm.full[i], kLoaders);
+      mbar_init(&sm.empty[i], kFp8 && i % 2 == 1 ? 4 : 1);  // e4m3: V's codes are read by the widening warps
+    }
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(&sm.piece_full[i], 1);
+      mbar_init(&sm.piece_empty[i], S::kReaders);
     }
     mbar_init(&sm.stat_full, 8);
     mbar_init(&sm.stat_empty, 4);
@@ -670,30 +866,31 @@ __global__ void __launch_bounds__(Shape<kFp8>::kThreads, 1)
   wait_prior_grid();
   const uint32_t tmem = sm.tmem_base;
   const GeoHead plan = load_head(p.pv.geo);
+  const int start = __ldg(p.starts + blockIdx.x);
   const Line line(plan.tree, int(gridDim.x));
   if ((tmem & 0xFFFFu) + kTmemCols > 512u || (smem_u32(smem_raw) & 1023u) != 0) {
     if (threadIdx.x == 0) atomicOr(p.pv.err, FI_DEVERR_TMEM);
   } else if (int(blockIdx.x) < line.ctas) {
-    Walk walk;
-    walk.init(p, plan, line, int(blockIdx.x));
     if (warp < 8) {
       tc::regs_increase<S::kSoftmaxRegs>();
-      softmax_keys<kFp8, kCap>(p, sm, walk, tmem, warp >> 2);
+      softmax_keys<kFp8, kCap>(p, sm, tmem, warp >> 2);
     } else if (warp < 12) {
-      if constexpr (S::kJoinRegs < S::kLaunchRegs) tc::regs_decrease<S::kJoinRegs>();
-      join_halves<kFp8>(p, sm, walk, tmem);
+      if constexpr (S::kWriteRegs < S::kLaunchRegs) tc::regs_decrease<S::kWriteRegs>();
+      write_pieces<kFp8>(p, sm, tmem);
     } else if (warp < 16) {
       tc::regs_decrease<S::kLoadRegs>();
-      load_tiles<kFp8>(p, sm, walk, &tm_q, &tm_k, &tm_v, warp - 12);
+      load_tiles<kFp8>(p, sm, &tm_q, &tm_k, &tm_v, warp - 12);
     } else if (warp < 20) {
       tc::regs_decrease<S::kIssueRegs>();
       if (warp == 16)
-        issue_scores<kFp8>(p, sm, walk, tmem);
+        issue_scores<kFp8>(p, sm, tmem);
       else if (warp == 17)
-        issue_outputs<kFp8>(p, sm, walk, tmem);
+        issue_outputs<kFp8>(p, sm, tmem);
+      else if (warp == 18)
+        find_pieces<kFp8>(p, sm, plan, line, int(blockIdx.x), start);
     } else if constexpr (kFp8) {
       tc::regs_decrease<S::kWidenRegs>();
-      widen_tiles(p, sm, walk, warp - 20);
+      widen_tiles(p, sm, warp - 20);
     }
   }
   tc::fence_before_sync();
@@ -705,65 +902,89 @@ __global__ void __launch_bounds__(Shape<kFp8>::kThreads, 1)
 }
 
 // ---- units that were cut -------------------------------------------------------------------------------
-// kJoinCtas CTAs for each place where the line was cut: if it is the first cut of a unit, they join the unit's states in
-// the pieces' order, a warp a row, four dims a lane.  What a row has to read, n states of 516 bytes, lies in L2.
+// kJoinCtas CTAs for each place where the line was cut; those of one unit's cuts share its rows and join their states in
+// the pieces' order.  What a row has to read, n states of 516 bytes, lies in L2, and most units have two or three pieces, so
+// latency counts: a warp takes up to four rows at a time, eight lanes a row for the states' sums, then all lanes, four dims
+// each, for two rows' states side by side.  (A row a warp: 30 us behind 160 us of 256-row units.)
 constexpr int kJoinThreads = 256;
-constexpr int kJoinCtas = 4;
-constexpr int kJoinAhead = 8;
+constexpr int kJoinCtas = 8;
+constexpr int kJoinRows = 4;
+constexpr int kJoinAhead = 4;
 
-__global__ void __launch_bounds__(kJoinThreads) tree_join_kernel(const __grid_constant__ TreeParams p, int grid) {
-  wait_prior_grid();
+__global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid_constant__ TreeParams p, int grid) {
+  // (the plan was there before the kernel whose states are waited for below)
   const GeoHead plan = load_head(p.pv.geo);
   const Line line(plan.tree, grid);
   const int cut = int(blockIdx.x) / kJoinCtas + 1, part = int(blockIdx.x) % kJoinCtas;
   if (cut >= line.ctas) return;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = int(threadIdx.x >> 5);
   const int x = cut * line.per;
-  Geo g = load_geo(p.pv.geo, find_request(p.pv.geo, plan.batch, &Geo::tree0, x));
-  const int tiles = max(1, (g.lkv + kKeys - 1) / kKeys), row_tiles = (g.lq + p.tile_tokens - 1) / p.tile_tokens;
+  const Geo g = load_geo(p.pv.geo, __ldg(p.starts + cut));
+  const int tokens = 2 * p.tile_tokens;
+  const int tiles = max(1, (g.lkv + kKeys - 1) / kKeys), sets = (g.lq + tokens - 1) / tokens;
   const int unit = (x - g.tree0) / tiles, a = g.tree0 + unit * tiles;
-  if (a == x || a / line.per != cut - 1) return;  // nothing is cut here, or it was cut before
-  const int n = (a + tiles - 1) / line.per - (cut - 1) + 1;
-  const long long first = 2ll * (cut - 1);
-  const int tile = unit % row_tiles, head = unit / row_tiles;
-  const int q0 = g.q0 + tile * p.tile_tokens, rows = min(p.tile_tokens, g.lq - tile * p.tile_tokens) * p.group;
-  for (int row = part * (kJoinThreads / 32) + (threadIdx.x >> 5); row < rows; row += kJoinCtas * (kJoinThreads / 32)) {
-    const float* lses = p.part_lse + first * kRows + row;
-    float m = -INFINITY;
-    for (int k = lane; k < n; k += 32) m = fmaxf(m, __ldcg(lses + (long long)k * kRows));
+  if (a == x) return;  // nothing is cut here
+  const int begins = a / line.per, n = (a + tiles - 1) / line.per - begins + 1;  // the CTA with the unit's first piece, pieces
+  const long long first = 2ll * begins;
+  const int head = unit / sets, q0 = g.q0 + unit % sets * tokens, nq = min(tokens, g.lq - unit % sets * tokens);
+  // row k of the unit lies at 128 h + x of a slot, for row x of its row tile h
+  const int tile_rows = p.tile_tokens * p.group, rows = nq * p.group;
+  auto place = [&](int k) { return first * 2 * kRows + (k < tile_rows ? k : kRows + k - tile_rows); };
+  const int warps = (n - 1) * kJoinCtas * (kJoinThreads / 32);
+  const int some = min(kJoinRows, (rows + warps - 1) / warps);  // rows at a time
+  wait_prior_grid();
+  for (int k0 = (((cut - 1 - begins) * kJoinCtas + part) * (kJoinThreads / 32) + warp) * some; k0 < rows; k0 += warps * some) {
+    // eight lanes a row: the largest of its states' LSEs and the sum of their weights
+    const int mine = min(k0 + min(lane >> 3, some - 1), rows - 1);
+    const float* lses = p.part_lse + place(mine);
+    float m = -INFINITY, sum = 0.f;
+    for (int i = lane & 7; i < n; i += 8) m = fmaxf(m, __ldcg(lses + (long long)i * 2 * kRows));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-    const float m_use = m == -INFINITY ? 0.f : m;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-    const float4* src = reinterpret_cast<const float4*>(p.part_o + (first * kRows + row) * kHeadDim) + lane;
-    for (int k0 = 0; k0 < n; k0 += 32) {
-      const float w = k0 + lane < n ? fast_exp2(__ldcg(lses + (long long)(k0 + lane) * kRows) - m_use) : 0.f;
-      sum += w;
-      const int some = min(32, n - k0);
-      for (int j = 0; j < some; j += kJoinAhead) {
-        float4 v[kJoinAhead];
+    for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+    m = m == -INFINITY ? 0.f : m;
+    for (int i = lane & 7; i < n; i += 8) sum += fast_exp2(__ldcg(lses + (long long)i * 2 * kRows) - m);
 #pragma unroll
-        for (int k = 0; k < kJoinAhead; ++k)
-          v[k] = j + k < some ? __ldcg(src + (long long)(k0 + j + k) * (kRows * kHeadDim / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (no state of the row has seen a key)
+    if ((lane & 7) == 0 && (lane >> 3) < some && k0 + (lane >> 3) < rows)
+      p.lse[(long long)(q0 + mine / p.group) * p.hqo + head * p.group + mine % p.group] = sum == 0.f ? -INFINITY : (m + fast_log2(sum)) * kLn2;
+#pragma unroll 1
+    for (int r0 = 0; r0 < some && k0 + r0 < rows; r0 += 2) {
+      float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+      const long long at[2] = {place(k0 + r0), place(min(k0 + r0 + 1, rows - 1))};
+      for (int i0 = 0; i0 < n; i0 += 8) {
+        // lane (row, i & 7) holds the weight of state i0 + (i & 7) of its row
+        const int i = i0 + (lane & 7);
+        const float w = i < n ? fast_exp2(__ldcg(lses + (long long)i * 2 * kRows) - m) * inv : 0.f;
+        for (int j = 0; j < 8 && i0 + j < n; j += kJoinAhead) {
+          float4 v[2][kJoinAhead];
 #pragma unroll
-        for (int k = 0; k < kJoinAhead; ++k) {
-          const float wk = __shfl_sync(kAll, w, (j + k) & 31);
-          if (wk == 0.f) continue;
-          acc.x = fmaf(wk, v[k].x, acc.x);
-          acc.y = fmaf(wk, v[k].y, acc.y);
-          acc.z = fmaf(wk, v[k].z, acc.z);
-          acc.w = fmaf(wk, v[k].w, acc.w);
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int e = 0; e < kJoinAhead; ++e)
+              v[r][e] = i0 + j + e < n ? __ldcg(reinterpret_cast<const float4*>(p.part_o + (at[r] + (long long)(i0 + j + e) * 2 * kRows) * kHeadDim) + lane)
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int e = 0; e < kJoinAhead; ++e) {
+              const float we = __shfl_sync(kAll, w, 8 * (r0 + r) + j + e);
+              if (we == 0.f) continue;
+              acc[r].x = fmaf(we, v[r][e].x, acc[r].x);
+              acc[r].y = fmaf(we, v[r][e].y, acc[r].y);
+              acc[r].z = fmaf(we, v[r][e].z, acc[r].z);
+              acc[r].w = fmaf(we, v[r][e].w, acc[r].w);
+            }
         }
       }
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    const float inv = m == -INFINITY ? 0.f : 1.f / sum;
-    const long long orow = (long long)(q0 + row / p.group) * p.hqo + head * p.group + row % p.group;
-    *reinterpret_cast<uint2*>(p.o + orow * kHeadDim + 4 * lane) =
-        make_uint2(f2_to_bf16x2(acc.x * inv, acc.y * inv), f2_to_bf16x2(acc.z * inv, acc.w * inv));
-    if (lane == 0) p.lse[orow] = m == -INFINITY ? -INFINITY : (m + fast_log2(sum)) * kLn2;
+      for (int r = 0; r < 2; ++r) {
+        const int k = k0 + r0 + r;
+        if (k >= rows || r0 + r >= some) continue;
+        const long long orow = (long long)(q0 + k / p.group) * p.hqo + head * p.group + k % p.group;
+        *reinterpret_cast<uint2*>(p.o + orow * kHeadDim + 4 * lane) = make_uint2(f2_to_bf16x2(acc[r].x, acc[r].y), f2_to_bf16x2(acc[r].z, acc[r].w));
+      }
+    }
   }
 }
 
@@ -849,16 +1070,15 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-// Pages of either layout as (dim, KV head, token in page, page); a box is one page and head, 64 dims of bf16
-// (128B-swizzled) or 128 codes.
+// Pages of either layout as (dim, KV head, token in page, page); a box is one page and head, 64 dims of bf16 or 128 codes,
+// 128B-swizzled.
 bool page_map(CUtensorMap* m, const void* base, const PageView& pv, bool fp8) {
   const cuuint64_t e = fp8 ? 1 : 2;
   const cuuint64_t dims[4] = {cuuint64_t(kHeadDim), cuuint64_t(pv.hkv), cuuint64_t(pv.page_size), cuuint64_t(pv.num_pages)};
   const cuuint64_t strides[3] = {pv.head_stride * e, pv.tok_stride * e, pv.page_stride * e};
   const cuuint32_t box[4] = {fp8 ? 128u : 64u, 1u, cuuint32_t(pv.page_size), 1u}, step[4] = {1u, 1u, 1u, 1u};
   return encoder()(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
-                   strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                   strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // q as (dim, head, token); a box is 64 dims of the rows of a tile.

@@ -37,17 +37,19 @@ constexpr int kTreeKeys = 128;
 constexpr int kTreeLeastTiles = 2;  // tiles of a CTA's piece of the line, as long as there are enough
 
 // Tiles of the requests before each one (Geo::tree0) and of all; false if there are more than 2^31 - 1.
-bool fill_tree(Geo* geo, int batch, int hkv, int group, int32_t* total);
+// starts: the request in which the line of each of `ctas` CTAs begins.
+bool fill_tree(Geo* geo, int batch, int hkv, int group, int ctas, int32_t* total, int32_t* starts);
 
 struct TreeParams {
   PageView pv;
   const __nv_bfloat16* q;
   const void *k_pages, *v_pages;
-  const uint32_t* mask;  // [total_q][mask_words]
+  const int32_t* starts;  // of each CTA, the request in which its part of the line begins
+  const uint32_t* mask;   // [total_q][mask_words]
   int mask_words;
   __nv_bfloat16* o;
   float* lse;
-  float* part_o;    // [2 CTAs][128 rows][128], normalised
+  float* part_o;    // [2 CTAs][2 row tiles][128 rows][128], normalised
   float* part_lse;  // log2 domain
   int hqo, group, tile_tokens;  // tile_tokens: 128 / group
   uint32_t q_tile_bytes;
