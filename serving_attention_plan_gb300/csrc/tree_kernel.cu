@@ -64,10 +64,10 @@ template <bool kFp8>
 struct Shape {
   static constexpr int kThreads = kFp8 ? 768 : 640;
   static constexpr int kLaunchRegs = kFp8 ? 80 : 96;
-  static constexpr uint32_t kSoftmaxRegs = kFp8 ? 152 : 160;
+  static constexpr uint32_t kSoftmaxRegs = kFp8 ? 136 : 144;
   static constexpr uint32_t kWriteRegs = kFp8 ? 72 : 80;
-  static constexpr uint32_t kLoadRegs = kFp8 ? 32 : 40;
-  static constexpr uint32_t kIssueRegs = kFp8 ? 32 : 40;
+  static constexpr uint32_t kLoadRegs = kFp8 ? 40 : 56;
+  static constexpr uint32_t kIssueRegs = 56;
   static constexpr uint32_t kWidenRegs = kFp8 ? 40 : 0;
   static_assert(2 * kSoftmaxRegs + kWriteRegs + kLoadRegs + kIssueRegs + kWidenRegs == kLaunchRegs * (kThreads / 128),
                 "the warpgroups' registers are those of the launch");
@@ -322,7 +322,7 @@ __device__ void widen_tiles(const TreeParams& p, TreeSmem<true>& sm, int w) {
       ok = __all_sync(kAll, wait_for(&sm.full[from], (n / S::kRing) & 1, p.pv.err, &sm.abort));
       if (!ok) break;
       const uint32_t src = smem_u32(sm.kv[from]) + uint32_t(r0 * 128), dst = smem_u32(sm.wide[to]) + half_off + uint32_t(r0 * 128);
-#pragma unroll
+#pragma unroll 1
       for (int i0 = 0; i0 < 8; i0 += 4) {
         uint32_t x[4][4];
 #pragma unroll
@@ -433,125 +433,139 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uin
       : "memory");
 }
 
-// S (kN columns) = Q K^T from the Q tile and the key rows at the given places.
-template <bool kFp8, int kN>
-__device__ __forceinline__ void score_products(uint32_t s, uint32_t q, uint32_t k) {
-  // (an e4m3 descriptor's type fields are zero, as f16's are)
-  constexpr uint32_t idesc = kFp8 ? tc::idesc_f16_f32(kRows, kN, 0, 0) : tc::idesc_bf16_f32(kRows, kN, 0, 0);
+// S = Q K^T from the descriptors of the Q tile's and the key rows' first products.  A later product's differ in the address alone,
+// whose 14 bits (16-byte units) hold all of shared memory, so it is added (made anew, the descriptors took longer than the products).
+template <bool kFp8>
+__device__ __forceinline__ void score_products(uint32_t s, uint64_t q, uint64_t k, uint32_t idesc) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     // 32 bytes of dims a product: 16 bf16 of either half, or 32 codes against either term
-    const uint32_t qi = q + uint32_t(i >> 2) * kHalfBytes + uint32_t(i & 3) * 32;
-    const uint32_t ki = k + (kFp8 ? 0u : uint32_t(i >> 2) * kHalfBytes) + uint32_t(i & 3) * 32;
-    const uint64_t a = tc::smem_desc(qi, 16, 1024, tc::kLayoutSw128), b = tc::smem_desc(ki, 16, 1024, tc::kLayoutSw128);
+    const uint64_t qi = q + uint64_t((i >> 2) * (kHalfBytes / 16) + (i & 3) * 2);
+    const uint64_t ki = k + uint64_t((kFp8 ? 0 : (i >> 2) * (kHalfBytes / 16)) + (i & 3) * 2);
     if constexpr (kFp8)
-      mma_e4m3(s, a, b, idesc, i != 0 ? 1u : 0u);
+      mma_e4m3(s, qi, ki, idesc, i != 0 ? 1u : 0u);
     else
-      tc::mma_ss(s, a, b, idesc, i != 0 ? 1u : 0u);
+      tc::mma_ss(s, qi, ki, idesc, i != 0 ? 1u : 0u);
   }
+}
+
+// The scores of one piece; false after a wait that ran out.  (A piece's kind, kTwo row tiles or one, is settled outside the loop:
+// the loop's code stays small, and a product's descriptors are constants but for their addresses.)
+template <bool kFp8, bool kTwo>
+__device__ bool issue_piece_scores(const TreeParams& p, TreeSmem<kFp8>& sm, uint32_t tmem, int steps, int& tt, int& ss, int& nq) {
+  using S = Shape<kFp8>;
+  // (an e4m3 descriptor's type fields are zero, as f16's are)
+  constexpr int kN = kTwo ? kHalfKeys : kKeys;
+  constexpr uint32_t idesc = kFp8 ? tc::idesc_f16_f32(kRows, kN, 0, 0) : tc::idesc_bf16_f32(kRows, kN, 0, 0);
+  uint64_t* q_in = kFp8 ? sm.q_ready : sm.q_full;
+  uint64_t q[kTwo ? 2 : 1];
+#pragma unroll
+  for (int h = 0; h < (kTwo ? 2 : 1); ++h) {
+    if (!__all_sync(kAll, wait_for(&q_in[(nq + h) & 1], ((nq + h) >> 1) & 1, p.pv.err, &sm.abort))) return false;
+    q[h] = tc::smem_desc(smem_u32(sm.q[(nq + h) & 1]), 16, 1024, tc::kLayoutSw128);
+  }
+  for (int s = 0; s < steps; ++s, ++ss) {
+    const int n = 2 * tt, slot = n % S::kRing, b = ss & 1, sub = kTwo ? s & 1 : 0;
+    if (sub == 0 && !__all_sync(kAll, wait_for(&sm.full[slot], (n / S::kRing) & 1, p.pv.err, &sm.abort))) return false;
+    const uint64_t k = tc::smem_desc(smem_u32(sm.kv[slot]) + uint32_t(sub * kHalfKeys * 128), 16, 1024, tc::kLayoutSw128);
+    const bool done = !kTwo || sub == 1 || s == steps - 1;  // with the tile
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      // the buffer's last P has been read; with one row tile, both groups' are
+      if (ss >= 2 && !__all_sync(kAll, wait_for(&sm.pv_done[h][b], ((ss >> 1) - 1) & 1, p.pv.err, &sm.abort))) return false;
+      if (!kTwo && h == 0) continue;
+      tc::fence_after_sync();
+      if (elect_one()) {
+        if constexpr (kTwo) {
+          score_products<kFp8>(tmem + uint32_t(b * kKeys + h * kHalfKeys), q[h], k, idesc);
+          tc::commit(&sm.s_full[h][b]);
+        } else {
+          score_products<kFp8>(tmem + uint32_t(b * kKeys), q[0], k, idesc);
+          tc::commit(&sm.s_full[0][b]);
+          tc::commit(&sm.s_full[1][b]);
+        }
+        if (h == 1 && done) tc::commit(&sm.empty[slot]);
+        if (h == 1 && s == steps - 1) {
+          tc::commit(&sm.q_empty[nq & 1]);
+          if (kTwo) tc::commit(&sm.q_empty[(nq + 1) & 1]);
+        }
+      }
+      __syncwarp();
+    }
+    if (done) ++tt;
+  }
+  nq += kTwo ? 2 : 1;
+  return true;
 }
 
 template <bool kFp8>
 __device__ void issue_scores(const TreeParams& p, TreeSmem<kFp8>& sm, uint32_t tmem) {
-  using S = Shape<kFp8>;
-  uint64_t* q_in = kFp8 ? sm.q_ready : sm.q_full;
   Piece c;
-  int tt = 0, ss = 0, nu = 0, nq = 0;  // tiles, steps, pieces, Q tiles
-  while (take(p, sm, nu, c)) {
-    ++nu;
-    const bool two = c.nq > p.tile_tokens;
-    bool ok = wait_for(&q_in[nq & 1], (nq >> 1) & 1, p.pv.err, &sm.abort);
-    if (two) ok = ok && wait_for(&q_in[(nq + 1) & 1], ((nq + 1) >> 1) & 1, p.pv.err, &sm.abort);
-    if (!__all_sync(kAll, ok)) return;
-    const uint32_t q0 = smem_u32(sm.q[nq & 1]), q1 = smem_u32(sm.q[(nq + 1) & 1]);
-    const int steps = steps_of(c, two);
-    for (int s = 0; s < steps; ++s, ++ss) {
-      const int n = 2 * tt, slot = n % S::kRing, b = ss & 1, sub = two ? s & 1 : 0;
-      if (sub == 0 && !__all_sync(kAll, wait_for(&sm.full[slot], (n / S::kRing) & 1, p.pv.err, &sm.abort))) return;
-      const uint32_t k = smem_u32(sm.kv[slot]) + uint32_t(sub * kHalfKeys * 128);
-      const bool done = !two || sub == 1 || s == steps - 1;  // with the tile
-      // a buffer's last P has been read
-      if (ss >= 2 && !__all_sync(kAll, wait_for(&sm.pv_done[0][b], ((ss >> 1) - 1) & 1, p.pv.err, &sm.abort))) return;
-      if (ss >= 2 && !two && !__all_sync(kAll, wait_for(&sm.pv_done[1][b], ((ss >> 1) - 1) & 1, p.pv.err, &sm.abort))) return;
+  int tt = 0, ss = 0, nq = 0;  // tiles, steps, Q tiles
+  bool ok = true;
+  for (int nu = 0; ok && take(p, sm, nu, c); ++nu)
+    ok = c.nq > p.tile_tokens ? issue_piece_scores<kFp8, true>(p, sm, tmem, steps_of(c, true), tt, ss, nq)
+                              : issue_piece_scores<kFp8, false>(p, sm, tmem, steps_of(c, false), tt, ss, nq);
+}
+
+template <bool kFp8, bool kTwo>
+__device__ bool issue_piece_outputs(const TreeParams& p, TreeSmem<kFp8>& sm, uint32_t tmem, int steps, int keys, int nu, int& tt, int& ss) {
+  using S = Shape<kFp8>;
+  constexpr uint32_t idesc = kFp8 ? tc::idesc_f16_f32(kRows, kHeadDim, 0, 1) : tc::idesc_bf16_f32(kRows, kHeadDim, 0, 1);
+  const int lane = threadIdx.x & 31;
+  for (int s = 0; s < steps; ++s, ++ss) {
+    const int n = 2 * tt + 1, slot = kFp8 ? tt % 2 : n % S::kRing, b = ss & 1, sub = kTwo ? s & 1 : 0;
+    uint8_t* tile = kFp8 ? sm.wide[kFp8 ? slot : 0] : sm.kv[slot];
+    if (sub == 0) {
+      if (!__all_sync(kAll, kFp8 ? wait_for(&sm.wide_full[slot & 1], (tt >> 1) & 1, p.pv.err, &sm.abort)
+                                 : wait_for(&sm.full[slot], (n / S::kRing) & 1, p.pv.err, &sm.abort)))
+        return false;
+      const int lim = keys - (kTwo ? s >> 1 : s) * kKeys;
+      if (!kFp8 && lim < kKeys) {
+        // the box of the last page brought the slots behind the last key, which may hold NaN: a weight of zero would not
+        // cancel it (the rows behind that page came in as zeros)
+        const int stop = min(kKeys, (max(lim, 0) + p.pv.page_size - 1) / p.pv.page_size * p.pv.page_size);
+        for (int i = max(lim, 0) * 16 + lane; i < stop * 16; i += 32)
+          *reinterpret_cast<uint4*>(tile + ((i >> 3) & 1) * kHalfBytes + (i >> 4) * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+    }
+    const bool done = !kTwo || sub == 1 || s == steps - 1;  // with the tile
+    // V as B (keys x dims), MN-major: 16 keys are two 8-row groups, the second 64 dims the leading step
+    const uint64_t v0 = tc::smem_desc(smem_u32(tile), kHalfBytes, 1024, tc::kLayoutSw128);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      bool ok = wait_for(&sm.p_full[h][b], (ss >> 1) & 1, p.pv.err, &sm.abort);
+      // the piece's first product overwrites O once the last piece's has been read out
+      if (s == 0 && h == 0 && nu > 0) ok = ok && wait_for(&sm.o_free, (nu - 1) & 1, p.pv.err, &sm.abort);
+      if (!__all_sync(kAll, ok)) return false;
       tc::fence_after_sync();
       if (elect_one()) {
-        if (two)
-          score_products<kFp8, kHalfKeys>(tmem + uint32_t(b * kKeys), q0, k);
-        else
-          score_products<kFp8, kKeys>(tmem + uint32_t(b * kKeys), q0, k);  // both groups' keys
-        tc::commit(&sm.s_full[0][b]);
+        const uint64_t v = v0 + uint64_t((kTwo ? sub : h) * (kHalfKeys * 128 / 16));
+#pragma unroll
+        for (int i = 0; i < kHalfKeys / 16; ++i)
+          tc::mma_ts(tmem + kColO + uint32_t(h * kHeadDim), tmem + uint32_t(b * kKeys + h * kHalfKeys + i * 8),
+                     v + uint64_t(i * (2048 / 16)), idesc, (s != 0 || i != 0) ? 1u : 0u);
+        tc::commit(&sm.pv_done[h][b]);
+        if (h == 1 && done) tc::commit(kFp8 ? &sm.wide_empty[slot & 1] : &sm.empty[slot]);
       }
       __syncwarp();
-      if (two) {
-        if (ss >= 2 && !__all_sync(kAll, wait_for(&sm.pv_done[1][b], ((ss >> 1) - 1) & 1, p.pv.err, &sm.abort))) return;
-        tc::fence_after_sync();
-      }
-      if (elect_one()) {
-        if (two) score_products<kFp8, kHalfKeys>(tmem + uint32_t(b * kKeys + kHalfKeys), q1, k);
-        tc::commit(&sm.s_full[1][b]);
-        if (done) tc::commit(&sm.empty[slot]);
-        if (s == steps - 1) {
-          tc::commit(&sm.q_empty[nq & 1]);
-          if (two) tc::commit(&sm.q_empty[(nq + 1) & 1]);
-        }
-      }
-      __syncwarp();
-      if (done) ++tt;
     }
-    nq += two ? 2 : 1;
+    if (done) ++tt;
   }
+  return true;
 }
 
 template <bool kFp8>
 __device__ void issue_outputs(const TreeParams& p, TreeSmem<kFp8>& sm, uint32_t tmem) {
-  using S = Shape<kFp8>;
-  constexpr uint32_t idesc = kFp8 ? tc::idesc_f16_f32(kRows, kHeadDim, 0, 1) : tc::idesc_bf16_f32(kRows, kHeadDim, 0, 1);
-  const int lane = threadIdx.x & 31;
   Piece c;
-  int tt = 0, ss = 0, nu = 0;
-  for (; take(p, sm, nu, c); ++nu) {
-    const bool two = c.nq > p.tile_tokens;
-    const int steps = steps_of(c, two);
-    for (int s = 0; s < steps; ++s, ++ss) {
-      const int n = 2 * tt + 1, slot = kFp8 ? tt % 2 : n % S::kRing, b = ss & 1, sub = two ? s & 1 : 0;
-      uint8_t* tile = kFp8 ? sm.wide[kFp8 ? slot : 0] : sm.kv[slot];
-      if (sub == 0) {
-        if (!__all_sync(kAll, kFp8 ? wait_for(&sm.wide_full[slot & 1], (tt >> 1) & 1, p.pv.err, &sm.abort)
-                                   : wait_for(&sm.full[slot], (n / S::kRing) & 1, p.pv.err, &sm.abort)))
-          return;
-        const int lim = c.lkv - (c.k0 + (two ? s >> 1 : s)) * kKeys;
-        if (!kFp8 && lim < kKeys) {
-          // the box of the last page brought the slots behind the last key, which may hold NaN: a weight of zero would not
-          // cancel it (the rows behind that page came in as zeros)
-          const int stop = min(kKeys, (max(lim, 0) + p.pv.page_size - 1) / p.pv.page_size * p.pv.page_size);
-          for (int i = max(lim, 0) * 16 + lane; i < stop * 16; i += 32)
-            *reinterpret_cast<uint4*>(tile + ((i >> 3) & 1) * kHalfBytes + (i >> 4) * 128 + (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-      }
-      const bool done = !two || sub == 1 || s == steps - 1;  // with the tile
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        bool ok = wait_for(&sm.p_full[h][b], (ss >> 1) & 1, p.pv.err, &sm.abort);
-        // the piece's first product overwrites O once the last piece's has been read out
-        if (s == 0 && h == 0 && nu > 0) ok = ok && wait_for(&sm.o_free, (nu - 1) & 1, p.pv.err, &sm.abort);
-        if (!__all_sync(kAll, ok)) return;
-        tc::fence_after_sync();
-        if (elect_one()) {
-          const uint32_t v = smem_u32(tile) + uint32_t((two ? sub : h) * kHalfKeys * 128);
-#pragma unroll
-          for (int i = 0; i < kHalfKeys / 16; ++i)
-            // V as B (keys x dims), MN-major: 16 keys are two 8-row groups, the second 64 dims the leading step
-            tc::mma_ts(tmem + kColO + uint32_t(h * kHeadDim), tmem + uint32_t(b * kKeys + h * kHalfKeys + i * 8),
-                       tc::smem_desc(v + uint32_t(i * 2048), kHalfBytes, 1024, tc::kLayoutSw128), idesc, (s != 0 || i != 0) ? 1u : 0u);
-          tc::commit(&sm.pv_done[h][b]);
-          if (h == 1 && done) tc::commit(kFp8 ? &sm.wide_empty[slot & 1] : &sm.empty[slot]);
-        }
-        __syncwarp();
-      }
-      if (done) ++tt;
-    }
+  int tt = 0, ss = 0;
+  bool ok = true;
+  for (int nu = 0; ok && take(p, sm, nu, c); ++nu) {
+    const int keys = c.lkv - c.k0 * kKeys;  // of the piece's tiles on
+    ok = c.nq > p.tile_tokens ? issue_piece_outputs<kFp8, true>(p, sm, tmem, steps_of(c, true), keys, nu, tt, ss)
+                              : issue_piece_outputs<kFp8, false>(p, sm, tmem, steps_of(c, false), keys, nu, tt, ss);
   }
 }
 
@@ -572,7 +586,7 @@ __device__ __forceinline__ uint64_t seen_keys(const uint32_t* mask, int words, i
   return seen | (d > 0 ? bits << d : bits);
 }
 
-template <bool kMasked, int kCap, bool kF16>
+template <int kCap, bool kF16>
 __device__ __forceinline__ void softmax_half(const TreeParams& p, float scale, uint32_t t_s, uint32_t t_o, uint64_t seen, float& m, float& l,
                                              bool first, uint64_t* pv_done, int pv_parity, int32_t* err, int* abort, bool& alive) {
   uint32_t s[kHalfKeys];
@@ -590,14 +604,15 @@ __device__ __forceinline__ void softmax_half(const TreeParams& p, float scale, u
     }
     scale = 1.f;
   }
+  if (!__all_sync(kAll, seen == ~0ull)) {
+#pragma unroll
+    for (int j = 0; j < kHalfKeys; ++j) s[j] = (uint32_t(seen >> (j & 32)) >> (j & 31)) & 1u ? s[j] : __float_as_uint(-INFINITY);
+  }
   float mx[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) mx[j] = -INFINITY;
 #pragma unroll
-  for (int j = 0; j < kHalfKeys; ++j) {
-    if (kMasked) s[j] = (uint32_t(seen >> (j & 32)) >> (j & 31)) & 1u ? s[j] : __float_as_uint(-INFINITY);
-    mx[j & 7] = fmaxf(mx[j & 7], __uint_as_float(s[j]));
-  }
+  for (int j = 0; j < kHalfKeys; ++j) mx[j & 7] = fmaxf(mx[j & 7], __uint_as_float(s[j]));
   const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
   const float m_new = fmaxf(m, top * scale);
   float alpha = 1.f;
@@ -679,10 +694,7 @@ __device__ void softmax_keys(const TreeParams& p, TreeSmem<kFp8>& sm, uint32_t t
         const uint32_t t_s = mine + uint32_t(b * kKeys + h * kHalfKeys);
         uint64_t* before = &sm.pv_done[h][b ^ 1];  // the product that wrote O last
         const int parity = ((ss - 1) >> 1) & 1;
-        if (__all_sync(kAll, seen == ~0ull))
-          softmax_half<false, kCap, kFp8>(p, scale, t_s, t_o, seen, m, l, s == 0, before, parity, p.pv.err, &sm.abort, alive);
-        else
-          softmax_half<true, kCap, kFp8>(p, scale, t_s, t_o, seen, m, l, s == 0, before, parity, p.pv.err, &sm.abort, alive);
+        softmax_half<kCap, kFp8>(p, scale, t_s, t_o, seen, m, l, s == 0, before, parity, p.pv.err, &sm.abort, alive);
         tc::fence_before_sync();
       }
       __syncwarp();
@@ -779,24 +791,16 @@ __device__ void write_pieces(const TreeParams& p, TreeSmem<kFp8>& sm, uint32_t t
                                  : ((long long)c.slot * 2 + h) * kRows + row;
 #pragma unroll 1
       for (int k = 0; k < kHeadDim; k += 16) {
+        // (a group without a seen key, or of other rows, has nothing to add, not even 0 x NaN)
         float v[16];
-        uint32_t a[16];
-        if (two) {
-          tmem_ld16(mine + h * kHeadDim + k, a);
-          tc::tmem_wait_ld();
-          const float w = h ? w1 : w0;
+        uint32_t a[16], b[16];
+        tmem_ld16(mine + k, a);
+        tmem_ld16(mine + kHeadDim + k, b);
+        tc::tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = w != 0.f ? __uint_as_float(a[j]) * w : 0.f;
-        } else {
-          uint32_t b[16];
-          tmem_ld16(mine + k, a);
-          tmem_ld16(mine + kHeadDim + k, b);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {  // a group without a seen key has nothing to add, not even 0 x NaN
-            const float x = w0 != 0.f ? __uint_as_float(a[j]) * w0 : 0.f;
-            v[j] = w1 != 0.f ? fmaf(__uint_as_float(b[j]), w1, x) : x;
-          }
+        for (int j = 0; j < 16; ++j) {
+          const float x = w0 != 0.f ? __uint_as_float(a[j]) * w0 : 0.f;
+          v[j] = w1 != 0.f ? fmaf(__uint_as_float(b[j]), w1, x) : x;
         }
         if (write) put16(p, whole, at, k, v);
       }
