@@ -1089,6 +1089,7 @@ int fi_score_pages(fi_workspace* ws, const void* q, const void* bounds, int num_
   p.bounds = static_cast<const __nv_bfloat16*>(bounds);
   p.scores = scores;
   p.row_pages = row_pages;
+  p.most_batch = ws->max_batch;
   p.hqo = ws->hqo;
   p.group = ws->hqo / ws->hkv;
   p.scale = 1.f / std::sqrt(float(ws->head_dim));
@@ -1115,7 +1116,7 @@ int fi_select_pages(fi_workspace* ws, const float* scores, int32_t row_pages, in
   p.pv = page_view(ws, 0);
   p.scores = scores;
   p.selected = selected;
-  p.row_pages = row_pages;
+  p.row_pages = scores == nullptr ? 0 : row_pages;  // nothing is read
   p.sink = sink;
   p.recent = recent;
   p.budget = budget;

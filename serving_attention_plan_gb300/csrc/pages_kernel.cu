@@ -32,6 +32,17 @@ __device__ __forceinline__ int pages_of(const PageView& pv, int keys) {
   return pv.page_shift >= 0 ? (keys + pv.page_size - 1) >> pv.page_shift : (keys + pv.page_size - 1) / pv.page_size;
 }
 
+// The request of query token t < total_q.  In a decode batch that is entry t itself, so it is looked at first; a whole warp calls.
+__device__ __forceinline__ Geo request_of(const Geo* geo, int batch, int t, int& r) {
+  r = min(t, batch - 1);
+  Geo g = load_geo(geo, r);
+  if (t < g.q0 || t >= g.q0 + g.lq) {
+    r = find_request(geo, batch, &Geo::q0, t);
+    g = load_geo(geo, r);
+  }
+  return g;
+}
+
 // ---- bounds ------------------------------------------------------------------------------------------
 //   bounds[page][head][0][d] = min, [1][d] = max over the page's keys of K[key][d]   (e4m3: of the codes' values)
 // NaN wins, so that a page with a NaN key ranks first and its attention shows it.  Exact: a minimum is one of its inputs, and every
@@ -70,10 +81,16 @@ __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t h) {
 constexpr int kBoundsThreads = 256;
 constexpr int kBoundsAhead = 8;
 
-// Pairs of dims that a lane holds: 4 words of bf16, or 8 of f16 (16 codes).
+// One step: up to kBoundsAhead loads of a (page, head), which takes more than one if its page is long.
+struct BoundsStep {
+  int page, keys, head, k0;  // page -1: nothing to read
+};
+
+// Words of two dims that a lane holds: 4 of bf16, or 8 of f16 (16 codes).  The loads of a step are under way while the one before it
+// is compared (116 -> 98 us for 13 prompts of 8 to 36 K keys).
 template <bool kFp8>
 __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const __grid_constant__ BoundsParams p) {
-  constexpr int kLanes = kFp8 ? 8 : 16, kSide = 32 / kLanes, kWords = kFp8 ? 8 : 4;
+  constexpr int kLanes = kFp8 ? 8 : 16, kSide = 32 / kLanes, kWords = kFp8 ? 8 : 4, kRowsStep = kBoundsAhead * kSide;
   wait_prior_grid();
   const PageView& pv = p.pv;
   const GeoHead plan = load_head(pv.geo);
@@ -85,83 +102,102 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const __grid_con
   const long long me = (long long)blockIdx.x * (kBoundsThreads / 32) + (threadIdx.x >> 5);
   const long long t0 = tasks * me / warps, t1 = tasks * (me + 1) / warps;
   if (t0 >= t1) return;
-  int unit = int(t0 / pv.hkv), head = int(t0 - (long long)unit * pv.hkv);
-  int r = find_request(pv.geo, plan.batch, p.new_keys ? &Geo::q0 : &Geo::kv0, unit);
-  Geo g = load_geo(pv.geo, r);
-  int page = -1, keys = 0;  // of the unit; -1: nothing to do
-  bool fresh = true;
-  for (long long task = t0; task < t1; ++task) {
-    if (fresh) {
-      fresh = false;
-      int e;
-      if (p.new_keys) {
-        while (unit >= g.q0 + g.lq) g = load_geo(pv.geo, ++r);
-        const int t = unit - g.q0, j = g.lkv - g.lq + t;
-        // the first new token of its page speaks for the page
-        const bool first = j >= 0 && (t == 0 || j == 0 || j % pv.page_size == 0);
-        e = first ? j / pv.page_size : -1;
-      } else {
-        while (unit >= g.kv0 + pages_of(pv, g.lkv)) g = load_geo(pv.geo, ++r);
-        e = unit - g.kv0;
-      }
-      page = -1;
-      if (e >= 0) {
-        keys = min(pv.page_size, g.lkv - e * pv.page_size);
-        page = __ldg(pv.kv_indices + g.kv0 + e);
-        if (static_cast<unsigned>(page) >= static_cast<unsigned>(pv.num_pages)) {
-          atomicOr(pv.err, FI_DEVERR_PAGE_OOB);
-          page = -1;
-        }
-      }
+  int unit = int(t0 / pv.hkv);
+  long long task = t0;
+  int r = p.new_keys ? 0 : find_request(pv.geo, plan.batch, &Geo::kv0, unit);
+  Geo g = p.new_keys ? request_of(pv.geo, plan.batch, unit, r) : load_geo(pv.geo, r);
+  BoundsStep next = {-1, 0, int(t0 - (long long)unit * pv.hkv), 0};
+  auto look_up = [&]() {  // the page of `unit`
+    int e;
+    next.page = -1;
+    next.keys = 0;
+    if (p.new_keys) {
+      while (unit >= g.q0 + g.lq) g = load_geo(pv.geo, ++r);
+      const int t = unit - g.q0, j = g.lkv - g.lq + t;
+      // the first new token of its page speaks for the page
+      const bool first = j >= 0 && (t == 0 || j == 0 || j % pv.page_size == 0);
+      e = first ? j / pv.page_size : -1;
+    } else {
+      while (unit >= g.kv0 + pages_of(pv, g.lkv)) g = load_geo(pv.geo, ++r);
+      e = unit - g.kv0;
     }
-    if (page >= 0) {
-      const char* src = static_cast<const char*>(p.k_pages) + kv_offset(pv, page, 0, head) * (kFp8 ? 1 : 2) + sub * 16;
-      const long long step = pv.tok_stride * (kFp8 ? 1 : 2);
-      uint32_t lo[kWords], hi[kWords];
-      bool any = false;
-      for (int k0 = 0; k0 < keys; k0 += kBoundsAhead * kSide) {
-        uint4 x[kBoundsAhead];
-#pragma unroll
-        for (int i = 0; i < kBoundsAhead; ++i)  // a row behind the last key stands for the last
-          x[i] = k0 + i * kSide < keys ? __ldcs(reinterpret_cast<const uint4*>(src + min(k0 + i * kSide + side, keys - 1) * step)) : x[0];
-#pragma unroll
-        for (int i = 0; i < kBoundsAhead; ++i) {
-          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-          for (int k = 0; k < kWords; ++k) {
-            const uint32_t v = kFp8 ? widen2(k & 1 ? w[k / 2] >> 16 : w[k / 2]) : w[k & 3];
-            lo[k] = any || i > 0 ? min2(lo[k], v, kFp8) : v;
-            hi[k] = any || i > 0 ? max2(hi[k], v, kFp8) : v;
-          }
-        }
-        any = true;
-      }
-#pragma unroll
-      for (int m = kLanes; m < 32; m <<= 1) {
-#pragma unroll
-        for (int k = 0; k < kWords; ++k) {
-          lo[k] = min2(lo[k], __shfl_xor_sync(kAll, lo[k], m), kFp8);
-          hi[k] = max2(hi[k], __shfl_xor_sync(kAll, hi[k], m), kFp8);
-        }
-      }
-      uint4* to = reinterpret_cast<uint4*>(p.bounds + ((long long)page * pv.hkv + head) * 2 * kHeadDim);
-      if constexpr (kFp8) {  // the row's four lanes of a sub take a half of its 16 minima or maxima each
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t a = side & 1 ? lo[4 + k] : lo[k], b = side & 1 ? hi[4 + k] : hi[k];
-          w[k] = f16x2_to_bf16x2(side & 2 ? b : a);
-        }
-        to[(side >> 1) * 16 + sub * 2 + (side & 1)] = make_uint4(w[0], w[1], w[2], w[3]);
-      } else {
-        to[side * 16 + sub] = side ? make_uint4(hi[0], hi[1], hi[2], hi[3]) : make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      }
+    if (e < 0) return;
+    next.keys = min(pv.page_size, g.lkv - e * pv.page_size);
+    next.page = __ldg(pv.kv_indices + g.kv0 + e);
+    if (static_cast<unsigned>(next.page) >= static_cast<unsigned>(pv.num_pages)) {
+      atomicOr(pv.err, FI_DEVERR_PAGE_OOB);
+      next.page = -1;
     }
-    if (++head == pv.hkv) {
-      head = 0;
+  };
+  auto advance = [&]() {  // to the step after `next`; false behind the last
+    if (next.page >= 0 && next.k0 + kRowsStep < next.keys) {
+      next.k0 += kRowsStep;
+      return true;
+    }
+    next.k0 = 0;
+    if (++task >= t1) return false;
+    if (++next.head == pv.hkv) {
+      next.head = 0;
       ++unit;
-      fresh = true;
+      look_up();
     }
+    return true;
+  };
+  const long long step = pv.tok_stride * (kFp8 ? 1 : 2);
+  auto fetch = [&](uint4 (&x)[kBoundsAhead]) {
+    if (next.page < 0) return;
+    const char* src = static_cast<const char*>(p.k_pages) + kv_offset(pv, next.page, 0, next.head) * (kFp8 ? 1 : 2) + sub * 16;
+#pragma unroll
+    for (int i = 0; i < kBoundsAhead; ++i)  // a row behind the last key stands for the last
+      if (next.k0 + i * kSide < next.keys)
+        x[i] = __ldcs(reinterpret_cast<const uint4*>(src + min(next.k0 + i * kSide + side, next.keys - 1) * step));
+  };
+  uint4 x[2][kBoundsAhead];
+  uint32_t lo[kWords], hi[kWords];
+  look_up();
+  fetch(x[0]);
+  bool more = true;
+  auto turn = [&](uint4 (&now)[kBoundsAhead], uint4 (&ahead)[kBoundsAhead]) {
+    const BoundsStep c = next;
+    more = advance();
+    if (more) fetch(ahead);
+    if (c.page < 0) return;
+#pragma unroll
+    for (int i = 0; i < kBoundsAhead; ++i) {
+      if (c.k0 + i * kSide >= c.keys) break;
+      const uint32_t w[4] = {now[i].x, now[i].y, now[i].z, now[i].w};
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) {
+        const uint32_t v = kFp8 ? widen2(k & 1 ? w[k / 2] >> 16 : w[k / 2]) : w[k & 3];
+        lo[k] = c.k0 > 0 || i > 0 ? min2(lo[k], v, kFp8) : v;
+        hi[k] = c.k0 > 0 || i > 0 ? max2(hi[k], v, kFp8) : v;
+      }
+    }
+    if (c.k0 + kRowsStep < c.keys) return;
+#pragma unroll
+    for (int m = kLanes; m < 32; m <<= 1) {
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) {
+        lo[k] = min2(lo[k], __shfl_xor_sync(kAll, lo[k], m), kFp8);
+        hi[k] = max2(hi[k], __shfl_xor_sync(kAll, hi[k], m), kFp8);
+      }
+    }
+    uint4* to = reinterpret_cast<uint4*>(p.bounds + ((long long)c.page * pv.hkv + c.head) * 2 * kHeadDim);
+    if constexpr (kFp8) {  // the row's four lanes of a sub take a half of its 16 minima or maxima each
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t a = side & 1 ? lo[4 + k] : lo[k], b = side & 1 ? hi[4 + k] : hi[k];
+        w[k] = f16x2_to_bf16x2(side & 2 ? b : a);
+      }
+      to[(side >> 1) * 16 + sub * 2 + (side & 1)] = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      to[side * 16 + sub] = side ? make_uint4(hi[0], hi[1], hi[2], hi[3]) : make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+  };
+  while (more) {
+    turn(x[0], x[1]);
+    if (more) turn(x[1], x[0]);
   }
 }
 
@@ -169,12 +205,18 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const __grid_con
 //   score(t, h, e) = scale * max over the query heads of h's group of  sum_d  min(q_d, 0) lo_d + max(q_d, 0) hi_d
 // no less than the logit of any key of page e; -inf for a page that token t does not see.  The sum is a product of 256 terms
 // whose one factor [lo, hi] is the page's row as it lies in memory, so it runs on warp-level products: 16 pages on the rows,
-// eight (token, head) columns.  Sums are fp32.  Reading the bounds once is the bound (64 products a byte at most): each
-// warp holds 16 rows in registers, 8 KB in flight, and runs all columns of the request over them.
-// The order of the 256 terms is free, so a lane's 16 bytes of a row are taken as they come, as the A operands of two
-// products, and the q operands are read in the same order: no shared memory, no shuffle.
+// eight (token, head) columns.  Sums are fp32.  Reading the bounds once is the bound; what it takes is warps, and few steps in each:
+//  * a warp stays with one request and KV head for its run of page blocks, so that q's operands stay in registers;
+//  * the order of the 256 terms is free, so a lane's 16 bytes of a row are taken as they come from memory, as the A operands
+//    of two products, and q is read in the same order: no shared memory, no shuffle;
+//  * the next block's lo halves are asked for when this one's have gone into the products, then the hi halves;
+//  * the first page entries of all requests are read at once, where a search through them cost one latency a step.
+// (Blocks on their way to rings in shared memory, one or two ahead, with nine to twelve warps an SM: 31 and 34 us for
+// 128 decode requests of 1 to 8 K keys; sixteen warps that took a page's heads in turn, with nothing ahead: 26.)
 constexpr int kScoreThreads = 128;
+constexpr int kScoreCtas = 4;
 constexpr int kScorePages = 16;
+constexpr int kScoreList = 1024;  // requests whose first entries a CTA reads at once
 
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -182,107 +224,202 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-__global__ void __launch_bounds__(kScoreThreads, 4) scores_kernel(const __grid_constant__ ScoreParams p) {
+// 16 pages of one KV head of a request.
+struct ScoreBlock {
+  Geo g;
+  int r, room, pages;  // blocks that the line has for each head of the request, pages it has
+  int head, block;
+  int id;              // of page 16 block + lane % 16, -1 for none
+};
+
+// kHeads: columns of a token in a set of eight, 1, 2, 4 or 8 (groups of more than 8 heads take several sets); 0: any other number,
+// by a loop over the set's tokens (with that loop for all, and divisions in it, two long contexts of four tokens and eight
+// heads a group took 2000 instructions a block: 25 us).
+template <int kHeads>
+__global__ void __launch_bounds__(kScoreThreads, kScoreCtas) scores_kernel(const __grid_constant__ ScoreParams p) {
+  __shared__ int firsts[kScoreList];
+  const int lane = threadIdx.x & 31, row = lane >> 2, c = lane & 3;
   wait_prior_grid();
   const PageView& pv = p.pv;
-  const GeoHead plan = load_head(pv.geo);
-  if (plan.batch == 0) return;
-  const int lane = threadIdx.x & 31, row = lane >> 2, c = lane & 3;
-  // blocks of 16 pages: request r's begin at (its first entry) / 16 + r, which leaves each room for all of its own
   const Geo* geo = pv.geo;
-  const long long blocks = (__ldg(&geo[plan.batch].kv0) >> 4) + plan.batch;
-  const long long tasks = blocks * pv.hkv, warps = (long long)gridDim.x * (kScoreThreads / 32);
+  for (int i = threadIdx.x; i < min(kScoreList, p.most_batch); i += kScoreThreads) firsts[i] = __ldg(&geo[i].kv0);
+  const GeoHead plan = load_head(geo);
+  if (plan.batch == 0) return;
+  const int entries = __ldg(&geo[plan.batch].kv0);
+  __syncthreads();
+  // The line: for every request and KV head a place for each block.  Request r's begin at (its first entry) / 16 + r blocks,
+  // which leaves room for all of its own (and at times one more).
+  auto begins = [&](int k) { return ((k == plan.batch ? entries : k < kScoreList ? firsts[k] : __ldg(&geo[k].kv0)) >> 4) + k; };
+  const long long tasks = (long long)begins(plan.batch) * pv.hkv, warps = (long long)gridDim.x * (kScoreThreads / 32);
   const long long me = (long long)blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5);
-  const long long t0 = tasks * me / warps, t1 = tasks * (me + 1) / warps;
-  if (t0 >= t1) return;
-  const int fit = max(1, 8 / p.group);                // tokens of a set of eight columns
-  const int sets = (p.group + 7) / 8;                 // sets of a token
-  const int heads = min(p.group, 8);                  // columns of a token in a set
-  int block = int(t0 / pv.hkv), head = int(t0 - (long long)block * pv.hkv);
-  int r = last_at_most(plan.batch, block, [&](int k) { return (__ldg(&geo[k].kv0) >> 4) + k; });
-  Geo g = load_geo(geo, r);
-  int pages = 0, e0 = 0, id = -1;
-  bool fresh = true;
-  for (long long task = t0; task < t1; ++task) {
-    if (fresh) {
-      fresh = false;
-      while (r + 1 < plan.batch && block >= (__ldg(&geo[r + 1].kv0) >> 4) + r + 1) g = load_geo(geo, ++r);
-      pages = pages_of(pv, g.lkv);
-      e0 = (block - ((g.kv0 >> 4) + r)) * kScorePages;
-      id = -1;
-      if (lane < kScorePages && e0 + lane < pages) {
-        id = __ldg(pv.kv_indices + g.kv0 + e0 + lane);
-        if (static_cast<unsigned>(id) >= static_cast<unsigned>(pv.num_pages)) {
-          atomicOr(pv.err, FI_DEVERR_PAGE_OOB);
-          id = -1;
+  long long task = tasks * me / warps;
+  const long long t1 = tasks * (me + 1) / warps;
+  if (task >= t1) return;
+  const int heads = kHeads ? kHeads : p.group;
+  const int fit = 8 / heads;                               // tokens of a set of eight columns
+  const int sets = kHeads == 8 ? (p.group + 7) / 8 : 1;    // sets of a token
+  const int col_tok = row / heads, col_head = row % heads;  // of column `row`
+
+  ScoreBlock next;
+  auto enter = [&]() {
+    next.g = load_geo(geo, next.r);
+    next.room = begins(next.r + 1) - begins(next.r);
+    next.pages = pages_of(pv, next.g.lkv);
+  };
+  int id_after;  // of the place after next's, if it is of the same request
+  auto ids_at = [&](int block) {
+    const int e = block * kScorePages + (lane & 15);
+    return e < next.pages ? __ldg(pv.kv_indices + next.g.kv0 + e) : -1;
+  };
+  auto look_up = [&](int id) {
+    next.id = id;
+    if (id != -1 && static_cast<unsigned>(id) >= static_cast<unsigned>(pv.num_pages)) {
+      atomicOr(pv.err, FI_DEVERR_PAGE_OOB);
+      next.id = -1;
+    }
+    id_after = ids_at(next.block + 1 == next.room ? 0 : next.block + 1);
+  };
+  uint4 a[8], b[8];  // this lane's pieces of rows `row` and `row + 8`: 64-byte chunks 0-3 are lo, 4-7 hi
+  auto fetch = [&](int k0) {
+    const int ia = __shfl_sync(kAll, next.id, row), ib = __shfl_sync(kAll, next.id, row + 8);
+    const uint4* pa = reinterpret_cast<const uint4*>(p.bounds + ((long long)max(ia, 0) * pv.hkv + next.head) * 2 * kHeadDim) + c;
+    const uint4* pb = reinterpret_cast<const uint4*>(p.bounds + ((long long)max(ib, 0) * pv.hkv + next.head) * 2 * kHeadDim) + c;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (k < k0 || k >= k0 + 4) continue;
+      a[k] = ia >= 0 ? __ldcs(pa + 4 * k) : make_uint4(0, 0, 0, 0);
+      b[k] = ib >= 0 ? __ldcs(pb + 4 * k) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  {
+    next.r = last_at_most(plan.batch, int(task / pv.hkv), begins);
+    enter();
+    const int in = int(task - (long long)begins(next.r) * pv.hkv);
+    next.head = in / next.room;
+    next.block = in - next.head * next.room;
+    look_up(ids_at(next.block));
+    fetch(0);
+    fetch(4);
+  }
+  uint4 q[4];         // column `row` of the set at hand
+  int q_key = -1;     // the (request, head) whose first set q holds
+  for (; task < t1; ++task) {
+    const ScoreBlock now = next;
+    const bool more = task + 1 < t1;
+    if (more) {
+      if (++next.block == next.room) {
+        next.block = 0;
+        if (++next.head == pv.hkv) {
+          next.head = 0;
+          ++next.r;
+          enter();
+          id_after = ids_at(0);
         }
       }
+      look_up(id_after);
     }
-    if (e0 < pages && g.lq > 0) {
-      const int ia = __shfl_sync(kAll, id, row), ib = __shfl_sync(kAll, id, row + 8);
-      // this lane's pieces of rows `row` and `row + 8`: 64-byte chunks 0-3 are lo, 4-7 hi
-      uint4 a[8], b[8];
-      const uint4* pa = reinterpret_cast<const uint4*>(p.bounds + ((long long)max(ia, 0) * pv.hkv + head) * 2 * kHeadDim) + c;
-      const uint4* pb = reinterpret_cast<const uint4*>(p.bounds + ((long long)max(ib, 0) * pv.hkv + head) * 2 * kHeadDim) + c;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        a[k] = ia >= 0 ? __ldcs(pa + 4 * k) : make_uint4(0, 0, 0, 0);
-        b[k] = ib >= 0 ? __ldcs(pb + 4 * k) : make_uint4(0, 0, 0, 0);
+    const int lq = now.g.lq;
+    if (now.block * kScorePages >= now.pages || lq == 0) {  // an empty place
+      if (more) {
+        fetch(0);
+        fetch(4);
       }
-      for (int tok = 0; tok < g.lq; tok += fit) {
-        float best[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};  // [page row][column of the lane's two]
-        for (int set = 0; set < sets; ++set) {
-          // column `row` of this set: (token, head of the group)
-          const int ct = tok + row / heads, ch = set * 8 + row % heads;
-          const bool on = row / heads < fit && ct < g.lq && ch < p.group;
-          const uint4* pq = reinterpret_cast<const uint4*>(p.q + ((long long)(g.q0 + (on ? ct : 0)) * p.hqo + head * p.group + (on ? ch : 0)) * kHeadDim) + c;
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      continue;
+    }
+    const int ia = __shfl_sync(kAll, now.id, row), ib = __shfl_sync(kAll, now.id, row + 8);
+    // column `row` of a set: (token, head of the group)
+    auto query = [&](int tok, int set) {
+      const int ct = tok + col_tok, ch = set * 8 + col_head;
+      const bool on = col_tok < fit && ct < lq && ch < p.group;
+      const uint4* pq = reinterpret_cast<const uint4*>(p.q + ((long long)(now.g.q0 + (on ? ct : 0)) * p.hqo + now.head * p.group + (on ? ch : 0)) * kHeadDim) + c;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint4 x = __ldg(pq + 4 * k);
-            const uint32_t neg[4] = {min2(x.x, 0u, false), min2(x.y, 0u, false), min2(x.z, 0u, false), min2(x.w, 0u, false)};
-            const uint32_t pos[4] = {max2(x.x, 0u, false), max2(x.y, 0u, false), max2(x.z, 0u, false), max2(x.w, 0u, false)};
-            const uint32_t l0[4] = {a[k].x, b[k].x, a[k].y, b[k].y}, l1[4] = {a[k].z, b[k].z, a[k].w, b[k].w};
-            const uint32_t h0[4] = {a[k + 4].x, b[k + 4].x, a[k + 4].y, b[k + 4].y}, h1[4] = {a[k + 4].z, b[k + 4].z, a[k + 4].w, b[k + 4].w};
-            mma_16816(acc, l0, neg[0], neg[1]);
-            mma_16816(acc, l1, neg[2], neg[3]);
-            mma_16816(acc, h0, pos[0], pos[1]);
-            mma_16816(acc, h1, pos[2], pos[3]);
-          }
-          // columns 2 c and 2 c + 1 of the set, where they are heads of the group
+      for (int k = 0; k < 4; ++k) q[k] = __ldg(pq + 4 * k);
+    };
+    const bool one = sets == 1 && lq <= fit;  // one set of columns: q stays
+    const int key = now.r * pv.hkv + now.head;
+    if (!one || key != q_key) query(0, 0);
+    q_key = one ? key : -1;
+    float best[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};  // [page row][column of the lane's two]
+    for (int tok = 0, set = 0; tok < lq;) {
+      const bool last = set + 1 == sets;
+      const int tok2 = last ? tok + fit : tok, set2 = last ? 0 : set + 1;
+      float lo[4] = {0.f, 0.f, 0.f, 0.f}, hi[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t neg[4] = {min2(q[k].x, 0u, false), min2(q[k].y, 0u, false), min2(q[k].z, 0u, false), min2(q[k].w, 0u, false)};
+        const uint32_t l0[4] = {a[k].x, b[k].x, a[k].y, b[k].y}, l1[4] = {a[k].z, b[k].z, a[k].w, b[k].w};
+        mma_16816(lo, l0, neg[0], neg[1]);
+        mma_16816(hi, l1, neg[2], neg[3]);
+      }
+      if (tok2 >= lq && more) fetch(0);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t pos[4] = {max2(q[k].x, 0u, false), max2(q[k].y, 0u, false), max2(q[k].z, 0u, false), max2(q[k].w, 0u, false)};
+        const uint32_t h0[4] = {a[k + 4].x, b[k + 4].x, a[k + 4].y, b[k + 4].y}, h1[4] = {a[k + 4].z, b[k + 4].z, a[k + 4].w, b[k + 4].w};
+        mma_16816(lo, h0, pos[0], pos[1]);
+        mma_16816(hi, h1, pos[2], pos[3]);
+      }
+      if (tok2 >= lq && more) fetch(4);
+      if (tok2 < lq) query(tok2, set2);
+      // columns 2 c and 2 c + 1 of the set, where they are heads of the group
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const bool head_on = kHeads != 8 || set * 8 + 2 * c + k < p.group;
+        best[0][k] = max_nan(best[0][k], head_on ? lo[k] + hi[k] : -INFINITY);
+        best[1][k] = max_nan(best[1][k], head_on ? lo[2 + k] + hi[2 + k] : -INFINITY);
+      }
+      if (last) {
+        const int e0 = now.block * kScorePages + row;
+        auto put = [&](int f, int half, float v) {  // the score of token tok + f and page e0 + 8 half
+          const int e = e0 + 8 * half;
+          if (f >= fit || tok + f >= lq || e >= now.pages) return;
+          const int limit = plan.causal ? now.g.lkv - lq + tok + f : now.g.lkv - 1;
+          const bool seen = (half ? ib : ia) >= 0 && (long long)e * pv.page_size <= limit;
+          p.scores[((long long)(now.g.q0 + tok + f) * pv.hkv + now.head) * p.row_pages + e] = seen ? v * p.scale : -INFINITY;
+        };
+        if constexpr (kHeads == 1) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const bool head_on = set * 8 + (2 * c + k) % heads < p.group;
-            best[0][k] = max_nan(best[0][k], head_on ? acc[k] : -INFINITY);
-            best[1][k] = max_nan(best[1][k], head_on ? acc[2 + k] : -INFINITY);
+            put(2 * c + k, 0, best[0][k]);
+            put(2 * c + k, 1, best[1][k]);
           }
-        }
-        for (int f = 0; f < fit && tok + f < g.lq; ++f) {
-          // the largest over the columns of token tok + f
-          float v0 = -INFINITY, v1 = -INFINITY;
+        } else if constexpr (kHeads != 0) {
+          // a token's columns are those of 1, 2 or 4 lanes; two of them write, or one both
+          float v0 = max_nan(best[0][0], best[0][1]), v1 = max_nan(best[1][0], best[1][1]);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const bool its = (2 * c + k) / heads == f;
-            v0 = max_nan(v0, its ? best[0][k] : -INFINITY);
-            v1 = max_nan(v1, its ? best[1][k] : -INFINITY);
+          for (int m = 1; m < kHeads / 2; m <<= 1) {
+            v0 = max_nan(v0, __shfl_xor_sync(kAll, v0, m));
+            v1 = max_nan(v1, __shfl_xor_sync(kAll, v1, m));
           }
-          v0 = max_nan(v0, __shfl_xor_sync(kAll, v0, 1));
-          v1 = max_nan(v1, __shfl_xor_sync(kAll, v1, 1));
-          v0 = max_nan(v0, __shfl_xor_sync(kAll, v0, 2));
-          v1 = max_nan(v1, __shfl_xor_sync(kAll, v1, 2));
-          const int e = e0 + row + (c & 1) * 8;
-          if (c < 2 && e < pages) {
-            const int limit = plan.causal ? g.lkv - g.lq + tok + f : g.lkv - 1;
-            const bool seen = (c ? ib : ia) >= 0 && (long long)e * pv.page_size <= limit;
-            p.scores[((long long)(g.q0 + tok + f) * pv.hkv + head) * p.row_pages + e] = seen ? (c ? v1 : v0) * p.scale : -INFINITY;
+          const int f = 2 * c / kHeads, at = c % (kHeads / 2);
+          if (kHeads == 2) {
+            put(f, 0, v0);
+            put(f, 1, v1);
+          } else if (at < 2) {
+            put(f, at, at ? v1 : v0);
+          }
+        } else {
+          for (int f = 0; f < fit && tok + f < lq; ++f) {
+            float v0 = -INFINITY, v1 = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const bool its = 2 * c + k >= f * heads && 2 * c + k < (f + 1) * heads;
+              v0 = max_nan(v0, its ? best[0][k] : -INFINITY);
+              v1 = max_nan(v1, its ? best[1][k] : -INFINITY);
+            }
+#pragma unroll
+            for (int m = 1; m < 4; m <<= 1) {
+              v0 = max_nan(v0, __shfl_xor_sync(kAll, v0, m));
+              v1 = max_nan(v1, __shfl_xor_sync(kAll, v1, m));
+            }
+            if (c < 2) put(f, c, c ? v1 : v0);
           }
         }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) best[0][k] = best[1][k] = -INFINITY;
       }
-    }
-    if (++head == pv.hkv) {
-      head = 0;
-      ++block;
-      fresh = true;
+      tok = tok2;
+      set = set2;
     }
   }
 }
@@ -325,7 +462,20 @@ __global__ void __launch_bounds__(kOne ? 32 : 1024) pick_kernel(const __grid_con
   };
   for (long long row = blockIdx.x; row < rows; row += gridDim.x) {
     const int t = int(row / pv.hkv);
-    const Geo g = load_geo(pv.geo, find_request(pv.geo, plan.batch, &Geo::q0, t));
+    const float* scores = p.scores + row * p.row_pages;
+    const int span = warps * 32 * kPickEach;
+    // this thread's scores of the run of positions that begins at `base`, as far as the row has room
+    auto read = [&](int base, float (&w)[kPickEach]) {
+#pragma unroll
+      for (int i = 0; i < kPickEach; ++i) {
+        const int pos = base + (warp * kPickEach + i) * 32 + lane;
+        w[i] = pos < p.row_pages ? __ldg(scores + pos) : 0.f;
+      }
+    };
+    float w0[kPickEach];
+    read(0, w0);  // on their way while the request is looked up
+    int r;
+    const Geo g = request_of(pv.geo, plan.batch, t, r);
     const int limit = plan.causal ? g.lkv - g.lq + (t - g.q0) : g.lkv - 1;  // the last key that the token sees
     const int n = limit < 0 ? 0 : pages_of(pv, limit + 1);
     const int32_t* ids = pv.kv_indices + g.kv0;
@@ -338,18 +488,21 @@ __global__ void __launch_bounds__(kOne ? 32 : 1024) pick_kernel(const __grid_con
     }
     const int f0 = p.sink, f1 = n - p.recent;  // positions that the scores decide about
     const uint32_t need = uint32_t(p.budget - p.sink - p.recent);
-    const float* scores = p.scores + row * p.row_pages;
-    const int span = warps * 32 * kPickEach;
-    // position i of this thread in the run that begins at `base`; no score maps to 0, which stands for none
-    auto fetch = [&](int base, uint32_t (&key)[kPickEach]) {
+    // no score maps to 0, which stands for none
+    auto keys_of = [&](int base, const float (&w)[kPickEach], uint32_t (&key)[kPickEach]) {
 #pragma unroll
       for (int i = 0; i < kPickEach; ++i) {
         const int pos = base + (warp * kPickEach + i) * 32 + lane;
-        key[i] = pos >= f0 && pos < f1 ? score_key(__ldg(scores + pos)) : 0u;
+        key[i] = pos >= f0 && pos < f1 ? score_key(w[i]) : 0u;
       }
     };
+    auto fetch = [&](int base, uint32_t (&key)[kPickEach]) {
+      float w[kPickEach];
+      read(base, w);
+      keys_of(base, w, key);
+    };
     uint32_t key[kPickEach];
-    fetch(0, key);
+    keys_of(0, w0, key);
     auto at_least = [&](uint32_t x) {
       uint32_t k = 0;
       if (n <= span) {
@@ -465,11 +618,12 @@ __global__ void __launch_bounds__(kPlanThreads) list_plan_kernel(const __grid_co
     return max(1, (pages + p.block_pages - 1) / p.block_pages);
   };
   // the line's length, and its part before the request of this CTA's first unit
-  int r = find_request(pv.geo, plan.batch, &Geo::q0, int(u0 / pv.hkv));
+  int r;
+  Geo g = request_of(pv.geo, plan.batch, int(u0 / pv.hkv), r);
   long long all = 0, before = 0;
   for (int k = threadIdx.x; k < plan.batch; k += kPlanThreads) {
-    const Geo g = load_geo(pv.geo, k);
-    const long long n = (long long)g.lq * pv.hkv * steps_of(g);
+    const Geo x = load_geo(pv.geo, k);
+    const long long n = (long long)x.lq * pv.hkv * steps_of(x);
     all += n;
     if (k < r) before += n;
   }
@@ -492,7 +646,6 @@ __global__ void __launch_bounds__(kPlanThreads) list_plan_kernel(const __grid_co
   const long long per = max((long long)p.least, (all + p.ctas - 1) / p.ctas);
   const int used = int((all + per - 1) / per);
 
-  Geo g = load_geo(pv.geo, r);
   int steps = steps_of(g);
   for (long long u = u0 + warp; u < u1; u += kPlanWarps) {
     const int t = int(u / pv.hkv), head = int(u - (long long)t * pv.hkv);
@@ -573,7 +726,7 @@ __global__ void __launch_bounds__(kPlanThreads) list_plan_kernel(const __grid_co
 
 int launch_bounds(const BoundsParams& p, int64_t tasks, bool fp8, int num_sms, cudaStream_t stream) {
   constexpr int kWarps = kBoundsThreads / 32;
-  const unsigned grid = unsigned(std::max<int64_t>(1, std::min<int64_t>((tasks + kWarps - 1) / kWarps, int64_t(num_sms) * 4)));
+  const unsigned grid = unsigned(std::max<int64_t>(1, std::min<int64_t>((tasks + kWarps - 1) / kWarps, int64_t(num_sms) * 2)));
   const cudaError_t e = fp8 ? launch_dependent(bounds_kernel<true>, grid, kBoundsThreads, 0, 1, stream, p)
                             : launch_dependent(bounds_kernel<false>, grid, kBoundsThreads, 0, 1, stream, p);
   return e == cudaSuccess ? FI_OK : record_cuda_error(e, "bounds_kernel launch");
@@ -581,8 +734,10 @@ int launch_bounds(const BoundsParams& p, int64_t tasks, bool fp8, int num_sms, c
 
 int launch_scores(const ScoreParams& p, int64_t tasks, int num_sms, cudaStream_t stream) {
   constexpr int kWarps = kScoreThreads / 32;
-  const unsigned grid = unsigned(std::max<int64_t>(1, std::min<int64_t>((tasks + kWarps - 1) / kWarps, int64_t(num_sms) * 4)));
-  const cudaError_t e = launch_dependent(scores_kernel, grid, kScoreThreads, 0, 1, stream, p);
+  const unsigned grid = unsigned(std::max<int64_t>(1, std::min<int64_t>((tasks + kWarps - 1) / kWarps, int64_t(num_sms) * kScoreCtas)));
+  const auto kernel = p.group >= 8 ? scores_kernel<8> : p.group == 4 ? scores_kernel<4> : p.group == 2 ? scores_kernel<2>
+                                                    : p.group == 1 ? scores_kernel<1> : scores_kernel<0>;
+  const cudaError_t e = launch_dependent(kernel, grid, kScoreThreads, 0, 1, stream, p);
   return e == cudaSuccess ? FI_OK : record_cuda_error(e, "scores_kernel launch");
 }
 

@@ -83,8 +83,9 @@ struct ScoreParams {
   const __nv_bfloat16* bounds;
   float* scores;  // [total_q][hkv][row_pages]
   int row_pages;
+  int most_batch;  // of the workspace
   int hqo, group;
-  float scale;    // includes k_scale
+  float scale;     // includes k_scale
 };
 int launch_scores(const ScoreParams& p, int64_t tasks, int num_sms, cudaStream_t stream);
 
