@@ -125,7 +125,7 @@ void set_geo(fi_workspace* ws, const int32_t* qo_indptr, const int32_t* kv_indpt
                       ws->variant.kv_dtype == FI_KV_DTYPE_E4M3 ? fi::kRowFormMostE4m3 : fi::kRowFormMostBf16,
                       causal != 0, window, &ws->geo);
   int32_t tree = 0;
-  ws->tree_ok = group <= fi::kTreeRows && fi::fill_tree(geo, batch, ws->hkv, group, ws->num_sms, &tree,
+  ws->tree_ok = group <= fi::kTreeRows && path != fi::kPathComposable && fi::fill_tree(geo, batch, ws->hkv, group, ws->num_sms, &tree,
                                                                  reinterpret_cast<int32_t*>(ws->hbuf + ws->off_tree));
   const fi::GeoHead head = {batch, qo_indptr[batch], int32_t(ws->geo.blocks), int32_t(ws->geo.work),
                             causal, window, tree, 0};

@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) scores_kernel(const
         const int e0 = now.block * kScorePages + row;
         auto put = [&](int f, int half, float v) {  // the score of token tok + f and page e0 + 8 half
           const int e = e0 + 8 * half;
-          if (f >= fit || tok + f >= lq || e >= now.pages) return;
+          if (f >= fit || tok + f >= lq || e >= now.pages || e >= p.row_pages) return;
           const int limit = plan.causal ? now.g.lkv - lq + tok + f : now.g.lkv - 1;
           const bool seen = (half ? ib : ia) >= 0 && (long long)e * pv.page_size <= limit;
           p.scores[((long long)(now.g.q0 + tok + f) * pv.hkv + now.head) * p.row_pages + e] = seen ? v * p.scale : -INFINITY;
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kOne ? 32 : 1024) pick_kernel(const __grid_con
     int r;
     const Geo g = request_of(pv.geo, plan.batch, t, r);
     const int limit = plan.causal ? g.lkv - g.lq + (t - g.q0) : g.lkv - 1;  // the last key that the token sees
-    const int n = limit < 0 ? 0 : pages_of(pv, limit + 1);
+    const int n = limit < 0 ? 0 : p.row_pages > 0 ? min(pages_of(pv, limit + 1), p.row_pages) : 0;
     const int32_t* ids = pv.kv_indices + g.kv0;
     int32_t* out = p.selected + row * p.budget;
     const int kept = min(n, p.budget);

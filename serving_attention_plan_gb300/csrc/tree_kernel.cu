@@ -911,32 +911,32 @@ __global__ void __launch_bounds__(Shape<kFp8>::kThreads, 1)
 // latency counts: a warp takes up to four rows at a time, eight lanes a row for the states' sums, then all lanes, four dims
 // each, for two rows' states side by side.  (A row a warp: 30 us behind 160 us of 256-row units.)
 constexpr int kJoinThreads = 256;
-constexpr int kJoinCtas = 8;
+constexpr int kJoinCtas = 4;
 constexpr int kJoinRows = 4;
 constexpr int kJoinAhead = 4;
 
 __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid_constant__ TreeParams p, int grid) {
-  // (the plan was there before the kernel whose states are waited for below)
+  // The plan was there before the kernel whose states this one joins, so it is read before the wait.  Every CTA waits, those
+  // with nothing to join too: a grid that ended before the one it depends on would let its own followers start.
   const GeoHead plan = load_head(p.pv.geo);
   const Line line(plan.tree, grid);
   const int cut = int(blockIdx.x) / kJoinCtas + 1, part = int(blockIdx.x) % kJoinCtas;
-  if (cut >= line.ctas) return;
   const int lane = threadIdx.x & 31, warp = int(threadIdx.x >> 5);
   const int x = cut * line.per;
-  const Geo g = load_geo(p.pv.geo, __ldg(p.starts + cut));
+  const Geo g = load_geo(p.pv.geo, cut < line.ctas ? __ldg(p.starts + cut) : 0);
   const int tokens = 2 * p.tile_tokens;
   const int tiles = max(1, (g.lkv + kKeys - 1) / kKeys), sets = (g.lq + tokens - 1) / tokens;
   const int unit = (x - g.tree0) / tiles, a = g.tree0 + unit * tiles;
-  if (a == x) return;  // nothing is cut here
   const int begins = a / line.per, n = (a + tiles - 1) / line.per - begins + 1;  // the CTA with the unit's first piece, pieces
   const long long first = 2ll * begins;
-  const int head = unit / sets, q0 = g.q0 + unit % sets * tokens, nq = min(tokens, g.lq - unit % sets * tokens);
+  const int head = unit / max(1, sets), set = unit - head * sets, q0 = g.q0 + set * tokens, nq = min(tokens, g.lq - set * tokens);
   // row k of the unit lies at 128 h + x of a slot, for row x of its row tile h
   const int tile_rows = p.tile_tokens * p.group, rows = nq * p.group;
   auto place = [&](int k) { return first * 2 * kRows + (k < tile_rows ? k : kRows + k - tile_rows); };
-  const int warps = (n - 1) * kJoinCtas * (kJoinThreads / 32);
+  const int warps = max(1, n - 1) * kJoinCtas * (kJoinThreads / 32);
   const int some = min(kJoinRows, (rows + warps - 1) / warps);  // rows at a time
   wait_prior_grid();
+  if (cut >= line.ctas || a == x) return;  // nothing is cut here
   for (int k0 = (((cut - 1 - begins) * kJoinCtas + part) * (kJoinThreads / 32) + warp) * some; k0 < rows; k0 += warps * some) {
     // eight lanes a row: the largest of its states' LSEs and the sum of their weights
     const int mine = min(k0 + min(lane >> 3, some - 1), rows - 1);

@@ -165,6 +165,49 @@ def test_tree_of_a_chain_is_causal_attention():
     assert (lse - rl).abs().max() <= 2.0 ** -12 and (o.float() - ro.float()).abs().max() <= 0.04
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_tree_rows_that_are_not_finite(dtype):
+    """A NaN or infinity in q shows in its own row alone."""
+    torch = torch_mod()
+    b = batch_of([5, 40], [300, 700], 8, 2, 16, False, seed=12)
+    k, v = (pool(b, x, dtype, "HND", 1.0)[0] for x in ("k_pages", "v_pages"))
+    ws = workspace(b, dtype=dtype)
+    q, (o, lse), (ro, rl) = bf16(b.q), outputs(b), outputs(b)
+    mask = dev(random_mask(np.random.default_rng(0), b, "tree"))
+    ws.tree_run(q, k, v, mask, ro, rl)
+    bad = q.clone()
+    bad[3, 1, 7], bad[20, 6, 100] = float("nan"), float("inf")
+    ws.tree_run(bad, k, v, mask, o, lse)
+    torch.cuda.synchronize()
+    assert torch.isnan(lse[3, 1]) and torch.isnan(o[3, 1]).all()
+    assert not torch.isfinite(lse[20, 6]) and not torch.isfinite(o[20, 6]).any()
+    rest = torch.ones(45, 8, dtype=torch.bool, device="cuda")
+    rest[3, 1] = rest[20, 6] = False
+    assert torch.equal(lse[rest], rl[rest]) and torch.equal(o[rest], ro[rest])
+
+
+def test_tree_then_a_launch_that_reads_its_output():
+    """Back to back, the second call on the first's output: where no unit is cut (the joining launch has nothing to do), where some are."""
+    torch = torch_mod()
+    for lq, lkv, sms in (([20] * 300, [256] * 300, 0), ([30, 60, 9] * 30, [5000, 900, 70] * 30, 0)):
+        b = W.make_paged_batch(np.random.default_rng(3), "chain", lq, lkv, 8, 2, 16, False)
+        ws, ws2 = workspace(b, num_sms=sms), workspace(b, num_sms=sms)
+        q, k, v = bf16(b.q), bf16(b.k_pages), bf16(b.v_pages)
+        mask = dev(random_mask(np.random.default_rng(1), b, "tree"))
+        (o1, l1), (o2, l2), (r1, s1), (r2, s2) = (outputs(b) for _ in range(4))
+        for turn in range(5):
+            ws.tree_run(q, k, v, mask, r1, s1)
+            torch.cuda.synchronize()
+            ws.tree_run(r1, k, v, mask, r2, s2)
+            torch.cuda.synchronize()
+            o1.fill_(float("nan"))
+            ws.tree_run(q, k, v, mask, o1, l1)
+            ws2.tree_run(o1, k, v, mask, o2, l2)
+            torch.cuda.synchronize()
+            assert torch.equal(o1, r1) and torch.equal(o2, r2) and torch.equal(l2, s2)
+        assert ws.get_error() == 0 and ws2.get_error() == 0
+
+
 def capture(call):
     torch = torch_mod()
     s = torch.cuda.Stream()
