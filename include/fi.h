@@ -449,9 +449,10 @@ int fi_compact(fi_workspace* ws, const int32_t* kept, int32_t budget, void* k_pa
  *
  * Query token t sees key j of its request when j < l_kv - l_q (the context), or when bit u = j - (l_kv - l_q) of its mask is
  * set; the plan's causal flag is not looked at.  A token that shall see itself needs its own bit.  Scale, soft-cap and e4m3
- * scales as for fi_run; the soft-cap's tanh is as exact as fi_key_weights's.  A row that sees nothing gets o = 0, lse = -inf.  A
- * plain K of any value in a key that a row does not see (NaN, infinite) does not reach the row; a V that is not finite
- * reaches every row of the request.
+ * scales as for fi_run; the soft-cap's tanh is as exact as fi_key_weights's.  A row that sees nothing gets o = 0, lse = -inf.
+ * What K holds in a key that a row does not see (NaN, infinities) does not reach the row; a V that is not finite
+ * reaches every row of the request.  With e4m3 pages a row of q is taken as a sum of two e4m3 numbers times a power of two:
+ * exact for elements above 2^-9 of its largest, right to 2^-17 of the largest for the others; a row with an infinity or NaN gives NaN.
  *
  *   mask         DEVICE int32 [total_q, mask_words]: bit u % 32 of word u / 32; bits from l_q on are ignored
  *   mask_words   at least ceil(l_q / 32) of the longest request (INVALID_ARG; in a replay: missing words count as zeros)
@@ -500,7 +501,7 @@ int fi_page_bounds(fi_workspace* ws, const void* k_pages, int num_pages, int32_t
  *
  *   bounds      as fi_page_bounds writes it
  *   scores      DEVICE float32 [total_q, num_kv_heads, row_pages]; entries from the request's page count on keep what they hold
- *   row_pages   at least the pages of the longest request (INVALID_ARG; a replay's plan must keep to it, unchecked)
+ *   row_pages   at least the pages of the longest request (INVALID_ARG; in a replay, further pages get no score)
  * UNSUPPORTED: composable plans, a sliding window.  Errors: NO_PLAN, INVALID_ARG, UNSUPPORTED, CUDA.
  */
 int fi_score_pages(fi_workspace* ws, const void* q, const void* bounds, int num_pages, float* scores, int32_t row_pages,
@@ -513,7 +514,7 @@ int fi_score_pages(fi_workspace* ws, const void* q, const void* bounds, int num_
  * the last `recent` and, of the others, those with the largest scores; equal scores go to the lowest place in the list, NaN
  * counts as the largest.
  *
- *   scores     as for fi_score_pages
+ *   scores     as for fi_score_pages; a replay looks at no more than row_pages pages of a request
  *   selected   DEVICE int32 [total_q, num_kv_heads, budget] (written): page ids in the order of the request's list, then -1
  * sink, recent >= 0, budget >= 1, sink + recent <= budget (else INVALID_ARG).
  * UNSUPPORTED: composable plans, a sliding window.  Errors: NO_PLAN, INVALID_ARG, UNSUPPORTED, CUDA.
