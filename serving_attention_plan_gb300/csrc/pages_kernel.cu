@@ -13,6 +13,10 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 
+// The kernels below read the plan before wait_prior_grid: it was there before the kernel that they wait for, which a copy of the plan
+// cannot lie behind.  What an earlier kernel may have written is read behind the wait, and every CTA waits, those without
+// work too: a grid that ended before the one it depends on would let its own followers start.
+
 // Last request r whose value of(r) (non-decreasing) is <= x, of(0) <= x; a whole warp, 32 probes a round.
 template <typename F>
 __device__ __forceinline__ int last_at_most(int n, int x, F of) {
@@ -91,17 +95,16 @@ struct BoundsStep {
 template <bool kFp8>
 __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const __grid_constant__ BoundsParams p) {
   constexpr int kLanes = kFp8 ? 8 : 16, kSide = 32 / kLanes, kWords = kFp8 ? 8 : 4, kRowsStep = kBoundsAhead * kSide;
-  wait_prior_grid();
   const PageView& pv = p.pv;
   const GeoHead plan = load_head(pv.geo);
-  if (plan.batch == 0) return;
+  if (plan.batch == 0) return wait_prior_grid();
   const int lane = threadIdx.x & 31, sub = lane % kLanes, side = lane / kLanes;
   // a task is a page entry (or, for new keys, a query token) and a head; heads of a page are neighbours in memory
   const long long units = p.new_keys ? plan.total_q : __ldg(&pv.geo[plan.batch].kv0);
   const long long tasks = units * pv.hkv, warps = (long long)gridDim.x * (kBoundsThreads / 32);
   const long long me = (long long)blockIdx.x * (kBoundsThreads / 32) + (threadIdx.x >> 5);
   const long long t0 = tasks * me / warps, t1 = tasks * (me + 1) / warps;
-  if (t0 >= t1) return;
+  if (t0 >= t1) return wait_prior_grid();
   int unit = int(t0 / pv.hkv);
   long long task = t0;
   int r = p.new_keys ? 0 : find_request(pv.geo, plan.batch, &Geo::kv0, unit);
@@ -155,6 +158,7 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const __grid_con
   uint4 x[2][kBoundsAhead];
   uint32_t lo[kWords], hi[kWords];
   look_up();
+  wait_prior_grid();
   fetch(x[0]);
   bool more = true;
   auto turn = [&](uint4 (&now)[kBoundsAhead], uint4 (&ahead)[kBoundsAhead]) {
@@ -239,12 +243,11 @@ template <int kHeads>
 __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) scores_kernel(const __grid_constant__ ScoreParams p) {
   __shared__ int firsts[kScoreList];
   const int lane = threadIdx.x & 31, row = lane >> 2, c = lane & 3;
-  wait_prior_grid();
   const PageView& pv = p.pv;
   const Geo* geo = pv.geo;
   for (int i = threadIdx.x; i < min(kScoreList, p.most_batch); i += kScoreThreads) firsts[i] = __ldg(&geo[i].kv0);
   const GeoHead plan = load_head(geo);
-  if (plan.batch == 0) return;
+  if (plan.batch == 0) return wait_prior_grid();
   const int entries = __ldg(&geo[plan.batch].kv0);
   __syncthreads();
   // The line: for every request and KV head a place for each block.  Request r's begin at (its first entry) / 16 + r blocks,
@@ -254,7 +257,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) scores_kernel(const
   const long long me = (long long)blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5);
   long long task = tasks * me / warps;
   const long long t1 = tasks * (me + 1) / warps;
-  if (task >= t1) return;
+  if (task >= t1) return wait_prior_grid();
   const int heads = kHeads ? kHeads : p.group;
   const int fit = 8 / heads;                               // tokens of a set of eight columns
   const int sets = kHeads == 8 ? (p.group + 7) / 8 : 1;    // sets of a token
@@ -298,6 +301,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) scores_kernel(const
     next.head = in / next.room;
     next.block = in - next.head * next.room;
     look_up(ids_at(next.block));
+    wait_prior_grid();
     fetch(0);
     fetch(4);
   }
@@ -428,11 +432,13 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) scores_kernel(const
 // Of the n pages that a (token, KV head) row sees, the first `sink`, the last `recent` and the best of the rest, budget in
 // all.  The threshold, the K-th largest score, is found bit by bit from the top: scores as integers of the same order, and
 // at each step a count of those at or above a candidate.  A count costs a compare and an add for each score that a thread
-// holds in registers, a warp sum and, with more than one warp, a barrier; it ends once exactly K are counted.  No
-// atomics: nothing depends on scheduling.  A warp holds a run of positions, so the chosen come out in order by counting.  Rows longer than the
-// CTA holds are read again for each count.
+// holds in registers, a warp sum and, with more than one warp, a barrier; it ends once exactly K are counted.  Once at most
+// 512 scores are left to decide about, one warp goes on with them alone (14.8 -> 12.8 us for 32 rows of 8192 pages).
+// Nothing depends on scheduling.  A warp holds a run of positions, so the chosen come out in order by counting.  Rows longer than the CTA
+// holds are read again for each count.
 constexpr int kPickEach = 16;  // scores of a thread
 constexpr int kPickMostWarps = 32;
+constexpr uint32_t kPickFew = 32 * kPickEach;
 
 // Order-preserving map; -0 counts as 0 and every NaN as the largest.
 __device__ __forceinline__ uint32_t score_key(float w) {
@@ -445,11 +451,15 @@ template <bool kOne>
 __global__ void __launch_bounds__(kOne ? 32 : 1024) pick_kernel(const __grid_constant__ PickParams p) {
   __shared__ uint32_t counts[2][kPickMostWarps];
   __shared__ uint2 runs[kPickMostWarps];
-  wait_prior_grid();
+  __shared__ uint32_t list[kOne ? 1 : kPickFew], list_end;
   const PageView& pv = p.pv;
   const GeoHead plan = load_head(pv.geo);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kOne ? 1 : int(blockDim.x >> 5);
   const long long rows = (long long)plan.total_q * pv.hkv;
+  Geo g = {};
+  int r;
+  if (blockIdx.x < rows) g = request_of(pv.geo, plan.batch, int(blockIdx.x / pv.hkv), r);
+  wait_prior_grid();
   int turn = 0;
   auto total = [&](uint32_t v) {  // over the CTA; every thread gets it
     v = __reduce_add_sync(kAll, v);
@@ -474,8 +484,7 @@ __global__ void __launch_bounds__(kOne ? 32 : 1024) pick_kernel(const __grid_con
     };
     float w0[kPickEach];
     read(0, w0);  // on their way while the request is looked up
-    int r;
-    const Geo g = request_of(pv.geo, plan.batch, t, r);
+    if (row != blockIdx.x) g = request_of(pv.geo, plan.batch, t, r);
     const int limit = plan.causal ? g.lkv - g.lq + (t - g.q0) : g.lkv - 1;  // the last key that the token sees
     const int n = limit < 0 ? 0 : p.row_pages > 0 ? min(pages_of(pv, limit + 1), p.row_pages) : 0;
     const int32_t* ids = pv.kv_indices + g.kv0;
@@ -521,15 +530,71 @@ __global__ void __launch_bounds__(kOne ? 32 : 1024) pick_kernel(const __grid_con
     uint32_t limit_key = 0;  // the largest x with at least `need` scores at or above it
     bool exact = need == 0;
     if (exact) limit_key = 0xffffffffu;
-    for (int bit = 31; bit >= 0 && !exact; --bit) {
+    uint32_t from = uint32_t(n), above = 0;  // scores at or above limit_key (at most), and at or above limit_key + 2^bit
+    int bit = 31;
+    for (; bit >= 0 && !exact; --bit) {
+      if (!kOne && n <= span && from - above <= kPickFew) break;
       const uint32_t x = limit_key | (1u << bit);
       const uint32_t k = at_least(x);
-      if (k >= need) limit_key = x;
+      if (k >= need) {
+        limit_key = x;
+        from = k;
+      } else {
+        above = k;
+      }
       exact = k == need;
     }
     // scores above the limit stay, of those at it the first few; if exactly `need` are at or above it, all of them
     uint32_t ties = exact && need != 0 ? 0xffffffffu : 0u;
-    if (!exact) ties = need - (limit_key == 0xffffffffu ? 0u : at_least(limit_key + 1));
+    if (!kOne && !exact && bit >= 0) {
+      // the few that the remaining bits decide about, to one warp
+      if (threadIdx.x == 0) list_end = 0;
+      __syncthreads();
+      const uint32_t low = limit_key, size = bit == 31 ? 0u : 2u << bit;  // low .. low + size - 1 (31: all)
+      auto in = [&](uint32_t v) { return v != 0 && v >= low && (bit == 31 || v - low < size); };
+      uint32_t mine = 0;
+#pragma unroll
+      for (int i = 0; i < kPickEach; ++i) mine += in(key[i]);
+      uint32_t to = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_up_sync(kAll, to, o);
+        to += lane >= o ? v : 0u;
+      }
+      uint32_t base = 0;
+      if (lane == 31) base = atomicAdd(&list_end, to);  // (their order does not matter, only how many lie where)
+      to += __shfl_sync(kAll, base, 31) - mine;
+#pragma unroll
+      for (int i = 0; i < kPickEach; ++i)
+        if (in(key[i])) list[to++] = key[i];
+      __syncthreads();
+      if (warp == 0) {
+        uint32_t some[kPickEach];
+#pragma unroll
+        for (int i = 0; i < kPickEach; ++i) some[i] = uint32_t(32 * i + lane) < list_end ? list[32 * i + lane] : 0u;
+        auto count = [&](uint32_t x) {
+          uint32_t k = 0;
+#pragma unroll
+          for (int i = 0; i < kPickEach; ++i) k += some[i] >= x;
+          return __reduce_add_sync(kAll, k);
+        };
+        const uint32_t left = need - above;
+        bool done = false;
+        for (; bit >= 0 && !done; --bit) {
+          const uint32_t x = limit_key | (1u << bit);
+          const uint32_t k = count(x);
+          if (k >= left) limit_key = x;
+          done = k == left;
+        }
+        ties = done ? 0xffffffffu : left - (limit_key == 0xffffffffu ? 0u : count(limit_key + 1));
+        if (lane == 0) runs[0] = make_uint2(limit_key, ties);
+      }
+      __syncthreads();
+      limit_key = runs[0].x;
+      ties = runs[0].y;
+    } else if (!exact) {
+      ties = need - (limit_key == 0xffffffffu ? 0u : at_least(limit_key + 1));
+    }
     uint32_t before = 0, ties_before = 0;  // chosen positions and ties in the runs before
     for (int base = 0; base < n; base += span) {
       if (base > 0) fetch(base, key);
@@ -595,16 +660,16 @@ __device__ __forceinline__ void put_unit(int32_t* units, int at, int slot, int n
 
 __global__ void __launch_bounds__(kPlanThreads) list_plan_kernel(const __grid_constant__ ListPlanParams p) {
   __shared__ long long sums[2][kPlanWarps];
-  wait_prior_grid();
   const PageView& pv = p.pv;
   const GeoHead plan = load_head(pv.geo);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long units = (long long)plan.total_q * pv.hkv;
-  if (blockIdx.x == 0 && threadIdx.x == 0) p.header[H_NUM_UNITS] = p.ctas;
   // (a replay may bring more tokens than the list numbers have room for)
   const bool room = units * p.budget <= INT32_MAX;
   if (units == 0 || !room) {
+    wait_prior_grid();
     if (blockIdx.x == 0) {
+      if (threadIdx.x == 0) p.header[H_NUM_UNITS] = p.ctas;
       for (int c = threadIdx.x; c <= p.ctas; c += kPlanThreads) p.cta_indptr[c] = 0;
       for (int c = threadIdx.x; c < p.ctas; c += kPlanThreads) put_unit(p.units, c, 0, 0, 0, 0, 0);
       if (threadIdx.x == 0 && !room) atomicOr(pv.err, FI_DEVERR_KEPT);
@@ -612,7 +677,7 @@ __global__ void __launch_bounds__(kPlanThreads) list_plan_kernel(const __grid_co
     return;
   }
   const long long u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
-  if (u0 >= u1) return;
+  if (u0 >= u1) return wait_prior_grid();
   auto steps_of = [&](const Geo& g) {
     const int pages = min(pages_of(pv, g.lkv), p.budget);
     return max(1, (pages + p.block_pages - 1) / p.block_pages);
@@ -647,6 +712,8 @@ __global__ void __launch_bounds__(kPlanThreads) list_plan_kernel(const __grid_co
   const int used = int((all + per - 1) / per);
 
   int steps = steps_of(g);
+  wait_prior_grid();
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.header[H_NUM_UNITS] = p.ctas;
   for (long long u = u0 + warp; u < u1; u += kPlanWarps) {
     const int t = int(u / pv.hkv), head = int(u - (long long)t * pv.hkv);
     while (t >= g.q0 + g.lq) {

@@ -867,11 +867,11 @@ __global__ void __launch_bounds__(Shape<kFp8>::kThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  wait_prior_grid();
   const uint32_t tmem = sm.tmem_base;
   const GeoHead plan = load_head(p.pv.geo);
   const int start = __ldg(p.starts + blockIdx.x);
   const Line line(plan.tree, int(gridDim.x));
+  wait_prior_grid();  // (the plan was there before the kernel that this one waits for)
   if ((tmem & 0xFFFFu) + kTmemCols > 512u || (smem_u32(smem_raw) & 1023u) != 0) {
     if (threadIdx.x == 0) atomicOr(p.pv.err, FI_DEVERR_TMEM);
   } else if (int(blockIdx.x) < line.ctas) {
@@ -908,11 +908,10 @@ __global__ void __launch_bounds__(Shape<kFp8>::kThreads, 1)
 // ---- units that were cut -------------------------------------------------------------------------------
 // kJoinCtas CTAs for each place where the line was cut; those of one unit's cuts share its rows and join their states in
 // the pieces' order.  What a row has to read, n states of 516 bytes, lies in L2, and most units have two or three pieces, so
-// latency counts: a warp takes up to four rows at a time, eight lanes a row for the states' sums, then all lanes, four dims
-// each, for two rows' states side by side.  (A row a warp: 30 us behind 160 us of 256-row units.)
+// latency counts: a warp takes two rows at a time, whose LSEs (sixteen lanes a row) and first states (all lanes, four dims each) are
+// asked for at once.  (A row a warp: 30 us behind 160 us of 256-row units.)
 constexpr int kJoinThreads = 256;
 constexpr int kJoinCtas = 4;
-constexpr int kJoinRows = 4;
 constexpr int kJoinAhead = 4;
 
 __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid_constant__ TreeParams p, int grid) {
@@ -934,60 +933,60 @@ __global__ void __launch_bounds__(kJoinThreads, 4) tree_join_kernel(const __grid
   const int tile_rows = p.tile_tokens * p.group, rows = nq * p.group;
   auto place = [&](int k) { return first * 2 * kRows + (k < tile_rows ? k : kRows + k - tile_rows); };
   const int warps = max(1, n - 1) * kJoinCtas * (kJoinThreads / 32);
-  const int some = min(kJoinRows, (rows + warps - 1) / warps);  // rows at a time
   wait_prior_grid();
   if (cut >= line.ctas || a == x) return;  // nothing is cut here
-  for (int k0 = (((cut - 1 - begins) * kJoinCtas + part) * (kJoinThreads / 32) + warp) * some; k0 < rows; k0 += warps * some) {
-    // eight lanes a row: the largest of its states' LSEs and the sum of their weights
-    const int mine = min(k0 + min(lane >> 3, some - 1), rows - 1);
-    const float* lses = p.part_lse + place(mine);
-    float m = -INFINITY, sum = 0.f;
-    for (int i = lane & 7; i < n; i += 8) m = fmaxf(m, __ldcg(lses + (long long)i * 2 * kRows));
+  for (int k0 = 2 * (((cut - 1 - begins) * kJoinCtas + part) * (kJoinThreads / 32) + warp); k0 < rows; k0 += 2 * warps) {
+    const long long at[2] = {place(k0), place(min(k0 + 1, rows - 1))};
+    // sixteen lanes a row: lane (row, i) holds the LSE of state i, then its weight
+    const float* lses = p.part_lse + (lane < 16 ? at[0] : at[1]);
+    auto lse_of = [&](int i) { return i < n ? __ldcg(lses + (long long)i * 2 * kRows) : -INFINITY; };
+    auto states = [&](int i0, float4 (&v)[2][kJoinAhead]) {  // states i0 .. of both rows, four dims a lane
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int e = 0; e < kJoinAhead; ++e)
+          v[r][e] = i0 + e < n ? __ldcg(reinterpret_cast<const float4*>(p.part_o + (at[r] + (long long)(i0 + e) * 2 * kRows) * kHeadDim) + lane)
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    const float own = lse_of(lane & 15);
+    float4 v[2][kJoinAhead];
+    states(0, v);  // the first states' numbers come with their LSEs
+    float m = own;
+    for (int i = 16 + (lane & 15); i < n; i += 16) m = fmaxf(m, lse_of(i));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
     m = m == -INFINITY ? 0.f : m;
-    for (int i = lane & 7; i < n; i += 8) sum += fast_exp2(__ldcg(lses + (long long)i * 2 * kRows) - m);
+    float sum = fast_exp2(own - m);
+    for (int i = 16 + (lane & 15); i < n; i += 16) sum += fast_exp2(lse_of(i) - m);
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (no state of the row has seen a key)
-    if ((lane & 7) == 0 && (lane >> 3) < some && k0 + (lane >> 3) < rows)
-      p.lse[(long long)(q0 + mine / p.group) * p.hqo + head * p.group + mine % p.group] = sum == 0.f ? -INFINITY : (m + fast_log2(sum)) * kLn2;
-#pragma unroll 1
-    for (int r0 = 0; r0 < some && k0 + r0 < rows; r0 += 2) {
-      float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-      const long long at[2] = {place(k0 + r0), place(min(k0 + r0 + 1, rows - 1))};
-      for (int i0 = 0; i0 < n; i0 += 8) {
-        // lane (row, i & 7) holds the weight of state i0 + (i & 7) of its row
-        const int i = i0 + (lane & 7);
-        const float w = i < n ? fast_exp2(__ldcg(lses + (long long)i * 2 * kRows) - m) * inv : 0.f;
-        for (int j = 0; j < 8 && i0 + j < n; j += kJoinAhead) {
-          float4 v[2][kJoinAhead];
+    if ((lane & 15) == 0 && k0 + (lane >> 4) < rows) {
+      const int k = k0 + (lane >> 4);
+      p.lse[(long long)(q0 + k / p.group) * p.hqo + head * p.group + k % p.group] = sum == 0.f ? -INFINITY : (m + fast_log2(sum)) * kLn2;
+    }
+    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int i0 = 0; i0 < n; i0 += kJoinAhead) {
+      if (i0 > 0) states(i0, v);
+      const float w = (i0 < 16 ? fast_exp2(own - m) : fast_exp2(lse_of((i0 & ~15) + (lane & 15)) - m)) * inv;
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int e = 0; e < kJoinAhead; ++e)
-              v[r][e] = i0 + j + e < n ? __ldcg(reinterpret_cast<const float4*>(p.part_o + (at[r] + (long long)(i0 + j + e) * 2 * kRows) * kHeadDim) + lane)
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int e = 0; e < kJoinAhead; ++e) {
-              const float we = __shfl_sync(kAll, w, 8 * (r0 + r) + j + e);
-              if (we == 0.f) continue;
-              acc[r].x = fmaf(we, v[r][e].x, acc[r].x);
-              acc[r].y = fmaf(we, v[r][e].y, acc[r].y);
-              acc[r].z = fmaf(we, v[r][e].z, acc[r].z);
-              acc[r].w = fmaf(we, v[r][e].w, acc[r].w);
-            }
+        for (int e = 0; e < kJoinAhead; ++e) {
+          const float we = __shfl_sync(kAll, w, 16 * r + ((i0 + e) & 15));
+          if (we == 0.f) continue;
+          acc[r].x = fmaf(we, v[r][e].x, acc[r].x);
+          acc[r].y = fmaf(we, v[r][e].y, acc[r].y);
+          acc[r].z = fmaf(we, v[r][e].z, acc[r].z);
+          acc[r].w = fmaf(we, v[r][e].w, acc[r].w);
         }
-      }
+    }
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int k = k0 + r0 + r;
-        if (k >= rows || r0 + r >= some) continue;
-        const long long orow = (long long)(q0 + k / p.group) * p.hqo + head * p.group + k % p.group;
-        *reinterpret_cast<uint2*>(p.o + orow * kHeadDim + 4 * lane) = make_uint2(f2_to_bf16x2(acc[r].x, acc[r].y), f2_to_bf16x2(acc[r].z, acc[r].w));
-      }
+    for (int r = 0; r < 2; ++r) {
+      const int k = k0 + r;
+      if (k >= rows) continue;
+      const long long orow = (long long)(q0 + k / p.group) * p.hqo + head * p.group + k % p.group;
+      *reinterpret_cast<uint2*>(p.o + orow * kHeadDim + 4 * lane) = make_uint2(f2_to_bf16x2(acc[r].x, acc[r].y), f2_to_bf16x2(acc[r].z, acc[r].w));
     }
   }
 }
@@ -1002,9 +1001,9 @@ template <bool kFp8>
 __global__ void __launch_bounds__(128) commit_kernel(const __grid_constant__ CommitParams p) {
   constexpr int kElem = kFp8 ? 1 : 2, kLanes = kHeadDim * kElem / 16;  // lanes of a row
   constexpr int kSide = 32 / kLanes, kSteps = kCommitRows / kSide;     // rows at a time
-  wait_prior_grid();
   const PageView& pv = p.pv;
   const int batch = load_head(pv.geo).batch;
+  wait_prior_grid();
   const int lane = threadIdx.x & 31;
   const long long tasks = (long long)batch * pv.hkv;
   for (long long task = (long long)blockIdx.x * 4 + (threadIdx.x >> 5); task < tasks; task += (long long)gridDim.x * 4) {

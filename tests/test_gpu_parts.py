@@ -488,6 +488,10 @@ SELECT = [
     ([2, 1], [700, 9], 2, 1, True, 0, 5, 2 ** 20, "normal"),     # all pages
     ([1], [40_000], 1, 1, False, 4, 16, 10_000, "ties"),         # longer than the threads hold
     ([3], [20_000], 2, 1, True, 1, 0, 64, "special"),
+    ([3], [16_000], 2, 1, True, 1, 0, 64, "special"),            # several warps: the last bits' few to one of them
+    ([1, 2], [9000, 300], 2, 1, False, 0, 0, 1, "normal"),
+    ([1], [6000], 1, 1, False, 2, 8, 2500, "near"),
+    ([1, 1], [900, 513], 1, 1, False, 0, 0, 512, "near"),
 ]
 
 
@@ -505,6 +509,8 @@ def test_select(case):
         x = np.round(x)
     elif kind == "equal":
         x[:] = -3.5
+    elif kind == "near":
+        x = 1 + np.round(x) * np.float32(2.0 ** -23)
     elif kind == "special":
         x[rng.random(x.shape) < 0.3] = -np.inf
         x[rng.random(x.shape) < 0.01] = np.nan
