@@ -774,3 +774,104 @@ def test_speculative_steps(dtype):
         plan(ws, batch((path >= 0).sum(1), lens))
         ws.page_bounds(k, bounds, new_keys=True)
         assert ws.get_error() == 0
+
+
+# ---- where calls can get in each other's way -----------------------------------------------------------
+
+
+def every_call(b, ws, q, k, v, mask, path, stream=None):
+    """The outputs of each operator on the batch, the pools' changes last (k and v are the call's own)."""
+    torch = torch_mod()
+    hk, row = b.num_kv_heads, int(np.diff(b.kv_indptr).max())
+    (o, lse), (po, plse) = outputs(b), outputs(b)
+    bounds = torch.empty(k.shape[0], hk, 2, 128, dtype=torch.bfloat16, device="cuda")
+    scores = torch.full((b.total_q, hk, row), 3.0, device="cuda")
+    sel = torch.empty(b.total_q, hk, 5, dtype=torch.int32, device="cuda")
+    ws.tree_run(q, k, v, mask, o, lse, stream=stream)
+    ws.page_bounds(k, bounds, stream=stream)
+    ws.score_pages(q, bounds, scores, stream=stream)
+    ws.select_pages(scores, sel, recent=1, stream=stream)
+    ws.run_pages(q, k, v, sel, po, plse, stream=stream)
+    ws.tree_commit(path, k, v, stream=stream)
+    return o, lse, scores, sel, po, plse, bounds
+
+
+def case_of(seed, lq, lkv, dtype="bf16"):
+    b = batch_of(lq, lkv, 8, 2, 16, False, seed=seed)
+    mask = dev(random_mask(np.random.default_rng(seed), b, "tree"))
+    path = dev(np.array([[i for i in range(1, n, 2)][:6] + [-1] * (6 - len(range(1, n, 2)[:6])) for n in lq], np.int32))
+    return b, bf16(b.q), bf16(b.k_pages), bf16(b.v_pages), mask, path
+
+
+def same(x, y):
+    return all(torch_mod().equal(a, c) for a, c in zip(x, y))
+
+
+def test_far_pages():
+    """Pages behind 2^32 bytes and 2^31 elements of a pool: bit for bit what the same pages give at its beginning."""
+    torch = torch_mod()
+    b = batch_of([20, 1, 40], [400, 33, 900], 32, 8, 16, False, seed=4)
+    far = 140_000
+    mask = dev(random_mask(np.random.default_rng(1), b, "tree"))
+    path = dev(np.array([[3, 7, 19, -1], [-1, -1, -1, -1], [1, 2, 30, 39]], np.int32))
+    q, k, v = bf16(b.q), bf16(b.k_pages), bf16(b.v_pages)
+    big = [torch.empty(far + x.shape[0], *x.shape[1:], dtype=x.dtype, device="cuda") for x in (k, v)]
+    for x, near in zip(big, (k, v)):
+        x[far:] = near
+    c = dataclasses.replace(b, kv_indices=(b.kv_indices + far).astype(np.int32))
+    near = every_call(b, workspace(b), q, k, v, mask, path)
+    ws = workspace(c)
+    got = every_call(c, ws, q, *big, mask, path)
+    torch.cuda.synchronize()
+    assert ws.get_error() == 0
+    used = dev(np.unique(b.kv_indices)).long()
+    assert same(near[:3], got[:3]) and same(near[4:6], got[4:6])
+    assert torch.equal(torch.where(near[3] >= 0, near[3] + far, near[3]), got[3])
+    assert torch.equal(near[6][used], got[6][used + far])
+    assert torch.equal(big[0][far:], k) and torch.equal(big[1][far:], v)
+
+
+def test_two_streams_at_once():
+    """Two workspaces on two streams, their launches side by side, against the same calls alone."""
+    torch = torch_mod()
+    cases = [case_of(5, [30, 9, 16] * 20, [3000, 90, 800] * 20), case_of(6, [12] * 90, [333] * 90)]
+    want, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for b, q, k, v, mask, path in cases:
+        kc, vc = k.clone(), v.clone()
+        want.append((every_call(b, workspace(b), q, kc, vc, mask, path), kc, vc))
+    spaces = [workspace(c[0]) for c in cases]
+    torch.cuda.synchronize()
+    for turn in range(4):
+        got = []
+        for ws, s, (b, q, k, v, mask, path) in zip(spaces, streams, cases):
+            with torch.cuda.stream(s):  # the outputs are made there, too
+                kc, vc = k.clone(), v.clone()
+                got.append((every_call(b, ws, q, kc, vc, mask, path, stream=s if turn % 2 else None), kc, vc))
+        torch.cuda.synchronize()
+        for (x, xk, xv), (y, yk, yv), (b, *_) in zip(got, want, cases):
+            used = dev(np.unique(b.kv_indices)).long()
+            assert same(x[:6], y[:6]) and torch.equal(x[6][used], y[6][used]) and torch.equal(xk, yk) and torch.equal(xv, yv)
+
+
+def test_plans_and_calls_in_turn():
+    """New plans between calls of one workspace, nothing waited for: each call sees its own plan."""
+    torch = torch_mod()
+    cases = [case_of(7, [30, 9, 16] * 20, [3000, 90, 800] * 20), case_of(8, [12, 1] * 30, [333, 20] * 30), case_of(9, [5], [16_000])]
+    ws = B.Workspace(60, 1100, 14_000, 8, 2)
+    want = []
+    for b, q, k, v, mask, path in cases:
+        kc, vc = k.clone(), v.clone()
+        want.append((every_call(b, workspace(b), q, kc, vc, mask, path), kc, vc))
+        torch.cuda.synchronize()
+    got = []
+    for turn in range(12):
+        b, q, k, v, mask, path = cases[turn % 3]
+        kc, vc = k.clone(), v.clone()
+        plan(ws, b)
+        got.append((every_call(b, ws, q, kc, vc, mask, path), kc, vc))
+    torch.cuda.synchronize()
+    assert ws.get_error() == 0
+    for turn, (x, xk, xv) in enumerate(got):
+        y, yk, yv = want[turn % 3]
+        used = dev(np.unique(cases[turn % 3][0].kv_indices)).long()
+        assert same(x[:6], y[:6]) and torch.equal(x[6][used], y[6][used]) and torch.equal(xk, yk) and torch.equal(xv, yv)
