@@ -1090,6 +1090,7 @@ int fi_score_pages(fi_workspace* ws, const void* q, const void* bounds, int num_
   p.scores = scores;
   p.row_pages = row_pages;
   p.most_batch = ws->max_batch;
+  p.most_lq = ws->max_lq;
   p.hqo = ws->hqo;
   p.group = ws->hqo / ws->hkv;
   p.scale = 1.f / std::sqrt(float(ws->head_dim));

@@ -217,8 +217,7 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const __grid_con
 //  * the first page entries of all requests are read at once, where a search through them cost one latency a step.
 // (Blocks on their way to rings in shared memory, one or two ahead, with nine to twelve warps an SM: 31 and 34 us for
 // 128 decode requests of 1 to 8 K keys; sixteen warps that took a page's heads in turn, with nothing ahead: 26.)
-// Measured: those requests 25 us (154 MB, 0.92 of the copy bandwidth); two contexts of 100 to 131 K keys, four tokens of 64/8
-// heads, 18.7 (62 MB, 0.5): 1350 instructions a block for its four sets, in three rounds of warps, and 4 us to the first block.
+// Measured: those requests 24.4 us (154 MB, 0.94 of the copy bandwidth).
 constexpr int kScoreThreads = 128;
 constexpr int kScoreCtas = 4;
 constexpr int kScorePages = 16;
@@ -236,54 +235,82 @@ struct ScoreBlock {
   int r, room, pages;  // blocks that the line has for each head of the request, pages it has
   int head, block;
   int id;              // of page 16 block + lane % 16, -1 for none
+  int id_after;        // of the place after it, if that is of the same request
 };
 
-// kHeads: columns of a token in a set of eight, 1, 2, 4 or 8 (groups of more than 8 heads take several sets); 0: any other number,
-// by a loop over the set's tokens (with that loop for all, and divisions in it, two long contexts of four tokens and eight
-// heads a group took 2000 instructions a block: 25 us).
+// The line: for every request and KV head a place for each block.  Request r's begin at (its first entry) / 16 + r blocks,
+// which leaves room for all of its own (and at times one more).
+struct ScoreLine {
+  const PageView& pv;
+  const int* firsts;
+  int batch, entries;
+
+  __device__ __forceinline__ int begins(int k) const {
+    return ((k == batch ? entries : k < kScoreList ? firsts[k] : __ldg(&pv.geo[k].kv0)) >> 4) + k;
+  }
+  __device__ __forceinline__ void enter(ScoreBlock& x) const {
+    x.g = load_geo(pv.geo, x.r);
+    x.room = begins(x.r + 1) - begins(x.r);
+    x.pages = pages_of(pv, x.g.lkv);
+  }
+  __device__ __forceinline__ int ids_at(const ScoreBlock& x, int block) const {
+    const int e = block * kScorePages + int(threadIdx.x & 15);
+    return e < x.pages ? __ldg(pv.kv_indices + x.g.kv0 + e) : -1;
+  }
+  __device__ __forceinline__ void look_up(ScoreBlock& x, int id) const {
+    x.id = id;
+    if (id != -1 && static_cast<unsigned>(id) >= static_cast<unsigned>(pv.num_pages)) {
+      atomicOr(pv.err, FI_DEVERR_PAGE_OOB);
+      x.id = -1;
+    }
+    x.id_after = ids_at(x, x.block + 1 == x.room ? 0 : x.block + 1);
+  }
+  __device__ __forceinline__ void start(ScoreBlock& x, long long task) const {
+    x.r = last_at_most(batch, int(task / pv.hkv), [&](int k) { return begins(k); });
+    enter(x);
+    const int in = int(task - (long long)begins(x.r) * pv.hkv);
+    x.head = in / x.room;
+    x.block = in - x.head * x.room;
+    look_up(x, ids_at(x, x.block));
+  }
+  __device__ __forceinline__ void step(ScoreBlock& x) const {
+    if (++x.block == x.room) {
+      x.block = 0;
+      if (++x.head == pv.hkv) {
+        x.head = 0;
+        ++x.r;
+        enter(x);
+        x.id_after = ids_at(x, 0);
+      }
+    }
+    look_up(x, x.id_after);
+  }
+};
+
+// Requests of up to eight columns (in a replay: of any number, eight at a time).  kHeads: heads of a group, 1, 2, 4 or 8; 0: any other
+// number below 8, by a loop over the set's tokens.
 template <int kHeads>
 __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) scores_kernel(const __grid_constant__ ScoreParams p) {
   __shared__ int firsts[kScoreList];
   const int lane = threadIdx.x & 31, row = lane >> 2, c = lane & 3;
   const PageView& pv = p.pv;
-  const Geo* geo = pv.geo;
-  for (int i = threadIdx.x; i < min(kScoreList, p.most_batch); i += kScoreThreads) firsts[i] = __ldg(&geo[i].kv0);
-  const GeoHead plan = load_head(geo);
+  for (int i = threadIdx.x; i < min(kScoreList, p.most_batch); i += kScoreThreads) firsts[i] = __ldg(&pv.geo[i].kv0);
+  const GeoHead plan = load_head(pv.geo);
   if (plan.batch == 0) return wait_prior_grid();
-  const int entries = __ldg(&geo[plan.batch].kv0);
+  const int entries = __ldg(&pv.geo[plan.batch].kv0);
   __syncthreads();
-  // The line: for every request and KV head a place for each block.  Request r's begin at (its first entry) / 16 + r blocks,
-  // which leaves room for all of its own (and at times one more).
-  auto begins = [&](int k) { return ((k == plan.batch ? entries : k < kScoreList ? firsts[k] : __ldg(&geo[k].kv0)) >> 4) + k; };
-  const long long tasks = (long long)begins(plan.batch) * pv.hkv, warps = (long long)gridDim.x * (kScoreThreads / 32);
+  const ScoreLine line = {pv, firsts, plan.batch, entries};
+  const long long tasks = (long long)line.begins(plan.batch) * pv.hkv, warps = (long long)gridDim.x * (kScoreThreads / 32);
   const long long me = (long long)blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5);
   long long task = tasks * me / warps;
   const long long t1 = tasks * (me + 1) / warps;
   if (task >= t1) return wait_prior_grid();
   const int heads = kHeads ? kHeads : p.group;
-  const int fit = 8 / heads;                               // tokens of a set of eight columns
-  const int sets = kHeads == 8 ? (p.group + 7) / 8 : 1;    // sets of a token
+  const int fit = 8 / heads;                                // tokens of a set of eight columns
   const int col_tok = row / heads, col_head = row % heads;  // of column `row`
 
   ScoreBlock next;
-  auto enter = [&]() {
-    next.g = load_geo(geo, next.r);
-    next.room = begins(next.r + 1) - begins(next.r);
-    next.pages = pages_of(pv, next.g.lkv);
-  };
-  int id_after;  // of the place after next's, if it is of the same request
-  auto ids_at = [&](int block) {
-    const int e = block * kScorePages + (lane & 15);
-    return e < next.pages ? __ldg(pv.kv_indices + next.g.kv0 + e) : -1;
-  };
-  auto look_up = [&](int id) {
-    next.id = id;
-    if (id != -1 && static_cast<unsigned>(id) >= static_cast<unsigned>(pv.num_pages)) {
-      atomicOr(pv.err, FI_DEVERR_PAGE_OOB);
-      next.id = -1;
-    }
-    id_after = ids_at(next.block + 1 == next.room ? 0 : next.block + 1);
-  };
+  line.start(next, task);
   uint4 a[8], b[8];  // this lane's pieces of rows `row` and `row + 8`: 64-byte chunks 0-3 are lo, 4-7 hi
   auto fetch = [&](int k0) {
     const int ia = __shfl_sync(kAll, next.id, row), ib = __shfl_sync(kAll, next.id, row + 8);
@@ -296,34 +323,15 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) scores_kernel(const
       b[k] = ib >= 0 ? __ldcs(pb + 4 * k) : make_uint4(0, 0, 0, 0);
     }
   };
-  {
-    next.r = last_at_most(plan.batch, int(task / pv.hkv), begins);
-    enter();
-    const int in = int(task - (long long)begins(next.r) * pv.hkv);
-    next.head = in / next.room;
-    next.block = in - next.head * next.room;
-    look_up(ids_at(next.block));
-    wait_prior_grid();
-    fetch(0);
-    fetch(4);
-  }
+  wait_prior_grid();
+  fetch(0);
+  fetch(4);
   uint4 q[4];         // column `row` of the set at hand
   int q_key = -1;     // the (request, head) whose first set q holds
   for (; task < t1; ++task) {
     const ScoreBlock now = next;
     const bool more = task + 1 < t1;
-    if (more) {
-      if (++next.block == next.room) {
-        next.block = 0;
-        if (++next.head == pv.hkv) {
-          next.head = 0;
-          ++next.r;
-          enter();
-          id_after = ids_at(0);
-        }
-      }
-      look_up(id_after);
-    }
+    if (more) line.step(next);
     const int lq = now.g.lq;
     if (now.block * kScorePages >= now.pages || lq == 0) {  // an empty place
       if (more) {
@@ -334,21 +342,19 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) scores_kernel(const
     }
     const int ia = __shfl_sync(kAll, now.id, row), ib = __shfl_sync(kAll, now.id, row + 8);
     // column `row` of a set: (token, head of the group)
-    auto query = [&](int tok, int set) {
-      const int ct = tok + col_tok, ch = set * 8 + col_head;
-      const bool on = col_tok < fit && ct < lq && ch < p.group;
-      const uint4* pq = reinterpret_cast<const uint4*>(p.q + ((long long)(now.g.q0 + (on ? ct : 0)) * p.hqo + now.head * p.group + (on ? ch : 0)) * kHeadDim) + c;
+    auto query = [&](int tok) {
+      const int ct = tok + col_tok;
+      const bool on = col_tok < fit && ct < lq;
+      const uint4* pq = reinterpret_cast<const uint4*>(p.q + ((long long)(now.g.q0 + (on ? ct : 0)) * p.hqo + now.head * p.group + (on ? col_head : 0)) * kHeadDim) + c;
 #pragma unroll
       for (int k = 0; k < 4; ++k) q[k] = __ldg(pq + 4 * k);
     };
-    const bool one = sets == 1 && lq <= fit;  // one set of columns: q stays
+    const bool one = lq <= fit;  // one set of columns: q stays
     const int key = now.r * pv.hkv + now.head;
-    if (!one || key != q_key) query(0, 0);
+    if (!one || key != q_key) query(0);
     q_key = one ? key : -1;
-    float best[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};  // [page row][column of the lane's two]
-    for (int tok = 0, set = 0; tok < lq;) {
-      const bool last = set + 1 == sets;
-      const int tok2 = last ? tok + fit : tok, set2 = last ? 0 : set + 1;
+    for (int tok = 0; tok < lq; tok += fit) {
+      const int tok2 = tok + fit;
       float lo[4] = {0.f, 0.f, 0.f, 0.f}, hi[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -366,63 +372,225 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) scores_kernel(const
         mma_16816(hi, h1, pos[2], pos[3]);
       }
       if (tok2 >= lq && more) fetch(4);
-      if (tok2 < lq) query(tok2, set2);
-      // columns 2 c and 2 c + 1 of the set, where they are heads of the group
+      if (tok2 < lq) query(tok2);
+      const float best[2][2] = {{lo[0] + hi[0], lo[1] + hi[1]}, {lo[2] + hi[2], lo[3] + hi[3]}};  // [page row][column 2 c, 2 c + 1]
+      const int e0 = now.block * kScorePages + row;
+      auto put = [&](int f, int half, float v) {  // the score of token tok + f and page e0 + 8 half
+        const int e = e0 + 8 * half;
+        if (f >= fit || tok + f >= lq || e >= now.pages || e >= p.row_pages) return;
+        const int limit = plan.causal ? now.g.lkv - lq + tok + f : now.g.lkv - 1;
+        const bool seen = (half ? ib : ia) >= 0 && (long long)e * pv.page_size <= limit;
+        p.scores[((long long)(now.g.q0 + tok + f) * pv.hkv + now.head) * p.row_pages + e] = seen ? v * p.scale : -INFINITY;
+      };
+      if constexpr (kHeads == 1) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const bool head_on = kHeads != 8 || set * 8 + 2 * c + k < p.group;
-        best[0][k] = max_nan(best[0][k], head_on ? lo[k] + hi[k] : -INFINITY);
-        best[1][k] = max_nan(best[1][k], head_on ? lo[2 + k] + hi[2 + k] : -INFINITY);
-      }
-      if (last) {
-        const int e0 = now.block * kScorePages + row;
-        auto put = [&](int f, int half, float v) {  // the score of token tok + f and page e0 + 8 half
-          const int e = e0 + 8 * half;
-          if (f >= fit || tok + f >= lq || e >= now.pages || e >= p.row_pages) return;
-          const int limit = plan.causal ? now.g.lkv - lq + tok + f : now.g.lkv - 1;
-          const bool seen = (half ? ib : ia) >= 0 && (long long)e * pv.page_size <= limit;
-          p.scores[((long long)(now.g.q0 + tok + f) * pv.hkv + now.head) * p.row_pages + e] = seen ? v * p.scale : -INFINITY;
-        };
-        if constexpr (kHeads == 1) {
+        for (int k = 0; k < 2; ++k) {
+          put(2 * c + k, 0, best[0][k]);
+          put(2 * c + k, 1, best[1][k]);
+        }
+      } else if constexpr (kHeads != 0) {
+        // a token's columns are those of 1, 2 or 4 lanes; two of them write, or one both
+        float v0 = max_nan(best[0][0], best[0][1]), v1 = max_nan(best[1][0], best[1][1]);
+#pragma unroll
+        for (int m = 1; m < kHeads / 2; m <<= 1) {
+          v0 = max_nan(v0, __shfl_xor_sync(kAll, v0, m));
+          v1 = max_nan(v1, __shfl_xor_sync(kAll, v1, m));
+        }
+        const int f = 2 * c / kHeads, at = c % (kHeads / 2);
+        if (kHeads == 2) {
+          put(f, 0, v0);
+          put(f, 1, v1);
+        } else if (at < 2) {
+          put(f, at, at ? v1 : v0);
+        }
+      } else {
+        for (int f = 0; f < fit && tok + f < lq; ++f) {
+          float v0 = -INFINITY, v1 = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            put(2 * c + k, 0, best[0][k]);
-            put(2 * c + k, 1, best[1][k]);
+            const bool its = 2 * c + k >= f * heads && 2 * c + k < (f + 1) * heads;
+            v0 = max_nan(v0, its ? best[0][k] : -INFINITY);
+            v1 = max_nan(v1, its ? best[1][k] : -INFINITY);
           }
-        } else if constexpr (kHeads != 0) {
-          // a token's columns are those of 1, 2 or 4 lanes; two of them write, or one both
-          float v0 = max_nan(best[0][0], best[0][1]), v1 = max_nan(best[1][0], best[1][1]);
 #pragma unroll
-          for (int m = 1; m < kHeads / 2; m <<= 1) {
+          for (int m = 1; m < 4; m <<= 1) {
             v0 = max_nan(v0, __shfl_xor_sync(kAll, v0, m));
             v1 = max_nan(v1, __shfl_xor_sync(kAll, v1, m));
           }
-          const int f = 2 * c / kHeads, at = c % (kHeads / 2);
-          if (kHeads == 2) {
-            put(f, 0, v0);
-            put(f, 1, v1);
-          } else if (at < 2) {
-            put(f, at, at ? v1 : v0);
-          }
-        } else {
-          for (int f = 0; f < fit && tok + f < lq; ++f) {
-            float v0 = -INFINITY, v1 = -INFINITY;
+          if (c < 2) put(f, c, c ? v1 : v0);
+        }
+      }
+    }
+  }
+}
+
+// Requests of more columns, sixteen at a time.  There the products' instructions count, not only the bounds' bytes, so q's columns are
+// the rows of a product and the pages its columns: the words of a page are its operand as they come from memory, where as rows
+// of a product four of them have to be moved together for each set (a fifth of all instructions), and 16 pages take two products an
+// operand of q.  q streams by, a piece ahead (all of it in registers, the block's were spilled).  Both forms measured, two contexts of
+// 131 K keys, 64/8 heads: 4 tokens each 19.2 us eight at a time, 16.0 sixteen (74 MB of bounds are 11); 16 tokens 55.8 and 39.2;
+// four of 65 K, 16 heads a group, 16 tokens 99 and 87.  128 decode requests of four heads a group: 25 eight at a time, 32 sixteen.
+// kHeads: heads of a group, 1, 2, 4 or 8; 16: more than 8, 16 at a time; 0: any other number below 8, by a loop over the set's tokens.
+constexpr int kScoreWideCtas = 3;
+
+template <int kHeads>
+__global__ void __launch_bounds__(kScoreThreads, kScoreWideCtas) scores_wide_kernel(const __grid_constant__ ScoreParams p) {
+  constexpr int kValues = kHeads == 16 ? 4 : 8;  // that a lane gets of a set, the two halves of a token's 16 heads joined
+  __shared__ int firsts[kScoreList];
+  const int lane = threadIdx.x & 31, row = lane >> 2, c = lane & 3;
+  const PageView& pv = p.pv;
+  for (int i = threadIdx.x; i < min(kScoreList, p.most_batch); i += kScoreThreads) firsts[i] = __ldg(&pv.geo[i].kv0);
+  const GeoHead plan = load_head(pv.geo);
+  if (plan.batch == 0) return wait_prior_grid();
+  const int entries = __ldg(&pv.geo[plan.batch].kv0);
+  __syncthreads();
+  const ScoreLine line = {pv, firsts, plan.batch, entries};
+  const long long tasks = (long long)line.begins(plan.batch) * pv.hkv, warps = (long long)gridDim.x * (kScoreThreads / 32);
+  const long long me = (long long)blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5);
+  long long task = tasks * me / warps;
+  const long long t1 = tasks * (me + 1) / warps;
+  if (task >= t1) return wait_prior_grid();
+  const int heads = kHeads ? kHeads : p.group;
+  const int fit = kHeads == 16 ? 1 : 16 / heads;            // tokens of a set
+  const int sets = kHeads == 16 ? (p.group + 15) / 16 : 1;  // sets of a token
+  ScoreBlock next;
+  line.start(next, task);
+  uint4 a[8], b[8];  // this lane's pieces of pages `row` and `row + 8`: 64-byte chunks 0-3 are lo, 4-7 hi
+  const uint4 *pa = nullptr, *pb = nullptr;
+  bool on_a = false, on_b = false;
+  auto rows_of = [&]() {
+    const int ia = __shfl_sync(kAll, next.id, row), ib = __shfl_sync(kAll, next.id, row + 8);
+    pa = reinterpret_cast<const uint4*>(p.bounds + ((long long)max(ia, 0) * pv.hkv + next.head) * 2 * kHeadDim) + c;
+    pb = reinterpret_cast<const uint4*>(p.bounds + ((long long)max(ib, 0) * pv.hkv + next.head) * 2 * kHeadDim) + c;
+    on_a = ia >= 0;
+    on_b = ib >= 0;
+  };
+  auto fetch = [&](int k) {
+    a[k] = on_a ? __ldcs(pa + 4 * k) : make_uint4(0, 0, 0, 0);
+    b[k] = on_b ? __ldcs(pb + 4 * k) : make_uint4(0, 0, 0, 0);
+  };
+  auto fetch_all = [&]() {
+    rows_of();
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const bool its = 2 * c + k >= f * heads && 2 * c + k < (f + 1) * heads;
-              v0 = max_nan(v0, its ? best[0][k] : -INFINITY);
-              v1 = max_nan(v1, its ? best[1][k] : -INFINITY);
-            }
+    for (int k = 0; k < 8; ++k) fetch(k);
+  };
+  wait_prior_grid();
+  fetch_all();
+  uint4 q[2][2];  // columns `row` and `row + 8`: the piece at hand and the next
+  for (; task < t1; ++task) {
+    const ScoreBlock now = next;
+    const bool more = task + 1 < t1;
+    if (more) line.step(next);
+    const int lq = now.g.lq;
+    if (now.block * kScorePages >= now.pages || lq == 0) {  // an empty place
+      if (more) fetch_all();
+      continue;
+    }
+    auto column = [&](int half, int tok, int set) {  // q's pieces, four apart
+      const int col = row + 8 * half, ct = tok + (kHeads == 16 ? 0 : col / heads), ch = kHeads == 16 ? set * 16 + col : col % heads;
+      const bool on = ct < min(tok + fit, lq) && ch < p.group;
+      return reinterpret_cast<const uint4*>(p.q + ((long long)(now.g.q0 + (on ? ct : 0)) * p.hqo + now.head * p.group + (on ? ch : 0)) * kHeadDim) + c;
+    };
+    const uint4* pq[2] = {column(0, 0, 0), column(1, 0, 0)};
+    q[0][0] = __ldg(pq[0]);
+    q[1][0] = __ldg(pq[1]);
+    float best[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // 16 heads at a time: of the sets so far
+    for (int tok = 0, set = 0; tok < lq;) {
+      const bool last = set + 1 == sets;
+      const int tok2 = last ? tok + fit : tok, set2 = last ? 0 : set + 1;
+      const bool refill = tok2 >= lq && more;
+      if (refill) rows_of();
+      float s[2][4] = {};  // [page half]: [column half][page 2 c, 2 c + 1]
 #pragma unroll
-            for (int m = 1; m < 4; m <<= 1) {
-              v0 = max_nan(v0, __shfl_xor_sync(kAll, v0, m));
-              v1 = max_nan(v1, __shfl_xor_sync(kAll, v1, m));
+      for (int k = 0; k < 4; ++k) {
+        const uint4 x = q[0][k & 1], y = q[1][k & 1];
+        if (k < 3) {
+          q[0][(k & 1) ^ 1] = __ldg(pq[0] + 4 * (k + 1));
+          q[1][(k & 1) ^ 1] = __ldg(pq[1] + 4 * (k + 1));
+        } else if (tok2 < lq) {
+          pq[0] = column(0, tok2, set2);
+          pq[1] = column(1, tok2, set2);
+          q[0][0] = __ldg(pq[0]);
+          q[1][0] = __ldg(pq[1]);
+        }
+        const uint32_t n0[4] = {min2(x.x, 0u, false), min2(y.x, 0u, false), min2(x.y, 0u, false), min2(y.y, 0u, false)};
+        const uint32_t n1[4] = {min2(x.z, 0u, false), min2(y.z, 0u, false), min2(x.w, 0u, false), min2(y.w, 0u, false)};
+        mma_16816(s[0], n0, a[k].x, a[k].y);
+        mma_16816(s[1], n0, b[k].x, b[k].y);
+        mma_16816(s[0], n1, a[k].z, a[k].w);
+        mma_16816(s[1], n1, b[k].z, b[k].w);
+        if (refill) fetch(k);
+        const uint32_t p0[4] = {max2(x.x, 0u, false), max2(y.x, 0u, false), max2(x.y, 0u, false), max2(y.y, 0u, false)};
+        const uint32_t p1[4] = {max2(x.z, 0u, false), max2(y.z, 0u, false), max2(x.w, 0u, false), max2(y.w, 0u, false)};
+        mma_16816(s[0], p0, a[k + 4].x, a[k + 4].y);
+        mma_16816(s[1], p0, b[k + 4].x, b[k + 4].y);
+        mma_16816(s[0], p1, a[k + 4].z, a[k + 4].w);
+        mma_16816(s[1], p1, b[k + 4].z, b[k + 4].w);
+        if (refill) fetch(k + 4);
+      }
+      // The best of v's columns that differ in the lowest `bits` bits of `row`: each step leaves a lane half of the values, as long as it
+      // has more than one.  put(f, index, value) for those that it is left with.
+      auto join = [&](auto& v, int n, int bits, auto&& put) {
+        int at = 0;
+        bool mine = true;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          if (k >= bits) continue;
+          const bool upper = lane >> (2 + k) & 1;
+          if (n > 1) {
+            n /= 2;
+#pragma unroll
+            for (int i = 0; i < kValues / 2; ++i) {
+              if (i >= n) continue;
+              const float keep = upper ? v[i + n] : v[i], give = upper ? v[i] : v[i + n];
+              v[i] = max_nan(keep, __shfl_xor_sync(kAll, give, 4 << k));
             }
-            if (c < 2) put(f, c, c ? v1 : v0);
+            at += upper ? n : 0;
+          } else {
+            v[0] = max_nan(v[0], __shfl_xor_sync(kAll, v[0], 4 << k));
+            mine = mine && !upper;
           }
         }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) best[0][k] = best[1][k] = -INFINITY;
+        for (int i = 0; i < kValues; ++i)
+          if (i < n) put(at + i, mine, v[i]);
+      };
+      // the score of token tok + f and the page of value `index`
+      auto put = [&](int f, int index, bool mine, float v) {
+        const int page = (index >> 1 & 1) * 8 + 2 * c + (index & 1), e = now.block * kScorePages + page;
+        const int id = __shfl_sync(kAll, now.id, page);
+        if (!mine || f >= fit || tok + f >= lq || e >= now.pages || e >= p.row_pages) return;
+        const int limit = plan.causal ? now.g.lkv - lq + tok + f : now.g.lkv - 1;
+        const bool seen = id >= 0 && (long long)e * pv.page_size <= limit;
+        p.scores[((long long)(now.g.q0 + tok + f) * pv.hkv + now.head) * p.row_pages + e] = seen ? v * p.scale : -INFINITY;
+      };
+      if constexpr (kHeads == 16) {
+        // 16 heads of one token, or what is left of them
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float x = set * 16 + row < p.group ? s[k >> 1][k & 1] : -INFINITY, y = set * 16 + row + 8 < p.group ? s[k >> 1][2 + (k & 1)] : -INFINITY;
+          best[k] = max_nan(best[k], max_nan(x, y));
+        }
+        if (last) {
+          join(best, 4, 3, [&](int index, bool mine, float v) { put(0, index, mine, v); });
+#pragma unroll
+          for (int k = 0; k < 4; ++k) best[k] = -INFINITY;
+        }
+      } else if constexpr (kHeads != 0) {
+        float v[kValues];  // [column half][page half][page 2 c + j of it]
+#pragma unroll
+        for (int k = 0; k < kValues; ++k) v[k] = s[k >> 1 & 1][(k >> 2) * 2 + (k & 1)];
+        constexpr int kBits = kHeads == 8 ? 3 : kHeads == 4 ? 2 : kHeads == 2 ? 1 : 0;
+        join(v, kValues, kBits, [&](int index, bool mine, float x) { put((row >> kBits) + (index >> 2) * (8 >> kBits), index, mine, x); });
+      } else {
+        for (int f = 0; f < fit && tok + f < lq; ++f) {
+          auto its = [&](int col) { return col >= f * heads && col < (f + 1) * heads; };
+          float v[kValues];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            v[k] = max_nan(its(row) ? s[k >> 1][k & 1] : -INFINITY, its(row + 8) ? s[k >> 1][2 + (k & 1)] : -INFINITY);
+          join(v, 4, 3, [&](int index, bool mine, float x) { put(f, index, mine, x); });
+        }
       }
       tok = tok2;
       set = set2;
@@ -805,9 +973,13 @@ int launch_bounds(const BoundsParams& p, int64_t tasks, bool fp8, int num_sms, c
 
 int launch_scores(const ScoreParams& p, int64_t tasks, int num_sms, cudaStream_t stream) {
   constexpr int kWarps = kScoreThreads / 32;
-  const unsigned grid = unsigned(std::max<int64_t>(1, std::min<int64_t>((tasks + kWarps - 1) / kWarps, int64_t(num_sms) * kScoreCtas)));
-  const auto kernel = p.group >= 8 ? scores_kernel<8> : p.group == 4 ? scores_kernel<4> : p.group == 2 ? scores_kernel<2>
-                                                    : p.group == 1 ? scores_kernel<1> : scores_kernel<0>;
+  using Kernel = void (*)(const ScoreParams);
+  static const Kernel kernels[2][5] = {{scores_kernel<0>, scores_kernel<1>, scores_kernel<2>, scores_kernel<4>, scores_kernel<8>},
+                                       {scores_wide_kernel<0>, scores_wide_kernel<1>, scores_wide_kernel<2>, scores_wide_kernel<4>, scores_wide_kernel<8>}};
+  const int heads = p.group == 8 ? 4 : p.group == 4 ? 3 : p.group == 2 ? 2 : p.group == 1 ? 1 : 0;
+  const bool wide = int64_t(std::max(1, p.most_lq)) * p.group > 8;
+  const Kernel kernel = p.group > 8 ? scores_wide_kernel<16> : kernels[wide][heads];
+  const unsigned grid = unsigned(std::max<int64_t>(1, std::min<int64_t>((tasks + kWarps - 1) / kWarps, int64_t(num_sms) * (wide ? kScoreWideCtas : kScoreCtas))));
   const cudaError_t e = launch_dependent(kernel, grid, kScoreThreads, 0, 1, stream, p);
   return e == cudaSuccess ? FI_OK : record_cuda_error(e, "scores_kernel launch");
 }

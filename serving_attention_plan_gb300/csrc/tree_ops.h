@@ -84,6 +84,7 @@ struct ScoreParams {
   float* scores;  // [total_q][hkv][row_pages]
   int row_pages;
   int most_batch;  // of the workspace
+  int most_lq;     // query tokens of a request of the plan at hand
   int hqo, group;
   float scale;     // includes k_scale
 };

@@ -433,6 +433,12 @@ SCORES = [
     ([40, 20], [700, 20], 8, 8, 16, True, 0),                      # a prompt's tokens
     ([1, 1], [40, 0], 4, 2, 1, True, 0),
     ([2, 1] * 40, [3 + 7 * (i % 40) for i in range(80)], 4, 2, 4, False, 0),
+    ([7, 0, 2, 1], [900, 40, 2, 333], 16, 2, 16, True, 2),         # more than eight columns, eight heads a group
+    ([13, 1], [413, 20], 8, 2, 16, False, 0),                      # four
+    ([9, 17], [109, 700], 4, 2, 8, True, 0),                       # two
+    ([6, 3], [777, 3], 18, 3, 32, True, 1),                        # six
+    ([1, 3], [600, 90], 64, 4, 16, True, 0),                       # sixteen
+    ([2, 1], [520, 33], 40, 2, 16, False, 0),                      # twenty
 ]
 
 
