@@ -432,8 +432,9 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) scores_kernel(const
 // four of 65 K, 16 heads a group, 16 tokens 99 and 87.  128 decode requests of four heads a group: 25 eight at a time, 32 sixteen.
 // kHeads: heads of a group, 1, 2, 4 or 8; 16: more than 8, 16 at a time; 0: any other number below 8, by a loop over the set's tokens.
 constexpr int kScoreWideCtas = 3;
+constexpr int kScoreMostParts = 16;
 
-template <int kHeads>
+template <int kHeads, bool kSplit>
 __global__ void __launch_bounds__(kScoreThreads, kScoreWideCtas) scores_wide_kernel(const __grid_constant__ ScoreParams p) {
   constexpr int kValues = kHeads == 16 ? 4 : 8;  // that a lane gets of a set, the two halves of a token's 16 heads joined
   __shared__ int firsts[kScoreList];
@@ -445,16 +446,18 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreWideCtas) scores_wide_ker
   const int entries = __ldg(&pv.geo[plan.batch].kv0);
   __syncthreads();
   const ScoreLine line = {pv, firsts, plan.batch, entries};
-  const long long tasks = (long long)line.begins(plan.batch) * pv.hkv, warps = (long long)gridDim.x * (kScoreThreads / 32);
+  // kSplit: a warp's piece of the line begins and ends within a block; part j of `parts` of it are the sets of every parts-th tokens
+  // from the j-th on.
+  const int parts = kSplit ? p.parts : 1;
+  const long long units = (long long)line.begins(plan.batch) * pv.hkv * parts, warps = (long long)gridDim.x * (kScoreThreads / 32);
   const long long me = (long long)blockIdx.x * (kScoreThreads / 32) + (threadIdx.x >> 5);
-  long long task = tasks * me / warps;
-  const long long t1 = tasks * (me + 1) / warps;
-  if (task >= t1) return wait_prior_grid();
+  const long long u0 = units * me / warps, u1 = units * (me + 1) / warps, t0 = u0 / parts, t1 = (u1 + parts - 1) / parts;
+  if (u0 >= u1) return wait_prior_grid();
   const int heads = kHeads ? kHeads : p.group;
   const int fit = kHeads == 16 ? 1 : 16 / heads;            // tokens of a set
   const int sets = kHeads == 16 ? (p.group + 15) / 16 : 1;  // sets of a token
   ScoreBlock next;
-  line.start(next, task);
+  line.start(next, t0);
   uint4 a[8], b[8];  // this lane's pieces of pages `row` and `row + 8`: 64-byte chunks 0-3 are lo, 4-7 hi
   const uint4 *pa = nullptr, *pb = nullptr;
   bool on_a = false, on_b = false;
@@ -477,12 +480,18 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreWideCtas) scores_wide_ker
   wait_prior_grid();
   fetch_all();
   uint4 q[2][2];  // columns `row` and `row + 8`: the piece at hand and the next
-  for (; task < t1; ++task) {
+  for (long long task = t0; task < t1; ++task) {
     const ScoreBlock now = next;
     const bool more = task + 1 < t1;
     if (more) line.step(next);
     const int lq = now.g.lq;
-    if (now.block * kScorePages >= now.pages || lq == 0) {  // an empty place
+    const int first = kSplit && task == t0 ? int(u0 - t0 * parts) : 0, end = kSplit && task + 1 == t1 ? int(u1 - task * parts) : parts;  // its parts
+    auto after = [&](int tok) {  // the next tokens of those parts
+      if (!kSplit) return tok + fit;
+      const int g = tok / fit + 1, part = g & (parts - 1);
+      return (part < first ? g - part + first : part >= end ? g - part + parts + first : g) * fit;
+    };
+    if (now.block * kScorePages >= now.pages || first * fit >= lq) {  // an empty place, or nothing in its parts
       if (more) fetch_all();
       continue;
     }
@@ -491,13 +500,13 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreWideCtas) scores_wide_ker
       const bool on = ct < min(tok + fit, lq) && ch < p.group;
       return reinterpret_cast<const uint4*>(p.q + ((long long)(now.g.q0 + (on ? ct : 0)) * p.hqo + now.head * p.group + (on ? ch : 0)) * kHeadDim) + c;
     };
-    const uint4* pq[2] = {column(0, 0, 0), column(1, 0, 0)};
+    const uint4* pq[2] = {column(0, first * fit, 0), column(1, first * fit, 0)};
     q[0][0] = __ldg(pq[0]);
     q[1][0] = __ldg(pq[1]);
     float best[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // 16 heads at a time: of the sets so far
-    for (int tok = 0, set = 0; tok < lq;) {
+    for (int tok = first * fit, set = 0; tok < lq;) {
       const bool last = set + 1 == sets;
-      const int tok2 = last ? tok + fit : tok, set2 = last ? 0 : set + 1;
+      const int tok2 = last ? after(tok) : tok, set2 = last ? 0 : set + 1;
       const bool refill = tok2 >= lq && more;
       if (refill) rows_of();
       float s[2][4] = {};  // [page half]: [column half][page 2 c, 2 c + 1]
@@ -971,14 +980,26 @@ int launch_bounds(const BoundsParams& p, int64_t tasks, bool fp8, int num_sms, c
   return e == cudaSuccess ? FI_OK : record_cuda_error(e, "bounds_kernel launch");
 }
 
-int launch_scores(const ScoreParams& p, int64_t tasks, int num_sms, cudaStream_t stream) {
+int launch_scores(ScoreParams p, int64_t tasks, int num_sms, cudaStream_t stream) {
   constexpr int kWarps = kScoreThreads / 32;
   using Kernel = void (*)(const ScoreParams);
-  static const Kernel kernels[2][5] = {{scores_kernel<0>, scores_kernel<1>, scores_kernel<2>, scores_kernel<4>, scores_kernel<8>},
-                                       {scores_wide_kernel<0>, scores_wide_kernel<1>, scores_wide_kernel<2>, scores_wide_kernel<4>, scores_wide_kernel<8>}};
-  const int heads = p.group == 8 ? 4 : p.group == 4 ? 3 : p.group == 2 ? 2 : p.group == 1 ? 1 : 0;
+  static const Kernel kernels[3][6] = {
+      {scores_kernel<0>, scores_kernel<1>, scores_kernel<2>, scores_kernel<4>, scores_kernel<8>, nullptr},
+      {scores_wide_kernel<0, false>, scores_wide_kernel<1, false>, scores_wide_kernel<2, false>, scores_wide_kernel<4, false>,
+       scores_wide_kernel<8, false>, scores_wide_kernel<16, false>},
+      {scores_wide_kernel<0, true>, scores_wide_kernel<1, true>, scores_wide_kernel<2, true>, scores_wide_kernel<4, true>,
+       scores_wide_kernel<8, true>, scores_wide_kernel<16, true>}};
+  const int heads = p.group > 8 ? 5 : p.group == 8 ? 4 : p.group == 4 ? 3 : p.group == 2 ? 2 : p.group == 1 ? 1 : 0;
   const bool wide = int64_t(std::max(1, p.most_lq)) * p.group > 8;
-  const Kernel kernel = p.group > 8 ? scores_wide_kernel<16> : kernels[wide][heads];
+  // Blocks' sets are shared out where there are fewer than two blocks a warp (one context of 16 K keys, 512 tokens of 32/8 heads 109 -> 47 us,
+  // two of 32 K, 64 tokens of 64/8 55 -> 41; with more, a block read by two warps costs more than even pieces save: two of 131 K, 16 tokens
+  // 39 and 42).
+  const int fit = p.group > 8 ? 1 : 16 / p.group;
+  p.parts = 1;
+  if (wide && tasks < int64_t(num_sms) * kScoreWideCtas * kWarps * 2)
+    while (p.parts < kScoreMostParts && 2 * int64_t(p.parts) * fit <= p.most_lq) p.parts *= 2;
+  tasks *= p.parts;
+  const Kernel kernel = kernels[wide ? 1 + (p.parts > 1) : 0][heads];
   const unsigned grid = unsigned(std::max<int64_t>(1, std::min<int64_t>((tasks + kWarps - 1) / kWarps, int64_t(num_sms) * (wide ? kScoreWideCtas : kScoreCtas))));
   const cudaError_t e = launch_dependent(kernel, grid, kScoreThreads, 0, 1, stream, p);
   return e == cudaSuccess ? FI_OK : record_cuda_error(e, "scores_kernel launch");

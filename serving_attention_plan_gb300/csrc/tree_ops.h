@@ -85,10 +85,11 @@ struct ScoreParams {
   int row_pages;
   int most_batch;  // of the workspace
   int most_lq;     // query tokens of a request of the plan at hand
+  int parts;       // set by the launcher: a power of two, parts of a block's sets that warps can have apart
   int hqo, group;
   float scale;     // includes k_scale
 };
-int launch_scores(const ScoreParams& p, int64_t tasks, int num_sms, cudaStream_t stream);
+int launch_scores(ScoreParams p, int64_t tasks, int num_sms, cudaStream_t stream);
 
 struct PickParams {
   PageView pv;

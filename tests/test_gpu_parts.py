@@ -439,6 +439,7 @@ SCORES = [
     ([6, 3], [777, 3], 18, 3, 32, True, 1),                        # six
     ([1, 3], [600, 90], 64, 4, 16, True, 0),                       # sixteen
     ([2, 1], [520, 33], 40, 2, 16, False, 0),                      # twenty
+    ([70, 3, 0, 33], [500, 90, 50, 1033], 16, 2, 16, True, 0),     # a block's tokens in sixteen parts
 ]
 
 
