@@ -860,9 +860,11 @@ def test_two_streams_at_once():
             assert same(x[:6], y[:6]) and torch.equal(x[6][used], y[6][used]) and torch.equal(xk, yk) and torch.equal(xv, yv)
 
 
-def test_plans_and_calls_in_turn():
-    """New plans between calls of one workspace, nothing waited for: each call sees its own plan."""
+@pytest.mark.parametrize("apart", [False, True], ids=["one stream", "plans on another stream"])
+def test_plans_and_calls_in_turn(apart):
+    """New plans between calls of one workspace, nothing waited for on the host: each call sees its own plan."""
     torch = torch_mod()
+    plans, calls = (torch.cuda.Stream(), torch.cuda.Stream()) if apart else (None, torch.cuda.current_stream())
     cases = [case_of(7, [30, 9, 16] * 20, [3000, 90, 800] * 20), case_of(8, [12, 1] * 30, [333, 20] * 30), case_of(9, [5], [16_000])]
     ws = B.Workspace(60, 1100, 14_000, 8, 2)
     want = []
@@ -873,9 +875,15 @@ def test_plans_and_calls_in_turn():
     got = []
     for turn in range(12):
         b, q, k, v, mask, path = cases[turn % 3]
-        kc, vc = k.clone(), v.clone()
-        plan(ws, b)
-        got.append((every_call(b, ws, q, kc, vc, mask, path), kc, vc))
+        with torch.cuda.stream(calls):
+            kc, vc = k.clone(), v.clone()
+            if apart:
+                plans.wait_stream(calls)
+            ws.plan(b.qo_indptr, b.kv_indptr, b.kv_indices, b.last_page_len, b.page_size, b.causal, stream=plans if apart else calls)
+            kc.add_(0)  # a kernel between the plan's copy and the calls, or beside it
+            if apart:
+                calls.wait_stream(plans)
+            got.append((every_call(b, ws, q, kc, vc, mask, path), kc, vc))
     torch.cuda.synchronize()
     assert ws.get_error() == 0
     for turn, (x, xk, xv) in enumerate(got):
