@@ -626,8 +626,10 @@ __device__ __forceinline__ uint32_t score_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-template <bool kOne>
-__global__ void __launch_bounds__(kOne ? 32 : 1024) pick_kernel(const __grid_constant__ PickParams p) {
+// kMost: the warps that it is compiled for, 1, 16 (128 registers a thread) or 32 (64).
+template <int kMost>
+__global__ void __launch_bounds__(32 * kMost) pick_kernel(const __grid_constant__ PickParams p) {
+  constexpr bool kOne = kMost == 1;
   __shared__ uint32_t counts[2][kPickMostWarps];
   __shared__ uint2 runs[kPickMostWarps];
   __shared__ uint32_t list[kOne ? 1 : kPickFew], list_end;
@@ -691,6 +693,17 @@ __global__ void __launch_bounds__(kOne ? 32 : 1024) pick_kernel(const __grid_con
     };
     uint32_t key[kPickEach];
     keys_of(0, w0, key);
+    // The page ids of the run at hand, all of them: asked for where one is chosen, each took a latency of its own (4000 clocks).
+    // Up to 16 warps ask before the search, where they cost nothing; more have no registers for that.
+    int id[kPickEach];
+    auto look_up = [&](int base) {
+#pragma unroll
+      for (int i = 0; i < kPickEach; ++i) {
+        const int pos = base + (warp * kPickEach + i) * 32 + lane;
+        id[i] = pos < n ? __ldg(ids + pos) : 0;
+      }
+    };
+    if (kMost <= 16) look_up(0);
     auto at_least = [&](uint32_t x) {
       uint32_t k = 0;
       if (n <= span) {
@@ -729,8 +742,9 @@ __global__ void __launch_bounds__(kOne ? 32 : 1024) pick_kernel(const __grid_con
       // the few that the remaining bits decide about, to one warp
       if (threadIdx.x == 0) list_end = 0;
       __syncthreads();
-      const uint32_t low = limit_key, size = bit == 31 ? 0u : 2u << bit;  // low .. low + size - 1 (31: all)
-      auto in = [&](uint32_t v) { return v != 0 && v >= low && (bit == 31 || v - low < size); };
+      const uint32_t low = max(limit_key, 1u);  // low .. limit_key + 2^(bit + 1) - 1, but never 0
+      const uint32_t size = (bit == 31 ? 0u : limit_key + (2u << bit)) - low;
+      auto in = [&](uint32_t v) { return v - low < size; };
       uint32_t mine = 0;
 #pragma unroll
       for (int i = 0; i < kPickEach; ++i) mine += in(key[i]);
@@ -777,16 +791,15 @@ __global__ void __launch_bounds__(kOne ? 32 : 1024) pick_kernel(const __grid_con
     uint32_t before = 0, ties_before = 0;  // chosen positions and ties in the runs before
     for (int base = 0; base < n; base += span) {
       if (base > 0) fetch(base, key);
-      uint32_t sure = 0, tied = 0;  // of this warp
-      unsigned tie_mask[kPickEach];
+      if (kMost > 16 || base > 0) look_up(base);
+      uint32_t stays = 0, ties_here = 0;  // bit i: of position i of this thread
 #pragma unroll
       for (int i = 0; i < kPickEach; ++i) {
         const int pos = base + (warp * kPickEach + i) * 32 + lane;
-        const bool forced = pos < f0 || (pos >= f1 && pos < n);
-        tie_mask[i] = __ballot_sync(kAll, key[i] == limit_key && key[i] != 0u);
-        sure += __popc(__ballot_sync(kAll, forced || (need != 0 && key[i] > limit_key)));
-        tied += __popc(tie_mask[i]);
+        if (pos < f0 || (pos >= f1 && pos < n) || key[i] > limit_key) stays |= 1u << i;
+        if (key[i] == limit_key && key[i] != 0u) ties_here |= 1u << i;
       }
+      const uint32_t sure = __reduce_add_sync(kAll, __popc(stays)), tied = __reduce_add_sync(kAll, __popc(ties_here));  // of this warp
       uint32_t my_sure = before, my_ties = ties_before;
       if (!kOne) {
         __syncthreads();  // the last reads of `runs` and `counts`
@@ -802,16 +815,23 @@ __global__ void __launch_bounds__(kOne ? 32 : 1024) pick_kernel(const __grid_con
         ties_before += tied;
       }
       uint32_t at = my_sure + min(my_ties, ties);
+      uint32_t take = ties - min(my_ties, ties);  // of this warp's ties the first so many
+      const unsigned below = (1u << lane) - 1;
+      if (take >= tied) {
+        stays |= ties_here;
+      } else if (take > 0) {
+#pragma unroll
+        for (int i = 0; i < kPickEach; ++i) {
+          const unsigned there = __ballot_sync(kAll, ties_here >> i & 1u);
+          if ((ties_here >> i & 1u) && __popc(there & below) < take) stays |= 1u << i;
+          take -= min(take, uint32_t(__popc(there)));
+        }
+      }
 #pragma unroll
       for (int i = 0; i < kPickEach; ++i) {
-        const int pos = base + (warp * kPickEach + i) * 32 + lane;
-        const bool forced = pos < f0 || (pos >= f1 && pos < n);
-        const unsigned below = (1u << lane) - 1;
-        const bool tie = (tie_mask[i] >> lane & 1u) && my_ties + __popc(tie_mask[i] & below) < ties;
-        const unsigned stay = __ballot_sync(kAll, forced || tie || (need != 0 && key[i] > limit_key));
-        if (stay >> lane & 1u) out[at + __popc(stay & below)] = __ldg(ids + pos);
-        at += __popc(stay);
-        my_ties += __popc(tie_mask[i]);
+        const unsigned there = __ballot_sync(kAll, stays >> i & 1u);
+        if (stays >> i & 1u) out[at + __popc(there & below)] = id[i];
+        at += __popc(there);
       }
     }
     if (!kOne) __syncthreads();
@@ -1008,8 +1028,8 @@ int launch_scores(ScoreParams p, int64_t tasks, int num_sms, cudaStream_t stream
 int launch_pick(const PickParams& p, int64_t rows, int most_pages, int num_sms, cudaStream_t stream) {
   const int warps = std::min(kPickMostWarps, std::max(1, (most_pages + 32 * kPickEach - 1) / (32 * kPickEach)));
   const unsigned grid = unsigned(std::max<int64_t>(1, std::min<int64_t>(rows, int64_t(num_sms) * std::min(32, 64 / warps))));
-  const cudaError_t e = warps == 1 ? launch_dependent(pick_kernel<true>, grid, 32, 0, 1, stream, p)
-                                   : launch_dependent(pick_kernel<false>, grid, unsigned(warps) * 32, 0, 1, stream, p);
+  const auto kernel = warps == 1 ? pick_kernel<1> : warps <= 16 ? pick_kernel<16> : pick_kernel<32>;
+  const cudaError_t e = launch_dependent(kernel, grid, unsigned(warps) * 32, 0, 1, stream, p);
   return e == cudaSuccess ? FI_OK : record_cuda_error(e, "pick_kernel launch");
 }
 
