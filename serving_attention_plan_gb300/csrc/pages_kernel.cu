@@ -609,12 +609,13 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreWideCtas) scores_wide_ker
 
 // ---- choice --------------------------------------------------------------------------------------------
 // Of the n pages that a (token, KV head) row sees, the first `sink`, the last `recent` and the best of the rest, budget in
-// all.  The threshold, the K-th largest score, is found bit by bit from the top: scores as integers of the same order, and
-// at each step a count of those at or above a candidate.  A count costs a compare and an add for each score that a thread
-// holds in registers, a warp sum and, with more than one warp, a barrier; it ends once exactly K are counted.  Once at most
-// 512 scores are left to decide about, one warp goes on with them alone (14.8 -> 12.8 us for 32 rows of 8192 pages).
-// Nothing depends on scheduling.  A warp holds a run of positions, so the chosen come out in order by counting.  Rows longer than the CTA
-// holds are read again for each count.
+// all.  The threshold, the K-th largest score, is found from the top, two bits at a time: scores as integers of the same order, and at
+// each step the counts of those at or above three candidates, which a warp sums as ten bits each of one number.  With more than one
+// warp a step costs a barrier; once at most 512 scores are left to decide about, one warp goes on with them alone.  It ends once
+// exactly K are counted.  Nothing depends on scheduling.  A warp holds a run of positions, so the chosen come out in order by counting.
+// Rows longer than the CTA holds are read again for each count, a bit at a time.
+// Bound by the chain of all this.  Measured: 64 x 8 rows of 128 to 512 pages 5.2 us (one bit a step, page ids where they are chosen, two votes
+// a position: 7.7), 32 rows of 8193 9.6 (12.8, and 14.8 with every bit by all warps).
 constexpr int kPickEach = 16;  // scores of a thread
 constexpr int kPickMostWarps = 32;
 constexpr uint32_t kPickFew = 32 * kPickEach;
@@ -626,7 +627,29 @@ __device__ __forceinline__ uint32_t score_key(float w) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// kMost: the warps that it is compiled for, 1, 16 (128 registers a thread) or 32 (64).
+// How many of a warp's (at most 512) scores are at or above x + 2^(bit - 1), x + 2^bit and x + both, ten bits each.
+__device__ __forceinline__ uint32_t count_three(const uint32_t (&v)[kPickEach], uint32_t x, int bit) {
+  const uint32_t x1 = x + (1u << (bit - 1)), x2 = x + (1u << bit), x3 = x2 + (1u << (bit - 1));
+  uint32_t c[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < kPickEach; ++i) c[i & 1] += (v[i] >= x1 ? 1u : 0u) + (v[i] >= x2 ? 1u << 10 : 0u) + (v[i] >= x3 ? 1u << 20 : 0u);
+  return __reduce_add_sync(kAll, c[0] + c[1]);
+}
+// The largest of the three and of x itself with at least `need` scores at or above it; whether they are exactly so many.
+__device__ __forceinline__ bool narrow(uint32_t& x, int bit, uint32_t need, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t& from, uint32_t& above) {
+  if (c1 < need) {
+    above = c1;
+    return false;
+  }
+  const uint32_t c = c3 >= need ? c3 : c2 >= need ? c2 : c1;
+  x += (c2 >= need ? 1u << bit : 0u) + (c3 >= need || c2 < need ? 1u << (bit - 1) : 0u);
+  above = c3 >= need ? above : c2 >= need ? c3 : c2;
+  from = c;
+  return c == need;
+}
+
+// kMost: the warps that it is compiled for, 1, 20 (96 registers a thread, 10240 pages) or 32 (64: 8193 pages 9.9 us in place
+// of 9.6).
 template <int kMost>
 __global__ void __launch_bounds__(32 * kMost) pick_kernel(const __grid_constant__ PickParams p) {
   constexpr bool kOne = kMost == 1;
@@ -694,7 +717,7 @@ __global__ void __launch_bounds__(32 * kMost) pick_kernel(const __grid_constant_
     uint32_t key[kPickEach];
     keys_of(0, w0, key);
     // The page ids of the run at hand, all of them: asked for where one is chosen, each took a latency of its own (4000 clocks).
-    // Up to 16 warps ask before the search, where they cost nothing; more have no registers for that.
+    // Up to 20 warps ask before the search, where they cost nothing; more have no registers for that.
     int id[kPickEach];
     auto look_up = [&](int base) {
 #pragma unroll
@@ -703,7 +726,7 @@ __global__ void __launch_bounds__(32 * kMost) pick_kernel(const __grid_constant_
         id[i] = pos < n ? __ldg(ids + pos) : 0;
       }
     };
-    if (kMost <= 16) look_up(0);
+    if (kMost <= 20) look_up(0);
     auto at_least = [&](uint32_t x) {
       uint32_t k = 0;
       if (n <= span) {
@@ -722,19 +745,32 @@ __global__ void __launch_bounds__(32 * kMost) pick_kernel(const __grid_constant_
     uint32_t limit_key = 0;  // the largest x with at least `need` scores at or above it
     bool exact = need == 0;
     if (exact) limit_key = 0xffffffffu;
-    uint32_t from = uint32_t(n), above = 0;  // scores at or above limit_key (at most), and at or above limit_key + 2^bit
+    uint32_t from = uint32_t(n), above = 0;  // scores at or above limit_key (at most), and at or above limit_key + 2^(bit + 1)
     int bit = 31;
-    for (; bit >= 0 && !exact; --bit) {
-      if (!kOne && n <= span && from - above <= kPickFew) break;
-      const uint32_t x = limit_key | (1u << bit);
-      const uint32_t k = at_least(x);
-      if (k >= need) {
-        limit_key = x;
-        from = k;
-      } else {
-        above = k;
+    if (n <= span) {
+      for (; bit >= 0 && !exact; bit -= 2) {  // two bits at a time
+        if (!kOne && from - above <= kPickFew) break;
+        const uint32_t c = count_three(key, limit_key, bit);  // of a warp
+        uint32_t c1 = c & 1023u, c2 = c >> 10 & 1023u, c3 = c >> 20;
+        if (!kOne) {
+          if (lane == 0) counts[turn][warp] = c;
+          __syncthreads();
+          const uint32_t v = lane < warps ? counts[turn][lane] : 0u;
+          const uint32_t two = __reduce_add_sync(kAll, (v & 1023u) | (v >> 10 & 1023u) << 16);
+          c1 = two & 0xffffu;
+          c2 = two >> 16;
+          c3 = __reduce_add_sync(kAll, v >> 20);
+          turn ^= 1;
+        }
+        exact = narrow(limit_key, bit, need, c1, c2, c3, from, above);
       }
-      exact = k == need;
+    } else {
+      for (; bit >= 0 && !exact; --bit) {
+        const uint32_t x = limit_key | (1u << bit);
+        const uint32_t k = at_least(x);
+        if (k >= need) limit_key = x;
+        exact = k == need;
+      }
     }
     // scores above the limit stay, of those at it the first few; if exactly `need` are at or above it, all of them
     uint32_t ties = exact && need != 0 ? 0xffffffffu : 0u;
@@ -773,11 +809,10 @@ __global__ void __launch_bounds__(32 * kMost) pick_kernel(const __grid_constant_
         };
         const uint32_t left = need - above;
         bool done = false;
-        for (; bit >= 0 && !done; --bit) {
-          const uint32_t x = limit_key | (1u << bit);
-          const uint32_t k = count(x);
-          if (k >= left) limit_key = x;
-          done = k == left;
+        uint32_t unused = 0;
+        for (; bit >= 0 && !done; bit -= 2) {
+          const uint32_t c = count_three(some, limit_key, bit);
+          done = narrow(limit_key, bit, left, c & 1023u, c >> 10 & 1023u, c >> 20, unused, unused);
         }
         ties = done ? 0xffffffffu : left - (limit_key == 0xffffffffu ? 0u : count(limit_key + 1));
         if (lane == 0) runs[0] = make_uint2(limit_key, ties);
@@ -791,7 +826,7 @@ __global__ void __launch_bounds__(32 * kMost) pick_kernel(const __grid_constant_
     uint32_t before = 0, ties_before = 0;  // chosen positions and ties in the runs before
     for (int base = 0; base < n; base += span) {
       if (base > 0) fetch(base, key);
-      if (kMost > 16 || base > 0) look_up(base);
+      if (kMost > 20 || base > 0) look_up(base);
       uint32_t stays = 0, ties_here = 0;  // bit i: of position i of this thread
 #pragma unroll
       for (int i = 0; i < kPickEach; ++i) {
@@ -1028,7 +1063,7 @@ int launch_scores(ScoreParams p, int64_t tasks, int num_sms, cudaStream_t stream
 int launch_pick(const PickParams& p, int64_t rows, int most_pages, int num_sms, cudaStream_t stream) {
   const int warps = std::min(kPickMostWarps, std::max(1, (most_pages + 32 * kPickEach - 1) / (32 * kPickEach)));
   const unsigned grid = unsigned(std::max<int64_t>(1, std::min<int64_t>(rows, int64_t(num_sms) * std::min(32, 64 / warps))));
-  const auto kernel = warps == 1 ? pick_kernel<1> : warps <= 16 ? pick_kernel<16> : pick_kernel<32>;
+  const auto kernel = warps == 1 ? pick_kernel<1> : warps <= 20 ? pick_kernel<20> : pick_kernel<32>;
   const cudaError_t e = launch_dependent(kernel, grid, unsigned(warps) * 32, 0, 1, stream, p);
   return e == cudaSuccess ? FI_OK : record_cuda_error(e, "pick_kernel launch");
 }
