@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const __grid_con
 //  * the first page entries of all requests are read at once, where a search through them cost one latency a step.
 // (Blocks on their way to rings in shared memory, one or two ahead, with nine to twelve warps an SM: 31 and 34 us for
 // 128 decode requests of 1 to 8 K keys; sixteen warps that took a page's heads in turn, with nothing ahead: 26.)
-// Measured: those requests 24.4 us (154 MB, 0.94 of the copy bandwidth).
+// Measured: those requests 25 us (154 MB, 0.92 of the copy bandwidth).
 constexpr int kScoreThreads = 128;
 constexpr int kScoreCtas = 4;
 constexpr int kScorePages = 16;
