@@ -890,3 +890,52 @@ def test_plans_and_calls_in_turn(apart):
         y, yk, yv = want[turn % 3]
         used = dev(np.unique(cases[turn % 3][0].kv_indices)).long()
         assert same(x[:6], y[:6]) and torch.equal(x[6][used], y[6][used]) and torch.equal(xk, yk) and torch.equal(xv, yv)
+
+
+# ---- where tensors may lie ------------------------------------------------------------------------------
+
+
+def moved(t):
+    """A copy of t whose data begin at the smallest offset that the calls allow behind an allocation's own alignment: 16 bytes
+    for rows of 128 elements, 4 for the others."""
+    torch = torch_mod()
+    off = (16 if t.shape[-1] == 128 else 4) // t.element_size()
+    flat = torch.empty(t.numel() + off, dtype=t.dtype, device="cuda")
+    out = flat[off:].view(t.shape)
+    out.copy_(t)
+    assert out.is_contiguous() and out.data_ptr() % 32 == off * t.element_size()
+    return out
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq", [8, 24], ids=["4 heads a group", "12"])
+def test_tensors_at_the_smallest_alignment(hq, dtype):
+    """Every operator on tensors that begin 16 bytes (rows of a head) or 4 bytes (all else) behind a multiple of 32: bit for bit as on
+    tensors of their own.  Trees with whole units and with cut ones, lists on both kinds of tiles."""
+    torch = torch_mod()
+    for lq, lkv in (([30, 4, 64], [2000, 4, 900]), ([3] * 200, [60] * 200)):
+        b = batch_of(lq, lkv, hq, 2, 16, False, seed=hq)
+        q, k, v = bf16(b.q), pool(b, "k_pages", dtype, "HND", 1.0)[0], pool(b, "v_pages", dtype, "HND", 1.0)[0]
+        mask = dev(random_mask(np.random.default_rng(1), b, "tree"))
+        path = dev(np.array([[0, 2, -1]] * len(lq), np.int32))
+        ws = workspace(b, dtype=dtype)
+        row = int(np.diff(b.kv_indptr).max())
+
+        def calls(at):
+            kc, vc, qc = at(k.clone()), at(v.clone()), at(q)
+            (o, lse), (po, plse) = (tuple(at(x) for x in outputs(b)) for _ in range(2))
+            bounds = at(torch.zeros(b.num_pages, 2, 2, 128, dtype=torch.bfloat16, device="cuda"))
+            scores = at(torch.full((b.total_q, 2, row), 3.0, device="cuda"))
+            sel = at(torch.zeros(b.total_q, 2, 5, dtype=torch.int32, device="cuda"))
+            ws.tree_run(qc, kc, vc, at(mask), o, lse)
+            ws.page_bounds(kc, bounds)
+            ws.score_pages(qc, bounds, scores)
+            ws.select_pages(scores, sel, recent=1)
+            ws.run_pages(qc, kc, vc, sel, po, plse)
+            ws.tree_commit(at(path), kc, vc)
+            torch.cuda.synchronize()
+            return o, lse, bounds, scores, sel, po, plse, kc.view(torch.uint8), vc.view(torch.uint8)
+
+        want, got = calls(lambda t: t), calls(moved)
+        assert ws.get_error() == 0
+        assert same(want, got)
