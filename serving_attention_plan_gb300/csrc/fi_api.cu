@@ -415,6 +415,8 @@ int fi_workspace_create(int max_batch, int max_total_q, int max_kv_pages, int nu
 
   cudaError_t e = cudaMalloc(&ws->dbuf, ws->dev_bytes);
   if (e == cudaSuccess) e = cudaMemset(ws->dbuf + ws->off_counters, 0, ws->off_part_lse - ws->off_counters);
+  // no work before the first plan: a count of units, or a CTA's items, that nothing has written is 0
+  if (e == cudaSuccess) e = cudaMemset(ws->dbuf + ws->off_l_header, 0, ws->off_l_items - ws->off_l_header);
   if (e == cudaSuccess) e = cudaHostAlloc(reinterpret_cast<void**>(&ws->hbuf), ws->plan_bytes, cudaHostAllocDefault);
   if (e == cudaSuccess) e = cudaEventCreateWithFlags(&ws->copy_done, cudaEventDisableTiming);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();

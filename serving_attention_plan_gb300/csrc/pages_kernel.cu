@@ -949,7 +949,6 @@ __global__ void __launch_bounds__(kPlanThreads) list_plan_kernel(const __grid_co
 
   int steps = steps_of(g);
   wait_prior_grid();
-  if (blockIdx.x == 0 && threadIdx.x == 0) p.header[H_NUM_UNITS] = p.ctas;
   for (long long u = u0 + warp; u < u1; u += kPlanWarps) {
     const int t = int(u / pv.hkv), head = int(u - (long long)t * pv.hkv);
     while (t >= g.q0 + g.lq) {
@@ -1016,7 +1015,8 @@ __global__ void __launch_bounds__(kPlanThreads) list_plan_kernel(const __grid_co
         }
       }
     }
-    if (u == units - 1) {
+    if (u == units - 1) {  // (whose CTA is not always the first: a captured grid may have more CTAs than there are units)
+      if (lane == 0) p.header[H_NUM_UNITS] = p.ctas;
       for (int c = used + lane; c <= p.ctas; c += 32) {
         p.cta_indptr[c] = int(units) + used - 1;
         put_unit(p.units, c - 1, 0, 0, 0, 0, 0);

@@ -939,3 +939,35 @@ def test_tensors_at_the_smallest_alignment(hq, dtype):
         want, got = calls(lambda t: t), calls(moved)
         assert ws.get_error() == 0
         assert same(want, got)
+
+
+def record(call):
+    """The call in a graph, with no call before it."""
+    torch = torch_mod()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s), torch.cuda.graph(g, stream=s):
+        call()
+    torch.cuda.synchronize()
+    return g
+
+
+@pytest.mark.parametrize("hq,most", [(16, 64), (16, 4), (4, 64)], ids=["few of many tokens", "all tokens", "decode tiles"])
+def test_lists_of_a_workspace_whose_first_call_is_captured(hq, most):
+    """Lists cut over many CTAs, replayed from a capture with no call before it, the grid made for more tokens than the plan has."""
+    torch = torch_mod()
+    b = batch_of([2, 1, 1], [3000, 900, 40], hq, 1, 16, True, seed=4)
+    ws = B.Workspace(8, most, 400, hq, 1)
+    plan(ws, b)
+    q, k, v, (o, lse) = bf16(b.q), bf16(b.k_pages), bf16(b.v_pages), outputs(b)
+    row = int(np.diff(b.kv_indptr).max())
+    selected = P.select_pages(b, np.random.default_rng(0).standard_normal((4, 1, row)), 0, 1, 150)
+    sel = dev(selected)
+    g = record(lambda: ws.run_pages(q, k, v, sel, o, lse))
+    for _ in range(2):
+        o.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert ws.get_error() == 0
+        assert_state(o, lse, P.pages_attention(b, f64(q), f64(k), f64(v), selected), BF16_WEIGHTS)
