@@ -536,7 +536,7 @@ int fi_select_pages(fi_workspace* ws, const float* scores, int32_t row_pages, in
  * UNSUPPORTED: composable plans, a sliding window; total_q * num_kv_heads * budget above 2^31 - 1 (in a replay: rows are not
  * written, FI_DEVERR_KEPT); up to 8 query heads a KV head, what fi_plan refuses for decode tiles, above that page sizes other than 8,
  * 16, 32, 64 and 128; more than 256 heads.  A replay on fi_run's tensor-core tiles (more than 8 heads) needs the total query count
- * of the capture.
+ * of the capture; there a plan without query tokens is not captured, as with fi_tree_run.
  * Errors: NO_PLAN, INVALID_ARG, UNSUPPORTED, CUDA.
  */
 int fi_run_pages(fi_workspace* ws, const void* q, const void* k_pages, const void* v_pages, int num_pages,

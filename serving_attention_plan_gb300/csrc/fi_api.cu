@@ -1147,7 +1147,8 @@ int fi_run_pages(fi_workspace* ws, const void* q, const void* k_pages, const voi
   bool captured = false;
   st = is_capturing(s, total_q < ws->max_total_q, &captured);
   if (st != FI_OK) return st;
-  if (total_q == 0 && !captured) return FI_OK;
+  // (a tensor-core launch holds a tensor map of q with the plan's tokens, so one without tokens serves no later plan)
+  if (total_q == 0 && (!captured || tensor)) return FI_OK;
   if (q == nullptr || k_pages == nullptr || v_pages == nullptr || selected == nullptr || o == nullptr || lse == nullptr || num_pages < 1)
     return FI_ERR_INVALID_ARG;
   if (misaligned(q, 16) || misaligned(k_pages, 16) || misaligned(v_pages, 16) || misaligned(o, 16) || misaligned(lse, 4) ||

@@ -971,3 +971,45 @@ def test_lists_of_a_workspace_whose_first_call_is_captured(hq, most):
         torch.cuda.synchronize()
         assert ws.get_error() == 0
         assert_state(o, lse, P.pages_attention(b, f64(q), f64(k), f64(v), selected), BF16_WEIGHTS)
+
+
+@pytest.mark.parametrize("hq", [8, 24], ids=["decode tiles", "tensor-core tiles"])
+def test_capture_of_calls_on_a_plan_without_tokens(hq):
+    """Every call of a step is accepted, and the graph does nothing on a plan without tokens.  What was captured on decode tiles follows
+    a later plan; trees and lists on tensor-core tiles hold the capture's tokens and are left out."""
+    torch = torch_mod()
+    none, b = batch_of([], [], hq, 2, 16, True, seed=3), batch_of([2, 1], [90, 40], hq, 2, 16, True, seed=4)
+    ws = B.Workspace(2, 3, 40, hq, 2)
+    q, k, v = bf16(b.q), bf16(b.k_pages), bf16(b.v_pages)
+    o, lse, to, tl = (torch.full(s, 9.0, dtype=t, device="cuda") for s, t in
+                      (((3, hq, 128), torch.bfloat16), ((3, hq), torch.float32), ((3, hq, 128), torch.bfloat16), ((3, hq), torch.float32)))
+    mask, path = torch.ones(3, 1, dtype=torch.int32, device="cuda"), torch.full((2, 1), -1, dtype=torch.int32, device="cuda")
+    bounds, scores = torch.zeros(b.num_pages, 2, 2, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(3, 2, 6, device="cuda")
+    sel = torch.full((3, 2, 6), 7, dtype=torch.int32, device="cuda")
+    L, h, n = B.lib(), ws.handle, b.num_pages
+
+    def step():
+        s = torch.cuda.current_stream().cuda_stream
+        x = lambda t: t.data_ptr()
+        assert L.fi_page_bounds(h, x(k), n, 0, x(bounds), s) == 0
+        assert L.fi_score_pages(h, x(q), x(bounds), n, x(scores), 6, s) == 0
+        assert L.fi_select_pages(h, x(scores), 6, 0, 0, 6, x(sel), s) == 0
+        assert L.fi_run_pages(h, x(q), x(k), x(v), n, x(sel), 6, x(o), x(lse), s) == 0
+        assert L.fi_tree_run(h, x(q), x(k), x(v), n, x(mask), 1, x(to), x(tl), s) == 0
+        assert L.fi_tree_commit(h, x(path), 1, x(k), x(v), n, s) == 0
+
+    plan(ws, none)
+    g = record(step)
+    g.replay()
+    torch.cuda.synchronize()
+    assert ws.get_error() == 0 and (o == 9).all() and (lse == 9).all() and (sel == 7).all() and (scores == 0).all() and (bounds == 0).all()
+    plan(ws, b)
+    g.replay()
+    torch.cuda.synchronize()
+    assert ws.get_error() == 0
+    host = P.select_pages(b, scores.cpu().numpy(), 0, 0, 6)
+    assert np.array_equal(sel.cpu().numpy(), host) and (to == 9).all()
+    if hq == 24:
+        assert (o == 9).all()
+    else:
+        assert_state(o, lse, P.pages_attention(b, f64(q), f64(k), f64(v), host), BF16_WEIGHTS)
