@@ -442,6 +442,9 @@ int fi_compact(fi_workspace* ws, const int32_t* kept, int32_t budget, void* k_pa
  * whole cache (fi_tree_run), and the accepted path's keys move to their places (fi_tree_commit).  All run on the workspace's
  * current plan, with the common behaviour of the cache operators above.  Query token t of request i (l_q tokens, l_kv keys)
  * is the key l_kv - l_q + t of its own cache, whose K and V fi_append has written.
+ *
+ * With a rotary position the tokens of a tree need fi_append's `positions`: a token's own is that of the context's end plus its depth in
+ * the tree, where fi_append's default is its slot's.  So written, a committed path is what appending its tokens alone leaves.
  */
 
 /*

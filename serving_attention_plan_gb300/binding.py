@@ -210,6 +210,23 @@ def tree_mask(qo_indptr, parents) -> np.ndarray:
     return mask.view(np.int32)
 
 
+def tree_positions(qo_indptr, parents, first) -> np.ndarray:
+    """append's positions of drafted trees: first[i], the position of a child of request i's context (the tokens before the tree), plus a
+    token's depth; parents as for tree_mask.  int32 [total_q]."""
+    qo, parents, first = _i32(qo_indptr), _i32(parents), _i32(first)
+    lens = np.diff(qo)
+    _need(parents.shape == (int(qo[-1]),), f"parents: shape {parents.shape}, expected {(int(qo[-1]),)}")
+    _need(first.shape == lens.shape, f"first: shape {first.shape}, expected {lens.shape}")
+    out = np.zeros(parents.shape[0], np.int32)
+    for t in range(int(lens.max(initial=0))):  # token t of all requests that have one
+        i = np.flatnonzero(lens > t)
+        q0, up = qo[i], parents[qo[i] + t]
+        bad = np.flatnonzero((up < -1) | (up >= t))
+        _need(len(bad) == 0, f"parents: token {t} of requests {i[bad].tolist()} does not have its parent before it")
+        out[q0 + t] = np.where(up < 0, first[i], out[q0 + np.maximum(up, 0)] + 1)
+    return out
+
+
 def device_sm_count() -> int:
     v = c_int(0)
     _check(lib().fi_device_sm_count(ctypes.byref(v)), "fi_device_sm_count")

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 
 from oracle import attention as A
+from oracle import cache as C
 from oracle import parts as P
 from serving_attention_plan_gb300 import binding as B
 from serving_attention_plan_gb300 import workloads as W
@@ -1013,3 +1014,76 @@ def test_capture_of_calls_on_a_plan_without_tokens(hq):
         assert (o == 9).all()
     else:
         assert_state(o, lse, P.pages_attention(b, f64(q), f64(k), f64(v), host), BF16_WEIGHTS)
+
+
+@pytest.mark.parametrize("dtype,inter", [("bf16", False), ("bf16", True), ("e4m3", False)])
+def test_tree_with_rotary_positions(dtype, inter):
+    """Trees appended at their depths: q and the tree's keys against a rotation by depth, the attention against the oracle on them, and the
+    committed path bit for bit as an append of its tokens alone."""
+    torch = torch_mod()
+    rng = np.random.default_rng(21)
+    hq, hk, ps, lq, ctx = 8, 2, 16, [13, 30, 1], [300, 47, 16]
+    scales = (0.0625, 0.03125) if dtype == "e4m3" else (1.0, 1.0)
+    b = batch_of(lq, [c + n for c, n in zip(ctx, lq)], hq, hk, ps, True, seed=2)
+    inv_freq = 10000.0 ** (-np.arange(0, 128, 2) / 128)
+    kind = torch.bfloat16 if dtype == "bf16" else torch.float8_e4m3fn
+    k, v = ((torch.randn(b.num_pages, hk, ps, 128, device="cuda") / s).to(kind) for s in scales)
+    k0, v0 = k.clone(), v.clone()
+    x = torch.randn(b.total_q, hq + 2 * hk, 128, device="cuda").to(torch.bfloat16)
+    parents = np.concatenate([[rng.integers(max(-1, t - 4), t) if t else -1 for t in range(n)] for n in lq])
+    depth = np.zeros(b.total_q, np.int64)  # by walking up, one token at a time
+    for i, n in enumerate(lq):
+        for t in range(n):
+            up = parents[b.qo_indptr[i] + t]
+            while up >= 0:
+                depth[b.qo_indptr[i] + t] += 1
+                up = parents[b.qo_indptr[i] + up]
+    positions = np.repeat(ctx, lq) + depth
+    given = B.tree_positions(b.qo_indptr, parents, ctx)
+    assert np.array_equal(given, positions)
+
+    ws = workspace(b, dtype=dtype, scales=scales)
+    ws.set_rope(inv_freq, inter)
+    q, (o, lse) = torch.empty(b.total_q, hq, 128, dtype=torch.bfloat16, device="cuda"), outputs(b)
+    ws.append(x[:, :hq], x[:, hq:hq + hk], x[:, hq + hk:], k, v, q, positions=dev(given))
+    mask = B.tree_mask(b.qo_indptr, parents)
+    ws.tree_run(q, k, v, dev(mask), o, lse)
+    torch.cuda.synchronize()
+    # the rotation by depth: rounded once, 2^-19 of the row's largest for the fp32 steps and the angle before that
+    rq, rk = (C.norm_rotate(f64(x[:, s]), None, 0.0, inv_freq, positions.astype(np.float64), inter) for s in (slice(0, hq), slice(hq, hq + hk)))
+    slack = lambda r: np.abs(r).max(-1, keepdims=True) * 2.0 ** -19
+    assert (np.abs(f64(q) - rq) <= np.abs(rq) * 2.0 ** -8 + slack(rq)).all()
+    tok, page, slot, _ = C.append_places(b)
+    rows = f64(k)[page, :, slot] * scales[0]
+    step = np.abs(rk[tok]) * 2.0 ** -8 if dtype == "bf16" else np.maximum(np.abs(rk[tok]) * 2.0 ** -4, scales[0] * 2.0 ** -10)
+    assert (np.abs(rows - rk[tok]) <= step + slack(rk[tok])).all()
+    assert_state(o, lse, P.tree_attention(b, f64(q), f64(k) * scales[0], f64(v) * scales[1], mask, q_floor=Q_FLOOR if dtype == "e4m3" else 0.0),
+                 F16_WEIGHTS if dtype == "e4m3" else BF16_WEIGHTS)
+
+    # the path to a leaf, committed; beside it the same tokens appended as a chain
+    path = np.full((3, 30), -1, np.int32)
+    for i, n in enumerate(lq):
+        up, at = [], n - 1
+        while at >= 0:
+            up.append(at)
+            at = int(parents[b.qo_indptr[i] + at])
+        path[i, :len(up)] = up[::-1]
+    taken = (path >= 0).sum(1)
+    assert taken.max() > 3 and (depth[b.qo_indptr[1:] - 1] == taken - 1).all()
+    ws.tree_commit(dev(path), k, v)
+    keep = dev(np.concatenate([b.qo_indptr[i] + path[i, :n] for i, n in enumerate(taken)])).long()
+    lkv = np.array(ctx) + taken
+    n = -(-lkv // ps)
+    lists = np.concatenate([b.kv_indices[b.kv_indptr[i]:b.kv_indptr[i] + m] for i, m in enumerate(n)])
+    ws2 = B.Workspace(3, 44, 64, hq, hk)
+    ws2.set_kv_dtype(dtype, *scales)
+    ws2.set_rope(inv_freq, inter)
+    ws2.plan(np.concatenate([[0], np.cumsum(taken)]), np.concatenate([[0], np.cumsum(n)]), lists, lkv - (n - 1) * ps, ps, True)
+    y = x[keep]
+    ws2.append(y[:, :hq], y[:, hq:hq + hk], y[:, hq + hk:], k0, v0, torch.empty(len(keep), hq, 128, dtype=torch.bfloat16, device="cuda"))
+    torch.cuda.synchronize()
+    assert ws.get_error() == 0 and ws2.get_error() == 0
+    for i in range(3):
+        for j in range(ctx[i], int(lkv[i])):
+            p, s = int(b.kv_indices[b.kv_indptr[i] + j // ps]), j % ps
+            assert torch.equal(k[p, :, s].view(torch.uint8), k0[p, :, s].view(torch.uint8)) and torch.equal(v[p, :, s].view(torch.uint8), v0[p, :, s].view(torch.uint8))

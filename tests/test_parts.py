@@ -87,3 +87,21 @@ def test_null_workspace():
     assert L.fi_score_pages(None, None, None, 1, None, 1, None) == 1
     assert L.fi_select_pages(None, None, 1, 0, 0, 1, None, None) == 1
     assert L.fi_run_pages(None, None, None, None, 1, None, 1, None, None, None) == 1
+
+
+def test_tree_positions():
+    # request 0: 0 and 1 under the context, 2 under 0, 3 under 2; request 1: none; request 2: a chain of 40
+    parents = np.concatenate([[-1, -1, 0, 2], np.arange(40) - 1])
+    p = B.tree_positions([0, 4, 4, 44], parents, [100, 7, 2 ** 30])
+    assert p.dtype == np.int32 and p[:4].tolist() == [100, 100, 101, 102] and p[4:].tolist() == [2 ** 30 + t for t in range(40)]
+    # the depth is the number of a row's mask bits but for its own
+    rng = np.random.default_rng(0)
+    lens = rng.integers(0, 70, size=30)
+    qo = np.concatenate([[0], np.cumsum(lens)])
+    parents = np.concatenate([[rng.integers(-1, t) if t else -1 for t in range(n)] for n in lens])
+    sees = np.unpackbits(B.tree_mask(qo, parents).view(np.uint8), axis=1).sum(1)
+    assert np.array_equal(B.tree_positions(qo, parents, np.arange(30) * 11), np.repeat(np.arange(30) * 11, lens) + sees - 1)
+    assert B.tree_positions([0], [], []).shape == (0,)
+    for qo, parents, first in (([0, 2], [-1, 1], [5]), ([0, 2], [-2, -1], [5]), ([0, 2], [-1, 5], [5]), ([0, 3], [-1, 0], [5]), ([0, 2], [-1, 0], [5, 6])):
+        with pytest.raises(ValueError):
+            B.tree_positions(qo, parents, first)
