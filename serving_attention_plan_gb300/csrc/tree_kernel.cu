@@ -690,7 +690,8 @@ __device__ void softmax_keys(const TreeParams& p, TreeSmem<kFp8>& sm, uint32_t t
       alive = alive && __all_sync(kAll, wait_for(&sm.s_full[h][b], (ss >> 1) & 1, p.pv.err, &sm.abort));
       if (kFp8 && s == 0) {  // the row's scale, once the products have seen the tile; then the Q tiles may go
         const int e = sm.q_exp[(nq + (two ? h : 0)) & 1][row];
-        scale = e == kQuiet ? __uint_as_float(0x7fc00000u) : scale * __uint_as_float(uint32_t(e + 127) << 23);
+        // (never 0, however small the row and k_scale: 0 times the -inf of an unseen key would be NaN)
+        scale = e == kQuiet ? __uint_as_float(0x7fc00000u) : fmaxf(scale * __uint_as_float(uint32_t(e + 127) << 23), __uint_as_float(1u));
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.q_empty[nq & 1]);
         if (lane == 0 && two) mbar_arrive(&sm.q_empty[(nq + 1) & 1]);

@@ -1087,3 +1087,21 @@ def test_tree_with_rotary_positions(dtype, inter):
         for j in range(ctx[i], int(lkv[i])):
             p, s = int(b.kv_indices[b.kv_indptr[i] + j // ps]), j % ps
             assert torch.equal(k[p, :, s].view(torch.uint8), k0[p, :, s].view(torch.uint8)) and torch.equal(v[p, :, s].view(torch.uint8), v0[p, :, s].view(torch.uint8))
+
+
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+@pytest.mark.parametrize("k_scale", [1.0, 2.0 ** -24, 2.0 ** -149])
+def test_tree_rows_of_the_smallest_numbers(k_scale, cap):
+    """e4m3 pages: rows of q down to bf16's smallest number, under scales whose product with a row's own leaves fp32's range."""
+    torch = torch_mod()
+    b = batch_of([5, 40], [300, 700], 8, 2, 16, False, seed=12)
+    (k, kv), (v, vv) = pool(b, "k_pages", "e4m3", "HND", 1.0), pool(b, "v_pages", "e4m3", "HND", 1.0)
+    q, (o, lse) = bf16(b.q), outputs(b)
+    q[::2] = (q[::2].double() * 2.0 ** -126).to(torch.bfloat16)
+    q[4], q[6] = 2.0 ** -133, -(2.0 ** -126)
+    mask = random_mask(np.random.default_rng(0), b, "tree")
+    ws = workspace(b, dtype="e4m3", scales=(k_scale, 1.0), cap=cap)
+    ws.tree_run(q, k, v, dev(mask), o, lse)
+    torch.cuda.synchronize()
+    assert ws.get_error() == 0
+    assert_state(o, lse, P.tree_attention(b, f64(q), kv * k_scale, vv, mask, cap, q_floor=Q_FLOOR), F16_WEIGHTS, cap)
