@@ -1105,3 +1105,29 @@ def test_tree_rows_of_the_smallest_numbers(k_scale, cap):
     torch.cuda.synchronize()
     assert ws.get_error() == 0
     assert_state(o, lse, P.tree_attention(b, f64(q), kv * k_scale, vv, mask, cap, q_floor=Q_FLOOR), F16_WEIGHTS, cap)
+
+
+@pytest.mark.parametrize("big", [2.0 ** 4, 2.0 ** 9, 2.0 ** 20])
+def test_tree_rows_with_one_large_element(big):
+    """e4m3 pages: a dim of q far above the others, whose elements fall below 2^-9 of it and are rounded to 2^-17 of it."""
+    torch = torch_mod()
+    b = batch_of([5, 40], [300, 700], 8, 2, 16, False, seed=13)
+    (k, kv), (v, vv) = pool(b, "k_pages", "e4m3", "HND", 1.0), pool(b, "v_pages", "e4m3", "HND", 1.0)
+    raw = k.view(torch.uint8)
+    raw[..., 7] = 0  # where the large element meets zeros the others decide
+    kv = A.e4m3_to_f64(raw.cpu().numpy())
+    q, (o, lse) = bf16(b.q), outputs(b)
+    q[:, :, 7] = big
+    mask = random_mask(np.random.default_rng(0), b, "tree")
+    ws = workspace(b, dtype="e4m3")
+    ws.tree_run(q, k, v, dev(mask), o, lse)
+    torch.cuda.synchronize()
+    assert ws.get_error() == 0
+    # an element is off by half of the second term's smallest step, 2^-10 where the row's largest is 128 or more: 2^-17 of the largest at most
+    ref = P.tree_attention(b, f64(q), kv, vv, mask)
+    off = big * 2.0 ** -17 / np.sqrt(128)
+    for i, (q0, q1) in enumerate(zip(b.qo_indptr[:-1], b.qo_indptr[1:])):
+        ids = b.kv_indices[b.kv_indptr[i]:b.kv_indptr[i + 1]]
+        for h in range(8):
+            ref[3][q0:q1, h] += off * np.abs(kv[ids, h // 4]).sum(-1).max() * 2.0 ** 16
+    assert_state(o, lse, ref, F16_WEIGHTS)
