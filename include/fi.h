@@ -316,10 +316,11 @@ int fi_merge_states(const void* o_a, const float* lse_a, const void* o_b, const 
  * on the workspace's current plan: its requests, page lists, page size, layout, KV type, window and
  * soft-cap.  With a composable plan they see the per-request part.
  *
- * Common behaviour: asynchronous on `stream`, launched as programmatic dependents that read nothing before
- * the previous kernel on the stream has completed.  Calls that share a workspace must not overlap on the GPU.
+ * Common behaviour: asynchronous on `stream`, launched as programmatic dependents that read nothing but the plan (whose copy a
+ * launch never overtakes) before the previous kernel on the stream has completed.  Calls that share a workspace must not overlap on the GPU.
  * Results are bit-identical from run to run.  The workspace's device must be the current one (else
- * INVALID_ARG).  Page ids >= num_pages: INVALID_ARG (in a replay: skipped, FI_DEVERR_PAGE_OOB).  Pools of
+ * INVALID_ARG).  Page ids >= num_pages: INVALID_ARG (in a replay: skipped, FI_DEVERR_PAGE_OOB;
+ * fi_tree_run takes the keys of such a page as zeros, as fi_run's tensor-core tiles do).  Pools of
  * more than 2^31 - 1 rows (pages * page size * KV heads): UNSUPPORTED.
  *
  * Capturable in a CUDA graph: a captured launch reads the requests and page lists of the plan that is current
@@ -501,6 +502,8 @@ int fi_page_bounds(fi_workspace* ws, const void* k_pages, int num_pages, int32_t
  *
  * for entry e of the page list of t's request, with scale = 1 / sqrt(128) (times k_scale); -inf for a page all of whose keys t
  * does not see (causal plans), or that a replay skips.  No soft-cap (it keeps the order).  fp32 sums.
+ * An infinite bound makes NaN of a q_d that takes the other one, by 0 * infinity as in the formula: such a page ranks first in
+ * fi_select_pages, which a bound must not do less.
  *
  *   bounds      as fi_page_bounds writes it
  *   scores      DEVICE float32 [total_q, num_kv_heads, row_pages]; entries from the request's page count on keep what they hold

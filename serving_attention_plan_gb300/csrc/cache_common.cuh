@@ -7,8 +7,8 @@
 
 namespace fi {
 
-// Set-up may overlap the previous kernel on the stream (programmatic dependent launch); nothing
-// global is read before it has completed, and followers are let go only after that.
+// Set-up may overlap the previous kernel on the stream (programmatic dependent launch); of global memory only the plan may be read before
+// it has completed (a copy of the plan is no kernel, so a launch behind it waits for all of it), and followers are let go only after that.
 __device__ __forceinline__ void wait_prior_grid() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

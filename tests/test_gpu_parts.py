@@ -1131,3 +1131,117 @@ def test_tree_rows_with_one_large_element(big):
         for h in range(8):
             ref[3][q0:q1, h] += off * np.abs(kv[ids, h // 4]).sum(-1).max() * 2.0 ** 16
     assert_state(o, lse, ref, F16_WEIGHTS)
+
+
+@pytest.mark.parametrize("tokens", [1, 5], ids=["eight columns", "sixteen"])
+def test_scores_of_infinite_bounds_against_either_sign(tokens):
+    """An infinite bound: infinity where q takes it, NaN by 0 * infinity where q takes the other one, in the kernel as in the formula; the
+    choice ranks both before every number."""
+    torch = torch_mod()
+    b = batch_of([tokens], [96], 4, 1, 16, False)
+    bounds = torch.ones(b.num_pages, 1, 2, 128, dtype=torch.bfloat16, device="cuda")
+    bounds[:, :, 0] = -1.0
+    p = [int(x) for x in b.kv_indices]
+    inf = float("inf")
+    bounds[p[0], 0, 1, 3] = inf     # against q > 0
+    bounds[p[1], 0, 1, 4] = inf     # against q < 0
+    bounds[p[2], 0, 0, 3] = -inf    # against q > 0
+    bounds[p[3], 0, 0, 4] = -inf    # against q < 0
+    bounds[p[4], 0, 1, 5] = inf     # against 0
+    q = torch.full((tokens, 4, 128), 0.5, dtype=torch.bfloat16, device="cuda")
+    q[..., 4], q[..., 5] = -0.5, 0.0
+    scores = torch.zeros(tokens, 1, 6, device="cuda")
+    ws = workspace(b)
+    ws.score_pages(q, bounds, scores)
+    got = scores.cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        want, _ = P.page_scores(b, f64(q), f64(bounds), np.zeros(scores.shape))
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(got == inf, want == inf)
+    assert np.isnan(got[0, 0]).tolist() == [False, True, True, False, True, False] and got[0, 0, 0] == got[0, 0, 3] == inf
+    assert np.allclose(got[:, 0, 5], 127 * 0.5 / np.sqrt(128))
+    sel = torch.zeros(tokens, 1, 5, dtype=torch.int32, device="cuda")
+    ws.select_pages(scores, sel)
+    assert (sel.cpu().numpy()[:, 0] == p[:5]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq", [8, 24], ids=["4 heads a group", "12"])
+def test_replays_on_pages_outside_the_pool(hq, dtype):
+    """A replay whose plan lists pages outside the pool: reported; a tree takes their keys as zeros, scores leave them out, bounds and commits
+    skip them, and what other requests get is right."""
+    torch = torch_mod()
+    hk, ps, lq, lkv = 2, 16, [5, 3, 7], [200, 90, 45]
+    a = batch_of(lq, lkv, hq, hk, ps, False, seed=5)
+    pages = a.num_pages  # the pools hold eight more, which the calls are not told of
+    ids = a.kv_indices.copy()
+    first, third = int(a.kv_indptr[0]), int(a.kv_indptr[2])
+    ids[first + 4], ids[first + 9], ids[third + 2] = pages, pages + 7, pages + 3  # within a context, and where drafted tokens lie
+    b = dataclasses.replace(a, kv_indices=ids)
+    inside = ids < pages
+    kind = torch.bfloat16 if dtype == "bf16" else torch.float8_e4m3fn
+    k, v = (torch.randn(pages + 8, hk, ps, 128, device="cuda").to(kind) for _ in range(2))
+    q, (o, lse), (po, plse) = bf16(a.q), outputs(a), outputs(a)
+    mask = random_mask(np.random.default_rng(2), a, "tree")
+    path = np.array([[1, 3, -1], [0, 2, -1], [2, 4, 6]], np.int32)
+    dmask, dpath = dev(mask), dev(path)
+    bounds = torch.full((pages + 8, hk, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    scores, sel = torch.zeros(15, hk, 13, device="cuda"), torch.zeros(15, hk, 4, dtype=torch.int32, device="cuda")
+    ws = workspace(a, dtype=dtype)
+    L, h, x = B.lib(), ws.handle, lambda t: t.data_ptr()
+
+    def graph(call):
+        return record(lambda: call(torch.cuda.current_stream().cuda_stream))
+
+    def ok(st):
+        assert st == 0
+
+    tree = graph(lambda s: ok(L.fi_tree_run(h, x(q), x(k), x(v), pages, x(dmask), mask.shape[1], x(o), x(lse), s)))
+    bound = graph(lambda s: ok(L.fi_page_bounds(h, x(k), pages, 0, x(bounds), s)))
+    score = graph(lambda s: ok(L.fi_score_pages(h, x(q), x(bounds), pages, x(scores), 13, s)))
+    pick = graph(lambda s: ok(L.fi_select_pages(h, x(scores), 13, 0, 0, 4, x(sel), s)))
+    lists = graph(lambda s: ok(L.fi_run_pages(h, x(q), x(k), x(v), pages, x(sel), 4, x(po), x(plse), s)))
+    commit = graph(lambda s: ok(L.fi_tree_commit(h, x(dpath), 3, x(k), x(v), pages, s)))
+    plan(ws, b)
+
+    def replay(g, bits):
+        g.replay()
+        torch.cuda.synchronize()
+        assert ws.get_error() == bits
+
+    kv, vv = f64(k), f64(v)
+    kz, vz = kv.copy(), vv.copy()
+    kz[pages:], vz[pages:] = 0, 0
+    replay(tree, B.DEVERR_PAGE_OOB)
+    assert_state(o, lse, P.tree_attention(b, f64(q), kz, vz, mask, q_floor=Q_FLOOR if dtype == "e4m3" else 0.0), F16_WEIGHTS if dtype == "e4m3" else BF16_WEIGHTS)
+    replay(bound, B.DEVERR_PAGE_OOB)
+    want = P.page_bounds(a, kv, np.full(bounds.shape, 7.0), False)
+    assert np.array_equal(f64(bounds)[ids[inside]], want[ids[inside]]) and (f64(bounds)[pages:] == 7.0).all()
+    replay(score, B.DEVERR_PAGE_OOB)
+    want, reach = P.page_scores(b, f64(q), f64(bounds), np.zeros(scores.shape))
+    for i in range(3):
+        at = inside[b.kv_indptr[i]:b.kv_indptr[i + 1]]
+        got = scores[b.qo_indptr[i]:b.qo_indptr[i + 1], :, :len(at)].cpu().numpy().astype(np.float64)
+        assert np.isneginf(got[:, :, ~at]).all()
+        assert np.abs(got - want[b.qo_indptr[i]:b.qo_indptr[i + 1], :, :len(at)])[:, :, at].max() <= reach * 2.0 ** -15
+    replay(pick, 0)
+    host = P.select_pages(b, scores.cpu().numpy(), 0, 0, 4)
+    assert np.array_equal(sel.cpu().numpy(), host)
+    outside = (host >= pages).any((1, 2))
+    assert outside[8:].all() and not outside[:8].any()  # the last request has three pages in all
+    replay(lists, B.DEVERR_PAGE_OOB)
+    ref = P.pages_attention(b, f64(q), kv, vv, host)
+    assert_state(po[:8], plse[:8], [r[:8] for r in ref], F16_WEIGHTS if dtype == "e4m3" else BF16_WEIGHTS)
+    raw = lambda t: t.view(torch.int16 if dtype == "bf16" else torch.uint8).cpu().numpy()
+    k0, v0 = raw(k), raw(v)
+    replay(commit, B.DEVERR_PAGE_OOB)
+    want_k, want_v = k0.copy(), v0.copy()
+    for i in range(3):
+        for j, e in enumerate(path[i]):
+            if e < 0:
+                break
+            off = lkv[i] - lq[i]
+            (fp,), (fs,) = P.places(b, i, [off + int(e)])
+            (tp,), (ts,) = P.places(b, i, [off + j])
+            if fp < pages and tp < pages:
+                want_k[tp, :, ts], want_v[tp, :, ts] = k0[fp, :, fs], v0[fp, :, fs]
+    assert np.array_equal(raw(k), want_k) and np.array_equal(raw(v), want_v)
