@@ -507,7 +507,7 @@ int fi_page_bounds(fi_workspace* ws, const void* k_pages, int num_pages, int32_t
  *
  *   bounds      as fi_page_bounds writes it
  *   scores      DEVICE float32 [total_q, num_kv_heads, row_pages]; entries from the request's page count on keep what they hold
- *   row_pages   at least the pages of the longest request (INVALID_ARG; in a replay, further pages get no score)
+ *   row_pages   at least 1 and the pages of the longest request (INVALID_ARG; in a replay, further pages get no score)
  * UNSUPPORTED: composable plans, a sliding window.  Errors: NO_PLAN, INVALID_ARG, UNSUPPORTED, CUDA.
  */
 int fi_score_pages(fi_workspace* ws, const void* q, const void* bounds, int num_pages, float* scores, int32_t row_pages,
@@ -539,8 +539,8 @@ int fi_select_pages(fi_workspace* ws, const float* scores, int32_t row_pages, in
  *              it elsewhere, too, counts as empty, FI_DEVERR_KEPT); other pages count in full, so none behind
  *              it may be listed.  A page listed twice counts twice.  Ids >= num_pages set FI_DEVERR_PAGE_OOB; what the rows of such a
  *              list are then is not defined.
- * UNSUPPORTED: composable plans, a sliding window; total_q * num_kv_heads * budget above 2^31 - 1 (in a replay: rows are not
- * written, FI_DEVERR_KEPT); up to 8 query heads a KV head, what fi_plan refuses for decode tiles, above that page sizes other than 8,
+ * UNSUPPORTED: composable plans, a sliding window; budget * page size above 2^30; total_q * num_kv_heads * budget above 2^31 - 1 (in a
+ * replay: rows are not written, FI_DEVERR_KEPT); up to 8 query heads a KV head, what fi_plan refuses for decode tiles, above that page sizes other than 8,
  * 16, 32, 64 and 128; more than 256 heads.  A replay on fi_run's tensor-core tiles (more than 8 heads) needs the total query count
  * of the capture; there a plan without query tokens is not captured, as with fi_tree_run.
  * Errors: NO_PLAN, INVALID_ARG, UNSUPPORTED, CUDA.

@@ -1245,3 +1245,16 @@ def test_replays_on_pages_outside_the_pool(hq, dtype):
             if fp < pages and tp < pages:
                 want_k[tp, :, ts], want_v[tp, :, ts] = k0[fp, :, fs], v0[fp, :, fs]
     assert np.array_equal(raw(k), want_k) and np.array_equal(raw(v), want_v)
+
+
+def test_lists_at_their_limits():
+    """A budget of 2^30 keys is the last that is taken: the next is refused before a pointer is looked at."""
+    b = batch_of([1], [40], 4, 1, 16, False)
+    ws = workspace(b)
+    L, s = B.lib(), ctypes.c_void_p(torch_mod().cuda.current_stream().cuda_stream)
+    for budget, status in ((2 ** 26, 1), (2 ** 26 + 1, 3), (2 ** 31 - 1, 3)):
+        assert L.fi_run_pages(ws.handle, None, None, None, b.num_pages, None, budget, None, None, s) == status
+    for row, status in ((0, 1), (2, 1), (3, 1)):  # three pages: the pointers are what is wrong with the last
+        assert L.fi_score_pages(ws.handle, None, None, b.num_pages, None, row, s) == status
+        assert L.fi_select_pages(ws.handle, None, row, 0, 0, 1, None, s) == status
+    assert ws.get_error() == 0
