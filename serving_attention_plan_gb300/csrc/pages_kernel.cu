@@ -424,12 +424,13 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreCtas) scores_kernel(const
   }
 }
 
-// Requests of more columns, sixteen at a time.  There the products' instructions count, not only the bounds' bytes, so q's columns are
+// Requests of more columns, sixteen at a time.  There the instructions of a block count, not only the bounds' bytes, so q's columns are
 // the rows of a product and the pages its columns: the words of a page are its operand as they come from memory, where as rows
 // of a product four of them have to be moved together for each set (a fifth of all instructions), and 16 pages take two products an
 // operand of q.  q streams by, a piece ahead (all of it in registers, the block's were spilled).  Both forms measured, two contexts of
 // 131 K keys, 64/8 heads: 4 tokens each 19.2 us eight at a time, 16.0 sixteen (74 MB of bounds are 11); 16 tokens 55.8 and 39.2;
-// four of 65 K, 16 heads a group, 16 tokens 99 and 87.  128 decode requests of four heads a group: 25 eight at a time, 32 sixteen.
+// four of 65 K, 16 heads a group, 16 tokens 99 and 87.  What is left is latency: no pipe is busy for a third of the time, DRAM for half
+// of it, with twelve warps an SM and two chains of sixteen dependent products a set.  128 decode requests of four heads a group: 25 eight at a time, 32 sixteen.
 // kHeads: heads of a group, 1, 2, 4 or 8; 16: more than 8, 16 at a time; 0: any other number below 8, by a loop over the set's tokens.
 constexpr int kScoreWideCtas = 3;
 constexpr int kScoreMostParts = 16;

@@ -11,9 +11,9 @@
 // as long as the first.  Two tiles are bound by the rate at which the products take their operands: 32 score products of 128 x
 // 64 at 76 clocks and 16 output products of 128 x 128 at 75 are 3600 of the 3900 clocks of 128 keys.
 //
-// Measured: 64 requests of 16 tokens over 1 to 8 K bf16 keys, 32/8 heads, 187 us (0.90 of the copy bandwidth), 128 of 8 tokens
-// over 0.5 to 4 K 208; 32 of 64 tokens over 2 to 8 K 168 (256 rows); the 64 requests with e4m3 keys 161; 12 requests of 17 to 30
-// tokens over 8 to 24 K e4m3 keys, 64/8 heads, 216.
+// Measured: 64 requests of 16 tokens over 265 K bf16 keys in all, 32/8 heads, 179 us (0.92 of the copy bandwidth), 128 of 8 tokens
+// over 283 K 190; 32 of 64 tokens over 158 K 171 (256 rows); the 64 requests with e4m3 keys 155; 12 requests of 17 to 30
+// tokens over 8 to 24 K e4m3 keys, 64/8 heads, 218.
 //
 // Split: the 128-key tiles of all (request, KV head, pair of row tiles) units form one line, and every CTA takes an equal
 // piece of it, wherever that cuts a unit.  Nothing of this is planned on the host but the line's prefix per request, so a
