@@ -265,7 +265,8 @@ int fi_plan_composable(fi_workspace* ws, const int32_t* shared_qo_indptr, const 
  * v_pages built from the call's pointers, num_pages and page size.
  * Calls that share a workspace must not overlap on the GPU.
  * Errors: NO_PLAN, INVALID_ARG (null pointers, q / k_pages / v_pages not
- * 16-byte aligned, page id >= num_pages), CUDA.
+ * 16-byte aligned, o not 8-byte (decode tiles) or 16-byte (tensor-core tiles)
+ * aligned, lse not 4-byte aligned, page id >= num_pages), CUDA.
  */
 int fi_run(fi_workspace* ws, const void* q, const void* k_pages, const void* v_pages, int num_pages, void* o,
            float* lse, void* stream);
@@ -285,7 +286,7 @@ int fi_run(fi_workspace* ws, const void* q, const void* k_pages, const void* v_p
  *             -inf for a row that saw no key)
  *   o, lse    written with (state of this plan) ⊕ (o_prev, lse_prev); they may
  *             be the same buffers as o_prev / lse_prev (in place)
- * Other arguments, behaviour and errors as fi_run; o_prev and lse_prev are
+ * Other arguments, behaviour and errors as fi_run (o_prev aligned as o); o_prev and lse_prev are
  * both null (plain fi_run) or both set (else INVALID_ARG).
  */
 int fi_run_merge(fi_workspace* ws, const void* q, const void* k_pages, const void* v_pages, int num_pages,
@@ -303,7 +304,8 @@ int fi_run_merge(fi_workspace* ws, const void* q, const void* k_pages, const voi
  *
  *   o_a, o_b, o   DEVICE bf16 [rows, heads, head_dim]   (o may alias o_a or o_b)
  *   lse_a, lse_b, lse   DEVICE float32 [rows, heads], natural log
- * Asynchronous on `stream`.  Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ * Asynchronous on `stream`.  Errors: INVALID_ARG (also for an o that is not 8-byte or an lse that is not
+ * 4-byte aligned), UNSUPPORTED, CUDA.
  */
 int fi_merge_states(const void* o_a, const float* lse_a, const void* o_b, const float* lse_b, void* o, float* lse,
                     int rows, int heads, int head_dim, void* stream);
@@ -633,7 +635,7 @@ int fi_plan_composable_compute(const int32_t* shared_qo_indptr, const int32_t* s
  * The first call on a device looks up the array's device address and sets the
  * kernel attribute (with that device current).
  * Errors: INVALID_ARG (also for q / k_pages / v_pages that are not
- * 16-byte aligned), CAPACITY (plan + page indices + slots do not
+ * 16-byte aligned, or o not 8-byte), CAPACITY (plan + page indices + slots do not
  * fit in the array), UNSUPPORTED (the batch needs tensor-core tiles, i.e. some
  * request has more than 8 rows = query tokens x group size, or a KV length
  * above 2^30), CUDA.

@@ -671,6 +671,10 @@ int fi_run_merge(fi_workspace* ws, const void* q, const void* k_pages, const voi
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_pages) | reinterpret_cast<uintptr_t>(v_pages)) & 15)
     return FI_ERR_INVALID_ARG;
   if (!any_rows) return FI_OK;
+  // rows of o and o_prev move 8 bytes at a time on decode tiles, 16 on tensor-core tiles
+  const uintptr_t row_align = h[fi::H_PATH] == fi::kPathTensor ? 16 : 8;
+  if (misaligned(o, row_align) || misaligned(o_prev, row_align) || misaligned(lse, 4) || misaligned(lse_prev, 4))
+    return FI_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int ps = h[fi::H_PAGE_SIZE];
   const float scale_log2 = fi::kLog2e / std::sqrt(float(ws->head_dim));
@@ -781,6 +785,9 @@ int fi_merge_states(const void* o_a, const float* lse_a, const void* o_b, const 
   if (head_dim != fi::kHeadDim) return FI_ERR_UNSUPPORTED;
   if (rows == 0) return FI_OK;
   if (!o_a || !lse_a || !o_b || !lse_b || !o || !lse) return FI_ERR_INVALID_ARG;
+  if (misaligned(o_a, 8) || misaligned(o_b, 8) || misaligned(o, 8) || misaligned(lse_a, 4) || misaligned(lse_b, 4) ||
+      misaligned(lse, 4))
+    return FI_ERR_INVALID_ARG;
   const long long n = (long long)rows * heads;
   int blocks = int(std::min<long long>((n + 7) / 8, 4096));
   fi::merge_states_kernel<<<blocks, 256, 0, static_cast<cudaStream_t>(stream)>>>(

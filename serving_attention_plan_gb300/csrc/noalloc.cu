@@ -163,6 +163,8 @@ extern "C" int fi_decode_noalloc(const int32_t* qo_indptr, const int32_t* kv_ind
   if (L.end > kNoAllocScratchBytes) return FI_ERR_CAPACITY;
   if (W > 0 && (q == nullptr || o == nullptr || lse == nullptr)) return FI_ERR_INVALID_ARG;
   if (nnz > 0 && (k_pages == nullptr || v_pages == nullptr)) return FI_ERR_INVALID_ARG;
+  if (W > 0 && ((reinterpret_cast<uintptr_t>(o) & 7) != 0 || (reinterpret_cast<uintptr_t>(lse) & 3) != 0))
+    return FI_ERR_INVALID_ARG;  // rows of o are stored 8 bytes at a time
   // the kernel moves q, K and V rows with 16-byte copies
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_pages) | reinterpret_cast<uintptr_t>(v_pages)) & 15)
     return FI_ERR_INVALID_ARG;

@@ -256,3 +256,37 @@ def test_decode_ignores_values_past_the_last_token():
         ro, rl = A.batch_attention(b)
         assert np.isfinite(o).all()
         assert_close(o, lse, ro, rl)
+
+
+def test_unaligned_outputs_rejected_on_host():
+    """Rows of o (and of a given state) go 8 bytes at a time on decode tiles, 16 on tensor-core tiles: other addresses are refused before
+    any launch, and 8 bytes behind a boundary of 16 a decode batch's rows are as they are on it."""
+    import ctypes
+    from serving_attention_plan_gb300 import binding as B
+    torch = torch_mod()
+    L, s = B.lib(), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    for prefill in (False, True):
+        b = W.random_small_batch(82, batch=4, num_qo_heads=8, num_kv_heads=2, page_size=16, causal=False,
+                                 q_len_range=(20, 40) if prefill else (1, 1), kv_len_range=(40, 64))
+        q, k, v = to_device(b)
+        (o, lse), (o2, lse2) = alloc_out(b), alloc_out(b)
+        ws = B.Workspace(4, 160, 64, 8, 2)
+        ws.plan(b.qo_indptr, b.kv_indptr, b.kv_indices, b.last_page_len, 16, False)
+        x = lambda t, off=0: ctypes.c_void_p(t.data_ptr() + off)
+        off = 8 if prefill else 4
+        for po, pl, prev_o, prev_l in (((o, off), (lse, 0), None, None), ((o, 2), (lse, 0), None, None), ((o, 0), (lse, 2), None, None),
+                                       ((o, 0), (lse, 0), (o2, off), (lse2, 0)), ((o, 0), (lse, 0), (o2, 0), (lse2, 1))):
+            assert L.fi_run_merge(ws.handle, x(q), x(k), x(v), b.num_pages, prev_o and x(*prev_o), prev_l and x(*prev_l), x(*po), x(*pl), s) == 1
+        if not prefill:
+            flat = torch.empty(o.numel() + 4, dtype=o.dtype, device="cuda")
+            ws.run(q, k, v, o, lse)
+            ws.run(q, k, v, flat[4:].view(o.shape), lse2)
+            torch.cuda.synchronize()
+            assert torch.equal(flat[4:].view(o.shape), o) and torch.equal(lse, lse2)
+            for bad in ((o, 4), (o, 2)):
+                assert L.fi_decode_noalloc(*(a.ctypes.data_as(ctypes.POINTER(ctypes.c_int32)) for a in (b.qo_indptr, b.kv_indptr, b.kv_indices, b.last_page_len)),
+                                           4, 8, 2, 128, 16, 0, x(q), x(k), x(v), b.num_pages, x(*bad), x(lse), s) == 1
+            n = b.total_q
+            ok = (x(o), x(lse), x(o2), x(lse2), x(o), x(lse))
+            for i, bad in ((0, x(o, 4)), (1, x(lse, 2)), (2, x(o2, 4)), (3, x(lse2, 1)), (4, x(o, 2)), (5, x(lse, 2))):
+                assert L.fi_merge_states(*ok[:i], bad, *ok[i + 1:], n, 8, 128, s) == 1
